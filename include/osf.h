@@ -216,6 +216,116 @@ int osf_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sk, i
                                     int num_splits, size_t *bytes);
 
 /*
+ * osf_attn_key_weights -- the attention weight that every key receives, summed over the query
+ * heads of its kv head and over the rows that see it: the column sums of the softmax matrix of
+ * osf_attn_fwd_gqa_ex, [Q3] "自注意力原理" + "GQA" (the pages materialise that matrix; here it is
+ * rebuilt tile by tile from the forward pass's log-sum-exp and never written):
+ *     weights[b, g, j] (+)= sum_{h in group g} sum_{i sees j} exp(Q[b,h,i,:].K[b,g,j,:] * scale - lse[b,h,i])
+ * The statistic that osf_kv_evict selects by.
+ * Q: [B, Hq, Sq, D], K: [B, Hkv, Sk, D] of `dtype`; lse: contiguous float32 [B, Hq, Sq] as the
+ *    forward call returned it (a row with lse = -inf adds nothing); weights: contiguous float32
+ *    [B, Hkv, Sk].
+ * strides: NULL (contiguous) or 6 element strides, Q: b, h, s  K: b, h, s (>= 0; 0 broadcasts).
+ * mask, scale: as given to the forward call.  accumulate: 0 overwrites weights, else adds to them.
+ * workspace: osf_attn_key_weights_workspace_bytes bytes (may be 0).
+ * weights must not overlap an input -> else OSF_ERR_INVALID.  B == 0 or Sk == 0: OSF_OK, nothing
+ * written; Sq == 0: weights are zeroed (accumulate == 0) or left.  B * Hkv > 65535:
+ * OSF_ERR_UNSUPPORTED.  Other errors as in osf_attn_fwd_gqa_ex.  The result does not depend on the
+ * order in which anything runs.  No gradient: the weights are a statistic of a finished pass.
+ */
+int osf_attn_key_weights(const void *Q, const void *K, const float *lse, float *weights, int dtype,
+                         int B, int Hq, int Hkv, int Sq, int Sk, int D, const long long *strides,
+                         int mask, float scale, int accumulate, void *workspace, size_t workspace_bytes,
+                         osf_stream stream);
+int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                                         size_t *bytes);
+
+/*
+ * The 4-bit K/V cache (not on the pages, which keep K and V in their input type).
+ * A cache is a contiguous device array [B, Hkv, S] of records of osf_kv4_record_bytes(D) = 1.25 D
+ * bytes, 16-byte aligned, D a multiple of 32 up to 256 (others: OSF_ERR_UNSUPPORTED).  A record holds
+ * K and V of one token of one kv head; every 32 channels share a bfloat16 scale and minimum, and a
+ * 4-bit code c stands for minimum + scale * c:
+ *     minimum = the largest bfloat16 <= the group's smallest value
+ *     scale   = the smallest bfloat16 >= (largest value - minimum) / 15
+ *     c       = round((x - minimum) / scale), ties to even
+ * so a stored value is off by at most scale / 2.  These are the exact results of the formulas, not of
+ * their float32 evaluation.  A group that holds a NaN or an infinity reads back as NaN.
+ * Lengths are device int32 arrays [B] (tokens of a sequence that are valid, the same for all its kv
+ * heads); a length outside [0, S] is cut to it, and recorded as OSF_ERR_INVALID in the device status
+ * word (osf_device_status).  The caller keeps the lengths and advances them.
+ */
+int osf_kv4_record_bytes(int D, size_t *bytes);
+
+/*
+ * osf_kv4_append -- store the rows K, V [B, Hkv, n, D] (of `dtype`) as records lens[b] ..
+ * lens[b] + n - 1 of each sequence.  lens NULL: from record 0.  counts: NULL, or the number of new
+ * tokens of each sequence (0 .. n; the rows behind them are padding and are not read).  Records that
+ * would fall behind S are not written, and recorded as OSF_ERR_INVALID in the device status word, as
+ * are counts and lengths out of range.  No other record is touched.
+ * strides: NULL (contiguous) or 6 element strides, K: b, h, s  V: b, h, s.
+ * n == 0 or B == 0: OSF_OK.  n > S without counts, a cache that overlaps an input, NULL pointers:
+ * OSF_ERR_INVALID.
+ */
+int osf_kv4_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D,
+                   const long long *strides, void *cache, int S, const int *lens, const int *counts,
+                   osf_stream stream);
+
+/*
+ * osf_kv4_read -- the values of records starts[b] .. starts[b] + n - 1 (starts NULL: from 0) as
+ * contiguous K, V [B, Hkv, n, D] of `dtype`; positions at or behind lens[b] (NULL: S), or below 0, give
+ * zeros.  E.g. to run osf_attn_fwd_gqa_ex over a stored prefix.
+ */
+int osf_kv4_read(const void *cache, void *K, void *V, int dtype, int B, int Hkv, int n, int D, int S,
+                 const int *starts, const int *lens, osf_stream stream);
+
+/*
+ * osf_attn_kv4 -- attention of a few query rows per sequence over a 4-bit cache (the operation of
+ * osf_attn_fwd_gqa_ex, [Q3] "自注意力原理" + "GQA", with K and V the values the records stand for):
+ * Q, O: [B, Hq, Sq, D] of `dtype`; cache: [B, Hkv, S] records; lens: NULL (all S) or the valid
+ * records of each sequence.
+ * strides: NULL (contiguous) or 6 element strides, Q: b, h, s  O: b, h, s, under the rules of
+ *     osf_attn_fwd_gqa_ex.
+ * mask: OSF_MASK_NONE, or OSF_MASK_BOTTOM_RIGHT: row i sees records 0 .. i + lens[b] - Sq (the Sq
+ *     rows are the sequence's last tokens).  OSF_MASK_TOP_LEFT: OSF_ERR_INVALID.
+ *     A row that sees nothing gets O = 0 and lse = -inf.
+ * lse: optional contiguous float32 [B, Hq, Sq].
+ * weights: optional contiguous float32 [B, Hkv, S]: the attention weight of every record, summed over
+ *     the query heads of its kv head and the Sq rows, as in osf_attn_key_weights.  accumulate 0:
+ *     overwritten (0 at and behind lens[b]); else added to (at and behind lens[b] left as they are).
+ * workspace: osf_attn_kv4_workspace_bytes(..., with_weights = weights != NULL) bytes.
+ * (Hq / Hkv) * Sq <= 32768, else OSF_ERR_UNSUPPORTED.  Outputs must not overlap one another or an
+ * input -> else OSF_ERR_INVALID.  B == 0 or Sq == 0: OSF_OK, nothing written.
+ */
+int osf_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, int Hq, int Hkv, int Sq,
+                 int S, int D, const long long *strides, const int *lens, int mask, float scale,
+                 float *lse, float *weights, int accumulate, void *workspace, size_t workspace_bytes,
+                 osf_stream stream);
+int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int S, int D,
+                                 int with_weights, size_t *bytes);
+
+/*
+ * osf_kv_evict -- shrink a K/V cache to `budget` keys per (batch, kv head) by accumulated attention
+ * weight (not on the pages).  Of the n = lens[b] valid keys of each (b, kv head) (lens NULL: S): all,
+ * when n <= budget; else the first `sinks`, the last `recent`, and of those between the
+ * budget - sinks - recent with the largest weights[b, g, j] (a tie keeps the lower index; -0 equals
+ * 0; a NaN weight ranks below every number).  Kept rows stay in their order.
+ * src0, src1: the cache arrays [B, Hkv, S] of rows of row_bytes0 / row_bytes1 bytes (e.g. K and V
+ *     with D * sizeof(element), or one array of 4-bit records); either may be NULL with its dst.
+ * dst0, dst1: [B, Hkv, S_out] rows, S_out >= budget; dst == src (with S_out == S) moves in place,
+ *     any other overlap is OSF_ERR_INVALID.  Rows at and behind the new length are left as they were.
+ * weights [B, Hkv, S] -> weights_out [B, Hkv, S_out]: the kept keys' weights, 0 behind them;
+ *     weights_out == weights (with S_out == S) is allowed.
+ * lens_out: NULL, or [B] receiving min(lens[b], budget); may be lens itself.
+ * idx: int32 [B, Hkv, budget] receiving the kept positions in ascending order, -1 behind them.
+ * budget >= 1, sinks + recent <= budget, S < 2^30 and budget * row_bytes < 2^31 are required.
+ */
+int osf_kv_evict(const void *src0, void *dst0, long long row_bytes0, const void *src1, void *dst1,
+                 long long row_bytes1, const float *weights, float *weights_out, const int *lens,
+                 int *lens_out, int *idx, int B, int Hkv, int S, int S_out, int budget, int sinks,
+                 int recent, osf_stream stream);
+
+/*
  * osf_softmax_rows -- row softmax, [TP] "Puzzle 8: Long Softmax" / [SO] "Online Softmax":
  *     z[r, j] = exp(x[r, j] - m_r) / l_r,  m_r = max_j x[r, j],  l_r = sum_j exp(x[r, j] - m_r)
  * x, z: [rows, T] float32 row-major, device.  z == x (in place) is allowed; any other overlap

@@ -20,6 +20,8 @@ __all__ = [
     "solve", "osf_attn_fwd_gqa_ex", "osf_softmax_rows_ex", "osf_softmax_ex_workspace_bytes",
     "osf_attn_bwd_gqa", "osf_attn_bwd_workspace_bytes", "osf_selftest_bounded_wait", "OSF_MASK_NONE", "OSF_MASK_TOP_LEFT", "OSF_MASK_BOTTOM_RIGHT",
     "osf_attn_fwd_gqa_host", "osf_attn_host_buffer_bytes",
+    "osf_attn_key_weights", "osf_attn_key_weights_workspace_bytes", "osf_kv4_record_bytes", "osf_kv4_append",
+    "osf_kv4_read", "osf_attn_kv4", "osf_attn_kv4_workspace_bytes", "osf_kv_evict",
 ]
 
 OSF_OK, OSF_ERR_INVALID, OSF_ERR_UNSUPPORTED, OSF_ERR_CUDA, OSF_ERR_TIMEOUT, OSF_ERR_WORKSPACE = range(6)
@@ -48,6 +50,14 @@ _SIGS = {
     "osf_attn_bwd_gqa": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                               _vp, _sz, _vp]),
     "osf_attn_bwd_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_attn_key_weights": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _f, _i, _vp, _sz, _vp]),
+    "osf_attn_key_weights_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_kv4_record_bytes": (_i, [_i, ctypes.POINTER(_sz)]),
+    "osf_kv4_append": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp]),
+    "osf_kv4_read": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "osf_attn_kv4": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _vp, _sz, _vp]),
+    "osf_attn_kv4_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_kv_evict": (_i, [_vp, _vp, _ll, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "osf_selftest_bounded_wait": (_i, [ctypes.c_ulonglong, _vp]),
     "osf_softmax_workspace_bytes": (_i, [_ll, _ll, ctypes.POINTER(_sz)]),
     "osf_device_status": (_i, [_vp]),
@@ -345,6 +355,215 @@ def osf_softmax_rows_ex(x, z=None, out_dtype=None, scale: float = 1.0, causal_pe
                                      float(scale), int(causal_period), _ptr(ws), ws_bytes, _stream(x.device)),
            "osf_softmax_rows_ex")
     return z
+
+
+def osf_attn_key_weights_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, Sk, D) -> int:
+    n = _sz(0)
+    _check(lib().osf_attn_key_weights_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, ctypes.byref(n)),
+           "osf_attn_key_weights_workspace_bytes")
+    return n.value
+
+
+def _view_strides(*named):
+    """The b, h, s element strides of [B, H, S, D] views, or None when all are contiguous."""
+    for name, t in named:
+        if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
+            raise ValueError(f"{name} must be a 4-D [B, H, S, D] view with a contiguous last dimension")
+    if all(t.is_contiguous() for _, t in named):
+        return None
+    st = (ctypes.c_longlong * (3 * len(named)))(*(int(t.stride(i)) for _, t in named for i in range(3)))
+    return ctypes.cast(st, ctypes.c_void_p)
+
+
+def _need(t, name: str, shape, dtype) -> None:
+    """A contiguous CUDA tensor of this shape and dtype, or None."""
+    if t is None:
+        return
+    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+
+
+def _same_device(first, *rest) -> None:
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors of a call must be on one device")
+
+
+def _kv4_dims(cache, D: int):
+    """(B, Hkv, S) of a contiguous uint8 [B, Hkv, S, osf_kv4_record_bytes(D)] cache."""
+    if not cache.is_cuda or cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() or \
+            cache.shape[3] != osf_kv4_record_bytes(D):
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, Hkv, S, osf_kv4_record_bytes(D)]")
+    return cache.shape[0], cache.shape[1], cache.shape[2]
+
+
+def osf_attn_key_weights(q, k, lse, weights=None, mask="none", scale: float | None = None, accumulate: bool = False,
+                         workspace=None):
+    """The attention weight every key receives, float32 [B, Hkv, Sk]: the softmax matrix of the forward
+    call that returned ``lse``, summed over the query heads of each kv head and over the rows.  ``q``,
+    ``k``: [B, H, S, D] views as in osf_attn_fwd_gqa_ex, ``mask`` and ``scale`` as given to it;
+    ``accumulate`` adds to ``weights`` instead of overwriting them.  Returns ``weights`` (allocated if
+    None)."""
+    _need_cuda(q, k, contiguous=False)
+    _same_device(q, k, lse, weights, workspace)
+    st = _view_strides(("q", q), ("k", k))
+    B, Hq, Sq, D = q.shape
+    Hkv, Sk = k.shape[1], k.shape[2]
+    if k.dtype != q.dtype or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("q and k must agree in dtype, batch and head dimension")
+    if weights is None:
+        if accumulate:
+            raise ValueError("accumulate needs the weights to add to")
+        weights = torch.empty((B, Hkv, Sk), dtype=torch.float32, device=q.device)
+    _need(lse, "lse", (B, Hq, Sq), torch.float32)
+    _need(weights, "weights", (B, Hkv, Sk), torch.float32)
+    dt = _dtype_code(q)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            workspace = _workspace(osf_attn_key_weights_workspace_bytes(dt, B, Hq, Hkv, Sq, Sk, D), q.device, None)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        m = _MASKS[mask] if isinstance(mask, str) else int(mask)
+        _check(lib().osf_attn_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(weights), dt, B, Hq, Hkv, Sq, Sk, D, st, m,
+                                          0.0 if scale is None else float(scale), int(bool(accumulate)),
+                                          _ptr(workspace), ws_bytes, _stream(q.device)),
+               "osf_attn_key_weights")
+    return weights
+
+
+def osf_kv4_record_bytes(D: int) -> int:
+    """Bytes of one 4-bit record (K and V of one token of one kv head): 1.25 D."""
+    n = _sz(0)
+    _check(lib().osf_kv4_record_bytes(int(D), ctypes.byref(n)), "osf_kv4_record_bytes")
+    return n.value
+
+
+def osf_kv4_append(k, v, cache, lens=None, counts=None):
+    """Store the rows ``k``, ``v`` ([B, Hkv, n, D] views, float32 or bfloat16) in the 4-bit ``cache``
+    (uint8 [B, Hkv, S, osf_kv4_record_bytes(D)]) behind the ``lens`` (int32 [B]; None: 0) tokens that
+    each sequence has; ``counts`` (int32 [B]): how many of the n are new, the rest being padding.
+    Returns ``cache``; the caller advances its lengths."""
+    _need_cuda(k, v, contiguous=False)
+    _same_device(k, v, cache, lens, counts)
+    st = _view_strides(("k", k), ("v", v))
+    B, Hkv, n, D = k.shape
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must agree in shape and dtype")
+    cb, ch, S = _kv4_dims(cache, D)
+    if (cb, ch) != (B, Hkv):
+        raise ValueError("cache must have the batch and kv heads of k")
+    _need(lens, "lens", (B,), torch.int32)
+    _need(counts, "counts", (B,), torch.int32)
+    with torch.cuda.device(k.device):
+        _check(lib().osf_kv4_append(_ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n, D, st, _ptr(cache), S, _ptr(lens),
+                                    _ptr(counts), _stream(k.device)),
+               "osf_kv4_append")
+    return cache
+
+
+def osf_kv4_read(cache, D: int, n: int, starts=None, lens=None, k=None, v=None, dtype=torch.bfloat16):
+    """The values of records starts[b] .. starts[b] + n - 1 (``starts`` None: from 0) of a 4-bit cache,
+    as contiguous (k, v) [B, Hkv, n, D] of ``dtype`` (or given tensors); zeros at and behind
+    ``lens``."""
+    B, Hkv, S = _kv4_dims(cache, D)
+    k = torch.empty((B, Hkv, n, D), dtype=dtype, device=cache.device) if k is None else k
+    v = torch.empty((B, Hkv, n, D), dtype=k.dtype, device=cache.device) if v is None else v
+    _same_device(cache, k, v, starts, lens)
+    _need(k, "k", (B, Hkv, n, D), k.dtype)
+    _need(v, "v", (B, Hkv, n, D), k.dtype)
+    _need(starts, "starts", (B,), torch.int32)
+    _need(lens, "lens", (B,), torch.int32)
+    with torch.cuda.device(cache.device):
+        _check(lib().osf_kv4_read(_ptr(cache), _ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n, D, S, _ptr(starts),
+                                  _ptr(lens), _stream(cache.device)),
+               "osf_kv4_read")
+    return k, v
+
+
+def osf_attn_kv4_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, S, D, with_weights: bool = False) -> int:
+    n = _sz(0)
+    _check(lib().osf_attn_kv4_workspace_bytes(dtype, B, Hq, Hkv, Sq, S, D, int(bool(with_weights)), ctypes.byref(n)),
+           "osf_attn_kv4_workspace_bytes")
+    return n.value
+
+
+def osf_attn_kv4(q, cache, lens=None, out=None, mask="none", scale: float | None = None, lse=None, weights=None,
+                 accumulate: bool = False, workspace=None):
+    """Attention of ``q`` ([B, Hq, Sq, D] view) over a 4-bit cache, ``lens`` (int32 [B]; None: all) of
+    whose records are valid; ``mask`` "none" or "bottom_right" (the Sq rows are the last tokens of each
+    sequence).  ``weights`` (float32 [B, Hkv, S]) receives, or with ``accumulate`` gains, the attention
+    weight of every record.  Returns ``out`` (a contiguous tensor if None)."""
+    _need_cuda(q, out, contiguous=False)
+    _same_device(q, cache, lens, out, lse, weights, workspace)
+    B, Hq, Sq, D = q.shape
+    cb, Hkv, S = _kv4_dims(cache, D)
+    if out is None:
+        out = torch.empty((B, Hq, Sq, D), dtype=q.dtype, device=q.device)
+    if cb != B or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q, out and cache must agree in batch, shape and dtype")
+    if accumulate and weights is None:
+        raise ValueError("accumulate needs the weights to add to")
+    st = _view_strides(("q", q), ("out", out))
+    _need(lens, "lens", (B,), torch.int32)
+    _need(lse, "lse", (B, Hq, Sq), torch.float32)
+    _need(weights, "weights", (B, Hkv, S), torch.float32)
+    dt = _dtype_code(q)
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            n = osf_attn_kv4_workspace_bytes(dt, B, Hq, Hkv, Sq, S, D, weights is not None)
+            workspace = _workspace(n, q.device, None)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        m = _MASKS[mask] if isinstance(mask, str) else int(mask)
+        _check(lib().osf_attn_kv4(_ptr(q), _ptr(cache), _ptr(out), dt, B, Hq, Hkv, Sq, S, D, st, _ptr(lens), m,
+                                  0.0 if scale is None else float(scale), _ptr(lse), _ptr(weights),
+                                  int(bool(accumulate)), _ptr(workspace), ws_bytes, _stream(q.device)),
+               "osf_attn_kv4")
+    return out
+
+
+def osf_kv_evict(k, v, weights, budget: int, lens=None, sinks: int = 0, recent: int = 0, k_out=None, v_out=None,
+                 weights_out=None, lens_out=None, idx=None):
+    """Shrink a cache to ``budget`` keys per (batch, kv head): the first ``sinks``, the last ``recent`` and
+    the heaviest of the rest by ``weights`` (float32 [B, Hkv, S]), in their old order.  ``k``, ``v``:
+    contiguous [B, Hkv, S, ...] arrays of any dtype (``v`` None: ``k`` alone, e.g. 4-bit records);
+    ``lens`` (int32 [B]; None: S) valid keys.  Outputs default to new [B, Hkv, budget, ...] tensors
+    (rows behind a shorter sequence are then zero); pass ``k_out=k`` and so on to move in place.
+    Returns (k_out, v_out, weights_out, lens_out, idx)."""
+    _need_cuda(k, v, weights)
+    _same_device(k, v, weights, lens, k_out, v_out, weights_out, lens_out, idx)
+    B, Hkv, S = weights.shape
+    budget = int(budget)
+    for name, t in (("k", k), ("v", v)):
+        if t is not None and tuple(t.shape[:3]) != (B, Hkv, S):
+            raise ValueError(f"{name} must be [B, Hkv, S, ...] with the sizes of weights")
+    _need(weights, "weights", (B, Hkv, S), torch.float32)
+    _need(lens, "lens", (B,), torch.int32)
+    given = next((t for t in (k_out, v_out, weights_out) if t is not None), None)
+    S_out = budget if given is None else given.shape[2]
+    dev = k.device
+    k_out = torch.zeros((B, Hkv, S_out, *k.shape[3:]), dtype=k.dtype, device=dev) if k_out is None else k_out
+    if v is not None and v_out is None:
+        v_out = torch.zeros((B, Hkv, S_out, *v.shape[3:]), dtype=v.dtype, device=dev)
+    weights_out = torch.empty((B, Hkv, S_out), device=dev) if weights_out is None else weights_out
+    lens_out = torch.empty(B, dtype=torch.int32, device=dev) if lens_out is None else lens_out
+    idx = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev) if idx is None else idx
+    _need(k_out, "k_out", (B, Hkv, S_out, *k.shape[3:]), k.dtype)
+    if v is not None:
+        _need(v_out, "v_out", (B, Hkv, S_out, *v.shape[3:]), v.dtype)
+    elif v_out is not None:
+        raise ValueError("v_out without v")
+    _need(weights_out, "weights_out", (B, Hkv, S_out), torch.float32)
+    _need(lens_out, "lens_out", (B,), torch.int32)
+    _need(idx, "idx", (B, Hkv, budget), torch.int32)
+
+    def row(t):
+        return 0 if t is None else t.element_size() * int(t.shape[3:].numel())
+
+    with torch.cuda.device(dev):
+        _check(lib().osf_kv_evict(_ptr(k), _ptr(k_out), row(k), _ptr(v), _ptr(v_out), row(v), _ptr(weights),
+                                  _ptr(weights_out), _ptr(lens), _ptr(lens_out), _ptr(idx), B, Hkv, S, S_out, budget,
+                                  int(sinks), int(recent), _stream(dev)),
+               "osf_kv_evict")
+    return k_out, v_out, weights_out, lens_out, idx
 
 
 def osf_selftest_bounded_wait(limit_ns: int = 1_000_000) -> int:

@@ -17,6 +17,9 @@
 #include "selftest.cuh"
 #include "attn_tc.cuh"
 #include "decode.cuh"
+#include "kv4.cuh"
+#include "key_weights.cuh"
+#include "kv_evict.cuh"
 
 namespace osf {
 
@@ -744,6 +747,296 @@ int osf_softmax_rows_ex(const void *x, void *z, int x_dtype, int z_dtype, long l
     SoftmaxExProblem q{x, z, x_dtype, z_dtype, rows, T, xs, zs, sc * kLog2e, causal_period, dev->sm_count,
                        dev->status};
     return launch_status(launch_softmax_ex(q, static_cast<float *>(workspace), (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ weights of keys
+// Shared validation of osf_attn_key_weights; `strides`: NULL (contiguous) or Q, K x (b, h, s).
+static int check_key_weights(const void *Q, const void *K, const float *lse, float *weights, int dtype, int B, int Hq,
+                             int Hkv, int Sq, int Sk, int D, const long long *strides, int mask, float scale,
+                             KeyWeightsProblem &w, bool &empty) {
+    // the forward problem's checks, with V = K and an output that overlaps nothing
+    AttnProblem p;
+    long long st[12];
+    if (strides) {
+        for (int i = 0; i < 6; ++i) st[i] = strides[i];
+        for (int i = 0; i < 3; ++i) st[6 + i] = strides[3 + i];
+        st[9] = (long long)Hq * Sq * D;
+        st[10] = (long long)Sq * D;
+        st[11] = D;
+    }
+    empty = false;
+    if (Sq == 0 && Sk > 0 && B > 0) {   // no rows: the weights are zero, so the sizes alone matter
+        const int st0 = check_gqa_ex(K, K, K, reinterpret_cast<void *>(~uintptr_t(0) >> 8), dtype, B, Hq, Hkv, 1, Sk, D,
+                                     nullptr, mask, scale, nullptr, p, empty);
+        if (st0 != OSF_OK) return st0;
+    } else {
+        // the placeholder output lies above every address in use
+        const int st0 = check_gqa_ex(Q, K, K, reinterpret_cast<void *>(~uintptr_t(0) >> 8), dtype, B, Hq, Hkv, Sq, Sk, D,
+                                     strides ? st : nullptr, mask, scale, nullptr, p, empty);
+        if (st0 != OSF_OK || empty) return st0;
+        if (!lse) return OSF_ERR_INVALID;
+    }
+    if (!weights) return OSF_ERR_INVALID;
+    if ((long long)B * Hkv > 65535) return OSF_ERR_UNSUPPORTED;
+    w = KeyWeightsProblem{};
+    w.q = Q; w.k = K; w.lse = lse; w.w = weights;
+    w.dtype = dtype; w.B = B; w.Hq = Hq; w.Hkv = Hkv; w.Sq = Sq; w.Sk = Sk; w.D = D;
+    if (Sq == 0) return OSF_OK;
+    w.causal = p.causal; w.causal_off = p.causal_off; w.scale_log2 = p.scale_log2;
+    w.q_sb = p.q_sb; w.q_sh = p.q_sh; w.q_ss = p.q_ss;
+    w.k_sb = p.k_sb; w.k_sh = p.k_sh; w.k_ss = p.k_ss;
+    const size_t es = elem_size(dtype), nw = (size_t)B * Hkv * Sk * sizeof(float);
+    if (overlaps(weights, nw, Q, span_bytes(B, Hq, Sq, D, w.q_sb, w.q_sh, w.q_ss, es)) ||
+        overlaps(weights, nw, K, span_bytes(B, Hkv, Sk, D, w.k_sb, w.k_sh, w.k_ss, es)) ||
+        overlaps(weights, nw, lse, (size_t)B * Hq * Sq * sizeof(float)))
+        return OSF_ERR_INVALID;
+    return OSF_OK;
+}
+
+static size_t key_weights_partial_bytes(const KeyWeightsProblem &w, int splits) {
+    return splits > 1 ? align256((size_t)splits * w.B * w.Hkv * w.Sk * sizeof(float)) : 0;
+}
+
+int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    KeyWeightsProblem w;
+    bool empty;
+    const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
+    const int st = check_key_weights(ph, ph, static_cast<const float *>(ph), reinterpret_cast<float *>(uintptr_t(1) << 44),
+                                     dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, OSF_MASK_NONE, 0.f, w, empty);
+    if (st != OSF_OK || empty || Sq == 0) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    *bytes = key_weights_partial_bytes(w, key_weights_simt_splits(w, dev->sm_count));
+    return OSF_OK;
+}
+
+int osf_attn_key_weights(const void *Q, const void *K, const float *lse, float *weights, int dtype, int B, int Hq, int Hkv,
+                         int Sq, int Sk, int D, const long long *strides, int mask, float scale, int accumulate,
+                         void *workspace, size_t workspace_bytes, osf_stream stream) {
+    KeyWeightsProblem w;
+    bool empty;
+    const int st = check_key_weights(Q, K, lse, weights, dtype, B, Hq, Hkv, Sq, Sk, D, strides, mask, scale, w, empty);
+    if (st != OSF_OK || empty) return st;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (Sq == 0)
+        return accumulate ? OSF_OK
+                          : launch_status(cudaMemsetAsync(weights, 0, (size_t)B * Hkv * Sk * sizeof(float), s));
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    w.accumulate = accumulate != 0;
+    w.status = dev->status;
+    w.splits = key_weights_simt_splits(w, dev->sm_count);
+    const size_t need = key_weights_partial_bytes(w, w.splits);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
+    w.part = static_cast<float *>(workspace);
+    cudaError_t e = launch_key_weights_simt(w, s);
+    if (e == cudaSuccess && w.splits > 1) e = launch_key_weights_reduce(w, s);
+    return launch_status(e);
+}
+
+// ------------------------------------------------------------------ 4-bit cache
+int osf_kv4_record_bytes(int D, size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    if (D <= 0) return OSF_ERR_INVALID;
+    if (D > 256 || D % kKv4Group != 0) return OSF_ERR_UNSUPPORTED;
+    *bytes = (size_t)kv4_record_bytes(D);
+    return OSF_OK;
+}
+
+// Sizes shared by the calls on a cache [B, Hkv, S, record].
+static int check_kv4(int dtype, int B, int Hkv, long long n, int S, int D) {
+    if (dtype != OSF_F32 && dtype != OSF_BF16) return OSF_ERR_INVALID;
+    if (B < 0 || Hkv <= 0 || n < 0 || S < 0) return OSF_ERR_INVALID;
+    size_t rec;
+    const int st = osf_kv4_record_bytes(D, &rec);
+    if (st != OSF_OK) return st;
+    if ((long long)B * Hkv > 65535 || (long long)n * D >= (1LL << 31) || (long long)S * D >= (1LL << 31))
+        return OSF_ERR_UNSUPPORTED;
+    return OSF_OK;
+}
+
+int osf_kv4_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D, const long long *strides, void *cache,
+                   int S, const int *lens, const int *counts, osf_stream stream) {
+    const int st = check_kv4(dtype, B, Hkv, n, S, D);
+    if (st != OSF_OK) return st;
+    Kv4StoreProblem p{};
+    long long sd[6] = {(long long)Hkv * n * D, (long long)n * D, D, (long long)Hkv * n * D, (long long)n * D, D};
+    if (strides)
+        for (int i = 0; i < 6; ++i) {
+            if (strides[i] < 0) return OSF_ERR_INVALID;
+            if (strides[i] >= (1LL << 40)) return OSF_ERR_UNSUPPORTED;
+            sd[i] = strides[i];
+        }
+    if (B == 0 || n == 0) return OSF_OK;
+    if (n > S && !counts) return OSF_ERR_INVALID;
+    if (!K || !V || !cache || (reinterpret_cast<uintptr_t>(cache) & 15u) != 0) return OSF_ERR_INVALID;
+    const size_t es = elem_size(dtype), nc = (size_t)B * Hkv * S * kv4_record_bytes(D);
+    if (overlaps(cache, nc, K, span_bytes(B, Hkv, n, D, sd[0], sd[1], sd[2], es)) ||
+        overlaps(cache, nc, V, span_bytes(B, Hkv, n, D, sd[3], sd[4], sd[5], es)) ||
+        overlaps(cache, nc, lens, (size_t)B * 4) || overlaps(cache, nc, counts, (size_t)B * 4))
+        return OSF_ERR_INVALID;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    p.k = K; p.v = V; p.cache = static_cast<unsigned char *>(cache); p.lens = lens; p.counts = counts;
+    p.dtype = dtype; p.B = B; p.Hkv = Hkv; p.n = n; p.S = S; p.D = D;
+    p.k_sb = sd[0]; p.k_sh = sd[1]; p.k_ss = sd[2]; p.v_sb = sd[3]; p.v_sh = sd[4]; p.v_ss = sd[5];
+    p.status = dev->status;
+    return launch_status(launch_kv4_append(p, dev->sm_count, (cudaStream_t)stream));
+}
+
+int osf_kv4_read(const void *cache, void *K, void *V, int dtype, int B, int Hkv, int n, int D, int S, const int *starts,
+                 const int *lens, osf_stream stream) {
+    const int st = check_kv4(dtype, B, Hkv, n, S, D);
+    if (st != OSF_OK) return st;
+    if (B == 0 || n == 0) return OSF_OK;
+    if (!K || !V || (!cache && S > 0) || (reinterpret_cast<uintptr_t>(cache) & 15u) != 0) return OSF_ERR_INVALID;
+    const size_t no = (size_t)B * Hkv * n * D * elem_size(dtype), nc = (size_t)B * Hkv * S * kv4_record_bytes(D);
+    if (overlaps(K, no, V, no) || overlaps(K, no, cache, nc) || overlaps(V, no, cache, nc) ||
+        overlaps(K, no, lens, (size_t)B * 4) || overlaps(V, no, lens, (size_t)B * 4) ||
+        overlaps(K, no, starts, (size_t)B * 4) || overlaps(V, no, starts, (size_t)B * 4))
+        return OSF_ERR_INVALID;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    Kv4StoreProblem p{};
+    p.ko = K; p.vo = V; p.cache = static_cast<unsigned char *>(const_cast<void *>(cache)); p.lens = lens; p.starts = starts;
+    p.dtype = dtype; p.B = B; p.Hkv = Hkv; p.n = n; p.S = S; p.D = D;
+    p.status = dev->status;
+    return launch_status(launch_kv4_read(p, dev->sm_count, (cudaStream_t)stream));
+}
+
+// Sizes and layout of an attention call over records; fills kp (without workspace pointers).
+static int check_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, int Hq, int Hkv, int Sq, int S, int D,
+                          const long long *strides, const int *lens, int mask, float scale, float *lse, float *weights,
+                          Kv4AttnProblem &kp, bool &empty) {
+    empty = false;
+    const int st = check_kv4(dtype, B, Hkv, 0, S, D);
+    if (st != OSF_OK) return st;
+    if (Hq <= 0 || Hq % Hkv != 0 || Sq < 0) return OSF_ERR_INVALID;
+    if (mask != OSF_MASK_NONE && mask != OSF_MASK_BOTTOM_RIGHT) return OSF_ERR_INVALID;
+    if (!(scale == scale)) return OSF_ERR_INVALID;
+    long long sd[6] = {(long long)Hq * Sq * D, (long long)Sq * D, D, (long long)Hq * Sq * D, (long long)Sq * D, D};
+    if (strides)
+        for (int i = 0; i < 6; ++i) {
+            if (strides[i] < 0) return OSF_ERR_INVALID;
+            if (strides[i] >= (1LL << 40)) return OSF_ERR_UNSUPPORTED;
+            sd[i] = strides[i];
+        }
+    // the query rows of one kv head number at most 2^15: one CTA column per few of them
+    if ((long long)(Hq / Hkv) * Sq > (1LL << 15)) return OSF_ERR_UNSUPPORTED;
+    if (B == 0 || Sq == 0) { empty = true; return OSF_OK; }
+    if (!Q || !O || (!cache && S > 0) || (reinterpret_cast<uintptr_t>(cache) & 15u) != 0) return OSF_ERR_INVALID;
+    if (!rows_disjoint(B, Hq, Sq, D, sd[3], sd[4], sd[5])) return OSF_ERR_INVALID;
+    const size_t es = elem_size(dtype);
+    const void *bufs[6] = {O, lse, weights, Q, cache, lens};
+    const size_t size[6] = {span_bytes(B, Hq, Sq, D, sd[3], sd[4], sd[5], es), (size_t)B * Hq * Sq * sizeof(float),
+                            (size_t)B * Hkv * S * sizeof(float), span_bytes(B, Hq, Sq, D, sd[0], sd[1], sd[2], es),
+                            (size_t)B * Hkv * S * kv4_record_bytes(D), (size_t)B * sizeof(int)};
+    for (int i = 0; i < 3; ++i)   // no output overlaps another buffer
+        for (int j = i + 1; j < 6; ++j)
+            if (overlaps(bufs[i], size[i], bufs[j], size[j])) return OSF_ERR_INVALID;
+    kp = Kv4AttnProblem{};
+    AttnProblem &p = kp.a;
+    p.q = Q; p.o = O; p.lse = lse;
+    p.dtype = dtype; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Sk = S; p.D = D;
+    p.causal = mask == OSF_MASK_BOTTOM_RIGHT && Sq > 1;   // one row sees every valid key
+    p.q_sb = sd[0]; p.q_sh = sd[1]; p.q_ss = sd[2]; p.o_sb = sd[3]; p.o_sh = sd[4]; p.o_ss = sd[5];
+    p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
+    p.splits = 1;
+    kp.cache = static_cast<const unsigned char *>(cache);
+    kp.lens = lens;
+    kp.weights = weights;
+    return OSF_OK;
+}
+
+// Workspace: split partial states | scores and the log-sum-exp, with weights.
+static size_t kv4_lse_bytes(const Kv4AttnProblem &kp) { return align256((size_t)kp.a.B * kp.a.Hq * kp.a.Sq * sizeof(float)); }
+static size_t kv4_scores_bytes(const Kv4AttnProblem &kp) {
+    return align256((size_t)kp.a.B * kp.a.Hq * kp.a.Sq * kp.a.Sk * sizeof(float));
+}
+static size_t kv4_workspace(const Kv4AttnProblem &kp, int splits, bool weights) {
+    return partial_bytes(splits, (long long)kp.a.B * kp.a.Hq * kp.a.Sq, kp.a.D) +
+           (weights ? kv4_lse_bytes(kp) + kv4_scores_bytes(kp) : 0);
+}
+
+int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int S, int D, int with_weights, size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    Kv4AttnProblem kp;
+    bool empty;
+    const int st = check_attn_kv4(reinterpret_cast<const void *>(uintptr_t(1) << 40), reinterpret_cast<const void *>(uintptr_t(1) << 50),
+                                  reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, S, D, nullptr, nullptr,
+                                  OSF_MASK_NONE, 0.f, nullptr, nullptr, kp, empty);
+    if (st != OSF_OK || empty) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    *bytes = kv4_workspace(kp, kv4_attn_pick_splits(kp, dev->sm_count), with_weights != 0);
+    return OSF_OK;
+}
+
+int osf_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, int Hq, int Hkv, int Sq, int S, int D,
+                 const long long *strides, const int *lens, int mask, float scale, float *lse, float *weights, int accumulate,
+                 void *workspace, size_t workspace_bytes, osf_stream stream) {
+    Kv4AttnProblem kp;
+    bool empty;
+    const int st = check_attn_kv4(Q, cache, O, dtype, B, Hq, Hkv, Sq, S, D, strides, lens, mask, scale, lse, weights, kp, empty);
+    if (st != OSF_OK || empty) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    AttnProblem &p = kp.a;
+    p.status = dev->status;
+    p.splits = kv4_attn_pick_splits(kp, dev->sm_count);
+    kp.accumulate = accumulate != 0;
+    const long long rows = (long long)B * Hq * Sq;
+    const size_t need = kv4_workspace(kp, p.splits, weights != nullptr);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
+    if (p.splits > 1) carve_partials(p, workspace, rows);
+    if (weights) {
+        char *at = static_cast<char *>(workspace) + partial_bytes(p.splits, rows, D);
+        if (!p.lse) p.lse = reinterpret_cast<float *>(at);
+        kp.scores = reinterpret_cast<float *>(at + kv4_lse_bytes(kp));
+    }
+    return launch_status(launch_attn_kv4(kp, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ eviction
+int osf_kv_evict(const void *src0, void *dst0, long long row_bytes0, const void *src1, void *dst1, long long row_bytes1,
+                 const float *weights, float *weights_out, const int *lens, int *lens_out, int *idx, int B, int Hkv, int S,
+                 int S_out, int budget, int sinks, int recent, osf_stream stream) {
+    if (B < 0 || Hkv <= 0 || S < 0 || budget < 1 || sinks < 0 || recent < 0 || S_out < budget) return OSF_ERR_INVALID;
+    if ((long long)sinks + recent > budget) return OSF_ERR_INVALID;
+    if ((src0 && row_bytes0 < 1) || (src1 && row_bytes1 < 1)) return OSF_ERR_INVALID;
+    if ((src0 == nullptr) != (dst0 == nullptr) || (src1 == nullptr) != (dst1 == nullptr)) return OSF_ERR_INVALID;
+    if ((long long)B * Hkv > 65535 || S >= (1 << 30) || S_out >= (1 << 30)) return OSF_ERR_UNSUPPORTED;
+    if ((src0 && row_bytes0 * budget >= (1LL << 31)) || (src1 && row_bytes1 * budget >= (1LL << 31))) return OSF_ERR_UNSUPPORTED;
+    if (B == 0) return OSF_OK;
+    if ((!weights && S > 0) || !weights_out || !idx) return OSF_ERR_INVALID;
+    const size_t heads = (size_t)B * Hkv;
+    // buffers read | buffers written; a pair that is the same buffer with the same row count is moved in place
+    const void *in[4] = {src0, src1, weights, lens};
+    const size_t in_n[4] = {heads * S * (src0 ? row_bytes0 : 0), heads * S * (src1 ? row_bytes1 : 0), heads * S * 4, (size_t)B * 4};
+    void *out[5] = {dst0, dst1, weights_out, lens_out, idx};
+    const size_t out_n[5] = {heads * S_out * (dst0 ? row_bytes0 : 0), heads * S_out * (dst1 ? row_bytes1 : 0), heads * S_out * 4,
+                             (size_t)B * 4, heads * budget * 4};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < 4; ++i) {
+            const bool in_place = o == i && in[i] == out[o] && (o == 3 || S == S_out);
+            if (!in_place && overlaps(out[o], out_n[o], in[i], in_n[i])) return OSF_ERR_INVALID;
+        }
+        for (int o2 = o + 1; o2 < 5; ++o2)
+            if (overlaps(out[o], out_n[o], out[o2], out_n[o2])) return OSF_ERR_INVALID;
+    }
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    EvictProblem p{};
+    p.w = weights; p.w_out = weights_out; p.lens = lens; p.lens_out = lens_out; p.idx = idx;
+    p.src[0] = static_cast<const unsigned char *>(src0); p.dst[0] = static_cast<unsigned char *>(dst0); p.row_bytes[0] = row_bytes0;
+    p.src[1] = static_cast<const unsigned char *>(src1); p.dst[1] = static_cast<unsigned char *>(dst1); p.row_bytes[1] = row_bytes1;
+    p.B = B; p.Hkv = Hkv; p.S = S; p.S_out = S_out; p.budget = budget; p.sinks = sinks; p.recent = recent;
+    p.status = dev->status;
+    return launch_status(launch_kv_evict(p, dev->sm_count, (cudaStream_t)stream));
 }
 
 int osf_selftest_bounded_wait(unsigned long long limit_ns, osf_stream stream) {

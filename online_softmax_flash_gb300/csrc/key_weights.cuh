@@ -1,0 +1,31 @@
+// Accumulated attention weight of every key (osf_attn_key_weights).
+#pragma once
+
+#include "osf_internal.cuh"
+
+namespace osf {
+
+struct KeyWeightsProblem {
+    const void *q, *k;
+    const float *lse;           // [B, Hq, Sq] natural log; -inf: the row sees no key
+    float *w;                   // [B, Hkv, Sk]
+    int dtype, B, Hq, Hkv, Sq, Sk, D;
+    int causal, causal_off;     // key j is visible to row i iff !causal or j <= i + causal_off
+    float scale_log2;           // scale * log2(e)
+    long long q_sb, q_sh, q_ss, k_sb, k_sh, k_ss;
+    int accumulate;
+    int splits;                 // parts of the rows, each with its own partial sums [splits][B * Hkv * Sk]
+    float *part;
+    int *status;
+};
+
+// Base-2 exponent offset of a row with this log-sum-exp: a row that sees nothing adds nothing.
+__device__ __forceinline__ float row_offset(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
+
+// CUDA-core kernel: any type, head dimension and strides.
+int key_weights_simt_splits(const KeyWeightsProblem &p, int sm_count);
+cudaError_t launch_key_weights_simt(const KeyWeightsProblem &p, cudaStream_t s);
+// w (+)= the sum of the splits' parts, in split order.
+cudaError_t launch_key_weights_reduce(const KeyWeightsProblem &p, cudaStream_t s);
+
+}  // namespace osf

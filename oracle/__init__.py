@@ -25,12 +25,13 @@ force, worked examples and invariants (``tests/test_oracle_pins.py``).
 """
 from .attention import attention, attention_gqa, attention_rows
 from .attention_bwd import attention_bwd, attention_gqa_bwd
+from .kv_cache import attention_records, evict, key_weights, quantise_group, record_values, records, visible
 from .softmax import softmax, softmax_masked
 from .recurrence import (combine_partials, online_attention_row, online_softmax,
                          online_softmax_state)
 
 __all__ = [
     "attention", "attention_gqa", "attention_rows", "attention_bwd", "attention_gqa_bwd", "softmax",
-    "softmax_masked",
+    "softmax_masked", "attention_records", "evict", "key_weights", "quantise_group", "record_values", "records", "visible",
     "online_softmax_state", "online_softmax", "online_attention_row", "combine_partials",
 ]
