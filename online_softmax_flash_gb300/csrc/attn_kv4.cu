@@ -4,13 +4,17 @@
 // online-softmax state (m, l, acc), and the log-sum-exp combine merges them.  The parts are cut from each
 // sequence's own length, on the device, so a ragged batch splits every sequence evenly.
 //
-// This kernel is the general one: any D that is a multiple of 32, float32 or bfloat16 queries.  A warp takes 32 keys
+// Two kernels.  The tensor-core one (bfloat16 queries, D 64 or 128) is described where it starts.  The
+// general one takes any D that is a multiple of 32 and float32 or bfloat16 queries.  There a warp takes 32 keys
 // at a time: first a key per lane (its whole dot product with up to 4 query rows held in shared memory),
 // then a channel of each group per lane (the weights come from the other lanes by shuffle).
 #include "kv4.cuh"
+#include "sm100_ptx.cuh"
 
 namespace osf {
 namespace {
+
+using namespace ptx;
 
 constexpr int GW = 4;        // warps per CTA
 constexpr int RB = 4;        // query rows per CTA
@@ -168,6 +172,396 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
     }
 }
 
+// ============================================================================ tensor-core kernel
+// Keys are the M rows of warp-level MMAs (m16n8k16) and query rows the N columns, so eight query rows
+// cost one MMA column block and the dequantised operand is always A, built in registers:
+//   S^T[16 keys x 8 rows]      = sum over groups of  scale * (codes . Q) + minimum * sum Q
+//   O^T[16 channels x 8 rows] += V^T[16 channels x 16 keys] P^T[16 keys x 8 rows]
+// K: a code masked out of its word is the float16 subnormal code * 2^-24 (nibbles 0, 4) or
+// code * 2^-20 (nibbles 1, 5; Q is scaled by 2^-4 there), so one AND per pair makes an exact operand.  Q is
+// held in float16 after an exact power-of-two scaling per row that puts its largest entry at 2^13 .. 2^14:
+// 8 significant bits fit, down to entries 2^-28 of the row's largest.  A group's two k-steps go to a
+// fresh accumulator, and scale and minimum are applied to it in float32.
+// V: halves of two keys' words interleave with one byte permute, so that an AND-OR gives the bfloat16 pair
+// (128 + code) of one channel and two keys; subtracting 128 is exact and one fma.bf16x2 makes
+// scale * code + minimum, rounded once (half a step of 2^-8, the precision a bfloat16 cache holds V to).
+// P is rounded to bfloat16 likewise, and moved from the S^T accumulator layout to the B operand by movmatrix.
+//
+// Each warp streams its own 2560-byte runs of records through a ring of bulk copies (one instruction
+// per run, since K and V of a token are adjacent) and keeps its own softmax state; the eight states merge
+// through shared memory at the end.  The running maximum is lazy: a row keeps its reference until a
+// score passes it by more than 8 in base 2, so most tiles need no cross-lane reduction and no rescale.
+constexpr int TW = 8;                     // warps per CTA
+constexpr uint32_t kSlot = 2560;          // bytes of one ring slot: 16 records at D = 128, 32 at D = 64
+constexpr float kRowFloor = -1.7e38f;     // reference maximum of a row that has seen nothing
+
+template <int D, int NT>
+struct TcCfg {
+    static constexpr int REC = D + D / 4;
+    static constexpr int TK = (int)kSlot / REC;
+    static constexpr int STAGES = 4;
+    static constexpr int NG = D / 32, J = D / 64;
+    static constexpr uint32_t RING = TW * STAGES * kSlot;
+    static constexpr uint32_t MERGE = TW * 8 * NT * D * 4;
+    static constexpr uint32_t SMEM = RING > MERGE ? RING : MERGE;
+};
+
+// Key of a 16-key tile that MMA row m (or k index m) stands for, m < 8 (m + 8: 8 more).  With 160-byte
+// records the 16-byte K reads of rows m, m + 1 and the 8-byte V reads of k = 0, 2, 4, 6 (and 1, 3, 5, 7)
+// then fall on different banks.
+__device__ __forceinline__ int tile_key(int m) { return ((m >> 1) & 1) | (((m & 1) ^ (m >> 2)) << 1) | (m & 4); }
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// scale * code + minimum of the bfloat16 pair whose codes are the nibbles 0 of the halves of u.
+__device__ __forceinline__ uint32_t dequant_pair(uint32_t u, uint32_t s, uint32_t m) {
+    uint32_t r;
+    asm("{\n .reg .b32 t;\n lop3.b32 t, %1, 0x000f000f, 0x43004300, 0xea;\n sub.rn.bf16x2 t, t, %4;\n"
+        " fma.rn.bf16x2 %0, t, %2, %3;\n}"
+        : "=r"(r)
+        : "r"(u), "r"(s), "r"(m), "r"(0x43004300u));
+    return r;
+}
+
+template <int N>
+struct Words {
+    uint32_t w[N];
+};
+template <int N>
+__device__ __forceinline__ Words<N> lds_words(const unsigned char *p) {
+    Words<N> r;
+    if (N == 4) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[N > 2 ? 2 : 0] = v.z; r.w[N > 3 ? 3 : 0] = v.w;
+    } else if (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x; r.w[N > 1 ? 1 : 0] = v.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    return r;
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(TW * 32, NT == 1 || D == 64 ? 2 : 1)
+attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
+    using C = TcCfg<D, NT>;
+    constexpr int NG = C::NG, J = C::J, REC = C::REC, TK = C::TK, STAGES = C::STAGES;
+    const AttnProblem &p = kp.a;
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ uint64_t full[TW][STAGES];
+    __shared__ float sm_m[TW][8 * NT], sm_l[TW][8 * NT];
+    __shared__ volatile int abort_flag;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int G = p.Hq / p.Hkv, R = G * p.Sq;
+    const int kvbh = blockIdx.x, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
+    const int r0 = blockIdx.z * (8 * NT), rows = min(8 * NT, R - r0);
+    const int n = kv4_length(kp.lens, b, p.Sk, p.status);
+    int begin, end;
+    part_of(n, TK, blockIdx.y, p.splits, begin, end);
+    const int tiles = (end - begin + TK - 1) / TK;
+    const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;   // this warp's tiles: warp, warp + 8, ...
+    const unsigned char *head = kp.cache + (long long)kvbh * p.Sk * REC;
+    unsigned char *ring = smem + warp * (STAGES * kSlot);
+    if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full[warp][s]), 1);
+        mbar_init_fence();
+        if (warp == 0) abort_flag = 0;
+    }
+    __syncthreads();
+    auto issue = [&](int i) {
+        const int k0 = begin + (warp + TW * i) * TK;
+        const uint32_t bytes = (uint32_t)min(TK, end - k0) * REC;
+        const uint32_t bar = smem_u32(&full[warp][i % STAGES]);
+        mbar_expect_tx(bar, bytes);
+        bulk_load(smem_u32(ring + (i % STAGES) * kSlot), head + (long long)k0 * REC, bytes, bar);
+    };
+    if (lane == 0)
+        for (int i = 0; i < min(STAGES, mine); ++i) issue(i);
+
+    // Q as the B operand: column n = query row, lane (g, t) holds row g's channels 8t .. 8t+7 of each group
+    uint32_t qb[NT][NG][4];
+    float qs[NT][NG][2];        // sums of Q over a group, of this lane's two columns 2t, 2t + 1
+    float f1[NT][2], f2[NT][2]; // S to base-2 score: undoes the scalings, times scale * log2 e
+    int lim[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = nt * 8 + g, gr = r0 + r;
+        const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(p.q);
+        if (r < rows) Q += q_at(p, b, kvh * G + gr / p.Sq, gr % p.Sq);
+        float x[NG][8];
+        float mx = 0.f;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+            if (r >= rows) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[gi][e] = 0.f;
+            } else if (q_vec) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(Q + 32 * gi + 8 * t);
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[gi][2 * e] = lo_bf16(w[e]);
+                    x[gi][2 * e + 1] = hi_bf16(w[e]);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[gi][e] = __bfloat162float(Q[32 * gi + 8 * t + e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[gi][e]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int ex = max(-114, min(126, 13 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+        const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+            float s = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[gi][e] *= up;
+                s += x[gi][e];
+            }
+            qb[nt][gi][0] = pack_f16x2(x[gi][0], x[gi][4]);
+            qb[nt][gi][1] = pack_f16x2(x[gi][1] * 0.0625f, x[gi][5] * 0.0625f);
+            qb[nt][gi][2] = pack_f16x2(x[gi][2], x[gi][6]);
+            qb[nt][gi][3] = pack_f16x2(x[gi][3] * 0.0625f, x[gi][7] * 0.0625f);
+            s += __shfl_xor_sync(0xffffffffu, s, 1);
+            s += __shfl_xor_sync(0xffffffffu, s, 2);
+            s *= 0x1p-24f;   // in the unit of the code products
+            qs[nt][gi][0] = __shfl_sync(0xffffffffu, s, 8 * t);
+            qs[nt][gi][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c), half = back / 2;
+            f1[nt][c] = __uint_as_float((uint32_t)(half + 127) << 23);
+            f2[nt][c] = __uint_as_float((uint32_t)(back - half + 127) << 23) * p.scale_log2;
+            const int col = r0 + nt * 8 + 2 * t + c;
+            lim[nt][c] = p.causal && col < R ? max(0, n - p.Sq + col % p.Sq + 1) : n;
+        }
+    }
+    const int lim_all = p.causal ? n - p.Sq + 1 : n;   // keys below this are visible to every row
+
+    float o[NT][J * 4][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int j = 0; j < J * 4; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+        m[nt][0] = m[nt][1] = kRowFloor;
+        l[nt][0] = l[nt][1] = 0.f;
+    }
+    const int ka = tile_key(g), va0 = tile_key(2 * t), va1 = tile_key(2 * t + 1);
+    const int ng0 = (g & 1) * J;   // V: this lane's words are 4 (ng0 + j) + g / 2, of groups ng0 + j
+    float *sc_out = kp.scores ? kp.scores + ((long long)kvbh * R + r0 + 2 * t) * p.Sk : nullptr;
+    bool ok = true;
+    int i = 0;
+    for (; i < mine; ++i) {
+        const int st = i % STAGES;
+        ok = mbar_wait(smem_u32(&full[warp][st]), (i / STAGES) & 1, &abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        unsigned char *slot = ring + st * kSlot;
+        const int k0 = begin + (warp + TW * i) * TK;
+        if (end - k0 < TK) {
+            // the sequence ends inside the tile (its last one): records behind it are zeroed, so that stale
+            // scales cannot turn a weight of zero into a NaN
+            for (int x = (end - k0) * REC / 16 + lane; x < (int)kSlot / 16; x += 32)
+                reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0, 0, 0, 0);
+            __syncwarp();
+        }
+#pragma unroll
+        for (int sub = 0; sub < TK / 16; ++sub) {
+            const unsigned char *tile = slot + sub * 16 * REC;
+            const int key = k0 + sub * 16 + ka;
+            float y[NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.f;
+            {
+                const unsigned char *ra = tile + ka * REC, *rb = ra + 8 * REC;
+                const Words<NG> xa = lds_words<NG>(ra + t * (D / 8)), xb = lds_words<NG>(rb + t * (D / 8));
+                const Words<NG> pa = lds_words<NG>(ra + D), pb = lds_words<NG>(rb + D);
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    const uint32_t a = xa.w[gi], c = xb.w[gi], a8 = a >> 8, c8 = c >> 8;
+                    const float s0 = lo_bf16(pa.w[gi]), m0 = hi_bf16(pa.w[gi]);
+                    const float s1 = lo_bf16(pb.w[gi]), m1 = hi_bf16(pb.w[gi]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        float d[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_f16(d, a & 0x000f000fu, c & 0x000f000fu, a & 0x00f000f0u, c & 0x00f000f0u, qb[nt][gi][0],
+                                qb[nt][gi][1]);
+                        mma_f16(d, a8 & 0x000f000fu, c8 & 0x000f000fu, a8 & 0x00f000f0u, c8 & 0x00f000f0u, qb[nt][gi][2],
+                                qb[nt][gi][3]);
+                        y[nt][0] = fmaf(s0, d[0], fmaf(m0, qs[nt][gi][0], y[nt][0]));
+                        y[nt][1] = fmaf(s0, d[1], fmaf(m0, qs[nt][gi][1], y[nt][1]));
+                        y[nt][2] = fmaf(s1, d[2], fmaf(m1, qs[nt][gi][0], y[nt][2]));
+                        y[nt][3] = fmaf(s1, d[3], fmaf(m1, qs[nt][gi][1], y[nt][3]));
+                    }
+                }
+            }
+            bool raise = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[nt][e] = y[nt][e] * f1[nt][e & 1] * f2[nt][e & 1];
+            if (k0 + sub * 16 + 16 > lim_all) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (key + (e >> 1) * 8 >= lim[nt][e & 1]) y[nt][e] = -INFINITY;
+            }
+            if (sc_out) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (nt * 8 + 2 * t + (e & 1) < rows && key + (e >> 1) * 8 < end)
+                            sc_out[(long long)(nt * 8 + (e & 1)) * p.Sk + key + (e >> 1) * 8] = y[nt][e];
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) raise |= y[nt][e] > m[nt][e & 1] + 8.f;
+            if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(m[nt][c], fmaxf(y[nt][c], y[nt][c + 2]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        const float a = ex2_approx(m[nt][c] - mx);
+                        m[nt][c] = mx;
+                        l[nt][c] *= a;
+#pragma unroll
+                        for (int j = 0; j < J * 4; ++j) {
+                            o[nt][j][c] *= a;
+                            o[nt][j][c + 2] *= a;
+                        }
+                    }
+            }
+            uint32_t pb0[NT], pb1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float pr[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(y[nt][e] - m[nt][e & 1]);
+                l[nt][0] += pr[0] + pr[2];
+                l[nt][1] += pr[1] + pr[3];
+                pb0[nt] = transpose_8x8(pack_bf16x2(pr[0], pr[1]));
+                pb1[nt] = transpose_8x8(pack_bf16x2(pr[2], pr[3]));
+            }
+            // V: keys of k = 2t, 2t + 1, 2t + 8, 2t + 9
+            const unsigned char *v0 = tile + va0 * REC, *v1 = tile + va1 * REC;
+            Words<J> w[4], s[4];
+            w[0] = lds_words<J>(v0 + D / 2 + g * 4 * J);
+            w[1] = lds_words<J>(v1 + D / 2 + g * 4 * J);
+            w[2] = lds_words<J>(v0 + 8 * REC + D / 2 + g * 4 * J);
+            w[3] = lds_words<J>(v1 + 8 * REC + D / 2 + g * 4 * J);
+            s[0] = lds_words<J>(v0 + D + D / 8 + ng0 * 4);
+            s[1] = lds_words<J>(v1 + D + D / 8 + ng0 * 4);
+            s[2] = lds_words<J>(v0 + 8 * REC + D + D / 8 + ng0 * 4);
+            s[3] = lds_words<J>(v1 + 8 * REC + D + D / 8 + ng0 * 4);
+#pragma unroll
+            for (int j = 0; j < J; ++j) {
+                const uint32_t s01 = __byte_perm(s[0].w[j], s[1].w[j], 0x5410), m01 = __byte_perm(s[0].w[j], s[1].w[j], 0x7632);
+                const uint32_t s23 = __byte_perm(s[2].w[j], s[3].w[j], 0x5410), m23 = __byte_perm(s[2].w[j], s[3].w[j], 0x7632);
+                const uint32_t lo01 = __byte_perm(w[0].w[j], w[1].w[j], 0x5410), hi01 = __byte_perm(w[0].w[j], w[1].w[j], 0x7632);
+                const uint32_t lo23 = __byte_perm(w[2].w[j], w[3].w[j], 0x5410), hi23 = __byte_perm(w[2].w[j], w[3].w[j], 0x7632);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    // channels 8 w + c (rows g) and 8 w + 4 + c (rows g + 8) of word w
+                    const uint32_t a[4] = {dequant_pair(lo01 >> (4 * c), s01, m01), dequant_pair(hi01 >> (4 * c), s01, m01),
+                                           dequant_pair(lo23 >> (4 * c), s23, m23), dequant_pair(hi23 >> (4 * c), s23, m23)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma_m16n8k16_bf16(o[nt][j * 4 + c], a, pb0[nt], pb1[nt]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0 && i + STAGES < mine) issue(i + STAGES);
+    }
+    if (!ok) {
+        abort_flag = 1;
+        if (lane == 0) {
+            atomicExch(p.status, kStatusTimeout);
+            for (int j = i; j < min(i + STAGES, mine); ++j)   // let issued copies land before the ring is reused
+                mbar_wait(smem_u32(&full[warp][j % STAGES]), (j / STAGES) & 1, nullptr, 20000000ull);
+        }
+    }
+    // ------------------------------------------------------------- merge the warps' states
+    __syncthreads();   // the rings are drained: their memory takes the outputs
+    float *so = reinterpret_cast<float *>(smem);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            float v = l[nt][c];
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            v += __shfl_xor_sync(0xffffffffu, v, 16);
+            const int r = nt * 8 + 2 * t + c;
+            if (g == 0) {
+                sm_m[warp][r] = v > 0.f || v != v ? m[nt][c] : -INFINITY;
+                sm_l[warp][r] = v;
+            }
+#pragma unroll
+            for (int j = 0; j < J * 4; ++j) {
+                const int ch = 8 * (4 * (ng0 + j / 4) + (g >> 1)) + (j & 3);
+                so[(warp * 8 * NT + r) * D + ch] = o[nt][j][c];
+                so[(warp * 8 * NT + r) * D + ch + 4] = o[nt][j][c + 2];
+            }
+        }
+    }
+    __syncthreads();
+    const long long rows_total = (long long)p.B * p.Hq * p.Sq;
+    for (int x = tid; x < rows * D; x += TW * 32) {
+        const int r = x / D, c = x % D, gr = r0 + r;
+        float M = -INFINITY, L = 0.f, A = 0.f;
+#pragma unroll
+        for (int w = 0; w < TW; ++w) M = fmaxf(M, sm_m[w][r]);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int w = 0; w < TW; ++w) {
+            const float wt = ex2_approx(sm_m[w][r] - ref);
+            A += wt * so[(w * 8 * NT + r) * D + c];
+            L += wt * sm_l[w][r];
+        }
+        const int hq = kvh * G + gr / p.Sq, qi = gr % p.Sq;
+        const long long grow = ((long long)b * p.Hq + hq) * p.Sq + qi;
+        if (p.splits == 1) {
+            static_cast<__nv_bfloat16 *>(p.o)[o_at(p, b, hq, qi) + c] = __float2bfloat16_rn(L > 0.f || L != L ? A / L : 0.f);
+            if (p.lse && c == 0) p.lse[grow] = L > 0.f ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+        } else {
+            p.part_acc[((size_t)blockIdx.y * rows_total + grow) * D + c] = A;
+            if (c == 0) {
+                p.part_m[(size_t)blockIdx.y * rows_total + grow] = M;
+                p.part_l[(size_t)blockIdx.y * rows_total + grow] = L;
+            }
+        }
+    }
+}
+
 // Weights from the stored scores, once every row's log-sum-exp is known.
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem kp) {
     griddep_wait();
@@ -194,11 +588,25 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
 
 }  // namespace
 
-bool kv4_attn_fast(int, int) { return false; }
+// Query rows per CTA of the tensor-core kernel: 8 or 16.
+static int tc_rows(int R) { return R <= 8 ? 8 : 16; }
+
+static bool use_tc(const AttnProblem &p) { return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128); }
 
 int kv4_attn_pick_splits(const Kv4AttnProblem &kp, int sm_count) {
     const AttnProblem &p = kp.a;
     const int R = p.Hq / p.Hkv * p.Sq;
+    if (use_tc(p)) {
+        const int rb = tc_rows(R), tk = (int)kSlot / kv4_record_bytes(p.D);
+        const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
+        const long long tiles = ((long long)p.Sk + tk - 1) / tk;
+        // about four waves of two CTAs per SM, so the last wave's imbalance stays small, but at least
+        // two tiles for each warp of a part
+        long long s = (8LL * sm_count + items / 2) / items;
+        const long long most = tiles / (2 * TW);
+        s = s < most ? s : most;
+        return (int)(s < 1 ? 1 : s > 65535 ? 65535 : s);
+    }
     const long long items = (long long)p.B * p.Hkv * ((R + RB - 1) / RB);
     const long long units = ((long long)p.Sk + 31) / 32;
     long long s = (8LL * sm_count + items - 1) / items;
@@ -207,14 +615,34 @@ int kv4_attn_pick_splits(const Kv4AttnProblem &kp, int sm_count) {
     return (int)(s < 1 ? 1 : s > 1024 ? 1024 : s);
 }
 
+template <int D, int NT>
+static cudaError_t launch_tc_t(const Kv4AttnProblem &kp, cudaStream_t s) {
+    using C = TcCfg<D, NT>;
+    const AttnProblem &p = kp.a;
+    const cudaError_t e = set_max_dynamic_smem((const void *)attn_kv4_tc_kernel<D, NT>, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    const int R = p.Hq / p.Hkv * p.Sq;
+    const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 7) == 0;
+    attn_kv4_tc_kernel<D, NT><<<dim3((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + 8 * NT - 1) / (8 * NT))), TW * 32,
+                                C::SMEM, s>>>(kp, q_vec);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp, cudaStream_t s) {
     const AttnProblem &p = kp.a;
     const int R = p.Hq / p.Hkv * p.Sq;
-    const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + RB - 1) / RB));
-    if (p.dtype == OSF_F32) attn_kv4_kernel<float><<<grid, GW * 32, 0, s>>>(kp);
-    else attn_kv4_kernel<__nv_bfloat16><<<grid, GW * 32, 0, s>>>(kp);
+    cudaError_t e;
+    if (use_tc(p)) {
+        const bool few = tc_rows(R) == 8;
+        e = p.D == 64 ? (few ? launch_tc_t<64, 1>(kp, s) : launch_tc_t<64, 2>(kp, s))
+                      : (few ? launch_tc_t<128, 1>(kp, s) : launch_tc_t<128, 2>(kp, s));
+    } else {
+        const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + RB - 1) / RB));
+        if (p.dtype == OSF_F32) attn_kv4_kernel<float><<<grid, GW * 32, 0, s>>>(kp);
+        else attn_kv4_kernel<__nv_bfloat16><<<grid, GW * 32, 0, s>>>(kp);
+        e = cudaGetLastError();
+    }
     count_launches(1);
-    cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     if (e == cudaSuccess && kp.weights && p.Sk > 0) {
         count_launches(1);

@@ -45,7 +45,6 @@ struct Kv4AttnProblem {
     int accumulate;             // add to weights instead of overwriting them
     float *scores;              // with weights: base-2 scores [B * Hkv][G * Sq][Sk]
 };
-bool kv4_attn_fast(int dtype, int D);
 int kv4_attn_pick_splits(const Kv4AttnProblem &p, int sm_count);
 cudaError_t launch_attn_kv4(const Kv4AttnProblem &p, cudaStream_t s);
 
