@@ -182,39 +182,41 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // held in float16 after an exact power-of-two scaling per row that puts its largest entry at 2^13 .. 2^14:
 // 8 significant bits fit, down to entries 2^-28 of the row's largest.  A group's two k-steps go to a
 // fresh accumulator, and scale and minimum are applied to it in float32.
-// V: halves of two keys' words interleave with one byte permute, so that an AND-OR gives the bfloat16 pair
-// (128 + code) of one channel and two keys; subtracting 128 is exact and one fma.bf16x2 makes
-// scale * code + minimum, rounded once (half a step of 2^-8, the precision a bfloat16 cache holds V to).
-// P is rounded to bfloat16 likewise, and moved from the S^T accumulator layout to the B operand by movmatrix.
+// V: likewise, with scale and minimum moved to the other side of the product: for the channels of one group
+//   sum_k P_k (minimum_k + scale_k code_kc) = sum_k P_k minimum_k + sum_k (P_k scale_k) code_kc,
+// the first sum in float32 (one per row and group), the second an MMA whose B operand is P * scale in
+// float16.  One byte permute interleaves the halves of two keys' words, after which one AND makes the pair
+// (code of key k, code of key k') of a channel.  P * scale is rounded to 11 bits; a power of two common to
+// the warp's keys keeps it in range: scales up to 64 times the reference need no new one, and 2^-21 of it
+// still keeps all 11 bits.  P moves from the S^T accumulator layout to the B operand by movmatrix.
 //
-// Each warp streams its own 2560-byte runs of records through a ring of bulk copies (one instruction
+// Each warp streams its own 5120-byte runs of records through a ring of bulk copies (one instruction
 // per run, since K and V of a token are adjacent) and keeps its own softmax state; the eight states merge
 // through shared memory at the end.  The running maximum is lazy: a row keeps its reference until a
 // score passes it by more than 8 in base 2, so most tiles need no cross-lane reduction and no rescale.
 constexpr int TW = 8;                     // warps per CTA
-constexpr uint32_t kSlot = 2560;          // bytes of one ring slot: 16 records at D = 128, 32 at D = 64
+constexpr uint32_t kSlot = 5120;          // bytes of one ring slot: 32 records at D = 128, 64 at D = 64
 constexpr float kRowFloor = -1.7e38f;     // reference maximum of a row that has seen nothing
 
 template <int D, int NT>
 struct TcCfg {
     static constexpr int REC = D + D / 4;
     static constexpr int TK = (int)kSlot / REC;
-    static constexpr int STAGES = 4;
-    static constexpr int NG = D / 32, J = D / 64;
+    static constexpr int STAGES = 2;
+    static constexpr int NG = D / 32;
     static constexpr uint32_t RING = TW * STAGES * kSlot;
     static constexpr uint32_t MERGE = TW * 8 * NT * D * 4;
     static constexpr uint32_t SMEM = RING > MERGE ? RING : MERGE;
 };
 
 // Key of a 16-key tile that MMA row m (or k index m) stands for, m < 8 (m + 8: 8 more).  With 160-byte
-// records the 16-byte K reads of rows m, m + 1 and the 8-byte V reads of k = 0, 2, 4, 6 (and 1, 3, 5, 7)
-// then fall on different banks.
+// records the 16-byte K reads of rows m, m + 1 and the V reads of k = 0, 2, 4, 6 (and 1, 3, 5, 7)
+// then fall on different banks (measured: no load conflicts).
 __device__ __forceinline__ int tile_key(int m) { return ((m >> 1) & 1) | (((m & 1) ^ (m >> 2)) << 1) | (m & 4); }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -226,15 +228,6 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-// scale * code + minimum of the bfloat16 pair whose codes are the nibbles 0 of the halves of u.
-__device__ __forceinline__ uint32_t dequant_pair(uint32_t u, uint32_t s, uint32_t m) {
-    uint32_t r;
-    asm("{\n .reg .b32 t;\n lop3.b32 t, %1, 0x000f000f, 0x43004300, 0xea;\n sub.rn.bf16x2 t, t, %4;\n"
-        " fma.rn.bf16x2 %0, t, %2, %3;\n}"
-        : "=r"(r)
-        : "r"(u), "r"(s), "r"(m), "r"(0x43004300u));
     return r;
 }
 
@@ -261,7 +254,7 @@ template <int D, int NT>
 __global__ void __launch_bounds__(TW * 32, NT == 1 || D == 64 ? 2 : 1)
 attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     using C = TcCfg<D, NT>;
-    constexpr int NG = C::NG, J = C::J, REC = C::REC, TK = C::TK, STAGES = C::STAGES;
+    constexpr int NG = C::NG, REC = C::REC, TK = C::TK, STAGES = C::STAGES;
     const AttnProblem &p = kp.a;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ uint64_t full[TW][STAGES];
@@ -275,9 +268,9 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     const int n = kv4_length(kp.lens, b, p.Sk, p.status);
     int begin, end;
     part_of(n, TK, blockIdx.y, p.splits, begin, end);
+    // this warp's tiles of the part: warp, warp + 8, ...
     const int tiles = (end - begin + TK - 1) / TK;
-    const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;   // this warp's tiles: warp, warp + 8, ...
-    const unsigned char *head = kp.cache + (long long)kvbh * p.Sk * REC;
+    const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;
     unsigned char *ring = smem + warp * (STAGES * kSlot);
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full[warp][s]), 1);
@@ -285,12 +278,14 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         if (warp == 0) abort_flag = 0;
     }
     __syncthreads();
-    auto issue = [&](int i) {
-        const int k0 = begin + (warp + TW * i) * TK;
-        const uint32_t bytes = (uint32_t)min(TK, end - k0) * REC;
-        const uint32_t bar = smem_u32(&full[warp][i % STAGES]);
+    const unsigned char *src = kp.cache + ((long long)kvbh * p.Sk + begin + warp * TK) * REC;   // the next tile to copy
+    int left = end - begin - warp * TK;                                                       // records from there on
+    auto issue = [&](int slot) {
+        const uint32_t bytes = (uint32_t)min(TK, left) * REC, bar = smem_u32(&full[warp][slot]);
         mbar_expect_tx(bar, bytes);
-        bulk_load(smem_u32(ring + (i % STAGES) * kSlot), head + (long long)k0 * REC, bytes, bar);
+        bulk_load(smem_u32(ring + slot * kSlot), src, bytes, bar);
+        src += TW * TK * REC;
+        left -= TW * TK;
     };
     if (lane == 0)
         for (int i = 0; i < min(STAGES, mine); ++i) issue(i);
@@ -298,8 +293,9 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     // Q as the B operand: column n = query row, lane (g, t) holds row g's channels 8t .. 8t+7 of each group
     uint32_t qb[NT][NG][4];
     float qs[NT][NG][2];        // sums of Q over a group, of this lane's two columns 2t, 2t + 1
-    float f1[NT][2], f2[NT][2]; // S to base-2 score: undoes the scalings, times scale * log2 e
+    float f[NT][2];             // S to base-2 score: undoes the scalings, times scale * log2 e
     int lim[NT][2];
+    bool wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g, gr = r0 + r;
@@ -351,25 +347,40 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c), half = back / 2;
-            f1[nt][c] = __uint_as_float((uint32_t)(half + 127) << 23);
-            f2[nt][c] = __uint_as_float((uint32_t)(back - half + 127) << 23) * p.scale_log2;
+            const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c);
+            wide |= back > 100;   // this and scale * log2 e may pass float32's range: applied in two steps
+            f[nt][c] = (float)back;
             const int col = r0 + nt * 8 + 2 * t + c;
             lim[nt][c] = p.causal && col < R ? max(0, n - p.Sq + col % p.Sq + 1) : n;
         }
     }
     const int lim_all = p.causal ? n - p.Sq + 1 : n;   // keys below this are visible to every row
 
-    float o[NT][J * 4][4], m[NT][2], l[NT][2];
+    wide = __any_sync(0xffffffffu, wide);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+            f[nt][c] = __uint_as_float((uint32_t)(max(-126, (int)f[nt][c] - (wide ? 64 : 0)) + 127) << 23) * p.scale_log2;
+
+    // o: code sums, tile (group, h), row g (+ 8) = channel 32 group + 4 g + 2 h (+ 1), in units of 2^-24 (2^-20)
+    // of the scale reference;  om: sums of P * minimum of a group
+    float o[NT][NG * 2][4], om[NT][NG][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int j = 0; j < J * 4; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+        for (int j = 0; j < NG * 2; ++j) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.f;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) om[nt][gi][0] = om[nt][gi][1] = 0.f;
         m[nt][0] = m[nt][1] = kRowFloor;
         l[nt][0] = l[nt][1] = 0.f;
     }
-    const int ka = tile_key(g), va0 = tile_key(2 * t), va1 = tile_key(2 * t + 1);
-    const int ng0 = (g & 1) * J;   // V: this lane's words are 4 (ng0 + j) + g / 2, of groups ng0 + j
+    float s_inv = 1.f, s_lim = -1.f;   // 1 / scale reference; the scale that asks for a new one
+    const int ka = tile_key(g);
+    const int off_a = ka * REC;                                                // K, and both halves' pairs: keys ka, ka + 8
+    const int off_v0 = tile_key(2 * t) * REC + D / 2 + (g >> 1) * (D / 8);     // V codes: keys of k = 2t, 2t + 1 (+ 8)
+    const int off_v1 = tile_key(2 * t + 1) * REC + D / 2 + (g >> 1) * (D / 8);
+    const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;                         // lane's half of a word, of two keys
     float *sc_out = kp.scores ? kp.scores + ((long long)kvbh * R + r0 + 2 * t) * p.Sk : nullptr;
     bool ok = true;
     int i = 0;
@@ -380,22 +391,23 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         if (!ok) break;
         unsigned char *slot = ring + st * kSlot;
         const int k0 = begin + (warp + TW * i) * TK;
+        const int subs = min(TK / 16, (end - k0 + 15) / 16);
         if (end - k0 < TK) {
             // the sequence ends inside the tile (its last one): records behind it are zeroed, so that stale
             // scales cannot turn a weight of zero into a NaN
-            for (int x = (end - k0) * REC / 16 + lane; x < (int)kSlot / 16; x += 32)
+            for (int x = (end - k0) * REC / 16 + lane; x < subs * REC; x += 32)
                 reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0, 0, 0, 0);
             __syncwarp();
         }
-#pragma unroll
-        for (int sub = 0; sub < TK / 16; ++sub) {
+#pragma unroll 1
+        for (int sub = 0; sub < subs; ++sub) {
             const unsigned char *tile = slot + sub * 16 * REC;
             const int key = k0 + sub * 16 + ka;
             float y[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.f;
+            const unsigned char *ra = tile + off_a, *rb = ra + 8 * REC;
             {
-                const unsigned char *ra = tile + ka * REC, *rb = ra + 8 * REC;
                 const Words<NG> xa = lds_words<NG>(ra + t * (D / 8)), xb = lds_words<NG>(rb + t * (D / 8));
                 const Words<NG> pa = lds_words<NG>(ra + D), pb = lds_words<NG>(rb + D);
 #pragma unroll
@@ -417,11 +429,17 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
                     }
                 }
             }
+            if (wide) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) y[nt][e] *= 0x1p64f;
+            }
             bool raise = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[nt][e] = y[nt][e] * f1[nt][e & 1] * f2[nt][e & 1];
+                for (int e = 0; e < 4; ++e) y[nt][e] *= f[nt][e & 1];
             if (k0 + sub * 16 + 16 > lim_all) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
@@ -437,11 +455,35 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
                         if (nt * 8 + 2 * t + (e & 1) < rows && key + (e >> 1) * 8 < end)
                             sc_out[(long long)(nt * 8 + (e & 1)) * p.Sk + key + (e >> 1) * 8] = y[nt][e];
             }
+            // V scales and minima of this lane's two keys
+            float vs[2][NG], vm[2][NG];
+            {
+                const Words<NG> pa = lds_words<NG>(ra + D + D / 8), pb = lds_words<NG>(rb + D + D / 8);
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    vs[0][gi] = lo_bf16(pa.w[gi]); vm[0][gi] = hi_bf16(pa.w[gi]);
+                    vs[1][gi] = lo_bf16(pb.w[gi]); vm[1][gi] = hi_bf16(pb.w[gi]);
+                }
+            }
+            float s_max = fmaxf(vs[0][0], vs[1][0]);
+#pragma unroll
+            for (int gi = 1; gi < NG; ++gi) s_max = fmax3(s_max, vs[0][gi], vs[1][gi]);
+            raise = s_max > s_lim;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) raise |= y[nt][e] > m[nt][e & 1] + 8.f;
             if (__any_sync(0xffffffffu, raise)) {
+                s_max = warp_max(s_max);
+                float sa = 1.f;
+                if (s_max > s_lim) {
+                    // the power of two at the largest scale becomes the reference
+                    const int ex = max(-120, min(126, (int)(__float_as_uint(s_max) >> 23) - 127));
+                    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
+                    sa = s_lim < 0.f ? 0.f : inv / s_inv;
+                    s_inv = inv;
+                    s_lim = 64.f * __uint_as_float((uint32_t)(127 + min(ex, 120)) << 23);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -454,52 +496,46 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
                         m[nt][c] = mx;
                         l[nt][c] *= a;
 #pragma unroll
-                        for (int j = 0; j < J * 4; ++j) {
-                            o[nt][j][c] *= a;
-                            o[nt][j][c + 2] *= a;
+                        for (int j = 0; j < NG * 2; ++j) {
+                            o[nt][j][c] *= a * sa;
+                            o[nt][j][c + 2] *= a * sa;
                         }
+#pragma unroll
+                        for (int gi = 0; gi < NG; ++gi) om[nt][gi][c] *= a;
                     }
             }
-            uint32_t pb0[NT], pb1[NT];
+            float pr[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                float pr[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) pr[e] = ex2_approx(y[nt][e] - m[nt][e & 1]);
-                l[nt][0] += pr[0] + pr[2];
-                l[nt][1] += pr[1] + pr[3];
-                pb0[nt] = transpose_8x8(pack_bf16x2(pr[0], pr[1]));
-                pb1[nt] = transpose_8x8(pack_bf16x2(pr[2], pr[3]));
+                for (int e = 0; e < 4; ++e) pr[nt][e] = ex2_approx(y[nt][e] - m[nt][e & 1]);
+                l[nt][0] += pr[nt][0] + pr[nt][2];
+                l[nt][1] += pr[nt][1] + pr[nt][3];
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    om[nt][gi][0] = fmaf(pr[nt][0], vm[0][gi], fmaf(pr[nt][2], vm[1][gi], om[nt][gi][0]));
+                    om[nt][gi][1] = fmaf(pr[nt][1], vm[0][gi], fmaf(pr[nt][3], vm[1][gi], om[nt][gi][1]));
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pr[nt][e] *= s_inv;
             }
-            // V: keys of k = 2t, 2t + 1, 2t + 8, 2t + 9
-            const unsigned char *v0 = tile + va0 * REC, *v1 = tile + va1 * REC;
-            Words<J> w[4], s[4];
-            w[0] = lds_words<J>(v0 + D / 2 + g * 4 * J);
-            w[1] = lds_words<J>(v1 + D / 2 + g * 4 * J);
-            w[2] = lds_words<J>(v0 + 8 * REC + D / 2 + g * 4 * J);
-            w[3] = lds_words<J>(v1 + 8 * REC + D / 2 + g * 4 * J);
-            s[0] = lds_words<J>(v0 + D + D / 8 + ng0 * 4);
-            s[1] = lds_words<J>(v1 + D + D / 8 + ng0 * 4);
-            s[2] = lds_words<J>(v0 + 8 * REC + D + D / 8 + ng0 * 4);
-            s[3] = lds_words<J>(v1 + 8 * REC + D + D / 8 + ng0 * 4);
+            const Words<NG> w0 = lds_words<NG>(tile + off_v0), w1 = lds_words<NG>(tile + off_v1);
+            const Words<NG> w2 = lds_words<NG>(tile + off_v0 + 8 * REC), w3 = lds_words<NG>(tile + off_v1 + 8 * REC);
 #pragma unroll
-            for (int j = 0; j < J; ++j) {
-                const uint32_t s01 = __byte_perm(s[0].w[j], s[1].w[j], 0x5410), m01 = __byte_perm(s[0].w[j], s[1].w[j], 0x7632);
-                const uint32_t s23 = __byte_perm(s[2].w[j], s[3].w[j], 0x5410), m23 = __byte_perm(s[2].w[j], s[3].w[j], 0x7632);
-                const uint32_t lo01 = __byte_perm(w[0].w[j], w[1].w[j], 0x5410), hi01 = __byte_perm(w[0].w[j], w[1].w[j], 0x7632);
-                const uint32_t lo23 = __byte_perm(w[2].w[j], w[3].w[j], 0x5410), hi23 = __byte_perm(w[2].w[j], w[3].w[j], 0x7632);
+            for (int gi = 0; gi < NG; ++gi) {
+                const uint32_t u = __byte_perm(w0.w[gi], w1.w[gi], pick), v = __byte_perm(w2.w[gi], w3.w[gi], pick);
+                const uint32_t u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    // channels 8 w + c (rows g) and 8 w + 4 + c (rows g + 8) of word w
-                    const uint32_t a[4] = {dequant_pair(lo01 >> (4 * c), s01, m01), dequant_pair(hi01 >> (4 * c), s01, m01),
-                                           dequant_pair(lo23 >> (4 * c), s23, m23), dequant_pair(hi23 >> (4 * c), s23, m23)};
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) mma_m16n8k16_bf16(o[nt][j * 4 + c], a, pb0[nt], pb1[nt]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint32_t b0 = transpose_8x8(pack_f16x2(pr[nt][0] * vs[0][gi], pr[nt][1] * vs[0][gi]));
+                    const uint32_t b1 = transpose_8x8(pack_f16x2(pr[nt][2] * vs[1][gi], pr[nt][3] * vs[1][gi]));
+                    mma_f16(o[nt][2 * gi], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
+                    mma_f16(o[nt][2 * gi + 1], u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u, b0, b1);
                 }
             }
         }
         __syncwarp();
-        if (lane == 0 && i + STAGES < mine) issue(i + STAGES);
+        if (lane == 0 && i + STAGES < mine) issue(st);
     }
     if (!ok) {
         abort_flag = 1;
@@ -525,11 +561,17 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
                 sm_m[warp][r] = v > 0.f || v != v ? m[nt][c] : -INFINITY;
                 sm_l[warp][r] = v;
             }
+            const float s_ref = 1.f / s_inv;
 #pragma unroll
-            for (int j = 0; j < J * 4; ++j) {
-                const int ch = 8 * (4 * (ng0 + j / 4) + (g >> 1)) + (j & 3);
-                so[(warp * 8 * NT + r) * D + ch] = o[nt][j][c];
-                so[(warp * 8 * NT + r) * D + ch + 4] = o[nt][j][c + 2];
+            for (int gi = 0; gi < NG; ++gi) {
+                float mn = om[nt][gi][c];
+                mn += __shfl_xor_sync(0xffffffffu, mn, 4);
+                mn += __shfl_xor_sync(0xffffffffu, mn, 8);
+                mn += __shfl_xor_sync(0xffffffffu, mn, 16);
+                const float *lo = o[nt][2 * gi], *hi = o[nt][2 * gi + 1];
+                *reinterpret_cast<float4 *>(so + (warp * 8 * NT + r) * D + 32 * gi + 4 * g) =
+                    make_float4(fmaf(lo[c] * 0x1p24f, s_ref, mn), fmaf(lo[c + 2] * 0x1p20f, s_ref, mn),
+                                fmaf(hi[c] * 0x1p24f, s_ref, mn), fmaf(hi[c + 2] * 0x1p20f, s_ref, mn));
             }
         }
     }
