@@ -956,9 +956,8 @@ static size_t kv4_lse_bytes(const Kv4AttnProblem &kp) { return align256((size_t)
 static size_t kv4_scores_bytes(const Kv4AttnProblem &kp) {
     return align256((size_t)kp.a.B * kp.a.Hq * kp.a.Sq * kp.a.Sk * sizeof(float));
 }
-static size_t kv4_workspace(const Kv4AttnProblem &kp, int splits, bool weights) {
-    return partial_bytes(splits, (long long)kp.a.B * kp.a.Hq * kp.a.Sq, kp.a.D) +
-           (weights ? kv4_lse_bytes(kp) + kv4_scores_bytes(kp) : 0);
+static size_t kv4_workspace(const Kv4AttnProblem &kp, int sm_count, bool weights) {
+    return kv4_attn_partial_bytes(kp, sm_count) + (weights ? kv4_lse_bytes(kp) + kv4_scores_bytes(kp) : 0);
 }
 
 int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int S, int D, int with_weights, size_t *bytes) {
@@ -972,7 +971,7 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
     if (st != OSF_OK || empty) return st;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
-    *bytes = kv4_workspace(kp, kv4_attn_pick_splits(kp, dev->sm_count), with_weights != 0);
+    *bytes = kv4_workspace(kp, dev->sm_count, with_weights != 0);
     return OSF_OK;
 }
 
@@ -987,18 +986,15 @@ int osf_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, in
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     AttnProblem &p = kp.a;
     p.status = dev->status;
-    p.splits = kv4_attn_pick_splits(kp, dev->sm_count);
     kp.accumulate = accumulate != 0;
-    const long long rows = (long long)B * Hq * Sq;
-    const size_t need = kv4_workspace(kp, p.splits, weights != nullptr);
+    const size_t need = kv4_workspace(kp, dev->sm_count, weights != nullptr);
     if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
-    if (p.splits > 1) carve_partials(p, workspace, rows);
     if (weights) {
-        char *at = static_cast<char *>(workspace) + partial_bytes(p.splits, rows, D);
+        char *at = static_cast<char *>(workspace) + kv4_attn_partial_bytes(kp, dev->sm_count);
         if (!p.lse) p.lse = reinterpret_cast<float *>(at);
         kp.scores = reinterpret_cast<float *>(at + kv4_lse_bytes(kp));
     }
-    return launch_status(launch_attn_kv4(kp, (cudaStream_t)stream));
+    return launch_status(launch_attn_kv4(kp, workspace, dev->sm_count, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ eviction

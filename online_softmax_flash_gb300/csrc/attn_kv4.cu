@@ -220,6 +220,13 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// D = A B, no accumulator.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
@@ -229,6 +236,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// Channels c .. c+3 of a finished row with maximum M, denominator L and numerator A.
+__device__ __forceinline__ void write_row(const AttnProblem &p, int b, int hq, int qi, int c, float4 A, float M, float L) {
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;   // a row that saw nothing gives 0
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + o_at(p, b, hq, qi) + c;
+    o[0] = __float2bfloat16_rn(A.x * inv); o[1] = __float2bfloat16_rn(A.y * inv);
+    o[2] = __float2bfloat16_rn(A.z * inv); o[3] = __float2bfloat16_rn(A.w * inv);
+    if (p.lse && c == 0)
+        p.lse[((long long)b * p.Hq + hq) * p.Sq + qi] = L > 0.f ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
 }
 
 template <int N>
@@ -250,9 +267,45 @@ __device__ __forceinline__ Words<N> lds_words(const unsigned char *p) {
     return r;
 }
 
+// Work is cut flat: an item is one block of query rows of one (batch, kv head), of max(1, ceil(length / TK))
+// tiles; the items lie one after another (batch, kv head, row block), and CTA c of nc takes the c-th
+// part of all tiles, whatever items it spans.  So every CTA gets the same number of tiles, in one wave,
+// for any mix of lengths.  An item inside one part is finished there; of the others a CTA holds at most
+// two pieces, the end of one that began before (slot 2c of the partial states) and the start of one that goes
+// on (slot 2c + 1).
+struct FlatWork {
+    long long total, base;   // tiles of all items, and of the batches before b
+    int nc;                  // CTAs that take part
+};
+constexpr int kMinTiles = 2 * TW;   // tiles worth a CTA: two for every warp
+
+__device__ __forceinline__ int item_tiles(const Kv4AttnProblem &kp, int b, int tk) {
+    return max(1, (kv4_length(kp.lens, b, kp.a.Sk, kp.a.status) + tk - 1) / tk);
+}
+// Called by a whole warp.
+__device__ __forceinline__ FlatWork flat_work(const Kv4AttnProblem &kp, int tk, int items_per_b, int b, int grid) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0, before = 0;
+    for (int i = lane; i < kp.a.B; i += 32) {
+        const long long n = item_tiles(kp, i, tk);
+        all += n;
+        before += i < b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    FlatWork f;
+    f.total = all * items_per_b;
+    f.base = before * items_per_b;
+    f.nc = (int)max(1LL, min((long long)grid, f.total / kMinTiles));
+    return f;
+}
+
 template <int D, int NT>
 __global__ void __launch_bounds__(TW * 32, NT == 1 || D == 64 ? 2 : 1)
-attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
+attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat) {
     using C = TcCfg<D, NT>;
     constexpr int NG = C::NG, REC = C::REC, TK = C::TK, STAGES = C::STAGES;
     const AttnProblem &p = kp.a;
@@ -263,14 +316,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
-    const int kvbh = blockIdx.x, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
-    const int r0 = blockIdx.z * (8 * NT), rows = min(8 * NT, R - r0);
-    const int n = kv4_length(kp.lens, b, p.Sk, p.status);
-    int begin, end;
-    part_of(n, TK, blockIdx.y, p.splits, begin, end);
-    // this warp's tiles of the part: warp, warp + 8, ...
-    const int tiles = (end - begin + TK - 1) / TK;
-    const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;
     unsigned char *ring = smem + warp * (STAGES * kSlot);
     if (lane == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&full[warp][s]), 1);
@@ -278,6 +323,40 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         if (warp == 0) abort_flag = 0;
     }
     __syncthreads();
+    const int items_per_b = p.Hkv * row_blocks;
+    int rest = 0;                     // tiles that this CTA still has to take
+    int b = 0, item = 0, tile0 = 0;   // the next piece: item of batch b, from tile0 on
+    if (flat) {
+        const FlatWork w = flat_work(kp, TK, items_per_b, 0, gridDim.x);
+        if ((int)blockIdx.x >= w.nc) return;
+        const long long pos = w.total * blockIdx.x / w.nc;
+        rest = (int)(w.total * (blockIdx.x + 1) / w.nc - pos);
+        long long at = 0;
+        for (;; ++b) {
+            const long long tb = (long long)item_tiles(kp, b, TK) * items_per_b;
+            if (pos < at + tb) break;
+            at += tb;
+        }
+        const int tb = item_tiles(kp, b, TK);
+        item = (int)((pos - at) / tb);
+        tile0 = (int)((pos - at) % tb);
+    } else {   // one whole item per CTA
+        b = blockIdx.x / items_per_b;
+        item = blockIdx.x % items_per_b;
+    }
+    int phase = 0;   // bit s: parity of the next wait on ring slot s
+    bool ok = true;
+    for (;;) {
+    const int kvh = item / row_blocks, kvbh = b * p.Hkv + kvh;
+    const int r0 = item % row_blocks * (8 * NT), rows = min(8 * NT, R - r0);
+    const int n = kv4_length(kp.lens, b, p.Sk, p.status);
+    const int nb = max(1, (n + TK - 1) / TK);
+    const int take = flat ? min(nb - tile0, rest) : nb;
+    const bool whole = take == nb;
+    const int begin = tile0 * TK, end = min(n, (tile0 + take) * TK);
+    // this warp's tiles of the piece: warp, warp + 8, ...
+    const int tiles = (end - begin + TK - 1) / TK;
+    const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;
     const unsigned char *src = kp.cache + ((long long)kvbh * p.Sk + begin + warp * TK) * REC;   // the next tile to copy
     int left = end - begin - warp * TK;                                                       // records from there on
     auto issue = [&](int slot) {
@@ -294,7 +373,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     uint32_t qb[NT][NG][4];
     float qs[NT][NG][2];        // sums of Q over a group, of this lane's two columns 2t, 2t + 1
     float f[NT][2];             // S to base-2 score: undoes the scalings, times scale * log2 e
-    int lim[NT][2];
     bool wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -350,8 +428,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
             const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c);
             wide |= back > 100;   // this and scale * log2 e may pass float32's range: applied in two steps
             f[nt][c] = (float)back;
-            const int col = r0 + nt * 8 + 2 * t + c;
-            lim[nt][c] = p.causal && col < R ? max(0, n - p.Sq + col % p.Sq + 1) : n;
         }
     }
     const int lim_all = p.causal ? n - p.Sq + 1 : n;   // keys below this are visible to every row
@@ -382,13 +458,13 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
     const int off_v1 = tile_key(2 * t + 1) * REC + D / 2 + (g >> 1) * (D / 8);
     const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;                         // lane's half of a word, of two keys
     float *sc_out = kp.scores ? kp.scores + ((long long)kvbh * R + r0 + 2 * t) * p.Sk : nullptr;
-    bool ok = true;
     int i = 0;
     for (; i < mine; ++i) {
         const int st = i % STAGES;
-        ok = mbar_wait(smem_u32(&full[warp][st]), (i / STAGES) & 1, &abort_flag);
+        ok = mbar_wait(smem_u32(&full[warp][st]), (phase >> st) & 1, &abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        phase ^= 1 << st;
         unsigned char *slot = ring + st * kSlot;
         const int k0 = begin + (warp + TW * i) * TK;
         const int subs = min(TK / 16, (end - k0 + 15) / 16);
@@ -417,8 +493,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
                     const float s1 = lo_bf16(pb.w[gi]), m1 = hi_bf16(pb.w[gi]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        float d[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(d, a & 0x000f000fu, c & 0x000f000fu, a & 0x00f000f0u, c & 0x00f000f0u, qb[nt][gi][0],
+                        float d[4];
+                        mma_f16_first(d, a & 0x000f000fu, c & 0x000f000fu, a & 0x00f000f0u, c & 0x00f000f0u, qb[nt][gi][0],
                                 qb[nt][gi][1]);
                         mma_f16(d, a8 & 0x000f000fu, c8 & 0x000f000fu, a8 & 0x00f000f0u, c8 & 0x00f000f0u, qb[nt][gi][2],
                                 qb[nt][gi][3]);
@@ -444,8 +520,11 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key + (e >> 1) * 8 >= lim[nt][e & 1]) y[nt][e] = -INFINITY;
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = r0 + nt * 8 + 2 * t + (e & 1);
+                        const int lim = p.causal ? n - p.Sq + row % p.Sq + 1 : n;
+                        if (key + (e >> 1) * 8 >= lim) y[nt][e] = -INFINITY;
+                    }
             }
             if (sc_out) {
 #pragma unroll
@@ -472,7 +551,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) raise |= y[nt][e] > m[nt][e & 1] + 8.f;
+                for (int e = 0; e < 4; ++e) raise |= y[nt][e] - m[nt][e & 1] > 8.f;
             if (__any_sync(0xffffffffu, raise)) {
                 s_max = warp_max(s_max);
                 float sa = 1.f;
@@ -542,7 +621,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         if (lane == 0) {
             atomicExch(p.status, kStatusTimeout);
             for (int j = i; j < min(i + STAGES, mine); ++j)   // let issued copies land before the ring is reused
-                mbar_wait(smem_u32(&full[warp][j % STAGES]), (j / STAGES) & 1, nullptr, 20000000ull);
+                mbar_wait(smem_u32(&full[warp][j % STAGES]), (phase >> (j % STAGES)) & 1, nullptr, 20000000ull);
         }
     }
     // ------------------------------------------------------------- merge the warps' states
@@ -576,31 +655,72 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec) {
         }
     }
     __syncthreads();
-    const long long rows_total = (long long)p.B * p.Hq * p.Sq;
-    for (int x = tid; x < rows * D; x += TW * 32) {
-        const int r = x / D, c = x % D, gr = r0 + r;
-        float M = -INFINITY, L = 0.f, A = 0.f;
+    const size_t slot = 2 * (size_t)blockIdx.x + (tile0 == 0 ? 1 : 0);
+    for (int x = tid; x < rows * (D / 4); x += TW * 32) {
+        const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
+        float M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < TW; ++w) M = fmaxf(M, sm_m[w][r]);
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int w = 0; w < TW; ++w) {
             const float wt = ex2_approx(sm_m[w][r] - ref);
-            A += wt * so[(w * 8 * NT + r) * D + c];
-            L += wt * sm_l[w][r];
+            const float4 v = *reinterpret_cast<const float4 *>(so + (w * 8 * NT + r) * D + c);
+            A.x = fmaf(wt, v.x, A.x); A.y = fmaf(wt, v.y, A.y);
+            A.z = fmaf(wt, v.z, A.z); A.w = fmaf(wt, v.w, A.w);
+            L = fmaf(wt, sm_l[w][r], L);
         }
-        const int hq = kvh * G + gr / p.Sq, qi = gr % p.Sq;
-        const long long grow = ((long long)b * p.Hq + hq) * p.Sq + qi;
-        if (p.splits == 1) {
-            static_cast<__nv_bfloat16 *>(p.o)[o_at(p, b, hq, qi) + c] = __float2bfloat16_rn(L > 0.f || L != L ? A / L : 0.f);
-            if (p.lse && c == 0) p.lse[grow] = L > 0.f ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
-        } else {
-            p.part_acc[((size_t)blockIdx.y * rows_total + grow) * D + c] = A;
-            if (c == 0) {
-                p.part_m[(size_t)blockIdx.y * rows_total + grow] = M;
-                p.part_l[(size_t)blockIdx.y * rows_total + grow] = L;
-            }
+        if (whole) write_row(p, b, kvh * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
+        else {
+            *reinterpret_cast<float4 *>(kp.part + (slot * 8 * NT + r) * D + c) = A;
+            if (c == 0) kp.part_ml[slot * 8 * NT + r] = make_float2(M, L);
         }
+    }
+    if (!flat) break;
+    rest -= take;
+    if (rest <= 0 || abort_flag) break;   // (after a timeout the copies are settled; the rest is left)
+    tile0 = 0;
+    if (++item == items_per_b) {
+        item = 0;
+        ++b;
+    }
+    fence_proxy_async_smem();   // the merge buffer becomes ring again: its accesses before the next copies
+    __syncthreads();
+    }
+}
+
+// Rows of the items that several CTAs shared: a block per item, the same cut of the work as above.
+template <int D, int NT>
+__global__ void __launch_bounds__(128) kv4_combine_kernel(const Kv4AttnProblem kp, int row_blocks, int grid) {
+    griddep_wait();
+    constexpr int TK = TcCfg<D, NT>::TK;
+    const AttnProblem &p = kp.a;
+    const int G = p.Hq / p.Hkv, R = G * p.Sq, items_per_b = p.Hkv * row_blocks;
+    const int b = blockIdx.x / items_per_b, item = blockIdx.x % items_per_b;
+    const FlatWork w = flat_work(kp, TK, items_per_b, b, grid);
+    const int nb = item_tiles(kp, b, TK);
+    const long long p0 = w.base + (long long)item * nb, p1 = p0 + nb;
+    // CTA of tile x: the last one whose part begins at or before it
+    const int c0 = (int)(((p0 + 1) * w.nc - 1) / w.total), c1 = (int)((p1 * w.nc - 1) / w.total);
+    if (c0 == c1) return;
+    const int r0 = item % row_blocks * (8 * NT), rows = min(8 * NT, R - r0);
+    for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
+        const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
+        float M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = c0; k <= c1; ++k) {
+            const size_t slot = 2 * (size_t)k + (k == c0 ? 1 : 0);
+            const float2 ml = kp.part_ml[slot * 8 * NT + r];
+            const float4 v = *reinterpret_cast<const float4 *>(kp.part + (slot * 8 * NT + r) * D + c);
+            const float mx = fmaxf(M, ml.x), ref = mx == -INFINITY ? 0.f : mx;
+            const float a = ex2_approx(M - ref), wt = ex2_approx(ml.x - ref);
+            A.x = fmaf(wt, v.x, A.x * a); A.y = fmaf(wt, v.y, A.y * a);
+            A.z = fmaf(wt, v.z, A.z * a); A.w = fmaf(wt, v.w, A.w * a);
+            L = fmaf(wt, ml.y, L * a);
+            M = mx;
+        }
+        write_row(p, b, item / row_blocks * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
     }
 }
 
@@ -630,25 +750,28 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
 
 }  // namespace
 
-// Query rows per CTA of the tensor-core kernel: 8 or 16.
-static int tc_rows(int R) { return R <= 8 ? 8 : 16; }
-
 static bool use_tc(const AttnProblem &p) { return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128); }
 
-int kv4_attn_pick_splits(const Kv4AttnProblem &kp, int sm_count) {
-    const AttnProblem &p = kp.a;
+// Launch shape of the tensor-core kernel.  Items whose tiles give every warp at most two are not cut (one
+// launch, no combine); else one wave of CTAs shares all tiles, as many as the longest possible lengths are worth.
+struct TcPlan {
+    int nt, row_blocks, flat, grid;
+};
+static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
+    TcPlan t;
+    const int R = p.Hq / p.Hkv * p.Sq, tk = (int)kSlot / kv4_record_bytes(p.D);
+    t.nt = R <= 8 ? 1 : 2;
+    t.row_blocks = (R + 8 * t.nt - 1) / (8 * t.nt);
+    const long long items = (long long)p.B * p.Hkv * t.row_blocks, per = ((long long)p.Sk + tk - 1) / tk;
+    const long long wave = (long long)sm_count * (t.nt == 1 || p.D == 64 ? 2 : 1);
+    t.flat = per > kMinTiles;
+    const long long worth = items * per / kMinTiles;
+    t.grid = (int)(!t.flat ? items : worth < wave ? (worth < 1 ? 1 : worth) : wave);
+    return t;
+}
+
+static int simt_splits(const AttnProblem &p, int sm_count) {
     const int R = p.Hq / p.Hkv * p.Sq;
-    if (use_tc(p)) {
-        const int rb = tc_rows(R), tk = (int)kSlot / kv4_record_bytes(p.D);
-        const long long items = (long long)p.B * p.Hkv * ((R + rb - 1) / rb);
-        const long long tiles = ((long long)p.Sk + tk - 1) / tk;
-        // about four waves of two CTAs per SM, so the last wave's imbalance stays small, but at least
-        // two tiles for each warp of a part
-        long long s = (8LL * sm_count + items / 2) / items;
-        const long long most = tiles / (2 * TW);
-        s = s < most ? s : most;
-        return (int)(s < 1 ? 1 : s > 65535 ? 65535 : s);
-    }
     const long long items = (long long)p.B * p.Hkv * ((R + RB - 1) / RB);
     const long long units = ((long long)p.Sk + 31) / 32;
     long long s = (8LL * sm_count + items - 1) / items;
@@ -657,35 +780,62 @@ int kv4_attn_pick_splits(const Kv4AttnProblem &kp, int sm_count) {
     return (int)(s < 1 ? 1 : s > 1024 ? 1024 : s);
 }
 
-template <int D, int NT>
-static cudaError_t launch_tc_t(const Kv4AttnProblem &kp, cudaStream_t s) {
-    using C = TcCfg<D, NT>;
+static size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
+
+size_t kv4_attn_partial_bytes(const Kv4AttnProblem &kp, int sm_count) {
     const AttnProblem &p = kp.a;
-    const cudaError_t e = set_max_dynamic_smem((const void *)attn_kv4_tc_kernel<D, NT>, (int)C::SMEM);
-    if (e != cudaSuccess) return e;
-    const int R = p.Hq / p.Hkv * p.Sq;
-    const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 7) == 0;
-    attn_kv4_tc_kernel<D, NT><<<dim3((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + 8 * NT - 1) / (8 * NT))), TW * 32,
-                                C::SMEM, s>>>(kp, q_vec);
-    return cudaGetLastError();
+    if (use_tc(p)) {
+        const TcPlan t = tc_plan(p, sm_count);
+        const size_t rows = 2 * (size_t)t.grid * 8 * t.nt;
+        return t.flat ? round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float2)) : 0;
+    }
+    const int splits = simt_splits(p, sm_count);
+    const size_t rows = (size_t)splits * p.B * p.Hq * p.Sq;
+    return splits > 1 ? round256(rows * p.D * sizeof(float)) + 2 * round256(rows * sizeof(float)) : 0;
 }
 
-cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp, cudaStream_t s) {
+template <int D, int NT>
+static cudaError_t launch_tc_t(Kv4AttnProblem kp, const TcPlan &t, char *partials, cudaStream_t s) {
+    using C = TcCfg<D, NT>;
     const AttnProblem &p = kp.a;
+    cudaError_t e = set_max_dynamic_smem((const void *)attn_kv4_tc_kernel<D, NT>, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    kp.part = reinterpret_cast<float *>(partials);
+    kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * 8 * NT * D * sizeof(float)));
+    const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 7) == 0;
+    attn_kv4_tc_kernel<D, NT><<<t.grid, TW * 32, C::SMEM, s>>>(kp, q_vec, t.row_blocks, t.flat);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !t.flat) return e;
+    count_launches(1);
+    return launch_dependent(kv4_combine_kernel<D, NT>, dim3((unsigned)(p.B * p.Hkv * t.row_blocks)), dim3(128), 0, s, kp,
+                            t.row_blocks, t.grid);
+}
+
+cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_count, cudaStream_t s) {
+    Kv4AttnProblem kp = kp0;
+    AttnProblem &p = kp.a;
     const int R = p.Hq / p.Hkv * p.Sq;
     cudaError_t e;
     if (use_tc(p)) {
-        const bool few = tc_rows(R) == 8;
-        e = p.D == 64 ? (few ? launch_tc_t<64, 1>(kp, s) : launch_tc_t<64, 2>(kp, s))
-                      : (few ? launch_tc_t<128, 1>(kp, s) : launch_tc_t<128, 2>(kp, s));
+        const TcPlan t = tc_plan(p, sm_count);
+        char *at = static_cast<char *>(partials);
+        e = p.D == 64 ? (t.nt == 1 ? launch_tc_t<64, 1>(kp, t, at, s) : launch_tc_t<64, 2>(kp, t, at, s))
+                      : (t.nt == 1 ? launch_tc_t<128, 1>(kp, t, at, s) : launch_tc_t<128, 2>(kp, t, at, s));
     } else {
+        p.splits = simt_splits(p, sm_count);
+        const size_t rows = (size_t)p.splits * p.B * p.Hq * p.Sq;
+        char *at = static_cast<char *>(partials);
+        p.part_acc = reinterpret_cast<float *>(at);
+        p.part_m = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)));
+        p.part_l = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float)));
         const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + RB - 1) / RB));
         if (p.dtype == OSF_F32) attn_kv4_kernel<float><<<grid, GW * 32, 0, s>>>(kp);
         else attn_kv4_kernel<__nv_bfloat16><<<grid, GW * 32, 0, s>>>(kp);
+        count_launches(1);
         e = cudaGetLastError();
+        if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     }
-    count_launches(1);
-    if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     if (e == cudaSuccess && kp.weights && p.Sk > 0) {
         count_launches(1);
         e = launch_dependent(kv4_weights_kernel, dim3((unsigned)((p.Sk + 255) / 256), (unsigned)(p.B * p.Hkv)), dim3(256), 0,

@@ -44,9 +44,12 @@ struct Kv4AttnProblem {
     float *weights;             // nullable [B, Hkv, Sk]
     int accumulate;             // add to weights instead of overwriting them
     float *scores;              // with weights: base-2 scores [B * Hkv][G * Sq][Sk]
+    float *part;                // tensor-core kernel: numerators of items that several CTAs share,
+    float2 *part_ml;            //   and their maxima and denominators
 };
-int kv4_attn_pick_splits(const Kv4AttnProblem &p, int sm_count);
-cudaError_t launch_attn_kv4(const Kv4AttnProblem &p, cudaStream_t s);
+// Bytes of partial states that the call keeps in `partials`.
+size_t kv4_attn_partial_bytes(const Kv4AttnProblem &p, int sm_count);
+cudaError_t launch_attn_kv4(const Kv4AttnProblem &p, void *partials, int sm_count, cudaStream_t s);
 
 // Valid records of sequence b; a length outside [0, S] is cut to it and recorded in the status word.
 __device__ __forceinline__ int kv4_length(const int *lens, int b, int S, int *status) {
