@@ -181,19 +181,21 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // code * 2^-20 (nibbles 1, 5; Q is scaled by 2^-4 there), so one AND per pair makes an exact operand.  Q is
 // held in float16 after an exact power-of-two scaling per row that puts its largest entry at 2^13 .. 2^14:
 // 8 significant bits fit, down to entries 2^-28 of the row's largest.  A group's two k-steps go to a
-// fresh accumulator, and scale and minimum are applied to it in float32.
+// fresh accumulator, and the scale is applied to it in float32; the sum of minimum * (sum Q of the group) is
+// one more MMA, bfloat16, whose k index runs over the groups three times, for three bfloat16 parts of sum Q.
 // V: likewise, with scale and minimum moved to the other side of the product: for the channels of one group
 //   sum_k P_k (minimum_k + scale_k code_kc) = sum_k P_k minimum_k + sum_k (P_k scale_k) code_kc,
 // the first sum in float32 (one per row and group), the second an MMA whose B operand is P * scale in
 // float16.  One byte permute interleaves the halves of two keys' words, after which one AND makes the pair
-// (code of key k, code of key k') of a channel.  P * scale is rounded to 11 bits; a power of two common to
-// the warp's keys keeps it in range: scales up to 64 times the reference need no new one, and 2^-21 of it
-// still keeps all 11 bits.  P moves from the S^T accumulator layout to the B operand by movmatrix.
+// (code of key k, code of key k') of a channel.  P * scale is rounded to 11 bits.  P is taken relative to a
+// reference that also holds the largest V scale seen, so that P * scale starts at 2^6 and may grow to 2^14
+// before the reference moves; products down to 2^-20 of the largest keep all 11 bits.
+// P moves from the S^T accumulator layout to the B operand by movmatrix.
 //
 // Each warp streams its own 5120-byte runs of records through a ring of bulk copies (one instruction
 // per run, since K and V of a token are adjacent) and keeps its own softmax state; the eight states merge
 // through shared memory at the end.  The running maximum is lazy: a row keeps its reference until a
-// score passes it by more than 8 in base 2, so most tiles need no cross-lane reduction and no rescale.
+// score passes it by 8 in base 2, so most tiles need no cross-lane reduction and no rescale.
 constexpr int TW = 8;                     // warps per CTA
 constexpr uint32_t kSlot = 5120;          // bytes of one ring slot: 32 records at D = 128, 64 at D = 64
 constexpr float kRowFloor = -1.7e38f;     // reference maximum of a row that has seen nothing
@@ -220,7 +222,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ float trunc_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 // D = A B, no accumulator.
+__device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                               uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
@@ -303,7 +312,7 @@ __device__ __forceinline__ FlatWork flat_work(const Kv4AttnProblem &kp, int tk, 
     return f;
 }
 
-template <int D, int NT>
+template <int D, int NT, bool SCORES>
 __global__ void __launch_bounds__(TW * 32, NT == 1 || D == 64 ? 2 : 1)
 attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat) {
     using C = TcCfg<D, NT>;
@@ -371,9 +380,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
 
     // Q as the B operand: column n = query row, lane (g, t) holds row g's channels 8t .. 8t+7 of each group
     uint32_t qb[NT][NG][4];
-    float qs[NT][NG][2];        // sums of Q over a group, of this lane's two columns 2t, 2t + 1
+    uint32_t qm[NT][2];         // sums of Q over the groups, as the B operand of the minima
     float f[NT][2];             // S to base-2 score: undoes the scalings, times scale * log2 e
-    bool wide = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int r = nt * 8 + g, gr = r0 + r;
@@ -403,8 +411,9 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int ex = max(-114, min(126, 13 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+        const int ex = max(-90, min(100, 13 - ((int)(__float_as_uint(mx) >> 23) - 127)));
         const float up = __uint_as_float((uint32_t)(ex + 127) << 23);
+        float sum[NG];
 #pragma unroll
         for (int gi = 0; gi < NG; ++gi) {
             float s = 0.f;
@@ -419,28 +428,27 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
             qb[nt][gi][3] = pack_f16x2(x[gi][3] * 0.0625f, x[gi][7] * 0.0625f);
             s += __shfl_xor_sync(0xffffffffu, s, 1);
             s += __shfl_xor_sync(0xffffffffu, s, 2);
-            s *= 0x1p-24f;   // in the unit of the code products
-            qs[nt][gi][0] = __shfl_sync(0xffffffffu, s, 8 * t);
-            qs[nt][gi][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+            sum[gi] = s * 0x1p-24f;   // in the unit of the code products
         }
+        // k = 2t, 2t + 1: lanes t < 2 the leading parts of groups 2t, 2t + 1, lanes t >= 2 the next parts of
+        // groups 2t - 4, 2t - 3;  k + 8: lanes t < 2 the last parts, else 0.  (D = 64: groups 0, 1 only.)
+        float s0 = sum[0], s1 = sum[1];
+        if (NG == 4 && (t & 1)) s0 = sum[NG - 2], s1 = sum[NG - 1];
+        if (NG == 2 && (t & 1)) s0 = s1 = 0.f;
+        const float h0 = trunc_bf16(s0), h1 = trunc_bf16(s1), e0 = s0 - h0, e1 = s1 - h1;
+        const float d0 = trunc_bf16(e0), d1 = trunc_bf16(e1);
+        qm[nt][0] = t < 2 ? pack_bf16x2(h0, h1) : pack_bf16x2(d0, d1);
+        qm[nt][1] = t < 2 ? pack_bf16x2(e0 - d0, e1 - d1) : 0u;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c);
-            wide |= back > 100;   // this and scale * log2 e may pass float32's range: applied in two steps
-            f[nt][c] = (float)back;
+            const int back = 24 - __shfl_sync(0xffffffffu, ex, 8 * t + 4 * c);   // -76 .. 114
+            f[nt][c] = __uint_as_float((uint32_t)(back + 127) << 23) * p.scale_log2;
         }
     }
     const int lim_all = p.causal ? n - p.Sq + 1 : n;   // keys below this are visible to every row
 
-    wide = __any_sync(0xffffffffu, wide);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            f[nt][c] = __uint_as_float((uint32_t)(max(-126, (int)f[nt][c] - (wide ? 64 : 0)) + 127) << 23) * p.scale_log2;
-
-    // o: code sums, tile (group, h), row g (+ 8) = channel 32 group + 4 g + 2 h (+ 1), in units of 2^-24 (2^-20)
-    // of the scale reference;  om: sums of P * minimum of a group
+    // o: code sums, tile (group, h), row g (+ 8) = channel 32 group + 4 g + 2 h (+ 1), in units of 2^-24 (2^-20);
+    // om: sums of P * minimum of a group
     float o[NT][NG * 2][4], om[NT][NG][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -451,13 +459,15 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
         m[nt][0] = m[nt][1] = kRowFloor;
         l[nt][0] = l[nt][1] = 0.f;
     }
-    float s_inv = 1.f, s_lim = -1.f;   // 1 / scale reference; the scale that asks for a new one
+    int s_exp = -60;           // above every V scale's exponent so far (scales below 2^-80 fade to 0)
+    float x_lim = 74.f;        // 14 - s_exp: a score this far above the reference has P * scale = 2^14
     const int ka = tile_key(g);
     const int off_a = ka * REC;                                                // K, and both halves' pairs: keys ka, ka + 8
+    const int off_m = off_a + D + (NG == 4 ? (t & 1) * 8 : 0);                 // K pairs whose minima this lane feeds
     const int off_v0 = tile_key(2 * t) * REC + D / 2 + (g >> 1) * (D / 8);     // V codes: keys of k = 2t, 2t + 1 (+ 8)
     const int off_v1 = tile_key(2 * t + 1) * REC + D / 2 + (g >> 1) * (D / 8);
     const uint32_t pick = (g & 1) ? 0x7632u : 0x5410u;                         // lane's half of a word, of two keys
-    float *sc_out = kp.scores ? kp.scores + ((long long)kvbh * R + r0 + 2 * t) * p.Sk : nullptr;
+    float *sc_out = SCORES ? kp.scores + ((long long)kvbh * R + r0 + 2 * t) * p.Sk : nullptr;
     int i = 0;
     for (; i < mine; ++i) {
         const int st = i % STAGES;
@@ -475,43 +485,55 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0, 0, 0, 0);
             __syncwarp();
         }
+        // the tile's largest V scale: a key per lane
+        {
+            float s_max = 0.f;
+#pragma unroll
+            for (int r = 0; r < TK; r += 32) {
+                if (r + lane < subs * 16) {
+                    const Words<NG> w = lds_words<NG>(slot + (r + lane) * REC + D + D / 8);
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) s_max = fmaxf(s_max, lo_bf16(w.w[gi]));
+                }
+            }
+            const int e = (int)(__float_as_uint(s_max) >> 23) - 126;   // s_max < 2^e
+            if (__any_sync(0xffffffffu, e > s_exp)) {
+                s_exp = max(s_exp, __reduce_max_sync(0xffffffffu, e));
+                x_lim = 14.f - (float)s_exp;
+            }
+        }
 #pragma unroll 1
         for (int sub = 0; sub < subs; ++sub) {
             const unsigned char *tile = slot + sub * 16 * REC;
             const int key = k0 + sub * 16 + ka;
             float y[NT][4];
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) y[nt][0] = y[nt][1] = y[nt][2] = y[nt][3] = 0.f;
             const unsigned char *ra = tile + off_a, *rb = ra + 8 * REC;
             {
+                const Words<2> ma = lds_words<2>(tile + off_m), mb = lds_words<2>(tile + off_m + 8 * REC);
+                const uint32_t a0 = __byte_perm(ma.w[0], ma.w[1], 0x7632), a1 = __byte_perm(mb.w[0], mb.w[1], 0x7632);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) mma_bf16_first(y[nt], a0, a1, a0, a1, qm[nt][0], qm[nt][1]);
                 const Words<NG> xa = lds_words<NG>(ra + t * (D / 8)), xb = lds_words<NG>(rb + t * (D / 8));
                 const Words<NG> pa = lds_words<NG>(ra + D), pb = lds_words<NG>(rb + D);
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
                     const uint32_t a = xa.w[gi], c = xb.w[gi], a8 = a >> 8, c8 = c >> 8;
-                    const float s0 = lo_bf16(pa.w[gi]), m0 = hi_bf16(pa.w[gi]);
-                    const float s1 = lo_bf16(pb.w[gi]), m1 = hi_bf16(pb.w[gi]);
+                    const float s0 = lo_bf16(pa.w[gi]), s1 = lo_bf16(pb.w[gi]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         float d[4];
                         mma_f16_first(d, a & 0x000f000fu, c & 0x000f000fu, a & 0x00f000f0u, c & 0x00f000f0u, qb[nt][gi][0],
-                                qb[nt][gi][1]);
+                                      qb[nt][gi][1]);
                         mma_f16(d, a8 & 0x000f000fu, c8 & 0x000f000fu, a8 & 0x00f000f0u, c8 & 0x00f000f0u, qb[nt][gi][2],
                                 qb[nt][gi][3]);
-                        y[nt][0] = fmaf(s0, d[0], fmaf(m0, qs[nt][gi][0], y[nt][0]));
-                        y[nt][1] = fmaf(s0, d[1], fmaf(m0, qs[nt][gi][1], y[nt][1]));
-                        y[nt][2] = fmaf(s1, d[2], fmaf(m1, qs[nt][gi][0], y[nt][2]));
-                        y[nt][3] = fmaf(s1, d[3], fmaf(m1, qs[nt][gi][1], y[nt][3]));
+                        y[nt][0] = fmaf(s0, d[0], y[nt][0]);
+                        y[nt][1] = fmaf(s0, d[1], y[nt][1]);
+                        y[nt][2] = fmaf(s1, d[2], y[nt][2]);
+                        y[nt][3] = fmaf(s1, d[3], y[nt][3]);
                     }
                 }
             }
-            if (wide) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) y[nt][e] *= 0x1p64f;
-            }
-            bool raise = false;
+            // base-2 scores; -inf where the row does not see the key
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -526,13 +548,42 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                         if (key + (e >> 1) * 8 >= lim) y[nt][e] = -INFINITY;
                     }
             }
-            if (sc_out) {
+            if (SCORES) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (nt * 8 + 2 * t + (e & 1) < rows && key + (e >> 1) * 8 < end)
                             sc_out[(long long)(nt * 8 + (e & 1)) * p.Sk + key + (e >> 1) * 8] = y[nt][e];
+            }
+            float top = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                top = fmax3(top, y[nt][0] - m[nt][0], y[nt][1] - m[nt][1]);
+                top = fmax3(top, y[nt][2] - m[nt][0], y[nt][3] - m[nt][1]);
+            }
+            if (__any_sync(0xffffffffu, top > x_lim)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(y[nt][c], y[nt][c + 2]);
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                        // the reference at which P * scale is at most 2^6, where that is higher
+                        mx = fmaxf(m[nt][c], mx - (x_lim - 8.f));
+                        const float a = ex2_approx(m[nt][c] - mx);
+                        m[nt][c] = mx;
+                        l[nt][c] *= a;
+#pragma unroll
+                        for (int j = 0; j < NG * 2; ++j) {
+                            o[nt][j][c] *= a;
+                            o[nt][j][c + 2] *= a;
+                        }
+#pragma unroll
+                        for (int gi = 0; gi < NG; ++gi) om[nt][gi][c] *= a;
+                    }
             }
             // V scales and minima of this lane's two keys
             float vs[2][NG], vm[2][NG];
@@ -543,45 +594,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                     vs[0][gi] = lo_bf16(pa.w[gi]); vm[0][gi] = hi_bf16(pa.w[gi]);
                     vs[1][gi] = lo_bf16(pb.w[gi]); vm[1][gi] = hi_bf16(pb.w[gi]);
                 }
-            }
-            float s_max = fmaxf(vs[0][0], vs[1][0]);
-#pragma unroll
-            for (int gi = 1; gi < NG; ++gi) s_max = fmax3(s_max, vs[0][gi], vs[1][gi]);
-            raise = s_max > s_lim;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) raise |= y[nt][e] - m[nt][e & 1] > 8.f;
-            if (__any_sync(0xffffffffu, raise)) {
-                s_max = warp_max(s_max);
-                float sa = 1.f;
-                if (s_max > s_lim) {
-                    // the power of two at the largest scale becomes the reference
-                    const int ex = max(-120, min(126, (int)(__float_as_uint(s_max) >> 23) - 127));
-                    const float inv = __uint_as_float((uint32_t)(127 - ex) << 23);
-                    sa = s_lim < 0.f ? 0.f : inv / s_inv;
-                    s_inv = inv;
-                    s_lim = 64.f * __uint_as_float((uint32_t)(127 + min(ex, 120)) << 23);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        float mx = fmaxf(m[nt][c], fmaxf(y[nt][c], y[nt][c + 2]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float a = ex2_approx(m[nt][c] - mx);
-                        m[nt][c] = mx;
-                        l[nt][c] *= a;
-#pragma unroll
-                        for (int j = 0; j < NG * 2; ++j) {
-                            o[nt][j][c] *= a * sa;
-                            o[nt][j][c + 2] *= a * sa;
-                        }
-#pragma unroll
-                        for (int gi = 0; gi < NG; ++gi) om[nt][gi][c] *= a;
-                    }
             }
             float pr[NT][4];
 #pragma unroll
@@ -595,8 +607,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                     om[nt][gi][0] = fmaf(pr[nt][0], vm[0][gi], fmaf(pr[nt][2], vm[1][gi], om[nt][gi][0]));
                     om[nt][gi][1] = fmaf(pr[nt][1], vm[0][gi], fmaf(pr[nt][3], vm[1][gi], om[nt][gi][1]));
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pr[nt][e] *= s_inv;
             }
             const Words<NG> w0 = lds_words<NG>(tile + off_v0), w1 = lds_words<NG>(tile + off_v1);
             const Words<NG> w2 = lds_words<NG>(tile + off_v0 + 8 * REC), w3 = lds_words<NG>(tile + off_v1 + 8 * REC);
@@ -640,7 +650,6 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 sm_m[warp][r] = v > 0.f || v != v ? m[nt][c] : -INFINITY;
                 sm_l[warp][r] = v;
             }
-            const float s_ref = 1.f / s_inv;
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
                 float mn = om[nt][gi][c];
@@ -649,8 +658,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 mn += __shfl_xor_sync(0xffffffffu, mn, 16);
                 const float *lo = o[nt][2 * gi], *hi = o[nt][2 * gi + 1];
                 *reinterpret_cast<float4 *>(so + (warp * 8 * NT + r) * D + 32 * gi + 4 * g) =
-                    make_float4(fmaf(lo[c] * 0x1p24f, s_ref, mn), fmaf(lo[c + 2] * 0x1p20f, s_ref, mn),
-                                fmaf(hi[c] * 0x1p24f, s_ref, mn), fmaf(hi[c + 2] * 0x1p20f, s_ref, mn));
+                    make_float4(fmaf(lo[c], 0x1p24f, mn), fmaf(lo[c + 2], 0x1p20f, mn), fmaf(hi[c], 0x1p24f, mn),
+                                fmaf(hi[c + 2], 0x1p20f, mn));
             }
         }
     }
@@ -798,12 +807,13 @@ template <int D, int NT>
 static cudaError_t launch_tc_t(Kv4AttnProblem kp, const TcPlan &t, char *partials, cudaStream_t s) {
     using C = TcCfg<D, NT>;
     const AttnProblem &p = kp.a;
-    cudaError_t e = set_max_dynamic_smem((const void *)attn_kv4_tc_kernel<D, NT>, (int)C::SMEM);
+    auto kernel = kp.scores ? attn_kv4_tc_kernel<D, NT, true> : attn_kv4_tc_kernel<D, NT, false>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     kp.part = reinterpret_cast<float *>(partials);
     kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * 8 * NT * D * sizeof(float)));
     const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 15u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 7) == 0;
-    attn_kv4_tc_kernel<D, NT><<<t.grid, TW * 32, C::SMEM, s>>>(kp, q_vec, t.row_blocks, t.flat);
+    kernel<<<t.grid, TW * 32, C::SMEM, s>>>(kp, q_vec, t.row_blocks, t.flat);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.flat) return e;
