@@ -793,7 +793,18 @@ static int check_key_weights(const void *Q, const void *K, const float *lse, flo
     return OSF_OK;
 }
 
-static size_t key_weights_partial_bytes(const KeyWeightsProblem &w, int splits) {
+// Which kernel runs a validated problem, and the bytes of partial sums it keeps in the workspace.
+enum class WeightsPath { Rows, TensorCore, Simt };
+
+static WeightsPath key_weights_path(const KeyWeightsProblem &w) {
+    if (key_weights_rows_supported(w)) return WeightsPath::Rows;
+    return key_weights_tc_supported(w) ? WeightsPath::TensorCore : WeightsPath::Simt;
+}
+
+static size_t key_weights_partial_bytes(const KeyWeightsProblem &w, WeightsPath path, int sm_count) {
+    if (path == WeightsPath::Rows) return 0;
+    if (path == WeightsPath::TensorCore) return align256(key_weights_tc_floats(sm_count) * sizeof(float));
+    const int splits = key_weights_simt_splits(w, sm_count);
     return splits > 1 ? align256((size_t)splits * w.B * w.Hkv * w.Sk * sizeof(float)) : 0;
 }
 
@@ -808,7 +819,11 @@ int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int 
     if (st != OSF_OK || empty || Sq == 0) return st;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
-    *bytes = key_weights_partial_bytes(w, key_weights_simt_splits(w, dev->sm_count));
+    // the larger of the possible paths' needs (alignment decides the path at call time)
+    const size_t simt = key_weights_partial_bytes(w, WeightsPath::Simt, dev->sm_count);
+    const size_t tc = dtype == OSF_BF16 && (D == 64 || D == 128)
+                          ? key_weights_partial_bytes(w, WeightsPath::TensorCore, dev->sm_count) : 0;
+    *bytes = std::max(simt, tc);
     return OSF_OK;
 }
 
@@ -827,10 +842,13 @@ int osf_attn_key_weights(const void *Q, const void *K, const float *lse, float *
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     w.accumulate = accumulate != 0;
     w.status = dev->status;
-    w.splits = key_weights_simt_splits(w, dev->sm_count);
-    const size_t need = key_weights_partial_bytes(w, w.splits);
+    const WeightsPath path = key_weights_path(w);
+    const size_t need = key_weights_partial_bytes(w, path, dev->sm_count);
     if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
     w.part = static_cast<float *>(workspace);
+    if (path == WeightsPath::Rows) return launch_status(launch_key_weights_rows(w, dev->sm_count, s));
+    if (path == WeightsPath::TensorCore) return launch_status(launch_key_weights_tc(w, dev->sm_count, s));
+    w.splits = key_weights_simt_splits(w, dev->sm_count);
     cudaError_t e = launch_key_weights_simt(w, s);
     if (e == cudaSuccess && w.splits > 1) e = launch_key_weights_reduce(w, s);
     return launch_status(e);

@@ -25,6 +25,12 @@ __device__ __forceinline__ float row_offset(float lse) { return lse == -INFINITY
 // CUDA-core kernel: any type, head dimension and strides.
 int key_weights_simt_splits(const KeyWeightsProblem &p, int sm_count);
 cudaError_t launch_key_weights_simt(const KeyWeightsProblem &p, cudaStream_t s);
+// Tensor-core kernels (bf16, D 64 or 128): a few rows per kv head, and any number of them.
+bool key_weights_rows_supported(const KeyWeightsProblem &p);
+cudaError_t launch_key_weights_rows(const KeyWeightsProblem &p, int sm_count, cudaStream_t s);
+bool key_weights_tc_supported(const KeyWeightsProblem &p);
+size_t key_weights_tc_floats(int sm_count);   // partial sums it keeps in `part`
+cudaError_t launch_key_weights_tc(const KeyWeightsProblem &p, int sm_count, cudaStream_t s);
 // w (+)= the sum of the splits' parts, in split order.
 cudaError_t launch_key_weights_reduce(const KeyWeightsProblem &p, cudaStream_t s);
 
