@@ -6,8 +6,9 @@
 // Otherwise key_weights_tc_kernel.  The score tile is taken transposed, S^T = K Q^T: a TMEM lane is then a
 // key and a thread owns one, so its sum over the rows stays in one register and no cross-thread reduction
 // or exchange is needed until the end.  One tcgen05 product of 128 x 128 scores costs the tensor pipe
-// D / 128 * 512 cycles; its 16384 exponentials cost the special-function unit 1024, so a share of them is
-// computed by a polynomial on the FMA pipe instead (kPolyPairs).
+// D / 128 * 512 cycles, its 16384 exponentials the special-function units about as much.  (A share of the
+// exponentials as a polynomial on the FMA pipe was measured and is slower: 3 of 16 pairs 153 us against
+// 143 us for the B=2 Hq=32 S=4096 D=128 causal prompt, 8 of 16 199 us.)
 //
 // A CTA holds 256 keys (two A tiles, so that a query tile from L2 feeds two products) and walks the query
 // tiles that see them, for the G heads of the group.  Warp roles (384 threads): warp 0 issues the TMA
@@ -81,8 +82,7 @@ struct KwBars {
 
 // One piece: steps [u0, u1) of the item (bh, kb).
 struct Piece {
-    int bh, kb;
-    long long u0, u1, units;
+    int bh, kb, u0, u1, units;
 };
 // Piece that begins at flat position `pos` of a part that ends at `end`.
 __device__ __forceinline__ Piece piece_at(const KwPlan &w, long long pos, long long end) {
@@ -97,44 +97,82 @@ __device__ __forceinline__ Piece piece_at(const KwPlan &w, long long pos, long l
     while (lo > 0 && w.before(lo + 1) == w.before(lo)) --lo;
     c.kb = lo;
     const long long b0 = w.before(lo);
-    c.units = w.before(lo + 1) - b0;
-    c.u0 = in - b0;
-    c.u1 = c.u0 + (end - pos);
-    if (c.u1 > c.units) c.u1 = c.units;
+    c.units = (int)(w.before(lo + 1) - b0);
+    c.u0 = (int)(in - b0);
+    c.u1 = (int)min((long long)c.units, c.u0 + (end - pos));
     return c;
 }
+// Query tile and head (of the group) of the steps of a piece, heads innermost.
+struct Step {
+    int qt, h, G;
+    __device__ __forceinline__ Step(const KwPlan &w, const Piece &c) : G(w.G) {
+        qt = (int)w.first_tile(c.kb) + c.u0 / G;
+        h = c.u0 % G;
+    }
+    __device__ __forceinline__ void next() {
+        if (++h == G) {
+            h = 0;
+            ++qt;
+        }
+    }
+};
 
 __device__ __forceinline__ void kw_timeout(volatile int *abort, int *status) {
     *abort = 1;
     atomicExch(status, kStatusTimeout);
 }
 
-// 2^x of a pair on the FMA pipe: x = n + f with |f| <= 1/2, a degree-5 minimax polynomial (relative error
-// 7.5e-8 before rounding, fitted by the Remez exchange) for 2^f, n added to the exponent.  x below -126
-// gives 2^-126.
-__device__ __forceinline__ uint64_t ex2_poly(uint64_t x) {
-    float a, b;
-    f2_unpack(x, a, b);
-    const uint64_t xc = f2_pack(fmaxf(a, -126.f), fmaxf(b, -126.f));
-    const uint64_t magic = f2_pack(12582912.f, 12582912.f), nmagic = f2_pack(-12582912.f, -12582912.f);
-    const uint64_t t = f2_add(xc, magic);
-    const uint64_t f = f2_fma(f2_add(t, nmagic), f2_pack(-1.f, -1.f), xc);
-    uint64_t p = f2_fma(f2_pack(1.3276472454890609e-3f, 1.3276472454890609e-3f), f,
-                        f2_pack(9.675540961325169e-3f, 9.675540961325169e-3f));
-    p = f2_fma(p, f, f2_pack(5.550713092088699e-2f, 5.550713092088699e-2f));
-    p = f2_fma(p, f, f2_pack(2.4022120237350464e-1f, 2.4022120237350464e-1f));
-    p = f2_fma(p, f, f2_pack(6.931469440460205e-1f, 6.931469440460205e-1f));
-    p = f2_fma(p, f, f2_pack(1.0000001192092896f, 1.0000001192092896f));
-    float ta, tb, pa, pb;
-    f2_unpack(t, ta, tb);
-    f2_unpack(p, pa, pb);
-    return f2_pack(__uint_as_float(__float_as_uint(ta) * 8388608u + __float_as_uint(pa)),
-                   __uint_as_float(__float_as_uint(tb) * 8388608u + __float_as_uint(pb)));
-}
-__device__ __forceinline__ uint64_t ex2_mufu(uint64_t x) {
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
     float a, b;
     f2_unpack(x, a, b);
     return f2_pack(ex2_approx(a), ex2_approx(b));
+}
+
+__device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
+}
+
+// One key's terms of a score tile: 128 TMEM columns against the offsets of their rows.  The next 32 columns
+// load while these are summed; `sempty` is told once the last are in registers.  The 128 terms are added
+// among themselves, so the long sum gets one rounding per tile.
+template <bool MASK>
+__device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_t c2, int qmin, int qmax, uint32_t sempty,
+                                          int lane) {
+    uint64_t acc[4] = {0, 0, 0, 0};
+    uint32_t s[2][32];
+    tmem_ld32(taddr, s[0]);
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        tmem_ld_wait();
+        if (ch < 3) {
+            tmem_ld32(taddr + 32 * (ch + 1), s[(ch + 1) & 1]);
+        } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sempty);
+        }
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+            uint64_t o[2];
+            lds_pairs(toff + (32 * ch + k) * 4, o[0], o[1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = k + 2 * e;
+                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[ch & 1][i]), __uint_as_float(s[ch & 1][i + 1])), c2, o[e]);
+                uint64_t v = ex2_pair(x);
+                if (MASK) {
+                    float a, b;
+                    f2_unpack(v, a, b);
+                    v = f2_pack(32 * ch + i >= qmin && 32 * ch + i < qmax ? a : 0.f,
+                                32 * ch + i + 1 >= qmin && 32 * ch + i + 1 < qmax ? b : 0.f);
+                }
+                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], v);
+            }
+        }
+    }
+    float a, b;
+    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+    return a + b;
 }
 
 template <int D>
@@ -177,9 +215,9 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     const uint32_t tmem = tmem_sh;
     const long long pos0 = w.total * blockIdx.x / w.nc, pos1 = w.total * (blockIdx.x + 1) / w.nc;
     // the second key tile of a block is past the first query tile that sees the first
-    auto sees = [&](const Piece &c, long long qt, int kt) {
+    auto sees = [&](const Piece &c, int qt, int kt) {
         const long long key0 = (long long)c.kb * 2 * TB + kt * TB;
-        return key0 < p.Sk && (!w.causal || qt * TB + TB - 1 + p.causal_off >= key0);
+        return key0 < p.Sk && (!w.causal || (long long)qt * TB + TB - 1 + p.causal_off >= key0);
     };
 
     if (warp == 0) {
@@ -198,15 +236,14 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                 mbar_expect_tx(smem_u32(&bars.k_full), 2 * C::TILE);
                 tma_load_5d(sK, &mk, smem_u32(&bars.k_full), 0, c.kb * 2 * TB, 0, kvh, b);
                 tma_load_5d(sK + C::TILE, &mk, smem_u32(&bars.k_full), 0, c.kb * 2 * TB + TB, 0, kvh, b);
-                const long long q0 = w.first_tile(c.kb);
-                for (long long u = c.u0; u < c.u1; ++u, ++n) {
+                Step at(w, c);
+                for (int u = c.u0; u < c.u1; ++u, ++n, at.next()) {
                     const int st = n % C::RING;
                     ok = mbar_wait(smem_u32(&bars.empty[st]), ((n / C::RING) & 1) ^ 1, &abort_flag);
                     if (!ok) break;
-                    const int qt = (int)(q0 + u / w.G), hq = kvh * w.G + (int)(u % w.G);
                     mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
-                    tma_load_5d_hint(sRing + st * C::TILE, &mq, smem_u32(&bars.full[st]), 0, qt * TB, 0, hq, b,
-                                     l2_policy_evict_last());
+                    tma_load_5d_hint(sRing + st * C::TILE, &mq, smem_u32(&bars.full[st]), 0, at.qt * TB, 0, kvh * w.G + at.h,
+                                     b, l2_policy_evict_last());
                 }
                 pos += c.u1 - c.u0;
                 ++items;
@@ -225,13 +262,13 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             int n = 0, items = 0, done[2] = {0, 0};
             for (long long pos = pos0; pos < pos1 && ok;) {
                 const Piece c = piece_at(w, pos, pos1);
-                const long long q0 = w.first_tile(c.kb);
+                Step at(w, c);
                 ok = mbar_wait_spin(smem_u32(&bars.k_full), items & 1, &abort_flag);
-                for (long long u = c.u0; u < c.u1 && ok; ++u, ++n) {
+                for (int u = c.u0; u < c.u1 && ok; ++u, ++n, at.next()) {
                     const int st = n % C::RING;
                     ok = mbar_wait_spin(smem_u32(&bars.full[st]), (n / C::RING) & 1, &abort_flag);
                     for (int kt = 0; kt < 2 && ok; ++kt) {
-                        if (!sees(c, q0 + u / w.G, kt)) continue;
+                        if (!sees(c, at.qt, kt)) continue;
                         const int buf = done[kt] & 1;
                         ok = mbar_wait_spin(smem_u32(&bars.s_empty[kt][buf]), ((done[kt] >> 1) & 1) ^ 1, &abort_flag);
                         if (!ok) break;
@@ -263,18 +300,18 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         for (long long pos = pos0; pos < pos1 && ok;) {
             const Piece c = piece_at(w, pos, pos1);
             const int b = c.bh / p.Hkv, kvh = c.bh % p.Hkv;
-            const long long q0 = w.first_tile(c.kb);
-            for (long long u = c.u0; u < c.u1; ++u, ++n) {
+            Step at(w, c);
+            for (int u = c.u0; u < c.u1; ++u, ++n, at.next()) {
                 const int st = n % TSTAGES;
                 ok = mbar_wait(smem_u32(&bars.t_empty[st]), ((n / TSTAGES) & 1) ^ 1, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const int qt = (int)(q0 + u / w.G);
-                const float *lse = p.lse + ((long long)b * p.Hq + kvh * w.G + u % w.G) * p.Sq;
+                const float *lse = p.lse + ((long long)b * p.Hq + kvh * w.G + at.h) * p.Sq;
 #pragma unroll
                 for (int i = 0; i < TB / 32; ++i) {
-                    const int r = lane + 32 * i, q = qt * TB + r;
-                    tab[st * TB + r] = q < p.Sq ? row_offset(lse[q]) : -INFINITY;
+                    const int r = lane + 32 * i, q = at.qt * TB + r;
+                    const float o = q < p.Sq ? row_offset(lse[q]) : -INFINITY;
+                        tab[st * TB + r] = o;
                 }
                 mbar_arrive(smem_u32(&bars.t_full[st]));
             }
@@ -290,63 +327,32 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         int n = 0, done = 0;
         for (long long pos = pos0; pos < pos1 && ok;) {
             const Piece c = piece_at(w, pos, pos1);
-            const long long q0 = w.first_tile(c.kb);
+            Step at(w, c);
             const int key = c.kb * 2 * TB + kt * TB + q4 * 32 + lane;
             float total = 0.f;
-            for (long long u = c.u0; u < c.u1; ++u, ++n) {
+            for (int u = c.u0; u < c.u1; ++u, ++n, at.next()) {
                 const int st = n % TSTAGES;
                 ok = mbar_wait(smem_u32(&bars.t_full[st]), (n / TSTAGES) & 1, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const long long qt = q0 + u / w.G;
-                if (sees(c, qt, kt)) {
+                if (sees(c, at.qt, kt)) {
                     const int buf = done & 1;
                     ok = mbar_wait(smem_u32(&bars.s_full[kt][buf]), (done >> 1) & 1, &abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     tc_fence_after();
                     // columns below qmin are rows that do not see this key, those from qmax on rows past the last (a
-                    // NaN key would get through their offset of -inf); a warp without either skips the test
-                    const long long first = (long long)key - p.causal_off - qt * TB;
+                    // NaN key would get through their offset of -inf); a warp whose keys all rows see skips the
+                    // tests
+                    const long long first = (long long)key - p.causal_off - (long long)at.qt * TB;
                     const int qmin = w.causal ? (int)max(0LL, min((long long)TB, first)) : 0;
-                    const int qmax = (int)min((long long)TB, p.Sq - qt * TB);
+                    const int qmax = min(TB, p.Sq - at.qt * TB);
                     const bool some = __any_sync(0xffffffffu, qmin > 0) || qmax < TB;
-                    uint64_t acc[2] = {0, 0};
                     const uint32_t taddr = tmem + (uint32_t)(kt * 2 + buf) * TB + lane_off;
-                    const float4 *off4 = reinterpret_cast<const float4 *>(tab + st * TB);
-#pragma unroll
-                    for (int ch = 0; ch < 4; ++ch) {
-                        uint32_t s[32];
-                        tmem_ld32(taddr + 32 * ch, s);
-                        tmem_ld_wait();
-                        if (ch == 3) {   // the scores are in registers: the buffer may take the step after next
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(smem_u32(&bars.s_empty[kt][buf]));
-                        }
-#pragma unroll
-                        for (int k4 = 0; k4 < 8; ++k4) {
-                            const float4 o = off4[8 * ch + k4];
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                const int k = 4 * k4 + e;
-                                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c2,
-                                                          e ? f2_pack(o.z, o.w) : f2_pack(o.x, o.y));
-                                uint64_t v = ex2_mufu(x);
-                                if (some) {
-                                    float a, bb;
-                                    f2_unpack(v, a, bb);
-                                    v = f2_pack(32 * ch + k >= qmin && 32 * ch + k < qmax ? a : 0.f,
-                                                32 * ch + k + 1 >= qmin && 32 * ch + k + 1 < qmax ? bb : 0.f);
-                                }
-                                acc[(k >> 1) & 1] = f2_add(acc[(k >> 1) & 1], v);
-                            }
-                        }
-                    }
+                    const uint32_t toff = smem_u32(tab + st * TB), sempty = smem_u32(&bars.s_empty[kt][buf]);
+                    total += some ? sum_tile<true>(taddr, toff, c2, qmin, qmax, sempty, lane)
+                                  : sum_tile<false>(taddr, toff, c2, qmin, qmax, sempty, lane);
                     ++done;
-                    float a, bb;
-                    f2_unpack(f2_add(acc[0], acc[1]), a, bb);
-                    total += a + bb;   // 128 terms among themselves, then one addition to the long sum
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[st]));
