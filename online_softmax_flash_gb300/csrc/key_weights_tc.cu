@@ -12,7 +12,7 @@
 //
 // A CTA holds 256 keys (two A tiles, so that a query tile from L2 feeds two products) and walks the query
 // tiles that see them, for the G heads of the group.  Warp roles (384 threads): warp 0 issues the TMA
-// loads, warp 1 the MMAs, warp 2 fills a ring of row offsets (-lse * log2 e, -inf for rows past the end);
+// loads, warps 1 and 3 the MMAs of key tile 0 and 1, warp 2 fills a ring of row offsets (-lse * log2 e, -inf for rows past the end);
 // warps 4-7 sum key tile 0, warps 8-11 key tile 1, each a TMEM lane quarter.  Score buffers are double
 // (TMEM: 2 key tiles x 2 buffers x 128 columns), so the products of a step run under the sums of the last.
 //
@@ -22,6 +22,8 @@
 // workspace (at most two per CTA: the end of an item, slot 2c, and the start of one, slot 2c + 1), and
 // key_weights_join_kernel adds the pieces in order.
 // Every wait is bounded (2 s): on expiry the CTA records OSF_ERR_TIMEOUT, drains, frees TMEM.
+#include <climits>
+
 #include "key_weights.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.cuh"
@@ -32,8 +34,8 @@ namespace {
 using namespace ptx;
 
 constexpr int TB = 128;                  // keys per A tile, query rows per B tile
-constexpr int NTHREADS = 384;
-constexpr int NCW = 8;                   // summing warps
+constexpr int NCW = 16;                  // summing warps: 2 key tiles x 2 step parities x 4 lane quarters
+constexpr int NTHREADS = (4 + NCW) * 32;
 constexpr int TSTAGES = 4;               // row-offset tables
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_RING = 8;
@@ -77,7 +79,7 @@ struct KwBars {
     uint64_t full[MAX_RING], empty[MAX_RING];
     uint64_t t_full[TSTAGES], t_empty[TSTAGES];
     uint64_t s_full[2][2], s_empty[2][2];   // [key tile][buffer]
-    uint64_t drain;
+    uint64_t drain[2];
 };
 
 // One piece: steps [u0, u1) of the item (bh, kb).
@@ -117,6 +119,12 @@ struct Step {
     }
 };
 
+// Number of query tiles, from tile `first` on, that begin before row x.
+__device__ __forceinline__ int tiles_before(long long x, int first) {
+    const long long t = x > 0 ? (x + TB - 1) / TB : 0;   // tiles qt with qt * 128 < x
+    return (int)max(0LL, t - first);
+}
+
 __device__ __forceinline__ void kw_timeout(volatile int *abort, int *status) {
     *abort = 1;
     atomicExch(status, kStatusTimeout);
@@ -138,7 +146,7 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &
 template <bool MASK>
 __device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_t c2, int qmin, int qmax, uint32_t sempty,
                                           int lane) {
-    uint64_t acc[4] = {0, 0, 0, 0};
+    uint64_t acc[2] = {0, 0};
     uint32_t s[2][32];
     tmem_ld32(taddr, s[0]);
 #pragma unroll
@@ -158,20 +166,19 @@ __device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = k + 2 * e;
-                const uint64_t x = f2_fma(f2_pack(__uint_as_float(s[ch & 1][i]), __uint_as_float(s[ch & 1][i + 1])), c2, o[e]);
-                uint64_t v = ex2_pair(x);
+                uint64_t v = ex2_pair(f2_fma(f2_pack(__uint_as_float(s[ch & 1][i]), __uint_as_float(s[ch & 1][i + 1])), c2, o[e]));
                 if (MASK) {
                     float a, b;
                     f2_unpack(v, a, b);
                     v = f2_pack(32 * ch + i >= qmin && 32 * ch + i < qmax ? a : 0.f,
                                 32 * ch + i + 1 >= qmin && 32 * ch + i + 1 < qmax ? b : 0.f);
                 }
-                acc[(i >> 1) & 3] = f2_add(acc[(i >> 1) & 3], v);
+                acc[e] = f2_add(acc[e], v);
             }
         }
     }
     float a, b;
-    f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a, b);
+    f2_unpack(f2_add(acc[0], acc[1]), a, b);
     return a + b;
 }
 
@@ -184,6 +191,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     __shared__ KwBars bars;
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
+    __shared__ float other[2][TB];        // sums of the odd steps
+    __shared__ volatile int failed[2];    // a summing warp of the key tile gave up
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t sK = sbase, sRing = sbase + C::RING_OFF;
@@ -191,22 +200,23 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TMEM_COLS);
     if (tid == 32) {
         mbar_init(smem_u32(&bars.k_full), 1);
-        mbar_init(smem_u32(&bars.k_empty), 1);
+        mbar_init(smem_u32(&bars.k_empty), 2);   // one release from each issuer
         for (int s = 0; s < C::RING; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 1);
-            mbar_init(smem_u32(&bars.empty[s]), 1);
+            mbar_init(smem_u32(&bars.empty[s]), 2);
         }
         for (int s = 0; s < TSTAGES; ++s) {
             mbar_init(smem_u32(&bars.t_full[s]), 32);
-            mbar_init(smem_u32(&bars.t_empty[s]), NCW);
+            mbar_init(smem_u32(&bars.t_empty[s]), NCW / 2);
         }
         for (int k = 0; k < 2; ++k)
             for (int s = 0; s < 2; ++s) {
                 mbar_init(smem_u32(&bars.s_full[k][s]), 1);
-                mbar_init(smem_u32(&bars.s_empty[k][s]), NCW / 2);
+                mbar_init(smem_u32(&bars.s_empty[k][s]), NCW / 4);
             }
-        mbar_init(smem_u32(&bars.drain), 1);
-        abort_flag = 0;
+        mbar_init(smem_u32(&bars.drain[0]), 1);
+        mbar_init(smem_u32(&bars.drain[1]), 1);
+        abort_flag = failed[0] = failed[1] = 0;
         mbar_init_fence();
     }
     tc_fence_before();
@@ -214,10 +224,11 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     tc_fence_after();
     const uint32_t tmem = tmem_sh;
     const long long pos0 = w.total * blockIdx.x / w.nc, pos1 = w.total * (blockIdx.x + 1) / w.nc;
-    // the second key tile of a block is past the first query tile that sees the first
-    auto sees = [&](const Piece &c, int qt, int kt) {
+    // step of a piece's item from which on a query tile sees key tile kt (INT_MAX: it is past the last key)
+    auto first_step = [&](const Piece &c, int kt) {
         const long long key0 = (long long)c.kb * 2 * TB + kt * TB;
-        return key0 < p.Sk && (!w.causal || (long long)qt * TB + TB - 1 + p.causal_off >= key0);
+        if (key0 >= p.Sk) return INT_MAX;
+        return w.causal ? tiles_before(key0 - p.causal_off - (TB - 1), (int)w.first_tile(c.kb)) * w.G : 0;
     };
 
     if (warp == 0) {
@@ -255,25 +266,26 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                 }
             }
         }
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 3) {
         if (lane == 0) {
-            // ------------------------------------------------------------ MMA: S^T = K Q^T
+            // ------------------------------------------------------------ MMA: S^T = K Q^T, an issuer per key tile
+            const int kt = warp >> 1;
             bool ok = true;
-            int n = 0, items = 0, done[2] = {0, 0};
+            int n = 0, items = 0;
+            int phase = 3;   // bit b: parity of the next wait for buffer b to be free
+            const uint64_t ad = sdesc_sw128(sK + kt * C::TILE, 16, 1024);
             for (long long pos = pos0; pos < pos1 && ok;) {
                 const Piece c = piece_at(w, pos, pos1);
-                Step at(w, c);
+                const int u_see = first_step(c, kt);
                 ok = mbar_wait_spin(smem_u32(&bars.k_full), items & 1, &abort_flag);
-                for (int u = c.u0; u < c.u1 && ok; ++u, ++n, at.next()) {
-                    const int st = n % C::RING;
+                for (int u = c.u0; u < c.u1 && ok; ++u, ++n) {
+                    const int st = n % C::RING, buf = n & 1;
                     ok = mbar_wait_spin(smem_u32(&bars.full[st]), (n / C::RING) & 1, &abort_flag);
-                    for (int kt = 0; kt < 2 && ok; ++kt) {
-                        if (!sees(c, at.qt, kt)) continue;
-                        const int buf = done[kt] & 1;
-                        ok = mbar_wait_spin(smem_u32(&bars.s_empty[kt][buf]), ((done[kt] >> 1) & 1) ^ 1, &abort_flag);
+                    if (ok && u >= u_see) {
+                        ok = mbar_wait_spin(smem_u32(&bars.s_empty[kt][buf]), (phase >> buf) & 1, &abort_flag);
                         if (!ok) break;
+                        phase ^= 1 << buf;
                         tc_fence_after();
-                        const uint64_t ad = sdesc_sw128(sK + kt * C::TILE, 16, 1024);
                         const uint64_t bd = sdesc_sw128(sRing + st * C::TILE, 16, 1024);
 #pragma unroll
                         for (int k = 0; k < D / 16; ++k) {
@@ -281,7 +293,6 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                             mma_ss(tmem + (uint32_t)(kt * 2 + buf) * TB, ad + off, bd + off, C::IDESC, k > 0);
                         }
                         mma_commit(smem_u32(&bars.s_full[kt][buf]));
-                        ++done[kt];
                     }
                     if (ok) mma_commit(smem_u32(&bars.empty[st]));
                 }
@@ -290,8 +301,8 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                 ++items;
             }
             if (!ok) kw_timeout(&abort_flag, p.status);
-            mma_commit(smem_u32(&bars.drain));
-            mbar_wait(smem_u32(&bars.drain), 0, nullptr, 20000000ull);
+            mma_commit(smem_u32(&bars.drain[kt]));
+            mbar_wait(smem_u32(&bars.drain[kt]), 0, nullptr, 20000000ull);
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------ row offsets of each step
@@ -319,53 +330,69 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
         }
         if (!ok) kw_timeout(&abort_flag, p.status);
     } else if (warp >= 4) {
-        // ------------------------------------------------------------ sums, one key per thread
-        const int kt = (warp - 4) >> 2, q4 = warp & 3;
-        const uint32_t lane_off = (uint32_t)(q4 * 32) << 16;
+        // ------------------------------------------------------------ sums, a key per thread
+        // steps of parity `odd` only, whose scores are in buffer `odd`: two warps of a lane quarter take turns
+        const int kt = (warp - 4) >> 3, odd = ((warp - 4) >> 2) & 1, q4 = warp & 3;
+        const uint32_t taddr = tmem + (uint32_t)(kt * 2 + odd) * TB + ((uint32_t)(q4 * 32) << 16);
+        const uint32_t toff0 = smem_u32(tab), sfull = smem_u32(&bars.s_full[kt][odd]), sempty = smem_u32(&bars.s_empty[kt][odd]);
         const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
         bool ok = true;
-        int n = 0, done = 0;
+        int n0 = 0, phase = 0;   // steps before the piece; parity of the next wait for scores
         for (long long pos = pos0; pos < pos1 && ok;) {
             const Piece c = piece_at(w, pos, pos1);
-            Step at(w, c);
-            const int key = c.kb * 2 * TB + kt * TB + q4 * 32 + lane;
+            const int key0 = c.kb * 2 * TB + kt * TB, key = key0 + q4 * 32 + lane;
+            const int q_first = (int)w.first_tile(c.kb);
+            // steps of the item from which on: the key tile is seen; every row of a tile sees all keys of this
+            // warp; the tile is the last one, where rows may be missing
+            const int u_see = first_step(c, kt);
+            const int u_full = w.causal ? tiles_before((long long)key0 + q4 * 32 + 31 - p.causal_off, q_first) * w.G : 0;
+            const int u_last = p.Sq % TB ? (w.nqt - 1 - q_first) * w.G : INT_MAX;
             float total = 0.f;
-            for (int u = c.u0; u < c.u1; ++u, ++n, at.next()) {
+            int n = n0 + ((n0 ^ odd) & 1);
+            for (int u = c.u0 + (n - n0); u < c.u1; u += 2, n += 2) {
                 const int st = n % TSTAGES;
                 ok = mbar_wait(smem_u32(&bars.t_full[st]), (n / TSTAGES) & 1, &abort_flag);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (sees(c, at.qt, kt)) {
-                    const int buf = done & 1;
-                    ok = mbar_wait(smem_u32(&bars.s_full[kt][buf]), (done >> 1) & 1, &abort_flag);
+                if (u >= u_see) {
+                    ok = ok && mbar_wait(sfull, phase, &abort_flag);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
+                    phase ^= 1;
                     tc_fence_after();
-                    // columns below qmin are rows that do not see this key, those from qmax on rows past the last (a
-                    // NaN key would get through their offset of -inf); a warp whose keys all rows see skips the
-                    // tests
-                    const long long first = (long long)key - p.causal_off - (long long)at.qt * TB;
-                    const int qmin = w.causal ? (int)max(0LL, min((long long)TB, first)) : 0;
-                    const int qmax = min(TB, p.Sq - at.qt * TB);
-                    const bool some = __any_sync(0xffffffffu, qmin > 0) || qmax < TB;
-                    const uint32_t taddr = tmem + (uint32_t)(kt * 2 + buf) * TB + lane_off;
-                    const uint32_t toff = smem_u32(tab + st * TB), sempty = smem_u32(&bars.s_empty[kt][buf]);
-                    total += some ? sum_tile<true>(taddr, toff, c2, qmin, qmax, sempty, lane)
-                                  : sum_tile<false>(taddr, toff, c2, qmin, qmax, sempty, lane);
-                    ++done;
+                    if (u >= u_full && u < u_last) {
+                        total += sum_tile<false>(taddr, toff0 + st * (TB * 4), c2, 0, 0, sempty, lane);
+                    } else {
+                        // columns below qmin are rows that do not see this key, those from qmax on rows past the last (a
+                        // NaN key would get through their offset of -inf)
+                        const int q0 = (q_first + u / w.G) * TB;
+                        const int qmin = w.causal ? (int)max(0LL, min((long long)TB, (long long)key - p.causal_off - q0)) : 0;
+                        total += sum_tile<true>(taddr, toff0 + st * (TB * 4), c2, qmin, p.Sq - q0, sempty, lane);
+                    }
+                } else {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.t_empty[st]));
             }
+            n0 += c.u1 - c.u0;
+            // the two parities of a key meet; a warp that gave up still comes here, so that none waits at the
+            // barriers alone, and all then stop together
+            if (!ok) abort_flag = failed[kt] = 1;
+            if (odd) other[kt][q4 * 32 + lane] = total;
+            named_barrier(1 + kt, NCW / 2 * 32);
+            const bool stop = failed[kt] != 0;
+            if (!odd) total += other[kt][q4 * 32 + lane];
+            named_barrier(1 + kt, NCW / 2 * 32);
+            if (stop) ok = false;
             if (!ok) break;
-            if (c.u1 - c.u0 == c.units) {
-                if (key < p.Sk) {
+            if (!odd) {
+                if (c.u1 - c.u0 != c.units) {
+                    const long long slot = 2LL * blockIdx.x + (c.u0 == 0 ? 1 : 0);
+                    p.part[slot * 2 * TB + kt * TB + q4 * 32 + lane] = total;
+                } else if (key < p.Sk) {
                     float *out = p.w + (long long)c.bh * p.Sk + key;
                     *out = p.accumulate ? *out + total : total;
                 }
-            } else {
-                const long long slot = 2LL * blockIdx.x + (c.u0 == 0 ? 1 : 0);
-                p.part[slot * 2 * TB + kt * TB + q4 * 32 + lane] = total;
             }
             pos += c.u1 - c.u0;
         }
