@@ -7,6 +7,7 @@ tensor is not on a CUDA device, the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -364,37 +365,70 @@ def osf_attn_key_weights_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, Sk, D) -> i
     return n.value
 
 
-def _view_strides(*named):
-    """The b, h, s element strides of [B, H, S, D] views, or None when all are contiguous."""
-    for name, t in named:
+def _view_strides(an: str, a, bn: str, b):
+    """The b, h, s element strides of two [B, H, S, D] views, or None when both are contiguous."""
+    for name, t in ((an, a), (bn, b)):
         if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
             raise ValueError(f"{name} must be a 4-D [B, H, S, D] view with a contiguous last dimension")
-    if all(t.is_contiguous() for _, t in named):
+    if a.is_contiguous() and b.is_contiguous():
         return None
-    st = (ctypes.c_longlong * (3 * len(named)))(*(int(t.stride(i)) for _, t in named for i in range(3)))
+    st = (ctypes.c_longlong * 6)(*a.stride()[:3], *b.stride()[:3])
     return ctypes.cast(st, ctypes.c_void_p)
 
 
-def _need(t, name: str, shape, dtype) -> None:
-    """A contiguous CUDA tensor of this shape and dtype, or None."""
+def _need(t, name: str, shape, dtype, dev: int) -> int | None:
+    """The address of a contiguous tensor of this shape and dtype on device ``dev``; None for None."""
     if t is None:
-        return
-    if not t.is_cuda or not t.is_contiguous() or tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+        return None
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on CUDA device {dev}")
+    return t.data_ptr()
 
 
-def _same_device(first, *rest) -> None:
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError("all tensors of a call must be on one device")
+def _on_device(t) -> int:
+    """The CUDA device index of a tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("libosf works on CUDA tensors only (no CPU path)")
+    return dev
+
+
+def _bytes_of(ws, dev: int) -> int:
+    if ws is None:
+        return 0
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of the call")
+    return ws.numel() * ws.element_size()
+
+
+def _call(name: str, dev: int, *args) -> None:
+    """Run an entry point whose last argument is the stream, with ``dev`` the current device."""
+    fn = getattr(lib(), name)
+    if dev == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status != OSF_OK:
+        raise OsfError(status, name)
+
+
+def _query(dev: int, fn, *args) -> int:
+    """A workspace query, with ``dev`` the current device."""
+    if dev == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 def _kv4_dims(cache, D: int):
-    """(B, Hkv, S) of a contiguous uint8 [B, Hkv, S, osf_kv4_record_bytes(D)] cache."""
-    if not cache.is_cuda or cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() or \
+    """(B, Hkv, S, device) of a contiguous uint8 [B, Hkv, S, osf_kv4_record_bytes(D)] cache."""
+    dev = cache.get_device()
+    if dev < 0 or cache.dim() != 4 or cache.dtype != torch.uint8 or not cache.is_contiguous() or \
             cache.shape[3] != osf_kv4_record_bytes(D):
         raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, Hkv, S, osf_kv4_record_bytes(D)]")
-    return cache.shape[0], cache.shape[1], cache.shape[2]
+    B, Hkv, S, _ = cache.shape
+    return B, Hkv, S, dev
 
 
 def osf_attn_key_weights(q, k, lse, weights=None, mask="none", scale: float | None = None, accumulate: bool = False,
@@ -404,32 +438,28 @@ def osf_attn_key_weights(q, k, lse, weights=None, mask="none", scale: float | No
     ``k``: [B, H, S, D] views as in osf_attn_fwd_gqa_ex, ``mask`` and ``scale`` as given to it;
     ``accumulate`` adds to ``weights`` instead of overwriting them.  Returns ``weights`` (allocated if
     None)."""
-    _need_cuda(q, k, contiguous=False)
-    _same_device(q, k, lse, weights, workspace)
-    st = _view_strides(("q", q), ("k", k))
+    dev = _on_device(q)
+    st = _view_strides("q", q, "k", k)
     B, Hq, Sq, D = q.shape
-    Hkv, Sk = k.shape[1], k.shape[2]
-    if k.dtype != q.dtype or k.shape[0] != B or k.shape[3] != D:
-        raise ValueError("q and k must agree in dtype, batch and head dimension")
+    Bk, Hkv, Sk, Dk = k.shape
+    if k.dtype != q.dtype or Bk != B or Dk != D or k.get_device() != dev:
+        raise ValueError("q and k must agree in dtype, batch, head dimension and device")
     if weights is None:
         if accumulate:
             raise ValueError("accumulate needs the weights to add to")
         weights = torch.empty((B, Hkv, Sk), dtype=torch.float32, device=q.device)
-    _need(lse, "lse", (B, Hq, Sq), torch.float32)
-    _need(weights, "weights", (B, Hkv, Sk), torch.float32)
     dt = _dtype_code(q)
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            workspace = _workspace(osf_attn_key_weights_workspace_bytes(dt, B, Hq, Hkv, Sq, Sk, D), q.device, None)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        m = _MASKS[mask] if isinstance(mask, str) else int(mask)
-        _check(lib().osf_attn_key_weights(_ptr(q), _ptr(k), _ptr(lse), _ptr(weights), dt, B, Hq, Hkv, Sq, Sk, D, st, m,
-                                          0.0 if scale is None else float(scale), int(bool(accumulate)),
-                                          _ptr(workspace), ws_bytes, _stream(q.device)),
-               "osf_attn_key_weights")
+    if workspace is None:
+        n = _query(dev, osf_attn_key_weights_workspace_bytes, dt, B, Hq, Hkv, Sq, Sk, D)
+        workspace = _workspace(n, q.device, None)
+    _call("osf_attn_key_weights", dev, q.data_ptr(), k.data_ptr(), _need(lse, "lse", (B, Hq, Sq), torch.float32, dev),
+          _need(weights, "weights", (B, Hkv, Sk), torch.float32, dev), dt, B, Hq, Hkv, Sq, Sk, D, st,
+          _MASKS[mask] if isinstance(mask, str) else int(mask), 0.0 if scale is None else float(scale),
+          int(bool(accumulate)), _ptr(workspace), _bytes_of(workspace, dev))
     return weights
 
 
+@functools.lru_cache(maxsize=None)
 def osf_kv4_record_bytes(D: int) -> int:
     """Bytes of one 4-bit record (K and V of one token of one kv head): 1.25 D."""
     n = _sz(0)
@@ -442,21 +472,16 @@ def osf_kv4_append(k, v, cache, lens=None, counts=None):
     (uint8 [B, Hkv, S, osf_kv4_record_bytes(D)]) behind the ``lens`` (int32 [B]; None: 0) tokens that
     each sequence has; ``counts`` (int32 [B]): how many of the n are new, the rest being padding.
     Returns ``cache``; the caller advances its lengths."""
-    _need_cuda(k, v, contiguous=False)
-    _same_device(k, v, cache, lens, counts)
-    st = _view_strides(("k", k), ("v", v))
+    dev = _on_device(k)
+    st = _view_strides("k", k, "v", v)
     B, Hkv, n, D = k.shape
-    if v.shape != k.shape or v.dtype != k.dtype:
-        raise ValueError("k and v must agree in shape and dtype")
-    cb, ch, S = _kv4_dims(cache, D)
-    if (cb, ch) != (B, Hkv):
-        raise ValueError("cache must have the batch and kv heads of k")
-    _need(lens, "lens", (B,), torch.int32)
-    _need(counts, "counts", (B,), torch.int32)
-    with torch.cuda.device(k.device):
-        _check(lib().osf_kv4_append(_ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n, D, st, _ptr(cache), S, _ptr(lens),
-                                    _ptr(counts), _stream(k.device)),
-               "osf_kv4_append")
+    if v.shape != k.shape or v.dtype != k.dtype or v.get_device() != dev:
+        raise ValueError("k and v must agree in shape, dtype and device")
+    cb, ch, S, cdev = _kv4_dims(cache, D)
+    if cb != B or ch != Hkv or cdev != dev:
+        raise ValueError("cache must have the batch, kv heads and device of k")
+    _call("osf_kv4_append", dev, k.data_ptr(), v.data_ptr(), _dtype_code(k), B, Hkv, n, D, st, cache.data_ptr(), S,
+          _need(lens, "lens", (B,), torch.int32, dev), _need(counts, "counts", (B,), torch.int32, dev))
     return cache
 
 
@@ -464,18 +489,13 @@ def osf_kv4_read(cache, D: int, n: int, starts=None, lens=None, k=None, v=None, 
     """The values of records starts[b] .. starts[b] + n - 1 (``starts`` None: from 0) of a 4-bit cache,
     as contiguous (k, v) [B, Hkv, n, D] of ``dtype`` (or given tensors); zeros at and behind
     ``lens``."""
-    B, Hkv, S = _kv4_dims(cache, D)
+    B, Hkv, S, dev = _kv4_dims(cache, D)
     k = torch.empty((B, Hkv, n, D), dtype=dtype, device=cache.device) if k is None else k
     v = torch.empty((B, Hkv, n, D), dtype=k.dtype, device=cache.device) if v is None else v
-    _same_device(cache, k, v, starts, lens)
-    _need(k, "k", (B, Hkv, n, D), k.dtype)
-    _need(v, "v", (B, Hkv, n, D), k.dtype)
-    _need(starts, "starts", (B,), torch.int32)
-    _need(lens, "lens", (B,), torch.int32)
-    with torch.cuda.device(cache.device):
-        _check(lib().osf_kv4_read(_ptr(cache), _ptr(k), _ptr(v), _dtype_code(k), B, Hkv, n, D, S, _ptr(starts),
-                                  _ptr(lens), _stream(cache.device)),
-               "osf_kv4_read")
+    shape = (B, Hkv, n, D)
+    _call("osf_kv4_read", dev, cache.data_ptr(), _need(k, "k", shape, k.dtype, dev), _need(v, "v", shape, k.dtype, dev),
+          _dtype_code(k), B, Hkv, n, D, S, _need(starts, "starts", (B,), torch.int32, dev),
+          _need(lens, "lens", (B,), torch.int32, dev))
     return k, v
 
 
@@ -492,31 +512,24 @@ def osf_attn_kv4(q, cache, lens=None, out=None, mask="none", scale: float | None
     whose records are valid; ``mask`` "none" or "bottom_right" (the Sq rows are the last tokens of each
     sequence).  ``weights`` (float32 [B, Hkv, S]) receives, or with ``accumulate`` gains, the attention
     weight of every record.  Returns ``out`` (a contiguous tensor if None)."""
-    _need_cuda(q, out, contiguous=False)
-    _same_device(q, cache, lens, out, lse, weights, workspace)
     B, Hq, Sq, D = q.shape
-    cb, Hkv, S = _kv4_dims(cache, D)
+    cb, Hkv, S, dev = _kv4_dims(cache, D)
     if out is None:
         out = torch.empty((B, Hq, Sq, D), dtype=q.dtype, device=q.device)
-    if cb != B or out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("q, out and cache must agree in batch, shape and dtype")
+    if cb != B or out.shape != q.shape or out.dtype != q.dtype or q.get_device() != dev or out.get_device() != dev:
+        raise ValueError("q, out and cache must agree in batch, shape, dtype and device")
     if accumulate and weights is None:
         raise ValueError("accumulate needs the weights to add to")
-    st = _view_strides(("q", q), ("out", out))
-    _need(lens, "lens", (B,), torch.int32)
-    _need(lse, "lse", (B, Hq, Sq), torch.float32)
-    _need(weights, "weights", (B, Hkv, S), torch.float32)
+    st = _view_strides("q", q, "out", out)
     dt = _dtype_code(q)
-    with torch.cuda.device(q.device):
-        if workspace is None:
-            n = osf_attn_kv4_workspace_bytes(dt, B, Hq, Hkv, Sq, S, D, weights is not None)
-            workspace = _workspace(n, q.device, None)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        m = _MASKS[mask] if isinstance(mask, str) else int(mask)
-        _check(lib().osf_attn_kv4(_ptr(q), _ptr(cache), _ptr(out), dt, B, Hq, Hkv, Sq, S, D, st, _ptr(lens), m,
-                                  0.0 if scale is None else float(scale), _ptr(lse), _ptr(weights),
-                                  int(bool(accumulate)), _ptr(workspace), ws_bytes, _stream(q.device)),
-               "osf_attn_kv4")
+    if workspace is None:
+        n = _query(dev, osf_attn_kv4_workspace_bytes, dt, B, Hq, Hkv, Sq, S, D, weights is not None)
+        workspace = _workspace(n, q.device, None)
+    _call("osf_attn_kv4", dev, q.data_ptr(), cache.data_ptr(), out.data_ptr(), dt, B, Hq, Hkv, Sq, S, D, st,
+          _need(lens, "lens", (B,), torch.int32, dev), _MASKS[mask] if isinstance(mask, str) else int(mask),
+          0.0 if scale is None else float(scale), _need(lse, "lse", (B, Hq, Sq), torch.float32, dev),
+          _need(weights, "weights", (B, Hkv, S), torch.float32, dev), int(bool(accumulate)), _ptr(workspace),
+          _bytes_of(workspace, dev))
     return out
 
 
@@ -528,41 +541,37 @@ def osf_kv_evict(k, v, weights, budget: int, lens=None, sinks: int = 0, recent: 
     ``lens`` (int32 [B]; None: S) valid keys.  Outputs default to new [B, Hkv, budget, ...] tensors
     (rows behind a shorter sequence are then zero); pass ``k_out=k`` and so on to move in place.
     Returns (k_out, v_out, weights_out, lens_out, idx)."""
-    _need_cuda(k, v, weights)
-    _same_device(k, v, weights, lens, k_out, v_out, weights_out, lens_out, idx)
+    dev = _on_device(weights)
     B, Hkv, S = weights.shape
     budget = int(budget)
-    for name, t in (("k", k), ("v", v)):
-        if t is not None and tuple(t.shape[:3]) != (B, Hkv, S):
-            raise ValueError(f"{name} must be [B, Hkv, S, ...] with the sizes of weights")
-    _need(weights, "weights", (B, Hkv, S), torch.float32)
-    _need(lens, "lens", (B,), torch.int32)
-    given = next((t for t in (k_out, v_out, weights_out) if t is not None), None)
+    row_k, kd = k.shape[3:], k.dtype
+    given = k_out if k_out is not None else v_out if v_out is not None else weights_out
     S_out = budget if given is None else given.shape[2]
-    dev = k.device
-    k_out = torch.zeros((B, Hkv, S_out, *k.shape[3:]), dtype=k.dtype, device=dev) if k_out is None else k_out
-    if v is not None and v_out is None:
-        v_out = torch.zeros((B, Hkv, S_out, *v.shape[3:]), dtype=v.dtype, device=dev)
-    weights_out = torch.empty((B, Hkv, S_out), device=dev) if weights_out is None else weights_out
-    lens_out = torch.empty(B, dtype=torch.int32, device=dev) if lens_out is None else lens_out
-    idx = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=dev) if idx is None else idx
-    _need(k_out, "k_out", (B, Hkv, S_out, *k.shape[3:]), k.dtype)
+    if k_out is None:
+        k_out = torch.zeros((B, Hkv, S_out, *row_k), dtype=kd, device=weights.device)
+    if weights_out is None:
+        weights_out = torch.empty((B, Hkv, S_out), dtype=torch.float32, device=weights.device)
+    if lens_out is None:
+        lens_out = torch.empty(B, dtype=torch.int32, device=weights.device)
+    if idx is None:
+        idx = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=weights.device)
+    vp = vo = None
+    vb = 0
     if v is not None:
-        _need(v_out, "v_out", (B, Hkv, S_out, *v.shape[3:]), v.dtype)
+        row_v = v.shape[3:]
+        if v_out is None:
+            v_out = torch.zeros((B, Hkv, S_out, *row_v), dtype=v.dtype, device=weights.device)
+        vp = _need(v, "v", (B, Hkv, S, *row_v), v.dtype, dev)
+        vo = _need(v_out, "v_out", (B, Hkv, S_out, *row_v), v.dtype, dev)
+        vb = v.element_size() * row_v.numel()
     elif v_out is not None:
         raise ValueError("v_out without v")
-    _need(weights_out, "weights_out", (B, Hkv, S_out), torch.float32)
-    _need(lens_out, "lens_out", (B,), torch.int32)
-    _need(idx, "idx", (B, Hkv, budget), torch.int32)
-
-    def row(t):
-        return 0 if t is None else t.element_size() * int(t.shape[3:].numel())
-
-    with torch.cuda.device(dev):
-        _check(lib().osf_kv_evict(_ptr(k), _ptr(k_out), row(k), _ptr(v), _ptr(v_out), row(v), _ptr(weights),
-                                  _ptr(weights_out), _ptr(lens), _ptr(lens_out), _ptr(idx), B, Hkv, S, S_out, budget,
-                                  int(sinks), int(recent), _stream(dev)),
-               "osf_kv_evict")
+    _call("osf_kv_evict", dev, _need(k, "k", (B, Hkv, S, *row_k), kd, dev),
+          _need(k_out, "k_out", (B, Hkv, S_out, *row_k), kd, dev), k.element_size() * row_k.numel(), vp, vo, vb,
+          _need(weights, "weights", (B, Hkv, S), torch.float32, dev),
+          _need(weights_out, "weights_out", (B, Hkv, S_out), torch.float32, dev),
+          _need(lens, "lens", (B,), torch.int32, dev), _need(lens_out, "lens_out", (B,), torch.int32, dev),
+          _need(idx, "idx", (B, Hkv, budget), torch.int32, dev), B, Hkv, S, S_out, budget, int(sinks), int(recent))
     return k_out, v_out, weights_out, lens_out, idx
 
 
