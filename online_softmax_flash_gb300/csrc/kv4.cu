@@ -88,6 +88,23 @@ __device__ __forceinline__ float bf16_floor(float x) {
     return __uint_as_float((u & 0xffff0000u) + ((u >> 31) ? 0x10000u : 0u));
 }
 
+// Smallest and largest of three, a NaN among them giving a NaN.
+__device__ __forceinline__ float min3_nan(float a, float b, float c) {
+    float d;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // (scale, minimum) of a group with the smallest value lo and the largest hi.
 __device__ __forceinline__ void group_scale(float lo, float hi, float &s, float &m) {
     m = __fadd_rn(bf16_floor(lo), 0.f);   // a minimum of -0 is stored as 0
@@ -97,42 +114,63 @@ __device__ __forceinline__ void group_scale(float lo, float hi, float &s, float 
         s = m = __uint_as_float(0x7fc00000u);
         return;
     }
-    // the float32 quotient is at most the wanted bfloat16, and above the one before it
-    s = __uint_as_float(__float_as_uint(__fdiv_rn(d, 15.f)) & 0xffff0000u);
-    if (cmp_exact(d, e, 15.f * s) > 0) s = __uint_as_float(__float_as_uint(s) + 0x10000u);
+    // a bfloat16 within one of the wanted one, which is the first with 15 s >= d + e
+    uint32_t u = __float_as_uint(d * 0.06666667f) & 0xffff0000u;
+    if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) {
+        u += 0x10000u;
+        if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
+    } else if (u && cmp_exact(d, e, 15.f * __uint_as_float(u - 0x10000u)) <= 0) {
+        u -= 0x10000u;
+    }
+    s = __uint_as_float(u);
 }
 
-// Codes of eight channels as one word.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s, float m) {
-    if (!(s > 0.f)) return 0u;   // a constant group, or NaN
+// One code, settled exactly near a tie.
+__device__ __noinline__ uint32_t quantise_exact(float x, float s, float m) {
     // a scale whose reciprocal could overflow is lifted first
     const float up = s < 0x1p-100f ? 0x1p60f : 1.f;
-    const float inv = __frcp_rn(s * up);
-    uint32_t w = 0;
+    float d = __fsub_rn(x, m), e;
+    const float t = d * up * __frcp_rn(s * up);   // within 2^-21 of (x - m) / s
+    float c = rintf(t);
+    if (fabsf(t - c) > 0.4999f) {
+        diff_exact(x, m, d, e);
+        c = floorf(t);   // the tie is at c + 1/2
+        const int side = cmp_exact(d, e, (c + 0.5f) * s);
+        if (side > 0 || (side == 0 && ((int)c & 1))) c += 1.f;
+    }
+    return (uint32_t)(int)c;
+}
+
+// Codes of eight channels as one word.  t + 1.5 * 2^23 has the rounded t in its low bits, so a code needs no
+// conversion: the eight sums of those bits times 16^i make the word and a constant.
+__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s, float m) {
+    if (!(s > 0.f)) return 0u;   // a constant group, or NaN
+    const float inv = rcp_approx(s), magic = 12582912.f;   // 0x4b400000
+    uint32_t w = 0u - 0x4b400000u * 0x11111111u;
+    float far = s < 0x1p-100f ? 1.f : 0.f;   // distance from the nearest integer; tiny scales go the exact way too
+    uint32_t place = 1u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float d = __fsub_rn(x[i], m);
-        const float t = d * up * inv;   // within 2^-21 of (x - m) / s
-        float c = rintf(t);
-        if (fabsf(t - c) > 0.4999f) {   // near a tie: settle it exactly
-            float e;
-            diff_exact(x[i], m, d, e);
-            c = floorf(t);   // the tie is at c + 1/2
-            const int side = cmp_exact(d, e, (c + 0.5f) * s);
-            if (side > 0 || (side == 0 && ((int)c & 1))) c += 1.f;
-        }
-        w |= (uint32_t)(int)c << (4 * i);
+    for (int i = 0; i < 8; ++i, place <<= 4) {
+        const float t = __fsub_rn(x[i], m) * inv;   // within 2^-20 of (x - m) / s
+        const float r = __fadd_rn(t, magic);
+        far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(r, magic))));
+        w += __float_as_uint(r) * place;
+    }
+    if (far > 0.4999f) {
+        w = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w |= quantise_exact(x[i], s, m) << (4 * i);
     }
     return w;
 }
 
-// One group of four lanes per (token, half, group of 32 channels): flat index over
-// [token of (b, h)][K groups, V groups].
-template <typename T>
+// Four lanes share a group of 32 channels; group i of a head is K group 0, 1, ..., V group 0, 1, ... of token
+// i / (2 groups).  DC: the head dimension where the compiler is to know it (its divisions become shifts), or 0.
+template <typename T, int DC>
 __global__ void __launch_bounds__(kThreads)
 kv4_append_kernel(const Kv4StoreProblem p, int k_vec, int v_vec) {
-    const int gph = p.D / kKv4Group, per_token = 2 * gph;
-    const long long per_head = (long long)p.n * per_token;
+    const int D = DC ? DC : p.D;
+    const unsigned gph = D / kKv4Group, per_token = 2 * gph;
     const int bh = blockIdx.y, b = bh / p.Hkv, h = bh % p.Hkv;
     const int n_new = p.counts ? p.counts[b] : p.n;
     const int base = p.lens ? p.lens[b] : 0;
@@ -140,73 +178,82 @@ kv4_append_kernel(const Kv4StoreProblem p, int k_vec, int v_vec) {
     const int fit = base < 0 ? 0 : (int)min((long long)min(n_new, p.n), (long long)p.S - base);
     if (blockIdx.x == 0 && threadIdx.x == 0 && (base < 0 || n_new < 0 || n_new > p.n || fit < n_new))
         atomicExch(p.status, (int)OSF_ERR_INVALID);
-    const int R = kv4_record_bytes(p.D);
+    if (fit <= 0) return;
+    const int R = kv4_record_bytes(D);
     const int t = threadIdx.x & 3;
-    unsigned char *head = p.cache + (long long)bh * p.S * R;
-    const long long live = (long long)max(fit, 0) * per_token;
-    for (long long i0 = (long long)blockIdx.x * (kThreads / 4); i0 < per_head; i0 += (long long)gridDim.x * (kThreads / 4)) {
-        if (i0 >= live) break;   // the whole block is done
-        const long long i = i0 + (threadIdx.x >> 2);
+    unsigned char *head = p.cache + ((long long)bh * p.S + base) * R;
+    const T *kh = static_cast<const T *>(p.k) + b * p.k_sb + h * p.k_sh + 8 * t;
+    const T *vh = static_cast<const T *>(p.v) + b * p.v_sb + h * p.v_sh + 8 * t;
+    const unsigned live = (unsigned)fit * per_token;   // n * D < 2^31
+    const unsigned step = gridDim.x * (kThreads / 4);
+    for (unsigned i0 = blockIdx.x * (kThreads / 4); i0 < live; i0 += step) {
+        const unsigned i = i0 + (threadIdx.x >> 2);
         const bool on = i < live;
-        const long long at = on ? i : live - 1;   // idle lanes repeat the last group: shuffles need them
-        const int tok = (int)(at / per_token), r = (int)(at - (long long)tok * per_token);
-        const int half = r >= gph, n = r - half * gph;
-        const T *src = half ? static_cast<const T *>(p.v) + b * p.v_sb + h * p.v_sh + tok * p.v_ss
-                            : static_cast<const T *>(p.k) + b * p.k_sb + h * p.k_sh + tok * p.k_ss;
+        const unsigned at = on ? i : live - 1;   // idle lanes repeat the last group: shuffles need them
+        const unsigned tok = at / per_token, r = at - tok * per_token;
+        const bool half = r >= gph;
+        const unsigned n = half ? r - gph : r;
         float x[8];
-        load8(src + n * kKv4Group + 8 * t, half ? v_vec : k_vec, x);
-        float lo = x[0], hi = x[0];
-        bool bad = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            lo = fminf(lo, x[e]);
-            hi = fmaxf(hi, x[e]);
-            bad |= x[e] != x[e];
-        }
+        load8((half ? vh + tok * p.v_ss : kh + tok * p.k_ss) + n * kKv4Group, half ? v_vec : k_vec, x);
+        float lo = min3_nan(min3_nan(x[0], x[1], x[2]), min3_nan(x[3], x[4], x[5]), min3_nan(x[6], x[7], x[7]));
+        float hi = max3_nan(max3_nan(x[0], x[1], x[2]), max3_nan(x[3], x[4], x[5]), max3_nan(x[6], x[7], x[7]));
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
-            lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-            hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-            bad |= __shfl_xor_sync(0xffffffffu, (int)bad, o) != 0;
+            lo = min3_nan(lo, lo, __shfl_xor_sync(0xffffffffu, lo, o));
+            hi = max3_nan(hi, hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        if (bad) lo = __uint_as_float(0x7fc00000u);
         float s, m;
         group_scale(lo, hi, s, m);
         const uint32_t w = quantise8(x, s, m);
         if (!on) continue;
-        unsigned char *rec = head + (long long)(base + tok) * R;
-        reinterpret_cast<uint32_t *>(rec + half * (p.D / 2))[kv4_word_at(p.D, n * 4 + t)] = w;
+        unsigned char *rec = head + (long long)tok * R;
+        reinterpret_cast<uint32_t *>(rec + (half ? D / 2 : 0))[kv4_word_at(D, n * 4 + t)] = w;
         if (t == 0)
-            reinterpret_cast<uint32_t *>(rec + p.D + half * (p.D / 8))[n] =
+            reinterpret_cast<uint32_t *>(rec + D + (half ? D / 8 : 0))[n] =
                 (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xffff0000u);
     }
 }
 
-template <typename T>
+// A thread takes one word (8 channels) of four tokens: their loads are in flight together.
+constexpr int kReadTokens = 4;
+template <typename T, int DC>
 __global__ void __launch_bounds__(kThreads)
 kv4_read_kernel(const Kv4StoreProblem p, int k_vec, int v_vec) {
-    const int wph = p.D / 8, per_token = 2 * wph;
+    const int D = DC ? DC : p.D;
+    const unsigned wph = D / 8, per_token = 2 * wph;
     const int bh = blockIdx.y, b = bh / p.Hkv;
     const int len = kv4_length(p.lens, b, p.S, p.status);
     const int start = p.starts ? p.starts[b] : 0;
-    const int R = kv4_record_bytes(p.D);
+    const int R = kv4_record_bytes(D);
     const unsigned char *head = p.cache + (long long)bh * p.S * R;
-    T *ko = static_cast<T *>(p.ko) + (long long)bh * p.n * p.D, *vo = static_cast<T *>(p.vo) + (long long)bh * p.n * p.D;
-    const long long total = (long long)p.n * per_token;
-    for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total; i += (long long)gridDim.x * kThreads) {
-        const int tok = (int)(i / per_token), r = (int)(i - (long long)tok * per_token);
-        const int half = r >= wph, w = r - half * wph;
-        const long long pos = (long long)start + tok;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (pos >= 0 && pos < len) {
-            const unsigned char *rec = head + pos * R;
-            const uint32_t c = reinterpret_cast<const uint32_t *>(rec + half * (p.D / 2))[kv4_word_at(p.D, w)];
-            const uint32_t sm = reinterpret_cast<const uint32_t *>(rec + p.D + half * (p.D / 8))[w >> 2];
-            const float s = bf16_bits_to_f32(sm & 0xffffu), m = __uint_as_float(sm & 0xffff0000u);
+    T *ko = static_cast<T *>(p.ko) + (long long)bh * p.n * D, *vo = static_cast<T *>(p.vo) + (long long)bh * p.n * D;
+    const unsigned quads = (unsigned)(p.n + kReadTokens - 1) / kReadTokens, total = quads * per_token;   // n * D < 2^31
+    for (unsigned i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
+        const unsigned quad = i / per_token, r = i - quad * per_token;
+        const bool half = r >= wph;
+        const unsigned w = half ? r - wph : r;
+        const unsigned code_at = (half ? D / 2 : 0) + 4 * kv4_word_at(D, w), pair_at = D + (half ? D / 8 : 0) + (w >> 2) * 4;
+        uint32_t c[kReadTokens], sm[kReadTokens];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((c >> (4 * e)) & 15u), s, m);
+        for (int e = 0; e < kReadTokens; ++e) {
+            const long long pos = (long long)start + quad * kReadTokens + e;
+            c[e] = sm[e] = 0;   // scale and minimum 0: the value 0
+            if (pos >= 0 && pos < len) {
+                const unsigned char *rec = head + pos * R;
+                c[e] = *reinterpret_cast<const uint32_t *>(rec + code_at);
+                sm[e] = *reinterpret_cast<const uint32_t *>(rec + pair_at);
+            }
         }
-        store8((half ? vo : ko) + (long long)tok * p.D + 8 * w, half ? v_vec : k_vec, x);
+#pragma unroll
+        for (int e = 0; e < kReadTokens; ++e) {
+            const unsigned tok = quad * kReadTokens + e;
+            if (tok >= (unsigned)p.n) break;
+            const float s = bf16_bits_to_f32(sm[e] & 0xffffu), m = __uint_as_float(sm[e] & 0xffff0000u);
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = fmaf((float)((c[e] >> (4 * j)) & 15u), s, m);
+            store8((half ? vo : ko) + (long long)tok * D + 8 * w, half ? v_vec : k_vec, x);
+        }
     }
 }
 
@@ -219,6 +266,22 @@ unsigned store_blocks(long long work, int heads, int sm_count) {
 
 }  // namespace
 
+template <typename T>
+static cudaError_t append_t(const Kv4StoreProblem &p, dim3 grid, int kvec, int vvec, cudaStream_t s) {
+    auto kernel = p.D == 128 ? kv4_append_kernel<T, 128> : p.D == 64 ? kv4_append_kernel<T, 64> : kv4_append_kernel<T, 0>;
+    kernel<<<grid, kThreads, 0, s>>>(p, kvec, vvec);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
+template <typename T>
+static cudaError_t read_t(const Kv4StoreProblem &p, dim3 grid, int kvec, int vvec, cudaStream_t s) {
+    auto kernel = p.D == 128 ? kv4_read_kernel<T, 128> : p.D == 64 ? kv4_read_kernel<T, 64> : kv4_read_kernel<T, 0>;
+    kernel<<<grid, kThreads, 0, s>>>(p, kvec, vvec);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_kv4_append(const Kv4StoreProblem &p, int sm_count, cudaStream_t s) {
     const long long groups = (long long)p.n * 2 * (p.D / kKv4Group);
     const dim3 grid(store_blocks((groups + kThreads / 4 - 1) / (kThreads / 4), p.B * p.Hkv, sm_count), p.B * p.Hkv);
@@ -227,20 +290,14 @@ cudaError_t launch_kv4_append(const Kv4StoreProblem &p, int sm_count, cudaStream
         return (reinterpret_cast<uintptr_t>(q) & 15u) == 0 && ((a | b | c) % unit) == 0;
     };
     const int kvec = vec(p.k, p.k_sb, p.k_sh, p.k_ss), vvec = vec(p.v, p.v_sb, p.v_sh, p.v_ss);
-    if (p.dtype == OSF_F32) kv4_append_kernel<float><<<grid, kThreads, 0, s>>>(p, kvec, vvec);
-    else kv4_append_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p, kvec, vvec);
-    count_launches(1);
-    return cudaGetLastError();
+    return p.dtype == OSF_F32 ? append_t<float>(p, grid, kvec, vvec, s) : append_t<__nv_bfloat16>(p, grid, kvec, vvec, s);
 }
 
 cudaError_t launch_kv4_read(const Kv4StoreProblem &p, int sm_count, cudaStream_t s) {
-    const long long words = (long long)p.n * 2 * (p.D / 8);
+    const long long words = (long long)((p.n + kReadTokens - 1) / kReadTokens) * 2 * (p.D / 8);
     const dim3 grid(store_blocks((words + kThreads - 1) / kThreads, p.B * p.Hkv, sm_count), p.B * p.Hkv);
     const int kvec = (reinterpret_cast<uintptr_t>(p.ko) & 15u) == 0, vvec = (reinterpret_cast<uintptr_t>(p.vo) & 15u) == 0;
-    if (p.dtype == OSF_F32) kv4_read_kernel<float><<<grid, kThreads, 0, s>>>(p, kvec, vvec);
-    else kv4_read_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(p, kvec, vvec);
-    count_launches(1);
-    return cudaGetLastError();
+    return p.dtype == OSF_F32 ? read_t<float>(p, grid, kvec, vvec, s) : read_t<__nv_bfloat16>(p, grid, kvec, vvec, s);
 }
 
 }  // namespace osf

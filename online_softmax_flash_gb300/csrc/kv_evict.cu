@@ -8,13 +8,15 @@
 // digits chosen so far, and take the digit in which the k-th largest lies.  A fourth pass writes the
 // indices of the keys above the threshold and the lowest-indexed of the equal ones.  Counts are
 // integers, so the result does not depend on the order of the atomics.
-// One (batch, kv head) is a cluster of up to 8 CTAs, each holding a slice of the keys; the digit
-// counts are summed, and the output offsets of the slices found, through distributed shared memory.
+// One (batch, kv head) is a cluster of up to 8 CTAs, each holding a slice of the keys, in registers while a
+// slice has at most 16384 (a pass then costs no memory latency; longer ones are read again).  The digit counts
+// are summed, and the output offsets of the slices found, through distributed shared memory.
 //
-// Move: rows are copied through registers in 16-byte pieces where their size and address allow.  Into
-// another buffer, every piece is independent.  In place, row r is overwritten by row idx[r] >= r, so
-// one CTA walks a slice of the columns of one (batch, kv head) in blocks of ascending rows: it reads a
-// whole block before it writes it, and a later block's sources are never behind its own first row.
+// Move: one launch for the cache arrays and the weights.  Rows are copied through registers in 16-byte pieces
+// where their size and address allow.  Into another buffer, every piece is independent.  In place, row r is
+// overwritten by row idx[r] >= r, so one CTA walks a slice of the columns of one (batch, kv head) in blocks of
+// ascending rows: it reads a whole block before it writes it, and a later block's sources are never behind its
+// own first row.
 #include "kv_evict.cuh"
 #include "sm100_ptx.cuh"
 
@@ -23,11 +25,10 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 1024;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSelItems = 4;                             // keys per thread and block step
-constexpr int kSliceStep = kSelThreads * kSelItems;
+constexpr int kStep = kSelThreads * 4;   // keys of one block step: four neighbours per thread
 
 __device__ __forceinline__ int valid_length(const EvictProblem &p, int b) {
     if (!p.lens) return p.S;
@@ -48,22 +49,23 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
-// Exclusive prefix sum over the block, and the block's total (two barriers).
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, uint32_t &total) {
+// Exclusive prefix sum over the block, and the block's total (two barriers).  T: one count, or two in the halves.
+template <typename T>
+__device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
+    T x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const T y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
-#pragma unroll
+    T before = 0, all = 0;
+#pragma unroll 8
     for (int i = 0; i < kSelThreads / 32; ++i) {
-        const uint32_t s = warp_sums[i];
-        before += i < warp ? s : 0u;
+        const T s = warp_sums[i];
+        before += i < warp ? s : T(0);
         all += s;
     }
     __syncthreads();
@@ -71,12 +73,14 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums, 
     return before + x - v;
 }
 
+// STEPS: block steps of a slice, its keys held in registers; 0: any number, read again in every pass.
+template <int STEPS>
 __global__ void __launch_bounds__(kSelThreads)
 kv_select_kernel(const EvictProblem p, int cluster) {
     __shared__ uint32_t hist[kBins];
-    __shared__ uint32_t warp_sums[kSelThreads / 32];
+    __shared__ uint64_t warp_sums[kSelThreads / 32];
     __shared__ uint32_t sh_bin, sh_above, sh_count;
-    __shared__ uint32_t slice_counts[2];   // keys above the threshold, keys equal to it, in this slice
+    __shared__ uint64_t slice_counts;   // of this slice: keys equal to the threshold | keys above it
     const int tid = threadIdx.x;
     const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int b = row / p.Hkv;
@@ -90,45 +94,63 @@ kv_select_kernel(const EvictProblem p, int cluster) {
     const float *w = p.w + (long long)row * p.S;
     const int lo = p.sinks, hi = n - p.recent;           // candidates: n > budget >= sinks + recent
     const int k = p.budget - p.sinks - p.recent;         // of which k are kept, k < hi - lo
-    for (int i = rank * kSelThreads + tid; i < p.sinks; i += cluster * kSelThreads) idx[i] = i;
-    for (int i = rank * kSelThreads + tid; i < p.recent; i += cluster * kSelThreads) idx[p.budget - p.recent + i] = hi + i;
-    if (k == 0) return;
     // this CTA's slice of the candidates
     const int per = (hi - lo + cluster - 1) / cluster;
     const int s0 = lo + rank * per, s1 = min(hi, s0 + per);
+    const int steps = STEPS ? STEPS : (per + kStep - 1) / kStep;
+    constexpr int HELD = STEPS ? STEPS : 1;
+    uint32_t key[HELD][4];
+    auto load = [&](int j, uint32_t (&x)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = s0 + j * kStep + tid * 4 + e;
+            x[e] = i < s1 ? order_key(w[i]) : 0u;
+        }
+    };
+    auto valid = [&](int j, int e) { return s0 + j * kStep + tid * 4 + e < s1; };
+    if (STEPS) {
+#pragma unroll
+        for (int j = 0; j < HELD; ++j) load(j, key[j]);
+    }
+    for (int i = rank * kSelThreads + tid; i < p.sinks; i += cluster * kSelThreads) idx[i] = i;
+    for (int i = rank * kSelThreads + tid; i < p.recent; i += cluster * kSelThreads) idx[p.budget - p.recent + i] = hi + i;
+    if (k == 0) return;
 
     uint32_t prefix = 0, mask = 0, left = (uint32_t)k;   // left: still to take among keys matching prefix
+    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digits = pass == 2 ? 1024u : 2048u;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
         __syncthreads();
-        for (int i = s0 + tid; i < s1; i += kSelThreads) {
-            const uint32_t key = order_key(w[i]);
-            if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (digits - 1)], 1u);
+#pragma unroll
+        for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
+            if (!STEPS) load(j, key[0]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t x = key[STEPS ? j : 0][e];
+                if (valid(j, e) && (x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (digits - 1)], 1u);
+            }
         }
         if (cluster > 1) cluster_sync();
         else __syncthreads();
-        // thread t owns digits 4t' .. 4t'+3 counted from the top, so a prefix sum gives the keys above
-        uint32_t c[4], sum = 0;
+        // thread t owns two digits, counted from the top, so a prefix sum gives the keys above
+        uint32_t c[2] = {0, 0};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t bin = kBins - 1 - (4 * tid + e);
-            c[e] = 0;
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t bin = kBins - 1 - (2 * tid + e);
             if (cluster > 1) {
                 for (int r = 0; r < cluster; ++r) c[e] += ld_cluster_u32(mapa_shared(smem_u32(&hist[bin]), r));
             } else {
                 c[e] = hist[bin];
             }
-            sum += c[e];
         }
         uint32_t total;
-        uint32_t above = block_scan(sum, warp_sums, total);
+        uint32_t above = block_scan(c[0] + c[1], reinterpret_cast<uint32_t *>(warp_sums), total);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
             if (above < left && left <= above + c[e]) {
-                sh_bin = kBins - 1 - (4 * tid + e);
+                sh_bin = kBins - 1 - (2 * tid + e);
                 sh_above = above;
                 sh_count = c[e];
             }
@@ -140,106 +162,107 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         mask |= (digits - 1) << shift;
         left -= sh_above;
         if (left == sh_count) break;   // every key with this prefix is taken (uniform over the cluster)
+        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     }
     // kept: (key & mask) > prefix, and the first `left` of those equal to it
-    uint32_t gt = 0, eq = 0;
-    for (int i = s0 + tid; i < s1; i += kSelThreads) {
-        const uint32_t key = order_key(w[i]) & mask;
-        gt += key > prefix;
-        eq += key == prefix;
+    uint64_t mine = 0;   // equal | above
+#pragma unroll
+    for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
+        if (!STEPS) load(j, key[0]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = key[STEPS ? j : 0][e] & mask;
+            if (valid(j, e)) mine += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
+        }
     }
-    uint32_t gt_all, eq_all;
-    block_scan(gt, warp_sums, gt_all);
-    block_scan(eq, warp_sums, eq_all);
+    uint64_t slice;
+    uint64_t before = block_scan(mine, warp_sums, slice);
     uint32_t out = (uint32_t)p.sinks, eq_before = 0;
     if (cluster > 1) {
-        if (tid == 0) {
-            slice_counts[0] = gt_all;
-            slice_counts[1] = eq_all;
-        }
+        if (tid == 0) slice_counts = slice;
         cluster_sync();
         for (int r = 0; r < rank; ++r) {
-            const uint32_t g = ld_cluster_u32(mapa_shared(smem_u32(&slice_counts[0]), r));
-            const uint32_t q = ld_cluster_u32(mapa_shared(smem_u32(&slice_counts[1]), r));
+            const uint32_t at = mapa_shared(smem_u32(&slice_counts), r);
+            const uint32_t g = ld_cluster_u32(at), q = ld_cluster_u32(at + 4);
             out += g + min(q, left - min(left, eq_before));
             eq_before += q;
         }
         cluster_sync();   // nobody leaves while its shared memory may still be read
     }
-    for (int i0 = s0; i0 < s1; i0 += kSliceStep) {
-        uint32_t flag[kSelItems];   // 1: above, 0x10000: equal
-        uint32_t sum = 0;
+    // Positions in index order: steps one after another, threads within a step, neighbours within a thread.
 #pragma unroll
-        for (int e = 0; e < kSelItems; ++e) {
-            const int i = i0 + tid * kSelItems + e;
-            const uint32_t key = i < s1 ? (order_key(w[i]) & mask) : 0u;
-            flag[e] = i >= s1 ? 0u : key > prefix ? 1u : key == prefix ? 0x10000u : 0u;
-            sum += flag[e];
+    for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
+        if (!STEPS) load(j, key[0]);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = key[STEPS ? j : 0][e] & mask;
+            if (valid(j, e)) sum += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
         }
-        uint32_t total;
-        uint32_t before = block_scan(sum, warp_sums, total);
+        uint64_t all = slice;
+        if (STEPS != 1) before = block_scan(sum, warp_sums, all);   // one step: the scan above holds
 #pragma unroll
-        for (int e = 0; e < kSelItems; ++e) {
-            const uint32_t g = before & 0xffffu, q = eq_before + (before >> 16);
-            if (flag[e] == 1u || (flag[e] == 0x10000u && q < left)) {
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t x = key[STEPS ? j : 0][e] & mask;
+            if (!valid(j, e)) continue;
+            const uint32_t g = (uint32_t)before, q = eq_before + (uint32_t)(before >> 32);
+            if (x > prefix || (x == prefix && q < left)) {
                 // equal keys before this one that were taken: those of the whole row, less those of earlier steps
                 const uint32_t taken = min(q, left) - min(eq_before, left);
-                idx[out + g + taken] = i0 + tid * kSelItems + e;
+                idx[out + g + taken] = s0 + j * kStep + tid * 4 + e;
             }
-            before += flag[e];
+            before += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
         }
-        const uint32_t q_after = eq_before + (total >> 16);
-        out += (total & 0xffffu) + min(q_after, left) - min(eq_before, left);
+        const uint32_t q_after = eq_before + (uint32_t)(all >> 32);
+        out += (uint32_t)all + min(q_after, left) - min(eq_before, left);
         eq_before = q_after;
     }
 }
 
-template <typename U>
-__device__ __forceinline__ U ld_stream(const U *p) { return __ldcs(p); }
+constexpr int kMoveThreads = 256;
+constexpr int IL = 4;   // independent pieces per thread
 
-// Rows to another buffer: piece u of the row block is unit u % upr of kept row u / upr.
+// One cache array of the call (0 or 1).
+struct Array {
+    const unsigned char *src;
+    unsigned char *dst;
+    long long row_bytes;
+};
+
+// Rows to another buffer, pieces of type U: piece u of the kept rows is unit u % upr of row u / upr.
 template <typename U>
-__global__ void __launch_bounds__(256)
-kv_move_kernel(const EvictProblem p, int t, int upr) {
-    griddep_wait();
-    const int row = blockIdx.y, b = row / p.Hkv;
-    const int keep = min(valid_length(p, b), p.budget);
+__device__ __forceinline__ void move_out(const EvictProblem &p, const Array &t, int row, int keep) {
     const int *idx = p.idx + (long long)row * p.budget;
-    const U *src = reinterpret_cast<const U *>(p.src[t] + (long long)row * p.S * p.row_bytes[t]);
-    U *dst = reinterpret_cast<U *>(p.dst[t] + (long long)row * p.S_out * p.row_bytes[t]);
-    constexpr int IL = 4;   // independent pieces per thread
-    const long long total = (long long)keep * upr;
-    for (long long u0 = (long long)blockIdx.x * (256 * IL) + threadIdx.x; u0 < total; u0 += (long long)gridDim.x * (256 * IL)) {
+    const U *src = reinterpret_cast<const U *>(t.src + (long long)row * p.S * t.row_bytes);
+    U *dst = reinterpret_cast<U *>(t.dst + (long long)row * p.S_out * t.row_bytes);
+    const unsigned upr = (unsigned)(t.row_bytes / sizeof(U)), total = keep * upr;   // budget * row_bytes < 2^31
+    const unsigned step = gridDim.x * (kMoveThreads * IL);
+    for (unsigned u0 = blockIdx.x * (kMoveThreads * IL) + threadIdx.x; u0 < total; u0 += step) {
         U v[IL];
 #pragma unroll
         for (int e = 0; e < IL; ++e) {
-            const long long u = u0 + e * 256;
+            const unsigned u = u0 + e * kMoveThreads;
             if (u < total) {
-                const int r = (int)(u / upr), c = (int)(u - (long long)r * upr);
-                v[e] = ld_stream(src + (long long)idx[r] * upr + c);
+                const unsigned r = u / upr;
+                v[e] = __ldcs(src + (long long)idx[r] * upr + (u - r * upr));
             }
         }
 #pragma unroll
-        for (int e = 0; e < IL; ++e) {
-            const long long u = u0 + e * 256;
-            if (u < total) dst[u] = v[e];
-        }
+        for (int e = 0; e < IL; ++e)
+            if (u0 + e * kMoveThreads < total) __stcs(dst + u0 + e * kMoveThreads, v[e]);
     }
 }
 
-// Rows within one buffer (see the top): `cols` neighbouring pieces of every row per CTA.
+// Rows within one buffer (see the top): 64 bytes, two whole sectors, of every row per CTA.
 template <typename U>
-__global__ void __launch_bounds__(256)
-kv_move_in_place_kernel(const EvictProblem p, int t, int upr, int cols) {
-    griddep_wait();
-    const int row = blockIdx.y, b = row / p.Hkv;
-    const int keep = min(valid_length(p, b), p.budget);
+__device__ __forceinline__ void move_in_place(const EvictProblem &p, const Array &t, int row, int keep) {
     const int *idx = p.idx + (long long)row * p.budget;
-    U *buf = reinterpret_cast<U *>(p.dst[t] + (long long)row * p.S * p.row_bytes[t]);
+    U *buf = reinterpret_cast<U *>(t.dst + (long long)row * p.S * t.row_bytes);
+    const int upr = (int)(t.row_bytes / sizeof(U)), cols = min(upr, (int)(64 / sizeof(U)));
     const int c = blockIdx.x * cols + threadIdx.x % cols;
-    const int rows_per = 256 / cols, r_in = threadIdx.x / cols;
+    const int rows_per = kMoveThreads / cols, r_in = threadIdx.x / cols;
     const bool on = r_in < rows_per && c < upr;
-    constexpr int IL = 4;
+    if ((int)blockIdx.x * cols >= upr) return;
     for (int r0 = 0; r0 < keep; r0 += rows_per * IL) {
         U v[IL];
         int from[IL];
@@ -259,77 +282,87 @@ kv_move_in_place_kernel(const EvictProblem p, int t, int upr, int cols) {
     }
 }
 
-// Weights of the kept rows, zeros behind them, and the new length.  In place like the rows.
-__global__ void __launch_bounds__(1024)
-kv_move_weights_kernel(const EvictProblem p) {
-    griddep_wait();
-    const int row = blockIdx.x, b = row / p.Hkv;
-    const int keep = min(valid_length(p, b), p.budget);
+// Weights of the kept rows, zeros behind them, and the new length.  One CTA per row when in place.
+__device__ __forceinline__ void move_weights(const EvictProblem &p, int row, int b, int keep) {
     const int *idx = p.idx + (long long)row * p.budget;
     const float *src = p.w + (long long)row * p.S;
     float *dst = p.w_out + (long long)row * p.S_out;
-    constexpr int IL = 4;
-    for (int r0 = 0; r0 < keep; r0 += 1024 * IL) {
-        float v[IL];
+    // a length that is written over the old one gives the same `keep` to a block that reads it late
+    if (blockIdx.x == 0 && p.lens_out && row % p.Hkv == 0 && threadIdx.x == 0) p.lens_out[b] = keep;
+    if (p.w != p.w_out) {
+        for (unsigned r = blockIdx.x * kMoveThreads + threadIdx.x; r < (unsigned)p.S_out; r += gridDim.x * kMoveThreads)
+            dst[r] = r < (unsigned)keep ? src[idx[r]] : 0.f;
+        return;
+    }
+    if (blockIdx.x != 0) return;
+    constexpr int WL = 16;
+    for (int r0 = 0; r0 < keep; r0 += kMoveThreads * WL) {
+        float v[WL];
 #pragma unroll
-        for (int e = 0; e < IL; ++e) {
-            const int r = r0 + e * 1024 + threadIdx.x;
+        for (int e = 0; e < WL; ++e) {
+            const int r = r0 + e * kMoveThreads + threadIdx.x;
             if (r < keep) v[e] = src[idx[r]];
         }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < IL; ++e) {
-            const int r = r0 + e * 1024 + threadIdx.x;
+        for (int e = 0; e < WL; ++e) {
+            const int r = r0 + e * kMoveThreads + threadIdx.x;
             if (r < keep) dst[r] = v[e];
         }
         __syncthreads();
     }
-    for (int r = keep + threadIdx.x; r < p.S_out; r += 1024) dst[r] = 0.f;
-    // a length that is written over the old one gives the same `keep` to a block that reads it late
-    if (p.lens_out && row % p.Hkv == 0 && threadIdx.x == 0) p.lens_out[b] = keep;
+    for (int r = keep + threadIdx.x; r < p.S_out; r += kMoveThreads) dst[r] = 0.f;
 }
 
-template <typename U>
-cudaError_t launch_move_t(const EvictProblem &p, int t, int sm_count, cudaStream_t s) {
-    const int rows = p.B * p.Hkv;
-    const long long upr = p.row_bytes[t] / (long long)sizeof(U);
-    if (p.src[t] == p.dst[t]) {
-        // 64 bytes of every row per CTA: two whole sectors
-        const int cols = (int)(upr < 64 / (int)sizeof(U) ? upr : 64 / (int)sizeof(U));
-        return launch_dependent(kv_move_in_place_kernel<U>, dim3((unsigned)((upr + cols - 1) / cols), rows), dim3(256), 0, s,
-                                p, t, (int)upr, cols);
+// blockIdx.z: 0 the weights, 1 and 2 the cache arrays.
+__global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictProblem p) {
+    griddep_wait();   // the indices
+    const int row = blockIdx.y, b = row / p.Hkv;
+    const int keep = min(valid_length(p, b), p.budget);
+    if (blockIdx.z == 0) {
+        move_weights(p, row, b, keep);
+        return;
     }
-    const long long work = ((long long)p.budget * upr + 1023) / 1024;
-    long long blocks = ((long long)sm_count * 16 + rows - 1) / rows;
-    blocks = blocks < work ? blocks : work;
-    return launch_dependent(kv_move_kernel<U>, dim3((unsigned)(blocks < 1 ? 1 : blocks), rows), dim3(256), 0, s, p, t, (int)upr);
-}
-
-cudaError_t launch_move(const EvictProblem &p, int t, int sm_count, cudaStream_t s) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p.src[t]) | reinterpret_cast<uintptr_t>(p.dst[t]) | (uintptr_t)p.row_bytes[t];
-    if ((a & 15) == 0) return launch_move_t<uint4>(p, t, sm_count, s);
-    if ((a & 3) == 0) return launch_move_t<uint32_t>(p, t, sm_count, s);
-    return launch_move_t<unsigned char>(p, t, sm_count, s);
+    const Array t = blockIdx.z == 1 ? Array{p.src[0], p.dst[0], p.row_bytes[0]} : Array{p.src[1], p.dst[1], p.row_bytes[1]};
+    if (!t.src) return;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(t.src) | reinterpret_cast<uintptr_t>(t.dst) | (uintptr_t)t.row_bytes;
+    if (t.src == t.dst) {
+        if ((a & 15) == 0) move_in_place<uint4>(p, t, row, keep);
+        else if ((a & 3) == 0) move_in_place<uint32_t>(p, t, row, keep);
+        else move_in_place<unsigned char>(p, t, row, keep);
+    } else {
+        if ((a & 15) == 0) move_out<uint4>(p, t, row, keep);
+        else if ((a & 3) == 0) move_out<uint32_t>(p, t, row, keep);
+        else move_out<unsigned char>(p, t, row, keep);
+    }
 }
 
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictProblem &p, int sm_count, cudaStream_t s) {
     const int rows = p.B * p.Hkv;
-    // a CTA takes up to 8192 keys before the row is spread over more of them
+    // up to 8192 keys for a CTA before the row is spread over more of them
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)cluster * 8192 < p.S) cluster *= 2;
-    cudaError_t e = launch_clustered(kv_select_kernel, dim3((unsigned)rows * cluster), dim3(kSelThreads), 0, s,
-                                     dim3(cluster, 1, 1), false, p, cluster);
+    while (cluster < kMaxCluster && (long long)cluster * 2 * kStep < p.S) cluster *= 2;
+    const long long per = ((long long)p.S + cluster - 1) / cluster;
+    auto select = per <= kStep ? kv_select_kernel<1> : per <= 2 * kStep ? kv_select_kernel<2>
+                : per <= 4 * kStep ? kv_select_kernel<4> : kv_select_kernel<0>;
+    cudaError_t e = launch_clustered(select, dim3((unsigned)rows * cluster), dim3(kSelThreads), 0, s, dim3(cluster, 1, 1), false,
+                                     p, cluster);
     if (e != cudaSuccess) return e;
-    int launches = 2;
-    for (int t = 0; t < 2 && e == cudaSuccess; ++t)
-        if (p.src[t]) {
-            e = launch_move(p, t, sm_count, s);
-            ++launches;
-        }
-    if (e == cudaSuccess) e = launch_dependent(kv_move_weights_kernel, dim3((unsigned)rows), dim3(1024), 0, s, p);
-    count_launches(launches);
+    // blocks along a row's pieces: all that the work can use, about sixteen to an SM over the grid; in place, a
+    // block per 64 bytes of the row
+    long long want = ((long long)sm_count * 16 + 2 * rows - 1) / (2 * rows), blocks = 1;
+    for (int t = 0; t < 2; ++t) {
+        if (!p.src[t]) continue;
+        const long long work = p.src[t] == p.dst[t] ? (p.row_bytes[t] + 63) / 64
+                                                    : (p.budget * p.row_bytes[t] / 16 + kMoveThreads * IL - 1) / (kMoveThreads * IL);
+        const long long need = p.src[t] == p.dst[t] ? work : work < want ? work : want;
+        blocks = need > blocks ? need : blocks;
+    }
+    count_launches(2);
+    e = launch_dependent(kv_move_kernel, dim3((unsigned)blocks, (unsigned)rows, p.src[1] ? 3 : p.src[0] ? 2 : 1), dim3(kMoveThreads), 0,
+                         s, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
