@@ -114,55 +114,64 @@ __device__ __forceinline__ void group_scale(float lo, float hi, float &s, float 
         s = m = __uint_as_float(0x7fc00000u);
         return;
     }
-    // a bfloat16 within one of the wanted one, which is the first with 15 s >= d + e
-    uint32_t u = __float_as_uint(d * 0.06666667f) & 0xffff0000u;
-    if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) {
-        u += 0x10000u;
-        if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
-    } else if (u && cmp_exact(d, e, 15.f * __uint_as_float(u - 0x10000u)) <= 0) {
-        u -= 0x10000u;
-    }
+    // 0x1.11111p-4 is below 1/15 by 2^-22: the truncated product is the wanted bfloat16, the first with
+    // 15 s >= d + e, or at most two below it
+    uint32_t u = __float_as_uint(d * 0x1.11111p-4f) & 0xffff0000u;
+    if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
+    if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
     s = __uint_as_float(u);
-}
-
-// One code, settled exactly near a tie.
-__device__ __noinline__ uint32_t quantise_exact(float x, float s, float m) {
-    // a scale whose reciprocal could overflow is lifted first
-    const float up = s < 0x1p-100f ? 0x1p60f : 1.f;
-    float d = __fsub_rn(x, m), e;
-    const float t = d * up * __frcp_rn(s * up);   // within 2^-21 of (x - m) / s
-    float c = rintf(t);
-    if (fabsf(t - c) > 0.4999f) {
-        diff_exact(x, m, d, e);
-        c = floorf(t);   // the tie is at c + 1/2
-        const int side = cmp_exact(d, e, (c + 0.5f) * s);
-        if (side > 0 || (side == 0 && ((int)c & 1))) c += 1.f;
-    }
-    return (uint32_t)(int)c;
 }
 
 // Codes of eight channels as one word.  t + 1.5 * 2^23 has the rounded t in its low bits, so a code needs no
 // conversion: the eight sums of those bits times 16^i make the word and a constant.
-__device__ __forceinline__ uint32_t quantise8(const float (&x)[8], float s, float m) {
-    if (!(s > 0.f)) return 0u;   // a constant group, or NaN
-    const float inv = rcp_approx(s), magic = 12582912.f;   // 0x4b400000
-    uint32_t w = 0u - 0x4b400000u * 0x11111111u;
-    float far = s < 0x1p-100f ? 1.f : 0.f;   // distance from the nearest integer; tiny scales go the exact way too
-    uint32_t place = 1u;
+constexpr float kMagic = 12582912.f;   // 0x4b400000
+__device__ __forceinline__ uint32_t word_of(const float (&r)[8]) {
+    uint32_t w = 0u - 0x4b400000u * 0x11111111u, place = 1u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i, place <<= 4) {
-        const float t = __fsub_rn(x[i], m) * inv;   // within 2^-20 of (x - m) / s
-        const float r = __fadd_rn(t, magic);
-        far = fmaxf(far, fabsf(__fsub_rn(t, __fsub_rn(r, magic))));
-        w += __float_as_uint(r) * place;
-    }
-    if (far > 0.4999f) {
-        w = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w |= quantise_exact(x[i], s, m) << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i, place <<= 4) w += __float_as_uint(r[i]) * place;
     return w;
 }
+
+// Any group.  t is off by up to 2^-20; what is left over, (x - m) - code * s, is exact, and only where it
+// reaches s / 2 is the code looked at again.
+__device__ __noinline__ uint32_t quantise8_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
+                                               float s, float m) {
+    const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+    const float up = s < 0x1p-100f ? 0x1p60f : 1.f;   // a reciprocal that could overflow: lifted first
+    const float inv = rcp_approx(s * up), half = 0.5f * s;
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float d = __fsub_rn(x[i], m), e;
+        r[i] = __fadd_rn(d * up * inv, kMagic);
+        const float c = __fsub_rn(r[i], kMagic), rest = fmaf(-c, s, d);
+        if (fabsf(rest) >= half) {
+            diff_exact(x[i], m, d, e);
+            // at the tie (rest = +- s / 2) the side is that of e, or the even code; past it the neighbour
+            const float over = fabsf(rest) > half ? 1.f : rest > 0.f ? e : -e;
+            if (over > 0.f || (over == 0.f && ((int)c & 1))) r[i] += rest > 0.f ? 1.f : -1.f;
+        }
+    }
+    return word_of(r);
+}
+
+// A group of bfloat16 values of which, with m, the smallest is at least 2^-11 s: they are multiples of 2^-19 s, so
+// x - m (< 16 s) is exact, and (x - m) / s is a tie or at least 2^-20 off one.  The correctly rounded quotient
+// (a product with the rounded reciprocal and one remainder step, Markstein) then rounds to the right code,
+// ties to even among them, which bfloat16's coarse grid makes common: one code in some hundred.
+__device__ __forceinline__ uint32_t quantise8_coarse(const float (&x)[8], float s, float m) {
+    const float inv = __frcp_rn(s);
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float d = __fsub_rn(x[i], m), t = d * inv;
+        r[i] = __fadd_rn(fmaf(fmaf(-t, s, d), inv, t), kMagic);
+    }
+    return word_of(r);
+}
+
+__device__ __forceinline__ bool coarse_type(const float *) { return false; }
+__device__ __forceinline__ bool coarse_type(const __nv_bfloat16 *) { return true; }
 
 // Four lanes share a group of 32 channels; group i of a head is K group 0, 1, ..., V group 0, 1, ... of token
 // i / (2 groups).  DC: the head dimension where the compiler is to know it (its divisions become shifts), or 0.
@@ -204,7 +213,16 @@ kv4_append_kernel(const Kv4StoreProblem p, int k_vec, int v_vec) {
         }
         float s, m;
         group_scale(lo, hi, s, m);
-        const uint32_t w = quantise8(x, s, m);
+        uint32_t w = 0;   // a constant group, or NaN
+        if (s > 0.f) {
+            float least = m == 0.f ? INFINITY : fabsf(m);
+            if (coarse_type(kh)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) least = fminf(least, fabsf(x[e]));
+            }
+            if (coarse_type(kh) && least >= 0x1p-11f * s && s >= 0x1p-80f) w = quantise8_coarse(x, s, m);
+            else w = quantise8_any(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], s, m);
+        }
         if (!on) continue;
         unsigned char *rec = head + (long long)tok * R;
         reinterpret_cast<uint32_t *>(rec + (half ? D / 2 : 0))[kv4_word_at(D, n * 4 + t)] = w;

@@ -97,6 +97,25 @@ def test_append_of_values_next_to_ties(osf):
     assert len(diff) == 0, diff[:20].tolist()
 
 
+def test_append_of_bfloat16_values_of_all_magnitudes(osf):
+    """Magnitudes spread over 2^-30 .. 2^4, tiny minima under coarse values, offsets far from zero: the codes
+    of bfloat16 groups are the exact ones too."""
+    rng = np.random.default_rng(4)
+    n = 48
+    x = rng.standard_normal((1, 1, n, 128)) * 2.0 ** rng.uniform(-30, 4, (1, 1, n, 128))
+    x[0, 0, :12] = np.abs(np.round(rng.standard_normal((12, 128)) * 8) / 8) + 0.125      # coarse, with exact ties
+    x[0, 0, :6, ::32] = 2.0 ** rng.uniform(-30, -12, (6, 4))                               # under a tiny minimum
+    x[0, 0, 6:12, 1::32] = 2.0 ** rng.uniform(-30, -12, (6, 4)) * rng.choice([-1, 1], (6, 4))
+    x[0, 0, 12:20] = 300 + np.round(rng.standard_normal((8, 128)) * 8)
+    x[0, 0, 20:24, :64] = 0
+    bits = si.f32_to_bf16_bits(x.astype(np.float32))
+    xv = si.bf16_bits_to_f32(bits)
+    cache = torch.zeros(1, 1, n, 160, dtype=torch.uint8, device="cuda")
+    osf.osf_kv4_append(bf16_tensor(bits), bf16_tensor(bits[:, :, ::-1].copy()), cache)
+    diff = np.argwhere(cache.cpu().numpy() != oracle.records(xv, xv[:, :, ::-1]))
+    assert len(diff) == 0, diff[:20].tolist()
+
+
 def test_append_counts_strides_and_bounds(osf):
     B, Hkv, n, D, S = 4, 2, 6, 64, 16
     # [B, n, H, D] projections seen as [B, H, n, D], padded rows poisoned
