@@ -17,6 +17,8 @@
 // overwritten by row idx[r] >= r, so one CTA walks a slice of the columns of one (batch, kv head) in blocks of
 // ascending rows: it reads a whole block before it writes it, and a later block's sources are never behind its
 // own first row.
+#include <type_traits>
+
 #include "kv_evict.cuh"
 #include "sm100_ptx.cuh"
 
@@ -25,7 +27,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
 constexpr int kStep = kSelThreads * 4;   // keys of one block step: four neighbours per thread
@@ -49,9 +51,18 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
+// 16 bytes of shared memory of this CTA or another of the cluster.
+__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
 // Exclusive prefix sum over the block, and the block's total (two barriers).  T: one count, or two in the halves.
 template <typename T>
 __device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
+    constexpr int W = kSelThreads / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     T x = v;
 #pragma unroll
@@ -61,26 +72,32 @@ __device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    T before = 0, all = 0;
-#pragma unroll 8
-    for (int i = 0; i < kSelThreads / 32; ++i) {
-        const T s = warp_sums[i];
-        before += i < warp ? s : T(0);
-        all += s;
+    T s = lane < W ? warp_sums[lane] : T(0);   // every warp scans the warps' sums
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+        const T y = __shfl_up_sync(0xffffffffu, s, o);
+        if (lane >= o) s += y;
     }
+    total = __shfl_sync(0xffffffffu, s, W - 1);
+    const T before = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : T(0);
     __syncthreads();
-    total = all;
     return before + x - v;
 }
 
 // STEPS: block steps of a slice, its keys held in registers; 0: any number, read again in every pass.
 template <int STEPS>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, 2)
 kv_select_kernel(const EvictProblem p, int cluster) {
-    __shared__ uint32_t hist[kBins];
-    __shared__ uint64_t warp_sums[kSelThreads / 32];
+    __shared__ __align__(16) uint32_t hist[kBins];
+    // two counts in one word, keys equal to the threshold in its upper half, keys above it in the lower: a slice
+    // held in registers has at most 2^14 keys
+    using Pair = typename std::conditional<STEPS != 0, uint32_t, uint64_t>::type;
+    constexpr int HALF = sizeof(Pair) * 4;
+    constexpr Pair ABOVE = 1, EQUAL = Pair(1) << HALF, LOW = EQUAL - 1;
+    __shared__ Pair warp_sums[kSelThreads / 32];
+    __shared__ uint32_t digit_sums[kSelThreads / 32];
     __shared__ uint32_t sh_bin, sh_above, sh_count;
-    __shared__ uint64_t slice_counts;   // of this slice: keys equal to the threshold | keys above it
+    __shared__ uint32_t slice_counts[2];   // of this slice: keys above the threshold, keys equal to it
     const int tid = threadIdx.x;
     const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int b = row / p.Hkv;
@@ -134,23 +151,27 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         }
         if (cluster > 1) cluster_sync();
         else __syncthreads();
-        // thread t owns two digits, counted from the top, so a prefix sum gives the keys above
-        uint32_t c[2] = {0, 0};
+        // thread t owns four digits, counted from the top, so a prefix sum gives the keys above; the counts of
+        // all ranks are read before any is used
+        constexpr int OWN = 4;
+        static_assert(kBins == OWN * kSelThreads, "a thread owns four digits");
+        const uint32_t mine_at = smem_u32(&hist[kBins - OWN * (tid + 1)]);
+        uint4 part[kMaxCluster];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const uint32_t bin = kBins - 1 - (2 * tid + e);
-            if (cluster > 1) {
-                for (int r = 0; r < cluster; ++r) c[e] += ld_cluster_u32(mapa_shared(smem_u32(&hist[bin]), r));
-            } else {
-                c[e] = hist[bin];
-            }
+        for (int r = 0; r < kMaxCluster; ++r)
+            part[r] = r < cluster ? ld_cluster_v4(cluster > 1 ? mapa_shared(mine_at, r) : mine_at) : make_uint4(0, 0, 0, 0);
+        uint32_t c[OWN] = {0, 0, 0, 0};
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+            c[0] += part[r].w; c[1] += part[r].z; c[2] += part[r].y; c[3] += part[r].x;
         }
+        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
         uint32_t total;
-        uint32_t above = block_scan(c[0] + c[1], reinterpret_cast<uint32_t *>(warp_sums), total);
+        uint32_t above = block_scan(sum, digit_sums, total);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int e = 0; e < OWN; ++e) {
             if (above < left && left <= above + c[e]) {
-                sh_bin = kBins - 1 - (2 * tid + e);
+                sh_bin = kBins - 1 - (OWN * tid + e);
                 sh_above = above;
                 sh_count = c[e];
             }
@@ -165,24 +186,27 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     }
     // kept: (key & mask) > prefix, and the first `left` of those equal to it
-    uint64_t mine = 0;   // equal | above
+    Pair mine = 0;
 #pragma unroll
     for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
         if (!STEPS) load(j, key[0]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t x = key[STEPS ? j : 0][e] & mask;
-            if (valid(j, e)) mine += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
+            if (valid(j, e)) mine += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
         }
     }
-    uint64_t slice;
-    uint64_t before = block_scan(mine, warp_sums, slice);
+    Pair slice;
+    Pair before = block_scan(mine, warp_sums, slice);
     uint32_t out = (uint32_t)p.sinks, eq_before = 0;
     if (cluster > 1) {
-        if (tid == 0) slice_counts = slice;
+        if (tid == 0) {
+            slice_counts[0] = (uint32_t)(slice & LOW);
+            slice_counts[1] = (uint32_t)(slice >> HALF);
+        }
         cluster_sync();
         for (int r = 0; r < rank; ++r) {
-            const uint32_t at = mapa_shared(smem_u32(&slice_counts), r);
+            const uint32_t at = mapa_shared(smem_u32(slice_counts), r);
             const uint32_t g = ld_cluster_u32(at), q = ld_cluster_u32(at + 4);
             out += g + min(q, left - min(left, eq_before));
             eq_before += q;
@@ -193,28 +217,28 @@ kv_select_kernel(const EvictProblem p, int cluster) {
 #pragma unroll
     for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
         if (!STEPS) load(j, key[0]);
-        uint64_t sum = 0;
+        Pair sum = 0;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t x = key[STEPS ? j : 0][e] & mask;
-            if (valid(j, e)) sum += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
+            if (valid(j, e)) sum += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
         }
-        uint64_t all = slice;
+        Pair all = slice;
         if (STEPS != 1) before = block_scan(sum, warp_sums, all);   // one step: the scan above holds
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const uint32_t x = key[STEPS ? j : 0][e] & mask;
             if (!valid(j, e)) continue;
-            const uint32_t g = (uint32_t)before, q = eq_before + (uint32_t)(before >> 32);
+            const uint32_t g = (uint32_t)(before & LOW), q = eq_before + (uint32_t)(before >> HALF);
             if (x > prefix || (x == prefix && q < left)) {
                 // equal keys before this one that were taken: those of the whole row, less those of earlier steps
                 const uint32_t taken = min(q, left) - min(eq_before, left);
                 idx[out + g + taken] = s0 + j * kStep + tid * 4 + e;
             }
-            before += x > prefix ? 1ull : x == prefix ? 1ull << 32 : 0ull;
+            before += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
         }
-        const uint32_t q_after = eq_before + (uint32_t)(all >> 32);
-        out += (uint32_t)all + min(q_after, left) - min(eq_before, left);
+        const uint32_t q_after = eq_before + (uint32_t)(all >> HALF);
+        out += (uint32_t)(all & LOW) + min(q_after, left) - min(eq_before, left);
         eq_before = q_after;
     }
 }
@@ -343,10 +367,10 @@ cudaError_t launch_kv_evict(const EvictProblem &p, int sm_count, cudaStream_t s)
     const int rows = p.B * p.Hkv;
     // up to 8192 keys for a CTA before the row is spread over more of them
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)cluster * 2 * kStep < p.S) cluster *= 2;
+    while (cluster < kMaxCluster && (long long)cluster * 4 * kStep < p.S) cluster *= 2;
     const long long per = ((long long)p.S + cluster - 1) / cluster;
     auto select = per <= kStep ? kv_select_kernel<1> : per <= 2 * kStep ? kv_select_kernel<2>
-                : per <= 4 * kStep ? kv_select_kernel<4> : kv_select_kernel<0>;
+                : per <= 4 * kStep ? kv_select_kernel<4> : per <= 8 * kStep ? kv_select_kernel<8> : kv_select_kernel<0>;
     cudaError_t e = launch_clustered(select, dim3((unsigned)rows * cluster), dim3(kSelThreads), 0, s, dim3(cluster, 1, 1), false,
                                      p, cluster);
     if (e != cudaSuccess) return e;
