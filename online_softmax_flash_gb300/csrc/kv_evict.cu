@@ -17,8 +17,6 @@
 // overwritten by row idx[r] >= r, so one CTA walks a slice of the columns of one (batch, kv head) in blocks of
 // ascending rows: it reads a whole block before it writes it, and a later block's sources are never behind its
 // own first row.
-#include <type_traits>
-
 #include "kv_evict.cuh"
 #include "sm100_ptx.cuh"
 
@@ -30,7 +28,7 @@ using namespace ptx;
 constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kStep = kSelThreads * 4;   // keys of one block step: four neighbours per thread
+constexpr int kSelWarps = kSelThreads / 32;
 
 __device__ __forceinline__ int valid_length(const EvictProblem &p, int b) {
     if (!p.lens) return p.S;
@@ -38,11 +36,10 @@ __device__ __forceinline__ int valid_length(const EvictProblem &p, int b) {
     return min(max(n, 0), p.S);
 }
 
-// Order-preserving integer of a weight: NaN is 0, -0 equals +0.
+// Order-preserving integer of a weight: NaN is 1, below every number, -0 equals +0; 0 stands for no key.
 __device__ __forceinline__ uint32_t order_key(float w) {
-    if (w != w) return 0u;
-    const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
-    return (u >> 31) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(__fadd_rn(w, 0.f));   // -0 + 0 = +0
+    return w != w ? 1u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
@@ -59,46 +56,40 @@ __device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
     return v;
 }
 
-// Exclusive prefix sum over the block, and the block's total (two barriers).  T: one count, or two in the halves.
-template <typename T>
-__device__ __forceinline__ T block_scan(T v, T *warp_sums, T &total) {
-    constexpr int W = kSelThreads / 32;
+// Exclusive prefix sum over the block (two barriers).
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T x = v;
+    uint32_t x = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, x, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    T s = lane < W ? warp_sums[lane] : T(0);   // every warp scans the warps' sums
+    uint32_t s = lane < kSelWarps ? warp_sums[lane] : 0u;   // every warp scans the warps' sums
 #pragma unroll
-    for (int o = 1; o < W; o <<= 1) {
-        const T y = __shfl_up_sync(0xffffffffu, s, o);
+    for (int o = 1; o < kSelWarps; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
-    total = __shfl_sync(0xffffffffu, s, W - 1);
-    const T before = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : T(0);
+    const uint32_t before = warp ? __shfl_sync(0xffffffffu, s, warp - 1) : 0u;
     __syncthreads();
     return before + x - v;
 }
 
-// STEPS: block steps of a slice, its keys held in registers; 0: any number, read again in every pass.
-template <int STEPS>
-__global__ void __launch_bounds__(kSelThreads, 2)
+// A warp owns a run of neighbouring keys of its CTA's slice, 32 at a time, so that positions within it come from
+// ballots.  KPT: keys per thread, held in registers; 0: any number, read again in every pass.  Places behind the
+// slice hold 0, below every key: fewer keys are kept than there are, so none of them is ever chosen.
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, KPT > 16 ? 1 : 2)
 kv_select_kernel(const EvictProblem p, int cluster) {
     __shared__ __align__(16) uint32_t hist[kBins];
-    // two counts in one word, keys equal to the threshold in its upper half, keys above it in the lower: a slice
-    // held in registers has at most 2^14 keys
-    using Pair = typename std::conditional<STEPS != 0, uint32_t, uint64_t>::type;
-    constexpr int HALF = sizeof(Pair) * 4;
-    constexpr Pair ABOVE = 1, EQUAL = Pair(1) << HALF, LOW = EQUAL - 1;
-    __shared__ Pair warp_sums[kSelThreads / 32];
-    __shared__ uint32_t digit_sums[kSelThreads / 32];
+    __shared__ uint32_t digit_sums[kSelWarps];
+    __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps];
     __shared__ uint32_t sh_bin, sh_above, sh_count;
     __shared__ uint32_t slice_counts[2];   // of this slice: keys above the threshold, keys equal to it
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int b = row / p.Hkv;
     const int n = valid_length(p, b);
@@ -108,30 +99,37 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         for (int i = rank * kSelThreads + tid; i < p.budget; i += cluster * kSelThreads) idx[i] = i < n ? i : -1;
         return;
     }
-    const float *w = p.w + (long long)row * p.S;
     const int lo = p.sinks, hi = n - p.recent;           // candidates: n > budget >= sinks + recent
     const int k = p.budget - p.sinks - p.recent;         // of which k are kept, k < hi - lo
-    // this CTA's slice of the candidates
+    // this CTA's slice of the candidates, this warp's run of it
     const int per = (hi - lo + cluster - 1) / cluster;
-    const int s0 = lo + rank * per, s1 = min(hi, s0 + per);
-    const int steps = STEPS ? STEPS : (per + kStep - 1) / kStep;
-    constexpr int HELD = STEPS ? STEPS : 1;
-    uint32_t key[HELD][4];
-    auto load = [&](int j, uint32_t (&x)[4]) {
+    const int s1 = min(hi, lo + (rank + 1) * per);
+    const int groups = KPT ? KPT : ((per + kSelWarps - 1) / kSelWarps + 31) / 32;   // of 32 keys
+    const int first = lo + rank * per + warp * groups * 32 + lane;
+    const float *w = p.w + (long long)row * p.S;
+    uint32_t key[KPT ? KPT : 1];
+    // unconditional loads (a place behind the slice reads its last key), so that all of a thread's are in flight
+    auto load = [&](int i) { return w[max(0, min(first + i * 32, s1 - 1))]; };
+    auto key_of = [&](int i, float v) { return first + i * 32 < s1 ? order_key(v) : 0u; };
+    if (KPT) {
+        float v[KPT ? KPT : 1];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = s0 + j * kStep + tid * 4 + e;
-            x[e] = i < s1 ? order_key(w[i]) : 0u;
-        }
-    };
-    auto valid = [&](int j, int e) { return s0 + j * kStep + tid * 4 + e < s1; };
-    if (STEPS) {
+        for (int i = 0; i < KPT; ++i) v[i] = load(i);
 #pragma unroll
-        for (int j = 0; j < HELD; ++j) load(j, key[j]);
+        for (int i = 0; i < KPT; ++i) key[i] = key_of(i, v[i]);
     }
     for (int i = rank * kSelThreads + tid; i < p.sinks; i += cluster * kSelThreads) idx[i] = i;
     for (int i = rank * kSelThreads + tid; i < p.recent; i += cluster * kSelThreads) idx[p.budget - p.recent + i] = hi + i;
     if (k == 0) return;
+    // apply f to every group's key of this lane, in order
+    auto each = [&](auto f) {
+        if (KPT) {
+#pragma unroll
+            for (int i = 0; i < KPT; ++i) f(i, key[i]);
+        } else {
+            for (int i = 0; i < groups; ++i) f(i, key_of(i, load(i)));
+        }
+    };
 
     uint32_t prefix = 0, mask = 0, left = (uint32_t)k;   // left: still to take among keys matching prefix
     for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
@@ -140,15 +138,9 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t digits = pass == 2 ? 1024u : 2048u;
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
-            if (!STEPS) load(j, key[0]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t x = key[STEPS ? j : 0][e];
-                if (valid(j, e) && (x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (digits - 1)], 1u);
-            }
-        }
+        each([&](int, uint32_t x) {
+            if ((x & mask) == prefix && x) atomicAdd(&hist[(x >> shift) & (digits - 1)], 1u);
+        });
         if (cluster > 1) cluster_sync();
         else __syncthreads();
         // thread t owns four digits, counted from the top, so a prefix sum gives the keys above; the counts of
@@ -165,9 +157,7 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         for (int r = 0; r < kMaxCluster; ++r) {
             c[0] += part[r].w; c[1] += part[r].z; c[2] += part[r].y; c[3] += part[r].x;
         }
-        const uint32_t sum = c[0] + c[1] + c[2] + c[3];
-        uint32_t total;
-        uint32_t above = block_scan(sum, digit_sums, total);
+        uint32_t above = block_scan(c[0] + c[1] + c[2] + c[3], digit_sums);
 #pragma unroll
         for (int e = 0; e < OWN; ++e) {
             if (above < left && left <= above + c[e]) {
@@ -185,62 +175,50 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         if (left == sh_count) break;   // every key with this prefix is taken (uniform over the cluster)
         for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
     }
-    // kept: (key & mask) > prefix, and the first `left` of those equal to it
-    Pair mine = 0;
-#pragma unroll
-    for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
-        if (!STEPS) load(j, key[0]);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t x = key[STEPS ? j : 0][e] & mask;
-            if (valid(j, e)) mine += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
-        }
+    // kept: (key & mask) > prefix, and the first `left` of those equal to it.  Of both, the number before each warp:
+    uint32_t above = 0, equal = 0;
+    each([&](int, uint32_t x) {
+        above += __popc(__ballot_sync(0xffffffffu, (x & mask) > prefix));
+        equal += __popc(__ballot_sync(0xffffffffu, (x & mask) == prefix && x));
+    });
+    if (lane == 0) {
+        warp_above[warp] = above;
+        warp_equal[warp] = equal;
     }
-    Pair slice;
-    Pair before = block_scan(mine, warp_sums, slice);
-    uint32_t out = (uint32_t)p.sinks, eq_before = 0;
+    __syncthreads();
+    uint32_t all_above = 0, all_equal = 0;
+    above = equal = 0;
+#pragma unroll
+    for (int i = 0; i < kSelWarps; ++i) {
+        above += i < warp ? warp_above[i] : 0u;
+        equal += i < warp ? warp_equal[i] : 0u;
+        all_above += warp_above[i];
+        all_equal += warp_equal[i];
+    }
     if (cluster > 1) {
         if (tid == 0) {
-            slice_counts[0] = (uint32_t)(slice & LOW);
-            slice_counts[1] = (uint32_t)(slice >> HALF);
+            slice_counts[0] = all_above;
+            slice_counts[1] = all_equal;
         }
         cluster_sync();
         for (int r = 0; r < rank; ++r) {
             const uint32_t at = mapa_shared(smem_u32(slice_counts), r);
-            const uint32_t g = ld_cluster_u32(at), q = ld_cluster_u32(at + 4);
-            out += g + min(q, left - min(left, eq_before));
-            eq_before += q;
+            above += ld_cluster_u32(at);
+            equal += ld_cluster_u32(at + 4);
         }
         cluster_sync();   // nobody leaves while its shared memory may still be read
     }
-    // Positions in index order: steps one after another, threads within a step, neighbours within a thread.
-#pragma unroll
-    for (int j = 0; j < (STEPS ? HELD : steps); ++j) {
-        if (!STEPS) load(j, key[0]);
-        Pair sum = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t x = key[STEPS ? j : 0][e] & mask;
-            if (valid(j, e)) sum += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
-        }
-        Pair all = slice;
-        if (STEPS != 1) before = block_scan(sum, warp_sums, all);   // one step: the scan above holds
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t x = key[STEPS ? j : 0][e] & mask;
-            if (!valid(j, e)) continue;
-            const uint32_t g = (uint32_t)(before & LOW), q = eq_before + (uint32_t)(before >> HALF);
-            if (x > prefix || (x == prefix && q < left)) {
-                // equal keys before this one that were taken: those of the whole row, less those of earlier steps
-                const uint32_t taken = min(q, left) - min(eq_before, left);
-                idx[out + g + taken] = s0 + j * kStep + tid * 4 + e;
-            }
-            before += x > prefix ? ABOVE : x == prefix ? EQUAL : 0;
-        }
-        const uint32_t q_after = eq_before + (uint32_t)(all >> HALF);
-        out += (uint32_t)(all & LOW) + min(q_after, left) - min(eq_before, left);
-        eq_before = q_after;
-    }
+    // Positions in index order; of the equal keys the first `left` take one.
+    uint32_t out = (uint32_t)p.sinks + above + min(equal, left);
+    const uint32_t lower = (1u << lane) - 1u;
+    each([&](int i, uint32_t x) {
+        const bool gt = (x & mask) > prefix, eq = (x & mask) == prefix && x;
+        const uint32_t g = __ballot_sync(0xffffffffu, gt), q = __ballot_sync(0xffffffffu, eq);
+        const uint32_t taken = min(equal, left), mine = min(equal + __popc(q & lower), left);
+        if (gt || (eq && equal + __popc(q & lower) < left)) idx[out + __popc(g & lower) + mine - taken] = first + i * 32;
+        equal += __popc(q);
+        out += __popc(g) + min(equal, left) - taken;
+    });
 }
 
 constexpr int kMoveThreads = 256;
@@ -367,10 +345,11 @@ cudaError_t launch_kv_evict(const EvictProblem &p, int sm_count, cudaStream_t s)
     const int rows = p.B * p.Hkv;
     // up to 8192 keys for a CTA before the row is spread over more of them
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)cluster * 4 * kStep < p.S) cluster *= 2;
+    while (cluster < kMaxCluster && (long long)cluster * 16 * kSelThreads < p.S) cluster *= 2;
     const long long per = ((long long)p.S + cluster - 1) / cluster;
-    auto select = per <= kStep ? kv_select_kernel<1> : per <= 2 * kStep ? kv_select_kernel<2>
-                : per <= 4 * kStep ? kv_select_kernel<4> : per <= 8 * kStep ? kv_select_kernel<8> : kv_select_kernel<0>;
+    auto select = per <= 4 * kSelThreads ? kv_select_kernel<4> : per <= 8 * kSelThreads ? kv_select_kernel<8>
+                : per <= 16 * kSelThreads ? kv_select_kernel<16> : per <= 32 * kSelThreads ? kv_select_kernel<32>
+                : kv_select_kernel<0>;
     cudaError_t e = launch_clustered(select, dim3((unsigned)rows * cluster), dim3(kSelThreads), 0, s, dim3(cluster, 1, 1), false,
                                      p, cluster);
     if (e != cudaSuccess) return e;
