@@ -276,17 +276,19 @@ __device__ __forceinline__ Words<N> lds_words(const unsigned char *p) {
     return r;
 }
 
-// Work is cut flat: an item is one block of query rows of one (batch, kv head), of max(1, ceil(length / TK))
-// tiles; the items lie one after another (batch, kv head, row block), and CTA c of nc takes the c-th
-// part of all tiles, whatever items it spans.  So every CTA gets the same number of tiles, in one wave,
-// for any mix of lengths.  An item inside one part is finished there; of the others a CTA holds at most
-// two pieces, the end of one that began before (slot 2c of the partial states) and the start of one that goes
-// on (slot 2c + 1).
+// Work is cut flat: an item is one block of query rows of one (batch, kv head), worth max(1, ceil(length / TK))
+// tiles and kItemCost more for what it costs besides them; the items lie one after another (batch, kv head, row
+// block), and CTA c of nc takes the c-th part of the whole, whatever items it spans.  So every CTA gets the same
+// work, in one wave, for any mix of lengths.  (Without kItemCost a CTA full of short sequences ran 60 us where
+// the average took 30: B=16 Hkv=8 Sq=4 D=64, lengths 4 .. 8192.)  An item whose tiles all lie in one part is finished
+// there; of the others a CTA holds at most two pieces, the end of one that began before (slot 2c of the partial
+// states) and the start of one that goes on (slot 2c + 1).
 struct FlatWork {
-    long long total, base;   // tiles of all items, and of the batches before b
+    long long total, base;   // units of all items, and of the batches before b
     int nc;                  // CTAs that take part
 };
 constexpr int kMinTiles = 2 * TW;   // tiles worth a CTA: two for every warp
+constexpr int kItemCost = 8;        // tiles that an item's set-up and merge take as long as
 
 __device__ __forceinline__ int item_tiles(const Kv4AttnProblem &kp, int b, int tk) {
     return max(1, (kv4_length(kp.lens, b, kp.a.Sk, kp.a.status) + tk - 1) / tk);
@@ -296,7 +298,7 @@ __device__ __forceinline__ FlatWork flat_work(const Kv4AttnProblem &kp, int tk, 
     const int lane = threadIdx.x & 31;
     long long all = 0, before = 0;
     for (int i = lane; i < kp.a.B; i += 32) {
-        const long long n = item_tiles(kp, i, tk);
+        const long long n = item_tiles(kp, i, tk) + kItemCost;
         all += n;
         before += i < b ? n : 0;
     }
@@ -308,9 +310,11 @@ __device__ __forceinline__ FlatWork flat_work(const Kv4AttnProblem &kp, int tk, 
     FlatWork f;
     f.total = all * items_per_b;
     f.base = before * items_per_b;
-    f.nc = (int)max(1LL, min((long long)grid, f.total / kMinTiles));
+    f.nc = (int)max(1LL, min((long long)grid, f.total / (kMinTiles + kItemCost)));
     return f;
 }
+// The CTA that has unit x: the last one whose part begins at or before it.
+__device__ __forceinline__ int cta_of(const FlatWork &w, long long x) { return (int)(((x + 1) * w.nc - 1) / w.total); }
 
 template <int D, int NT, bool SCORES>
 __global__ void __launch_bounds__(TW * 32, NT == 1 || D == 64 ? 2 : 1)
@@ -333,8 +337,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     }
     __syncthreads();
     const int items_per_b = p.Hkv * row_blocks;
-    int rest = 0;                     // tiles that this CTA still has to take
-    int b = 0, item = 0, tile0 = 0;   // the next piece: item of batch b, from tile0 on
+    int rest = 0;                     // units that this CTA still has to take
+    int b = 0, item = 0, unit0 = 0;   // the next piece: item of batch b, from unit0 on
     if (flat) {
         const FlatWork w = flat_work(kp, TK, items_per_b, 0, gridDim.x);
         if ((int)blockIdx.x >= w.nc) return;
@@ -342,13 +346,13 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
         rest = (int)(w.total * (blockIdx.x + 1) / w.nc - pos);
         long long at = 0;
         for (;; ++b) {
-            const long long tb = (long long)item_tiles(kp, b, TK) * items_per_b;
-            if (pos < at + tb) break;
-            at += tb;
+            const long long ub = (long long)(item_tiles(kp, b, TK) + kItemCost) * items_per_b;
+            if (pos < at + ub) break;
+            at += ub;
         }
-        const int tb = item_tiles(kp, b, TK);
-        item = (int)((pos - at) / tb);
-        tile0 = (int)((pos - at) % tb);
+        const int ui = item_tiles(kp, b, TK) + kItemCost;
+        item = (int)((pos - at) / ui);
+        unit0 = (int)((pos - at) % ui);
     } else {   // one whole item per CTA
         b = blockIdx.x / items_per_b;
         item = blockIdx.x % items_per_b;
@@ -360,9 +364,15 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     const int r0 = item % row_blocks * (8 * NT), rows = min(8 * NT, R - r0);
     const int n = kv4_length(kp.lens, b, p.Sk, p.status);
     const int nb = max(1, (n + TK - 1) / TK);
-    const int take = flat ? min(nb - tile0, rest) : nb;
-    const bool whole = take == nb;
-    const int begin = tile0 * TK, end = min(n, (tile0 + take) * TK);
+    // units [unit0, unit0 + take) of the item: its first kItemCost units hold no tiles
+    const int take = flat ? min(nb + kItemCost - unit0, rest) : nb + kItemCost;
+    const int tile0 = max(0, unit0 - kItemCost), tile1 = unit0 + take - kItemCost;
+    if (tile1 <= tile0) {   // the part ends before the item's first tile
+        rest -= take;
+        break;
+    }
+    const bool whole = tile1 - tile0 == nb;
+    const int begin = tile0 * TK, end = min(n, tile1 * TK);
     // this warp's tiles of the piece: warp, warp + 8, ...
     const int tiles = (end - begin + TK - 1) / TK;
     const int mine = tiles > warp ? (tiles - warp + TW - 1) / TW : 0;
@@ -689,7 +699,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     if (!flat) break;
     rest -= take;
     if (rest <= 0 || abort_flag) break;   // (after a timeout the copies are settled; the rest is left)
-    tile0 = 0;
+    unit0 = 0;
     if (++item == items_per_b) {
         item = 0;
         ++b;
@@ -701,60 +711,99 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
 
 // Rows of the items that several CTAs shared: a block per item, the same cut of the work as above.
 template <int D, int NT>
-__global__ void __launch_bounds__(128) kv4_combine_kernel(const Kv4AttnProblem kp, int row_blocks, int grid) {
+__global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnProblem kp, int row_blocks, int grid) {
     griddep_wait();
     constexpr int TK = TcCfg<D, NT>::TK;
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq, items_per_b = p.Hkv * row_blocks;
     const int b = blockIdx.x / items_per_b, item = blockIdx.x % items_per_b;
     const FlatWork w = flat_work(kp, TK, items_per_b, b, grid);
-    const int nb = item_tiles(kp, b, TK);
-    const long long p0 = w.base + (long long)item * nb, p1 = p0 + nb;
-    // CTA of tile x: the last one whose part begins at or before it
-    const int c0 = (int)(((p0 + 1) * w.nc - 1) / w.total), c1 = (int)((p1 * w.nc - 1) / w.total);
+    const int ui = item_tiles(kp, b, TK) + kItemCost;
+    const long long p0 = w.base + (long long)item * ui;
+    const int c0 = cta_of(w, p0 + kItemCost), c1 = cta_of(w, p0 + ui - 1);   // CTAs of the first and the last tile
     if (c0 == c1) return;
     const int r0 = item % row_blocks * (8 * NT), rows = min(8 * NT, R - r0);
-    for (int x = threadIdx.x; x < rows * (D / 4); x += 128) {
+    constexpr int KG = 8;   // pieces whose states are loaded together
+    for (int x = threadIdx.x; x < rows * (D / 4); x += blockDim.x) {
         const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
         float M = -INFINITY, L = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = c0; k <= c1; ++k) {
-            const size_t slot = 2 * (size_t)k + (k == c0 ? 1 : 0);
-            const float2 ml = kp.part_ml[slot * 8 * NT + r];
-            const float4 v = *reinterpret_cast<const float4 *>(kp.part + (slot * 8 * NT + r) * D + c);
-            const float mx = fmaxf(M, ml.x), ref = mx == -INFINITY ? 0.f : mx;
-            const float a = ex2_approx(M - ref), wt = ex2_approx(ml.x - ref);
-            A.x = fmaf(wt, v.x, A.x * a); A.y = fmaf(wt, v.y, A.y * a);
-            A.z = fmaf(wt, v.z, A.z * a); A.w = fmaf(wt, v.w, A.w * a);
-            L = fmaf(wt, ml.y, L * a);
+        for (int k0 = c0; k0 <= c1; k0 += KG) {
+            float2 ml[KG];
+            float4 v[KG];
+            float mx = M;
+#pragma unroll
+            for (int e = 0; e < KG; ++e) {
+                const size_t slot = 2 * (size_t)min(k0 + e, c1) + (k0 + e == c0 ? 1 : 0);
+                ml[e] = k0 + e <= c1 ? kp.part_ml[slot * 8 * NT + r] : make_float2(-INFINITY, 0.f);
+                v[e] = k0 + e <= c1 ? *reinterpret_cast<const float4 *>(kp.part + (slot * 8 * NT + r) * D + c)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                mx = fmaxf(mx, ml[e].x);
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx, a = ex2_approx(M - ref);
+            A.x *= a; A.y *= a; A.z *= a; A.w *= a;
+            L *= a;
             M = mx;
+#pragma unroll
+            for (int e = 0; e < KG; ++e) {
+                const float wt = ex2_approx(ml[e].x - ref);
+                A.x = fmaf(wt, v[e].x, A.x); A.y = fmaf(wt, v[e].y, A.y);
+                A.z = fmaf(wt, v[e].z, A.z); A.w = fmaf(wt, v[e].w, A.w);
+                L = fmaf(wt, ml[e].y, L);
+            }
         }
         write_row(p, b, item / row_blocks * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
     }
 }
 
-// Weights from the stored scores, once every row's log-sum-exp is known.
+// Weights from the stored scores, once every row's log-sum-exp is known: a thread sums the rows of V neighbouring
+// keys.  Bound by reading the scores once.
+template <int V>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem kp) {
-    griddep_wait();
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
     const int kvbh = blockIdx.y, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
     const int n = kv4_length(kp.lens, b, p.Sk, p.status);
-    const int key = blockIdx.x * 256 + threadIdx.x;
-    if (key >= p.Sk) return;
+    const int key = (blockIdx.x * 256 + threadIdx.x) * V;
     float *w = kp.weights + (long long)kvbh * p.Sk + key;
-    if (key >= n) {
-        if (!kp.accumulate) *w = 0.f;
-        return;
+    float sum[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum[i] = 0.f;
+    griddep_wait();
+    if (key >= p.Sk) return;
+    if (key < n) {
+        const float *lse = p.lse + ((long long)b * p.Hq + kvh * G) * p.Sq;   // the R rows of a kv head are consecutive
+        const float *sc = kp.scores + (long long)kvbh * R * p.Sk + key;
+        constexpr int RG = 4;   // rows whose scores are loaded together
+        for (int r0 = 0; r0 < R; r0 += RG) {
+            float x[RG][V], z[RG];
+#pragma unroll
+            for (int e = 0; e < RG; ++e) {
+                const int r = min(r0 + e, R - 1);
+                z[e] = lse[r];
+                const float *at = sc + (long long)r * p.Sk;
+                if (V == 4) {
+                    const float4 v = __ldcs(reinterpret_cast<const float4 *>(at));
+                    x[e][0] = v.x; x[e][V > 1 ? 1 : 0] = v.y; x[e][V > 2 ? 2 : 0] = v.z; x[e][V > 3 ? 3 : 0] = v.w;
+                } else {
+                    x[e][0] = __ldcs(at);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < RG; ++e) {
+                // a row that saw nothing, or a repeated one past the last, adds 0
+                const float off = r0 + e < R && z[e] != -INFINITY ? -z[e] * kLog2e : -INFINITY;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum[i] += ex2_approx(x[e][i] + off);
+            }
+        }
     }
-    const float *lse = p.lse + ((long long)b * p.Hq + kvh * G) * p.Sq;   // the R rows of a kv head are consecutive
-    const float *sc = kp.scores + (long long)kvbh * R * p.Sk + key;
-    float v = 0.f;
-    for (int r = 0; r < R; ++r) {
-        const float z = lse[r];
-        v += ex2_approx(sc[(long long)r * p.Sk] - (z == -INFINITY ? INFINITY : z * kLog2e));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        if (key + i >= p.Sk || (key + i >= n && kp.accumulate)) continue;
+        const float v = key + i < n ? sum[i] : 0.f;   // scores behind the length were never written
+        w[i] = kp.accumulate ? w[i] + v : v;
     }
-    *w = kp.accumulate ? *w + v : v;
 }
 
 }  // namespace
@@ -818,7 +867,7 @@ static cudaError_t launch_tc_t(Kv4AttnProblem kp, const TcPlan &t, char *partial
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.flat) return e;
     count_launches(1);
-    return launch_dependent(kv4_combine_kernel<D, NT>, dim3((unsigned)(p.B * p.Hkv * t.row_blocks)), dim3(128), 0, s, kp,
+    return launch_dependent(kv4_combine_kernel<D, NT>, dim3((unsigned)(p.B * p.Hkv * t.row_blocks)), dim3(256), 0, s, kp,
                             t.row_blocks, t.grid);
 }
 
@@ -848,8 +897,10 @@ cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_co
     }
     if (e == cudaSuccess && kp.weights && p.Sk > 0) {
         count_launches(1);
-        e = launch_dependent(kv4_weights_kernel, dim3((unsigned)((p.Sk + 255) / 256), (unsigned)(p.B * p.Hkv)), dim3(256), 0,
-                             s, kp);
+        // four keys per thread where a row of scores keeps 16-byte alignment
+        const int v = p.Sk % 4 == 0 ? 4 : 1;
+        const dim3 grid((unsigned)((p.Sk + 256 * v - 1) / (256 * v)), (unsigned)(p.B * p.Hkv));
+        e = launch_dependent(v == 4 ? kv4_weights_kernel<4> : kv4_weights_kernel<1>, grid, dim3(256), 0, s, kp);
     }
     return e;
 }
