@@ -801,11 +801,11 @@ static WeightsPath key_weights_path(const KeyWeightsProblem &w) {
     return key_weights_tc_supported(w) ? WeightsPath::TensorCore : WeightsPath::Simt;
 }
 
-static size_t key_weights_partial_bytes(const KeyWeightsProblem &w, WeightsPath path, int sm_count) {
+static size_t key_weights_partial_bytes(KeyWeightsProblem w, WeightsPath path, int sm_count) {
     if (path == WeightsPath::Rows) return 0;
     if (path == WeightsPath::TensorCore) return align256(key_weights_tc_floats(sm_count) * sizeof(float));
-    const int splits = key_weights_simt_splits(w, sm_count);
-    return splits > 1 ? align256((size_t)splits * w.B * w.Hkv * w.Sk * sizeof(float)) : 0;
+    key_weights_simt_plan(w, sm_count);
+    return w.splits > 1 ? align256((size_t)w.splits * w.B * w.Hkv * w.Sk * sizeof(float)) : 0;
 }
 
 int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, size_t *bytes) {
@@ -814,16 +814,19 @@ int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int 
     KeyWeightsProblem w;
     bool empty;
     const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
-    const int st = check_key_weights(ph, ph, static_cast<const float *>(ph), reinterpret_cast<float *>(uintptr_t(1) << 44),
-                                     dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, OSF_MASK_NONE, 0.f, w, empty);
-    if (st != OSF_OK || empty || Sq == 0) return st;
-    DeviceInfo *dev;
-    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
-    // the larger of the possible paths' needs (alignment decides the path at call time)
-    const size_t simt = key_weights_partial_bytes(w, WeightsPath::Simt, dev->sm_count);
-    const size_t tc = dtype == OSF_BF16 && (D == 64 || D == 128)
-                          ? key_weights_partial_bytes(w, WeightsPath::TensorCore, dev->sm_count) : 0;
-    *bytes = std::max(simt, tc);
+    // the larger of the possible paths' needs, over the masks (the call's mask and alignment decide then)
+    size_t need = 0;
+    for (int mask : {OSF_MASK_NONE, OSF_MASK_TOP_LEFT, OSF_MASK_BOTTOM_RIGHT}) {
+        const int st = check_key_weights(ph, ph, static_cast<const float *>(ph), reinterpret_cast<float *>(uintptr_t(1) << 44),
+                                         dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, mask, 0.f, w, empty);
+        if (st != OSF_OK || empty || Sq == 0) return st;
+        DeviceInfo *dev;
+        if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+        need = std::max(need, key_weights_partial_bytes(w, WeightsPath::Simt, dev->sm_count));
+        if (dtype == OSF_BF16 && (D == 64 || D == 128))
+            need = std::max(need, key_weights_partial_bytes(w, WeightsPath::TensorCore, dev->sm_count));
+    }
+    *bytes = need;
     return OSF_OK;
 }
 
@@ -848,7 +851,7 @@ int osf_attn_key_weights(const void *Q, const void *K, const float *lse, float *
     w.part = static_cast<float *>(workspace);
     if (path == WeightsPath::Rows) return launch_status(launch_key_weights_rows(w, dev->sm_count, s));
     if (path == WeightsPath::TensorCore) return launch_status(launch_key_weights_tc(w, dev->sm_count, s));
-    w.splits = key_weights_simt_splits(w, dev->sm_count);
+    key_weights_simt_plan(w, dev->sm_count);
     cudaError_t e = launch_key_weights_simt(w, s);
     if (e == cudaSuccess && w.splits > 1) e = launch_key_weights_reduce(w, s);
     return launch_status(e);

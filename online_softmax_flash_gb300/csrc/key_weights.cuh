@@ -14,7 +14,8 @@ struct KeyWeightsProblem {
     float scale_log2;           // scale * log2(e)
     long long q_sb, q_sh, q_ss, k_sb, k_sh, k_ss;
     int accumulate;
-    int splits;                 // parts of the rows, each with its own partial sums [splits][B * Hkv * Sk]
+    int splits;                 // most parts of a key block's rows; each has partial sums in [splits][B * Hkv * Sk]
+    long long tiles_per_part;   // row tiles of one part
     float *part;
     int *status;
 };
@@ -23,7 +24,7 @@ struct KeyWeightsProblem {
 __device__ __forceinline__ float row_offset(float lse) { return lse == -INFINITY ? -INFINITY : -lse * kLog2e; }
 
 // CUDA-core kernel: any type, head dimension and strides.
-int key_weights_simt_splits(const KeyWeightsProblem &p, int sm_count);
+void key_weights_simt_plan(KeyWeightsProblem &p, int sm_count);   // sets splits and tiles_per_part
 cudaError_t launch_key_weights_simt(const KeyWeightsProblem &p, cudaStream_t s);
 // Tensor-core kernels (bf16, D 64 or 128): a few rows per kv head, and any number of them.
 bool key_weights_rows_supported(const KeyWeightsProblem &p);

@@ -141,6 +141,17 @@ def test_large_and_infinite_values(osf):
     assert np.all(got[want > 1.01 * far] == np.inf) and np.all(got[want < 0.99 * far] < np.inf)
 
 
+@pytest.mark.parametrize("dtype,D", [("f32", 64), ("f32", 40), ("bf16", 96)])
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk", [(1, 3, 1, 700, 700), (1, 2, 2, 65, 3000), (2, 4, 1, 900, 130), (1, 1, 1, 2500, 64), (1, 5, 1, 3, 2000)])
+def test_cuda_core_path_row_parts(osf, dtype, D, B, Hq, Hkv, Sq, Sk):
+    """Rows in several parts, key blocks that few or no rows see, tiles that cross heads."""
+    for mask in ("none", "top_left", "bottom_right"):
+        q, k = qk(B, Hq, Hkv, Sq, Sk, D, dtype, Sq + Sk)
+        n = osf.osf_attn_key_weights_workspace_bytes(osf.OSF_F32 if dtype == "f32" else osf.OSF_BF16, B, Hq, Hkv, Sq, Sk, D)
+        assert n == osf.osf_attn_key_weights_workspace_bytes(osf.OSF_F32 if dtype == "f32" else osf.OSF_BF16, B, Hq, Hkv, Sq, Sk, D)
+        check(osf, q, k, mask)
+
+
 def test_no_rows(osf):
     q, k = torch.empty(1, 2, 0, 64, device="cuda"), torch.randn(1, 2, 9, 64, device="cuda")
     w = torch.ones(1, 2, 9, device="cuda")
