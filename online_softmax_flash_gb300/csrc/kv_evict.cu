@@ -8,8 +8,8 @@
 // digits chosen so far, and take the digit in which the k-th largest lies.  A fourth pass writes the
 // indices of the keys above the threshold and the lowest-indexed of the equal ones.  Counts are
 // integers, so the result does not depend on the order of the atomics.
-// One (batch, kv head) is a cluster of up to 8 CTAs, each holding a slice of the keys, in registers while a
-// slice has at most 16384 (a pass then costs no memory latency; longer ones are read again).  The digit counts
+// One (batch, kv head) is a cluster of up to 8 CTAs, each holding a slice of the keys, in shared memory while a
+// slice has at most 49152 (longer ones are read again in every pass).  The digit counts
 // are summed, and the output offsets of the slices found, through distributed shared memory.
 //
 // Move: one launch for the cache arrays and the weights.  Rows are copied through registers in 16-byte pieces
@@ -25,10 +25,8 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSelThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kMaxCluster = 8;
-constexpr int kSelWarps = kSelThreads / 32;
 
 __device__ __forceinline__ int valid_length(const EvictProblem &p, int b) {
     if (!p.lens) return p.S;
@@ -48,15 +46,15 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
     return v;
 }
 
-// 16 bytes of shared memory of this CTA or another of the cluster.
-__device__ __forceinline__ uint4 ld_cluster_v4(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+// 8 bytes of shared memory of this CTA or another of the cluster.
+__device__ __forceinline__ uint2 ld_cluster_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 
-// Exclusive prefix sum over the block (two barriers).
+// Exclusive prefix sum over a block of THREADS (two barriers).
+template <int THREADS>
 __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t x = v;
@@ -67,9 +65,10 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums) 
     }
     if (lane == 31) warp_sums[warp] = x;
     __syncthreads();
-    uint32_t s = lane < kSelWarps ? warp_sums[lane] : 0u;   // every warp scans the warps' sums
+    constexpr int WARPS = THREADS / 32;
+    uint32_t s = lane < WARPS ? warp_sums[lane] : 0u;   // every warp scans the warps' sums
 #pragma unroll
-    for (int o = 1; o < kSelWarps; o <<= 1) {
+    for (int o = 1; o < WARPS; o <<= 1) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
@@ -79,14 +78,16 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *warp_sums) 
 }
 
 // A warp owns a run of neighbouring keys of its CTA's slice, 32 at a time, so that positions within it come from
-// ballots.  KPT: keys per thread, held in registers; 0: any number, read again in every pass.  Places behind the
-// slice hold 0, below every key: fewer keys are kept than there are, so none of them is ever chosen.
-template <int KPT>
-__global__ void __launch_bounds__(kSelThreads, KPT > 16 ? 1 : 2)
+// ballots.  HELD: the slice's keys stay in shared memory; else they are read again in every pass.  Places behind
+// the slice hold 0, below every key: fewer keys are kept than there are, so none of them is ever chosen.
+template <bool HELD, int THREADS>
+__global__ void __launch_bounds__(THREADS)
 kv_select_kernel(const EvictProblem p, int cluster) {
+    constexpr int WARPS = THREADS / 32;
+    extern __shared__ uint32_t held[];   // [groups][THREADS]
     __shared__ __align__(16) uint32_t hist[kBins];
-    __shared__ uint32_t digit_sums[kSelWarps];
-    __shared__ uint32_t warp_above[kSelWarps], warp_equal[kSelWarps];
+    __shared__ uint32_t digit_sums[WARPS];
+    __shared__ uint32_t warp_above[WARPS], warp_equal[WARPS];
     __shared__ uint32_t sh_bin, sh_above, sh_count;
     __shared__ uint32_t slice_counts[2];   // of this slice: keys above the threshold, keys equal to it
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -96,7 +97,7 @@ kv_select_kernel(const EvictProblem p, int cluster) {
     int *idx = p.idx + (long long)row * p.budget;
     if (rank == 0 && tid == 0 && p.lens && (p.lens[b] < 0 || p.lens[b] > p.S)) atomicExch(p.status, (int)OSF_ERR_INVALID);
     if (n <= p.budget) {   // everything stays (uniform over the cluster)
-        for (int i = rank * kSelThreads + tid; i < p.budget; i += cluster * kSelThreads) idx[i] = i < n ? i : -1;
+        for (int i = rank * THREADS + tid; i < p.budget; i += cluster * THREADS) idx[i] = i < n ? i : -1;
         return;
     }
     const int lo = p.sinks, hi = n - p.recent;           // candidates: n > budget >= sinks + recent
@@ -104,35 +105,28 @@ kv_select_kernel(const EvictProblem p, int cluster) {
     // this CTA's slice of the candidates, this warp's run of it
     const int per = (hi - lo + cluster - 1) / cluster;
     const int s1 = min(hi, lo + (rank + 1) * per);
-    const int groups = KPT ? KPT : ((per + kSelWarps - 1) / kSelWarps + 31) / 32;   // of 32 keys
+    const int groups = (per + THREADS - 1) / THREADS;   // of 32 keys
     const int first = lo + rank * per + warp * groups * 32 + lane;
     const float *w = p.w + (long long)row * p.S;
-    uint32_t key[KPT ? KPT : 1];
-    // unconditional loads (a place behind the slice reads its last key), so that all of a thread's are in flight
-    auto load = [&](int i) { return w[max(0, min(first + i * 32, s1 - 1))]; };
-    auto key_of = [&](int i, float v) { return first + i * 32 < s1 ? order_key(v) : 0u; };
-    if (KPT) {
-        float v[KPT ? KPT : 1];
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) v[i] = load(i);
-#pragma unroll
-        for (int i = 0; i < KPT; ++i) key[i] = key_of(i, v[i]);
+    auto key_of = [&](int i) {   // the load is unconditional, so that several are in flight
+        const float v = w[max(0, min(first + i * 32, s1 - 1))];
+        return first + i * 32 < s1 ? order_key(v) : 0u;
+    };
+    if (HELD) {
+#pragma unroll 8
+        for (int i = 0; i < groups; ++i) held[i * THREADS + tid] = key_of(i);
     }
-    for (int i = rank * kSelThreads + tid; i < p.sinks; i += cluster * kSelThreads) idx[i] = i;
-    for (int i = rank * kSelThreads + tid; i < p.recent; i += cluster * kSelThreads) idx[p.budget - p.recent + i] = hi + i;
+    for (int i = rank * THREADS + tid; i < p.sinks; i += cluster * THREADS) idx[i] = i;
+    for (int i = rank * THREADS + tid; i < p.recent; i += cluster * THREADS) idx[p.budget - p.recent + i] = hi + i;
     if (k == 0) return;
     // apply f to every group's key of this lane, in order
     auto each = [&](auto f) {
-        if (KPT) {
-#pragma unroll
-            for (int i = 0; i < KPT; ++i) f(i, key[i]);
-        } else {
-            for (int i = 0; i < groups; ++i) f(i, key_of(i, load(i)));
-        }
+#pragma unroll 4
+        for (int i = 0; i < groups; ++i) f(i, HELD ? held[i * THREADS + tid] : key_of(i));
     };
 
     uint32_t prefix = 0, mask = 0, left = (uint32_t)k;   // left: still to take among keys matching prefix
-    for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
 #pragma unroll 1
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
@@ -143,21 +137,28 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         });
         if (cluster > 1) cluster_sync();
         else __syncthreads();
-        // thread t owns four digits, counted from the top, so a prefix sum gives the keys above; the counts of
-        // all ranks are read before any is used
-        constexpr int OWN = 4;
-        static_assert(kBins == OWN * kSelThreads, "a thread owns four digits");
+        // thread t owns OWN digits, counted from the top, so a prefix sum gives the keys above; the counts of all
+        // ranks are read before any is used
+        constexpr int OWN = kBins / THREADS;
         const uint32_t mine_at = smem_u32(&hist[kBins - OWN * (tid + 1)]);
-        uint4 part[kMaxCluster];
+        uint2 part[kMaxCluster][OWN / 2];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r)
-            part[r] = r < cluster ? ld_cluster_v4(cluster > 1 ? mapa_shared(mine_at, r) : mine_at) : make_uint4(0, 0, 0, 0);
-        uint32_t c[OWN] = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < kMaxCluster; ++r) {
-            c[0] += part[r].w; c[1] += part[r].z; c[2] += part[r].y; c[3] += part[r].x;
+            for (int e = 0; e < OWN / 2; ++e)
+                part[r][e] = r < cluster ? ld_cluster_v2((cluster > 1 ? mapa_shared(mine_at, r) : mine_at) + 8 * e) : make_uint2(0, 0);
+        uint32_t c[OWN], sum = 0;
+#pragma unroll
+        for (int e = 0; e < OWN; ++e) {   // digit kBins - 1 - (OWN tid + e)
+            c[e] = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                const uint2 v = part[r][(OWN - 1 - e) / 2];
+                c[e] += (OWN - 1 - e) & 1 ? v.y : v.x;
+            }
+            sum += c[e];
         }
-        uint32_t above = block_scan(c[0] + c[1] + c[2] + c[3], digit_sums);
+        uint32_t above = block_scan<THREADS>(sum, digit_sums);
 #pragma unroll
         for (int e = 0; e < OWN; ++e) {
             if (above < left && left <= above + c[e]) {
@@ -173,7 +174,7 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         mask |= (digits - 1) << shift;
         left -= sh_above;
         if (left == sh_count) break;   // every key with this prefix is taken (uniform over the cluster)
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+        for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
     }
     // kept: (key & mask) > prefix, and the first `left` of those equal to it.  Of both, the number before each warp:
     uint32_t above = 0, equal = 0;
@@ -189,7 +190,7 @@ kv_select_kernel(const EvictProblem p, int cluster) {
     uint32_t all_above = 0, all_equal = 0;
     above = equal = 0;
 #pragma unroll
-    for (int i = 0; i < kSelWarps; ++i) {
+    for (int i = 0; i < WARPS; ++i) {
         above += i < warp ? warp_above[i] : 0u;
         equal += i < warp ? warp_equal[i] : 0u;
         all_above += warp_above[i];
@@ -343,15 +344,25 @@ __global__ void __launch_bounds__(kMoveThreads) kv_move_kernel(const EvictProble
 
 cudaError_t launch_kv_evict(const EvictProblem &p, int sm_count, cudaStream_t s) {
     const int rows = p.B * p.Hkv;
-    // up to 8192 keys for a CTA before the row is spread over more of them
+    // CTAs of a row: what its keys need of shared memory, and up to four while the GPU has room for them and each
+    // gets 2048 keys.  (16 rows of 131072 keys: 35 us with eight, clusters of which the GPU cannot place all at
+    // once, 29 us with four.)  Up to 4096 keys for a CTA, half the threads meet at its barriers: 7.5 us against
+    // 8.6 us for 8 rows of 1237.
+    constexpr int kHeldKeys = 48 * 1024;
     int cluster = 1;
-    while (cluster < kMaxCluster && (long long)cluster * 16 * kSelThreads < p.S) cluster *= 2;
+    while (cluster < kMaxCluster && ((long long)cluster * kHeldKeys < p.S ||
+                                     (cluster < 4 && rows * cluster * 2 <= sm_count && cluster * 4096 <= p.S)))
+        cluster *= 2;
     const long long per = ((long long)p.S + cluster - 1) / cluster;
-    auto select = per <= 4 * kSelThreads ? kv_select_kernel<4> : per <= 8 * kSelThreads ? kv_select_kernel<8>
-                : per <= 16 * kSelThreads ? kv_select_kernel<16> : per <= 32 * kSelThreads ? kv_select_kernel<32>
-                : kv_select_kernel<0>;
-    cudaError_t e = launch_clustered(select, dim3((unsigned)rows * cluster), dim3(kSelThreads), 0, s, dim3(cluster, 1, 1), false,
-                                     p, cluster);
+    const int threads = per <= 4096 ? 512 : 1024;
+    const long long keys = (per + threads - 1) / threads * threads;
+    const bool held = keys <= kHeldKeys;
+    auto select = threads == 512 ? kv_select_kernel<true, 512> : held ? kv_select_kernel<true, 1024> : kv_select_kernel<false, 1024>;
+    const size_t smem = held ? (size_t)keys * sizeof(uint32_t) : 0;
+    cudaError_t e = set_max_dynamic_smem((const void *)select, (int)smem);
+    if (e != cudaSuccess) return e;
+    e = launch_clustered(select, dim3((unsigned)rows * cluster), dim3((unsigned)threads), smem, s, dim3(cluster, 1, 1), false, p,
+                         cluster);
     if (e != cudaSuccess) return e;
     // blocks along a row's pieces: all that the work can use, about sixteen to an SM over the grid; in place, a
     // block per 64 bytes of the row

@@ -76,6 +76,12 @@ def test_selection_over_several_slices(osf, kind, S):
     check(osf, weights(1, 2, S, S, kind), S // 3, 4, 1000, row=(torch.uint8, 16), two=False)
 
 
+def test_selection_longer_than_the_slices_hold(osf):
+    """More keys than eight CTAs keep in shared memory: they are read again in every pass."""
+    for kind in ("skewed", "ties"):
+        check(osf, weights(1, 1, 500003, 12, kind), 200001, 3, 777, row=(torch.uint8, 4), two=False)
+
+
 def test_ragged_lengths(osf):
     lens = [0, 1, 63, 64, 65, 500, 1000]
     for in_place in (False, True):
