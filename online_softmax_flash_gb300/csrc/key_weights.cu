@@ -9,7 +9,7 @@
 // splits.  A CTA holds 64 keys of one kv head in shared memory and walks the kv head's G * Sq query rows in
 // tiles of 64 (of 16 where there are no more: a decode step); a thread computes 4 (1) rows x 4 keys.  The next 32 channels of
 // the rows are in flight while these are multiplied.  Bound by FMA issue: B=1 Hq=8 Hkv=2 S=1001 D=64 float32,
-// causal, 0.51 GFLOP, NNN us.  Rows that see none of the keys are left out, and the others cut into parts of
+// causal, 0.51 GFLOP, 33 us with the join.  Rows that see none of the keys are left out, and the others cut into parts of
 // `tiles_per_part` tiles, so that the key blocks of a causal problem, whose row counts differ, give even parts.
 #include "key_weights.cuh"
 
@@ -99,7 +99,7 @@ key_weights_simt_kernel(const KeyWeightsProblem p, int q_vec, int k_vec) {
             const unsigned x = i0 + tid;
             const int h = h0 + (int)(x / Vu), i = v0 + (int)(x % Vu);
             off[tid] = h < G ? row_offset(p.lse[((long long)b * p.Hq + kvh * G + h) * p.Sq + i]) : -INFINITY;
-            lim[tid] = h >= G ? 0 : p.causal ? (int)min((long long)p.Sk, (long long)i + p.causal_off + 1) : p.Sk;
+            lim[tid] = off[tid] == -INFINITY ? 0 : p.causal ? (int)min((long long)p.Sk, (long long)i + p.causal_off + 1) : p.Sk;
         }
         const bool loads = lr < TR;
         const unsigned y = i0 + lr;

@@ -11,10 +11,16 @@
 // 143 us for the B=2 Hq=32 S=4096 D=128 causal prompt, 8 of 16 199 us.)
 //
 // A CTA holds 256 keys (two A tiles, so that a query tile from L2 feeds two products) and walks the query
-// tiles that see them, for the G heads of the group.  Warp roles (384 threads): warp 0 issues the TMA
-// loads, warps 1 and 3 the MMAs of key tile 0 and 1, warp 2 fills a ring of row offsets (-lse * log2 e, -inf for rows past the end);
-// warps 4-7 sum key tile 0, warps 8-11 key tile 1, each a TMEM lane quarter.  Score buffers are double
-// (TMEM: 2 key tiles x 2 buffers x 128 columns), so the products of a step run under the sums of the last.
+// tiles that see them, for the G heads of the group.  Warp roles (640 threads): warp 0 issues the TMA
+// loads, warps 1 and 3 the MMAs of key tile 0 and 1 (one issuer for both: 140 us against 120 us for that prompt,
+// since it waits for the slower of the two), warp 2 fills a ring of row offsets (-lse * log2 e, -inf for rows past
+// the end); warps 4-11 sum key tile 0, warps 12-19 key tile 1: a warp has a TMEM lane quarter and every other step.
+// Score buffers are double (TMEM: 2 key tiles x 2 buffers x 128 columns), one to a parity, so the products of a
+// step run under the sums of the last.
+//
+// The 1.1e9 exponentials of that prompt take 70 us of the special-function units, the kernel 120 us (0.58 of that
+// rate): a summing warp issues about two other instructions per exponential pair (the packed multiply-add and add),
+// and waits out the TMEM loads and barriers of a tile.
 //
 // Work is cut flat: an item is 256 keys of one (batch, kv head), of (heads x query tiles that see them)
 // steps; CTA c takes the c-th part of all steps.  Causal items shrink along the keys, yet every CTA gets
@@ -143,9 +149,9 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &
 // One key's terms of a score tile: 128 TMEM columns against the offsets of their rows.  The next 32 columns
 // load while these are summed; `sempty` is told once the last are in registers.  The 128 terms are added
 // among themselves, so the long sum gets one rounding per tile.
+// MASK: columns below qmin, and those whose offset is -inf, add nothing whatever their score (a NaN as well).
 template <bool MASK>
-__device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_t c2, int qmin, int qmax, uint32_t sempty,
-                                          int lane) {
+__device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_t c2, int qmin, uint32_t sempty, int lane) {
     uint64_t acc[2] = {0, 0};
     uint32_t s[2][32];
     tmem_ld32(taddr, s[0]);
@@ -168,10 +174,11 @@ __device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_
                 const int i = k + 2 * e;
                 uint64_t v = ex2_pair(f2_fma(f2_pack(__uint_as_float(s[ch & 1][i]), __uint_as_float(s[ch & 1][i + 1])), c2, o[e]));
                 if (MASK) {
-                    float a, b;
+                    float a, b, oa, ob;
                     f2_unpack(v, a, b);
-                    v = f2_pack(32 * ch + i >= qmin && 32 * ch + i < qmax ? a : 0.f,
-                                32 * ch + i + 1 >= qmin && 32 * ch + i + 1 < qmax ? b : 0.f);
+                    f2_unpack(o[e], oa, ob);
+                    v = f2_pack(32 * ch + i >= qmin && oa != -INFINITY ? a : 0.f,
+                                32 * ch + i + 1 >= qmin && ob != -INFINITY ? b : 0.f);
                 }
                 acc[e] = f2_add(acc[e], v);
             }
@@ -192,6 +199,7 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
     __shared__ float other[2][TB];        // sums of the odd steps
+    __shared__ int holes[TSTAGES];        // an offset of the table is -inf
     __shared__ volatile int failed[2];    // a summing warp of the key tile gave up
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -318,12 +326,16 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const float *lse = p.lse + ((long long)b * p.Hq + kvh * w.G + at.h) * p.Sq;
+                bool hole = false;
 #pragma unroll
                 for (int i = 0; i < TB / 32; ++i) {
                     const int r = lane + 32 * i, q = at.qt * TB + r;
                     const float o = q < p.Sq ? row_offset(lse[q]) : -INFINITY;
-                        tab[st * TB + r] = o;
+                    tab[st * TB + r] = o;
+                    hole |= o == -INFINITY;
                 }
+                hole = __any_sync(0xffffffffu, hole);
+                if (lane == 0) holes[st] = hole;
                 mbar_arrive(smem_u32(&bars.t_full[st]));
             }
             pos += c.u1 - c.u0;
@@ -342,11 +354,9 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
             const Piece c = piece_at(w, pos, pos1);
             const int key0 = c.kb * 2 * TB + kt * TB, key = key0 + q4 * 32 + lane;
             const int q_first = (int)w.first_tile(c.kb);
-            // steps of the item from which on: the key tile is seen; every row of a tile sees all keys of this
-            // warp; the tile is the last one, where rows may be missing
+            // steps of the item from which on: the key tile is seen; every row of a tile sees all keys of this warp
             const int u_see = first_step(c, kt);
             const int u_full = w.causal ? tiles_before((long long)key0 + q4 * 32 + 31 - p.causal_off, q_first) * w.G : 0;
-            const int u_last = p.Sq % TB ? (w.nqt - 1 - q_first) * w.G : INT_MAX;
             float total = 0.f;
             int n = n0 + ((n0 ^ odd) & 1);
             for (int u = c.u0 + (n - n0); u < c.u1; u += 2, n += 2) {
@@ -358,14 +368,13 @@ key_weights_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_const
                     if (!ok) break;
                     phase ^= 1;
                     tc_fence_after();
-                    if (u >= u_full && u < u_last) {
-                        total += sum_tile<false>(taddr, toff0 + st * (TB * 4), c2, 0, 0, sempty, lane);
+                    if (u >= u_full && !holes[st]) {
+                        total += sum_tile<false>(taddr, toff0 + st * (TB * 4), c2, 0, sempty, lane);
                     } else {
-                        // columns below qmin are rows that do not see this key, those from qmax on rows past the last (a
-                        // NaN key would get through their offset of -inf)
+                        // columns below qmin are rows that do not see this key
                         const int q0 = (q_first + u / w.G) * TB;
                         const int qmin = w.causal ? (int)max(0LL, min((long long)TB, (long long)key - p.causal_off - q0)) : 0;
-                        total += sum_tile<true>(taddr, toff0 + st * (TB * 4), c2, qmin, p.Sq - q0, sempty, lane);
+                        total += sum_tile<true>(taddr, toff0 + st * (TB * 4), c2, qmin, sempty, lane);
                     }
                 } else {
                     ok = __all_sync(0xffffffffu, ok);
@@ -514,7 +523,7 @@ key_weights_rows_kernel(const KeyWeightsProblem p, int q_vec) {
         for (int c = 0; c < 2; ++c) {
             const int col = nt * 8 + 2 * t + c;
             off[nt][c] = col < R ? row_offset(p.lse[((long long)b * p.Hq + kvh * G + col / p.Sq) * p.Sq + col % p.Sq]) : -INFINITY;
-            lim[nt][c] = col >= R ? 0 : p.causal ? max(0, min(p.Sk, col % p.Sq + p.causal_off + 1)) : p.Sk;
+            lim[nt][c] = col >= R || off[nt][c] == -INFINITY ? 0 : p.causal ? max(0, min(p.Sk, col % p.Sq + p.causal_off + 1)) : p.Sk;
         }
     }
     float *W = p.w + (long long)kvbh * p.Sk;

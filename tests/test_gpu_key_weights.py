@@ -108,6 +108,21 @@ def test_rows_that_see_nothing_or_have_no_lse(osf):
     assert bool((osf.osf_attn_key_weights(q, k, lse) == 0).all())
 
 
+@pytest.mark.parametrize("dtype,Sq", [("bf16", 1), ("bf16", 4), ("bf16", 300), ("f32", 4), ("f32", 300)])
+def test_rows_without_an_lse_may_hold_anything(osf, dtype, Sq):
+    """Padding rows: lse = -inf, and NaN or infinite queries."""
+    for mask in ("none", "bottom_right"):
+        q, k = qk(1, 4, 2, Sq, 500, 64, dtype, 17)
+        lse = torch.full((1, 4, Sq), 7.0, device="cuda")
+        lse[0, 1] = float("-inf")
+        lse[0, 2:, Sq // 2 + 1:] = float("-inf")
+        clean = osf.osf_attn_key_weights(q, k, lse, mask=mask)
+        check(osf, q, k, mask, lse=lse)
+        q[0, 1, 0] = float("nan")
+        q[0, 2:, Sq // 2 + 1:] = float("inf")
+        assert torch.equal(osf.osf_attn_key_weights(q, k, lse, mask=mask), clean)
+
+
 def test_strides(osf):
     B, Hq, Hkv, Sq, Sk, D = 2, 4, 2, 150, 260, 128
     x = bf16_tensor(si.qkv((B, Sq, Hq, D + 8), (B, Sk, Hkv, D + 8), seed=8, dtype="bf16")[0])
