@@ -111,13 +111,13 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
         const int cnt = min(32, end - k0);
         for (int kk = 0; kk < cnt; ++kk) {
             float pk[RB];
-            float any = 0.f;
+            bool any = false;   // a NaN weight counts
 #pragma unroll
             for (int r = 0; r < RB; ++r) {
                 pk[r] = __shfl_sync(0xffffffffu, pr[r], kk);
-                any = fmaxf(any, pk[r]);
+                any |= pk[r] != 0.f;
             }
-            if (any == 0.f) continue;   // no row of this CTA sees the key
+            if (!any) continue;   // no row of this CTA sees the key
             const unsigned char *row = head + (long long)(k0 + kk) * rec;
             const uint32_t *codes = reinterpret_cast<const uint32_t *>(row + p.D / 2);
             const uint32_t *pairs = reinterpret_cast<const uint32_t *>(row + p.D + p.D / 8);
@@ -344,11 +344,24 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
         if ((int)blockIdx.x >= w.nc) return;
         const long long pos = w.total * blockIdx.x / w.nc;
         rest = (int)(w.total * (blockIdx.x + 1) / w.nc - pos);
-        long long at = 0;
-        for (;; ++b) {
-            const long long ub = (long long)(item_tiles(kp, b, TK) + kItemCost) * items_per_b;
-            if (pos < at + ub) break;
-            at += ub;
+        long long at = 0;   // units before batch b: 32 batches at a time, a lane each
+        for (int b0 = 0;; b0 += 32) {
+            const int bi = b0 + lane;
+            const long long ub = bi < p.B ? (long long)(item_tiles(kp, bi, TK) + kItemCost) * items_per_b : 0;
+            long long upto = ub;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            const uint32_t past = __ballot_sync(0xffffffffu, pos < at + upto);
+            if (past) {
+                const int f = __ffs(past) - 1;
+                b = b0 + f;
+                at += __shfl_sync(0xffffffffu, upto - ub, f);
+                break;
+            }
+            at += __shfl_sync(0xffffffffu, upto, 31);
         }
         const int ui = item_tiles(kp, b, TK) + kItemCost;
         item = (int)((pos - at) / ui);
@@ -548,7 +561,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[nt][e] *= f[nt][e & 1];
-            if (k0 + sub * 16 + 16 > lim_all) {
+            const bool masked = k0 + sub * 16 + 16 > lim_all;   // some row does not see some key
+            if (masked) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -612,10 +626,27 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 for (int e = 0; e < 4; ++e) pr[nt][e] = ex2_approx(y[nt][e] - m[nt][e & 1]);
                 l[nt][0] += pr[nt][0] + pr[nt][2];
                 l[nt][1] += pr[nt][1] + pr[nt][3];
+            }
+            if (!masked) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        om[nt][gi][0] = fmaf(pr[nt][0], vm[0][gi], fmaf(pr[nt][2], vm[1][gi], om[nt][gi][0]));
+                        om[nt][gi][1] = fmaf(pr[nt][1], vm[0][gi], fmaf(pr[nt][3], vm[1][gi], om[nt][gi][1]));
+                    }
+            } else {
+                // a NaN group (scale and minimum) must not reach a row that does not see its key: through the minimum it
+                // comes where the row sees it, through the scale nowhere
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    om[nt][gi][0] = fmaf(pr[nt][0], vm[0][gi], fmaf(pr[nt][2], vm[1][gi], om[nt][gi][0]));
-                    om[nt][gi][1] = fmaf(pr[nt][1], vm[0][gi], fmaf(pr[nt][3], vm[1][gi], om[nt][gi][1]));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (y[nt][e] != -INFINITY) om[nt][gi][e & 1] = fmaf(pr[nt][e], vm[e >> 1][gi], om[nt][gi][e & 1]);
+                    vs[0][gi] = vs[0][gi] == vs[0][gi] ? vs[0][gi] : 0.f;
+                    vs[1][gi] = vs[1][gi] == vs[1][gi] ? vs[1][gi] : 0.f;
                 }
             }
             const Words<NG> w0 = lds_words<NG>(tile + off_v0), w1 = lds_words<NG>(tile + off_v1);

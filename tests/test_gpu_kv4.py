@@ -261,6 +261,34 @@ def test_attention_records_behind_the_length_do_not_matter(osf):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b) and torch.equal(w[0], w[1])
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_attention_nan_records_that_the_mask_hides(osf, dtype, D):
+    """A NaN record is met by the rows that see it, and by no other row of the call."""
+    S, Sq = 700, 4
+    q, _ = rows((1, 4, Sq, D), 51, dtype)
+    clean, _ = random_cache(1, 2, S, D, 52)
+    want = osf.osf_attn_kv4(q, clean, mask="bottom_right")
+    for part in (slice(D, D + D // 8), slice(D + D // 8, D + D // 4), slice(D, None)):   # pairs of K, of V, of both
+        bad = clean.clone()
+        bad[0, :, S - 2, part] = 0xFF        # seen by rows 2 and 3
+        got = osf.osf_attn_kv4(q, bad, mask="bottom_right")
+        assert torch.equal(got[:, :, :2], want[:, :, :2])
+        assert bool(torch.isnan(got[:, :, 2:]).all())
+    bad = clean.clone()
+    bad[0, :, S - 2, D + D // 8:D + D // 8 + 4] = 0xFF   # the first group of V alone
+    got = osf.osf_attn_kv4(q, bad, mask="bottom_right")
+    assert torch.equal(got[:, :, :2], want[:, :, :2]) and torch.equal(got[..., 32:], want[..., 32:])
+    assert bool(torch.isnan(got[:, :, 2:, :32]).all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_large_ragged_batch(osf, D):
+    lens = [int(x) for x in np.random.default_rng(D).integers(0, 1501, 75)]
+    lens[:40] = [0] * 40
+    check_attention(osf, 75, 2, 1, 1, 1500, D, "bf16", lens=lens, seed=53)
+    check_attention(osf, 75, 4, 2, 2, 1500, D, "bf16", lens=lens[::-1], mask="bottom_right", seed=54, weights=False)
+
+
 def test_attention_strided_queries_and_outputs(osf):
     B, Hq, Hkv, Sq, S, D = 2, 4, 2, 3, 90, 128
     cache, _ = random_cache(B, Hkv, S, D, 11)
@@ -326,3 +354,12 @@ def test_workspace_too_small_is_refused(osf):
     with pytest.raises(osf.OsfError) as err:
         osf.osf_attn_kv4(q, cache, weights=w, workspace=torch.empty(n - 1, dtype=torch.uint8, device="cuda"))
     assert err.value.status == osf.OSF_ERR_WORKSPACE
+
+
+def test_workspace_that_is_not_aligned_is_refused(osf):
+    cache, _ = random_cache(1, 1, 4096, 128, 36)
+    q, _ = rows((1, 4, 1, 128), 37, "bf16")
+    n = osf.osf_attn_kv4_workspace_bytes(osf.OSF_BF16, 1, 4, 1, 1, 4096, 128)
+    with pytest.raises(osf.OsfError) as err:
+        osf.osf_attn_kv4(q, cache, workspace=torch.empty(n + 4, dtype=torch.uint8, device="cuda")[4:])
+    assert err.value.status == osf.OSF_ERR_INVALID
