@@ -223,11 +223,11 @@ int osf_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sk, i
  *     weights[b, g, j] (+)= sum_{h in group g} sum_{i sees j} exp(Q[b,h,i,:].K[b,g,j,:] * scale - lse[b,h,i])
  * The statistic that osf_kv_evict selects by.
  * Q: [B, Hq, Sq, D], K: [B, Hkv, Sk, D] of `dtype`; lse: contiguous float32 [B, Hq, Sq] as the
- *    forward call returned it (a row with lse = -inf adds nothing); weights: contiguous float32
- *    [B, Hkv, Sk].
+ *    forward call returned it (a row with lse = -inf adds nothing, whatever its Q holds, so padding
+ *    rows can be marked so); weights: contiguous float32 [B, Hkv, Sk].
  * strides: NULL (contiguous) or 6 element strides, Q: b, h, s  K: b, h, s (>= 0; 0 broadcasts).
  * mask, scale: as given to the forward call.  accumulate: 0 overwrites weights, else adds to them.
- * workspace: osf_attn_key_weights_workspace_bytes bytes (may be 0).
+ * workspace: osf_attn_key_weights_workspace_bytes bytes (may be 0), 16-byte aligned.
  * weights must not overlap an input -> else OSF_ERR_INVALID.  B == 0 or Sk == 0: OSF_OK, nothing
  * written; Sq == 0: weights are zeroed (accumulate == 0) or left.  B * Hkv > 65535:
  * OSF_ERR_UNSUPPORTED.  Other errors as in osf_attn_fwd_gqa_ex.  The result does not depend on the
@@ -262,7 +262,8 @@ int osf_kv4_record_bytes(int D, size_t *bytes);
  * lens[b] + n - 1 of each sequence.  lens NULL: from record 0.  counts: NULL, or the number of new
  * tokens of each sequence (0 .. n; the rows behind them are padding and are not read).  Records that
  * would fall behind S are not written, and recorded as OSF_ERR_INVALID in the device status word, as
- * are counts and lengths out of range.  No other record is touched.
+ * are counts out of range (cut to it) and a negative length (nothing of that sequence is stored).  No
+ * other record is touched.
  * strides: NULL (contiguous) or 6 element strides, K: b, h, s  V: b, h, s.
  * n == 0 or B == 0: OSF_OK.  n > S without counts, a cache that overlaps an input, NULL pointers:
  * OSF_ERR_INVALID.
@@ -289,11 +290,13 @@ int osf_kv4_read(const void *cache, void *K, void *V, int dtype, int B, int Hkv,
  * mask: OSF_MASK_NONE, or OSF_MASK_BOTTOM_RIGHT: row i sees records 0 .. i + lens[b] - Sq (the Sq
  *     rows are the sequence's last tokens).  OSF_MASK_TOP_LEFT: OSF_ERR_INVALID.
  *     A row that sees nothing gets O = 0 and lse = -inf.
- * lse: optional contiguous float32 [B, Hq, Sq].
+ * lse: optional contiguous float32 [B, Hq, Sq]; of a row with a NaN score: NaN or -inf.
  * weights: optional contiguous float32 [B, Hkv, S]: the attention weight of every record, summed over
  *     the query heads of its kv head and the Sq rows, as in osf_attn_key_weights.  accumulate 0:
  *     overwritten (0 at and behind lens[b]); else added to (at and behind lens[b] left as they are).
- * workspace: osf_attn_kv4_workspace_bytes(..., with_weights = weights != NULL) bytes.
+ * workspace: osf_attn_kv4_workspace_bytes(..., with_weights = weights != NULL) bytes, 16-byte aligned.
+ * Ranges: with bfloat16 and D 64 or 128, entries of Q from 2^104 on are taken for infinite, entries below
+ *     2^-28 of their row's largest lose low bits, and V scales below 2^-80 count as 0.
  * (Hq / Hkv) * Sq <= 32768, else OSF_ERR_UNSUPPORTED.  Outputs must not overlap one another or an
  * input -> else OSF_ERR_INVALID.  B == 0 or Sq == 0: OSF_OK, nothing written.
  */
@@ -311,7 +314,8 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
  * budget - sinks - recent with the largest weights[b, g, j] (a tie keeps the lower index; -0 equals
  * 0; a NaN weight ranks below every number).  Kept rows stay in their order.
  * src0, src1: the cache arrays [B, Hkv, S] of rows of row_bytes0 / row_bytes1 bytes (e.g. K and V
- *     with D * sizeof(element), or one array of 4-bit records); either may be NULL with its dst.
+ *     with D * sizeof(element), or one array of 4-bit records); either may be NULL with its dst, or
+ *     where S == 0.
  * dst0, dst1: [B, Hkv, S_out] rows, S_out >= budget; dst == src (with S_out == S) moves in place,
  *     any other overlap is OSF_ERR_INVALID.  Rows at and behind the new length are left as they were.
  * weights [B, Hkv, S] -> weights_out [B, Hkv, S_out]: the kept keys' weights, 0 behind them;

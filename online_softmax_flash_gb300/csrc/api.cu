@@ -749,6 +749,13 @@ int osf_softmax_rows_ex(const void *x, void *z, int x_dtype, int z_dtype, long l
     return launch_status(launch_softmax_ex(q, static_cast<float *>(workspace), (cudaStream_t)stream));
 }
 
+// A workspace of `need` bytes: large enough, and aligned for the 16-byte accesses that the kernels make to it.
+static int check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return OSF_OK;
+    if (!workspace || bytes < need) return OSF_ERR_WORKSPACE;
+    return (reinterpret_cast<uintptr_t>(workspace) & 15u) ? OSF_ERR_INVALID : OSF_OK;
+}
+
 // ------------------------------------------------------------------ weights of keys
 // Shared validation of osf_attn_key_weights; `strides`: NULL (contiguous) or Q, K x (b, h, s).
 static int check_key_weights(const void *Q, const void *K, const float *lse, float *weights, int dtype, int B, int Hq,
@@ -847,7 +854,8 @@ int osf_attn_key_weights(const void *Q, const void *K, const float *lse, float *
     w.status = dev->status;
     const WeightsPath path = key_weights_path(w);
     const size_t need = key_weights_partial_bytes(w, path, dev->sm_count);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
+    const int ws = check_workspace(workspace, workspace_bytes, need);
+    if (ws != OSF_OK) return ws;
     w.part = static_cast<float *>(workspace);
     if (path == WeightsPath::Rows) return launch_status(launch_key_weights_rows(w, dev->sm_count, s));
     if (path == WeightsPath::TensorCore) return launch_status(launch_key_weights_tc(w, dev->sm_count, s));
@@ -1009,7 +1017,8 @@ int osf_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, in
     p.status = dev->status;
     kp.accumulate = accumulate != 0;
     const size_t need = kv4_workspace(kp, dev->sm_count, weights != nullptr);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return OSF_ERR_WORKSPACE;
+    const int ws = check_workspace(workspace, workspace_bytes, need);
+    if (ws != OSF_OK) return ws;
     if (weights) {
         char *at = static_cast<char *>(workspace) + kv4_attn_partial_bytes(kp, dev->sm_count);
         if (!p.lse) p.lse = reinterpret_cast<float *>(at);
@@ -1025,7 +1034,8 @@ int osf_kv_evict(const void *src0, void *dst0, long long row_bytes0, const void 
     if (B < 0 || Hkv <= 0 || S < 0 || budget < 1 || sinks < 0 || recent < 0 || S_out < budget) return OSF_ERR_INVALID;
     if ((long long)sinks + recent > budget) return OSF_ERR_INVALID;
     if ((src0 && row_bytes0 < 1) || (src1 && row_bytes1 < 1)) return OSF_ERR_INVALID;
-    if ((src0 == nullptr) != (dst0 == nullptr) || (src1 == nullptr) != (dst1 == nullptr)) return OSF_ERR_INVALID;
+    // (an array of no keys may have no address)
+    if ((src0 && !dst0) || (!src0 && dst0 && S > 0) || (src1 && !dst1) || (!src1 && dst1 && S > 0)) return OSF_ERR_INVALID;
     if ((long long)B * Hkv > 65535 || S >= (1 << 30) || S_out >= (1 << 30)) return OSF_ERR_UNSUPPORTED;
     if ((src0 && row_bytes0 * budget >= (1LL << 31)) || (src1 && row_bytes1 * budget >= (1LL << 31))) return OSF_ERR_UNSUPPORTED;
     if (B == 0) return OSF_OK;

@@ -125,6 +125,14 @@ def test_length_out_of_range_is_cut_and_recorded(osf):
     assert osf.osf_device_status() == osf.OSF_OK
 
 
+def test_empty_cache(osf):
+    k = torch.empty(2, 3, 0, 64, device="cuda")
+    ko, vo, wo, lo, idx = osf.osf_kv_evict(k, k.clone(), torch.empty(2, 3, 0, device="cuda"), 4, sinks=1)
+    assert bool((ko == 0).all()) and bool((vo == 0).all()) and bool((wo == 0).all())
+    assert lo.tolist() == [0, 0] and bool((idx == -1).all())
+    assert osf.osf_device_status() == osf.OSF_OK
+
+
 def test_weights_alone(osf):
     """Without cache arrays the call only selects (the caller gathers by idx)."""
     w = weights(1, 2, 90, 9)
