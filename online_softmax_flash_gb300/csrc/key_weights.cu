@@ -7,10 +7,13 @@
 //
 // This file: the CUDA-core kernel for every type, head dimension and stride, and the sum over row
 // splits.  A CTA holds 64 keys of one kv head in shared memory and walks the kv head's G * Sq query rows in
-// tiles of 64 (of 16 where there are no more: a decode step); a thread computes 4 (1) rows x 4 keys.  The next 32 channels of
-// the rows are in flight while these are multiplied.  Bound by FMA issue: B=1 Hq=8 Hkv=2 S=1001 D=64 float32,
-// causal, 0.51 GFLOP, 33 us with the join.  Rows that see none of the keys are left out, and the others cut into parts of
-// `tiles_per_part` tiles, so that the key blocks of a causal problem, whose row counts differ, give even parts.
+// tiles of 64 (of 16 where there are no more: a decode step); a thread computes 4 (1) rows x 4 keys.  The next 32
+// channels of the rows are in flight while these are multiplied.  Rows that see none of the keys are left out, and
+// the others cut into parts of `tiles_per_part` tiles, so that the key blocks of a causal problem, whose row counts
+// differ, give even parts.
+// Bound by instruction issue (two 16-byte shared loads to 16 FMAs) and the latency of a part's first loads: B=1 Hq=8
+// Hkv=2 S=1001 D=64 float32, causal, 0.51 GFLOP, 27 us with the sum of the parts.  Packed pairs of FMAs, with the
+// rows' values doubled in shared memory, are bound by that memory's bandwidth: the kernel alone 32 us against 26 us.
 #include "key_weights.cuh"
 
 namespace osf {
@@ -167,16 +170,24 @@ key_weights_simt_kernel(const KeyWeightsProblem p, int q_vec, int k_vec) {
     }
 }
 
-// The parts of every key, in order.
-__global__ void __launch_bounds__(256) key_weights_reduce_kernel(const KeyWeightsProblem p, int tile_rows) {
-    griddep_wait();
+// The parts of every key: eight threads of a block share a key, each takes every eighth part, and their sums are
+// added in order.  (A thread per key: 14 us under ncu for the 63 parts of the problem above, its loads one after another.)
+constexpr int RK = 32, RT = 8;   // keys of a block, threads of a key
+__global__ void __launch_bounds__(RK * RT) key_weights_reduce_kernel(const KeyWeightsProblem p, int tile_rows) {
+    __shared__ float sums[RT][RK];
     const long long n = (long long)p.B * p.Hkv * p.Sk;
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    const int parts = parts_of(p, (int)(i % p.Sk) / TK * TK, tile_rows);
+    const int k = threadIdx.x % RK, t = threadIdx.x / RK;
+    const long long i = (long long)blockIdx.x * RK + k;
+    const int parts = i < n ? parts_of(p, (int)(i % p.Sk) / TK * TK, tile_rows) : 0;
+    griddep_wait();
     float v = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < parts; ++s) v += p.part[s * n + i];
+#pragma unroll 8
+    for (int s = t; s < parts; s += RT) v += p.part[s * n + i];
+    sums[t][k] = v;
+    __syncthreads();
+    if (t != 0 || i >= n) return;
+#pragma unroll
+    for (int e = 1; e < RT; ++e) v += sums[e][k];
     p.w[i] = p.accumulate ? p.w[i] + v : v;
 }
 
@@ -185,7 +196,8 @@ __global__ void __launch_bounds__(256) key_weights_reduce_kernel(const KeyWeight
 static int tile_rows(const KeyWeightsProblem &p) { return (long long)(p.Hq / p.Hkv) * p.Sq <= 16 ? 16 : 64; }
 
 void key_weights_simt_plan(KeyWeightsProblem &p, int sm_count) {
-    // about four CTAs to an SM over all key blocks, of equal numbers of tiles; at most 64 parts of a block
+    // at most four CTAs to an SM over all key blocks, one wave, of equal numbers of tiles (the problem above: 27 us; a
+    // little more than a wave 29 us, three to an SM 33 us); at most 64 parts of a block
     const int tr = tile_rows(p);
     const long long blocks = (p.Sk + TK - 1) / TK;
     auto tiles = [&](long long kb) {
@@ -202,7 +214,7 @@ void key_weights_simt_plan(KeyWeightsProblem &p, int sm_count) {
         all += t;
     }
     all *= (long long)p.B * p.Hkv;
-    long long per = all / (4LL * sm_count);
+    long long per = (all + 4LL * sm_count - 1) / (4LL * sm_count);
     const long long least = (most + 63) / 64;
     per = per < least ? least : per;
     p.tiles_per_part = per < 1 ? 1 : per;
@@ -234,7 +246,7 @@ cudaError_t launch_key_weights_simt(const KeyWeightsProblem &p, cudaStream_t s) 
 cudaError_t launch_key_weights_reduce(const KeyWeightsProblem &p, cudaStream_t s) {
     const long long n = (long long)p.B * p.Hkv * p.Sk;
     count_launches(1);
-    return launch_dependent(key_weights_reduce_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, p, tile_rows(p));
+    return launch_dependent(key_weights_reduce_kernel, dim3((unsigned)((n + RK - 1) / RK)), dim3(RK * RT), 0, s, p, tile_rows(p));
 }
 
 }  // namespace osf

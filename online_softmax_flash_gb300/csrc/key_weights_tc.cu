@@ -18,9 +18,9 @@
 // Score buffers are double (TMEM: 2 key tiles x 2 buffers x 128 columns), one to a parity, so the products of a
 // step run under the sums of the last.
 //
-// The 1.1e9 exponentials of that prompt take 70 us of the special-function units, the kernel 120 us (0.58 of that
-// rate): a summing warp issues about two other instructions per exponential pair (the packed multiply-add and add),
-// and waits out the TMEM loads and barriers of a tile.
+// That prompt: 117 us for the whole call, where its products take 60 us of the tensor pipe at 1.9 GHz and its 5.5e8
+// exponentials as long of the special-function units; both are busy 59 % of the time.  A score buffer waits
+// for its turn on the one, then on the other, and TMEM holds no more than these four.
 //
 // Work is cut flat: an item is 256 keys of one (batch, kv head), of (heads x query tiles that see them)
 // steps; CTA c takes the c-th part of all steps.  Causal items shrink along the keys, yet every CTA gets
@@ -146,21 +146,20 @@ __device__ __forceinline__ void lds_pairs(uint32_t addr, uint64_t &a, uint64_t &
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(addr));
 }
 
-// One key's terms of a score tile: 128 TMEM columns against the offsets of their rows.  The next 32 columns
-// load while these are summed; `sempty` is told once the last are in registers.  The 128 terms are added
-// among themselves, so the long sum gets one rounding per tile.
+// One key's terms of a score tile: 128 TMEM columns against the offsets of their rows; `sempty` is told once the
+// last are in registers.  (The SM quarter's four warps cover each other's TMEM loads: loads of the next 32
+// columns under the sums of these, 117.9 us against 116.8 us; 64 columns at once 121.5 us.)  The 128 terms are
+// added among themselves, so the long sum gets one rounding per tile.
 // MASK: columns below qmin, and those whose offset is -inf, add nothing whatever their score (a NaN as well).
 template <bool MASK>
 __device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_t c2, int qmin, uint32_t sempty, int lane) {
     uint64_t acc[2] = {0, 0};
-    uint32_t s[2][32];
-    tmem_ld32(taddr, s[0]);
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch) {
+        uint32_t s[32];
+        tmem_ld32(taddr + 32 * ch, s);
         tmem_ld_wait();
-        if (ch < 3) {
-            tmem_ld32(taddr + 32 * (ch + 1), s[(ch + 1) & 1]);
-        } else {
+        if (ch == 3) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(sempty);
@@ -172,7 +171,7 @@ __device__ __forceinline__ float sum_tile(uint32_t taddr, uint32_t toff, uint64_
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int i = k + 2 * e;
-                uint64_t v = ex2_pair(f2_fma(f2_pack(__uint_as_float(s[ch & 1][i]), __uint_as_float(s[ch & 1][i + 1])), c2, o[e]));
+                uint64_t v = ex2_pair(f2_fma(f2_pack(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), c2, o[e]));
                 if (MASK) {
                     float a, b, oa, ob;
                     f2_unpack(v, a, b);
