@@ -38,6 +38,7 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
     __shared__ float sq[RB][WS_D];
     __shared__ float sacc[GW][RB][WS_D];
     __shared__ float sm[GW][RB], sl[GW][RB];
+    griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
     const int kvbh = blockIdx.x, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
@@ -326,6 +327,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     __shared__ uint64_t full[TW][STAGES];
     __shared__ float sm_m[TW][8 * NT], sm_l[TW][8 * NT];
     __shared__ volatile int abort_flag;
+    griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t = lane & 3;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
@@ -743,7 +745,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
 // Rows of the items that several CTAs shared: a block per item, the same cut of the work as above.
 template <int D, int NT>
 __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnProblem kp, int row_blocks, int grid) {
-    griddep_wait();
+    griddep_launch();
     constexpr int TK = TcCfg<D, NT>::TK;
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq, items_per_b = p.Hkv * row_blocks;
@@ -752,6 +754,7 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnProblem k
     const int ui = item_tiles(kp, b, TK) + kItemCost;
     const long long p0 = w.base + (long long)item * ui;
     const int c0 = cta_of(w, p0 + kItemCost), c1 = cta_of(w, p0 + ui - 1);   // CTAs of the first and the last tile
+    griddep_wait();
     if (c0 == c1) return;
     const int r0 = item % row_blocks * (8 * NT), rows = min(8 * NT, R - r0);
     constexpr int KG = 8;   // pieces whose states are loaded together

@@ -71,6 +71,7 @@ key_weights_simt_kernel(const KeyWeightsProblem p, int q_vec, int k_vec) {
     __shared__ float off[TR];
     __shared__ int lim[TR];       // keys below this are visible to the row
     __shared__ float red[16][TK];
+    griddep_launch();
     const int tid = threadIdx.x, tk = tid & 15, tr = tid >> 4;
     const int kvbh = blockIdx.y, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
     const int key0 = blockIdx.x * TK;

@@ -209,6 +209,7 @@ kv_select_kernel(const EvictProblem p, int cluster) {
         }
         cluster_sync();   // nobody leaves while its shared memory may still be read
     }
+    griddep_launch();
     // Positions in index order; of the equal keys the first `left` take one.
     uint32_t out = (uint32_t)p.sinks + above + min(equal, left);
     const uint32_t lower = (1u << lane) - 1u;

@@ -21,6 +21,9 @@ constexpr int kStatusTimeout = OSF_ERR_TIMEOUT;
 // Wait until the grid this kernel was launched as a programmatic dependent of has completed and
 // its memory is visible (a no-op for a kernel launched normally).
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Once every CTA of the grid has come here, the CTAs of a programmatic dependent may be placed where there is room:
+// they run up to their griddep_wait, which still waits for the whole grid.
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float y;
