@@ -19,8 +19,12 @@
 // step run under the sums of the last.
 //
 // That prompt: 117 us for the whole call, where its products take 60 us of the tensor pipe at 1.9 GHz and its 5.5e8
-// exponentials as long of the special-function units; both are busy 59 % of the time.  A score buffer waits
-// for its turn on the one, then on the other, and TMEM holds no more than these four.
+// exponentials as long of the special-function units; both are busy 59 % of the time.  A score buffer goes round from
+// product to sum to product, with some 700 cycles of hand-off on the way even where there is nothing to compute, and
+// TMEM holds no more than these four.  (Without the exponentials the call takes 113 us, with half the products 109 us,
+// without the loads of Q 115 us.  The other way round, S = Q K^T, a row to a lane and 64 keys' sums to a thread, with
+// products of 256 columns in two buffers, needs no table of offsets and less of shared memory's bandwidth, but has only
+// two buffers to hide the hand-off: 128 us.  Eight warps that take a whole tile into registers: 141 us.)
 //
 // Work is cut flat: an item is 256 keys of one (batch, kv head), of (heads x query tiles that see them)
 // steps; CTA c takes the c-th part of all steps.  Causal items shrink along the keys, yet every CTA gets
