@@ -367,11 +367,11 @@ def osf_attn_key_weights_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, Sk, D) -> i
 
 def _view_strides(an: str, a, bn: str, b):
     """The b, h, s element strides of two [B, H, S, D] views, or None when both are contiguous."""
+    if a.dim() == b.dim() == 4 and a.is_contiguous() and b.is_contiguous():
+        return None
     for name, t in ((an, a), (bn, b)):
         if t.dim() != 4 or (t.shape[3] > 1 and t.stride(3) != 1):
             raise ValueError(f"{name} must be a 4-D [B, H, S, D] view with a contiguous last dimension")
-    if a.is_contiguous() and b.is_contiguous():
-        return None
     st = (ctypes.c_longlong * 6)(*a.stride()[:3], *b.stride()[:3])
     return ctypes.cast(st, ctypes.c_void_p)
 
@@ -403,8 +403,8 @@ def _bytes_of(ws, dev: int) -> int:
 
 def _call(name: str, dev: int, *args) -> None:
     """Run an entry point whose last argument is the stream, with ``dev`` the current device."""
-    fn = getattr(lib(), name)
-    if dev == torch.cuda.current_device():
+    fn = getattr(_lib or lib(), name)
+    if dev == torch._C._cuda_getDevice():   # a tensor on `dev` exists, so CUDA is initialised
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -415,7 +415,7 @@ def _call(name: str, dev: int, *args) -> None:
 
 def _query(dev: int, fn, *args) -> int:
     """A workspace query, with ``dev`` the current device."""
-    if dev == torch.cuda.current_device():
+    if dev == torch._C._cuda_getDevice():
         return fn(*args)
     with torch.cuda.device(dev):
         return fn(*args)
