@@ -26,7 +26,7 @@ __device__ __forceinline__ float row_offset(float lse) { return lse == -INFINITY
 // CUDA-core kernel: any type, head dimension and strides.
 void key_weights_simt_plan(KeyWeightsProblem &p, int sm_count);   // sets splits and tiles_per_part
 cudaError_t launch_key_weights_simt(const KeyWeightsProblem &p, cudaStream_t s);
-// Tensor-core kernels (bf16, D 64 or 128): a few rows per kv head, and any number of them.
+// Tensor-core kernels (bf16): a few rows per kv head (D 32, 64, 96, 128), and any number of them (D 64, 128).
 bool key_weights_rows_supported(const KeyWeightsProblem &p);
 cudaError_t launch_key_weights_rows(const KeyWeightsProblem &p, int sm_count, cudaStream_t s);
 bool key_weights_tc_supported(const KeyWeightsProblem &p);

@@ -1,9 +1,9 @@
-// Weights of keys on the tensor cores, bf16 with D 64 or 128 (the operation: key_weights.cu).
+// Weights of keys on the tensor cores, bf16 (the operation: key_weights.cu).
 //
-// Few query rows per kv head (G * Sq <= 16: a decode step): key_weights_rows_kernel, at the end of this
-// file, bound by reading K once.
+// Few query rows per kv head (G * Sq <= 16: a decode step), D 32, 64, 96 or 128: key_weights_rows_kernel, at the end
+// of this file, bound by reading K once.
 //
-// Otherwise key_weights_tc_kernel.  The score tile is taken transposed, S^T = K Q^T: a TMEM lane is then a
+// Otherwise, with D 64 or 128, key_weights_tc_kernel.  The score tile is taken transposed, S^T = K Q^T: a TMEM lane is then a
 // key and a thread owns one, so its sum over the rows stays in one register and no cross-thread reduction
 // or exchange is needed until the end.  One tcgen05 product of 128 x 128 scores costs the tensor pipe
 // D / 128 * 512 cycles, its 16384 exponentials the special-function units about as much.  (A share of the
@@ -477,7 +477,7 @@ struct KeyTile {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(RW * 32, D == 64 ? 3 : 2)
+__global__ void __launch_bounds__(RW * 32, D <= 64 ? 3 : 2)
 key_weights_rows_kernel(const KeyWeightsProblem p, int q_vec) {
     constexpr int NG = D / 32;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -570,7 +570,7 @@ template <int D, int NT>
 cudaError_t launch_rows_t(const KeyWeightsProblem &p, int sm_count, cudaStream_t s) {
     const long long items = (long long)p.B * p.Hkv, tiles = ((long long)p.Sk + 15) / 16;
     // about four waves, so the last wave's imbalance stays small; two tiles for every warp at least
-    long long parts = (4LL * sm_count * (D == 64 ? 3 : 2) + items / 2) / items;
+    long long parts = (4LL * sm_count * (D <= 64 ? 3 : 2) + items / 2) / items;
     const long long most = tiles / (2 * RW);
     parts = parts < most ? parts : most;
     parts = parts < 1 ? 1 : parts > 65535 ? 65535 : parts;
@@ -583,7 +583,7 @@ cudaError_t launch_rows_t(const KeyWeightsProblem &p, int sm_count, cudaStream_t
 }  // namespace
 
 bool key_weights_rows_supported(const KeyWeightsProblem &p) {
-    return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128) && (long long)(p.Hq / p.Hkv) * p.Sq <= 16 && aligned16(p.k) &&
+    return p.dtype == OSF_BF16 && p.D % 32 == 0 && p.D <= 128 && (long long)(p.Hq / p.Hkv) * p.Sq <= 16 && aligned16(p.k) &&
            ((p.k_sb | p.k_sh | p.k_ss) & 7) == 0;
 }
 
@@ -595,10 +595,16 @@ bool key_weights_tc_supported(const KeyWeightsProblem &p) {
 
 size_t key_weights_tc_floats(int sm_count) { return (size_t)2 * sm_count * 2 * TB; }
 
+template <int D>
+static cudaError_t launch_rows_d(const KeyWeightsProblem &p, int sm_count, cudaStream_t s) {
+    return (p.Hq / p.Hkv) * p.Sq <= 8 ? launch_rows_t<D, 1>(p, sm_count, s) : launch_rows_t<D, 2>(p, sm_count, s);
+}
+
 cudaError_t launch_key_weights_rows(const KeyWeightsProblem &p, int sm_count, cudaStream_t s) {
-    const bool few = (p.Hq / p.Hkv) * p.Sq <= 8;
-    return p.D == 64 ? (few ? launch_rows_t<64, 1>(p, sm_count, s) : launch_rows_t<64, 2>(p, sm_count, s))
-                     : (few ? launch_rows_t<128, 1>(p, sm_count, s) : launch_rows_t<128, 2>(p, sm_count, s));
+    return p.D == 32   ? launch_rows_d<32>(p, sm_count, s)
+           : p.D == 64 ? launch_rows_d<64>(p, sm_count, s)
+           : p.D == 96 ? launch_rows_d<96>(p, sm_count, s)
+                       : launch_rows_d<128>(p, sm_count, s);
 }
 
 cudaError_t launch_key_weights_tc(const KeyWeightsProblem &p, int sm_count, cudaStream_t s) {

@@ -77,6 +77,15 @@ def test_few_rows(osf, D, Hq, Hkv, Sq):
             check(osf, q, k, "bottom_right")
 
 
+@pytest.mark.parametrize("D", [32, 96])
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(1, 1, 1), (8, 1, 1), (6, 3, 4), (16, 2, 2), (10, 2, 2)])
+def test_few_rows_of_other_head_dims(osf, D, Hq, Hkv, Sq):
+    for Sk in (Sq, 17, 1111):
+        q, k = qk(2, Hq, Hkv, Sq, Sk, D, "bf16", Hq + Sq + Sk)
+        check(osf, q, k, "bottom_right")
+        check(osf, q, k, "none")
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_longer_prompts(osf, D):
     q, k = qk(1, 4, 2, 1100, 1100, D, "bf16", 3)
