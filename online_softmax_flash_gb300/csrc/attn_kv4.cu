@@ -5,9 +5,9 @@
 // sequence's own length, on the device, so a ragged batch splits every sequence evenly.
 //
 // Two kernels.  The tensor-core one (bfloat16 queries, D 64 or 128) is described where it starts.  The
-// general one takes any D that is a multiple of 32 and float32 or bfloat16 queries.  There a warp takes 32 keys
-// at a time: first a key per lane (its whole dot product with up to 4 query rows held in shared memory),
-// then a channel of each group per lane (the weights come from the other lanes by shuffle).
+// general one takes any D that is a multiple of 32 and float32 or bfloat16 queries.  There a warp copies the records of
+// 32 keys to shared memory and takes a key per lane (its whole dot product with up to 4 query rows), then a channel of
+// each group per lane.
 #include "kv4.cuh"
 #include "sm100_ptx.cuh"
 
@@ -21,6 +21,11 @@ constexpr int RB = 4;        // query rows per CTA
 constexpr int MAXG = 8;      // groups of 32 channels: D <= 256
 constexpr int WS_D = 256;
 
+template <bool B>
+struct Flag {
+    static constexpr bool value = B;
+};
+
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
@@ -31,12 +36,23 @@ __device__ __forceinline__ void part_of(int n, int unit, int split, int splits, 
     end = min(n, (int)(units * (split + 1) / splits) * unit);
 }
 
-template <typename T>
+// Words between the staged records of two keys: one more than a record, so that 32 lanes that read the same word of
+// their keys hit 32 banks.
+__host__ __device__ __forceinline__ int stage_stride(int D) { return kv4_record_bytes(D) / 4 + 1; }
+__host__ __device__ __forceinline__ int general_smem(int D) {
+    const int stage = GW * 32 * stage_stride(D) * 4, out = GW * RB * D * 4;
+    return stage > out ? stage : out;
+}
+
+// NGC: groups of a head dimension where the compiler is to know them (D up to 128), or 0.
+template <typename T, int NGC>
 __global__ void __launch_bounds__(GW * 32)
 attn_kv4_kernel(const Kv4AttnProblem kp) {
+    constexpr int MG = NGC ? NGC : MAXG;
     const AttnProblem &p = kp.a;
-    __shared__ float sq[RB][WS_D];
-    __shared__ float sacc[GW][RB][WS_D];
+    extern __shared__ __align__(16) uint32_t stage[];   // [GW][32][stride] words; at the end [GW][RB][D] outputs
+    __shared__ __align__(16) float sq[RB][WS_D];
+    __shared__ __align__(16) float sp[GW][32][RB];      // weights of a warp's 32 keys
     __shared__ float sm[GW][RB], sl[GW][RB];
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -44,9 +60,9 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
     const int kvbh = blockIdx.x, b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
     const int r0 = blockIdx.z * RB, rows = min(RB, R - r0);
     const int n = kv4_length(kp.lens, b, p.Sk, p.status);
-    const int NG = p.D / kKv4Group, rec = kv4_record_bytes(p.D);
-    for (int i = tid; i < RB * p.D; i += GW * 32) {
-        const int r = i / p.D, c = i % p.D;
+    const int NG = NGC ? NGC : p.D / kKv4Group, D = 32 * NG, rec = kv4_record_bytes(D), stride = stage_stride(D);
+    for (int i = tid; i < RB * D; i += GW * 32) {
+        const int r = i / D, c = i % D;
         float x = 0.f;
         if (r < rows) {
             const int gr = r0 + r;
@@ -55,41 +71,71 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
         sq[r][c] = x;
     }
     __syncthreads();
-    int lim[RB];
+    int lim[RB], lim_all = n;   // keys below lim_all are seen by every row
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
         const int i = (r0 + min(r, rows - 1)) % p.Sq;
         lim[r] = r >= rows ? 0 : p.causal ? min(n, max(0, n - p.Sq + i + 1)) : n;
+        if (r < rows) lim_all = min(lim_all, lim[r]);
     }
     int begin, end;
     part_of(n, 32, blockIdx.y, p.splits, begin, end);
     const unsigned char *head = kp.cache + (long long)kvbh * p.Sk * rec;
-    float m[RB], l[RB], acc[RB][MAXG];
+    uint32_t *mine = stage + warp * 32 * stride;
+    float m[RB], l[RB], acc[RB][MG];
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
         m[r] = -INFINITY;
         l[r] = 0.f;
 #pragma unroll
-        for (int g = 0; g < MAXG; ++g) acc[r][g] = 0.f;
+        for (int g = 0; g < MG; ++g) acc[r][g] = 0.f;
     }
     for (int k0 = begin + warp * 32; k0 < end; k0 += GW * 32) {
-        const int key = k0 + lane;
+        const int key = k0 + lane, cnt = min(32, end - k0);
+        // the keys' records, 8 bytes at a time (their alignment), ten loads of a lane in flight
+        const uint2 *src = reinterpret_cast<const uint2 *>(head + (long long)k0 * rec);
+        const int per = 5 * NG;   // 8-byte pieces of a record
+#pragma unroll
+        for (int c0 = 0; c0 < 5 * MG; c0 += 10) {
+            if (c0 >= per) break;
+            uint2 v[10];
+#pragma unroll
+            for (int c = 0; c < 10; ++c) {
+                const int i = (c0 + c) * 32 + lane;
+                if (i < cnt * per) v[c] = __ldcs(src + i);
+            }
+#pragma unroll
+            for (int c = 0; c < 10; ++c) {
+                const int i = (c0 + c) * 32 + lane, k = i / per;
+                if (i < cnt * per) {
+                    mine[k * stride + 2 * (i - k * per)] = v[c].x;
+                    mine[k * stride + 2 * (i - k * per) + 1] = v[c].y;
+                }
+            }
+        }
+        __syncwarp();
         float s[RB] = {0.f, 0.f, 0.f, 0.f};
         if (key < end) {
-            const unsigned char *row = head + (long long)key * rec;
-            const uint32_t *codes = reinterpret_cast<const uint32_t *>(row);
-            const uint32_t *pairs = reinterpret_cast<const uint32_t *>(row + p.D);
-            for (int g = 0; g < NG; ++g) {
-                const uint32_t sp = pairs[g];
-                const float sc = lo_bf16(sp), mn = hi_bf16(sp);
+            const uint32_t *codes = mine + lane * stride, *pairs = codes + 8 * NG;
+#pragma unroll
+            for (int g = 0; g < MG; ++g) {
+                if (g >= NG) break;
+                const uint32_t sp2 = pairs[g];
+                const float sc = lo_bf16(sp2), mn = hi_bf16(sp2);
 #pragma unroll
                 for (int t = 0; t < 4; ++t) {
                     const uint32_t w = codes[t * NG + g];
+                    float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float x = fmaf((float)((w >> (4 * e)) & 15u), sc, mn);
+                    for (int e = 0; e < 8; ++e) x[e] = fmaf((float)((w >> (4 * e)) & 15u), sc, mn);
 #pragma unroll
-                        for (int r = 0; r < RB; ++r) s[r] = fmaf(x, sq[r][g * 32 + t * 8 + e], s[r]);
+                    for (int r = 0; r < RB; ++r) {
+                        const float4 a = *reinterpret_cast<const float4 *>(&sq[r][g * 32 + t * 8]);
+                        const float4 c = *reinterpret_cast<const float4 *>(&sq[r][g * 32 + t * 8 + 4]);
+                        s[r] = fmaf(x[0], a.x, s[r]); s[r] = fmaf(x[1], a.y, s[r]);
+                        s[r] = fmaf(x[2], a.z, s[r]); s[r] = fmaf(x[3], a.w, s[r]);
+                        s[r] = fmaf(x[4], c.x, s[r]); s[r] = fmaf(x[5], c.y, s[r]);
+                        s[r] = fmaf(x[6], c.z, s[r]); s[r] = fmaf(x[7], c.w, s[r]);
                     }
                 }
             }
@@ -107,33 +153,34 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
             l[r] = l[r] * a + warp_sum(pr[r]);
             m[r] = mx;
 #pragma unroll
-            for (int g = 0; g < MAXG; ++g) acc[r][g] *= a;
+            for (int g = 0; g < MG; ++g) acc[r][g] *= a;
         }
-        const int cnt = min(32, end - k0);
-        for (int kk = 0; kk < cnt; ++kk) {
-            float pk[RB];
-            bool any = false;   // a NaN weight counts
+        *reinterpret_cast<float4 *>(sp[warp][lane]) = make_float4(pr[0], pr[1], pr[2], pr[3]);
+        __syncwarp();
+        const bool all_seen = k0 + cnt <= lim_all;
+        auto values = [&](auto masked) {
+#pragma unroll 4
+            for (int kk = 0; kk < cnt; ++kk) {
+                const float4 pk4 = *reinterpret_cast<const float4 *>(sp[warp][kk]);
+                const float pk[RB] = {pk4.x, pk4.y, pk4.z, pk4.w};
+                const uint32_t *codes = mine + kk * stride + 4 * NG, *pairs = codes + 5 * NG;
 #pragma unroll
-            for (int r = 0; r < RB; ++r) {
-                pk[r] = __shfl_sync(0xffffffffu, pr[r], kk);
-                any |= pk[r] != 0.f;
-            }
-            if (!any) continue;   // no row of this CTA sees the key
-            const unsigned char *row = head + (long long)(k0 + kk) * rec;
-            const uint32_t *codes = reinterpret_cast<const uint32_t *>(row + p.D / 2);
-            const uint32_t *pairs = reinterpret_cast<const uint32_t *>(row + p.D + p.D / 8);
+                for (int g = 0; g < MG; ++g) {
+                    if (g >= NG) break;
+                    const uint32_t sp2 = pairs[g], w = codes[(lane >> 3) * NG + g];
+                    const float x = fmaf((float)((w >> (4 * (lane & 7))) & 15u), lo_bf16(sp2), hi_bf16(sp2));
 #pragma unroll
-            for (int g = 0; g < MAXG; ++g) {
-                if (g < NG) {
-                    const uint32_t sp = pairs[g], w = codes[(lane >> 3) * NG + g];
-                    const float x = fmaf((float)((w >> (4 * (lane & 7))) & 15u), lo_bf16(sp), hi_bf16(sp));
-#pragma unroll
-                    for (int r = 0; r < RB; ++r)
-                        acc[r][g] = pk[r] != 0.f ? fmaf(pk[r], x, acc[r][g]) : acc[r][g];
+                    for (int r = 0; r < RB; ++r)   // a NaN value must not reach a row that does not see its key
+                        acc[r][g] = masked.value && pk[r] == 0.f ? acc[r][g] : fmaf(pk[r], x, acc[r][g]);
                 }
             }
-        }
+        };
+        if (all_seen) values(Flag<false>{});
+        else values(Flag<true>{});
+        __syncwarp();
     }
+    __syncthreads();   // the records are done with: their memory takes the outputs
+    float *sacc = reinterpret_cast<float *>(stage);
 #pragma unroll
     for (int r = 0; r < RB; ++r) {
         if (lane == 0) {
@@ -141,13 +188,13 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
             sl[warp][r] = l[r];
         }
 #pragma unroll
-        for (int g = 0; g < MAXG; ++g)
-            if (g < NG) sacc[warp][r][g * 32 + lane] = acc[r][g];
+        for (int g = 0; g < MG; ++g)
+            if (g < NG) sacc[(warp * RB + r) * D + g * 32 + lane] = acc[r][g];
     }
     __syncthreads();
     const long long rows_total = (long long)p.B * p.Hq * p.Sq;
-    for (int i = tid; i < rows * p.D; i += GW * 32) {
-        const int r = i / p.D, c = i % p.D, gr = r0 + r;
+    for (int i = tid; i < rows * D; i += GW * 32) {
+        const int r = i / D, c = i % D, gr = r0 + r;
         float M = -INFINITY, L = 0.f, A = 0.f;
 #pragma unroll
         for (int w = 0; w < GW; ++w) M = fmaxf(M, sm[w][r]);
@@ -155,7 +202,7 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 #pragma unroll
         for (int w = 0; w < GW; ++w) {
             const float wt = ex2_approx(sm[w][r] - ref);
-            A += wt * sacc[w][r][c];
+            A += wt * sacc[(w * RB + r) * D + c];
             L += wt * sl[w][r];
         }
         const int hq = kvh * G + gr / p.Sq, qi = gr % p.Sq;
@@ -164,7 +211,7 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
             static_cast<T *>(p.o)[o_at(p, b, hq, qi) + c] = from_f32<T>(L > 0.f || L != L ? A / L : 0.f);
             if (p.lse && c == 0) p.lse[grow] = L > 0.f ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
         } else {
-            p.part_acc[((size_t)blockIdx.y * rows_total + grow) * p.D + c] = A;
+            p.part_acc[((size_t)blockIdx.y * rows_total + grow) * D + c] = A;
             if (c == 0) {
                 p.part_m[(size_t)blockIdx.y * rows_total + grow] = M;
                 p.part_l[(size_t)blockIdx.y * rows_total + grow] = L;
@@ -905,6 +952,21 @@ static cudaError_t launch_tc_t(Kv4AttnProblem kp, const TcPlan &t, char *partial
                             t.row_blocks, t.grid);
 }
 
+template <typename T>
+static cudaError_t launch_general(const Kv4AttnProblem &kp, dim3 grid, cudaStream_t s) {
+    const int D = kp.a.D, smem = general_smem(D);
+    auto kernel = D == 96 ? attn_kv4_kernel<T, 3> : attn_kv4_kernel<T, 0>;
+    if constexpr (sizeof(T) == 4) {   // (bfloat16 with these goes to the tensor cores)
+        if (D == 64) kernel = attn_kv4_kernel<T, 2>;
+        if (D == 128) kernel = attn_kv4_kernel<T, 4>;
+    }
+    const cudaError_t e = set_max_dynamic_smem((const void *)kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, GW * 32, smem, s>>>(kp);
+    count_launches(1);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_count, cudaStream_t s) {
     Kv4AttnProblem kp = kp0;
     AttnProblem &p = kp.a;
@@ -923,10 +985,7 @@ cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_co
         p.part_m = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)));
         p.part_l = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float)));
         const dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)p.splits, (unsigned)((R + RB - 1) / RB));
-        if (p.dtype == OSF_F32) attn_kv4_kernel<float><<<grid, GW * 32, 0, s>>>(kp);
-        else attn_kv4_kernel<__nv_bfloat16><<<grid, GW * 32, 0, s>>>(kp);
-        count_launches(1);
-        e = cudaGetLastError();
+        e = p.dtype == OSF_F32 ? launch_general<float>(kp, grid, s) : launch_general<__nv_bfloat16>(kp, grid, s);
         if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     }
     if (e == cudaSuccess && kp.weights && p.Sk > 0) {
