@@ -847,8 +847,9 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnProblem k
 }
 
 // Weights from the stored scores, once every row's log-sum-exp is known: a thread sums the rows of V neighbouring
-// keys.  Bound by reading the scores once: 32 MB (B=16 Hkv=8, 16 rows, lengths 4 .. 8192) in 10 us.
-template <int V>
+// keys, RG rows' loads in flight together.  Bound by the latency of reading the scores once: 32 MB (B=16 Hkv=8, 16 rows,
+// lengths 4 .. 8192), the whole call 47 .. 49 us with RG = 8, 48 .. 50 us with 4, 54 us with 16.
+template <int V, int RG>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem kp) {
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
@@ -864,7 +865,6 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
     if (key < n) {
         const float *lse = p.lse + ((long long)b * p.Hq + kvh * G) * p.Sq;   // the R rows of a kv head are consecutive
         const float *sc = kp.scores + (long long)kvbh * R * p.Sk + key;
-        constexpr int RG = 4;   // rows whose scores are loaded together
         for (int r0 = 0; r0 < R; r0 += RG) {
             float x[RG][V], z[RG];
 #pragma unroll
@@ -1002,7 +1002,10 @@ cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_co
         // four keys per thread where a row of scores keeps 16-byte alignment
         const int v = p.Sk % 4 == 0 ? 4 : 1;
         const dim3 grid((unsigned)((p.Sk + 256 * v - 1) / (256 * v)), (unsigned)(p.B * p.Hkv));
-        e = launch_dependent(v == 4 ? kv4_weights_kernel<4> : kv4_weights_kernel<1>, grid, dim3(256), 0, s, kp);
+        // (up to four rows need no more than four loads)
+        auto kernel = R > 4 ? (v == 4 ? kv4_weights_kernel<4, 8> : kv4_weights_kernel<1, 8>)
+                            : (v == 4 ? kv4_weights_kernel<4, 4> : kv4_weights_kernel<1, 4>);
+        e = launch_dependent(kernel, grid, dim3(256), 0, s, kp);
     }
     return e;
 }
