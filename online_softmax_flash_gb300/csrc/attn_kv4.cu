@@ -900,8 +900,11 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
 
 static bool use_tc(const AttnProblem &p) { return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128); }
 
-// Launch shape of the tensor-core kernel.  Items whose tiles give every warp at most two are not cut (one
-// launch, no combine); else one wave of CTAs shares all tiles, as many as the longest possible lengths are worth.
+// Launch shape of the tensor-core kernel.  Items of few tiles are not cut: a CTA each, one launch, no combine.  Else one wave
+// of CTAs shares all tiles, as many as the longest possible lengths are worth.  Few is 48 tiles, or 64 where the items
+// fill half of the SMs (Hq=32 Hkv=8 D=128, whole against cut: 8 items of 48 tiles 11.9 against 12.9 us, 8 of 64 14.7
+// against 10.8, 64 of 64 15.0 against 14.4, 128 of 64 15.0 against 19.0, 256 of 32 14.0 against 20.5; longer items are
+// cut so that ragged batches stay even, though 256 equal ones of 128 tiles would take 40.8 against 44.4).
 struct TcPlan {
     int nt, row_blocks, flat, grid;
 };
@@ -912,7 +915,7 @@ static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
     t.row_blocks = (R + 8 * t.nt - 1) / (8 * t.nt);
     const long long items = (long long)p.B * p.Hkv * t.row_blocks, per = ((long long)p.Sk + tk - 1) / tk;
     const long long wave = (long long)sm_count * (t.nt == 1 || p.D == 64 ? 2 : 1);
-    t.flat = per > kMinTiles;
+    t.flat = per > (items * 2 > sm_count ? 64 : 48);
     const long long worth = items * per / kMinTiles;
     t.grid = (int)(!t.flat ? items : worth < wave ? (worth < 1 ? 1 : worth) : wave);
     return t;

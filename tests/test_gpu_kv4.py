@@ -281,6 +281,16 @@ def test_attention_nan_records_that_the_mask_hides(osf, dtype, D):
     assert bool(torch.isnan(got[:, :, 2:, :32]).all())
 
 
+@pytest.mark.parametrize("D,tile", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("B,Hkv", [(1, 2), (10, 8)])
+@pytest.mark.parametrize("tiles", [48, 49, 64, 65])
+def test_attention_around_the_cut_of_the_work(osf, D, tile, B, Hkv, tiles):
+    """Lengths at which items begin to be shared among CTAs, whole batches and ragged ones."""
+    S = tiles * tile
+    lens = [max(S - 7 * b * tile, 0) for b in range(B)]   # 48 tiles less 7 * 9 would be a negative length, which is recorded
+    check_attention(osf, B, 2 * Hkv, Hkv, 1, S, D, "bf16", lens=lens, seed=tiles, weights=B == 1)
+
+
 @pytest.mark.parametrize("D", [64, 128])
 def test_attention_large_ragged_batch(osf, D):
     lens = [int(x) for x in np.random.default_rng(D).integers(0, 1501, 75)]
