@@ -10,9 +10,8 @@
 // integers, so the result does not depend on the order of the atomics.
 // One (batch, kv head) is a cluster of up to 8 CTAs, each holding a slice of the keys, in shared memory while a
 // slice has at most 49152 (longer ones are read again in every pass).  (In registers, with every pass unrolled over
-// them, the code is too long for one walk through it: a whole call of 16 rows of 131072 keys 59 us against 50 us.)  The digit counts
-// are summed, and the output offsets of the slices found, through distributed shared memory.
-//
+// them, the code is too long for one walk through it: a whole call of 16 rows of 131072 keys 59 us against 50 us.)
+// The digit counts are summed, and the output offsets of the slices found, through distributed shared memory.
 // 64 rows of 32768 keys: 20 us, 16 rows of 131072: 29 us, both bound by the barriers between the passes and the integer
 // instructions of the scans (137 per 32 keys over all passes), not by the 8 MB read.
 //
