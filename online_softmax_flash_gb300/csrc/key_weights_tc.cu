@@ -49,8 +49,8 @@ constexpr int NTHREADS = (4 + NCW) * 32;
 constexpr int TSTAGES = 4;               // row-offset tables
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_RING = 8;
-// Most steps of an item that is left to one CTA without the join (B=13 Hq=16 Hkv=8 Sq=49 Sk=129, 2 steps: 8.1 us against
-// 12.7 us; B=5 Hq=40 Hkv=8 Sq=64, 5 steps: 8.8 us against 10.9 us; B=1 Hq=32 Hkv=8 Sq=256, 8 steps: 12.0 us against 10.7 us).
+// Most steps of an item that is left to one CTA without the join (B=13 Hq=16 Hkv=8 Sq=49 Sk=129, 2 steps: 8.0 us against
+// 9.1 us; B=5 Hq=40 Hkv=8 Sq=64, 5 steps: 8.7 us against 9.6 us; B=1 Hq=32 Hkv=8 Sq=256, 8 steps: 12.0 us against 8.6 us).
 constexpr int kWholeSteps = 5;
 
 template <int D>
@@ -449,7 +449,9 @@ KwPlan make_plan(const KeyWeightsProblem &p, int sm_count) {
     w.shift = p.causal_off >= 0 ? (p.causal_off + TB - 1) / TB : -(long long)(-(long long)p.causal_off / TB);
     w.per_bh = w.before(w.nkb);
     w.total = w.per_bh * p.B * p.Hkv;
-    const long long worth = w.total / 4;   // at least four steps for a CTA
+    // at least two steps for a CTA (B=1 Hq=32 Hkv=8 Sq=256: 8.6 us; four 10.6 us, eight 13.1 us; one 8.0 us, but 11.7 us
+    // against 10.2 us for B=3 Hq=40 Hkv=8 Sq=201)
+    const long long worth = w.total / 2;
     w.nc = (int)(worth < 1 ? 1 : worth < sm_count ? worth : sm_count);
     // Short items that are all alike, one to a CTA: no piece is shared, and nothing to join.
     const long long items = (long long)w.nkb * p.B * p.Hkv, steps = w.total / items;
