@@ -343,7 +343,9 @@ struct FlatWork {
     long long total, base;   // units of all items, and of the batches before b
     int nc;                  // CTAs that take part
 };
-constexpr int kMinTiles = 2 * TW;   // tiles worth a CTA: two for every warp
+// Tiles worth a CTA: one for every warp (Hq=32 Hkv=8 D=128, 4096 records: B=1 10.6 us, B=4 13.6 us; two for every warp 13.3 and
+// 16.9 us, three 13.6 and 14.2 us).
+constexpr int kMinTiles = TW;
 constexpr int kItemCost = 8;        // tiles that an item's set-up and merge take as long as
 
 __device__ __forceinline__ int item_tiles(const Kv4AttnProblem &kp, int b, int tk) {
@@ -902,9 +904,10 @@ static bool use_tc(const AttnProblem &p) { return p.dtype == OSF_BF16 && (p.D ==
 
 // Launch shape of the tensor-core kernel.  Items of few tiles are not cut: a CTA each, one launch, no combine.  Else one wave
 // of CTAs shares all tiles, as many as the longest possible lengths are worth.  Few is 48 tiles, or 64 where the items
-// fill half of the SMs (Hq=32 Hkv=8 D=128, whole against cut: 8 items of 48 tiles 11.9 against 12.9 us, 8 of 64 14.7
-// against 10.8, 64 of 64 15.0 against 14.4, 128 of 64 15.0 against 19.0, 256 of 32 14.0 against 20.5; longer items are
-// cut so that ragged batches stay even, though 256 equal ones of 128 tiles would take 40.8 against 44.4).
+// fill half of the SMs (Hq=32 Hkv=8 D=128, whole against cut: 8 items of 24 tiles 8.0 against 9.2 us, of 47 12.1 against
+// 11.7, of 64 14.7 against 9.4; 64 of 47 12.3 against 15.0, of 64 14.9 against 13.1; 128 of 64 15.0 against 19.1; 256 of 32
+// 14.0 against 20.5; longer items are cut so that ragged batches stay even, though 256 equal ones of 128 tiles would
+// take 40.8 against 44.4).
 struct TcPlan {
     int nt, row_blocks, flat, grid;
 };
