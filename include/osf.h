@@ -295,8 +295,9 @@ int osf_kv4_read(const void *cache, void *K, void *V, int dtype, int B, int Hkv,
  *     the query heads of its kv head and the Sq rows, as in osf_attn_key_weights.  accumulate 0:
  *     overwritten (0 at and behind lens[b]); else added to (at and behind lens[b] left as they are).
  * workspace: osf_attn_kv4_workspace_bytes(..., with_weights = weights != NULL) bytes, 16-byte aligned.
- * Ranges: with bfloat16 and D 64 or 128, entries of Q from 2^104 on are taken for infinite, entries below
- *     2^-28 of their row's largest lose low bits, and V scales below 2^-80 count as 0.
+ * Ranges: the sum of |V| over a sequence has to stay within float32.  With bfloat16 and D 64 or 128, entries
+ *     of Q from 2^104 on are taken for infinite, entries below 2^-28 of their row's largest lose low bits, and so do
+ *     V codes whose record's (weight over the row's largest) * scale is below 2^-100 of the call's largest V scale.
  * (Hq / Hkv) * Sq <= 32768, else OSF_ERR_UNSUPPORTED.  Outputs must not overlap one another or an
  * input -> else OSF_ERR_INVALID.  B == 0 or Sq == 0: OSF_OK, nothing written.
  */

@@ -235,18 +235,24 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // V: likewise, with scale and minimum moved to the other side of the product: for the channels of one group
 //   sum_k P_k (minimum_k + scale_k code_kc) = sum_k P_k minimum_k + sum_k (P_k scale_k) code_kc,
 // the first sum in float32 (one per row and group), the second an MMA whose B operand is P * scale in
-// float16.  One byte permute interleaves the halves of two keys' words, after which one AND makes the pair
-// (code of key k, code of key k') of a channel.  P * scale is rounded to 11 bits.  P is taken relative to a
-// reference that also holds the largest V scale seen, so that P * scale starts at 2^6 and may grow to 2^14
-// before the reference moves; products down to 2^-20 of the largest keep all 11 bits.
+// float16, 11 bits.  One byte permute interleaves the halves of two keys' words, after which one AND makes the pair
+// (code of key k, code of key k') of a channel.  P <= 1 and scale < 2^e, e following the largest V scale that the warp
+// has met, so P * scale is lifted by 2^(14 - e); what float16 cannot hold of a key is then at most 2^(e - 39).  That
+// is little beside the scales of a tile that are at least 2^(e - 6).  A tile with a smaller one (groups or keys
+// whose values lie far apart) takes P * scale in two bfloat16 parts, 16 bits, lifted by 2^109 more, against the codes
+// as bfloat16 subnormals (code * 2^-133): two MMAs, the same unit in the accumulators, all 16 bits down to P * scale =
+// 2^(e - 108) and none below 2^(e - 116).  (Always in float16: with equal weights a scale 2^-28 of the largest had 12 % error, one of 2^-32 was gone.
+// Always in two parts: the decode step below 88 us.)
 // P moves from the S^T accumulator layout to the B operand by movmatrix.
 //
 // Each warp streams its own 5120-byte runs of records through a ring of bulk copies (one instruction
 // per run, since K and V of a token are adjacent) and keeps its own softmax state; the eight states merge
-// through shared memory at the end.  The running maximum is lazy: a row keeps its reference until a
-// score passes it by 8 in base 2, so most tiles need no cross-lane reduction and no rescale.
+// through shared memory at the end.  The running maximum is lazy: a row's reference starts 4 (in base 2) above its
+// largest score and moves when a score passes it, so most tiles need no cross-lane reduction and no rescale, and
+// P <= 1.  References are whole numbers: rescaling is exact, and log2 of the denominator meets no large number whose
+// rounding it would share.
 //
-// B=8 Hq=32 Hkv=8, 32768 records of D=128: 336 MB in 69 us (4.9 TB/s of 6.8), 73.5 us with the join, against 631 us for the
+// B=8 Hq=32 Hkv=8, 32768 records of D=128: 336 MB in 72 us (4.7 TB/s of 6.8), 76 us with the join, against 631 us for the
 // general kernel's layout on the CUDA cores.  Bound by the integer pipe, busy 54 % of the time (the masks that take codes
 // out of their words run at half rate), and by the latency of a warp's chain from scores to products: 2.7
 // instructions per code, the matrix pipe busy 23 %.  tcgen05 takes its operands from shared memory or TMEM, so the
@@ -254,7 +260,9 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // flight per CTA, two CTAs to an SM; smaller slots 86 us.
 constexpr int TW = 8;                     // warps per CTA
 constexpr uint32_t kSlot = 5120;          // bytes of one ring slot: 32 records at D = 128, 64 at D = 64
-constexpr float kRowFloor = -1.7e38f;     // reference maximum of a row that has seen nothing
+constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
+constexpr float kNarrow = 0x1p-6f;            // scales this far below the largest still go through float16
+constexpr float kHeadroom = 4.f;              // what a new reference is above the largest score
 
 template <int D, int NT>
 struct TcCfg {
@@ -278,6 +286,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ float trunc_bf16(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
 // D = A B, no accumulator.
 __device__ __forceinline__ void mma_bf16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -297,6 +311,11 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
+// Two values as the sum of two bfloat16 pairs: 16 bits of each.
+__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t &hi, uint32_t &lo) {
+    hi = pack_bf16x2(a, b);
+    lo = pack_bf16x2(a - lo_bf16(hi), b - hi_bf16(hi));
+}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -310,7 +329,7 @@ __device__ __forceinline__ void write_row(const AttnProblem &p, int b, int hq, i
     o[0] = __float2bfloat16_rn(A.x * inv); o[1] = __float2bfloat16_rn(A.y * inv);
     o[2] = __float2bfloat16_rn(A.z * inv); o[3] = __float2bfloat16_rn(A.w * inv);
     if (p.lse && c == 0)
-        p.lse[((long long)b * p.Hq + hq) * p.Sq + qi] = L > 0.f ? (M + __log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+        p.lse[((long long)b * p.Hq + hq) * p.Sq + qi] = L > 0.f ? (M + log2f(L)) * kLn2 : L != L ? L : -INFINITY;
 }
 
 template <int N>
@@ -529,8 +548,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     }
     const int lim_all = p.causal ? n - p.Sq + 1 : n;   // keys below this are visible to every row
 
-    // o: code sums, tile (group, h), row g (+ 8) = channel 32 group + 4 g + 2 h (+ 1), in units of 2^-24 (2^-20);
-    // om: sums of P * minimum of a group
+    // o: code sums, tile (group, h), row g (+ 8) = channel 32 group + 4 g + 2 h (+ 1), in units of 2^(e - 38)
+    // (2^(e - 34)), 2^e = s_top; om: sums of P * minimum of a group
     float o[NT][NG * 2][4], om[NT][NG][2], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -541,8 +560,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
         m[nt][0] = m[nt][1] = kRowFloor;
         l[nt][0] = l[nt][1] = 0.f;
     }
-    int s_exp = -60;           // above every V scale's exponent so far (scales below 2^-80 fade to 0)
-    float x_lim = 74.f;        // 14 - s_exp: a score this far above the reference has P * scale = 2^14
+    float s_top = 0x1p-100f;   // V scales so far are below it: 2^e
+    float lift = 0x1p114f;     // 2^(14 - e)
     const int ka = tile_key(g);
     const int off_a = ka * REC;                                                // K, and both halves' pairs: keys ka, ka + 8
     const int off_m = off_a + D + (NG == 4 ? (t & 1) * 8 : 0);                 // K pairs whose minima this lane feeds
@@ -567,23 +586,37 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 reinterpret_cast<uint4 *>(slot)[x] = make_uint4(0, 0, 0, 0);
             __syncwarp();
         }
-        // the tile's largest V scale: a key per lane
-        {
-            float s_max = 0.f;
+        // The tile's largest and smallest V scale, a key per lane.  (A scale of 0 counts as small: right, only slower.)
+        float s_max = 0.f, s_min = INFINITY;
 #pragma unroll
-            for (int r = 0; r < TK; r += 32) {
-                if (r + lane < subs * 16) {
-                    const Words<NG> w = lds_words<NG>(slot + (r + lane) * REC + D + D / 8);
+        for (int r = 0; r < TK; r += 32) {
+            if (r + lane < end - k0) {
+                const Words<NG> w = lds_words<NG>(slot + (r + lane) * REC + D + D / 8);
 #pragma unroll
-                    for (int gi = 0; gi < NG; ++gi) s_max = fmaxf(s_max, lo_bf16(w.w[gi]));
+                for (int gi = 0; gi < NG; gi += 2) {
+                    s_max = fmax3(s_max, lo_bf16(w.w[gi]), lo_bf16(w.w[gi + 1]));
+                    s_min = fminf(s_min, fminf(lo_bf16(w.w[gi]), lo_bf16(w.w[gi + 1])));
                 }
             }
-            const int e = (int)(__float_as_uint(s_max) >> 23) - 126;   // s_max < 2^e
-            if (__any_sync(0xffffffffu, e > s_exp)) {
-                s_exp = max(s_exp, __reduce_max_sync(0xffffffffu, e));
-                x_lim = 14.f - (float)s_exp;
-            }
         }
+        bool wide = false;
+        if (__any_sync(0xffffffffu, s_max >= s_top || s_min < s_top * kNarrow)) {
+            const int e = __reduce_max_sync(0xffffffffu, min(254, (int)(__float_as_uint(s_max) >> 23) + 1));
+            const float top = __uint_as_float((uint32_t)e << 23);   // the power of two above the tile's scales, at most 2^127
+            if (top > s_top) {
+                const float a = s_top / top;
+                s_top = top;
+                lift = 0x1p14f / top;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < NG * 2; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) o[nt][j][q] *= a;
+            }
+            wide = __any_sync(0xffffffffu, s_min < s_top * kNarrow);
+        }
+        auto sub_tiles = [&](auto two_parts) {
 #pragma unroll 1
         for (int sub = 0; sub < subs; ++sub) {
             const unsigned char *tile = slot + sub * 16 * REC;
@@ -645,7 +678,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 top = fmax3(top, y[nt][0] - m[nt][0], y[nt][1] - m[nt][1]);
                 top = fmax3(top, y[nt][2] - m[nt][0], y[nt][3] - m[nt][1]);
             }
-            if (__any_sync(0xffffffffu, top > x_lim)) {
+            if (__any_sync(0xffffffffu, top > 0.f)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -654,8 +687,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        // the reference at which P * scale is at most 2^6, where that is higher
-                        mx = fmaxf(m[nt][c], mx - (x_lim - 8.f));
+                        mx = fmaxf(m[nt][c], ceilf(mx) + kHeadroom);
                         const float a = ex2_approx(m[nt][c] - mx);
                         m[nt][c] = mx;
                         l[nt][c] *= a;
@@ -708,6 +740,11 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                     vs[1][gi] = vs[1][gi] == vs[1][gi] ? vs[1][gi] : 0.f;
                 }
             }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2)
+                    f2_unpack(f2_mul(f2_pack(pr[nt][e], pr[nt][e + 1]), f2_pack(lift, lift)), pr[nt][e], pr[nt][e + 1]);
             const Words<NG> w0 = lds_words<NG>(tile + off_v0), w1 = lds_words<NG>(tile + off_v1);
             const Words<NG> w2 = lds_words<NG>(tile + off_v0 + 8 * REC), w3 = lds_words<NG>(tile + off_v1 + 8 * REC);
 #pragma unroll
@@ -716,13 +753,30 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 const uint32_t u8 = u >> 8, v8 = v >> 8;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    const uint32_t b0 = transpose_8x8(pack_f16x2(pr[nt][0] * vs[0][gi], pr[nt][1] * vs[0][gi]));
-                    const uint32_t b1 = transpose_8x8(pack_f16x2(pr[nt][2] * vs[1][gi], pr[nt][3] * vs[1][gi]));
-                    mma_f16(o[nt][2 * gi], u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
-                    mma_f16(o[nt][2 * gi + 1], u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u, b0, b1);
+                    float(&oa)[4] = o[nt][2 * gi], (&ob)[4] = o[nt][2 * gi + 1];
+                    const float p0 = pr[nt][0] * vs[0][gi], p1 = pr[nt][1] * vs[0][gi];
+                    const float p2 = pr[nt][2] * vs[1][gi], p3 = pr[nt][3] * vs[1][gi];
+                    if constexpr (two_parts.value) {
+                        uint32_t b0, b1, c0, c1;
+                        split_bf16x2(p0 * 0x1p109f, p1 * 0x1p109f, b0, c0);
+                        split_bf16x2(p2 * 0x1p109f, p3 * 0x1p109f, b1, c1);
+                        b0 = transpose_8x8(b0); b1 = transpose_8x8(b1);
+                        c0 = transpose_8x8(c0); c1 = transpose_8x8(c1);
+                        mma_bf16(oa, u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
+                        mma_bf16(ob, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u, b0, b1);
+                        mma_bf16(oa, u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, c0, c1);
+                        mma_bf16(ob, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u, c0, c1);
+                    } else {
+                        const uint32_t b0 = transpose_8x8(pack_f16x2(p0, p1)), b1 = transpose_8x8(pack_f16x2(p2, p3));
+                        mma_f16(oa, u & 0x000f000fu, u & 0x00f000f0u, v & 0x000f000fu, v & 0x00f000f0u, b0, b1);
+                        mma_f16(ob, u8 & 0x000f000fu, u8 & 0x00f000f0u, v8 & 0x000f000fu, v8 & 0x00f000f0u, b0, b1);
+                    }
                 }
             }
         }
+        };
+        if (wide) sub_tiles(Flag<true>{});
+        else sub_tiles(Flag<false>{});
         __syncwarp();
         if (lane == 0 && i + STAGES < mine) issue(st);
     }
@@ -737,6 +791,7 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
     // ------------------------------------------------------------- merge the warps' states
     __syncthreads();   // the rings are drained: their memory takes the outputs
     float *so = reinterpret_cast<float *>(smem);
+    const float back = s_top * 0x1p-6f;   // 2^(e + 10) in two steps, each within float32's range
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -758,8 +813,8 @@ attn_kv4_tc_kernel(const Kv4AttnProblem kp, int q_vec, int row_blocks, int flat)
                 mn += __shfl_xor_sync(0xffffffffu, mn, 16);
                 const float *lo = o[nt][2 * gi], *hi = o[nt][2 * gi + 1];
                 *reinterpret_cast<float4 *>(so + (warp * 8 * NT + r) * D + 32 * gi + 4 * g) =
-                    make_float4(fmaf(lo[c], 0x1p24f, mn), fmaf(lo[c + 2], 0x1p20f, mn), fmaf(hi[c], 0x1p24f, mn),
-                                fmaf(hi[c + 2], 0x1p20f, mn));
+                    make_float4(fmaf(lo[c] * 0x1p16f, back, mn), fmaf(lo[c + 2] * 0x1p12f, back, mn),
+                                fmaf(hi[c] * 0x1p16f, back, mn), fmaf(hi[c + 2] * 0x1p12f, back, mn));
             }
         }
     }
