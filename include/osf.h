@@ -290,7 +290,8 @@ int osf_kv4_read(const void *cache, void *K, void *V, int dtype, int B, int Hkv,
  * mask: OSF_MASK_NONE, or OSF_MASK_BOTTOM_RIGHT: row i sees records 0 .. i + lens[b] - Sq (the Sq
  *     rows are the sequence's last tokens).  OSF_MASK_TOP_LEFT: OSF_ERR_INVALID.
  *     A row that sees nothing gets O = 0 and lse = -inf.
- * lse: optional contiguous float32 [B, Hq, Sq]; of a row with a NaN score: NaN or -inf.
+ * lse: optional contiguous float32 [B, Hq, Sq]; of a row that sees a score of NaN or +inf: NaN, as its O and the
+ *     weights of the records that it sees.
  * weights: optional contiguous float32 [B, Hkv, S]: the attention weight of every record, summed over
  *     the query heads of its kv head and the Sq rows, as in osf_attn_key_weights.  accumulate 0:
  *     overwritten (0 at and behind lens[b]); else added to (at and behind lens[b] left as they are).

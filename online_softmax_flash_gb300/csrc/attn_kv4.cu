@@ -923,11 +923,12 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
         const float *lse = p.lse + ((long long)b * p.Hq + kvh * G) * p.Sq;   // the R rows of a kv head are consecutive
         const float *sc = kp.scores + (long long)kvbh * R * p.Sk + key;
         for (int r0 = 0; r0 < R; r0 += RG) {
-            float x[RG][V], z[RG];
+            float x[RG][V], off[RG];
+            bool nan = false;
 #pragma unroll
             for (int e = 0; e < RG; ++e) {
                 const int r = min(r0 + e, R - 1);
-                z[e] = lse[r];
+                off[e] = lse[r];
                 const float *at = sc + (long long)r * p.Sk;
                 if (V == 4) {
                     const float4 v = __ldcs(reinterpret_cast<const float4 *>(at));
@@ -939,9 +940,20 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
 #pragma unroll
             for (int e = 0; e < RG; ++e) {
                 // a row that saw nothing, or a repeated one past the last, adds 0
-                const float off = r0 + e < R && z[e] != -INFINITY ? -z[e] * kLog2e : -INFINITY;
+                off[e] = r0 + e < R && off[e] != -INFINITY ? -off[e] * kLog2e : -INFINITY;
+                nan |= off[e] != off[e];
+            }
+            if (!nan) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum[i] += ex2_approx(x[e][i] + off);
+                for (int e = 0; e < RG; ++e)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] += ex2_approx(x[e][i] + off[e]);
+            } else {   // the NaN of a row is for the keys that it sees alone (the others' scores are -inf)
+#pragma unroll
+                for (int e = 0; e < RG; ++e)
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        if (!p.causal || key + i <= n - p.Sq + (r0 + e) % p.Sq) sum[i] += ex2_approx(x[e][i] + off[e]);
             }
         }
     }
@@ -1049,6 +1061,7 @@ cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_co
                       : (t.nt == 1 ? launch_tc_t<128, 1>(kp, t, at, s) : launch_tc_t<128, 2>(kp, t, at, s));
     } else {
         p.splits = simt_splits(p, sm_count);
+        p.keep_nan = 1;
         const size_t rows = (size_t)p.splits * p.B * p.Hq * p.Sq;
         char *at = static_cast<char *>(partials);
         p.part_acc = reinterpret_cast<float *>(at);

@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnProblem p) 
 #pragma unroll
     for (int e = 0; e < 4; ++e)
         if (c0 + e < p.D) Og[c0 + e] = from_f32<T>(a[e] * inv);
-    if (p.lse && c0 == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    if (p.lse && c0 == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2 : p.keep_nan && L != L ? L : -INFINITY;
 }
 
 template <typename T, int DP, int BM>

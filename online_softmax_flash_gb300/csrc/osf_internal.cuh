@@ -77,6 +77,7 @@ struct AttnProblem {
     float *part_acc, *part_m, *part_l;
     void *x3_ws;         // fp32 on the tensor-core path: bf16 high / low parts of Q, K, V
     int *status;         // device status word
+    int keep_nan;        // attn_combine_kernel: the lse of a row with a NaN score is NaN (0: -inf)
 };
 
 // Element offsets of row s of head h in batch b.
