@@ -172,7 +172,7 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
                     const float x = fmaf((float)((w >> (4 * (lane & 7))) & 15u), lo_bf16(sp2), hi_bf16(sp2));
 #pragma unroll
                     for (int r = 0; r < RB; ++r)   // a NaN value must not reach a row that does not see its key
-                        acc[r][g] = masked.value && pk[r] == 0.f ? acc[r][g] : fmaf(pk[r], x, acc[r][g]);
+                        acc[r][g] = masked.value && k0 + kk >= lim[r] ? acc[r][g] : fmaf(pk[r], x, acc[r][g]);
                 }
             }
         };

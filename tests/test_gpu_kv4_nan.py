@@ -55,3 +55,21 @@ def test_a_nan_key_reaches_the_rows_that_see_it(osf, dtype, D, S):
     out = osf.osf_attn_kv4(q, bad, mask="bottom_right", lse=lse, weights=w)
     assert torch.equal(out[:, :, :2], want[:, :, :2]) and torch.equal(lse[:, :, :2], clean_lse[:, :, :2])
     assert bool(torch.isnan(out[:, :, 2]).all()) and bool(torch.isnan(lse[:, :, 2]).all()) and bool(torch.isnan(w).all())
+
+
+@pytest.mark.parametrize("dtype,D", KINDS)
+@pytest.mark.parametrize("S", [40, 300])
+def test_a_nan_value_reaches_the_rows_that_see_it_whatever_its_weight(osf, dtype, D, S):
+    """A record whose weight underflows to 0 still gives NaN to the rows that see it (0 * NaN), inside and outside of the
+    tiles that the mask cuts."""
+    Sq = 4
+    q = torch.ones(1, 2, Sq, D, device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32)
+    for at in (2, S - 3):                                            # row 0 does not see record S - 3, rows 1 .. 3 do
+        cache, _ = random_cache(1, 1, S, D, 65)
+        far = torch.tensor([0.0, -512.0] * (D // 32), dtype=torch.bfloat16, device="cuda").view(torch.uint8)
+        cache[0, 0, at, D:D + D // 8] = far                          # K = -512 in every channel: a score of -512 sqrt(D)
+        want = osf.osf_attn_kv4(q, cache, mask="bottom_right")
+        cache[0, 0, at, D + D // 8:] = 0xFF                          # V: NaN
+        out = osf.osf_attn_kv4(q, cache, mask="bottom_right")
+        first = 0 if at == 2 else 1
+        assert bool(torch.isnan(out[:, :, first:]).all()) and torch.equal(out[:, :, :first], want[:, :, :first])
