@@ -250,7 +250,8 @@ int osf_attn_key_weights_workspace_bytes(int dtype, int B, int Hq, int Hkv, int 
  *     scale   = the smallest bfloat16 >= (largest value - minimum) / 15
  *     c       = round((x - minimum) / scale), ties to even
  * so a stored value is off by at most scale / 2.  These are the exact results of the formulas, not of
- * their float32 evaluation.  A group that holds a NaN or an infinity reads back as NaN.
+ * their float32 evaluation.  A group that holds a NaN, an infinity or a value below the least finite bfloat16
+ * (-3.39e38) reads back as NaN.
  * Lengths are device int32 arrays [B] (tokens of a sequence that are valid, the same for all its kv
  * heads); a length outside [0, S] is cut to it, and recorded as OSF_ERR_INVALID in the device status
  * word (osf_device_status).  The caller keeps the lengths and advances them.

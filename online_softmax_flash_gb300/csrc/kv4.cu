@@ -6,7 +6,8 @@
 // three are decided exactly, whatever float32 rounds on the way: x - m is kept as a float32 and its
 // rounding error (Knuth's two-sum), and the comparisons that settle s and a code near a tie use
 // 15 s and (c +- 1/2) s, which float32 holds exactly (8 significant bits times at most 5).
-// A group with a NaN, an infinity or a range past float32 is stored as s = m = NaN: it reads back NaN.
+// A group with a NaN, an infinity or a value below the least finite bfloat16 (m would be -inf) is stored as s = m = NaN: it
+// reads back NaN.  Ranges near float32's end, or past it, are worked out in halves.
 //
 // Both directions move bytes: 4 D + 1.25 D per bf16 token and kv head.  Two lanes share a group when storing, sixteen
 // channels (a 32-byte sector of bf16) each, with the next token's row in flight; that leaves 16 instructions
@@ -88,20 +89,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // (scale, minimum) of a group whose largest value is hi and whose minimum, a bfloat16, is m.
+constexpr float kMaxF32 = 3.4028235e38f;
 __device__ __forceinline__ void group_scale(float hi, float &s, float &m) {
     m = __fadd_rn(m, 0.f);   // a minimum of -0 is stored as 0
-    float d, e;
+    float d, e, unit = 1.f;
     diff_exact(hi, m, d, e);
-    if (!(fabsf(d) <= 3.0e38f) || !(fabsf(m) <= 3.39e38f)) {
-        s = m = __uint_as_float(0x7fc00000u);
-        return;
+    if (!(fabsf(d) <= 3.0e38f)) {   // 15 s could overflow, or hi - m did: in halves (of e the sign is enough)
+        if (!(fabsf(hi) <= kMaxF32 && fabsf(m) <= kMaxF32)) {
+            s = m = __uint_as_float(0x7fc00000u);
+            return;
+        }
+        if (fabsf(d) <= kMaxF32) d *= 0.5f;
+        else diff_exact(0.5f * hi, 0.5f * m, d, e);   // (both far from the subnormals, so exact)
+        unit = 2.f;
     }
     // 0x1.11111p-4 is below 1/15 by 2^-22: the truncated product is the wanted bfloat16, the first with
     // 15 s >= d + e, or at most two below it
     uint32_t u = __float_as_uint(d * 0x1.11111p-4f) & 0xffff0000u;
     if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
     if (cmp_exact(d, e, 15.f * __uint_as_float(u)) > 0) u += 0x10000u;
-    s = __uint_as_float(u);
+    s = __uint_as_float(u) * unit;
 }
 
 // Codes of eight channels as one word.  t + 1.5 * 2^23 has the rounded t in its low bits, so a code needs no
@@ -115,20 +122,23 @@ __device__ __forceinline__ uint32_t word_of(const float (&r)[8]) {
 }
 
 // Any group.  t is off by up to 2^-20; what is left over, (x - m) - code * s, is exact, and only where it
-// reaches s / 2 is the code looked at again.
+// reaches s / 2 is the code looked at again.  From kWideScale on, where x - m may overflow, all in halves.
+constexpr float kWideScale = 0x1p123f;
 __device__ __noinline__ uint32_t quantise8_any(float x0, float x1, float x2, float x3, float x4, float x5, float x6, float x7,
                                                float s, float m) {
     const float x[8] = {x0, x1, x2, x3, x4, x5, x6, x7};
+    const float h = s >= kWideScale ? 0.5f : 1.f, sh = s * h, mh = m * h;
     const float up = s < 0x1p-100f ? 0x1p60f : 1.f;   // a reciprocal that could overflow: lifted first
-    const float inv = rcp_approx(s * up), half = 0.5f * s;
+    const float inv = rcp_approx(sh * up), half = 0.5f * sh;
     float r[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float d = __fsub_rn(x[i], m), e;
+        float d = fmaf(x[i], h, -mh), e;
         r[i] = __fadd_rn(d * up * inv, kMagic);
-        const float c = __fsub_rn(r[i], kMagic), rest = fmaf(-c, s, d);
+        const float c = __fsub_rn(r[i], kMagic), rest = fmaf(-c, sh, d);
         if (fabsf(rest) >= half) {
             diff_exact(x[i], m, d, e);
+            if (!(fabsf(d) <= kMaxF32)) diff_exact(x[i] * h, mh, d, e);   // (of e the sign is enough)
             // at the tie (rest = +- s / 2) the side is that of e, or the even code; past it the neighbour
             const float over = fabsf(rest) > half ? 1.f : rest > 0.f ? e : -e;
             if (over > 0.f || (over == 0.f && ((int)c & 1))) r[i] += rest > 0.f ? 1.f : -1.f;
@@ -242,7 +252,7 @@ struct Half<__nv_bfloat16> {
         for (int i = 1; i < 8; ++i) w = min_s16x2(w, (v[i] | 0x80008000u) - 0x00010001u);
         const int least = min((int)(short)w, (int)w >> 16) + 0x8000;
         const int bound = (int)(__float_as_uint(s) >> 16) - (11 << 7);   // 2^-11 s as a bfloat16's bits
-        if (least >= bound - 1 && (m == 0.f || fabsf(m) >= 0x1p-11f * s) && s >= 0x1p-80f) {
+        if (least >= bound - 1 && (m == 0.f || fabsf(m) >= 0x1p-11f * s) && s >= 0x1p-80f && s < kWideScale) {
             const float inv = __frcp_rn(s);
             a = quantise8_coarse(v, s, m, inv);
             b = quantise8_coarse(v + 4, s, m, inv);
