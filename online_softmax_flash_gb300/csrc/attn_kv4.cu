@@ -970,11 +970,12 @@ __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem k
 static bool use_tc(const AttnProblem &p) { return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128); }
 
 // Launch shape of the tensor-core kernel.  Items of few tiles are not cut: a CTA each, one launch, no combine.  Else one wave
-// of CTAs shares all tiles, as many as the longest possible lengths are worth.  Few is 48 tiles, or 64 where the items
-// fill half of the SMs (Hq=32 Hkv=8 D=128, whole against cut: 8 items of 24 tiles 8.0 against 9.2 us, of 47 12.1 against
-// 11.7, of 64 14.7 against 9.4; 64 of 47 12.3 against 15.0, of 64 14.9 against 13.1; 128 of 64 15.0 against 19.1; 256 of 32
-// 14.0 against 20.5; longer items are cut so that ragged batches stay even, though 256 equal ones of 128 tiles would
-// take 40.8 against 44.4).
+// of CTAs shares all tiles, as many as the longest possible lengths are worth.  Few is 28 tiles, 48 where the items fill a
+// quarter of the SMs, 64 where they fill half.  (Hq=32 Hkv=8 D=128, whole against cut, us: 8 items of 24 tiles 9.1 against
+// 10.3, of 32 10.4 against 10.4, of 48 13.1 against 10.6; 64 of 40 12.5 against 14.2, of 48 14.0 against 15.0, of 64 16.8
+// against 16.1; 128 of 64 17.4 against 23.1; 256 of 64 26.0 against 31.7.  D=64 crosses at the same numbers, 16 rows of
+// 32 items at 28 tiles and, D=128, 36.  Longer items are cut so that ragged batches stay even: 16 x 8 of up to 64 tiles 17.2
+// against 18.4, of up to 96 22.4 against 21.8.)
 struct TcPlan {
     int nt, row_blocks, flat, grid;
 };
@@ -985,7 +986,7 @@ static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
     t.row_blocks = (R + 8 * t.nt - 1) / (8 * t.nt);
     const long long items = (long long)p.B * p.Hkv * t.row_blocks, per = ((long long)p.Sk + tk - 1) / tk;
     const long long wave = (long long)sm_count * (t.nt == 1 || p.D == 64 ? 2 : 1);
-    t.flat = per > (items * 2 > sm_count ? 64 : 48);
+    t.flat = per > (items * 2 > sm_count ? 64 : items * 4 > sm_count ? 48 : 28);
     const long long worth = items * per / kMinTiles;
     t.grid = (int)(!t.flat ? items : worth < wave ? (worth < 1 ? 1 : worth) : wave);
     return t;
