@@ -241,8 +241,8 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // is little beside the scales of a tile that are at least 2^(e - 6).  A tile with a smaller one (groups or keys
 // whose values lie far apart) takes P * scale in two bfloat16 parts, 16 bits, lifted by 2^109 more, against the codes
 // as bfloat16 subnormals (code * 2^-133): two MMAs, the same unit in the accumulators, all 16 bits down to P * scale =
-// 2^(e - 108) and none below 2^(e - 116).  (Always in float16: with equal weights a scale 2^-28 of the largest had 12 % error, one of 2^-32 was gone.
-// Always in two parts: the decode step below 88 us.)
+// 2^(e - 108) and none below 2^(e - 116).  (Always in float16: with equal weights a scale 2^-28 of the largest had
+// 12 % error, one of 2^-32 was gone.  Always in two parts: the decode step below 88 us.)
 // P moves from the S^T accumulator layout to the B operand by movmatrix.
 //
 // Each warp streams its own 5120-byte runs of records through a ring of bulk copies (one instruction
@@ -365,7 +365,10 @@ struct FlatWork {
 // Tiles worth a CTA: one for every warp (Hq=32 Hkv=8 D=128, 4096 records: B=1 10.6 us, B=4 13.6 us; two for every warp 13.3 and
 // 16.9 us, three 13.6 and 14.2 us).
 constexpr int kMinTiles = TW;
-constexpr int kItemCost = 8;        // tiles that an item's set-up and merge take as long as
+// Tiles that an item's set-up and merge are counted as.  (Hkv=8, D=128, 16 lengths even up to 8192: 34.9 us with 8, 41.5
+// with 4, 33.7 with 16; 32 lengths, most of them short: 42.7, 59.3, 30.6; 4 equal ones of 4096, 12 rows of D=64: 19.7,
+// 25.6, 25.3.)
+constexpr int kItemCost = 8;
 
 __device__ __forceinline__ int item_tiles(const Kv4AttnProblem &kp, int b, int tk) {
     return max(1, (kv4_length(kp.lens, b, kp.a.Sk, kp.a.status) + tk - 1) / tk);
@@ -905,8 +908,9 @@ __global__ void __launch_bounds__(256) kv4_combine_kernel(const Kv4AttnProblem k
 
 // Weights from the stored scores, once every row's log-sum-exp is known: a thread sums the rows of V neighbouring
 // keys, RG rows' loads in flight together.  Bound by the latency of reading the scores once: 32 MB (B=16 Hkv=8, 16 rows,
-// lengths 4 .. 8192), the whole call 47 .. 49 us with RG = 8, 48 .. 50 us with 4, 54 us with 16.
-template <int V, int RG>
+// lengths 4 .. 8192) in 9 us.  (RG = 8: that call 43.2 us against 42.8, B=8 Hkv=8 Hq=32 over 32768 records 94.5 against 92.3.)
+constexpr int RG = 4;
+template <int V>
 __global__ void __launch_bounds__(256) kv4_weights_kernel(const Kv4AttnProblem kp) {
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq;
@@ -1077,10 +1081,7 @@ cudaError_t launch_attn_kv4(const Kv4AttnProblem &kp0, void *partials, int sm_co
         // four keys per thread where a row of scores keeps 16-byte alignment
         const int v = p.Sk % 4 == 0 ? 4 : 1;
         const dim3 grid((unsigned)((p.Sk + 256 * v - 1) / (256 * v)), (unsigned)(p.B * p.Hkv));
-        // (up to four rows need no more than four loads)
-        auto kernel = R > 4 ? (v == 4 ? kv4_weights_kernel<4, 8> : kv4_weights_kernel<1, 8>)
-                            : (v == 4 ? kv4_weights_kernel<4, 4> : kv4_weights_kernel<1, 4>);
-        e = launch_dependent(kernel, grid, dim3(256), 0, s, kp);
+        e = launch_dependent(v == 4 ? kv4_weights_kernel<4> : kv4_weights_kernel<1>, grid, dim3(256), 0, s, kp);
     }
     return e;
 }
