@@ -54,7 +54,7 @@ def weight_sum(q, rec, lens, mask, scale):
         n = S if lens is None else lens[b]
         for h in range(Hq):
             s = np.where(oracle.kv_cache.visible(Sq, n, mask, n), (q[b, h] @ K[b, h * Hkv // Hq, :n].T) * scale, -np.inf)
-            out[b, h] = np.maximum(np.exp(s - np.maximum(s.max(-1, keepdims=True), -1e300)).sum(-1), 1)
+            out[b, h] = np.maximum(np.exp(s - np.maximum(s.max(-1, keepdims=True, initial=-np.inf), -1e300)).sum(-1), 1)
     return out
 
 
@@ -166,3 +166,12 @@ def test_scores_do_not_depend_on_the_values(osf, dtype, D, exponent):
     # scores 0.5 and -1 times scale * D: 18 ln 2 apart
     check(osf, torch.ones(1, 2, 1, D, device="cuda", dtype=torch.bfloat16 if dtype == "bf16" else torch.float32), rec,
           scale=float(np.float32(12 * np.log(2) / D)), what="one key above the others")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(1, 1, 1), (4, 1, 1), (6, 2, 3), (16, 1, 1), (8, 2, 5)])
+@pytest.mark.parametrize("S", [1, 17, 100, 1000, 5000])
+def test_ordinary_records_keep_eleven_bits(osf, D, Hq, Hkv, Sq, S):
+    _, rec = random_cache(2, Hkv, S, D, S + Hq)
+    q, _ = rows((2, Hq, Sq, D), S, "bf16")
+    check(osf, q, rec, lens=[S, S // 2], mask="bottom_right")
