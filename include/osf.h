@@ -229,7 +229,7 @@ int osf_attn_decode_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sk, i
  * mask, scale: as given to the forward call.  accumulate: 0 overwrites weights, else adds to them.
  * workspace: osf_attn_key_weights_workspace_bytes bytes (may be 0), 16-byte aligned.
  * weights must not overlap an input -> else OSF_ERR_INVALID.  B == 0 or Sk == 0: OSF_OK, nothing
- * written; Sq == 0: weights are zeroed (accumulate == 0) or left.  B * Hkv > 65535:
+ * written; Sq == 0: weights are zeroed (accumulate == 0) or left.  B * Hkv > 65535 or Sk > 2^31 - 64:
  * OSF_ERR_UNSUPPORTED.  Other errors as in osf_attn_fwd_gqa_ex.  The result does not depend on the
  * order in which anything runs.  No gradient: the weights are a statistic of a finished pass.
  */

@@ -1,6 +1,7 @@
 // C ABI of libosf (declared in include/osf.h): argument checks, kernel choice, workspace
 // sizing and the device status word.  Every entry point validates on the host, then enqueues
 // kernels on the caller's stream and returns; nothing here allocates device memory.
+#include <limits.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -784,7 +785,8 @@ static int check_key_weights(const void *Q, const void *K, const float *lse, flo
         if (!lse) return OSF_ERR_INVALID;
     }
     if (!weights) return OSF_ERR_INVALID;
-    if ((long long)B * Hkv > 65535) return OSF_ERR_UNSUPPORTED;
+    // (kernels count keys in ints, up to the end of the last block of 64)
+    if ((long long)B * Hkv > 65535 || Sk > INT_MAX - 63) return OSF_ERR_UNSUPPORTED;
     w = KeyWeightsProblem{};
     w.q = Q; w.k = K; w.lse = lse; w.w = weights;
     w.dtype = dtype; w.B = B; w.Hq = Hq; w.Hkv = Hkv; w.Sq = Sq; w.Sk = Sk; w.D = D;
