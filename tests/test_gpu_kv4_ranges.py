@@ -17,7 +17,7 @@ import numpy as np
 import pytest
 
 import oracle
-from test_gpu_kv4 import H, U, ints, random_cache, rows
+from test_gpu_kv4 import H, U, check_attention, ints, random_cache, rows
 
 pytestmark = pytest.mark.gpu
 
@@ -175,3 +175,19 @@ def test_ordinary_records_keep_eleven_bits(osf, D, Hq, Hkv, Sq, S):
     _, rec = random_cache(2, Hkv, S, D, S + Hq)
     q, _ = rows((2, Hq, Sq, D), S, "bf16")
     check(osf, q, rec, lens=[S, S // 2], mask="bottom_right")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv,Sq", [(16, 1, 1), (8, 2, 4), (24, 1, 1), (4, 1, 5)])
+@pytest.mark.parametrize("S", [50, 4600])
+def test_scales_far_apart_with_many_rows_and_weights(osf, D, Hq, Hkv, Sq, S):
+    """Groups 2^20 and keys 2^12 apart under 16 and more rows, with the records' weights, a mask and ragged lengths."""
+    _, rec = random_cache(3, Hkv, S, D, S + Hq)
+    p = pairs(rec, D, 1)
+    p[..., 1, :] *= 2.0 ** -20
+    p[:, :, ::7] *= 2.0 ** 12
+    set_pairs(rec, D, 1, p)
+    q, _ = rows((3, Hq, Sq, D), S, "bf16")
+    lens = [S, S // 2, 3]
+    check(osf, q, rec, lens=lens, mask="bottom_right")
+    check_attention(osf, 3, Hq, Hkv, Sq, S, D, "bf16", lens=lens, mask="bottom_right", q=q, cache=torch.from_numpy(rec).cuda())
