@@ -253,16 +253,19 @@ attn_kv4_kernel(const Kv4AttnProblem kp) {
 // rounding it would share.
 //
 // B=8 Hq=32 Hkv=8, 32768 records of D=128: 336 MB in 72 us (4.7 TB/s of 6.8), 76 us with the join, against 631 us for the
-// general kernel's layout on the CUDA cores.  Bound by the integer pipe, busy 54 % of the time (the masks that take codes
-// out of their words run at half rate), and by the latency of a warp's chain from scores to products: 2.7
-// instructions per code, the matrix pipe busy 23 %.  tcgen05 takes its operands from shared memory or TMEM, so the
+// general kernel's layout on the CUDA cores.  Bound by the integer pipe, busy 53 % of the time (the masks that take codes
+// out of their words run at half rate), and by the latency of a warp's chain from scores to products: 2.8
+// instructions per code, the matrix pipe busy 22 %.  tcgen05 takes its operands from shared memory or TMEM, so the
 // codes would have to be expanded there and read again, for at most 16 rows.  Two slots to a warp keep 80 KB in
 // flight per CTA, two CTAs to an SM; smaller slots 86 us.
 constexpr int TW = 8;                     // warps per CTA
 constexpr uint32_t kSlot = 5120;          // bytes of one ring slot: 32 records at D = 128, 64 at D = 64
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
-constexpr float kNarrow = 0x1p-6f;            // scales this far below the largest still go through float16
-constexpr float kHeadroom = 4.f;              // what a new reference is above the largest score
+// Scales this far below the largest still go through float16: a row's heaviest key has P >= 2^-5, so float16's least step
+// (2^(e - 38) of P * scale) is at most 2^-27 of that key's P * scale.  (The decode step above with every tile past it
+// 92 us, with none 82, caches cold.)
+constexpr float kNarrow = 0x1p-6f;
+constexpr float kHeadroom = 4.f;              // what a new reference is above the largest score (8 takes the same time)
 
 template <int D, int NT>
 struct TcCfg {
@@ -362,8 +365,8 @@ struct FlatWork {
     long long total, base;   // units of all items, and of the batches before b
     int nc;                  // CTAs that take part
 };
-// Tiles worth a CTA: one for every warp (Hq=32 Hkv=8 D=128, 4096 records: B=1 10.6 us, B=4 13.6 us; two for every warp 13.3 and
-// 16.9 us, three 13.6 and 14.2 us).
+// Tiles worth a CTA: one for every warp (Hq=32 Hkv=8 D=128, 4096 records: B=1 11.6 us, B=4 16.2 us; two for every warp 14.7 and
+// 19.3 us, three 14.9 and 16.7 us).
 constexpr int kMinTiles = TW;
 // Tiles that an item's set-up and merge are counted as.  (Hkv=8, D=128, 16 lengths even up to 8192: 34.9 us with 8, 41.5
 // with 4, 33.7 with 16; 32 lengths, most of them short: 42.7, 59.3, 30.6; 4 equal ones of 4096, 12 rows of D=64: 19.7,

@@ -12,7 +12,7 @@
 // the others cut into parts of `tiles_per_part` tiles, so that the key blocks of a causal problem, whose row counts
 // differ, give even parts.
 // Bound by instruction issue (two 16-byte shared loads to 16 FMAs) and the latency of a part's first loads: B=1 Hq=8
-// Hkv=2 S=1001 D=64 float32, causal, 0.51 GFLOP, 27 us with the sum of the parts.  Packed pairs of FMAs, with the
+// Hkv=2 S=1001 D=64 float32, causal, 0.51 GFLOP, 25 us with the sum of the parts.  Packed pairs of FMAs, with the
 // rows' values doubled in shared memory, are bound by that memory's bandwidth: the kernel alone 32 us against 26 us.
 #include "key_weights.cuh"
 
@@ -197,8 +197,8 @@ __global__ void __launch_bounds__(RK * RT) key_weights_reduce_kernel(const KeyWe
 static int tile_rows(const KeyWeightsProblem &p) { return (long long)(p.Hq / p.Hkv) * p.Sq <= 16 ? 16 : 64; }
 
 void key_weights_simt_plan(KeyWeightsProblem &p, int sm_count) {
-    // at most four CTAs to an SM over all key blocks, one wave, of equal numbers of tiles (the problem above: 27 us; a
-    // little more than a wave 29 us, three to an SM 33 us); at most 64 parts of a block
+    // at most four CTAs to an SM over all key blocks, one wave, of equal numbers of tiles (the problem above: 27 us, now
+    // 25; a little more than a wave then 29 us, three to an SM 33 us); at most 64 parts of a block
     const int tr = tile_rows(p);
     const long long blocks = (p.Sk + TK - 1) / TK;
     auto tiles = [&](long long kb) {
