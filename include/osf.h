@@ -165,6 +165,41 @@ int osf_attn_fwd_gqa_ex(const void *Q, const void *K, const void *V, void *O, in
                         int mask, float scale, float *lse, void *workspace, size_t workspace_bytes,
                         osf_stream stream);
 
+/*
+ * osf_attn_fwd_gqa_window -- osf_attn_fwd_gqa_ex under a sliding window whose first tokens stay visible (sinks; not on the
+ * pages, whose attention, [Q3] "自注意力原理" + "GQA", sees every earlier key).  The Sq rows are the last of Sk tokens: row i
+ * stands at position p = i + Sk - Sq and sees key j where
+ *     j <= p  and  (p - j < window  or  j < sinks).
+ * Key tiles that no row sees are not read: the work grows with the window, not with Sk.
+ * window >= 1 (1: a row sees itself and the sinks), sinks >= 0.  A window that hides nothing (window + sinks >= Sk) is
+ * OSF_MASK_BOTTOM_RIGHT of osf_attn_fwd_gqa_ex, by the same kernels.
+ * strides, scale, lse, errors: as there.  A row that sees no key (p < 0, or Sk == 0) gets O = 0 and lse = -inf.
+ * workspace: osf_attn_window_workspace_bytes with the same sizes, window and sinks.
+ * Sq or Sk >= 2^29: OSF_ERR_UNSUPPORTED.
+ * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores, CUDA cores.
+ */
+int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O, int dtype,
+                            int B, int Hq, int Hkv, int Sq, int Sk, int D, const long long *strides,
+                            int window, int sinks, float scale, float *lse, void *workspace,
+                            size_t workspace_bytes, osf_stream stream);
+int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                    int sinks, size_t *bytes);
+
+/*
+ * osf_attn_bwd_gqa_window -- gradients of osf_attn_fwd_gqa_window: osf_attn_bwd_gqa (same tensors, formulas and errors)
+ * with the keys that a row sees given by window and sinks, as in the forward call.
+ * workspace: osf_attn_bwd_window_workspace_bytes bytes, 128-byte aligned: row sums, the sums of the key tiles that hold
+ *     sinks (whose rows are shared out over several CTAs), and dS^T in bf16 of the tile pairs that some row sees while it
+ *     stays within 16 GiB.  A workspace short of the last part selects the path that keeps no dS.
+ * The result does not depend on the order in which anything runs.  Sq == 0 or Sk == 0: what gradients there are are zero.
+ */
+int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const void *O, const void *dO,
+                            const float *lse, void *dQ, void *dK, void *dV, int dtype, int B, int Hq,
+                            int Hkv, int Sq, int Sk, int D, int window, int sinks, float scale,
+                            void *workspace, size_t workspace_bytes, osf_stream stream);
+int osf_attn_bwd_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window,
+                                        int sinks, size_t *bytes);
+
 /* Bytes of workspace osf_attn_fwd_gqa needs for these arguments (written to *bytes). */
 int osf_attn_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D,
                              size_t *bytes);

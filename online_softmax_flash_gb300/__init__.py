@@ -21,6 +21,8 @@ __all__ = [
     "solve", "osf_attn_fwd_gqa_ex", "osf_softmax_rows_ex", "osf_softmax_ex_workspace_bytes",
     "osf_attn_bwd_gqa", "osf_attn_bwd_workspace_bytes", "osf_selftest_bounded_wait", "OSF_MASK_NONE", "OSF_MASK_TOP_LEFT", "OSF_MASK_BOTTOM_RIGHT",
     "osf_attn_fwd_gqa_host", "osf_attn_host_buffer_bytes",
+    "osf_attn_fwd_gqa_window", "osf_attn_window_workspace_bytes", "osf_attn_bwd_gqa_window",
+    "osf_attn_bwd_window_workspace_bytes",
     "osf_attn_key_weights", "osf_attn_key_weights_workspace_bytes", "osf_kv4_record_bytes", "osf_kv4_append",
     "osf_kv4_read", "osf_attn_kv4", "osf_attn_kv4_workspace_bytes", "osf_kv_evict",
 ]
@@ -51,6 +53,11 @@ _SIGS = {
     "osf_attn_bwd_gqa": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                               _vp, _sz, _vp]),
     "osf_attn_bwd_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_attn_fwd_gqa_window": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _f, _vp, _vp, _sz, _vp]),
+    "osf_attn_window_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_attn_bwd_gqa_window": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
+                                     _vp, _sz, _vp]),
+    "osf_attn_bwd_window_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "osf_attn_key_weights": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _i, _f, _i, _vp, _sz, _vp]),
     "osf_attn_key_weights_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "osf_kv4_record_bytes": (_i, [_i, ctypes.POINTER(_sz)]),
@@ -429,6 +436,78 @@ def _kv4_dims(cache, D: int):
         raise ValueError("cache must be a contiguous uint8 CUDA tensor [B, Hkv, S, osf_kv4_record_bytes(D)]")
     B, Hkv, S, _ = cache.shape
     return B, Hkv, S, dev
+
+
+def osf_attn_window_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, Sk, D, window: int, sinks: int = 0) -> int:
+    n = _sz(0)
+    _check(lib().osf_attn_window_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks, ctypes.byref(n)),
+           "osf_attn_window_workspace_bytes")
+    return n.value
+
+
+def _qkv_dims(q, k, v):
+    """(B, Hq, Hkv, Sq, Sk, D, device) of q [B, Hq, Sq, D] and k, v [B, Hkv, Sk, D] of one dtype on one device."""
+    dev = _on_device(q)
+    if q.dim() != 4 or k.dim() != 4 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[3] != q.shape[3] or \
+            not q.dtype == k.dtype == v.dtype or k.get_device() != dev or v.get_device() != dev:
+        raise ValueError("q, k and v must be 4-D and agree in dtype, batch, head dimension and device, k and v in shape")
+    B, Hq, Sq, D = q.shape
+    return B, Hq, k.shape[1], Sq, k.shape[2], D, dev
+
+
+def osf_attn_fwd_gqa_window(q, k, v, window: int, sinks: int = 0, out=None, scale: float | None = None, lse=None,
+                            workspace=None):
+    """Grouped-query attention on [B, H, S, D] views (as in osf_attn_fwd_gqa_ex) under a sliding window: the rows are
+    the last Sq of Sk tokens, and the row at position p sees the keys j <= p with p - j < ``window`` or j < ``sinks``.
+    ``lse`` (float32 [B, Hq, Sq]) receives the rows' log-sum-exp.  Returns ``out`` (a contiguous tensor if None)."""
+    B, Hq, Hkv, Sq, Sk, D, dev = _qkv_dims(q, k, v)
+    if out is None:
+        out = torch.empty((B, Hq, Sq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev:
+        raise ValueError("out must have the shape, dtype and device of q")
+    st = None
+    if not (q.is_contiguous() and k.is_contiguous() and v.is_contiguous() and out.is_contiguous()):
+        for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{name} must be a 4-D [B, H, S, D] view with a contiguous last dimension")
+        st = ctypes.cast((ctypes.c_longlong * 12)(*q.stride()[:3], *k.stride()[:3], *v.stride()[:3], *out.stride()[:3]),
+                         ctypes.c_void_p)
+    dt = _dtype_code(q)
+    if workspace is None:
+        n = _query(dev, osf_attn_window_workspace_bytes, dt, B, Hq, Hkv, Sq, Sk, D, int(window), int(sinks))
+        workspace = _workspace(n, q.device, None)
+    _call("osf_attn_fwd_gqa_window", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), dt, B, Hq, Hkv, Sq, Sk,
+          D, st, int(window), int(sinks), 0.0 if scale is None else float(scale),
+          _need(lse, "lse", (B, Hq, Sq), torch.float32, dev), _ptr(workspace), _bytes_of(workspace, dev))
+    return out
+
+
+def osf_attn_bwd_window_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, Sk, D, window: int, sinks: int = 0) -> int:
+    n = _sz(0)
+    _check(lib().osf_attn_bwd_window_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks, ctypes.byref(n)),
+           "osf_attn_bwd_window_workspace_bytes")
+    return n.value
+
+
+def osf_attn_bwd_gqa_window(q, k, v, o, dout, lse, window: int, sinks: int = 0, dq=None, dk=None, dv=None,
+                            scale: float | None = None, workspace=None):
+    """Gradients (dq, dk, dv) of osf_attn_fwd_gqa_window on contiguous [B, H, S, D] tensors, given its output ``o``, its
+    log-sum-exp ``lse`` and the gradient ``dout`` of the loss with respect to ``o``; ``window``, ``sinks`` and ``scale``
+    as in the forward call."""
+    B, Hq, Hkv, Sq, Sk, D, dev = _qkv_dims(q, k, v)
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    dt = _dtype_code(q)
+    if workspace is None:
+        n = _query(dev, osf_attn_bwd_window_workspace_bytes, dt, B, Hq, Hkv, Sq, Sk, D, int(window), int(sinks))
+        workspace = _workspace(n, q.device, None)
+    _call("osf_attn_bwd_gqa_window", dev, _need(q, "q", q.shape, q.dtype, dev), _need(k, "k", k.shape, q.dtype, dev),
+          _need(v, "v", k.shape, q.dtype, dev), _need(o, "o", q.shape, q.dtype, dev), _need(dout, "dout", q.shape, q.dtype, dev),
+          _need(lse, "lse", (B, Hq, Sq), torch.float32, dev), _need(dq, "dq", q.shape, q.dtype, dev),
+          _need(dk, "dk", k.shape, q.dtype, dev), _need(dv, "dv", k.shape, q.dtype, dev), dt, B, Hq, Hkv, Sq, Sk, D,
+          int(window), int(sinks), 0.0 if scale is None else float(scale), _ptr(workspace), _bytes_of(workspace, dev))
+    return dq, dk, dv
 
 
 def osf_attn_key_weights(q, k, lse, weights=None, mask="none", scale: float | None = None, accumulate: bool = False,

@@ -653,6 +653,34 @@ int osf_attn_bwd_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
     return OSF_OK;
 }
 
+// The backward problem of a checked forward one (p, whose output is dQ): its buffers' checks, and its fields but for the
+// workspace.
+static int check_bwd(const AttnProblem &p, const void *O, const void *dO, const float *lse, void *dK, void *dV, BwdProblem &b) {
+    if (!O || !dO || !lse || !dK || !dV) return OSF_ERR_INVALID;
+    const size_t es = elem_size(p.dtype);
+    const size_t nq = (size_t)p.B * p.Hq * p.Sq * p.D * es, nkv = (size_t)p.B * p.Hkv * p.Sk * p.D * es;
+    const size_t nl = (size_t)p.B * p.Hq * p.Sq * sizeof(float);
+    const void *ins[6] = {p.q, p.k, p.v, O, dO, lse};
+    const size_t in_n[6] = {nq, nkv, nkv, nq, nq, nl};
+    void *outs[3] = {p.o, dK, dV};
+    const size_t out_n[3] = {nq, nkv, nkv};
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 6; ++i)
+            if (overlaps(outs[o], out_n[o], ins[i], in_n[i])) return OSF_ERR_INVALID;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(outs[o], out_n[o], outs[o2], out_n[o2])) return OSF_ERR_INVALID;
+    }
+    b = BwdProblem{};
+    b.q = p.q; b.k = p.k; b.v = p.v; b.o = O; b.dout = dO; b.lse = lse;
+    b.dq = p.o; b.dk = dK; b.dv = dV;
+    b.dtype = p.dtype;
+    b.B = p.B; b.Hq = p.Hq; b.Hkv = p.Hkv; b.Sq = p.Sq; b.Sk = p.Sk; b.D = p.D;
+    b.causal = p.causal; b.causal_off = p.causal_off;
+    b.scale_log2 = p.scale_log2;
+    b.scale = p.scale_log2 / kLog2e;
+    return OSF_OK;
+}
+
 int osf_attn_bwd_gqa(const void *Q, const void *K, const void *V, const void *O, const void *dO,
                      const float *lse, void *dQ, void *dK, void *dV, int dtype, int B, int Hq, int Hkv,
                      int Sq, int Sk, int D, int mask, float scale, void *workspace, size_t workspace_bytes,
@@ -666,32 +694,13 @@ int osf_attn_bwd_gqa(const void *Q, const void *K, const void *V, const void *O,
         // no keys or no rows: gradients are zero (written when there is anything to write)
         return OSF_OK;
     }
-    if (!O || !dO || !lse || !dK || !dV) return OSF_ERR_INVALID;
-    const size_t es = elem_size(dtype);
-    const size_t nq = (size_t)B * Hq * Sq * D * es, nkv = (size_t)B * Hkv * Sk * D * es;
-    const size_t nl = (size_t)B * Hq * Sq * sizeof(float);
-    const void *ins[6] = {Q, K, V, O, dO, lse};
-    const size_t in_n[6] = {nq, nkv, nkv, nq, nq, nl};
-    void *outs[3] = {dQ, dK, dV};
-    const size_t out_n[3] = {nq, nkv, nkv};
-    for (int o = 0; o < 3; ++o) {
-        for (int i = 0; i < 6; ++i)
-            if (overlaps(outs[o], out_n[o], ins[i], in_n[i])) return OSF_ERR_INVALID;
-        for (int o2 = o + 1; o2 < 3; ++o2)
-            if (overlaps(outs[o], out_n[o], outs[o2], out_n[o2])) return OSF_ERR_INVALID;
-    }
-    const size_t need = align256(nl);
+    BwdProblem b;
+    st = check_bwd(p, O, dO, lse, dK, dV, b);
+    if (st != OSF_OK) return st;
+    const size_t need = align256((size_t)B * Hq * Sq * sizeof(float));
     if (!workspace || workspace_bytes < need) return OSF_ERR_WORKSPACE;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
-    BwdProblem b{};
-    b.q = Q; b.k = K; b.v = V; b.o = O; b.dout = dO; b.lse = lse;
-    b.dq = dQ; b.dk = dK; b.dv = dV;
-    b.dtype = dtype;
-    b.B = B; b.Hq = Hq; b.Hkv = Hkv; b.Sq = Sq; b.Sk = Sk; b.D = D;
-    b.causal = p.causal; b.causal_off = p.causal_off;
-    b.scale_log2 = p.scale_log2;
-    b.scale = p.scale_log2 / kLog2e;
     b.dvec = static_cast<float *>(workspace);
     // a workspace that also holds dS^T selects the tensor-core path's separate dQ product
     const size_t ds_bytes = bwd_ds_bytes(dtype, B, Hq, Sq, Sk, D);
@@ -701,6 +710,155 @@ int osf_attn_bwd_gqa(const void *Q, const void *K, const void *V, const void *O,
         b.ds_rows = ((long long)Sk + 127) / 128 * 128;
         b.ds_ld = ((long long)Sq + 127) / 128 * 128;
     }
+    b.status = dev->status;
+    return launch_status(launch_attn_bwd(b, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ a window with sinks
+// The checks of a windowed problem: those of a bottom-right one, then the window.  One that hides nothing is dropped.
+static int check_window(const void *Q, const void *K, const void *V, void *O, int dtype, int B, int Hq, int Hkv, int Sq,
+                        int Sk, int D, const long long *strides, int window, int sinks, float scale, float *lse,
+                        AttnProblem &p, bool &empty) {
+    empty = false;
+    if (window < 1 || sinks < 0) return OSF_ERR_INVALID;
+    const int st = check_gqa_ex(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, OSF_MASK_BOTTOM_RIGHT, scale, lse, p, empty);
+    if (st != OSF_OK || empty) return st;
+    // kernels add lengths and the window in ints
+    if (Sq >= (1 << 29) || Sk >= (1 << 29)) return OSF_ERR_UNSUPPORTED;
+    // the last row sees the most hidden keys: those between the sinks and its window
+    if ((long long)window + sinks < Sk) {
+        p.causal = 1;
+        p.causal_off = Sk - Sq;
+        p.window = window;
+        p.sinks = sinks;
+    }
+    return OSF_OK;
+}
+
+int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                                    size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    AttnProblem p;
+    bool empty;
+    const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
+    const int st = check_window(ph, ph, ph, reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, Sk, D,
+                                nullptr, window, sinks, 0.f, nullptr, p, empty);
+    if (st != OSF_OK || empty) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    // the largest of the possible paths' needs (alignment decides the path at call time)
+    size_t need = path_workspace(p, Path::Simt, plan_splits(p, Path::Simt, dev->sm_count, 0));
+    if (Sq > 1 && ((dtype == OSF_BF16 && (D == 64 || D == 128)) || (dtype == OSF_F32 && D == 64)))
+        need = std::max(need, path_workspace(p, Path::TensorCore, plan_splits(p, Path::TensorCore, dev->sm_count, 0)));
+    if (dtype == OSF_BF16 && (long long)(Hq / Hkv) * Sq <= 16)
+        need = std::max(need, path_workspace(p, Path::Decode, plan_splits(p, Path::Decode, dev->sm_count, 0)));
+    *bytes = need;
+    return OSF_OK;
+}
+
+int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O, int dtype, int B, int Hq, int Hkv, int Sq,
+                            int Sk, int D, const long long *strides, int window, int sinks, float scale, float *lse,
+                            void *workspace, size_t workspace_bytes, osf_stream stream) {
+    AttnProblem p;
+    bool empty;
+    int st = check_window(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, window, sinks, scale, lse, p, empty);
+    if (st != OSF_OK) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    if (empty) {
+        if (B == 0 || Sq == 0) return OSF_OK;
+        // no keys: every row sees nothing.  The problem of one key, whose place nothing reads, without it
+        long long sd[12] = {};   // (K and V: strides of no extent)
+        for (int i = 0; strides && i < 3; ++i) {
+            sd[i] = strides[i];
+            sd[9 + i] = strides[9 + i];
+        }
+        st = check_window(Q, Q, Q, O, dtype, B, Hq, Hkv, Sq, 1, D, strides ? sd : nullptr, window, sinks, scale, lse, p, empty);
+        if (st != OSF_OK) return st;
+        p.Sk = p.causal = 0;
+        return run_gqa(p, Path::Simt, nullptr, 0, 1, dev, (cudaStream_t)stream);
+    }
+    const Path path = choose_path(p, Q, K, V, O);
+    return run_gqa(p, path, workspace, workspace_bytes, plan_splits(p, path, dev->sm_count, 0), dev, (cudaStream_t)stream);
+}
+
+// Workspace of the windowed backward: row sums | sums of the tiles that hold sinks | dS^T tiles that some row sees.  The
+// last are left out where they would pass 16 GiB, and may be left out by the caller (dQ then recomputes S and dP).
+struct BwdWindowLayout {
+    size_t rows = 0, ds = 0, sink = 0;
+    int slots = 0, parts = 1;
+};
+static BwdWindowLayout bwd_window_layout(const AttnProblem &p, int sm_count) {
+    BwdWindowLayout L;
+    L.rows = align256((size_t)p.B * p.Hq * p.Sq * sizeof(float));
+    if (p.dtype != OSF_BF16 || (p.D != 64 && p.D != 128)) return L;
+    L.slots = bwd_window_slots(p.Sk, p.window, p.sinks);
+    L.parts = bwd_window_sink_parts(p.B, p.Hkv, p.Sq, p.Sk, p.window, p.sinks, sm_count);
+    const size_t tile = (size_t)128 * 128 * 2, per_head = (size_t)L.slots * (((size_t)p.Sq + 127) / 128) * tile;
+    const size_t cap = (size_t)16 << 30, heads = (size_t)p.B * p.Hq;
+    if (per_head <= cap / heads) L.ds = per_head * heads;
+    if (L.parts > 1)
+        L.sink = (size_t)bwd_window_sink_tiles(p.Sk, p.sinks) * L.parts * p.B * p.Hkv * 2 * 128 * p.D * sizeof(float);
+    return L;
+}
+
+int osf_attn_bwd_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
+                                        size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    AttnProblem p;
+    bool empty;
+    const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
+    const int st = check_window(ph, ph, ph, reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, Sk, D,
+                                nullptr, window, sinks, 0.f, nullptr, p, empty);
+    if (st != OSF_OK || empty) return st;
+    if (!p.window) return osf_attn_bwd_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, bytes);
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    const BwdWindowLayout L = bwd_window_layout(p, dev->sm_count);
+    *bytes = L.rows + L.ds + L.sink;
+    return OSF_OK;
+}
+
+int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const void *O, const void *dO, const float *lse,
+                            void *dQ, void *dK, void *dV, int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D,
+                            int window, int sinks, float scale, void *workspace, size_t workspace_bytes, osf_stream stream) {
+    AttnProblem p;
+    bool empty;
+    const int st = check_window(Q, K, V, dQ, dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, window, sinks, scale, nullptr, p, empty);
+    if (st != OSF_OK) return st;
+    if (empty) {   // no rows, or no keys: what gradients there are are zero
+        const size_t es = elem_size(dtype), nq = (size_t)B * Hq * Sq * D * es, nk = (size_t)B * Hkv * Sk * D * es;
+        if ((nq && !dQ) || (nk && (!dK || !dV)) || overlaps(dK, nk, dV, nk)) return OSF_ERR_INVALID;
+        if (nq && cudaMemsetAsync(dQ, 0, nq, (cudaStream_t)stream) != cudaSuccess) return OSF_ERR_CUDA;
+        if (nk && (cudaMemsetAsync(dK, 0, nk, (cudaStream_t)stream) != cudaSuccess ||
+                   cudaMemsetAsync(dV, 0, nk, (cudaStream_t)stream) != cudaSuccess))
+            return OSF_ERR_CUDA;
+        return OSF_OK;
+    }
+    if (!p.window)
+        return osf_attn_bwd_gqa(Q, K, V, O, dO, lse, dQ, dK, dV, dtype, B, Hq, Hkv, Sq, Sk, D, OSF_MASK_BOTTOM_RIGHT, scale,
+                                workspace, workspace_bytes, stream);
+    BwdProblem b;
+    const int sb = check_bwd(p, O, dO, lse, dK, dV, b);
+    if (sb != OSF_OK) return sb;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    const BwdWindowLayout L = bwd_window_layout(p, dev->sm_count);
+    const size_t need = L.rows + L.sink;
+    if (!workspace || workspace_bytes < need) return OSF_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (L.ds + L.sink ? 127u : 3u)) != 0) return OSF_ERR_INVALID;
+    char *at = static_cast<char *>(workspace);
+    b.window = window;
+    b.sinks = sinks;
+    b.dvec = reinterpret_cast<float *>(at);
+    b.sink_parts = L.parts;
+    b.ds_slots = L.slots;
+    b.ds_ld = ((long long)Sq + 127) / 128 * 128;
+    b.ds_rows = (long long)L.slots * 128;
+    if (L.sink) b.sink_acc = reinterpret_cast<float *>(at + L.rows);
+    if (L.ds && workspace_bytes >= need + L.ds) b.ds = at + need;
     b.status = dev->status;
     return launch_status(launch_attn_bwd(b, (cudaStream_t)stream));
 }

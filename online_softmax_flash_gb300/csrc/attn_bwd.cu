@@ -147,7 +147,9 @@ __global__ void __launch_bounds__(256) bwd_dq_simt_kernel(BwdProblem p) {
     }
     const float lse2 = p.lse[row] * kLog2e, dv = p.dvec[row];
     const int j_end = p.causal ? min(p.Sk, max(0, i + p.causal_off + 1)) : p.Sk;
-    for (int j = 0; j < j_end; ++j) {
+    // with a window: the sinks, then the window
+    const int j_near = p.window ? max(0, i + p.causal_off - p.window + 1) : 0, j_sinks = min(p.sinks, j_near);
+    for (int j = j_sinks > 0 ? 0 : j_near; j < j_end; j = j + 1 == j_sinks ? j_near : j + 1) {
         float s = 0.f, dp = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -198,11 +200,13 @@ __global__ void __launch_bounds__(256) bwd_dkdv_simt_kernel(BwdProblem p) {
         dk[c] = dv[c] = 0.f;
     }
     const int i_begin = p.causal ? max(0, j - p.causal_off) : 0;
+    // with a window: a key that is no sink leaves it after `window` rows
+    const int i_end = p.window && j >= p.sinks ? min(p.Sq, max(0, j - p.causal_off + p.window)) : p.Sq;
     for (int g = 0; g < G; ++g) {
         const long long bh = (long long)b * p.Hq + kvh * G + g;
         const T *Q = static_cast<const T *>(p.q) + bh * p.Sq * D;
         const T *GO = static_cast<const T *>(p.dout) + bh * p.Sq * D;
-        for (int i = i_begin; i < p.Sq; ++i) {
+        for (int i = i_begin; i < i_end; ++i) {
             float s = 0.f, dp = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -575,7 +579,7 @@ cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (attn_bwd_tc_supported(p)) return launch_attn_bwd_tc(p, s);
-    if (attn_bwd_mma_supported(p)) return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
+    if (!p.window && attn_bwd_mma_supported(p)) return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
     return p.dtype == OSF_BF16 ? launch_simt<__nv_bfloat16>(p, s) : launch_simt<float>(p, s);
 }
 

@@ -10,17 +10,32 @@ struct BwdProblem {
     int dtype;             // OSF_F32 / OSF_BF16
     int B, Hq, Hkv, Sq, Sk, D;
     int causal, causal_off;  // key j visible to row i iff !causal || j <= i + causal_off
+    // 0, or (with causal = 1, causal_off = Sk - Sq): of those keys only j > i + causal_off - window or j < sinks
+    int window, sinks;
     float scale, scale_log2;
     float *dvec;           // workspace [B, Hq, Sq]: rowsum(dO * O)
     // optional workspace (tensor-core path): dS^T as bf16 [128 x 128] tiles, tile (bh, key tile,
     // query tile) at ((bh * ds_rows / 128 + key tile) * ds_ld / 128 + query tile) * 32 KB, each
     // [128 keys][128 queries]; ds_rows and ds_ld the key and query counts rounded up to 128.
     // null: dQ recomputes S and dP instead
+    // With a window only the tiles that some row sees: that of query tile t and place s of its key_stream at
+    // (bh * (ds_ld / 128) + t) * ds_slots + s
     void *ds;
     long long ds_rows, ds_ld;
+    int ds_slots;
+    // with a window: the query tiles of each key tile that holds sinks are shared out over sink_parts CTAs, whose sums
+    // of dK and dV (float32 [128][D] each) meet in sink_acc [sink tile][part][b, kv head][2]; 1: no sharing out
+    int sink_parts;
+    float *sink_acc;
     int *status;
 };
 // True when the bf16 tensor-core (mma.sync) kernels handle the problem.
 bool attn_bwd_mma_supported(const BwdProblem &p);
 cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s);
+
+// Sizes of a windowed problem on the tensor-core path: tiles of the longest key stream, key tiles that hold sinks, and
+// CTAs that share the rows of each of those.
+int bwd_window_slots(int Sk, int window, int sinks);
+int bwd_window_sink_tiles(int Sk, int sinks);
+int bwd_window_sink_parts(int B, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count);
 }  // namespace osf

@@ -137,6 +137,11 @@ __device__ __forceinline__ void tmem_to_bf16(uint32_t taddr, bool have, float sc
     }
 }
 
+// With a window: the key tiles that the query tile from row q0 on sees.
+__device__ __forceinline__ KeyStream row_stream(const BwdProblem &p, int q0) {
+    return key_stream(q0 + p.causal_off, min(q0 + TB, p.Sq) - 1 + p.causal_off, p.Sk, p.window, p.sinks, TB);
+}
+
 template <int D>
 __device__ __forceinline__ void init_bars(BtBars &bars, volatile int &abort_flag) {
     using C = BtCfg<D>;
@@ -163,7 +168,8 @@ __device__ __forceinline__ void init_bars(BtBars &bars, volatile int &abort_flag
 // ====================================================================== dQ
 // The two bodies below run as one grid (bwd_tc_kernel): CTA `bid` of each.  The tensor maps are
 // the kernel's __grid_constant__ parameters, passed by reference so TMA sees their addresses.
-template <int D>
+// WIN: a window with sinks (BwdProblem::window).
+template <int D, bool WIN>
 __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtensorMap &mg, const CUtensorMap &mk,
                                             const CUtensorMap &mv, const BwdProblem &p, unsigned bid) {
     using C = BtCfg<D>;
@@ -180,10 +186,15 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
     const int bh = (int)(bid % BH), b = bh / p.Hq, hq = bh % p.Hq;
     const int kvh = hq / (p.Hq / p.Hkv);
     int n = (p.Sk + TB - 1) / TB;   // key tiles these rows see
-    if (p.causal) {
+    KeyStream ks{};
+    if constexpr (WIN) {
+        ks = row_stream(p, q0);
+        n = ks.n;
+    } else if (p.causal) {
         const int last = min(q0 + TB - 1, p.Sq - 1) + p.causal_off;
         n = min(n, last < 0 ? 0 : last / TB + 1);
     }
+    auto key_of = [&](int j) { return (WIN ? ks.tile(j) : j) * TB; };   // first key of the j-th tile
     if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TMEM_COLS);
     if (tid == 32) init_bars<D>(bars, abort_flag);
     tc_fence_before();
@@ -203,7 +214,7 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
             ok = mbar_wait(smem_u32(&bars.empty[st]), ((m / C::RING) & 1) ^ 1, &abort_flag);
             if (!ok) break;
             mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
-            tma_load_5d(sRing + st * C::TILE, (m & 1) ? &mv : &mk, smem_u32(&bars.full[st]), 0, (m >> 1) * TB, 0, kvh,
+            tma_load_5d(sRing + st * C::TILE, (m & 1) ? &mv : &mk, smem_u32(&bars.full[st]), 0, key_of(m >> 1), 0, kvh,
                         b);
         }
         if (!ok) {
@@ -291,12 +302,20 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc_fence_after();
-            const int key0 = j * TB;
+            const int key0 = key_of(j);
             // a full tile: every key exists and every row of the tile sees all of them
-            const bool full = key0 + TB <= p.Sk && (!p.causal || key0 + TB - 1 <= q0 + p.causal_off);
+            bool full = key0 + TB <= p.Sk && (!p.causal || key0 + TB - 1 <= q0 + p.causal_off);
             int lim = p.Sk - key0 - col0;
             if (p.causal) lim = min(lim, row + p.causal_off - key0 + 1 - col0);
             if (!row_ok) lim = 0;
+            // with a window: of those the columns from low on, or before snk
+            int low = 0, snk = 0;
+            if constexpr (WIN) {
+                full = full && (key0 + p.window > q0 + TB - 1 + p.causal_off || key0 + TB <= p.sinks);
+                low = row + p.causal_off - p.window + 1 - key0 - col0;
+                snk = p.sinks - key0 - col0;
+            }
+            auto sees = [&](int k) { return k < lim && (!WIN || k >= low || k < snk); };
             // phase A: P for this warp's 64 columns, kept in registers
             float pv[64];
             {
@@ -309,8 +328,8 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
                     float a0, a1;
                     f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), c22, nl2), a0, a1);
                     const float e0 = ex2_approx(a0), e1 = ex2_approx(a1);
-                    pv[k] = (full || k < lim) ? e0 : 0.f;
-                    pv[k + 1] = (full || k + 1 < lim) ? e1 : 0.f;
+                    pv[k] = (full || sees(k)) ? e0 : 0.f;
+                    pv[k + 1] = (full || sees(k + 1)) ? e1 : 0.f;
                 }
             }
             tc_fence_before();
@@ -365,7 +384,9 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
 }
 
 // ====================================================================== dK, dV
-template <int D>
+// WIN: the CTAs of the key tiles that hold sinks come first, sink_parts of them for each tile and (b, kv head): every later
+// row sees a sink, so one CTA would walk Sq / 128 query tiles while the others walk window / 128.
+template <int D, bool WIN>
 __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUtensorMap &mg, const CUtensorMap &mk,
                                               const CUtensorMap &mv, const CUtensorMap &mdst, const BwdProblem &p,
                                               unsigned bid) {
@@ -380,13 +401,35 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
     float *tab = reinterpret_cast<float *>(smem_raw + (sbase - smem_u32(smem_raw)) + C::TAB_OFF);
     // the key tiles seen by the most query tiles (the first ones, under a causal mask) go first
     const int BK = p.B * p.Hkv;
-    const int key0 = (int)(bid / BK) * TB;
+    int kt = (int)(bid / BK), part = 0;
+    if constexpr (WIN) {
+        const int shared_out = min((p.sinks - 1 + TB) / TB, (p.Sk - 1) / TB + 1) * p.sink_parts;
+        if (kt < shared_out) {
+            part = kt % p.sink_parts;
+            kt /= p.sink_parts;
+        } else {
+            kt += shared_out / p.sink_parts - shared_out;
+        }
+    }
+    const int key0 = kt * TB;
     const int bk = (int)(bid % BK), b = bk / p.Hkv, kvh = bk % p.Hkv;
     const int G = p.Hq / p.Hkv;
     // query tiles that see a key of this block: from the first row that sees key0
     int q_first = p.causal ? max(0, key0 - p.causal_off) : 0;
     q_first /= TB;
-    const int n_qt = (p.Sq + TB - 1) / TB;
+    int n_qt = (p.Sq + TB - 1) / TB;
+    bool partial = false;   // this CTA has only a part of the rows
+    if constexpr (WIN) {
+        if (key0 >= p.sinks) {
+            const int last = key0 + TB - 1 + p.window - 1 - p.causal_off;   // last row whose window holds a key of the block
+            n_qt = last < 0 ? 0 : min(n_qt, last / TB + 1);
+        } else if (p.sink_parts > 1) {
+            const int all = max(0, n_qt - q_first), per = (all + p.sink_parts - 1) / p.sink_parts;
+            q_first = min(n_qt, q_first + part * per);
+            n_qt = min(n_qt, q_first + per);
+            partial = true;
+        }
+    }
     const int per_head = max(0, n_qt - q_first);
     const int n = G * per_head;   // steps: (head g, query tile) pairs
     if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TMEM_COLS);
@@ -511,8 +554,14 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
             const float4 *td4 = reinterpret_cast<const float4 *>(tab + st * 2 * TB + TB + col0);
             // query column q is visible to this key iff (causal) key <= q + off; columns past
             // Sq have lse = +inf (P = 0) and zero Q, dO rows; keys past Sk are never stored
-            const bool full = !p.causal || key0 + TB - 1 - p.causal_off <= qbase;
+            bool full = !p.causal || key0 + TB - 1 - p.causal_off <= qbase;
             const int qmin = p.causal ? key - p.causal_off - qbase - col0 : INT_MIN;
+            int qmax = INT_MAX;   // with a window: and q <= qmax
+            if constexpr (WIN) {
+                full = full && (qbase + TB - 1 <= key0 + p.window - 1 - p.causal_off || key0 + TB <= p.sinks);
+                if (key >= p.sinks) qmax = qmin + p.window - 1;
+            }
+            auto sees = [&](int k) { return k >= qmin && (!WIN || k <= qmax); };
             // phase A: P^T for this warp's 64 columns (fp32 in registers, bf16 into TMEM)
             float pv[64];
 #pragma unroll
@@ -531,8 +580,8 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
                                          e ? f2_pack(l.z, l.w) : f2_pack(l.x, l.y)),
                                   a0, a1);
                         const float x0 = ex2_approx(a0), x1 = ex2_approx(a1);
-                        pv[32 * c + k] = (full || 32 * c + k >= qmin) ? x0 : 0.f;
-                        pv[32 * c + k + 1] = (full || 32 * c + k + 1 >= qmin) ? x1 : 0.f;
+                        pv[32 * c + k] = (full || sees(32 * c + k)) ? x0 : 0.f;
+                        pv[32 * c + k + 1] = (full || sees(32 * c + k + 1)) ? x1 : 0.f;
                     }
                 }
                 pack_store16(tS + lane_off + col0 + 16 * c, *reinterpret_cast<const float(*)[32]>(pv + 32 * c));
@@ -597,7 +646,9 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
                     __syncwarp();
                     if (lane == 0) {
                         const int nkt = (int)(p.ds_rows / TB), nqt = (int)(p.ds_ld / TB);
-                        const int tile = (((b * p.Hq + hq) * nkt) + key0 / TB) * nqt + qbase / TB;
+                        int tile;
+                        if constexpr (WIN) tile = ((b * p.Hq + hq) * nqt + qt) * p.ds_slots + row_stream(p, qbase).place(kt);
+                        else tile = (((b * p.Hq + hq) * nkt) + key0 / TB) * nqt + qbase / TB;
                         // dS^T is read once, by the dQ product: it gives way in L2 first
                         tma_store_3d_hint(&mdst, stg, col0 + 32 * c, q4 * 32, tile, l2_policy_evict_first());
                         bulk_commit();
@@ -617,12 +668,32 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
             tc_fence_after();
         }
         const bool key_ok = key < p.Sk;
+        if (WIN && partial) {
+            // this part's sums, [key][D] float32, zero where it has no rows
+            float *out = p.sink_acc + ((((size_t)kt * p.sink_parts + part) * BK + bk) * 2 + h) * TB * D + (size_t)r * D;
+            const uint32_t src = (h ? tV : tK) + lane_off;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                if (have) {
+                    tmem_ld32(src + c * 32, o);
+                    tmem_ld_wait();
+                }
+#pragma unroll
+                for (int k = 0; k < 32; k += 4)
+                    *reinterpret_cast<float4 *>(out + c * 32 + k) =
+                        have ? make_float4(__uint_as_float(o[k]), __uint_as_float(o[k + 1]), __uint_as_float(o[k + 2]),
+                                           __uint_as_float(o[k + 3]))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        } else {
         const long long gk = (long long)bk * p.Sk + (key_ok ? key : 0);
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(h ? p.dv : p.dk) + gk * D;
         const uint32_t src = (h ? tV : tK) + lane_off;
         const float sc = h ? 1.f : p.scale;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) tmem_to_bf16(src + c * 32, have, sc, key_ok, out + c * 32);
+        }
     }
     tc_fence_before();
     __syncwarp();
@@ -635,13 +706,33 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
 
 // One grid: CTAs [0, n_dkdv) are dK/dV CTAs, the rest dQ CTAs, each group heaviest first, so
 // dQ work fills the SMs the dK/dV tail leaves idle.
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(NT_THREADS, 1)
 bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mg,
               const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
               const __grid_constant__ CUtensorMap mdst, const BwdProblem p, unsigned n_dkdv) {
-    if (blockIdx.x < n_dkdv) bwd_dkdv_body<D>(mq, mg, mk, mv, mdst, p, blockIdx.x);
-    else bwd_dq_body<D>(mq, mg, mk, mv, p, blockIdx.x - n_dkdv);
+    if (blockIdx.x < n_dkdv) bwd_dkdv_body<D, WIN>(mq, mg, mk, mv, mdst, p, blockIdx.x);
+    else bwd_dq_body<D, WIN>(mq, mg, mk, mv, p, blockIdx.x - n_dkdv);
+}
+
+// dK and dV of the keys in tiles that hold sinks: the parts' sums, added in the order of the parts.  One thread per four
+// channels of a key: gridDim = (keys of the tiles * D / 4 / 256, b * kv head, dK | dV).
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdProblem p) {
+    griddep_wait();
+    const int per = p.D / 4, i = blockIdx.x * 256 + threadIdx.x;
+    const int key = i / per, c = i % per * 4, BK = gridDim.y, bk = blockIdx.y, h = blockIdx.z;
+    if (key >= p.Sk) return;
+    const size_t part = (size_t)BK * 2 * TB * p.D;
+    const float *src = p.sink_acc + (((size_t)(key / TB) * p.sink_parts * BK + bk) * 2 + h) * TB * p.D + (size_t)(key % TB) * p.D + c;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int s = 0; s < p.sink_parts; ++s) {
+        const float4 x = *reinterpret_cast<const float4 *>(src + s * part);
+        a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
+    }
+    const float sc = h ? 1.f : p.scale;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(h ? p.dv : p.dk) + ((size_t)bk * p.Sk + key) * p.D + c;
+    *reinterpret_cast<uint2 *>(out) = make_uint2(pack_bf16x2(a.x * sc, a.y * sc), pack_bf16x2(a.z * sc, a.w * sc));
 }
 
 // ====================================================================== dQ as one product
@@ -677,10 +768,16 @@ struct DqBars {
 };
 
 // Item `it`, heaviest first: its first query row, first (b, q head) index and key-tile count.
-__device__ __forceinline__ void dq_item(const BwdProblem &p, int hp, int it, int &q0, int &bh, int &n) {
+template <bool WIN>
+__device__ __forceinline__ void dq_item(const BwdProblem &p, int hp, int it, int &q0, int &bh, int &n, KeyStream &ks) {
     const int BHP = p.B * p.Hq / hp, nqt = (p.Sq + TB - 1) / TB;
     q0 = (nqt - 1 - it / BHP) * TB;
     bh = (it % BHP) * hp;
+    if constexpr (WIN) {
+        ks = row_stream(p, q0);
+        n = ks.n;
+        return;
+    }
     n = (p.Sk + TB - 1) / TB;
     if (p.causal) {
         const int last = min(q0 + TB - 1, p.Sq - 1) + p.causal_off;
@@ -694,7 +791,7 @@ __device__ __forceinline__ int dq_item_of(int r, int n_items) {
     return it < n_items ? (int)it : -1;
 }
 
-template <int D>
+template <int D, bool WIN>
 __global__ void __launch_bounds__(DQ_THREADS, 1)
 bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constant__ CUtensorMap mk, const BwdProblem p,
                    int hp, int n_items) {
@@ -745,7 +842,8 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
             const int it = dq_item_of(r, n_items);
             if (it < 0) break;
             int q0, bh, n;
-            dq_item(p, hp, it, q0, bh, n);
+            KeyStream ks;
+            dq_item<WIN>(p, hp, it, q0, bh, n, ks);
             const int b = bh / p.Hq, kvh = (bh % p.Hq) / G;
             for (int j = 0; j < n && ok; ++j) {
                 for (int h = 0; h < per; ++h, ++g) {
@@ -756,9 +854,10 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
                     mbar_expect_tx(smem_u32(&full[st]), tile);
                     if (is_ds)   // read once: evict first, so the K tiles and dQ rows stay in L2
                         tma_load_4d_hint(dst, &mds, smem_u32(&full[st]), 0, 0, 0,
-                                         (int)(((long long)(bh + h) * (p.ds_rows / TB) + j) * (p.ds_ld / TB) + q0 / TB),
+                                         WIN ? (int)(((long long)(bh + h) * (p.ds_ld / TB) + q0 / TB) * p.ds_slots + j)
+                                             : (int)(((long long)(bh + h) * (p.ds_rows / TB) + j) * (p.ds_ld / TB) + q0 / TB),
                                          l2_policy_evict_first());
-                    else tma_load_5d(dst, &mk, smem_u32(&full[st]), 0, j * TB, 0, kvh, b);
+                    else tma_load_5d(dst, &mk, smem_u32(&full[st]), 0, (WIN ? ks.tile(j) : j) * TB, 0, kvh, b);
                 }
             }
         }
@@ -774,7 +873,8 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
             const int it = dq_item_of(r, n_items);
             if (it < 0) break;
             int q0, bh, n;
-            dq_item(p, hp, it, q0, bh, n);
+            KeyStream ks;
+            dq_item<WIN>(p, hp, it, q0, bh, n, ks);
             if (n == 0) continue;
             const int buf = a & 1;
             // the epilogue has read this set's previous item
@@ -815,7 +915,8 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
             const int it = dq_item_of(r, n_items);
             if (it < 0) break;
             int q0, bh, n;
-            dq_item(p, hp, it, q0, bh, n);
+            KeyStream ks;
+            dq_item<WIN>(p, hp, it, q0, bh, n, ks);
             const int row = q0 + q4 * 32 + lane;
             const bool row_ok = row < p.Sq;
             const int buf = a & 1;
@@ -852,10 +953,10 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
     }
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
     using C = BtCfg<D>;
-    const cudaError_t attr_err = set_max_dynamic_smem((const void *)bwd_tc_kernel<D>, (int)C::SMEM_BYTES);
+    const cudaError_t attr_err = set_max_dynamic_smem((const void *)bwd_tc_kernel<D, WIN>, (int)C::SMEM_BYTES);
     if (attr_err != cudaSuccess) return attr_err;
     const long long qs = (long long)p.Sq * D, ks = (long long)p.Sk * D;
     CUtensorMap mq, mg, mk, mv;
@@ -864,13 +965,21 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
         !make_bf16_tile_map_strided(&mk, p.k, D, p.Sk, p.Hkv, p.B, D, ks, ks * p.Hkv, TB) ||
         !make_bf16_tile_map_strided(&mv, p.v, D, p.Sk, p.Hkv, p.B, D, ks, ks * p.Hkv, TB))
         return cudaErrorInvalidValue;
-    const unsigned nkv = (unsigned)((p.Sk + TB - 1) / TB) * (unsigned)(p.B * p.Hkv);
+    const int sink_tiles = WIN ? bwd_window_sink_tiles(p.Sk, p.sinks) : 0;
+    const unsigned nkv = (unsigned)((p.Sk + TB - 1) / TB + (WIN ? sink_tiles * (p.sink_parts - 1) : 0)) * (unsigned)(p.B * p.Hkv);
     const unsigned nq = (unsigned)((p.Sq + TB - 1) / TB) * (unsigned)(p.B * p.Hq);
     if ((unsigned long long)nkv + nq >= (1ull << 31)) return cudaErrorInvalidValue;
+    auto sink_sums = [&]() -> cudaError_t {
+        if (!WIN || sink_tiles == 0 || p.sink_parts == 1) return cudaSuccess;
+        const dim3 g((unsigned)(((long long)sink_tiles * TB * D / 4 + 255) / 256), (unsigned)(p.B * p.Hkv), 2);
+        count_launches(1);
+        return launch_dependent(bwd_sink_sum_kernel, g, dim3(256), 0, s, p);
+    };
     if (!p.ds) {
         // dK/dV and dQ CTAs in one grid
-        cudaError_t e = launch_dependent(bwd_tc_kernel<D>, dim3(nkv + nq), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg,
+        cudaError_t e = launch_dependent(bwd_tc_kernel<D, WIN>, dim3(nkv + nq), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg,
                                          mk, mv, mq, p, nkv);   // (no dS stores: the fifth map is unused)
+        if (e == cudaSuccess) e = sink_sums();
         if (e != cudaSuccess) return e;
         count_launches(1);
         return cudaGetLastError();
@@ -878,20 +987,21 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
     // dK/dV CTAs (they also store dS^T), then dQ = scale * dS K as a dependent grid
     using Q = DqCfg<D>;
     CUtensorMap mds, mdst;
-    const long long n_tiles = (long long)p.B * p.Hq * (p.ds_rows / TB) * (p.ds_ld / TB);
+    const long long n_tiles = (long long)p.B * p.Hq * (WIN ? p.ds_slots : p.ds_rows / TB) * (p.ds_ld / TB);
     if (!make_bf16_tile_map(&mds, p.ds, TB, TB, n_tiles, TB, 2) ||
         !make_bf16_store_map_32x32(&mdst, p.ds, TB, TB, n_tiles))
         return cudaErrorInvalidValue;
-    cudaError_t e = set_max_dynamic_smem((const void *)bwd_dq_gemm_kernel<D>, (int)Q::SMEM_BYTES);
+    cudaError_t e = set_max_dynamic_smem((const void *)bwd_dq_gemm_kernel<D, WIN>, (int)Q::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     int sms = 0;
     if (device_sm_count(&sms) != OSF_OK || sms <= 0) return cudaErrorInvalidValue;
-    e = launch_dependent(bwd_tc_kernel<D>, dim3(nkv), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg, mk, mv, mdst, p,
+    e = launch_dependent(bwd_tc_kernel<D, WIN>, dim3(nkv), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg, mk, mv, mdst, p,
                          nkv);
+    if (e == cudaSuccess) e = sink_sums();
     if (e != cudaSuccess) return e;
     const int hp = (p.Hq / p.Hkv) % 2 == 0 ? 2 : 1;   // query heads per item: two of one kv group
     const int n_items = (int)nq / hp;
-    e = launch_dependent(bwd_dq_gemm_kernel<D>, dim3((unsigned)min(sms, n_items)), dim3(DQ_THREADS), Q::SMEM_BYTES, s,
+    e = launch_dependent(bwd_dq_gemm_kernel<D, WIN>, dim3((unsigned)min(sms, n_items)), dim3(DQ_THREADS), Q::SMEM_BYTES, s,
                          mds, mk, p, hp, n_items);
     if (e != cudaSuccess) return e;
     count_launches(2);
@@ -915,7 +1025,25 @@ bool attn_bwd_tc_supported(const BwdProblem &p) {
 }
 
 cudaError_t launch_attn_bwd_tc(const BwdProblem &p, cudaStream_t s) {
-    return p.D == 64 ? launch_t<64>(p, s) : launch_t<128>(p, s);
+    if (p.window) return p.D == 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s);
+    return p.D == 64 ? launch_t<64, false>(p, s) : launch_t<128, false>(p, s);
+}
+
+int bwd_window_slots(int Sk, int window, int sinks) { return key_stream_max(TB, Sk, window, sinks, TB); }
+int bwd_window_sink_tiles(int Sk, int sinks) {
+    const long long tiles = ((long long)sinks + TB - 1) / TB, all = ((long long)Sk + TB - 1) / TB;
+    return (int)(tiles < all ? tiles : all);
+}
+int bwd_window_sink_parts(int B, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count) {
+    const long long tiles = bwd_window_sink_tiles(Sk, sinks);
+    if (tiles == 0) return 1;
+    // parts as long as the walk of a key tile without sinks, as long as they stay within four CTAs to an SM (which bounds
+    // the sums' memory too: 128 KB a CTA at D = 128)
+    const long long q_tiles = ((long long)Sq + TB - 1) / TB, walk = ((long long)window + TB - 1) / TB + 1;
+    long long parts = (q_tiles + walk - 1) / walk;
+    const long long most = (4LL * sm_count + tiles * B * Hkv - 1) / (tiles * B * Hkv);
+    if (parts > most) parts = most;
+    return (int)(parts < 1 ? 1 : parts);
 }
 
 }  // namespace osf

@@ -34,7 +34,8 @@ struct SimtCfg {
 template <typename T>
 __device__ __forceinline__ float ld(const T *p) { return to_f32(*p); }
 
-template <typename T, int DP, int BM>
+// WIN: a window with sinks (AttnProblem::window); the key tiles are then those of the block's key_stream.
+template <typename T, int DP, int BM, bool WIN>
 __global__ void __launch_bounds__(BM * 4)
 attn_simt_kernel(const AttnProblem p) {
     using C = SimtCfg<DP, BM>;
@@ -63,11 +64,15 @@ attn_simt_kernel(const AttnProblem p) {
     const T *Vg = static_cast<const T *>(p.v) + v_at(p, b, kvh, 0);
 
     // key range of this split: a fixed partition of [0, Sk) in whole tiles, clipped by causality
-    const int n_kt_all = (p.Sk + BN - 1) / BN;
+    // (with a window: a partition of the stream's places, of BN keys each)
+    KeyStream ks{};
+    if constexpr (WIN)
+        ks = key_stream(q0 + p.causal_off, min(q0 + BM, p.Sq) - 1 + p.causal_off, p.Sk, p.window, p.sinks, BN);
+    const int n_kt_all = WIN ? ks.n : (p.Sk + BN - 1) / BN;
     const int tps = (n_kt_all + p.splits - 1) / p.splits;
     const int k_begin = split * tps * BN;
-    int k_end = min(p.Sk, (split + 1) * tps * BN);
-    if (p.causal) k_end = min(k_end, max(k_begin, q0 + BM + p.causal_off));
+    int k_end = min(WIN ? ks.n * BN : p.Sk, (split + 1) * tps * BN);
+    if (p.causal && !WIN) k_end = min(k_end, max(k_begin, q0 + BM + p.causal_off));
 
     for (int idx = tid; idx < BM * DP; idx += C::THREADS) {
         const int r = idx / DP, d = idx % DP;
@@ -83,11 +88,13 @@ attn_simt_kernel(const AttnProblem p) {
         for (int c = 0; c < C::OC; ++c) acc[i][c] = 0.f;
     }
 
-    for (int kt0 = k_begin; kt0 < k_end; kt0 += BN) {
+    for (int at = k_begin; at < k_end; at += BN) {
+        const int kt0 = WIN ? ks.tile(at / BN) * BN : at;   // the tile's first key, and the end of the keys that exist
+        const int k_lim = WIN ? p.Sk : k_end;
         __syncthreads();  // previous tile's K/V/P fully consumed (and Q stored, first time)
         for (int idx = tid; idx < BN * DP; idx += C::THREADS) {
             const int c = idx / DP, d = idx % DP;
-            const bool ok = (kt0 + c < k_end) && d < D;
+            const bool ok = (kt0 + c < k_lim) && d < D;
             Ks[d * C::KS + c] = ok ? ld(Kg + (long long)(kt0 + c) * p.k_ss + d) : 0.f;
             Vs[c * DP + d] = ok ? ld(Vg + (long long)(kt0 + c) * p.v_ss + d) : 0.f;
         }
@@ -119,7 +126,8 @@ attn_simt_kernel(const AttnProblem p) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int key = kt0 + tx * 4 + j;
-                const bool valid = key < k_end && (!p.causal || key <= row + p.causal_off);
+                const bool valid = key < k_lim && (!p.causal || key <= row + p.causal_off) &&
+                                   (!WIN || key > row + p.causal_off - p.window || key < p.sinks);
                 s[i][j] = valid ? s[i][j] * p.scale_log2 : -INFINITY;
                 tmax = fmaxf(tmax, s[i][j]);
             }
@@ -411,15 +419,20 @@ __global__ void __launch_bounds__(256) attn_combine_kernel(const AttnProblem p) 
     if (p.lse && c0 == 0) p.lse[row] = L > 0.f ? (M + __log2f(L)) * kLn2 : p.keep_nan && L != L ? L : -INFINITY;
 }
 
-template <typename T, int DP, int BM>
-cudaError_t launch_t(const AttnProblem &p, cudaStream_t s) {
+template <typename T, int DP, int BM, bool WIN>
+cudaError_t launch_w(const AttnProblem &p, cudaStream_t s) {
     using C = SimtCfg<DP, BM>;
-    const cudaError_t e = set_max_dynamic_smem((const void *)attn_simt_kernel<T, DP, BM>, (int)C::SMEM_BYTES);
+    const cudaError_t e = set_max_dynamic_smem((const void *)attn_simt_kernel<T, DP, BM, WIN>, (int)C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     dim3 grid((p.Sq + BM - 1) / BM, p.B * p.Hq, p.splits);
-    attn_simt_kernel<T, DP, BM><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p);
+    attn_simt_kernel<T, DP, BM, WIN><<<grid, C::THREADS, C::SMEM_BYTES, s>>>(p);
     count_launches(1);
     return cudaGetLastError();
+}
+
+template <typename T, int DP, int BM>
+cudaError_t launch_t(const AttnProblem &p, cudaStream_t s) {
+    return p.window ? launch_w<T, DP, BM, true>(p, s) : launch_w<T, DP, BM, false>(p, s);
 }
 
 template <typename T>
@@ -436,7 +449,7 @@ int block_m(int D) { return D <= 128 ? 64 : 32; }
 // Problems the few-rows kernel runs: float32, D <= 64, at most kRowsSk keys, at most 2048 query
 // rows in all (512 CTAs, each staging its kv head's K and V).
 bool rows_eligible(const AttnProblem &p) {
-    return p.dtype == OSF_F32 && p.D <= 64 && p.Sk <= kRowsSk && (long long)p.B * p.Hq * p.Sq <= 2048;
+    return p.dtype == OSF_F32 && !p.window && p.D <= 64 && p.Sk <= kRowsSk && (long long)p.B * p.Hq * p.Sq <= 2048;
 }
 
 template <int DP>
@@ -460,7 +473,7 @@ int attn_simt_pick_splits(const AttnProblem &p, int sm_count) {
     if (rows_eligible(p)) return 1;
     const int BM = block_m(p.D);
     const long long ctas = (long long)((p.Sq + BM - 1) / BM) * p.B * p.Hq;
-    const int n_kt = (p.Sk + BN - 1) / BN;
+    const int n_kt = p.window ? key_stream_max(BM, p.Sk, p.window, p.sinks, BN) : (p.Sk + BN - 1) / BN;
     if (ctas >= 2LL * sm_count || n_kt <= 1) return 1;
     long long want = (2LL * sm_count + ctas - 1) / ctas;
     if (want > n_kt) want = n_kt;

@@ -119,12 +119,30 @@ __device__ __forceinline__ void settle_copies() {
 }
 
 // One work item: 2 x 128 query rows of one (b, q-head), over the key tiles of this CTA's split.
+// With a window the key tiles are places kt_begin .. of the stream of tiles that the block's rows see (key_stream); of
+// those, Q tile 1 leaves out the places gap0 .. gap1 - 1, which lie before its window, and begins with place first1.
 struct Item {
     int q0, bh, b, hq, kvh, ntiles, n0, n1, n_kv, kt_begin;
+    int gap0, gap1, first1;
+    KeyStream ks;
 };
+
+// First key of the item's key tile i, and whether Q tile t takes part in it, and the first in which it does.
+template <bool WIN>
+__device__ __forceinline__ int key_at(const Item &w, int i) {
+    return (WIN ? w.ks.tile(w.kt_begin + i) : w.kt_begin + i) * BN;
+}
+template <bool WIN>
+__device__ __forceinline__ bool takes(const Item &w, int t, int i) {
+    if (t == 0) return i < w.n0;
+    return i < w.n1 && !(WIN && i >= w.gap0 && i < w.gap1);
+}
+template <bool WIN>
+__device__ __forceinline__ int first_of(const Item &w, int t) { return WIN && t ? w.first1 : 0; }
 
 // Item of round r for this CTA: rounds walk the item list in snake order (forward on even
 // rounds, backward on odd ones), which pairs heavy causal blocks with light ones.
+template <bool WIN>
 __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_items, int r, Item &w) {
     const int g = (int)gridDim.x;
     const int c = (r & 1) ? g - 1 - (int)blockIdx.x : (int)blockIdx.x;
@@ -139,6 +157,29 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
     w.hq = w.bh % p.Hq;
     w.kvh = w.hq / (p.Hq / p.Hkv);
     w.ntiles = (w.q0 + BM < p.Sq) ? 2 : 1;
+    if constexpr (WIN) {
+        // the stream of both tiles' rows, cut into the splits; tile 1's window begins at most one key tile later
+        const int pos0 = w.q0 + p.causal_off, last = min(w.q0 + 2 * BM, p.Sq) - 1 + p.causal_off;
+        w.ks = key_stream(pos0, last, p.Sk, p.window, p.sinks, BN);
+        const int n_all = w.ks.n, tps = (n_all + p.splits - 1) / p.splits;
+        w.kt_begin = min(n_all, (int)blockIdx.y * tps);
+        const int end = min(n_all, w.kt_begin + tps);
+        const KeyStream k0 = key_stream(pos0, min(w.q0 + BM, p.Sq) - 1 + p.causal_off, p.Sk, p.window, p.sinks, BN);
+        w.n0 = max(0, min(end, k0.n) - w.kt_begin);
+        w.n1 = w.gap0 = w.gap1 = w.first1 = 0;
+        if (w.ntiles == 2) {
+            const KeyStream k1 = key_stream(pos0 + BM, last, p.Sk, p.window, p.sinks, BN);
+            const int sink_tiles = (p.sinks - 1 + BN) / BN;
+            w.n1 = end - w.kt_begin;
+            w.gap0 = w.ks.ns + max(0, sink_tiles - w.ks.ws) - w.kt_begin;
+            w.gap1 = max(w.gap0, w.ks.ns + k1.ws - w.ks.ws - w.kt_begin);
+            if (w.gap0 < w.n1 && w.gap1 >= w.n1) w.n1 = max(0, w.gap0);   // the part ends inside the gap
+            if (w.gap0 <= 0 && w.gap1 > 0) w.first1 = min(w.gap1, w.n1);    // it begins there
+            if (w.first1 >= w.n1) w.n1 = 0;
+        }
+        w.n_kv = max(w.n0, w.n1);
+        return true;
+    }
     const int n_kt_all = (p.Sk + BN - 1) / BN;
     const int tps = (n_kt_all + p.splits - 1) / p.splits;
     w.kt_begin = blockIdx.y * tps;
@@ -164,7 +205,8 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
 // MERGE (key splits, one item per CTA): the CTAs of a thread-block cluster run the splits of one
 // item and merge their results through distributed shared memory at the end, instead of writing
 // partial states for a separate combine kernel.
-template <int D, bool X3, bool MERGE>
+// WIN: a window with sinks (AttnProblem::window).
+template <int D, bool X3, bool MERGE, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mqm,
@@ -239,7 +281,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         bool ok = true;
         int gt = 0, qc = 0;   // key tiles streamed so far, Q loads so far
         Item w;
-        for (int r = 0; ok && item_at(p, n_qb, n_items, r, w); ++r) {
+        for (int r = 0; ok && item_at<WIN>(p, n_qb, n_items, r, w); ++r) {
             if (w.n_kv == 0) continue;
             if (!odd) {
                 ok = mbar_wait(smem_u32(&bars.q_empty), (qc & 1) ^ 1, &abort_flag);
@@ -261,7 +303,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (!ok) break;
                     mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
                     const CUtensorMap *mp = part == 0 ? map : (part == 2 || odd) ? map_lo : &mkm;
-                    tma_load_5d(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), 0, (w.kt_begin + j) * BN, 0,
+                    tma_load_5d(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), 0, key_at<WIN>(w, j), 0,
                                 w.kvh, w.b);
                 }
             }
@@ -373,23 +415,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         // PV for Q tile t at key tile i of an item; pc[t] counts P handshakes, oe[t] the O
         // hand-backs owed by earlier items
         int pc[2] = {0, 0}, oe[2] = {0, 0};
-        auto pv_step = [&](int t, int i, int nt, int sv) -> bool {
-            if (i == 0 && oe[t] > 0 &&
+        auto pv_step = [&](int t, int i, int first, int nt, int sv) -> bool {
+            if (i == first && oe[t] > 0 &&
                 !mbar_wait_spin(smem_u32(&bars.o_empty[t]), (oe[t] - 1) & 1, &abort_flag))
                 return false;
             if (!mbar_wait_spin(smem_u32(&bars.p_full[t]), pc[t] & 1, &abort_flag)) return false;
             ++pc[t];
             tc_fence_after();
-            issue_pv(t, sv, i > 0);
+            issue_pv(t, sv, i > first);
             if (i == nt - 1) mma_commit(smem_u32(&bars.o_final[t]));
             return true;
         };
         bool ok = true;
         int gt = 0, qc = 0;
         Item w;
-        for (int r = 0; ok && item_at(p, n_qb, n_items, r, w); ++r) {
+        for (int r = 0; ok && item_at<WIN>(p, n_qb, n_items, r, w); ++r) {
             if (w.n_kv == 0) continue;
-            const int n0 = w.n0, n1 = w.n1, n_kv = w.n_kv;
+            const int n0 = w.n0, n1 = w.n1, n_kv = w.n_kv, first1 = first_of<WIN>(w, 1);
             ok = mbar_wait_spin(smem_u32(&bars.q_full), qc & 1, &abort_flag);
             ++qc;
             const int sk0 = stage_of(C::NPOS * gt);
@@ -400,7 +442,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 issue_s(0, sk0);
                 mma_commit(smem_u32(&bars.s_full[0]));
             }
-            if (n1 > 0) {
+            if (takes<WIN>(w, 1, 0)) {
                 issue_s(1, sk0);
                 mma_commit(smem_u32(&bars.s_full[1]));
             }
@@ -416,7 +458,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 const bool more = i + 1 < n_kv;
                 ok = wait_parts(sv, phv, C::VP);
                 if (!ok) break;
-                if (i < n0 && !(ok = pv_step(0, i, n0, sv))) break;
+                if (i < n0 && !(ok = pv_step(0, i, 0, n0, sv))) break;
                 if (more) {
                     ok = wait_parts(sk, phk, C::KP);
                     if (!ok) break;
@@ -426,10 +468,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         mma_commit(smem_u32(&bars.s_full[0]));
                     }
                 }
-                if (i < n1 && !(ok = pv_step(1, i, n1, sv))) break;
+                if (takes<WIN>(w, 1, i) && !(ok = pv_step(1, i, first1, n1, sv))) break;
                 release_parts(sv, C::VP);
                 if (more) {
-                    if (i + 1 < n1) {
+                    if (takes<WIN>(w, 1, i + 1)) {
                         issue_s(1, sk);
                         mma_commit(smem_u32(&bars.s_full[1]));
                     }
@@ -462,23 +504,32 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         bool ok = true;
         int sc = 0, oc = 0;   // S handshakes and finished O tiles so far
         Item w;
-        for (int rr = 0; ok && item_at(p, n_qb, n_items, rr, w); ++rr) {
+        for (int rr = 0; ok && item_at<WIN>(p, n_qb, n_items, rr, w); ++rr) {
             const int nt = t ? w.n1 : w.n0;
             const int row_first = w.q0 + t * BM;   // first row of this tile
             const int row = row_first + r;
             float m_ref = -INFINITY, l = 0.f;
-            for (int i = 0; i < nt; ++i) {
+            for (int i = first_of<WIN>(w, t); i < nt; ++i) {
+                if (WIN && !takes<WIN>(w, t, i)) continue;
                 ok = mbar_wait(smem_u32(&bars.s_full[t]), sc & 1, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ++sc;
                 tc_fence_after();
-                const int key0 = (w.kt_begin + i) * BN;
-                const bool need_mask = (key0 + BN > p.Sk) || (p.causal && key0 + BN - 1 > row_first + p.causal_off);
+                const int key0 = key_at<WIN>(w, i);
+                bool need_mask = (key0 + BN > p.Sk) || (p.causal && key0 + BN - 1 > row_first + p.causal_off);
                 // column j of the tile (key key0 + j) is kept iff j < lim: inside the sequence
                 // and, when causal, not after the last key this row sees
                 int lim = p.Sk - key0;
                 if (p.causal) lim = min(lim, row + p.causal_off - key0 + 1);
+                // with a window: and iff j >= low or j < snk
+                int low = 0, snk = 0;
+                if constexpr (WIN) {
+                    low = row + p.causal_off - p.window + 1 - key0;
+                    snk = p.sinks - key0;
+                    need_mask = need_mask || (key0 + p.window <= row_first + BM - 1 + p.causal_off && key0 + BN > p.sinks);
+                }
+                auto hidden = [&](int j) { return j >= lim || (WIN && j < low && j >= snk); };
                 uint32_t sr[X3 ? 1 : 4][32];   // bf16 mode: the whole score row in registers
                 float mx;
                 if constexpr (X3) {
@@ -491,7 +542,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            const float x = (need_mask && c * 32 + k >= lim) ? -INFINITY : __uint_as_float(sr[0][k]);
+                            const float x = (need_mask && hidden(c * 32 + k)) ? -INFINITY : __uint_as_float(sr[0][k]);
                             m4[k & 3] = fmaxf(m4[k & 3], x);
                         }
                     }
@@ -505,7 +556,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (c * 32 + k >= lim) sr[c][k] = __float_as_uint(-INFINITY);
+                                if (hidden(c * 32 + k)) sr[c][k] = __float_as_uint(-INFINITY);
                     }
                     // row max: eight independent chains of 3-input max, then a short tree
                     float mm[8];
@@ -544,9 +595,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         uint32_t ph[16], pl[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float s0 = (need_mask && c * 32 + 2 * k >= lim) ? -INFINITY : __uint_as_float(sr[0][2 * k]);
-                            const float s1 = (need_mask && c * 32 + 2 * k + 1 >= lim) ? -INFINITY
-                                                                                     : __uint_as_float(sr[0][2 * k + 1]);
+                            const float s0 = (need_mask && hidden(c * 32 + 2 * k)) ? -INFINITY : __uint_as_float(sr[0][2 * k]);
+                            const float s1 = (need_mask && hidden(c * 32 + 2 * k + 1)) ? -INFINITY
+                                                                                       : __uint_as_float(sr[0][2 * k + 1]);
                             float p0, p1;
                             f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), p0, p1);
                             p0 = ex2_approx(p0);
@@ -602,7 +653,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     f2_unpack(a2, lo, hi);
                     rs = lo + hi;
                 }
-                if (rescale && i > 0) {
+                if (rescale && i > first_of<WIN>(w, t)) {
                     // O_t += P V of earlier tiles has completed: the commit that signalled s_full
                     // for this tile covers every MMA issued before it.  The PV MMA of this tile
                     // waits for p_full, signalled below, after the rescaled O is stored.
@@ -795,7 +846,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
         const int rank = (int)cluster_ctarank();
         const int R = (2 * BM + ns - 1) / ns;
         Item w;
-        item_at(p, n_qb, n_items, 0, w);
+        item_at<WIN>(p, n_qb, n_items, 0, w);
         for (int task = tid; task < R * CH; task += NTHREADS) {
             const int rl = rank * R + task / CH, ch = task % CH;
             const int row = w.q0 + rl;
@@ -916,14 +967,14 @@ __global__ void __launch_bounds__(256) split_parts_kernel(const AttnProblem p, _
     }
 }
 
-template <int D, bool X3, bool MERGE>
+template <int D, bool X3, bool MERGE, bool WIN>
 cudaError_t set_smem_attr() {
-    return set_max_dynamic_smem((const void *)attn_tc_kernel<D, X3, MERGE>, (int)TcCfg<D, X3>::SMEM_BYTES);
+    return set_max_dynamic_smem((const void *)attn_tc_kernel<D, X3, MERGE, WIN>, (int)TcCfg<D, X3>::SMEM_BYTES);
 }
 
 // Whether `clusters` clusters of `ns` CTAs of the merging kernel can all run at once (one wave;
 // otherwise the splits are merged by the combine kernel).  Cached per device and cluster size.
-template <int D, bool X3>
+template <int D, bool X3, bool WIN>
 bool merge_fits(int clusters, int ns) {
     static std::mutex mu;
     static std::map<std::pair<int, int>, int> most;   // (device, ns) -> clusters resident at once
@@ -947,7 +998,7 @@ bool merge_fits(int clusters, int ns) {
         cfg.attrs = &a;
         cfg.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, attn_tc_kernel<D, X3, true>, &cfg) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, attn_tc_kernel<D, X3, true, WIN>, &cfg) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
@@ -957,11 +1008,11 @@ bool merge_fits(int clusters, int ns) {
 }
 
 // `merged`: the key splits were merged inside the kernel (no combine kernel needed).
-template <int D, bool X3>
-cudaError_t launch_t(const AttnProblem &p, const CUtensorMap (&m)[8], int sm_count, cudaStream_t s, bool &merged) {
+template <int D, bool X3, bool WIN>
+cudaError_t launch_w(const AttnProblem &p, const CUtensorMap (&m)[8], int sm_count, cudaStream_t s, bool &merged) {
     using C = TcCfg<D, X3>;
     merged = false;
-    cudaError_t attr_err = set_smem_attr<D, X3, false>();
+    cudaError_t attr_err = set_smem_attr<D, X3, false, WIN>();
     if (attr_err != cudaSuccess) return attr_err;
     const int n_qb = (p.Sq + 2 * BM - 1) / (2 * BM);
     const long long items = (long long)n_qb * p.B * p.Hq;
@@ -971,24 +1022,29 @@ cudaError_t launch_t(const AttnProblem &p, const CUtensorMap (&m)[8], int sm_cou
     const dim3 g((unsigned)grid, (unsigned)p.splits);
     // key splits of few items: a cluster per item when its splits fit one (portable size 8)
     // and all clusters run at once
-    if (p.splits > 1 && p.splits <= 8 && items < sm_count && set_smem_attr<D, X3, true>() == cudaSuccess &&
-        merge_fits<D, X3>(grid, p.splits)) {
-        cudaError_t e = launch_clustered(attn_tc_kernel<D, X3, true>, g, dim3(NTHREADS), C::SMEM_BYTES, s,
+    if (p.splits > 1 && p.splits <= 8 && items < sm_count && set_smem_attr<D, X3, true, WIN>() == cudaSuccess &&
+        merge_fits<D, X3, WIN>(grid, p.splits)) {
+        cudaError_t e = launch_clustered(attn_tc_kernel<D, X3, true, WIN>, g, dim3(NTHREADS), C::SMEM_BYTES, s,
                                          dim3(1, (unsigned)p.splits, 1), X3, m[0], m[1], m[2], m[3], m[4], m[5], m[6],
                                          m[7], p, n_qb, (int)items);
         if (e != cudaSuccess) return e;
         merged = true;
     } else if (X3) {
         // dependent of the split pre-pass (see the producers' griddep_wait)
-        cudaError_t e = launch_dependent(attn_tc_kernel<D, X3, false>, g, dim3(NTHREADS), C::SMEM_BYTES, s, m[0],
+        cudaError_t e = launch_dependent(attn_tc_kernel<D, X3, false, WIN>, g, dim3(NTHREADS), C::SMEM_BYTES, s, m[0],
                                          m[1], m[2], m[3], m[4], m[5], m[6], m[7], p, n_qb, (int)items);
         if (e != cudaSuccess) return e;
     } else {
-        attn_tc_kernel<D, X3, false><<<g, NTHREADS, C::SMEM_BYTES, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7],
+        attn_tc_kernel<D, X3, false, WIN><<<g, NTHREADS, C::SMEM_BYTES, s>>>(m[0], m[1], m[2], m[3], m[4], m[5], m[6], m[7],
                                                                          p, n_qb, (int)items);
     }
     count_launches(1);
     return cudaGetLastError();
+}
+
+template <int D, bool X3>
+cudaError_t launch_t(const AttnProblem &p, const CUtensorMap (&m)[8], int sm_count, cudaStream_t s, bool &merged) {
+    return p.window ? launch_w<D, X3, true>(p, m, sm_count, s, merged) : launch_w<D, X3, false>(p, m, sm_count, s, merged);
 }
 
 // bf16 inputs: maps on the caller's tensors (the part maps are unused copies).
@@ -1067,7 +1123,7 @@ size_t attn_tc_extra_bytes(const AttnProblem &p) {
 
 int attn_tc_pick_splits(const AttnProblem &p, int sm_count) {
     const long long ctas = tc_ctas(p);
-    const int n_kt = (p.Sk + BN - 1) / BN;
+    const int n_kt = p.window ? key_stream_max(2 * BM, p.Sk, p.window, p.sinks, BN) : (p.Sk + BN - 1) / BN;
     if (ctas >= sm_count || n_kt <= 1) return 1;
     // as many splits as keep every CTA in one wave (one CTA per SM): a second wave would cost
     // more than the extra split saves

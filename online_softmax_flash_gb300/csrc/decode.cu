@@ -17,6 +17,8 @@
 // rows padded to 16, then the S accumulator fragments are reused in registers as the P operand
 // of O += P V.  At the end the four warps' states are merged through shared memory.  With
 // Sq > 1 the 16 rows hold G heads x Sq query rows, each with its own causal key limit.
+#include <algorithm>
+
 #include "decode.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.cuh"
@@ -52,7 +54,8 @@ __device__ __forceinline__ uint32_t ld_bf16x2(const __nv_bfloat16 *p) {
     return *reinterpret_cast<const uint32_t *>(p);
 }
 
-template <int D>
+// WIN: a window with sinks (AttnProblem::window); the tiles are then those of the rows' key_stream.
+template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 2)
 decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
               const AttnProblem p, int tps) {
@@ -68,11 +71,14 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     const int split = blockIdx.y;
     const int G = p.Hq / p.Hkv;
     const int b = kvbh / p.Hkv, kvh = kvbh % p.Hkv;
-    const int n_kt_all = (p.Sk + KT - 1) / KT;
+    KeyStream ks{};
+    if constexpr (WIN) ks = key_stream(p.causal_off, p.causal_off + p.Sq - 1, p.Sk, p.window, p.sinks, KT);
+    const int n_kt_all = WIN ? ks.n : (p.Sk + KT - 1) / KT;
     const int t_begin = split * tps;
+    auto key_at = [&](int i) { return (WIN ? ks.tile(t_begin + i) : t_begin + i) * KT; };   // first key of tile i
     const int t_end = min(n_kt_all, t_begin + tps);
     const int ntile = max(0, t_end - t_begin);
-    const int key_end = min(p.Sk, t_end * KT);
+    const int key_end = WIN ? p.Sk : min(p.Sk, t_end * KT);
 
     if (tid == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -99,7 +105,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&full[st]);
                 mbar_expect_tx(bar, C::TILE);
-                tma_load_5d(ring + st * C::TILE, map, bar, 0, (t_begin + i) * KT, 0, kvh, b);
+                tma_load_5d(ring + st * C::TILE, map, bar, 0, key_at(i), 0, kvh, b);
                 issued = i + 1;
             }
             if (!ok) {
@@ -133,6 +139,8 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     // last key each of this thread's two rows may see (exclusive bound)
     const int lim0 = p.causal ? min(key_end, r0 % p.Sq + p.causal_off + 1) : key_end;
     const int lim1 = p.causal ? min(key_end, r1 % p.Sq + p.causal_off + 1) : key_end;
+    // with a window: the first key that they see, but for the sinks
+    const int low0 = r0 % p.Sq + p.causal_off - p.window + 1, low1 = r1 % p.Sq + p.causal_off - p.window + 1;
     float o[C::NT][4];
 #pragma unroll
     for (int j = 0; j < C::NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -160,13 +168,14 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
             mma_m16n8k16_bf16(s[1], qa[kk], b2, b3);
         }
         // scale to base 2, mask keys past this chunk's end
-        const int key_g = (t_begin + i) * KT + kb + kc;
+        const int key_g = key_at(i) + kb + kc;
         float mx0 = -INFINITY, mx1 = -INFINITY;
 #pragma unroll
         for (int n = 0; n < 2; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const bool valid = key_g + n * 8 + (e & 1) < (e < 2 ? lim0 : lim1);
+                const int key = key_g + n * 8 + (e & 1);
+                const bool valid = key < (e < 2 ? lim0 : lim1) && (!WIN || key >= (e < 2 ? low0 : low1) || key < p.sinks);
                 s[n][e] = valid ? s[n][e] * sl2 : -INFINITY;
                 if (e < 2) mx0 = fmaxf(mx0, s[n][e]); else mx1 = fmaxf(mx1, s[n][e]);
             }
@@ -269,17 +278,23 @@ bool make_maps(const AttnProblem &p, CUtensorMap *mk, CUtensorMap *mv) {
            make_bf16_tile_map_strided(mv, p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb, KT);
 }
 
-template <int D>
+// Key tiles that a call goes through.
+int key_tiles(const AttnProblem &p) {
+    if (p.window) return key_stream(p.causal_off, p.causal_off + p.Sq - 1, p.Sk, p.window, p.sinks, KT).n;
+    return (p.Sk + KT - 1) / KT;
+}
+
+template <int D, bool WIN>
 cudaError_t launch_t(const AttnProblem &p, cudaStream_t s) {
     using C = DecCfg<D>;
-    const cudaError_t attr_err = set_max_dynamic_smem((const void *)decode_kernel<D>, (int)C::SMEM);
+    const cudaError_t attr_err = set_max_dynamic_smem((const void *)decode_kernel<D, WIN>, (int)C::SMEM);
     if (attr_err != cudaSuccess) return attr_err;
     CUtensorMap mk, mv;
     if (!make_maps(p, &mk, &mv)) return cudaErrorInvalidValue;
-    const int n_kt = (p.Sk + KT - 1) / KT;
+    const int n_kt = key_tiles(p);
     const int tps = (n_kt + p.splits - 1) / p.splits;
     dim3 grid((unsigned)(p.B * p.Hkv), (unsigned)p.splits);
-    decode_kernel<D><<<grid, NTHREADS, C::SMEM, s>>>(mk, mv, p, tps);
+    decode_kernel<D, WIN><<<grid, NTHREADS, C::SMEM, s>>>(mk, mv, p, tps);
     count_launches(1);
     return cudaGetLastError();
 }
@@ -299,7 +314,7 @@ bool decode_supported(const AttnProblem &p, const void *Q, const void *K, const 
 }
 
 int decode_pick_splits(const AttnProblem &p, int sm_count, int requested) {
-    const int n_kt = (p.Sk + KT - 1) / KT;
+    const int n_kt = std::max(1, key_tiles(p));
     int s;
     if (requested > 0) {
         s = requested;
@@ -317,7 +332,8 @@ int decode_pick_splits(const AttnProblem &p, int sm_count, int requested) {
 }
 
 cudaError_t launch_decode(const AttnProblem &p, cudaStream_t s) {
-    cudaError_t e = p.D == 64 ? launch_t<64>(p, s) : launch_t<128>(p, s);
+    cudaError_t e = p.window ? p.D == 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s)
+                             : p.D == 64 ? launch_t<64, false>(p, s) : launch_t<128, false>(p, s);
     if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     return e;
 }

@@ -69,6 +69,8 @@ struct AttnProblem {
     int B, Hq, Hkv, Sq, Sk, D;
     int causal;          // 1: key j is visible to query row i iff j <= i + causal_off
     int causal_off;      // 0 (top-left) or Sk - Sq (bottom-right)
+    // 0, or (with causal = 1, causal_off = Sk - Sq): of those keys only j > i + causal_off - window or j < sinks
+    int window, sinks;
     float scale_log2;    // scale * log2(e)
     // element strides of the b, h and s dimensions of Q, K, V, O (d is contiguous)
     long long q_sb, q_sh, q_ss, k_sb, k_sh, k_ss, v_sb, v_sh, v_ss, o_sb, o_sh, o_ss;
@@ -92,6 +94,31 @@ __host__ __device__ __forceinline__ long long v_at(const AttnProblem &p, int b, 
 }
 __host__ __device__ __forceinline__ long long o_at(const AttnProblem &p, int b, int h, long long s) {
     return b * p.o_sb + h * p.o_sh + s * p.o_ss;
+}
+
+// The key tiles of `tile` keys that some row of a block sees under a window with sinks: tiles 0 .. ns - 1 (sinks that lie
+// before the window), then ws, ws + 1, ...; n in all.  pos_lo, pos_hi: the positions (row + Sk - Sq) of the block's first
+// and last row.  n = 0: the block lies before the first key.
+struct KeyStream {
+    int ns, ws, n;
+    // the tile at place i of the stream, and the place of a tile that is in it
+    __host__ __device__ __forceinline__ int tile(int i) const { return i < ns ? i : i - ns + ws; }
+    __host__ __device__ __forceinline__ int place(int t) const { return t < ns ? t : t - ws + ns; }
+};
+__host__ __device__ __forceinline__ KeyStream key_stream(int pos_lo, int pos_hi, int Sk, int window, int sinks, int tile) {
+    KeyStream k;
+    const int n_kt = (Sk - 1) / tile + 1;
+    const int end = pos_hi < 0 ? 0 : pos_hi / tile + 1, first = pos_lo - window + 1, sink_tiles = (sinks - 1 + tile) / tile;
+    k.ws = first > 0 ? first / tile : 0;
+    k.ns = sink_tiles < k.ws ? sink_tiles : k.ws;
+    k.n = pos_hi < 0 ? 0 : k.ns + (end < n_kt ? end : n_kt) - k.ws;
+    return k;
+}
+// The most tiles that the stream of any `rows` consecutive rows has.
+inline int key_stream_max(int rows, int Sk, int window, int sinks, int tile) {
+    const long long n_kt = ((long long)Sk + tile - 1) / tile, sink_tiles = ((long long)sinks + tile - 1) / tile;
+    const long long n = sink_tiles + ((long long)window + rows - 1 + tile - 2) / tile + 1;
+    return (int)(n < n_kt ? n : n_kt);
 }
 
 // SM count of the current device, looked up once per device (the same value every entry point

@@ -29,9 +29,11 @@ from .kv_cache import attention_records, evict, key_weights, quantise_group, rec
 from .softmax import softmax, softmax_masked
 from .recurrence import (combine_partials, online_attention_row, online_softmax,
                          online_softmax_state)
+from .window import attention_window, window_mask
 
 __all__ = [
     "attention", "attention_gqa", "attention_rows", "attention_bwd", "attention_gqa_bwd", "softmax",
     "softmax_masked", "attention_records", "evict", "key_weights", "quantise_group", "record_values", "records", "visible",
+    "attention_window", "window_mask",
     "online_softmax_state", "online_softmax", "online_attention_row", "combine_partials",
 ]
