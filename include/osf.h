@@ -346,6 +346,76 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
                                  int with_weights, size_t *bytes);
 
 /*
+ * The paged 8-bit K/V cache (not on the pages, which keep K and V in their input type and in one piece).
+ * pages:  device array [n_pages, 2, Hkv, P, D] of e4m3 codes, K's and then V's, of P = page_tokens tokens (16, 32, 64 or
+ *         128); D a multiple of 32 up to 256; 16-byte aligned.
+ * scales: device float32 [n_pages, 2, Hkv], a power of two for each page, kv head, and K or V.  A value is code * scale.
+ *         (A scale that is no power of two counts as the next one below.)
+ * table:  device int32 [B, table_len]: the page that holds tokens P i .. P i + P - 1 of a sequence.  Entries for tokens that a
+ *         call neither writes nor sees are not read.
+ * lens:   device int32 [B], the tokens of each sequence.
+ * The scale of a page is 2^e with the least e >= -110 for which its largest finite magnitude is at most 448 * 2^e, and codes
+ * are round(x / scale) to the nearest e4m3, ties to even: a value is off by at most 2^-4 of itself, or by 2^-10 * scale where
+ * that is more.  NaN and infinities are stored as NaN.  (From 2^127 * 1.9375 on a value reads back as infinity.)
+ * An entry that is no page of the cache, and a length outside [0, table_len * P], are recorded as OSF_ERR_INVALID in the
+ * device status word (osf_device_status); the tokens of such an entry are neither stored nor seen, such a length is cut.
+ */
+
+/*
+ * osf_kv8_append -- store the rows K, V [B, Hkv, n, D] (of `dtype`) as tokens lens[b] .. lens[b] + n - 1 of each sequence
+ * (lens NULL: from 0), K rotated by its position on the way.  counts: NULL, or the number of new tokens of each sequence
+ * (0 .. n; the rows behind them are padding and are not read).
+ * A page that a sequence's first token falls into (slot 0 is new) gets its scale from the new tokens alone.  A page that
+ * holds earlier tokens keeps its scale, unless the new ones need a larger one: then the codes there are rounded again, to
+ * the new scale.  Two sequences of a call must not write to the same page.  Slots that hold no token of the sequence are
+ * left as they were.
+ * Rotation: cos_table, sin_table: float32 [max_positions, rotary_dim / 2] (rotary_dim 0: none; a multiple of 8, at most D):
+ *     (a, b) -> (a cos - b sin, b cos + a sin), rounded once to float32, for channels i and i + rotary_dim / 2, or with
+ *     interleaved 2 i and 2 i + 1, at position lens[b] + t.  Channels from rotary_dim on are stored as they are.
+ * Q, Q_out: NULL, or queries [B, Hq, n, D] of the same tokens, rotated the same way and rounded to `dtype`; Q_out may be Q
+ *     (with the same strides).  Rows at and behind counts[b] are left as they were.
+ * strides: NULL (contiguous), or 6 element strides, K: b, h, s  V: b, h, s, and with Q 6 more, Q: b, h, s  Q_out: b, h, s.
+ * Tokens that would fall behind table_len * P are not stored, and recorded as OSF_ERR_INVALID in the device status word, as
+ * are counts out of range (cut to it), a negative length (nothing of that sequence is stored) and positions that the tables
+ * do not hold (the last one is taken).
+ * n == 0 or B == 0: OSF_OK.  n > table_len * P without counts, outputs that overlap an input, NULL pointers: OSF_ERR_INVALID.
+ */
+int osf_kv8_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D,
+                   const long long *strides, void *pages, float *scales, int n_pages, int page_tokens,
+                   const int *table, int table_len, const int *lens, const int *counts,
+                   const float *cos_table, const float *sin_table, int max_positions, int rotary_dim,
+                   int interleaved, const void *Q, void *Q_out, int Hq, osf_stream stream);
+
+/*
+ * osf_kv8_read -- the values of tokens starts[b] .. starts[b] + n - 1 (starts NULL: from 0) as contiguous K, V
+ * [B, Hkv, n, D] of `dtype` (K as it was stored: rotated); positions at or behind lens[b] (NULL: table_len * P), or below 0,
+ * give zeros.  E.g. to run osf_attn_fwd_gqa_window for a prompt's later pieces over the stored ones.
+ */
+int osf_kv8_read(const void *pages, const float *scales, int n_pages, int page_tokens, const int *table,
+                 int table_len, void *K, void *V, int dtype, int B, int Hkv, int n, int D, const int *starts,
+                 const int *lens, osf_stream stream);
+
+/*
+ * osf_attn_kv8 -- attention of the last Sq tokens of each sequence over its pages (the operation of
+ * osf_attn_fwd_gqa_window, with K and V the values that the pages stand for): row i stands at position p = lens[b] - Sq + i
+ * and sees token j where j <= p and, with window > 0, (p - j < window or j < sinks).
+ * Q, O: [B, Hq, Sq, D] of `dtype`; lens: NULL (table_len * P each) or the tokens of each sequence.
+ * window: 0 (none) or at least 1; sinks >= 0 (without a window of no effect).  Pages that no row sees are not read.
+ * strides: NULL (contiguous) or 6 element strides, Q: b, h, s  O: b, h, s, under the rules of osf_attn_fwd_gqa_ex.
+ * A row that sees nothing gets O = 0 and lse = -inf.
+ * lse: optional contiguous float32 [B, Hq, Sq]; of a row that sees a score of NaN or +inf: NaN, as its O.
+ * workspace: osf_attn_kv8_workspace_bytes bytes, 16-byte aligned.
+ * (Hq / Hkv) * Sq <= 32768, else OSF_ERR_UNSUPPORTED.  Outputs must not overlap one another or an input -> else
+ * OSF_ERR_INVALID.  B == 0 or Sq == 0: OSF_OK, nothing written.
+ */
+int osf_attn_kv8(const void *Q, const void *pages, const float *scales, void *O, int dtype, int B, int Hq,
+                 int Hkv, int Sq, int n_pages, int page_tokens, int D, const long long *strides,
+                 const int *table, int table_len, const int *lens, int window, int sinks, float scale,
+                 float *lse, void *workspace, size_t workspace_bytes, osf_stream stream);
+int osf_attn_kv8_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int D, int page_tokens,
+                                 int table_len, int window, int sinks, size_t *bytes);
+
+/*
  * osf_kv_evict -- shrink a K/V cache to `budget` keys per (batch, kv head) by accumulated attention
  * weight (not on the pages).  Of the n = lens[b] valid keys of each (b, kv head) (lens NULL: S): all,
  * when n <= budget; else the first `sinks`, the last `recent`, and of those between the

@@ -24,6 +24,7 @@ __all__ = [
     "osf_attn_fwd_gqa_window", "osf_attn_window_workspace_bytes", "osf_attn_bwd_gqa_window",
     "osf_attn_bwd_window_workspace_bytes",
     "osf_attn_key_weights", "osf_attn_key_weights_workspace_bytes", "osf_kv4_record_bytes", "osf_kv4_append",
+    "osf_kv8_append", "osf_kv8_read", "osf_attn_kv8", "osf_attn_kv8_workspace_bytes",
     "osf_kv4_read", "osf_attn_kv4", "osf_attn_kv4_workspace_bytes", "osf_kv_evict",
 ]
 
@@ -65,6 +66,12 @@ _SIGS = {
     "osf_kv4_read": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
     "osf_attn_kv4": (_i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _f, _vp, _vp, _i, _vp, _sz, _vp]),
     "osf_attn_kv4_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "osf_kv8_append": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _vp,
+                            _vp, _i, _vp]),
+    "osf_kv8_read": (_i, [_vp, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp]),
+    "osf_attn_kv8": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _i, _i, _f, _vp, _vp, _sz,
+                          _vp]),
+    "osf_attn_kv8_workspace_bytes": (_i, [_i, _i, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "osf_kv_evict": (_i, [_vp, _vp, _ll, _vp, _vp, _ll, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp]),
     "osf_selftest_bounded_wait": (_i, [ctypes.c_ulonglong, _vp]),
     "osf_softmax_workspace_bytes": (_i, [_ll, _ll, ctypes.POINTER(_sz)]),
@@ -608,6 +615,112 @@ def osf_attn_kv4(q, cache, lens=None, out=None, mask="none", scale: float | None
           _need(lens, "lens", (B,), torch.int32, dev), _MASKS[mask] if isinstance(mask, str) else int(mask),
           0.0 if scale is None else float(scale), _need(lse, "lse", (B, Hq, Sq), torch.float32, dev),
           _need(weights, "weights", (B, Hkv, S), torch.float32, dev), int(bool(accumulate)), _ptr(workspace),
+          _bytes_of(workspace, dev))
+    return out
+
+
+def _kv8_dims(pages, scales, table):
+    """(n_pages, Hkv, P, D, B, table_len, device) of a paged 8-bit cache: uint8 (or float8_e4m3fn) pages
+    [n_pages, 2, Hkv, P, D], float32 scales [n_pages, 2, Hkv], int32 table [B, table_len]."""
+    dev = pages.get_device()
+    if dev < 0 or pages.dim() != 5 or pages.element_size() != 1 or pages.shape[1] != 2 or not pages.is_contiguous():
+        raise ValueError("pages must be a contiguous 8-bit CUDA tensor [n_pages, 2, Hkv, P, D]")
+    n_pages, _, Hkv, P, D = pages.shape
+    if table.dim() != 2:
+        raise ValueError("table must be [B, pages of a sequence]")
+    B, per = table.shape
+    _need(scales, "scales", (n_pages, 2, Hkv), torch.float32, dev)
+    _need(table, "table", (B, per), torch.int32, dev)
+    return n_pages, Hkv, P, D, B, per, dev
+
+
+def osf_kv8_append(k, v, pages, scales, table, lens=None, counts=None, cos=None, sin=None, interleaved: bool = False,
+                   q=None, q_out=None):
+    """Store the rows ``k``, ``v`` ([B, Hkv, n, D] views, float32 or bfloat16) in the paged 8-bit cache behind the ``lens``
+    (int32 [B]; None: 0) tokens that each sequence has; ``counts`` (int32 [B]): how many of the n are new, the rest being
+    padding.  ``cos``, ``sin`` (float32 [positions, R / 2]): K, and the queries ``q`` ([B, Hq, n, D]) of the same tokens,
+    are rotated by their positions.  Returns the rotated queries (``q_out``, a contiguous tensor if None), or None without
+    ``q``; the caller advances its lengths."""
+    n_pages, Hkv, P, D, B, per, dev = _kv8_dims(pages, scales, table)
+    n = k.shape[2] if k.dim() == 4 else -1
+    if k.shape != (B, Hkv, n, D) or v.shape != k.shape or v.dtype != k.dtype or k.get_device() != dev or \
+            v.get_device() != dev:
+        raise ValueError("k and v must be [B, Hkv, n, D] of one dtype, with the cache's sizes and device")
+    views, Hq = [("k", k), ("v", v)], 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 4 else 0
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+        for name, t in (("q", q), ("q_out", q_out)):
+            if t.shape != (B, Hq, n, D) or t.dtype != k.dtype or t.get_device() != dev:
+                raise ValueError(f"{name} must be [B, Hq, n, D] of the dtype and device of k")
+            views.append((name, t))
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    st = None
+    if not all(t.is_contiguous() for _, t in views):
+        for name, t in views:
+            if t.shape[3] > 1 and t.stride(3) != 1:
+                raise ValueError(f"{name} must be a 4-D [B, H, n, D] view with a contiguous last dimension")
+        flat = [s for _, t in views for s in t.stride()[:3]]
+        st = ctypes.cast((ctypes.c_longlong * len(flat))(*flat), ctypes.c_void_p)
+    rot = positions = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        if cos.dim() != 2:
+            raise ValueError("cos and sin must be [positions, R / 2]")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        _need(cos, "cos", cos.shape, torch.float32, dev)
+        _need(sin, "sin", cos.shape, torch.float32, dev)
+    _call("osf_kv8_append", dev, k.data_ptr(), v.data_ptr(), _dtype_code(k), B, Hkv, n, D, st, pages.data_ptr(),
+          scales.data_ptr(), n_pages, P, table.data_ptr(), per, _need(lens, "lens", (B,), torch.int32, dev),
+          _need(counts, "counts", (B,), torch.int32, dev), _ptr(cos), _ptr(sin), positions, rot, int(bool(interleaved)),
+          _ptr(q), _ptr(q_out), Hq)
+    return q_out
+
+
+def osf_kv8_read(pages, scales, table, n: int, starts=None, lens=None, k=None, v=None, dtype=torch.bfloat16):
+    """The values of tokens starts[b] .. starts[b] + n - 1 (``starts`` None: from 0) of a paged 8-bit cache, as contiguous
+    (k, v) [B, Hkv, n, D] of ``dtype`` (or given tensors); zeros at and behind ``lens``."""
+    n_pages, Hkv, P, D, B, per, dev = _kv8_dims(pages, scales, table)
+    shape = (B, Hkv, n, D)
+    k = torch.empty(shape, dtype=dtype, device=pages.device) if k is None else k
+    v = torch.empty(shape, dtype=k.dtype, device=pages.device) if v is None else v
+    _call("osf_kv8_read", dev, pages.data_ptr(), scales.data_ptr(), n_pages, P, table.data_ptr(), per,
+          _need(k, "k", shape, k.dtype, dev), _need(v, "v", shape, k.dtype, dev), _dtype_code(k), B, Hkv, n, D,
+          _need(starts, "starts", (B,), torch.int32, dev), _need(lens, "lens", (B,), torch.int32, dev))
+    return k, v
+
+
+def osf_attn_kv8_workspace_bytes(dtype: int, B, Hq, Hkv, Sq, D, page_tokens: int, table_len: int, window: int = 0,
+                                 sinks: int = 0) -> int:
+    n = _sz(0)
+    _check(lib().osf_attn_kv8_workspace_bytes(dtype, B, Hq, Hkv, Sq, D, page_tokens, table_len, window, sinks,
+                                              ctypes.byref(n)), "osf_attn_kv8_workspace_bytes")
+    return n.value
+
+
+def osf_attn_kv8(q, pages, scales, table, lens=None, out=None, window: int = 0, sinks: int = 0, scale: float | None = None,
+                 lse=None, workspace=None):
+    """Attention of ``q`` ([B, Hq, Sq, D] view), the last Sq of each sequence's ``lens`` (int32 [B]; None: all that the
+    table holds) tokens, over a paged 8-bit cache.  With ``window`` > 0 the row at position p sees the tokens j <= p with
+    p - j < ``window`` or j < ``sinks``, else all j <= p.  Returns ``out`` (a contiguous tensor if None)."""
+    n_pages, Hkv, P, D, B, per, dev = _kv8_dims(pages, scales, table)
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != D or q.get_device() != dev:
+        raise ValueError("q must be [B, Hq, Sq, D] with the cache's batch, head dimension and device")
+    _, Hq, Sq, _ = q.shape
+    if out is None:
+        out = torch.empty((B, Hq, Sq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype != q.dtype or out.get_device() != dev:
+        raise ValueError("out must have the shape, dtype and device of q")
+    st = _view_strides("q", q, "out", out)
+    dt = _dtype_code(q)
+    if workspace is None:
+        n = _query(dev, osf_attn_kv8_workspace_bytes, dt, B, Hq, Hkv, Sq, D, P, per, int(window), int(sinks))
+        workspace = _workspace(n, q.device, None)
+    _call("osf_attn_kv8", dev, q.data_ptr(), pages.data_ptr(), scales.data_ptr(), out.data_ptr(), dt, B, Hq, Hkv, Sq, n_pages,
+          P, D, st, table.data_ptr(), per, _need(lens, "lens", (B,), torch.int32, dev), int(window), int(sinks),
+          0.0 if scale is None else float(scale), _need(lse, "lse", (B, Hq, Sq), torch.float32, dev), _ptr(workspace),
           _bytes_of(workspace, dev))
     return out
 

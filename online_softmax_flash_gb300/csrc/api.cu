@@ -19,6 +19,7 @@
 #include "attn_tc.cuh"
 #include "decode.cuh"
 #include "kv4.cuh"
+#include "kv8.cuh"
 #include "key_weights.cuh"
 #include "kv_evict.cuh"
 
@@ -763,11 +764,10 @@ int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O
     AttnProblem p;
     bool empty;
     int st = check_window(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, window, sinks, scale, lse, p, empty);
-    if (st != OSF_OK) return st;
+    if (st != OSF_OK || B == 0 || Sq == 0) return st;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     if (empty) {
-        if (B == 0 || Sq == 0) return OSF_OK;
         // no keys: every row sees nothing.  The problem of one key, whose place nothing reads, without it
         long long sd[12] = {};   // (K and V: strides of no extent)
         for (int i = 0; strides && i < 3; ++i) {
@@ -1185,6 +1185,205 @@ int osf_attn_kv4(const void *Q, const void *cache, void *O, int dtype, int B, in
         kp.scores = reinterpret_cast<float *>(at + kv4_lse_bytes(kp));
     }
     return launch_status(launch_attn_kv4(kp, workspace, dev->sm_count, (cudaStream_t)stream));
+}
+
+// ------------------------------------------------------------------ paged 8-bit cache
+// Sizes and buffers shared by the calls on a paged cache.
+static int check_kv8(const void *pages, const float *scales, int n_pages, int page_tokens, const int *table, int per_seq,
+                     int dtype, int B, int Hkv, long long n, int D, Kv8Cache &c) {
+    if (dtype != OSF_F32 && dtype != OSF_BF16) return OSF_ERR_INVALID;
+    if (B < 0 || Hkv <= 0 || n < 0 || D <= 0 || n_pages < 0 || per_seq < 0 || page_tokens <= 0) return OSF_ERR_INVALID;
+    if (D > 256 || D % 32 != 0) return OSF_ERR_UNSUPPORTED;
+    if (page_tokens != 16 && page_tokens != 32 && page_tokens != 64 && page_tokens != 128) return OSF_ERR_UNSUPPORTED;
+    if ((long long)B * Hkv > 65535 || n * D >= (1LL << 31) || (long long)per_seq * page_tokens >= (1LL << 29))
+        return OSF_ERR_UNSUPPORTED;
+    if ((long long)n_pages * 2 * Hkv * page_tokens >= (1LL << 31)) return OSF_ERR_UNSUPPORTED;   // rows of the pages
+    c.pages = static_cast<unsigned char *>(const_cast<void *>(pages));
+    c.scales = const_cast<float *>(scales);
+    c.table = table;
+    c.n_pages = n_pages; c.P = page_tokens; c.per_seq = per_seq; c.Hkv = Hkv; c.D = D;
+    return OSF_OK;
+}
+static int check_kv8_buffers(const Kv8Cache &c, int B) {
+    if ((c.n_pages > 0 && (!c.pages || !c.scales)) || (B > 0 && c.per_seq > 0 && !c.table)) return OSF_ERR_INVALID;
+    return (reinterpret_cast<uintptr_t>(c.pages) & 15u) != 0 ? OSF_ERR_INVALID : OSF_OK;
+}
+// The cache's three buffers, for the checks of overlaps.
+struct Kv8Buffers {
+    const void *at[3];
+    size_t size[3];
+};
+static Kv8Buffers kv8_buffers(const Kv8Cache &c, int B) {
+    const size_t heads = (size_t)c.n_pages * 2 * c.Hkv;
+    return {{c.pages, c.scales, c.table}, {heads * c.P * c.D, heads * sizeof(float), (size_t)B * c.per_seq * sizeof(int)}};
+}
+// `count` element strides into st, or the contiguous ones of [B, H, n, D] for each three.
+static int take_strides(const long long *strides, int count, const int *H, long long n, int D, long long *st) {
+    for (int i = 0; i < count; ++i) {
+        const long long h = H[i / 3];
+        st[i] = strides ? strides[i] : i % 3 == 0 ? h * n * D : i % 3 == 1 ? n * D : D;
+        if (st[i] < 0) return OSF_ERR_INVALID;
+        if (st[i] >= (1LL << 40)) return OSF_ERR_UNSUPPORTED;
+    }
+    return OSF_OK;
+}
+
+int osf_kv8_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D, const long long *strides, void *pages,
+                   float *scales, int n_pages, int page_tokens, const int *table, int table_len, const int *lens,
+                   const int *counts, const float *cos_table, const float *sin_table, int max_positions, int rotary_dim,
+                   int interleaved, const void *Q, void *Q_out, int Hq, osf_stream stream) {
+    Kv8StoreProblem p{};
+    Kv8Cache &c = p.c;
+    int st = check_kv8(pages, scales, n_pages, page_tokens, table, table_len, dtype, B, Hkv, n, D, c);
+    if (st != OSF_OK) return st;
+    if (rotary_dim < 0 || rotary_dim > D || max_positions < 0) return OSF_ERR_INVALID;
+    if (rotary_dim % 8 != 0) return OSF_ERR_UNSUPPORTED;
+    if ((Q == nullptr) != (Q_out == nullptr)) return OSF_ERR_INVALID;
+    if (Q && (Hq <= 0 || Hq % Hkv != 0)) return OSF_ERR_INVALID;
+    if (Q && (long long)B * Hq > 65535) return OSF_ERR_UNSUPPORTED;
+    const int heads[4] = {Hkv, Hkv, Hq, Hq};
+    long long sd[12];
+    st = take_strides(strides, Q ? 12 : 6, heads, n, D, sd);
+    if (st != OSF_OK) return st;
+    if (B == 0 || n == 0) return OSF_OK;
+    if (!K || !V || (rotary_dim > 0 && (!cos_table || !sin_table || max_positions == 0))) return OSF_ERR_INVALID;
+    st = check_kv8_buffers(c, B);
+    if (st != OSF_OK) return st;
+    if ((long long)table_len * page_tokens < n && !counts) return OSF_ERR_INVALID;
+    const size_t es = elem_size(dtype), nt = (size_t)max_positions * (rotary_dim / 2) * sizeof(float);
+    const size_t nk = span_bytes(B, Hkv, n, D, sd[0], sd[1], sd[2], es), nv = span_bytes(B, Hkv, n, D, sd[3], sd[4], sd[5], es);
+    const size_t nq = Q ? span_bytes(B, Hq, n, D, sd[6], sd[7], sd[8], es) : 0;
+    const size_t no = Q ? span_bytes(B, Hq, n, D, sd[9], sd[10], sd[11], es) : 0;
+    const Kv8Buffers cb = kv8_buffers(c, B);
+    // written: pages, scales, Q_out; read: the others
+    const void *in[8] = {K, V, lens, counts, rotary_dim ? cos_table : nullptr, rotary_dim ? sin_table : nullptr, table, Q};
+    const size_t in_n[8] = {nk, nv, (size_t)B * 4, (size_t)B * 4, nt, nt, cb.size[2], nq};
+    const void *out[3] = {pages, scales, Q_out};
+    const size_t out_n[3] = {cb.size[0], cb.size[1], no};
+    const bool in_place = Q && Q == Q_out && sd[6] == sd[9] && sd[7] == sd[10] && sd[8] == sd[11];
+    for (int o = 0; o < 3; ++o) {
+        for (int i = 0; i < 8; ++i)
+            if (!(o == 2 && i == 7 && in_place) && overlaps(out[o], out_n[o], in[i], in_n[i])) return OSF_ERR_INVALID;
+        for (int o2 = o + 1; o2 < 3; ++o2)
+            if (overlaps(out[o], out_n[o], out[o2], out_n[o2])) return OSF_ERR_INVALID;
+    }
+    if (Q && !rows_disjoint(B, Hq, n, D, sd[9], sd[10], sd[11])) return OSF_ERR_INVALID;
+    if (n_pages == 0 || table_len == 0) return OSF_ERR_INVALID;   // nowhere to put the tokens
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    p.k = K; p.v = V; p.q = Q; p.qo = Q_out; p.lens = lens; p.counts = counts;
+    p.cos = cos_table; p.sin = sin_table; p.max_pos = rotary_dim ? max_positions : INT_MAX; p.R = rotary_dim;
+    p.interleaved = interleaved != 0;
+    p.dtype = dtype; p.B = B; p.Hq = Hq; p.n = n;
+    p.k_sb = sd[0]; p.k_sh = sd[1]; p.k_ss = sd[2]; p.v_sb = sd[3]; p.v_sh = sd[4]; p.v_ss = sd[5];
+    if (Q) {
+        p.q_sb = sd[6]; p.q_sh = sd[7]; p.q_ss = sd[8]; p.o_sb = sd[9]; p.o_sh = sd[10]; p.o_ss = sd[11];
+    }
+    p.status = dev->status;
+    return launch_status(launch_kv8_append(p, dev->sm_count, (cudaStream_t)stream));
+}
+
+int osf_kv8_read(const void *pages, const float *scales, int n_pages, int page_tokens, const int *table, int table_len, void *K,
+                 void *V, int dtype, int B, int Hkv, int n, int D, const int *starts, const int *lens, osf_stream stream) {
+    Kv8StoreProblem p{};
+    int st = check_kv8(pages, scales, n_pages, page_tokens, table, table_len, dtype, B, Hkv, n, D, p.c);
+    if (st != OSF_OK) return st;
+    if (B == 0 || n == 0) return OSF_OK;
+    if (!K || !V) return OSF_ERR_INVALID;
+    st = check_kv8_buffers(p.c, B);
+    if (st != OSF_OK) return st;
+    const size_t no = (size_t)B * Hkv * n * D * elem_size(dtype);
+    const Kv8Buffers cb = kv8_buffers(p.c, B);
+    const void *in[5] = {cb.at[0], cb.at[1], cb.at[2], starts, lens};
+    const size_t in_n[5] = {cb.size[0], cb.size[1], cb.size[2], (size_t)B * 4, (size_t)B * 4};
+    if (overlaps(K, no, V, no)) return OSF_ERR_INVALID;
+    for (int i = 0; i < 5; ++i)
+        if (overlaps(K, no, in[i], in_n[i]) || overlaps(V, no, in[i], in_n[i])) return OSF_ERR_INVALID;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    p.ko = K; p.vo = V; p.lens = lens; p.starts = starts;
+    p.dtype = dtype; p.B = B; p.n = n;
+    p.status = dev->status;
+    return launch_status(launch_kv8_read(p, dev->sm_count, (cudaStream_t)stream));
+}
+
+// Sizes and layout of an attention call over pages; fills kp (without workspace pointers).
+static int check_attn_kv8(const void *Q, const void *pages, const float *scales, void *O, int dtype, int B, int Hq, int Hkv,
+                          int Sq, int n_pages, int page_tokens, int D, const long long *strides, const int *table, int table_len,
+                          const int *lens, int window, int sinks, float scale, float *lse, Kv8AttnProblem &kp, bool &empty) {
+    empty = false;
+    kp = Kv8AttnProblem{};
+    int st = check_kv8(pages, scales, n_pages, page_tokens, table, table_len, dtype, B, Hkv, Sq, D, kp.c);
+    if (st != OSF_OK) return st;
+    if (Hq <= 0 || Hq % Hkv != 0 || window < 0 || sinks < 0 || !(scale == scale)) return OSF_ERR_INVALID;
+    const int heads[2] = {Hq, Hq};
+    long long sd[6];
+    st = take_strides(strides, 6, heads, Sq, D, sd);
+    if (st != OSF_OK) return st;
+    // the query rows of one kv head number at most 2^15: one CTA column per few of them
+    if ((long long)(Hq / Hkv) * Sq > (1LL << 15)) return OSF_ERR_UNSUPPORTED;
+    if (B == 0 || Sq == 0) { empty = true; return OSF_OK; }
+    if (!Q || !O) return OSF_ERR_INVALID;
+    st = check_kv8_buffers(kp.c, B);
+    if (st != OSF_OK) return st;
+    if (!rows_disjoint(B, Hq, Sq, D, sd[3], sd[4], sd[5])) return OSF_ERR_INVALID;
+    const size_t es = elem_size(dtype);
+    const Kv8Buffers cb = kv8_buffers(kp.c, B);
+    const void *bufs[7] = {O, lse, Q, cb.at[0], cb.at[1], cb.at[2], lens};
+    const size_t size[7] = {span_bytes(B, Hq, Sq, D, sd[3], sd[4], sd[5], es), (size_t)B * Hq * Sq * sizeof(float),
+                            span_bytes(B, Hq, Sq, D, sd[0], sd[1], sd[2], es), cb.size[0], cb.size[1], cb.size[2],
+                            (size_t)B * sizeof(int)};
+    for (int i = 0; i < 2; ++i)   // no output overlaps another buffer
+        for (int j = i + 1; j < 7; ++j)
+            if (overlaps(bufs[i], size[i], bufs[j], size[j])) return OSF_ERR_INVALID;
+    AttnProblem &p = kp.a;
+    p.q = Q; p.o = O; p.lse = lse;
+    p.dtype = dtype; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Sk = table_len * page_tokens; p.D = D;
+    p.causal = 1;
+    // a window that hides nothing of the longest sequence is none
+    if (window > 0 && (long long)window + sinks < p.Sk) {
+        p.window = window;
+        p.sinks = sinks;
+    }
+    p.q_sb = sd[0]; p.q_sh = sd[1]; p.q_ss = sd[2]; p.o_sb = sd[3]; p.o_sh = sd[4]; p.o_ss = sd[5];
+    p.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf((float)D)) * kLog2e;
+    p.splits = 1;
+    kp.lens = lens;
+    return OSF_OK;
+}
+
+int osf_attn_kv8_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int D, int page_tokens, int table_len, int window,
+                                 int sinks, size_t *bytes) {
+    if (!bytes) return OSF_ERR_INVALID;
+    *bytes = 0;
+    Kv8AttnProblem kp;
+    bool empty;
+    // (placeholder addresses, far from one another)
+    auto at = [](int i) { return reinterpret_cast<char *>(uintptr_t(i) << 44); };
+    const int st = check_attn_kv8(at(1), at(2), reinterpret_cast<const float *>(at(3)), at(4), dtype, B, Hq, Hkv, Sq, 1, page_tokens,
+                                  D, nullptr, reinterpret_cast<const int *>(at(5)), table_len, nullptr, window, sinks, 0.f, nullptr,
+                                  kp, empty);
+    if (st != OSF_OK || empty) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    *bytes = kv8_attn_partial_bytes(kp, dev->sm_count);
+    return OSF_OK;
+}
+
+int osf_attn_kv8(const void *Q, const void *pages, const float *scales, void *O, int dtype, int B, int Hq, int Hkv, int Sq,
+                 int n_pages, int page_tokens, int D, const long long *strides, const int *table, int table_len, const int *lens,
+                 int window, int sinks, float scale, float *lse, void *workspace, size_t workspace_bytes, osf_stream stream) {
+    Kv8AttnProblem kp;
+    bool empty;
+    const int st = check_attn_kv8(Q, pages, scales, O, dtype, B, Hq, Hkv, Sq, n_pages, page_tokens, D, strides, table, table_len,
+                                  lens, window, sinks, scale, lse, kp, empty);
+    if (st != OSF_OK || empty) return st;
+    DeviceInfo *dev;
+    if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    kp.a.status = dev->status;
+    const int ws = check_workspace(workspace, workspace_bytes, kv8_attn_partial_bytes(kp, dev->sm_count));
+    if (ws != OSF_OK) return ws;
+    return launch_status(launch_attn_kv8(kp, workspace, dev->sm_count, (cudaStream_t)stream));
 }
 
 // ------------------------------------------------------------------ eviction

@@ -315,7 +315,14 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
                 low = row + p.causal_off - p.window + 1 - key0 - col0;
                 snk = p.sinks - key0 - col0;
             }
-            auto sees = [&](int k) { return k < lim && (!WIN || k >= low || k < snk); };
+            uint32_t seen[2];
+            if constexpr (WIN)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) seen[c] = seen_bits(lim - 32 * c, low - 32 * c, snk - 32 * c);
+            auto sees = [&](int k) {
+                if constexpr (WIN) return (seen[k / 32] >> k % 32 & 1u) != 0;
+                else return k < lim;
+            };
             // phase A: P for this warp's 64 columns, kept in registers
             float pv[64];
             {
@@ -561,7 +568,15 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
                 full = full && (qbase + TB - 1 <= key0 + p.window - 1 - p.causal_off || key0 + TB <= p.sinks);
                 if (key >= p.sinks) qmax = qmin + p.window - 1;
             }
-            auto sees = [&](int k) { return k >= qmin && (!WIN || k <= qmax); };
+            uint32_t seen[2];
+            if constexpr (WIN)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                    seen[c] = ~bits_below(qmin - 32 * c) & (qmax == INT_MAX ? ~0u : bits_below(qmax + 1 - 32 * c));
+            auto sees = [&](int k) {
+                if constexpr (WIN) return (seen[k / 32] >> k % 32 & 1u) != 0;
+                else return k >= qmin;
+            };
             // phase A: P^T for this warp's 64 columns (fp32 in registers, bf16 into TMEM)
             float pv[64];
 #pragma unroll

@@ -529,7 +529,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     snk = p.sinks - key0;
                     need_mask = need_mask || (key0 + p.window <= row_first + BM - 1 + p.causal_off && key0 + BN > p.sinks);
                 }
-                auto hidden = [&](int j) { return j >= lim || (WIN && j < low && j >= snk); };
+                uint32_t seen[WIN ? 4 : 1];   // a bit for each column
+                if constexpr (WIN)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) seen[c] = need_mask ? seen_bits(lim - 32 * c, low - 32 * c, snk - 32 * c) : ~0u;
+                auto hidden = [&](int c, int k) {
+                    if constexpr (WIN) return !(seen[c] >> k & 1u);
+                    else return c * 32 + k >= lim;
+                };
                 uint32_t sr[X3 ? 1 : 4][32];   // bf16 mode: the whole score row in registers
                 float mx;
                 if constexpr (X3) {
@@ -542,7 +549,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         tmem_ld_wait();
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            const float x = (need_mask && hidden(c * 32 + k)) ? -INFINITY : __uint_as_float(sr[0][k]);
+                            const float x = (need_mask && hidden(c, k)) ? -INFINITY : __uint_as_float(sr[0][k]);
                             m4[k & 3] = fmaxf(m4[k & 3], x);
                         }
                     }
@@ -556,7 +563,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (hidden(c * 32 + k)) sr[c][k] = __float_as_uint(-INFINITY);
+                                if (hidden(c, k)) sr[c][k] = __float_as_uint(-INFINITY);
                     }
                     // row max: eight independent chains of 3-input max, then a short tree
                     float mm[8];
@@ -595,8 +602,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         uint32_t ph[16], pl[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float s0 = (need_mask && hidden(c * 32 + 2 * k)) ? -INFINITY : __uint_as_float(sr[0][2 * k]);
-                            const float s1 = (need_mask && hidden(c * 32 + 2 * k + 1)) ? -INFINITY
+                            const float s0 = (need_mask && hidden(c, 2 * k)) ? -INFINITY : __uint_as_float(sr[0][2 * k]);
+                            const float s1 = (need_mask && hidden(c, 2 * k + 1)) ? -INFINITY
                                                                                        : __uint_as_float(sr[0][2 * k + 1]);
                             float p0, p1;
                             f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), p0, p1);

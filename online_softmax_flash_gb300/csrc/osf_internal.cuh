@@ -121,6 +121,14 @@ inline int key_stream_max(int rows, int Sk, int window, int sinks, int tile) {
     return (int)(n < n_kt ? n : n_kt);
 }
 
+// Bits 0 .. n - 1 of a word, for any n.
+__device__ __forceinline__ uint32_t bits_below(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+// Which of 32 columns a row sees that sees those before `lim` which are at or behind `low` or before `snk`.  (The three
+// comparisons for each column cost 9 us a tile of 128 x 256 scores, the bits of one word less than 0.5.)
+__device__ __forceinline__ uint32_t seen_bits(int lim, int low, int snk) {
+    return bits_below(lim) & (~bits_below(low) | bits_below(snk));
+}
+
 // SM count of the current device, looked up once per device (the same value every entry point
 // sizes its grids and workspaces with).  Returns an osf_status.
 int device_sm_count(int *sms);

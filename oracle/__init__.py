@@ -25,6 +25,7 @@ force, worked examples and invariants (``tests/test_oracle_pins.py``).
 """
 from .attention import attention, attention_gqa, attention_rows
 from .attention_bwd import attention_bwd, attention_gqa_bwd
+from .kv8 import e4m3_codes, e4m3_values, kv8_append, kv8_values, rotate, scale_exponent
 from .kv_cache import attention_records, evict, key_weights, quantise_group, record_values, records, visible
 from .softmax import softmax, softmax_masked
 from .recurrence import (combine_partials, online_attention_row, online_softmax,
@@ -34,6 +35,6 @@ from .window import attention_window, window_mask
 __all__ = [
     "attention", "attention_gqa", "attention_rows", "attention_bwd", "attention_gqa_bwd", "softmax",
     "softmax_masked", "attention_records", "evict", "key_weights", "quantise_group", "record_values", "records", "visible",
-    "attention_window", "window_mask",
+    "attention_window", "window_mask", "e4m3_codes", "e4m3_values", "kv8_append", "kv8_values", "rotate", "scale_exponent",
     "online_softmax_state", "online_softmax", "online_attention_row", "combine_partials",
 ]
