@@ -1338,7 +1338,7 @@ static int check_attn_kv8(const void *Q, const void *pages, const float *scales,
             if (overlaps(bufs[i], size[i], bufs[j], size[j])) return OSF_ERR_INVALID;
     AttnProblem &p = kp.a;
     p.q = Q; p.o = O; p.lse = lse;
-    p.dtype = dtype; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Sk = table_len * page_tokens; p.D = D;
+    p.dtype = dtype; p.B = B; p.Hq = Hq; p.Hkv = Hkv; p.Sq = Sq; p.Sk = n_pages > 0 ? table_len * page_tokens : 0; p.D = D;
     p.causal = 1;
     // a window that hides nothing of the longest sequence is none
     if (window > 0 && (long long)window + sinks < p.Sk) {

@@ -6,6 +6,7 @@
 // (its whole dot product with the rows), then a channel of every 32 per lane.
 #include "kv8.cuh"
 #include "sm100_ptx.cuh"
+#include "tma_host.cuh"
 
 namespace osf {
 namespace {
@@ -182,6 +183,694 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
     }
 }
 
+
+// ============================================================================ tensor-core kernel
+// bfloat16 queries, D 64 or 128.  The codes go from memory to the tensor cores as they are: TMA copies pages into shared
+// memory, and tcgen05.mma (kind::f8f6f4) takes both products' large operands from there,
+//   S^T[128 tokens x columns]   = K[128 x D] . Q parts^T,      O^T[D x columns] += V^T[D x 128] . P parts[128 x columns],
+// so no thread touches a code but at a sequence's edges.  The small operands are sums of e4m3 parts, one column of the
+// product each, the k-th part in units of 16^-k: a bfloat16 query has 8 bits, which are two parts exactly (its row scaled by
+// a power of two to a largest entry in 128 .. 256; entries below 2^-14 of that lose low bits, 2^-22 of it at most).  P takes
+// three parts: 12 bits, and at most 2^-26 of the row's reference is lost of a weight below that.
+// A token's V scale is not applied to its codes but to its weight.  Scales can lie far apart, so what goes into the
+// product is 2^(y + e - m'), y the base-2 score, e the exponent of the scale and m' a reference of the sums y + e: exact
+// relative to the largest P * scale, whichever page it comes from.  The denominator has its own reference m of the y.
+// Both references are whole numbers and move only when a value passes them, to 1 .. 2 above the largest.
+//
+// A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Warp 8 loads, warp 9 issues the
+// products, and two groups of four warps take the tiles in turn, each with its own S^T, O^T and references, one token's
+// scores per thread; their states meet at the end of the run.  Runs are cut flat over all sequences (see FlatCut), and a
+// second kernel joins the pieces of a sequence that several CTAs share.
+constexpr int TT = 128;                   // tokens per tile
+constexpr int TC_THREADS = 320;
+constexpr uint32_t TC_TMEM = 256;
+constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
+constexpr int kMaxRing = 12;
+
+template <int D, int NR>
+struct Tc8 {
+    static constexpr uint32_t TILE = TT * D;                        // K or V of a tile
+    static constexpr int NQ = 2 * NR < 16 ? 16 : 2 * NR;            // columns of Q parts: part p of row r at p * NR + r
+    static constexpr int PLANES = (3 * NR + 15) / 16, NP = 16 * PLANES;   // columns of P parts, in planes of 16
+    static constexpr uint32_t Q_BYTES = 4096, P_BYTES = PLANES * TT * 16;
+    static constexpr uint32_t O_BYTES = 2 * NR * D * 4;
+    static constexpr uint32_t Q_OFF = 0, P_OFF = Q_BYTES, O_OFF = P_OFF + 2 * P_BYTES;
+    static constexpr uint32_t RING_OFF = (O_OFF + O_BYTES + 1023) / 1024 * 1024;
+    static constexpr int FIT = (int)((232448u - 1024u - 4096u - RING_OFF) / (2 * TILE));   // 4 KB for the static part
+    static constexpr int STAGES = FIT < kMaxRing ? FIT : kMaxRing;
+    static constexpr uint32_t SMEM = RING_OFF + STAGES * 2 * TILE + 1024;
+    static constexpr uint32_t SWZ = D == 128 ? 2 : 4, GROUP8 = 8 * D;   // swizzle type, bytes of eight rows
+    static constexpr uint32_t IDESC_S = idesc_e4m3_f32(TT, NQ, 0, 0), IDESC_O = idesc_e4m3_f32(D, NP, 1, 1);
+    static constexpr uint32_t S_COL = 0, O_COL = 64;                // + 32 g, + 48 g
+};
+
+// Work is cut flat: an item is one block of query rows of one (batch, kv head), worth its tiles and kItemCost more for what it
+// costs besides them; the items lie one after another (batch, kv head, row block), and CTA c of nc takes the c-th part of the
+// whole, whatever items it spans.  So every CTA gets the same work, in one wave, for any mix of lengths.  An item whose tiles
+// all lie in one part is finished there; of the others a CTA holds at most two pieces, the end of one that began before (slot
+// 2 c of the partial states) and the start of one that goes on (slot 2 c + 1).
+constexpr int kItemCost = 3;
+constexpr int kMinTiles = 2;   // tiles worth a CTA
+struct FlatCut {
+    long long total, base;   // units of all items, and of the batches before b
+    int nc;                  // CTAs that take part
+};
+__device__ __forceinline__ KeyStream stream_of(const Kv8AttnProblem &kp, int b, int &n) {
+    n = kv8_length(kp.lens, b, kp.a.Sk, kp.a.status);
+    KeyStream ks = kv8_stream(kp, max(n, 1), TT);
+    if (n == 0) ks.n = 0;
+    return ks;
+}
+__device__ __forceinline__ int item_units(const Kv8AttnProblem &kp, int b) {
+    int n;
+    return max(1, stream_of(kp, b, n).n) + kItemCost;
+}
+// Called by a whole warp.
+__device__ __forceinline__ FlatCut flat_cut(const Kv8AttnProblem &kp, int items_per_b, int b, int grid) {
+    const int lane = threadIdx.x & 31;
+    long long all = 0, before = 0;
+    for (int i = lane; i < kp.a.B; i += 32) {
+        const long long n = item_units(kp, i);
+        all += n;
+        before += i < b ? n : 0;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        all += __shfl_xor_sync(0xffffffffu, all, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    FlatCut f;
+    f.total = all * items_per_b;
+    f.base = before * items_per_b;
+    f.nc = (int)max(1LL, min((long long)grid, f.total / (kMinTiles + kItemCost)));
+    return f;
+}
+// The CTA that has unit x: the last one whose part begins at or before it.
+__device__ __forceinline__ int cta_of(const FlatCut &w, long long x) { return (int)(((x + 1) * w.nc - 1) / w.total); }
+
+// A CTA's pieces, one after another.  Every warp walks them for itself.
+struct Walk {
+    int rest, b, item, unit0;                    // what is left
+    int kvh, r0, rows, n, tile0, tiles, whole;   // the piece: tiles [tile0, tile0 + tiles) of the sequence's stream
+    KeyStream ks;
+};
+// False when this CTA has no work.  Called by a whole warp.
+__device__ __forceinline__ bool walk_begin(const Kv8AttnProblem &kp, int items_per_b, int flat, Walk &w) {
+    const int lane = threadIdx.x & 31;
+    w.unit0 = 0;
+    if (!flat) {
+        w.b = blockIdx.x / items_per_b;
+        w.item = blockIdx.x % items_per_b;
+        w.rest = 1;
+        return true;
+    }
+    const FlatCut f = flat_cut(kp, items_per_b, 0, gridDim.x);
+    if ((int)blockIdx.x >= f.nc) return false;
+    const long long pos = f.total * blockIdx.x / f.nc;
+    w.rest = (int)(f.total * (blockIdx.x + 1) / f.nc - pos);
+    long long at = 0;   // units before batch b: 32 batches at a time, a lane each
+    for (int b0 = 0;; b0 += 32) {
+        const int bi = b0 + lane;
+        const long long ub = bi < kp.a.B ? (long long)item_units(kp, bi) * items_per_b : 0;
+        long long upto = ub;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, pos < at + upto);
+        if (past) {
+            const int first = __ffs(past) - 1;
+            w.b = b0 + first;
+            at += __shfl_sync(0xffffffffu, upto - ub, first);
+            break;
+        }
+        at += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    const int ui = item_units(kp, w.b);
+    w.item = (int)((pos - at) / ui);
+    w.unit0 = (int)((pos - at) % ui);
+    return true;
+}
+// The next piece; false behind the last one.
+template <int NR>
+__device__ __forceinline__ bool walk_next(const Kv8AttnProblem &kp, int row_blocks, int flat, Walk &w) {
+    if (w.rest <= 0) return false;
+    const AttnProblem &p = kp.a;
+    w.ks = stream_of(kp, w.b, w.n);
+    const int all = max(1, w.ks.n), units = all + kItemCost;   // the item's first kItemCost units hold no tiles
+    const int take = flat ? min(units - w.unit0, w.rest) : units;
+    w.tile0 = max(0, w.unit0 - kItemCost);
+    const int tile1 = w.unit0 + take - kItemCost;
+    if (tile1 <= w.tile0) {   // the part ends before the item's first tile
+        w.rest = 0;
+        return false;
+    }
+    w.whole = tile1 - w.tile0 == all;
+    w.tiles = min(tile1, w.ks.n) - w.tile0;   // (an empty sequence has a tile's unit, and no tile)
+    w.kvh = w.item / row_blocks;
+    w.r0 = w.item % row_blocks * NR;
+    w.rows = min(NR, p.Hq / p.Hkv * p.Sq - w.r0);
+    w.rest = flat ? w.rest - take : 0;
+    w.unit0 = 0;
+    return true;
+}
+__device__ __forceinline__ void walk_step(const Kv8AttnProblem &kp, int row_blocks, Walk &w) {
+    if (++w.item == kp.a.Hkv * row_blocks) {
+        w.item = 0;
+        ++w.b;
+    }
+}
+
+// Channels c .. c+3 of a finished row with maximum M, denominator L and numerator A.
+__device__ __forceinline__ void write_row(const AttnProblem &p, int b, int hq, int qi, int c, float4 A, float M, float L) {
+    const float inv = L > 0.f || L != L ? 1.f / L : 0.f;   // a row that saw nothing gives 0
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.o) + o_at(p, b, hq, qi) + c;
+    o[0] = __float2bfloat16_rn(A.x * inv); o[1] = __float2bfloat16_rn(A.y * inv);
+    o[2] = __float2bfloat16_rn(A.z * inv); o[3] = __float2bfloat16_rn(A.w * inv);
+    if (p.lse && c == 0)
+        p.lse[((long long)b * p.Hq + hq) * p.Sq + qi] = L > 0.f ? (M + log2f(L)) * kLn2 : L != L ? L : -INFINITY;
+}
+
+struct Tc8Bars {
+    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], p_full[2], pv_done[2], q_full, drain;
+};
+
+// x * 2^d for a whole d in -254 .. 254.
+__device__ __forceinline__ float scale_by(float x, int d) { return x * pow2_of(d / 2) * pow2_of(d - d / 2); }
+
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
+    if constexpr (N == 8) tmem_ld8(addr, r);
+    else if constexpr (N == 16) tmem_ld16(addr, r);
+    else tmem_ld32(addr, r);
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(TC_THREADS, 1)
+attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProblem kp, int q_vec, int row_blocks, int flat) {
+    using C = Tc8<D, NR>;
+    const AttnProblem &p = kp.a;
+    const Kv8Cache &c = kp.c;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Tc8Bars bars;
+    __shared__ uint32_t tmem_sh;
+    __shared__ volatile int abort_flag;
+    __shared__ float q_back[NR];              // raw score times K scale to base-2 score
+    __shared__ int row_pos[NR];               // positions of the rows
+    __shared__ float red[2][4][2][NR];        // maxima of a group's warps
+    __shared__ float sum_l[2][4][NR], ref_m[2][NR];
+    __shared__ uint32_t poison[NR][D / 32];   // channels that a NaN value reaches
+    griddep_launch();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint8_t *sgen = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sbase = smem_u32(sgen);
+    const uint32_t sQ = sbase + C::Q_OFF, sP = sbase + C::P_OFF, sRing = sbase + C::RING_OFF;
+    const int G = p.Hq / p.Hkv, items_per_b = p.Hkv * row_blocks;
+
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TC_TMEM);
+    if (tid == 32) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(smem_u32(&bars.full[s]), 1);
+            mbar_init(smem_u32(&bars.empty[s]), 1);
+        }
+        for (int g = 0; g < 2; ++g) {
+            mbar_init(smem_u32(&bars.s_full[g]), 1);
+            mbar_init(smem_u32(&bars.p_full[g]), 4);
+            mbar_init(smem_u32(&bars.pv_done[g]), 1);
+        }
+        mbar_init(smem_u32(&bars.q_full), 8);
+        mbar_init(smem_u32(&bars.drain), 1);
+        abort_flag = 0;
+        mbar_init_fence();
+    }
+    for (int i = tid; i < (int)C::Q_BYTES / 16; i += TC_THREADS) st_shared_v4(sQ + 16 * i, 0u, 0u, 0u, 0u);   // unused columns
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_sh;
+    Walk w;
+    bool live = walk_begin(kp, items_per_b, flat, w);
+
+    if (warp == 8) {
+        // ================================================================ loads: a lane per page of the tile
+        const int per_tile = TT / c.P;
+        const int rows_total = c.n_pages * 2 * c.Hkv * c.P;
+        tma_prefetch_desc(&mpages);
+        bool ok = true;
+        int gt = 0;
+        while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
+            // first row of the K page of this lane at the piece's tile i; past the end (zeros) where no row sees the page
+            auto row_of = [&](int i) {
+                const int tok = i < w.tiles && lane < per_tile ? w.ks.tile(w.tile0 + i) * TT + lane * c.P : w.n;
+                const bool wanted = tok < w.n && (!p.window || tok + c.P - 1 > w.n - p.Sq - p.window || tok < p.sinks);
+                const int page = wanted ? kv8_page(c, w.b, tok, p.status) : -1;
+                return page < 0 ? -1 : (page * 2 * c.Hkv + w.kvh) * c.P;
+            };
+            int next = row_of(0);
+            for (int i = 0; i < w.tiles; ++i, ++gt) {
+                const int row = next, st = gt % C::STAGES;
+                next = row_of(i + 1);
+                ok = mbar_wait(smem_u32(&bars.empty[st]), ((gt / C::STAGES) & 1) ^ 1, &abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const uint32_t bar = smem_u32(&bars.full[st]), dst = sRing + st * 2 * C::TILE + lane * c.P * D;
+                if (lane == 0) mbar_expect_tx(bar, 2 * C::TILE);
+                __syncwarp();
+                if (lane < per_tile) {
+                    tma_load_2d(dst, &mpages, bar, 0, row < 0 ? rows_total : row);
+                    tma_load_2d(dst + C::TILE, &mpages, bar, 0, row < 0 ? rows_total : row + c.Hkv * c.P);
+                }
+            }
+            walk_step(kp, row_blocks, w);
+        }
+        if (!ok) {
+            abort_flag = 1;
+            if (lane == 0) atomicExch(p.status, kStatusTimeout);
+            const uint64_t t0 = globaltimer_ns();   // copies in flight land
+            while (globaltimer_ns() - t0 < 50000ull) {
+            }
+        }
+    } else if (warp == 9) {
+        // ================================================================ products
+        bool ok = true;
+        int gt = 0, pieces = 0, cnt[2] = {0, 0};   // tiles and pieces so far, and tiles of each group
+        while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
+            if (lane == 0) {
+                ok = mbar_wait(smem_u32(&bars.q_full), pieces & 1, &abort_flag);
+                auto scores = [&](int i) {   // S^T of the piece's tile i
+                    const int st = (gt + i) % C::STAGES, g = (gt + i) & 1;
+                    if (!mbar_wait_spin(smem_u32(&bars.full[st]), ((gt + i) / C::STAGES) & 1, &abort_flag)) return false;
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_any(sRing + st * 2 * C::TILE, 16, C::GROUP8, C::SWZ), bd = sdesc_any(sQ, 16, C::GROUP8, C::SWZ);
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k)
+                        mma_ss_f8(tmem + C::S_COL + 32 * g, ad + 2 * k, bd + 2 * k, C::IDESC_S, k > 0);
+                    mma_commit(smem_u32(&bars.s_full[g]));
+                    return true;
+                };
+                for (int i = 0; i < min(2, w.tiles) && ok; ++i) ok = scores(i);
+                for (int i = 0; i < w.tiles && ok; ++i) {
+                    const int st = (gt + i) % C::STAGES, g = (gt + i) & 1;
+                    ok = mbar_wait_spin(smem_u32(&bars.p_full[g]), cnt[g] & 1, &abort_flag);
+                    if (!ok) break;
+                    ++cnt[g];
+                    tc_fence_after();
+                    const uint64_t ad = sdesc_any(sRing + st * 2 * C::TILE + C::TILE, 16, C::GROUP8, C::SWZ);
+                    const uint64_t bd = sdesc_any(sP + g * C::P_BYTES, 128, TT * 16, 0);
+#pragma unroll
+                    for (int k = 0; k < TT / 32; ++k)
+                        mma_ss_f8(tmem + C::O_COL + 48 * g, ad + k * (4 * C::GROUP8 / 16), bd + k * (512 / 16), C::IDESC_O, i > 1 || k > 0);
+                    mma_commit(smem_u32(&bars.pv_done[g]));
+                    mma_commit(smem_u32(&bars.empty[st]));
+                    if (i + 2 < w.tiles) ok = scores(i + 2);
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            gt += w.tiles;
+            ++pieces;
+            walk_step(kp, row_blocks, w);
+        }
+        if (lane == 0) {
+            if (!ok) {
+                abort_flag = 1;
+                atomicExch(p.status, kStatusTimeout);
+            }
+            mma_commit(smem_u32(&bars.drain));
+            mbar_wait(smem_u32(&bars.drain), 0, nullptr, 20000000ull);
+        }
+        __syncwarp();
+    } else {
+        // ================================================================ scores to weights
+        const int g = warp >> 2, w4 = warp & 3, r128 = tid & 127;
+        const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
+        const uint32_t s_addr = tmem + C::S_COL + 32 * g + lane_off, o_addr = tmem + C::O_COL + 48 * g + lane_off;
+        const uint32_t p_row = sP + g * C::P_BYTES + r128 * 16;
+        // a wait that ran out is told to the whole group at its next vote, so that all leave together
+        bool failed = false;
+        int gt = 0, done = 0;   // tiles so far, of both groups and of this one
+        while (live && walk_next<NR>(kp, row_blocks, flat, w)) {
+            // ------------------------------------------------------------ Q parts: a warp per row
+            for (int r = warp; r < NR; r += 8) {
+                constexpr int E = D / 32;   // channels E * lane ..
+                const int gr = w.r0 + r;
+                float x[E], mx = 0.f;
+                bool bad = false;
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] = 0.f;
+                if (r < w.rows) {
+                    const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(p.q) +
+                                             q_at(p, w.b, w.kvh * G + gr / p.Sq, gr % p.Sq) + E * lane;
+                    if (q_vec) {
+#pragma unroll
+                        for (int e = 0; e < E; e += 2) {
+                            const uint32_t v = *reinterpret_cast<const uint32_t *>(Q + e);
+                            x[e] = __uint_as_float(v << 16);
+                            x[e + 1] = __uint_as_float(v & 0xffff0000u);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < E; ++e) x[e] = __bfloat162float(Q[e]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    mx = fmaxf(mx, fabsf(x[e]));
+                    bad |= !(fabsf(x[e]) <= 3.4028235e38f);
+                }
+                mx = warp_max(mx);
+                bad = __any_sync(0xffffffffu, bad);
+                const int ex = max(-100, min(100, 7 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+                const float up = pow2_of(ex);
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    const int col = part * NR + r;
+                    uint32_t word = 0;
+#pragma unroll
+                    for (int e = 0; e < E; e += 2) {
+                        const float a = x[e] * (part ? 16.f : up), b2 = x[e + 1] * (part ? 16.f : up);
+                        const uint32_t k = bad ? 0x7f7fu : f32_to_e4m3x2(a, b2);
+                        const float2 f = e4m3x2_to_f32(k);
+                        x[e] = a - f.x;          // what is left, for the next part
+                        x[e + 1] = b2 - f.y;
+                        word |= k << (8 * e);
+                    }
+                    const uint32_t byte = E * lane, piece = byte >> 4;
+                    const uint32_t at = sQ - sbase + col * D + ((D == 128 ? piece ^ (col & 7) : piece ^ (col >> 1 & 3)) << 4) + (byte & 15);
+                    if (E == 4) *reinterpret_cast<uint32_t *>(sgen + at) = word;
+                    else *reinterpret_cast<uint16_t *>(sgen + at) = (uint16_t)word;
+                }
+                if (lane == 0) {
+                    q_back[r] = pow2_of(-ex) * p.scale_log2;
+                    row_pos[r] = w.n - p.Sq + gr % p.Sq;
+                }
+            }
+            for (int i = tid; i < NR * (D / 32); i += 256) poison[i / (D / 32)][i % (D / 32)] = 0;
+            fence_proxy_async_smem();
+            named_barrier(1, 256);
+            if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+
+            float m[NR], mp[NR], l[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                m[r] = mp[r] = kRowFloor;
+                l[r] = 0.f;
+            }
+            // tokens that some row sees, and the page of one; its scales
+            auto page_of = [&](int i) {
+                const int key = i < w.tiles ? w.ks.tile(w.tile0 + i) * TT + r128 : w.n;
+                const bool wanted = key < w.n && (!p.window || key > w.n - p.Sq - p.window || key < p.sinks);
+                return wanted ? kv8_page(c, w.b, key, p.status) : -1;
+            };
+            auto scales_of = [&](int page, float &a, float &b) {
+                a = b = 1.f;
+                if (page < 0) return;
+                const float *s = c.scales + (long long)page * 2 * c.Hkv + w.kvh;
+                a = s[0];
+                b = s[c.Hkv];
+            };
+            // this group's tiles of the piece, the pages of the next two and the scales of the next in flight
+            int i = (gt & 1) == g ? 0 : 1, taken = 0;
+            int page = page_of(i), page1 = page_of(i + 2);
+            float ks, vs;
+            scales_of(page, ks, vs);
+            for (; i < w.tiles; i += 2) {
+                const int page2 = page_of(i + 4);
+                float ks1, vs1;
+                scales_of(page1, ks1, vs1);
+                const int tile = w.ks.tile(w.tile0 + i), key0 = tile * TT, key = key0 + r128;
+                const int st = (gt + i) % C::STAGES;
+                bool ok = !failed && mbar_wait(smem_u32(&bars.s_full[g]), done & 1, &abort_flag);
+                failed = !__all_sync(0xffffffffu, ok);
+                tc_fence_after();
+                uint32_t raw[2 * NR];
+                tmem_ld_n(s_addr, raw);
+                tmem_ld_wait();
+                const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs);
+                float y[NR];
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+                    y[r] = fmaf(__uint_as_float(raw[NR + r]), 0.0625f, __uint_as_float(raw[r])) * (q_back[r] * kscale);
+                // a tile that some row does not see the whole of
+                const bool edge = key0 + TT - 1 > w.n - p.Sq || (p.window && key0 <= w.n - 1 - p.window && key0 + TT > p.sinks);
+                if (edge) {
+                    bool all = true;
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const int pos = row_pos[r];
+                        const bool sees = page >= 0 && key <= pos && (!p.window || key > pos - p.window || key < p.sinks);
+                        all = all && (sees || r >= w.rows);
+                        y[r] = sees ? y[r] : -INFINITY;
+                    }
+                    // Values of tokens that no row sees, or not all, must not reach the others as 0 * NaN: the former are
+                    // cleared, the latter's NaN codes too, and remembered for the rows that do see them.
+                    if (!all && !failed) {
+                        const uint32_t vrow = sRing + st * 2 * C::TILE + C::TILE + r128 * D;
+                        if (mbar_wait(smem_u32(&bars.full[st]), ((gt + i) / C::STAGES) & 1, &abort_flag)) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                const uint32_t at = vrow + 16 * q;
+                                if (page < 0) {
+                                    st_shared_v4(at, 0u, 0u, 0u, 0u);
+                                    continue;
+                                }
+                                const uint4 v = ld_shared_v4(at);
+                                uint32_t x[4] = {v.x, v.y, v.z, v.w}, nan_any = 0, bits = 0;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    // top bit of each byte whose other seven are all set
+                                    const uint32_t nan = ((x[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                                    nan_any |= nan;
+                                    bits |= ((nan >> 7 & 1u) | (nan >> 14 & 2u) | (nan >> 21 & 4u) | (nan >> 28 & 8u)) << (4 * e);
+                                    x[e] &= ~((nan >> 7) * 0xffu);
+                                }
+                                if (!nan_any) continue;
+                                st_shared_v4(at, x[0], x[1], x[2], x[3]);
+                                const int ch = 16 * (D == 128 ? q ^ (r128 & 7) : q ^ (r128 >> 1 & 3));
+#pragma unroll
+                                for (int r = 0; r < NR; ++r)
+                                    if (y[r] != -INFINITY) atomicOr(&poison[r][ch / 32], bits << (ch & 31));
+                            }
+                        }
+                    }
+                } else if (page < 0) {   // the table holds no page for it: its codes are zeros
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) y[r] = -INFINITY;
+                }
+                bool up = failed;
+#pragma unroll
+                for (int r = 0; r < NR; ++r) up |= y[r] > m[r] || y[r] + ev > mp[r];
+                if (named_barrier_or(2 + g, 128, up)) {
+                    // some reference has to move
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const float a = warp_max(y[r]), b2 = warp_max(y[r] + ev);
+                        if (lane == 0) {
+                            red[g][w4][0][r] = a;
+                            red[g][w4][1][r] = b2;
+                        }
+                    }
+                    if (named_barrier_or(2 + g, 128, failed)) {
+                        failed = true;
+                        break;
+                    }
+                    float f[NR];
+#pragma unroll
+                    for (int r = 0; r < NR; ++r) {
+                        const float a = fmaxf(fmaxf(red[g][0][0][r], red[g][1][0][r]), fmaxf(red[g][2][0][r], red[g][3][0][r]));
+                        const float b2 = fmaxf(fmaxf(red[g][0][1][r], red[g][1][1][r]), fmaxf(red[g][2][1][r], red[g][3][1][r]));
+                        const float mn = a > m[r] ? ceilf(a) + 1.f : m[r], mpn = b2 > mp[r] ? ceilf(b2) + 1.f : mp[r];
+                        l[r] *= ex2_approx(m[r] - mn);
+                        f[r] = ex2_approx(mp[r] - mpn);
+                        m[r] = mn;
+                        mp[r] = mpn;
+                    }
+                    if (taken > 0) {   // (every product of the group so far is waited for first)
+                        ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
+                        failed = !__all_sync(0xffffffffu, ok);
+                        tc_fence_after();
+#pragma unroll
+                        for (int pl = 0; pl < C::PLANES; ++pl) {
+                            uint32_t o[16];
+                            tmem_ld16(o_addr + 16 * pl, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                if (16 * pl + e < 3 * NR) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(16 * pl + e) % NR]);
+                            tmem_st16(o_addr + 16 * pl, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], o[8], o[9], o[10], o[11],
+                                      o[12], o[13], o[14], o[15]);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                // weights, and their parts in words of four rows
+                uint32_t part[3][NR / 4];
+#pragma unroll
+                for (int r = 0; r < NR; r += 2) {
+                    l[r] += ex2_approx(y[r] - m[r]);
+                    l[r + 1] += ex2_approx(y[r + 1] - m[r + 1]);
+                    float a = ex2_approx(y[r] + ev - mp[r] + 8.f), b2 = ex2_approx(y[r + 1] + ev - mp[r + 1] + 8.f);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) {
+                        const uint32_t x = f32_to_e4m3x2(a, b2);
+                        if (r % 4 == 0) part[k][r / 4] = x;
+                        else part[k][r / 4] |= x << 16;
+                        const float2 f = e4m3x2_to_f32(x);
+                        a = (a - f.x) * 16.f;
+                        b2 = (b2 - f.y) * 16.f;
+                    }
+                }
+                // the product that read the last weights is done
+                if (done > 0) {
+                    ok = !failed && mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
+                    failed = !__all_sync(0xffffffffu, ok);
+                }
+#pragma unroll
+                for (int pl = 0; pl < C::PLANES; ++pl) {
+                    uint32_t x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        constexpr int W = NR / 4;   // words of a part
+                        const int word = 4 * pl + e;
+                        x[e] = word < 3 * W ? part[word / W < 3 ? word / W : 0][word % W] : 0u;
+                    }
+                    st_shared_v4(p_row + pl * TT * 16, x[0], x[1], x[2], x[3]);
+                }
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g]));
+                ++done;
+                ++taken;
+                page = page1; page1 = page2;
+                ks = ks1; vs = vs1;
+            }
+            // ------------------------------------------------------------ the groups' states meet
+            float *so = reinterpret_cast<float *>(sgen + C::O_OFF);   // [2][NR][D]
+            if (taken > 0 && !failed) {
+                const bool ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
+                failed = !__all_sync(0xffffffffu, ok);
+            }
+            tc_fence_after();
+            uint32_t o[C::NP];
+#pragma unroll
+            for (int pl = 0; pl < C::PLANES; ++pl) tmem_ld16(o_addr + 16 * pl, o + 16 * pl);
+            tmem_ld_wait();
+            tc_fence_before();
+            const int ch = D == 128 ? r128 : w4 * 16 + lane;   // M = 64: 16 lanes of each warp's 32
+            const bool mine = D == 128 || lane < 16;
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const float sum = warp_sum(l[r]);
+                if (lane == 0) sum_l[g][w4][r] = sum;
+                if (r128 == 0) ref_m[g][r] = m[r];
+                float v = fmaf(__uint_as_float(o[2 * NR + r]), 0x1p-8f, fmaf(__uint_as_float(o[NR + r]), 0x1p-4f, __uint_as_float(o[r])));
+                // in units of 2^(m' - 8) so far: relative to m
+                v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, mp[r] - m[r]))) : 0.f;
+                if (mine) so[(g * NR + r) * D + ch] = v;
+            }
+            named_barrier(1, 256);
+            const size_t slot = 2 * (size_t)blockIdx.x + (w.tile0 == 0 ? 1 : 0);
+            for (int x = tid; x < w.rows * (D / 4); x += 256) {
+                const int r = x / (D / 4), c4 = x % (D / 4) * 4, gr = w.r0 + r;
+                float M = -INFINITY, L = 0.f, mg[2], lg[2];
+                float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    lg[e] = (sum_l[e][0][r] + sum_l[e][1][r]) + (sum_l[e][2][r] + sum_l[e][3][r]);
+                    mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref_m[e][r] : -INFINITY;
+                    M = fmaxf(M, mg[e]);
+                }
+                const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float wt = ex2_approx(mg[e] - ref);
+                    const float4 v = *reinterpret_cast<const float4 *>(so + (e * NR + r) * D + c4);
+                    A.x = fmaf(wt, v.x, A.x); A.y = fmaf(wt, v.y, A.y);
+                    A.z = fmaf(wt, v.z, A.z); A.w = fmaf(wt, v.w, A.w);
+                    L = fmaf(wt, lg[e], L);
+                }
+                const uint32_t nan = poison[r][c4 / 32] >> (c4 & 31);
+                if (nan & 15u) {
+                    if (nan & 1u) A.x = NAN;
+                    if (nan & 2u) A.y = NAN;
+                    if (nan & 4u) A.z = NAN;
+                    if (nan & 8u) A.w = NAN;
+                }
+                if (w.whole) write_row(p, w.b, w.kvh * G + gr / p.Sq, gr % p.Sq, c4, A, M, L);
+                else {
+                    *reinterpret_cast<float4 *>(kp.part + (slot * NR + r) * D + c4) = A;
+                    if (c4 == 0) kp.part_ml[slot * NR + r] = make_float2(M, L);
+                }
+            }
+            gt += w.tiles;
+            walk_step(kp, row_blocks, w);
+            if (named_barrier_or(1, 256, failed)) {   // (and the buffers are free again)
+                failed = true;
+                break;
+            }
+        }
+        if (failed) {
+            abort_flag = 1;
+            if (lane == 0) atomicExch(p.status, kStatusTimeout);
+        }
+    }
+    tc_fence_before();
+    __syncwarp();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, TC_TMEM);
+    }
+}
+
+// Rows of the items that several CTAs shared: a block per item, the same cut of the work as above.
+template <int D, int NR>
+__global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnProblem kp, int row_blocks, int grid) {
+    const AttnProblem &p = kp.a;
+    const int G = p.Hq / p.Hkv, R = G * p.Sq, items_per_b = p.Hkv * row_blocks;
+    const int b = blockIdx.x / items_per_b, item = blockIdx.x % items_per_b;
+    const FlatCut w = flat_cut(kp, items_per_b, b, grid);
+    const int ui = item_units(kp, b);
+    const long long p0 = w.base + (long long)item * ui;
+    const int c0 = cta_of(w, p0 + kItemCost), c1 = cta_of(w, p0 + ui - 1);   // CTAs of the first and the last tile
+    griddep_wait();
+    if (c0 == c1) return;
+    const int r0 = item % row_blocks * NR, rows = min(NR, R - r0);
+    constexpr int KG = 8;   // pieces whose states are loaded together
+    for (int x = threadIdx.x; x < rows * (D / 4); x += blockDim.x) {
+        const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
+        float M = -INFINITY, L = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k0 = c0; k0 <= c1; k0 += KG) {
+            float2 ml[KG];
+            float4 v[KG];
+            float mx = M;
+#pragma unroll
+            for (int e = 0; e < KG; ++e) {
+                const size_t slot = 2 * (size_t)min(k0 + e, c1) + (k0 + e == c0 ? 1 : 0);
+                ml[e] = k0 + e <= c1 ? kp.part_ml[slot * NR + r] : make_float2(-INFINITY, 0.f);
+                v[e] = k0 + e <= c1 ? *reinterpret_cast<const float4 *>(kp.part + (slot * NR + r) * D + c)
+                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+                mx = fmaxf(mx, ml[e].x);
+            }
+            const float ref = mx == -INFINITY ? 0.f : mx, a = ex2_approx(M - ref);
+            A.x *= a; A.y *= a; A.z *= a; A.w *= a;
+            L *= a;
+            M = mx;
+#pragma unroll
+            for (int e = 0; e < KG; ++e) {
+                const float wt = ex2_approx(ml[e].x - ref);
+                A.x = fmaf(wt, v[e].x, A.x); A.y = fmaf(wt, v[e].y, A.y);
+                A.z = fmaf(wt, v[e].z, A.z); A.w = fmaf(wt, v[e].w, A.w);
+                L = fmaf(wt, ml[e].y, L);
+            }
+        }
+        write_row(p, b, item / row_blocks * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
+    }
+}
+
 int general_splits(const AttnProblem &p, int sm_count) {
     const int R = p.Hq / p.Hkv * p.Sq;
     const long long items = (long long)p.B * p.Hkv * ((R + RB - 1) / RB);
@@ -196,21 +885,75 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
+static bool use_tc(const AttnProblem &p) {
+    return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128) && p.Sk > 0 && tensor_map_encoder() != nullptr;
+}
+
+// Launch shape of the tensor-core kernel: items of few tiles are not cut (a CTA each, one launch, no join), else one wave of
+// CTAs shares all tiles.
+struct TcPlan {
+    int nr, row_blocks, flat, grid;
+};
+static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
+    TcPlan t;
+    const int R = p.Hq / p.Hkv * p.Sq;
+    t.nr = R <= 4 ? 4 : R <= 8 ? 8 : 16;
+    t.row_blocks = (R + t.nr - 1) / t.nr;
+    const long long items = (long long)p.B * p.Hkv * t.row_blocks;
+    const long long per = key_stream_max(p.Sq, p.Sk, p.window ? p.window : p.Sk, p.sinks, TT);
+    t.flat = per > 4;
+    const long long worth = items * per / kMinTiles;
+    t.grid = (int)(!t.flat ? items : worth < sm_count ? (worth < 1 ? 1 : worth) : sm_count);
+    return t;
+}
+
 size_t kv8_attn_partial_bytes(const Kv8AttnProblem &kp, int sm_count) {
     const AttnProblem &p = kp.a;
+    if (use_tc(p)) {
+        const TcPlan t = tc_plan(p, sm_count);
+        const size_t rows = 2 * (size_t)t.grid * t.nr;
+        return t.flat ? round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float2)) : 0;
+    }
     const int splits = general_splits(p, sm_count);
     const size_t rows = (size_t)splits * p.B * p.Hq * p.Sq;
     return splits > 1 ? round256(rows * p.D * sizeof(float)) + 2 * round256(rows * sizeof(float)) : 0;
+}
+
+template <int D, int NR>
+static cudaError_t launch_tc_t(Kv8AttnProblem kp, const TcPlan &t, char *partials, cudaStream_t s) {
+    using C = Tc8<D, NR>;
+    const AttnProblem &p = kp.a;
+    cudaError_t e = set_max_dynamic_smem((const void *)attn_kv8_tc_kernel<D, NR>, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    CUtensorMap m;
+    const long long rows = (long long)kp.c.n_pages * 2 * kp.c.Hkv * kp.c.P;
+    if (!make_u8_rows_map(&m, kp.c.pages, D, rows, (uint32_t)kp.c.P)) return cudaErrorInvalidValue;
+    kp.part = reinterpret_cast<float *>(partials);
+    kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * NR * D * sizeof(float)));
+    const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 1) == 0;
+    attn_kv8_tc_kernel<D, NR><<<t.grid, TC_THREADS, C::SMEM, s>>>(m, kp, q_vec, t.row_blocks, t.flat);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || !t.flat) return e;
+    count_launches(1);
+    return launch_dependent(kv8_combine_kernel<D, NR>, dim3((unsigned)(p.B * p.Hkv * t.row_blocks)), dim3(256), 0, s, kp,
+                            t.row_blocks, t.grid);
 }
 
 cudaError_t launch_attn_kv8(const Kv8AttnProblem &kp0, void *partials, int sm_count, cudaStream_t s) {
     Kv8AttnProblem kp = kp0;
     AttnProblem &p = kp.a;
     const int R = p.Hq / p.Hkv * p.Sq;
+    char *at = static_cast<char *>(partials);
+    if (use_tc(p)) {
+        const TcPlan t = tc_plan(p, sm_count);
+        if (p.D == 64)
+            return t.nr == 4 ? launch_tc_t<64, 4>(kp, t, at, s) : t.nr == 8 ? launch_tc_t<64, 8>(kp, t, at, s) : launch_tc_t<64, 16>(kp, t, at, s);
+        return t.nr == 4 ? launch_tc_t<128, 4>(kp, t, at, s) : t.nr == 8 ? launch_tc_t<128, 8>(kp, t, at, s) : launch_tc_t<128, 16>(kp, t, at, s);
+    }
     p.splits = general_splits(p, sm_count);
     p.keep_nan = 1;
     const size_t rows = (size_t)p.splits * p.B * p.Hq * p.Sq;
-    char *at = static_cast<char *>(partials);
     p.part_acc = reinterpret_cast<float *>(at);
     p.part_m = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)));
     p.part_l = reinterpret_cast<float *>(at + round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float)));

@@ -99,6 +99,20 @@ inline bool make_bf16_tile_map_strided(CUtensorMap *m, const void *g, int D, lon
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2-D map over contiguous 8-bit rows [rows][D], D 64 or 128: boxes of box_rows whole rows, swizzled over the row's bytes
+// (D = 128: 16-byte piece c of row r at c ^ (r % 8); D = 64: at c ^ ((r / 2) % 4)); rows past the end read as zero.
+inline bool make_u8_rows_map(CUtensorMap *m, const void *g, int D, long long rows, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc || (D != 64 && D != 128)) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)D};
+    cuuint32_t box[2] = {(cuuint32_t)D, box_rows};
+    cuuint32_t es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(g), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // True when make_bf16_tile_map_strided can describe the tensor (no encoding call): 16-byte
 // aligned base, D a multiple of 64, and every stride of a dimension longer than one a non-zero
 // multiple of 16 bytes below 2^40.
