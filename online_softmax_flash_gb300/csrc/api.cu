@@ -1201,7 +1201,7 @@ static int check_kv8(const void *pages, const float *scales, int n_pages, int pa
     c.pages = static_cast<unsigned char *>(const_cast<void *>(pages));
     c.scales = const_cast<float *>(scales);
     c.table = table;
-    c.n_pages = n_pages; c.P = page_tokens; c.per_seq = per_seq; c.Hkv = Hkv; c.D = D;
+    c.n_pages = n_pages; c.P = page_tokens; c.log2_p = 31 - __builtin_clz(page_tokens); c.per_seq = per_seq; c.Hkv = Hkv; c.D = D;
     return OSF_OK;
 }
 static int check_kv8_buffers(const Kv8Cache &c, int B) {

@@ -71,7 +71,7 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
             const long long s = (long long)page * 2 * c.Hkv + kvh;
             kscale = pow2_of(kv8_exponent(c.scales[s])) * p.scale_log2;
             vscale = pow2_of(kv8_exponent(c.scales[s + c.Hkv]));
-            at = (s * c.P + key % c.P) * D;
+            at = (s * c.P + (key & (c.P - 1))) * D;
         }
         const long long v_off = (long long)c.Hkv * c.P * D;
         const int per = 2 * D / 16;   // 16-byte pieces of a key: K's, then V's
@@ -195,7 +195,7 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 // A token's V scale is not applied to its codes but to its weight.  Scales can lie far apart, so what goes into the
 // product is 2^(y + e - m'), y the base-2 score, e the exponent of the scale and m' a reference of the sums y + e: exact
 // relative to the largest P * scale, whichever page it comes from.  The denominator has its own reference m of the y.
-// Both references are whole numbers and move only when a value passes them, to 1 .. 2 above the largest.
+// Both references are whole numbers and move only when a value passes them, to 3 .. 4 above the largest.
 //
 // A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Warp 8 loads, warp 9 issues the
 // products, and two groups of four warps take the tiles in turn, each with its own S^T, O^T and references, one token's
@@ -206,6 +206,7 @@ constexpr int TC_THREADS = 320;
 constexpr uint32_t TC_TMEM = 256;
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
 constexpr int kMaxRing = 12;
+constexpr float kHeadroom = 3.f;              // a new reference is this, and up to 1 more, above the largest
 
 template <int D, int NR>
 struct Tc8 {
@@ -359,6 +360,31 @@ struct Tc8Bars {
 // x * 2^d for a whole d in -254 .. 254.
 __device__ __forceinline__ float scale_by(float x, int d) { return x * pow2_of(d / 2) * pow2_of(d - d / 2); }
 
+// The maxima over a warp of each of N values (N a power of two up to 32): v[0] becomes the maximum of the value whose index
+// is returned.  Every step halves the values that a lane still follows.
+template <int N>
+__device__ __forceinline__ int warp_max_each(float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    int at = 0;
+#pragma unroll
+    for (int s = 16, n = N; s > 0; s >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool hi = lane & s;
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                if (i >= n) break;
+                const float keep = hi ? v[i + n] : v[i], send = hi ? v[i] : v[i + n];
+                v[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, send, s));
+            }
+            at = 2 * at + hi;
+        } else {
+            v[0] = fmaxf(v[0], __shfl_xor_sync(0xffffffffu, v[0], s));
+        }
+    }
+    return at;
+}
+
 template <int N>
 __device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
     if constexpr (N == 8) tmem_ld8(addr, r);
@@ -376,10 +402,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     __shared__ Tc8Bars bars;
     __shared__ uint32_t tmem_sh;
     __shared__ volatile int abort_flag;
-    __shared__ float q_back[NR];              // raw score times K scale to base-2 score
-    __shared__ int row_pos[NR];               // positions of the rows
-    __shared__ float red[2][4][2][NR];        // maxima of a group's warps
-    __shared__ float sum_l[2][4][NR], ref_m[2][NR];
+    __shared__ __align__(16) float q_back[NR];             // raw score times K scale to base-2 score
+    __shared__ int row_pos[NR];                            // positions of the rows
+    __shared__ float red[2][4][2 * NR];                    // maxima of a group's warps: of y, then of y + e
+    __shared__ __align__(16) float ref[2][2 * NR], fac[2][2 * NR];   // references m, m', and what moves to them
+    __shared__ float sum_l[2][4][NR];
     __shared__ uint32_t poison[NR][D / 32];   // channels that a NaN value reaches
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -567,14 +594,15 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 }
             }
             for (int i = tid; i < NR * (D / 32); i += 256) poison[i / (D / 32)][i % (D / 32)] = 0;
+            if (r128 < 2 * NR) ref[g][r128] = kRowFloor;
             fence_proxy_async_smem();
             named_barrier(1, 256);
             if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
 
-            float m[NR], mp[NR], l[NR];
+            float m[NR], mp[NR], l[NR];   // -m, -m' and this thread's part of the denominator
 #pragma unroll
             for (int r = 0; r < NR; ++r) {
-                m[r] = mp[r] = kRowFloor;
+                m[r] = mp[r] = -kRowFloor;
                 l[r] = 0.f;
             }
             // tokens that some row sees, and the page of one; its scales
@@ -607,11 +635,16 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 uint32_t raw[2 * NR];
                 tmem_ld_n(s_addr, raw);
                 tmem_ld_wait();
-                const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs);
+                const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs), ev8 = ev + 8.f;
                 float y[NR];
 #pragma unroll
-                for (int r = 0; r < NR; ++r)
-                    y[r] = fmaf(__uint_as_float(raw[NR + r]), 0.0625f, __uint_as_float(raw[r])) * (q_back[r] * kscale);
+                for (int r = 0; r < NR; r += 4) {
+                    const float4 back = *reinterpret_cast<const float4 *>(q_back + r);
+                    const float qb[4] = {back.x, back.y, back.z, back.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        y[r + e] = fmaf(__uint_as_float(raw[NR + r + e]), 0.0625f, __uint_as_float(raw[r + e])) * (qb[e] * kscale);
+                }
                 // a tile that some row does not see the whole of
                 const bool edge = key0 + TT - 1 > w.n - p.Sq || (p.window && key0 <= w.n - 1 - p.window && key0 + TT > p.sinks);
                 if (edge) {
@@ -658,33 +691,37 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
 #pragma unroll
                     for (int r = 0; r < NR; ++r) y[r] = -INFINITY;
                 }
-                bool up = failed;
+                float top = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) up |= y[r] > m[r] || y[r] + ev > mp[r];
-                if (named_barrier_or(2 + g, 128, up)) {
+                for (int r = 0; r < NR; ++r) top = fmax3(top, y[r] + m[r], y[r] + (mp[r] + ev));
+                if (named_barrier_or(2 + g, 128, failed || top > 0.f)) {
                     // some reference has to move
+                    float v[2 * NR];
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
-                        const float a = warp_max(y[r]), b2 = warp_max(y[r] + ev);
-                        if (lane == 0) {
-                            red[g][w4][0][r] = a;
-                            red[g][w4][1][r] = b2;
-                        }
+                        v[r] = y[r];
+                        v[NR + r] = y[r] + ev;
                     }
+                    const int at = warp_max_each(v);
+                    if ((lane & (32 / (2 * NR) - 1)) == 0) red[g][w4][at] = v[0];
                     if (named_barrier_or(2 + g, 128, failed)) {
                         failed = true;
                         break;
                     }
+                    if (r128 < 2 * NR) {
+                        const float a = fmaxf(fmaxf(red[g][0][r128], red[g][1][r128]), fmaxf(red[g][2][r128], red[g][3][r128]));
+                        const float old = ref[g][r128], now = a > old ? ceilf(a) + kHeadroom : old;
+                        fac[g][r128] = ex2_approx(old - now);
+                        ref[g][r128] = now;
+                    }
+                    named_barrier(2 + g, 128);
                     float f[NR];
 #pragma unroll
                     for (int r = 0; r < NR; ++r) {
-                        const float a = fmaxf(fmaxf(red[g][0][0][r], red[g][1][0][r]), fmaxf(red[g][2][0][r], red[g][3][0][r]));
-                        const float b2 = fmaxf(fmaxf(red[g][0][1][r], red[g][1][1][r]), fmaxf(red[g][2][1][r], red[g][3][1][r]));
-                        const float mn = a > m[r] ? ceilf(a) + 1.f : m[r], mpn = b2 > mp[r] ? ceilf(b2) + 1.f : mp[r];
-                        l[r] *= ex2_approx(m[r] - mn);
-                        f[r] = ex2_approx(mp[r] - mpn);
-                        m[r] = mn;
-                        mp[r] = mpn;
+                        l[r] *= fac[g][r];
+                        f[r] = fac[g][NR + r];
+                        m[r] = -ref[g][r];
+                        mp[r] = -ref[g][NR + r];
                     }
                     if (taken > 0) {   // (every product of the group so far is waited for first)
                         ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
@@ -708,17 +745,15 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 uint32_t part[3][NR / 4];
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
-                    l[r] += ex2_approx(y[r] - m[r]);
-                    l[r + 1] += ex2_approx(y[r + 1] - m[r + 1]);
-                    float a = ex2_approx(y[r] + ev - mp[r] + 8.f), b2 = ex2_approx(y[r + 1] + ev - mp[r + 1] + 8.f);
+                    l[r] += ex2_approx(y[r] + m[r]);
+                    l[r + 1] += ex2_approx(y[r + 1] + m[r + 1]);
+                    uint32_t h = f32_to_f16x2(ex2_approx(y[r] + (mp[r] + ev8)), ex2_approx(y[r + 1] + (mp[r + 1] + ev8)));
 #pragma unroll
                     for (int k = 0; k < 3; ++k) {
-                        const uint32_t x = f32_to_e4m3x2(a, b2);
+                        const uint32_t x = f16x2_to_e4m3x2(h);
                         if (r % 4 == 0) part[k][r / 4] = x;
                         else part[k][r / 4] |= x << 16;
-                        const float2 f = e4m3x2_to_f32(x);
-                        a = (a - f.x) * 16.f;
-                        b2 = (b2 - f.y) * 16.f;
+                        if (k < 2) h = f16x2_rest16(h, e4m3x2_to_f16x2(x));
                     }
                 }
                 // the product that read the last weights is done
@@ -764,10 +799,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             for (int r = 0; r < NR; ++r) {
                 const float sum = warp_sum(l[r]);
                 if (lane == 0) sum_l[g][w4][r] = sum;
-                if (r128 == 0) ref_m[g][r] = m[r];
                 float v = fmaf(__uint_as_float(o[2 * NR + r]), 0x1p-8f, fmaf(__uint_as_float(o[NR + r]), 0x1p-4f, __uint_as_float(o[r])));
                 // in units of 2^(m' - 8) so far: relative to m
-                v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, mp[r] - m[r]))) : 0.f;
+                v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, m[r] - mp[r]))) : 0.f;
                 if (mine) so[(g * NR + r) * D + ch] = v;
             }
             named_barrier(1, 256);
@@ -779,13 +813,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     lg[e] = (sum_l[e][0][r] + sum_l[e][1][r]) + (sum_l[e][2][r] + sum_l[e][3][r]);
-                    mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref_m[e][r] : -INFINITY;
+                    mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref[e][r] : -INFINITY;
                     M = fmaxf(M, mg[e]);
                 }
-                const float ref = M == -INFINITY ? 0.f : M;
+                const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float wt = ex2_approx(mg[e] - ref);
+                    const float wt = ex2_approx(mg[e] - base);
                     const float4 v = *reinterpret_cast<const float4 *>(so + (e * NR + r) * D + c4);
                     A.x = fmaf(wt, v.x, A.x); A.y = fmaf(wt, v.y, A.y);
                     A.z = fmaf(wt, v.z, A.z); A.w = fmaf(wt, v.w, A.w);

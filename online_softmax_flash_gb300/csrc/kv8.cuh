@@ -15,7 +15,7 @@ struct Kv8Cache {
     unsigned char *pages;
     float *scales;
     const int *table;
-    int n_pages, P, per_seq, Hkv, D;
+    int n_pages, P, log2_p, per_seq, Hkv, D;
 };
 
 struct Kv8StoreProblem {
@@ -56,7 +56,7 @@ __device__ __forceinline__ int kv8_length(const int *lens, int b, int most, int 
 }
 // Page of token `tok` (within the table) of sequence b; -1, recorded, where the table holds no page of the cache.
 __device__ __forceinline__ int kv8_page(const Kv8Cache &c, int b, int tok, int *status) {
-    const int page = c.table[(long long)b * c.per_seq + tok / c.P];
+    const int page = c.table[(long long)b * c.per_seq + (tok >> c.log2_p)];
     if (page >= 0 && page < c.n_pages) return page;
     atomicExch(status, (int)OSF_ERR_INVALID);
     return -1;
@@ -80,6 +80,29 @@ __device__ __forceinline__ float2 e4m3x2_to_f32(uint32_t codes) {
 __device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
     unsigned short r;
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The same of two float16.
+__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
+    return h;
+}
+__device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// 16 (a - b) of two float16 pairs, exact where a - b is.
+__device__ __forceinline__ uint32_t f16x2_rest16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("{\n .reg .b32 t;\n sub.rn.f16x2 t, %1, %2;\n mul.rn.f16x2 %0, t, %3;\n}" : "=r"(r) : "r"(a), "r"(b), "r"(0x4c004c00u));
     return r;
 }
 
