@@ -197,32 +197,36 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 // relative to the largest P * scale, whichever page it comes from.  The denominator has its own reference m of the y.
 // Both references are whole numbers and move only when a value passes them, to 3 .. 4 above the largest.
 //
-// A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Warp 8 loads, warp 9 issues the
-// products, and two groups of four warps take the tiles in turn, each with its own S^T, O^T and references, one token's
-// scores per thread; their states meet at the end of the run.  Runs are cut flat over all sequences (see FlatCut), and a
+// A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  One warp loads, two issue the
+// products, and NG groups of four warps take the tiles in turn, each with its own S^T, O^T and references, one token's
+// scores per thread; their states meet at the end of the run.  A group's next scores are computed while it works on these: S^T
+// is free as soon as the group has read it.  Runs are cut flat over all sequences (see FlatCut), and a
 // second kernel joins the pieces of a sequence that several CTAs share.
 constexpr int TT = 128;                   // tokens per tile
-constexpr int TC_THREADS = 320;
-constexpr uint32_t TC_TMEM = 256;
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
 constexpr int kMaxRing = 12;
 constexpr float kHeadroom = 3.f;              // a new reference is this, and up to 1 more, above the largest
 
 template <int D, int NR>
 struct Tc8 {
+    // Groups: as many as their registers allow (a thread holds the scores of NR rows).
+    static constexpr int NG = NR == 4 ? 4 : NR == 8 ? 3 : 2;
+    static constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, THREADS = (W_MMA + 2) * 32;
     static constexpr uint32_t TILE = TT * D;                        // K or V of a tile
     static constexpr int NQ = 2 * NR < 16 ? 16 : 2 * NR;            // columns of Q parts: part p of row r at p * NR + r
     static constexpr int PLANES = (3 * NR + 15) / 16, NP = 16 * PLANES;   // columns of P parts, in planes of 16
     static constexpr uint32_t Q_BYTES = 4096, P_BYTES = PLANES * TT * 16;
-    static constexpr uint32_t O_BYTES = 2 * NR * D * 4;
-    static constexpr uint32_t Q_OFF = 0, P_OFF = Q_BYTES, O_OFF = P_OFF + 2 * P_BYTES;
+    static constexpr uint32_t O_BYTES = NG * NR * D * 4;
+    static constexpr uint32_t Q_OFF = 0, P_OFF = Q_BYTES, O_OFF = P_OFF + NG * P_BYTES;
     static constexpr uint32_t RING_OFF = (O_OFF + O_BYTES + 1023) / 1024 * 1024;
     static constexpr int FIT = (int)((232448u - 1024u - 4096u - RING_OFF) / (2 * TILE));   // 4 KB for the static part
     static constexpr int STAGES = FIT < kMaxRing ? FIT : kMaxRing;
     static constexpr uint32_t SMEM = RING_OFF + STAGES * 2 * TILE + 1024;
     static constexpr uint32_t SWZ = D == 128 ? 2 : 4, GROUP8 = 8 * D;   // swizzle type, bytes of eight rows
     static constexpr uint32_t IDESC_S = idesc_e4m3_f32(TT, NQ, 0, 0), IDESC_O = idesc_e4m3_f32(D, NP, 1, 1);
-    static constexpr uint32_t S_COL = 0, O_COL = 64;                // + 32 g, + 48 g
+    static constexpr uint32_t O_COL = NG * NQ, COLS = O_COL + NG * NP;   // S^T of group g at column NQ g, O^T at O_COL + NP g
+    static constexpr uint32_t TMEM = COLS <= 128 ? 128 : 256;
+    static_assert(COLS <= 256, "TMEM");
 };
 
 // Work is cut flat: an item is one block of query rows of one (batch, kv head), worth its tiles and kItemCost more for what it
@@ -354,7 +358,7 @@ __device__ __forceinline__ void write_row(const AttnProblem &p, int b, int hq, i
 }
 
 struct Tc8Bars {
-    uint64_t full[kMaxRing], empty[kMaxRing], s_full[2], p_full[2], pv_done[2], q_full, drain;
+    uint64_t full[kMaxRing], empty[kMaxRing], s_full[4], s_free[4], p_full[4], pv_done[4], q_full, drain[2];
 };
 
 // x * 2^d for a whole d in -254 .. 254.
@@ -393,9 +397,10 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__((Tc8<D, NR>::THREADS), 1)
 attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProblem kp, int q_vec, int row_blocks, int flat) {
     using C = Tc8<D, NR>;
+    constexpr int NG = C::NG;
     const AttnProblem &p = kp.a;
     const Kv8Cache &c = kp.c;
     extern __shared__ uint8_t smem_raw[];
@@ -404,9 +409,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     __shared__ volatile int abort_flag;
     __shared__ __align__(16) float q_back[NR];             // raw score times K scale to base-2 score
     __shared__ int row_pos[NR];                            // positions of the rows
-    __shared__ float red[2][4][2 * NR];                    // maxima of a group's warps: of y, then of y + e
-    __shared__ __align__(16) float ref[2][2 * NR], fac[2][2 * NR];   // references m, m', and what moves to them
-    __shared__ float sum_l[2][4][NR];
+    __shared__ float red[NG][4][2 * NR];                   // maxima of a group's warps: of y, then of y + e
+    __shared__ __align__(16) float ref[NG][2 * NR], fac[NG][2 * NR];   // references m, m', and what moves to them
+    __shared__ float sum_l[NG][4][NR];
     __shared__ uint32_t poison[NR][D / 32];   // channels that a NaN value reaches
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -415,23 +420,25 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     const uint32_t sQ = sbase + C::Q_OFF, sP = sbase + C::P_OFF, sRing = sbase + C::RING_OFF;
     const int G = p.Hq / p.Hkv, items_per_b = p.Hkv * row_blocks;
 
-    if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TC_TMEM);
+    if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), C::TMEM);
     if (tid == 32) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(smem_u32(&bars.full[s]), 1);
             mbar_init(smem_u32(&bars.empty[s]), 1);
         }
-        for (int g = 0; g < 2; ++g) {
+        for (int g = 0; g < NG; ++g) {
             mbar_init(smem_u32(&bars.s_full[g]), 1);
+            mbar_init(smem_u32(&bars.s_free[g]), 4);
             mbar_init(smem_u32(&bars.p_full[g]), 4);
             mbar_init(smem_u32(&bars.pv_done[g]), 1);
         }
-        mbar_init(smem_u32(&bars.q_full), 8);
-        mbar_init(smem_u32(&bars.drain), 1);
+        mbar_init(smem_u32(&bars.q_full), 4 * NG);
+        mbar_init(smem_u32(&bars.drain[0]), 1);
+        mbar_init(smem_u32(&bars.drain[1]), 1);
         abort_flag = 0;
         mbar_init_fence();
     }
-    for (int i = tid; i < (int)C::Q_BYTES / 16; i += TC_THREADS) st_shared_v4(sQ + 16 * i, 0u, 0u, 0u, 0u);   // unused columns
+    for (int i = tid; i < (int)C::Q_BYTES / 16; i += C::THREADS) st_shared_v4(sQ + 16 * i, 0u, 0u, 0u, 0u);   // unused columns
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -440,7 +447,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     Walk w;
     bool live = walk_begin(kp, items_per_b, flat, w);
 
-    if (warp == 8) {
+    if (warp == C::W_LOAD) {
         // ================================================================ loads: a lane per page of the tile
         const int per_tile = TT / c.P;
         const int rows_total = c.n_pages * 2 * c.Hkv * c.P;
@@ -448,17 +455,22 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         bool ok = true;
         int gt = 0;
         while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
-            // first row of the K page of this lane at the piece's tile i; past the end (zeros) where no row sees the page
-            auto row_of = [&](int i) {
-                const int tok = i < w.tiles && lane < per_tile ? w.ks.tile(w.tile0 + i) * TT + lane * c.P : w.n;
-                const bool wanted = tok < w.n && (!p.window || tok + c.P - 1 > w.n - p.Sq - p.window || tok < p.sinks);
-                const int page = wanted ? kv8_page(c, w.b, tok, p.status) : -1;
-                return page < 0 ? -1 : (page * 2 * c.Hkv + w.kvh) * c.P;
+            // whether some row sees this lane's page of the piece's tile i, and the table's entry for it
+            auto token_of = [&](int i) { return w.ks.tile(w.tile0 + i) * TT + lane * c.P; };
+            auto wanted = [&](int i) {
+                const int tok = token_of(i);
+                return i < w.tiles && lane < per_tile && tok < w.n &&
+                       (!p.window || tok + c.P - 1 > w.n - p.Sq - p.window || tok < p.sinks);
             };
-            int next = row_of(0);
+            auto entry_of = [&](int i) { return wanted(i) ? kv8_entry(c, w.b, token_of(i)) : 0; };
+            int next = entry_of(0), next2 = entry_of(1);
             for (int i = 0; i < w.tiles; ++i, ++gt) {
-                const int row = next, st = gt % C::STAGES;
-                next = row_of(i + 1);
+                const int st = gt % C::STAGES, entry = next;
+                next = next2;
+                next2 = entry_of(i + 2);
+                const int page = wanted(i) ? kv8_checked(c, entry, p.status) : -1;
+                // first row of the K page; past the end (zeros) where there is none
+                const int row = page < 0 ? rows_total : (page * 2 * c.Hkv + w.kvh) * c.P;
                 ok = mbar_wait(smem_u32(&bars.empty[st]), ((gt / C::STAGES) & 1) ^ 1, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -466,8 +478,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 if (lane == 0) mbar_expect_tx(bar, 2 * C::TILE);
                 __syncwarp();
                 if (lane < per_tile) {
-                    tma_load_2d(dst, &mpages, bar, 0, row < 0 ? rows_total : row);
-                    tma_load_2d(dst + C::TILE, &mpages, bar, 0, row < 0 ? rows_total : row + c.Hkv * c.P);
+                    tma_load_2d(dst, &mpages, bar, 0, row);
+                    tma_load_2d(dst + C::TILE, &mpages, bar, 0, page < 0 ? rows_total : row + c.Hkv * c.P);
                 }
             }
             walk_step(kp, row_blocks, w);
@@ -479,44 +491,56 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             while (globaltimer_ns() - t0 < 50000ull) {
             }
         }
-    } else if (warp == 9) {
+    } else if (warp >= C::W_MMA) {
         // ================================================================ products
+        // Two issuers, the scores' and the values': a product takes 66 cycles whatever its layout (128 bytes x 32 of its large
+        // operand from shared memory), so what one thread does around them is as much as they take (one issuer for both:
+        // 1300 cycles a tile, of which the products 400 at D = 64).
+        const bool is_s = warp == C::W_MMA;
         bool ok = true;
-        int gt = 0, pieces = 0, cnt[2] = {0, 0};   // tiles and pieces so far, and tiles of each group
+        int st = 0, g = 0;                           // stage and group of the next tile,
+        uint32_t st_par = 0, g_par = 0, q_par = 0;   // and the parities of their barriers
+        bool again = false;                          // the groups have had a tile each
         while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
             if (lane == 0) {
-                ok = mbar_wait(smem_u32(&bars.q_full), pieces & 1, &abort_flag);
-                auto scores = [&](int i) {   // S^T of the piece's tile i
-                    const int st = (gt + i) % C::STAGES, g = (gt + i) & 1;
-                    if (!mbar_wait_spin(smem_u32(&bars.full[st]), ((gt + i) / C::STAGES) & 1, &abort_flag)) return false;
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_any(sRing + st * 2 * C::TILE, 16, C::GROUP8, C::SWZ), bd = sdesc_any(sQ, 16, C::GROUP8, C::SWZ);
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k)
-                        mma_ss_f8(tmem + C::S_COL + 32 * g, ad + 2 * k, bd + 2 * k, C::IDESC_S, k > 0);
-                    mma_commit(smem_u32(&bars.s_full[g]));
-                    return true;
-                };
-                for (int i = 0; i < min(2, w.tiles) && ok; ++i) ok = scores(i);
+                if (is_s) ok = mbar_wait(smem_u32(&bars.q_full), q_par, &abort_flag);
+                q_par ^= 1;
+                const uint64_t qd = sdesc_any(sQ, 16, C::GROUP8, C::SWZ), pd0 = sdesc_any(sP, 128, TT * 16, 0);
+                const uint64_t kd0 = sdesc_any(sRing, 16, C::GROUP8, C::SWZ);
                 for (int i = 0; i < w.tiles && ok; ++i) {
-                    const int st = (gt + i) % C::STAGES, g = (gt + i) & 1;
-                    ok = mbar_wait_spin(smem_u32(&bars.p_full[g]), cnt[g] & 1, &abort_flag);
-                    if (!ok) break;
-                    ++cnt[g];
-                    tc_fence_after();
-                    const uint64_t ad = sdesc_any(sRing + st * 2 * C::TILE + C::TILE, 16, C::GROUP8, C::SWZ);
-                    const uint64_t bd = sdesc_any(sP + g * C::P_BYTES, 128, TT * 16, 0);
+                    const uint64_t kd = kd0 + st * (2 * C::TILE / 16);
+                    if (is_s) {   // S^T, once its group has read the one before
+                        if (again) ok = mbar_wait_spin(smem_u32(&bars.s_free[g]), g_par ^ 1, &abort_flag);
+                        ok = ok && mbar_wait_spin(smem_u32(&bars.full[st]), st_par, &abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll
-                    for (int k = 0; k < TT / 32; ++k)
-                        mma_ss_f8(tmem + C::O_COL + 48 * g, ad + k * (4 * C::GROUP8 / 16), bd + k * (512 / 16), C::IDESC_O, i > 1 || k > 0);
-                    mma_commit(smem_u32(&bars.pv_done[g]));
-                    mma_commit(smem_u32(&bars.empty[st]));
-                    if (i + 2 < w.tiles) ok = scores(i + 2);
+                        for (int k = 0; k < D / 32; ++k) mma_ss_f8(tmem + C::NQ * g, kd + 2 * k, qd + 2 * k, C::IDESC_S, k > 0);
+                        mma_commit(smem_u32(&bars.s_full[g]));
+                    } else {      // O^T, once its group has its weights; the stage is free when it is done
+                        ok = mbar_wait_spin(smem_u32(&bars.p_full[g]), g_par, &abort_flag);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t vd = kd + C::TILE / 16, pd = pd0 + g * (C::P_BYTES / 16);
+#pragma unroll
+                        for (int k = 0; k < TT / 32; ++k)
+                            mma_ss_f8(tmem + C::O_COL + C::NP * g, vd + k * (4 * C::GROUP8 / 16), pd + k * (512 / 16), C::IDESC_O,
+                                      i >= NG || k > 0);
+                        mma_commit(smem_u32(&bars.pv_done[g]));
+                        mma_commit(smem_u32(&bars.empty[st]));
+                    }
+                    if (++st == C::STAGES) {
+                        st = 0;
+                        st_par ^= 1;
+                    }
+                    if (++g == NG) {
+                        g = 0;
+                        g_par ^= 1;
+                        again = true;
+                    }
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
-            gt += w.tiles;
-            ++pieces;
             walk_step(kp, row_blocks, w);
         }
         if (lane == 0) {
@@ -524,22 +548,23 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 abort_flag = 1;
                 atomicExch(p.status, kStatusTimeout);
             }
-            mma_commit(smem_u32(&bars.drain));
-            mbar_wait(smem_u32(&bars.drain), 0, nullptr, 20000000ull);
+            const uint32_t dr = smem_u32(&bars.drain[is_s ? 0 : 1]);
+            mma_commit(dr);
+            mbar_wait(dr, 0, nullptr, 20000000ull);
         }
         __syncwarp();
     } else {
         // ================================================================ scores to weights
         const int g = warp >> 2, w4 = warp & 3, r128 = tid & 127;
         const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
-        const uint32_t s_addr = tmem + C::S_COL + 32 * g + lane_off, o_addr = tmem + C::O_COL + 48 * g + lane_off;
+        const uint32_t s_addr = tmem + C::NQ * g + lane_off, o_addr = tmem + C::O_COL + C::NP * g + lane_off;
         const uint32_t p_row = sP + g * C::P_BYTES + r128 * 16;
         // a wait that ran out is told to the whole group at its next vote, so that all leave together
         bool failed = false;
-        int gt = 0, done = 0;   // tiles so far, of both groups and of this one
+        int gt = 0;   // tiles of the CTA so far; tile t is its group's t / NG-th
         while (live && walk_next<NR>(kp, row_blocks, flat, w)) {
             // ------------------------------------------------------------ Q parts: a warp per row
-            for (int r = warp; r < NR; r += 8) {
+            for (int r = warp; r < NR; r += 4 * NG) {
                 constexpr int E = D / 32;   // channels E * lane ..
                 const int gr = w.r0 + r;
                 float x[E], mx = 0.f;
@@ -593,10 +618,10 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                     row_pos[r] = w.n - p.Sq + gr % p.Sq;
                 }
             }
-            for (int i = tid; i < NR * (D / 32); i += 256) poison[i / (D / 32)][i % (D / 32)] = 0;
+            for (int i = tid; i < NR * (D / 32); i += 128 * NG) poison[i / (D / 32)][i % (D / 32)] = 0;
             if (r128 < 2 * NR) ref[g][r128] = kRowFloor;
             fence_proxy_async_smem();
-            named_barrier(1, 256);
+            named_barrier(1, 128 * NG);
             if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
 
             float m[NR], mp[NR], l[NR];   // -m, -m' and this thread's part of the denominator
@@ -605,12 +630,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 m[r] = mp[r] = -kRowFloor;
                 l[r] = 0.f;
             }
-            // tokens that some row sees, and the page of one; its scales
-            auto page_of = [&](int i) {
-                const int key = i < w.tiles ? w.ks.tile(w.tile0 + i) * TT + r128 : w.n;
-                const bool wanted = key < w.n && (!p.window || key > w.n - p.Sq - p.window || key < p.sinks);
-                return wanted ? kv8_page(c, w.b, key, p.status) : -1;
+            // whether some row sees this thread's token of the piece's tile i, and the table's entry for it; its page's scales
+            auto token_of = [&](int i) { return w.ks.tile(w.tile0 + i) * TT + r128; };
+            auto wanted = [&](int i) {
+                const int key = token_of(i);
+                return i < w.tiles && key < w.n && (!p.window || key > w.n - p.Sq - p.window || key < p.sinks);
             };
+            auto entry_of = [&](int i) { return wanted(i) ? kv8_entry(c, w.b, token_of(i)) : 0; };
             auto scales_of = [&](int page, float &a, float &b) {
                 a = b = 1.f;
                 if (page < 0) return;
@@ -619,12 +645,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 b = s[c.Hkv];
             };
             // this group's tiles of the piece, the pages of the next two and the scales of the next in flight
-            int i = (gt & 1) == g ? 0 : 1, taken = 0;
-            int page = page_of(i), page1 = page_of(i + 2);
+            int i = (g + NG - gt % NG) % NG, done = (gt + i) / NG, taken = 0;   // done: this group's tiles before it
+            int entry1 = entry_of(i + NG), page = entry_of(i);
+            page = wanted(i) ? kv8_checked(c, page, p.status) : -1;
             float ks, vs;
             scales_of(page, ks, vs);
-            for (; i < w.tiles; i += 2) {
-                const int page2 = page_of(i + 4);
+            for (; i < w.tiles; i += NG) {
+                const int entry2 = entry_of(i + 2 * NG), page1 = wanted(i + NG) ? kv8_checked(c, entry1, p.status) : -1;
                 float ks1, vs1;
                 scales_of(page1, ks1, vs1);
                 const int tile = w.ks.tile(w.tile0 + i), key0 = tile * TT, key = key0 + r128;
@@ -635,6 +662,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 uint32_t raw[2 * NR];
                 tmem_ld_n(s_addr, raw);
                 tmem_ld_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&bars.s_free[g]));
                 const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs), ev8 = ev + 8.f;
                 float y[NR];
 #pragma unroll
@@ -778,11 +808,11 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 if (lane == 0) mbar_arrive(smem_u32(&bars.p_full[g]));
                 ++done;
                 ++taken;
-                page = page1; page1 = page2;
+                page = page1; entry1 = entry2;
                 ks = ks1; vs = vs1;
             }
             // ------------------------------------------------------------ the groups' states meet
-            float *so = reinterpret_cast<float *>(sgen + C::O_OFF);   // [2][NR][D]
+            float *so = reinterpret_cast<float *>(sgen + C::O_OFF);   // [NG][NR][D]
             if (taken > 0 && !failed) {
                 const bool ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
                 failed = !__all_sync(0xffffffffu, ok);
@@ -804,21 +834,21 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, m[r] - mp[r]))) : 0.f;
                 if (mine) so[(g * NR + r) * D + ch] = v;
             }
-            named_barrier(1, 256);
+            named_barrier(1, 128 * NG);
             const size_t slot = 2 * (size_t)blockIdx.x + (w.tile0 == 0 ? 1 : 0);
-            for (int x = tid; x < w.rows * (D / 4); x += 256) {
+            for (int x = tid; x < w.rows * (D / 4); x += 128 * NG) {
                 const int r = x / (D / 4), c4 = x % (D / 4) * 4, gr = w.r0 + r;
-                float M = -INFINITY, L = 0.f, mg[2], lg[2];
+                float M = -INFINITY, L = 0.f, mg[NG], lg[NG];
                 float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < NG; ++e) {
                     lg[e] = (sum_l[e][0][r] + sum_l[e][1][r]) + (sum_l[e][2][r] + sum_l[e][3][r]);
                     mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref[e][r] : -INFINITY;
                     M = fmaxf(M, mg[e]);
                 }
                 const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
+                for (int e = 0; e < NG; ++e) {
                     const float wt = ex2_approx(mg[e] - base);
                     const float4 v = *reinterpret_cast<const float4 *>(so + (e * NR + r) * D + c4);
                     A.x = fmaf(wt, v.x, A.x); A.y = fmaf(wt, v.y, A.y);
@@ -840,7 +870,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             }
             gt += w.tiles;
             walk_step(kp, row_blocks, w);
-            if (named_barrier_or(1, 256, failed)) {   // (and the buffers are free again)
+            if (named_barrier_or(1, 128 * NG, failed)) {   // (and the buffers are free again)
                 failed = true;
                 break;
             }
@@ -855,7 +885,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, TC_TMEM);
+        tmem_dealloc(tmem, C::TMEM);
     }
 }
 
@@ -965,7 +995,7 @@ static cudaError_t launch_tc_t(Kv8AttnProblem kp, const TcPlan &t, char *partial
     kp.part = reinterpret_cast<float *>(partials);
     kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * NR * D * sizeof(float)));
     const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 1) == 0;
-    attn_kv8_tc_kernel<D, NR><<<t.grid, TC_THREADS, C::SMEM, s>>>(m, kp, q_vec, t.row_blocks, t.flat);
+    attn_kv8_tc_kernel<D, NR><<<t.grid, C::THREADS, C::SMEM, s>>>(m, kp, q_vec, t.row_blocks, t.flat);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.flat) return e;

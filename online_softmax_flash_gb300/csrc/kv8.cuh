@@ -54,12 +54,18 @@ __device__ __forceinline__ int kv8_length(const int *lens, int b, int most, int 
     if (n < 0 || n > most) atomicExch(status, (int)OSF_ERR_INVALID);
     return min(max(n, 0), most);
 }
-// Page of token `tok` (within the table) of sequence b; -1, recorded, where the table holds no page of the cache.
-__device__ __forceinline__ int kv8_page(const Kv8Cache &c, int b, int tok, int *status) {
-    const int page = c.table[(long long)b * c.per_seq + (tok >> c.log2_p)];
-    if (page >= 0 && page < c.n_pages) return page;
+// Page of token `tok` (within the table) of sequence b; -1, recorded, where the table holds no page of the cache.  In two
+// steps, so that an entry can be on its way while others are worked with.
+__device__ __forceinline__ int kv8_entry(const Kv8Cache &c, int b, int tok) {
+    return c.table[(long long)b * c.per_seq + (tok >> c.log2_p)];
+}
+__device__ __forceinline__ int kv8_checked(const Kv8Cache &c, int entry, int *status) {
+    if (entry >= 0 && entry < c.n_pages) return entry;
     atomicExch(status, (int)OSF_ERR_INVALID);
     return -1;
+}
+__device__ __forceinline__ int kv8_page(const Kv8Cache &c, int b, int tok, int *status) {
+    return kv8_checked(c, kv8_entry(c, b, tok), status);
 }
 // Exponent of a scale (one that is no power of two counts as the next below), and the power of two of an exponent.
 __device__ __forceinline__ int kv8_exponent(float scale) {
