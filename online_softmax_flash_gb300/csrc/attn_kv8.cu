@@ -197,9 +197,9 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 // relative to the largest P * scale, whichever page it comes from.  The denominator has its own reference m of the y.
 // Both references are whole numbers and move only when a value passes them, to 3 .. 4 above the largest.
 //
-// A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  One warp loads, two issue the
-// products, and NG groups of four warps take the tiles in turn, each with its own S^T, O^T and references, one token's
-// scores per thread; their states meet at the end of the run.  A group's next scores are computed while it works on these: S^T
+// A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Two warps load, two issue the
+// products, and NG teams take the tiles in turn, each with its own S^T, O^T and references, one token's scores per thread;
+// their states meet at the end of the run.  A team is four warps, or with 16 rows two groups of four that take 8 rows each.  A group's next scores are computed while it works on these: S^T
 // is free as soon as the group has read it.  Runs are cut flat over all sequences (see FlatCut), and a
 // second kernel joins the pieces of a sequence that several CTAs share.
 constexpr int TT = 128;                   // tokens per tile
@@ -209,9 +209,10 @@ constexpr float kHeadroom = 3.f;              // a new reference is this, and up
 
 template <int D, int NR>
 struct Tc8 {
-    // Groups: as many as their registers allow (a thread holds the scores of NR rows).
+    // Teams: as many as their registers allow (a thread holds the scores of RT rows).
     static constexpr int NG = NR == 4 ? 4 : NR == 8 ? 3 : 2;
-    static constexpr int W_LOAD = 4 * NG, W_MMA = W_LOAD + 1, THREADS = (W_MMA + 2) * 32;
+    static constexpr int RT = NR == 16 ? 8 : NR, HS = NR / RT, GROUPS = NG * HS;   // rows of a thread, groups of a team
+    static constexpr int W_LOAD = 4 * GROUPS, W_MMA = W_LOAD + 2, THREADS = (W_MMA + 2) * 32;
     static constexpr uint32_t TILE = TT * D;                        // K or V of a tile
     static constexpr int NQ = 2 * NR < 16 ? 16 : 2 * NR;            // columns of Q parts: part p of row r at p * NR + r
     static constexpr int PLANES = (3 * NR + 15) / 16, NP = 16 * PLANES;   // columns of P parts, in planes of 16
@@ -224,7 +225,7 @@ struct Tc8 {
     static constexpr uint32_t SMEM = RING_OFF + STAGES * 2 * TILE + 1024;
     static constexpr uint32_t SWZ = D == 128 ? 2 : 4, GROUP8 = 8 * D;   // swizzle type, bytes of eight rows
     static constexpr uint32_t IDESC_S = idesc_e4m3_f32(TT, NQ, 0, 0), IDESC_O = idesc_e4m3_f32(D, NP, 1, 1);
-    static constexpr uint32_t O_COL = NG * NQ, COLS = O_COL + NG * NP;   // S^T of group g at column NQ g, O^T at O_COL + NP g
+    static constexpr uint32_t O_COL = NG * NQ, COLS = O_COL + NG * NP;   // S^T of team g at column NQ g, O^T at O_COL + NP g
     static constexpr uint32_t TMEM = COLS <= 128 ? 128 : 256;
     static_assert(COLS <= 256, "TMEM");
 };
@@ -400,7 +401,7 @@ template <int D, int NR>
 __global__ void __launch_bounds__((Tc8<D, NR>::THREADS), 1)
 attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProblem kp, int q_vec, int row_blocks, int flat) {
     using C = Tc8<D, NR>;
-    constexpr int NG = C::NG;
+    constexpr int NG = C::NG, RT = C::RT, HS = C::HS, SOFT = 128 * C::GROUPS;
     const AttnProblem &p = kp.a;
     const Kv8Cache &c = kp.c;
     extern __shared__ uint8_t smem_raw[];
@@ -409,9 +410,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     __shared__ volatile int abort_flag;
     __shared__ __align__(16) float q_back[NR];             // raw score times K scale to base-2 score
     __shared__ int row_pos[NR];                            // positions of the rows
-    __shared__ float red[NG][4][2 * NR];                   // maxima of a group's warps: of y, then of y + e
-    __shared__ __align__(16) float ref[NG][2 * NR], fac[NG][2 * NR];   // references m, m', and what moves to them
-    __shared__ float sum_l[NG][4][NR];
+    __shared__ float red[C::GROUPS][4][2 * RT];                  // maxima of a group's warps: of y, then of y + e
+    __shared__ __align__(16) float ref[C::GROUPS][2 * RT], fac[C::GROUPS][2 * RT];   // references m, m', and what moves to them
+    __shared__ float sum_l[C::GROUPS][4][RT];
     __shared__ uint32_t poison[NR][D / 32];   // channels that a NaN value reaches
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -423,16 +424,16 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), C::TMEM);
     if (tid == 32) {
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(smem_u32(&bars.full[s]), 1);
+            mbar_init(smem_u32(&bars.full[s]), 2);   // the K and the V loads
             mbar_init(smem_u32(&bars.empty[s]), 1);
         }
         for (int g = 0; g < NG; ++g) {
             mbar_init(smem_u32(&bars.s_full[g]), 1);
-            mbar_init(smem_u32(&bars.s_free[g]), 4);
-            mbar_init(smem_u32(&bars.p_full[g]), 4);
+            mbar_init(smem_u32(&bars.s_free[g]), 4 * HS);
+            mbar_init(smem_u32(&bars.p_full[g]), 4 * HS);
             mbar_init(smem_u32(&bars.pv_done[g]), 1);
         }
-        mbar_init(smem_u32(&bars.q_full), 4 * NG);
+        mbar_init(smem_u32(&bars.q_full), 4 * C::GROUPS);
         mbar_init(smem_u32(&bars.drain[0]), 1);
         mbar_init(smem_u32(&bars.drain[1]), 1);
         abort_flag = 0;
@@ -447,39 +448,46 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     Walk w;
     bool live = walk_begin(kp, items_per_b, flat, w);
 
-    if (warp == C::W_LOAD) {
-        // ================================================================ loads: a lane per page of the tile
-        const int per_tile = TT / c.P;
+    if (warp >= C::W_LOAD && warp < C::W_MMA) {
+        // ================================================================ loads: K and V, a lane per page of the tile
+        // (one warp for both: 820 cycles a tile, more than its bytes take at D = 64)
+        const int half = warp - C::W_LOAD, per_tile = TT >> c.log2_p;
         const int rows_total = c.n_pages * 2 * c.Hkv * c.P;
         tma_prefetch_desc(&mpages);
         bool ok = true;
-        int gt = 0;
+        int st = 0;
+        uint32_t par = 1;
         while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
             // whether some row sees this lane's page of the piece's tile i, and the table's entry for it
-            auto token_of = [&](int i) { return w.ks.tile(w.tile0 + i) * TT + lane * c.P; };
-            auto wanted = [&](int i) {
-                const int tok = token_of(i);
-                return i < w.tiles && lane < per_tile && tok < w.n &&
-                       (!p.window || tok + c.P - 1 > w.n - p.Sq - p.window || tok < p.sinks);
+            const int near = p.window ? w.n - p.Sq - p.window : -c.P;   // the window of the first row begins behind it
+            const int *entries = c.table + (long long)w.b * c.per_seq;
+            auto token_of = [&](int i) { return w.ks.tile(w.tile0 + i) * TT + (lane << c.log2_p); };
+            auto wanted = [&](int i, int tok) {
+                return i < w.tiles && lane < per_tile && tok < w.n && (tok + c.P - 1 > near || tok < p.sinks);
             };
-            auto entry_of = [&](int i) { return wanted(i) ? kv8_entry(c, w.b, token_of(i)) : 0; };
-            int next = entry_of(0), next2 = entry_of(1);
-            for (int i = 0; i < w.tiles; ++i, ++gt) {
-                const int st = gt % C::STAGES, entry = next;
-                next = next2;
-                next2 = entry_of(i + 2);
-                const int page = wanted(i) ? kv8_checked(c, entry, p.status) : -1;
-                // first row of the K page; past the end (zeros) where there is none
-                const int row = page < 0 ? rows_total : (page * 2 * c.Hkv + w.kvh) * c.P;
-                ok = mbar_wait(smem_u32(&bars.empty[st]), ((gt / C::STAGES) & 1) ^ 1, &abort_flag);
+            auto entry_of = [&](int i, int tok) { return wanted(i, tok) ? entries[tok >> c.log2_p] : 0; };
+            int tok = token_of(0), tok1 = token_of(1), next = entry_of(0, tok), next1 = entry_of(1, tok1);
+            for (int i = 0; i < w.tiles; ++i) {
+                const int entry = next, tok2 = token_of(i + 2);
+                const bool want = wanted(i, tok);
+                next = next1;
+                next1 = entry_of(i + 2, tok2);
+                tok = tok1;
+                tok1 = tok2;
+                const int page = want ? kv8_checked(c, entry, p.status) : -1;
+                // first row of the page; past the end (zeros) where there is none
+                const int row = page < 0 ? rows_total : ((page * 2 + half) * c.Hkv + w.kvh) << c.log2_p;
+                ok = mbar_wait(smem_u32(&bars.empty[st]), par, &abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                const uint32_t bar = smem_u32(&bars.full[st]), dst = sRing + st * 2 * C::TILE + lane * c.P * D;
-                if (lane == 0) mbar_expect_tx(bar, 2 * C::TILE);
+                const uint32_t bar = smem_u32(&bars.full[st]);
+                if (lane == 0) mbar_expect_tx(bar, C::TILE);
                 __syncwarp();
-                if (lane < per_tile) {
-                    tma_load_2d(dst, &mpages, bar, 0, row);
-                    tma_load_2d(dst + C::TILE, &mpages, bar, 0, page < 0 ? rows_total : row + c.Hkv * c.P);
+                if (lane < per_tile)
+                    tma_load_2d(sRing + (2 * st + half) * C::TILE + (lane << c.log2_p) * D, &mpages, bar, 0, row);
+                if (++st == C::STAGES) {
+                    st = 0;
+                    par ^= 1;
                 }
             }
             walk_step(kp, row_blocks, w);
@@ -555,16 +563,17 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         __syncwarp();
     } else {
         // ================================================================ scores to weights
-        const int g = warp >> 2, w4 = warp & 3, r128 = tid & 127;
+        const int gi = warp >> 2, g = gi / HS, rh = gi % HS * RT;   // group, team, and the group's first row
+        const int w4 = warp & 3, r128 = tid & 127;
         const uint32_t lane_off = (uint32_t)(w4 * 32) << 16;
-        const uint32_t s_addr = tmem + C::NQ * g + lane_off, o_addr = tmem + C::O_COL + C::NP * g + lane_off;
-        const uint32_t p_row = sP + g * C::P_BYTES + r128 * 16;
+        const uint32_t s_addr = tmem + C::NQ * g + rh + lane_off, o_addr = tmem + C::O_COL + C::NP * g + rh + lane_off;
+        const uint32_t p_row = sP + g * C::P_BYTES + r128 * 16 + rh;
         // a wait that ran out is told to the whole group at its next vote, so that all leave together
         bool failed = false;
-        int gt = 0;   // tiles of the CTA so far; tile t is its group's t / NG-th
+        int gt = 0;   // tiles of the CTA so far; tile t is its team's t / NG-th
         while (live && walk_next<NR>(kp, row_blocks, flat, w)) {
             // ------------------------------------------------------------ Q parts: a warp per row
-            for (int r = warp; r < NR; r += 4 * NG) {
+            for (int r = warp; r < NR; r += 4 * C::GROUPS) {
                 constexpr int E = D / 32;   // channels E * lane ..
                 const int gr = w.r0 + r;
                 float x[E], mx = 0.f;
@@ -618,25 +627,27 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                     row_pos[r] = w.n - p.Sq + gr % p.Sq;
                 }
             }
-            for (int i = tid; i < NR * (D / 32); i += 128 * NG) poison[i / (D / 32)][i % (D / 32)] = 0;
-            if (r128 < 2 * NR) ref[g][r128] = kRowFloor;
+            for (int i = tid; i < NR * (D / 32); i += SOFT) poison[i / (D / 32)][i % (D / 32)] = 0;
+            if (r128 < 2 * RT) ref[gi][r128] = kRowFloor;
             fence_proxy_async_smem();
-            named_barrier(1, 128 * NG);
+            named_barrier(1, SOFT);
             if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
 
-            float m[NR], mp[NR], l[NR];   // -m, -m' and this thread's part of the denominator
+            float m[RT], mp[RT], l[RT];   // -m, -m' and this thread's part of the denominator
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
+            for (int r = 0; r < RT; ++r) {
                 m[r] = mp[r] = -kRowFloor;
                 l[r] = 0.f;
             }
             // whether some row sees this thread's token of the piece's tile i, and the table's entry for it; its page's scales
+            const int near = p.window ? w.n - p.Sq - p.window : -1;   // the window of the first row begins behind it
+            const int *entries = c.table + (long long)w.b * c.per_seq;
             auto token_of = [&](int i) { return w.ks.tile(w.tile0 + i) * TT + r128; };
             auto wanted = [&](int i) {
                 const int key = token_of(i);
-                return i < w.tiles && key < w.n && (!p.window || key > w.n - p.Sq - p.window || key < p.sinks);
+                return i < w.tiles && key < w.n && (key > near || key < p.sinks);
             };
-            auto entry_of = [&](int i) { return wanted(i) ? kv8_entry(c, w.b, token_of(i)) : 0; };
+            auto entry_of = [&](int i) { return wanted(i) ? entries[token_of(i) >> c.log2_p] : 0; };
             auto scales_of = [&](int page, float &a, float &b) {
                 a = b = 1.f;
                 if (page < 0) return;
@@ -644,8 +655,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 a = s[0];
                 b = s[c.Hkv];
             };
-            // this group's tiles of the piece, the pages of the next two and the scales of the next in flight
-            int i = (g + NG - gt % NG) % NG, done = (gt + i) / NG, taken = 0;   // done: this group's tiles before it
+            // this team's tiles of the piece, the pages of the next two and the scales of the next in flight
+            int i = (g + NG - gt % NG) % NG, done = (gt + i) / NG, taken = 0;   // done: this team's tiles before it
             int entry1 = entry_of(i + NG), page = entry_of(i);
             page = wanted(i) ? kv8_checked(c, page, p.status) : -1;
             float ks, vs;
@@ -659,35 +670,40 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 bool ok = !failed && mbar_wait(smem_u32(&bars.s_full[g]), done & 1, &abort_flag);
                 failed = !__all_sync(0xffffffffu, ok);
                 tc_fence_after();
-                uint32_t raw[2 * NR];
-                tmem_ld_n(s_addr, raw);
+                uint32_t raw[2 * RT];   // the first parts' scores, then the second's
+                if constexpr (HS == 1) {
+                    tmem_ld_n(s_addr, raw);
+                } else {
+                    tmem_ld8(s_addr, raw);
+                    tmem_ld8(s_addr + NR, raw + RT);
+                }
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.s_free[g]));
                 const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs), ev8 = ev + 8.f;
-                float y[NR];
+                float y[RT];
 #pragma unroll
-                for (int r = 0; r < NR; r += 4) {
-                    const float4 back = *reinterpret_cast<const float4 *>(q_back + r);
+                for (int r = 0; r < RT; r += 4) {
+                    const float4 back = *reinterpret_cast<const float4 *>(q_back + rh + r);
                     const float qb[4] = {back.x, back.y, back.z, back.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        y[r + e] = fmaf(__uint_as_float(raw[NR + r + e]), 0.0625f, __uint_as_float(raw[r + e])) * (qb[e] * kscale);
+                        y[r + e] = fmaf(__uint_as_float(raw[RT + r + e]), 0.0625f, __uint_as_float(raw[r + e])) * (qb[e] * kscale);
                 }
                 // a tile that some row does not see the whole of
                 const bool edge = key0 + TT - 1 > w.n - p.Sq || (p.window && key0 <= w.n - 1 - p.window && key0 + TT > p.sinks);
                 if (edge) {
-                    bool all = true;
+                    auto sees = [&](int pos) {
+                        return page >= 0 && key <= pos && (!p.window || key > pos - p.window || key < p.sinks);
+                    };
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        const int pos = row_pos[r];
-                        const bool sees = page >= 0 && key <= pos && (!p.window || key > pos - p.window || key < p.sinks);
-                        all = all && (sees || r >= w.rows);
-                        y[r] = sees ? y[r] : -INFINITY;
-                    }
+                    for (int r = 0; r < RT; ++r) y[r] = sees(row_pos[rh + r]) ? y[r] : -INFINITY;
                     // Values of tokens that no row sees, or not all, must not reach the others as 0 * NaN: the former are
                     // cleared, the latter's NaN codes too, and remembered for the rows that do see them.
+                    bool all = true;
+                    if (rh == 0)
+                        for (int r = 0; r < w.rows; ++r) all = all && sees(row_pos[r]);
                     if (!all && !failed) {
                         const uint32_t vrow = sRing + st * 2 * C::TILE + C::TILE + r128 * D;
                         if (mbar_wait(smem_u32(&bars.full[st]), ((gt + i) / C::STAGES) & 1, &abort_flag)) {
@@ -711,70 +727,81 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                                 if (!nan_any) continue;
                                 st_shared_v4(at, x[0], x[1], x[2], x[3]);
                                 const int ch = 16 * (D == 128 ? q ^ (r128 & 7) : q ^ (r128 >> 1 & 3));
-#pragma unroll
-                                for (int r = 0; r < NR; ++r)
-                                    if (y[r] != -INFINITY) atomicOr(&poison[r][ch / 32], bits << (ch & 31));
+                                for (int r = 0; r < w.rows; ++r)
+                                    if (sees(row_pos[r])) atomicOr(&poison[r][ch / 32], bits << (ch & 31));
                             }
                         }
                     }
                 } else if (page < 0) {   // the table holds no page for it: its codes are zeros
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) y[r] = -INFINITY;
+                    for (int r = 0; r < RT; ++r) y[r] = -INFINITY;
                 }
                 float top = -INFINITY;
 #pragma unroll
-                for (int r = 0; r < NR; ++r) top = fmax3(top, y[r] + m[r], y[r] + (mp[r] + ev));
-                if (named_barrier_or(2 + g, 128, failed || top > 0.f)) {
+                for (int r = 0; r < RT; ++r) top = fmax3(top, y[r] + m[r], y[r] + (mp[r] + ev));
+                if (named_barrier_or(2 + gi, 128, failed || top > 0.f)) {
                     // some reference has to move
-                    float v[2 * NR];
+                    float v[2 * RT];
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
+                    for (int r = 0; r < RT; ++r) {
                         v[r] = y[r];
-                        v[NR + r] = y[r] + ev;
+                        v[RT + r] = y[r] + ev;
                     }
                     const int at = warp_max_each(v);
-                    if ((lane & (32 / (2 * NR) - 1)) == 0) red[g][w4][at] = v[0];
-                    if (named_barrier_or(2 + g, 128, failed)) {
+                    if ((lane & (32 / (2 * RT) - 1)) == 0) red[gi][w4][at] = v[0];
+                    if (named_barrier_or(2 + gi, 128, failed)) {
                         failed = true;
                         break;
                     }
-                    if (r128 < 2 * NR) {
-                        const float a = fmaxf(fmaxf(red[g][0][r128], red[g][1][r128]), fmaxf(red[g][2][r128], red[g][3][r128]));
-                        const float old = ref[g][r128], now = a > old ? ceilf(a) + kHeadroom : old;
-                        fac[g][r128] = ex2_approx(old - now);
-                        ref[g][r128] = now;
+                    if (r128 < 2 * RT) {
+                        const float a = fmaxf(fmaxf(red[gi][0][r128], red[gi][1][r128]), fmaxf(red[gi][2][r128], red[gi][3][r128]));
+                        const float old = ref[gi][r128], now = a > old ? ceilf(a) + kHeadroom : old;
+                        fac[gi][r128] = ex2_approx(old - now);
+                        ref[gi][r128] = now;
                     }
-                    named_barrier(2 + g, 128);
-                    float f[NR];
+                    named_barrier(2 + gi, 128);
+                    float f[RT];
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) {
-                        l[r] *= fac[g][r];
-                        f[r] = fac[g][NR + r];
-                        m[r] = -ref[g][r];
-                        mp[r] = -ref[g][NR + r];
+                    for (int r = 0; r < RT; ++r) {
+                        l[r] *= fac[gi][r];
+                        f[r] = fac[gi][RT + r];
+                        m[r] = -ref[gi][r];
+                        mp[r] = -ref[gi][RT + r];
                     }
                     if (taken > 0) {   // (every product of the group so far is waited for first)
                         ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
                         failed = !__all_sync(0xffffffffu, ok);
                         tc_fence_after();
+                        if constexpr (HS == 1) {
 #pragma unroll
-                        for (int pl = 0; pl < C::PLANES; ++pl) {
-                            uint32_t o[16];
-                            tmem_ld16(o_addr + 16 * pl, o);
-                            tmem_ld_wait();
+                            for (int pl = 0; pl < C::PLANES; ++pl) {
+                                uint32_t o[16];
+                                tmem_ld16(o_addr + 16 * pl, o);
+                                tmem_ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                if (16 * pl + e < 3 * NR) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(16 * pl + e) % NR]);
-                            tmem_st16(o_addr + 16 * pl, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], o[8], o[9], o[10], o[11],
-                                      o[12], o[13], o[14], o[15]);
+                                for (int e = 0; e < 16; ++e)
+                                    if (16 * pl + e < 3 * NR) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(16 * pl + e) % NR]);
+                                tmem_st16(o_addr + 16 * pl, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], o[8], o[9], o[10],
+                                          o[11], o[12], o[13], o[14], o[15]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 3; ++k) {
+                                uint32_t o[8];
+                                tmem_ld8(o_addr + NR * k, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e % RT]);
+                                tmem_st8(o_addr + NR * k, o);
+                            }
                         }
                         tmem_st_wait();
                     }
                 }
                 // weights, and their parts in words of four rows
-                uint32_t part[3][NR / 4];
+                uint32_t part[3][RT / 4];
 #pragma unroll
-                for (int r = 0; r < NR; r += 2) {
+                for (int r = 0; r < RT; r += 2) {
                     l[r] += ex2_approx(y[r] + m[r]);
                     l[r + 1] += ex2_approx(y[r + 1] + m[r + 1]);
                     uint32_t h = f32_to_f16x2(ex2_approx(y[r] + (mp[r] + ev8)), ex2_approx(y[r + 1] + (mp[r + 1] + ev8)));
@@ -791,16 +818,22 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                     ok = !failed && mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
                     failed = !__all_sync(0xffffffffu, ok);
                 }
+                if constexpr (HS == 1) {
 #pragma unroll
-                for (int pl = 0; pl < C::PLANES; ++pl) {
-                    uint32_t x[4];
+                    for (int pl = 0; pl < C::PLANES; ++pl) {
+                        uint32_t x[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        constexpr int W = NR / 4;   // words of a part
-                        const int word = 4 * pl + e;
-                        x[e] = word < 3 * W ? part[word / W < 3 ? word / W : 0][word % W] : 0u;
+                        for (int e = 0; e < 4; ++e) {
+                            constexpr int W = RT / 4;   // words of a part
+                            const int word = 4 * pl + e;
+                            x[e] = word < 3 * W ? part[word / W < 3 ? word / W : 0][word % W] : 0u;
+                        }
+                        st_shared_v4(p_row + pl * TT * 16, x[0], x[1], x[2], x[3]);
                     }
-                    st_shared_v4(p_row + pl * TT * 16, x[0], x[1], x[2], x[3]);
+                } else {   // a plane holds a part of all 16 rows
+#pragma unroll
+                    for (int k = 0; k < 3; ++k)
+                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_row + k * TT * 16), "r"(part[k][0]), "r"(part[k][1]) : "memory");
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
@@ -818,32 +851,38 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 failed = !__all_sync(0xffffffffu, ok);
             }
             tc_fence_after();
-            uint32_t o[C::NP];
+            uint32_t o[3 * RT < 16 ? 16 : 3 * RT];   // part k of row r at k * RT + r
+            if constexpr (HS == 1) {
+                tmem_ld16(o_addr, o);
+                if constexpr (NR == 8) tmem_ld8(o_addr + 16, o + 16);
+            } else {
 #pragma unroll
-            for (int pl = 0; pl < C::PLANES; ++pl) tmem_ld16(o_addr + 16 * pl, o + 16 * pl);
+                for (int k = 0; k < 3; ++k) tmem_ld8(o_addr + NR * k, o + RT * k);
+            }
             tmem_ld_wait();
             tc_fence_before();
             const int ch = D == 128 ? r128 : w4 * 16 + lane;   // M = 64: 16 lanes of each warp's 32
             const bool mine = D == 128 || lane < 16;
 #pragma unroll
-            for (int r = 0; r < NR; ++r) {
+            for (int r = 0; r < RT; ++r) {
                 const float sum = warp_sum(l[r]);
-                if (lane == 0) sum_l[g][w4][r] = sum;
-                float v = fmaf(__uint_as_float(o[2 * NR + r]), 0x1p-8f, fmaf(__uint_as_float(o[NR + r]), 0x1p-4f, __uint_as_float(o[r])));
+                if (lane == 0) sum_l[gi][w4][r] = sum;
+                float v = fmaf(__uint_as_float(o[2 * RT + r]), 0x1p-8f, fmaf(__uint_as_float(o[RT + r]), 0x1p-4f, __uint_as_float(o[r])));
                 // in units of 2^(m' - 8) so far: relative to m
                 v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, m[r] - mp[r]))) : 0.f;
-                if (mine) so[(g * NR + r) * D + ch] = v;
+                if (mine) so[(g * NR + rh + r) * D + ch] = v;
             }
-            named_barrier(1, 128 * NG);
+            named_barrier(1, SOFT);
             const size_t slot = 2 * (size_t)blockIdx.x + (w.tile0 == 0 ? 1 : 0);
-            for (int x = tid; x < w.rows * (D / 4); x += 128 * NG) {
+            for (int x = tid; x < w.rows * (D / 4); x += SOFT) {
                 const int r = x / (D / 4), c4 = x % (D / 4) * 4, gr = w.r0 + r;
                 float M = -INFINITY, L = 0.f, mg[NG], lg[NG];
                 float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                 for (int e = 0; e < NG; ++e) {
-                    lg[e] = (sum_l[e][0][r] + sum_l[e][1][r]) + (sum_l[e][2][r] + sum_l[e][3][r]);
-                    mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref[e][r] : -INFINITY;
+                    const int ge = e * HS + r / RT, re = r % RT;
+                    lg[e] = (sum_l[ge][0][re] + sum_l[ge][1][re]) + (sum_l[ge][2][re] + sum_l[ge][3][re]);
+                    mg[e] = lg[e] > 0.f || lg[e] != lg[e] ? ref[ge][re] : -INFINITY;
                     M = fmaxf(M, mg[e]);
                 }
                 const float base = M == -INFINITY ? 0.f : M;
@@ -870,7 +909,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             }
             gt += w.tiles;
             walk_step(kp, row_blocks, w);
-            if (named_barrier_or(1, 128 * NG, failed)) {   // (and the buffers are free again)
+            if (named_barrier_or(1, SOFT, failed)) {   // (and the buffers are free again)
                 failed = true;
                 break;
             }
