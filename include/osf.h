@@ -372,8 +372,8 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
  * Rotation: cos_table, sin_table: float32 [max_positions, rotary_dim / 2] (rotary_dim 0: none; a multiple of 8, at most D):
  *     (a, b) -> (a cos - b sin, b cos + a sin), rounded once to float32, for channels i and i + rotary_dim / 2, or with
  *     interleaved 2 i and 2 i + 1, at position lens[b] + t.  Channels from rotary_dim on are stored as they are.
- * Q, Q_out: NULL, or queries [B, Hq, n, D] of the same tokens, rotated the same way and rounded to `dtype`; Q_out may be Q
- *     (with the same strides).  Rows at and behind counts[b] are left as they were.
+ * Q, Q_out: NULL, or queries [B, Hq, n, D] of the same tokens, rotated by the same angles in float32 (one product rounded, the
+ *     other fused into the difference) and rounded to `dtype`; Q_out may be Q (with the same strides).  Rows at and behind counts[b] are left as they were.
  * strides: NULL (contiguous), or 6 element strides, K: b, h, s  V: b, h, s, and with Q 6 more, Q: b, h, s  Q_out: b, h, s.
  * Tokens that would fall behind table_len * P are not stored, and recorded as OSF_ERR_INVALID in the device status word, as
  * are counts out of range (cut to it), a negative length (nothing of that sequence is stored) and positions that the tables

@@ -992,8 +992,14 @@ static bool use_tc(const AttnProblem &p) {
     return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128) && p.Sk > 0 && tensor_map_encoder() != nullptr;
 }
 
-// Launch shape of the tensor-core kernel: items of few tiles are not cut (a CTA each, one launch, no join), else one wave of
-// CTAs shares all tiles.
+// Launch shape of the tensor-core kernel.  Whole items, a CTA each, need one launch and no join; cut, all tiles are shared by
+// one wave of CTAs.  A cut costs what kCutCost tiles take (a second piece in most CTAs, the join), so it is made where the
+// waves of whole items would take that much longer.  (Hkv=8 D=128, whole against cut, us: 1 row x 4 heads, 8 items of 16
+// tiles 17.0 against 17.0, of 32 23.2 against 17.0, of 64 37.5 against 21.1; 64 of 32 25.2 against 27.3, of 64 37.5 against
+// 35.5; 128 of 64 47.7 against 53.9; 256 of 64 88.7 against 90.8; 512 of 16 62.1 against 58.0, of 32 101 against 94.  16 rows:
+// 8 of 16 23.3 against 23.2, of 32 33.4 against 23.2; 64 of 32 33.5 against 37.5, of 64 55.9 against 47.7; 128 of 64 58.0
+// against 68.2; 512 of 32 136 against 127.)
+constexpr int kCutCost = 20, kCutCost16 = 28;
 struct TcPlan {
     int nr, row_blocks, flat, grid;
 };
@@ -1004,7 +1010,8 @@ static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
     t.row_blocks = (R + t.nr - 1) / t.nr;
     const long long items = (long long)p.B * p.Hkv * t.row_blocks;
     const long long per = key_stream_max(p.Sq, p.Sk, p.window ? p.window : p.Sk, p.sinks, TT);
-    t.flat = per > 4;
+    const long long waves = (items + sm_count - 1) / sm_count;
+    t.flat = waves * per - items * per / sm_count > (t.nr == 16 ? kCutCost16 : kCutCost);
     const long long worth = items * per / kMinTiles;
     t.grid = (int)(!t.flat ? items : worth < sm_count ? (worth < 1 ? 1 : worth) : sm_count);
     return t;

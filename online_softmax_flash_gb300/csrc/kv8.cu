@@ -20,39 +20,62 @@ constexpr float kMaxF32 = 3.4028235e38f;
 __device__ __forceinline__ float lo_bf16(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ float hi_bf16(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
 
-// Four neighbouring channels of a row.
-__device__ __forceinline__ void load4(const float *p, bool vec, float *x) {
+// W (4 or 8) neighbouring channels of a row.
+template <int W>
+__device__ __forceinline__ void load_run(const float *p, bool vec, float *x) {
     if (vec) {
-        const float4 v = *reinterpret_cast<const float4 *>(p);
-        x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(p + i);
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = p[i];
+        for (int i = 0; i < W; ++i) x[i] = p[i];
     }
 }
-__device__ __forceinline__ void load4(const __nv_bfloat16 *p, bool vec, float *x) {
+template <int W>
+__device__ __forceinline__ void load_run(const __nv_bfloat16 *p, bool vec, float *x) {
     if (vec) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        x[0] = lo_bf16(v.x); x[1] = hi_bf16(v.x); x[2] = lo_bf16(v.y); x[3] = hi_bf16(v.y);
+        uint32_t v[W / 2];
+        if constexpr (W == 8) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            v[0] = q.x; v[1] = q.y;
+        }
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            x[2 * i] = lo_bf16(v[i]);
+            x[2 * i + 1] = hi_bf16(v[i]);
+        }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = __bfloat162float(p[i]);
+        for (int i = 0; i < W; ++i) x[i] = __bfloat162float(p[i]);
     }
 }
-__device__ __forceinline__ void store4(float *p, bool vec, const float *x) {
+template <int W>
+__device__ __forceinline__ void store_run(float *p, bool vec, const float *x) {
     if (vec) {
-        *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
+#pragma unroll
+        for (int i = 0; i < W; i += 4) *reinterpret_cast<float4 *>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = x[i];
+        for (int i = 0; i < W; ++i) p[i] = x[i];
     }
 }
-__device__ __forceinline__ void store4(__nv_bfloat16 *p, bool vec, const float *x) {
+template <int W>
+__device__ __forceinline__ void store_run(__nv_bfloat16 *p, bool vec, const float *x) {
     if (vec) {
-        *reinterpret_cast<uint2 *>(p) = make_uint2(ptx::pack_bf16x2(x[0], x[1]), ptx::pack_bf16x2(x[2], x[3]));
+        uint32_t v[W / 2];
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) v[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+        if constexpr (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(v[0], v[1], v[2], v[3]);
+        else *reinterpret_cast<uint2 *>(p) = make_uint2(v[0], v[1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = __float2bfloat16_rn(x[i]);
+        for (int i = 0; i < W; ++i) p[i] = __float2bfloat16_rn(x[i]);
     }
 }
 
@@ -65,103 +88,158 @@ __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     return fabsf(h) <= kMaxF32 ? __fadd_rn(h, __fadd_rn(he, __fsub_rn(pe, qe))) : h;
 }
 
-// Where the eight channels of unit u of a row lie: two runs of four, at first and second.
+// Where the 2 W channels of unit u of a row lie: two runs of W, at first and second.  The W pairs of a unit that is rotated
+// have the angles in columns angle .. angle + W - 1 of the tables.
 struct Unit {
-    int first, second;
+    int first, second, angle;
     bool rotated;
-    int angle;   // of the four pairs: columns angle .. angle + 3 of the tables
 };
+template <int W>
 __device__ __forceinline__ Unit unit_of(int u, int R, bool interleaved) {
     Unit w;
-    w.rotated = 8 * u < R;
-    w.angle = 4 * u;
+    w.rotated = 2 * W * u < R;
+    w.angle = W * u;
     const bool halves = w.rotated && !interleaved;
-    w.first = halves ? 4 * u : 8 * u;
-    w.second = halves ? R / 2 + 4 * u : 8 * u + 4;
+    w.first = halves ? W * u : 2 * W * u;
+    w.second = halves ? R / 2 + W * u : 2 * W * u + W;
     return w;
 }
-
-// The eight channels of a unit of a row at position pos, rotated where they are to be.
-template <typename T>
-__device__ __forceinline__ void load_unit(const Kv8StoreProblem &p, const T *row, const Unit &w, int pos, bool vec, float (&x)[8]) {
-    load4(row + w.first, vec, x);
-    load4(row + w.second, vec, x + 4);
-    if (!w.rotated) return;
-    float c[4], s[4];
-    const bool tv = ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15u) == 0 && p.R % 8 == 0;
-    load4(p.cos + (long long)pos * (p.R / 2) + w.angle, tv, c);
-    load4(p.sin + (long long)pos * (p.R / 2) + w.angle, tv, s);
+// cos and sin of a unit's angles at position pos.
+template <int W>
+__device__ __forceinline__ void load_angles(const Kv8StoreProblem &p, const Unit &w, int pos, float (&c)[W], float (&s)[W]) {
+    load_run<W>(p.cos + (long long)pos * (p.R / 2) + w.angle, p.table_vec, c);
+    load_run<W>(p.sin + (long long)pos * (p.R / 2) + w.angle, p.table_vec, s);
+}
+// The first and second channels of a unit's pairs, and back.
+template <int W>
+__device__ __forceinline__ void split_pairs(const float (&x)[2 * W], bool interleaved, float (&a)[W], float (&b)[W]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float &a = p.interleaved ? x[2 * i] : x[i], &b = p.interleaved ? x[2 * i + 1] : x[i + 4];
-        const float ra = rotate1(a, c[i], b, s[i]), rb = rotate1(b, c[i], -a, s[i]);
-        a = ra;
-        b = rb;
+    for (int i = 0; i < W; ++i) {
+        a[i] = interleaved ? x[2 * i] : x[i];
+        b[i] = interleaved ? x[2 * i + 1] : x[i + W];
     }
+}
+template <int W>
+__device__ __forceinline__ void join_pairs(float (&x)[2 * W], bool interleaved, const float (&a)[W], const float (&b)[W]) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        x[i] = interleaved ? (i & 1 ? b[i / 2] : a[i / 2]) : a[i];
+        x[i + W] = interleaved ? (i & 1 ? b[(i + W) / 2] : a[(i + W) / 2]) : b[i];
+    }
+}
+
+// A unit of K, rotated exactly.
+template <int W>
+__device__ __forceinline__ void rotate_unit(const Kv8StoreProblem &p, const Unit &w, int pos, float (&x)[2 * W]) {
+    float c[W], s[W], a[W], b[W];
+    load_angles<W>(p, w, pos, c, s);
+    split_pairs<W>(x, p.interleaved, a, b);
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const float ra = rotate1(a[i], c[i], b[i], s[i]), rb = rotate1(b[i], c[i], -a[i], s[i]);
+        a[i] = ra;
+        b[i] = rb;
+    }
+    join_pairs<W>(x, p.interleaved, a, b);
 }
 
 __device__ __forceinline__ uint32_t code4(const float *x, float inv) {
     uint32_t w = f32_to_e4m3x2(x[0] * inv, x[1] * inv) | f32_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
+    const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    if (!(top <= kMaxF32) || x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3]) {   // NaN and infinities
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (!(fabsf(x[i]) <= kMaxF32)) w = (w & ~(0xffu << 8 * i)) | 0x7fu << 8 * i;
+        for (int i = 0; i < 4; ++i)
+            if (!(fabsf(x[i]) <= kMaxF32)) w = (w & ~(0xffu << 8 * i)) | 0x7fu << 8 * i;
+    }
     return w;
 }
+template <int W>
+__device__ __forceinline__ void store_codes(unsigned char *p, const float *x, float inv) {
+    if constexpr (W == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(code4(x, inv), code4(x + 4, inv));
+    else *reinterpret_cast<uint32_t *>(p) = code4(x, inv);
+}
 
-// Blocks: [0, pages) x (b, kv head) x (K, V): the page-th page that new tokens of the sequence may fall into.
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-kv8_append_kernel(const Kv8StoreProblem p, int k_vec, int v_vec) {
+// The new tokens of one page of one kv head, K or V, by `size` threads: a warp (few tokens) or a block.  K units per thread
+// stay in registers between the search for the largest magnitude and the rounding.
+template <typename T, int W, bool BLOCK>
+__device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, int half, int page_no, int me, int size, bool vec) {
+    constexpr int KEEP = 4;
     __shared__ float sh_max[kThreads / 32];
     const Kv8Cache &c = p.c;
-    const int D = c.D, P = c.P, units = D / 8;
-    const int bh = blockIdx.y, b = bh / c.Hkv, h = bh % c.Hkv, half = blockIdx.z;
+    const int D = c.D, P = c.P, units = D / (2 * W);
+    const int b = bh / c.Hkv, h = bh % c.Hkv;
     const int n_new = p.counts ? p.counts[b] : p.n;
     const int base = p.lens ? p.lens[b] : 0, most = c.per_seq * P;
     // new tokens that fit: the rest is left out, and recorded
     const int fit = base < 0 ? 0 : (int)min((long long)min(n_new, p.n), (long long)most - base);
-    if (blockIdx.x == 0 && h == 0 && half == 0 && threadIdx.x == 0) {
+    if (page_no == 0 && h == 0 && half == 0 && me == 0) {
         if (base < 0 || n_new < 0 || n_new > p.n || fit < n_new) atomicExch(p.status, (int)OSF_ERR_INVALID);
         if (p.R && fit > 0 && base + fit > p.max_pos) atomicExch(p.status, (int)OSF_ERR_INVALID);
     }
     if (fit <= 0) return;
-    const int first = (base / P + blockIdx.x) * P;        // first token of the page
+    const int first = (base / P + page_no) * P;           // first token of the page
     if (first >= base + fit) return;
     const int t0 = max(base, first), t1 = min(base + fit, first + P);   // its new tokens
-    const int page = kv8_page(c, b, first, p.status);
-    if (page < 0) return;
+    const int entry = kv8_entry(c, b, first);
     const T *rows = half ? static_cast<const T *>(p.v) + b * p.v_sb + h * p.v_sh
                          : static_cast<const T *>(p.k) + b * p.k_sb + h * p.k_sh;
     const long long ss = half ? p.v_ss : p.k_ss;
-    const bool vec = half ? v_vec : k_vec;
-    const int R = half ? 0 : p.R;
-    const long long at = ((long long)page * 2 + half) * c.Hkv + h;
-    unsigned char *codes = c.pages + at * P * D;
-    const int work = (t1 - t0) * units;
-    float x[8], mx = 0.f;
-    for (int i = threadIdx.x; i < work; i += blockDim.x) {
+    const int R = half ? 0 : p.R, work = (t1 - t0) * units;
+    auto load = [&](int i, float (&x)[2 * W]) {
         const int tok = t0 + i / units;
-        load_unit(p, rows + (tok - base) * ss, unit_of(i % units, R, p.interleaved), min(tok, p.max_pos - 1), vec, x);
+        const Unit w = unit_of<W>(i % units, R, p.interleaved);
+        const T *row = rows + (tok - base) * ss;
+        load_run<W>(row + w.first, vec, x);
+        load_run<W>(row + w.second, vec, x + W);
+    };
+    auto rotate = [&](int i, float (&x)[2 * W]) {
+        const Unit w = unit_of<W>(i % units, R, p.interleaved);
+        if (w.rotated) rotate_unit<W>(p, w, min(t0 + i / units, p.max_pos - 1), x);
+    };
+    float mx = 0.f;
+    auto largest = [&](const float (&x)[2 * W]) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 2 * W; ++e) {
             const float a = fabsf(x[e]);
             mx = a <= kMaxF32 ? fmaxf(mx, a) : mx;
         }
+    };
+    float kept[KEEP][2 * W];
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        if (me + k * size < work) load(me + k * size, kept[k]);
+    const int page = kv8_checked(c, entry, p.status);
+    if (page < 0) return;
+    const long long at = ((long long)page * 2 + half) * c.Hkv + h;
+    const float old_scale = c.scales[at];
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        if (me + k * size < work) {
+            rotate(me + k * size, kept[k]);
+            largest(kept[k]);
+        }
+    for (int i = me + KEEP * size; i < work; i += size) {
+        float x[2 * W];
+        load(i, x);
+        rotate(i, x);
+        largest(x);
     }
     mx = warp_max(mx);
-    if ((threadIdx.x & 31) == 0) sh_max[threadIdx.x >> 5] = mx;
-    const float old_scale = c.scales[at];
-    __syncthreads();
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) mx = fmaxf(mx, sh_max[w]);
+    if constexpr (BLOCK) {
+        if ((me & 31) == 0) sh_max[me >> 5] = mx;
+        __syncthreads();
+        for (int w = 0; w < size / 32; ++w) mx = fmaxf(mx, sh_max[w]);
+    }
     // mx = (1 + m / 2^23) 2^x: the least e with mx <= 1.75 * 2^(8 + e)
     const uint32_t bits = __float_as_uint(mx);
     int e = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), kKv8MinExp);
+    unsigned char *codes = c.pages + at * P * D;
     if (t0 > first) {   // earlier tokens: the scale only grows, and their codes follow it
         const int old = kv8_exponent(old_scale);
         if (e > old) {
             const float f = pow2_of(max(old - e, -126));
             const int words = (t0 - first) * D / 4;
-            for (int i = threadIdx.x; i < words; i += blockDim.x) {
+            for (int i = me; i < words; i += size) {
                 uint32_t *w = reinterpret_cast<uint32_t *>(codes) + i;
                 const float2 lo = e4m3x2_to_f32(*w), hi = e4m3x2_to_f32(*w >> 16);
                 *w = f32_to_e4m3x2(lo.x * f, lo.y * f) | f32_to_e4m3x2(hi.x * f, hi.y * f) << 16;
@@ -170,37 +248,85 @@ kv8_append_kernel(const Kv8StoreProblem p, int k_vec, int v_vec) {
         e = max(e, old);
     }
     const float inv = pow2_of(-e);
-    for (int i = threadIdx.x; i < work; i += blockDim.x) {
-        const int tok = t0 + i / units;
-        const Unit w = unit_of(i % units, R, p.interleaved);
-        load_unit(p, rows + (tok - base) * ss, w, min(tok, p.max_pos - 1), vec, x);
-        unsigned char *row = codes + (long long)(tok - first) * D;
-        *reinterpret_cast<uint32_t *>(row + w.first) = code4(x, inv);
-        *reinterpret_cast<uint32_t *>(row + w.second) = code4(x + 4, inv);
+    auto store = [&](int i, const float (&x)[2 * W]) {
+        const Unit w = unit_of<W>(i % units, R, p.interleaved);
+        unsigned char *row = codes + (long long)(t0 + i / units - first) * D;
+        store_codes<W>(row + w.first, x, inv);
+        store_codes<W>(row + w.second, x + W, inv);
+    };
+#pragma unroll
+    for (int k = 0; k < KEEP; ++k)
+        if (me + k * size < work) store(me + k * size, kept[k]);
+    for (int i = me + KEEP * size; i < work; i += size) {   // pages of more: once more from the start
+        float x[2 * W];
+        load(i, x);
+        rotate(i, x);
+        store(i, x);
     }
-    if (threadIdx.x == 0) c.scales[at] = pow2_of(e);
+    if constexpr (BLOCK) __syncthreads();   // (every thread has read the old scale)
+    else __syncwarp();
+    if (me == 0) c.scales[at] = pow2_of(e);
 }
 
-// The queries of the new tokens, rotated.  A thread takes a unit of a row.
-template <typename T>
+// The queries of the new tokens, rotated in float32.  A thread takes a unit of a token for HB heads: the angles are read once.
+template <typename T, int W, int HB>
+__device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, long long i, int q_vec, int o_vec) {
+    const int units = p.c.D / (2 * W), chunks = (p.Hq + HB - 1) / HB;
+    const int u = (int)(i % units);
+    const long long row = i / units;
+    const int t = (int)(row % p.n), bc = (int)(row / p.n), b = bc / chunks, h0 = bc % chunks * HB;
+    if (b >= p.B || t >= (p.counts ? min(p.counts[b], p.n) : p.n)) return;
+    const Unit w = unit_of<W>(u, p.R, p.interleaved);
+    const T *src = static_cast<const T *>(p.q) + b * p.q_sb + h0 * p.q_sh + t * p.q_ss;
+    T *dst = static_cast<T *>(p.qo) + b * p.o_sb + h0 * p.o_sh + t * p.o_ss;
+    float c[W], s[W];
+    if (w.rotated) load_angles<W>(p, w, min(max((p.lens ? p.lens[b] : 0) + t, 0), p.max_pos - 1), c, s);
+    float x[HB][2 * W];
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+        if (h0 + k < p.Hq) {
+            load_run<W>(src + k * p.q_sh + w.first, q_vec, x[k]);
+            load_run<W>(src + k * p.q_sh + w.second, q_vec, x[k] + W);
+        }
+#pragma unroll
+    for (int k = 0; k < HB; ++k)
+        if (h0 + k < p.Hq) {
+            if (w.rotated) {
+                float a[W], b2[W];
+                split_pairs<W>(x[k], p.interleaved, a, b2);
+#pragma unroll
+                for (int e = 0; e < W; ++e) {
+                    const float ra = fmaf(a[e], c[e], -(b2[e] * s[e])), rb = fmaf(b2[e], c[e], a[e] * s[e]);
+                    a[e] = ra;
+                    b2[e] = rb;
+                }
+                join_pairs<W>(x[k], p.interleaved, a, b2);
+            }
+            store_run<W>(dst + k * p.o_sh + w.first, o_vec, x[k]);
+            store_run<W>(dst + k * p.o_sh + w.second, o_vec, x[k] + W);
+        }
+}
+
+// One launch: the pages that new tokens may fall into, then the queries.
+template <typename T, int W, bool BLOCK, int HB>
 __global__ void __launch_bounds__(kThreads)
-kv8_rotate_kernel(const Kv8StoreProblem p, int q_vec, int o_vec) {
-    const int units = p.c.D / 8;
-    const int bh = blockIdx.y, b = bh / p.Hq, h = bh % p.Hq;
-    const int count = min(p.counts ? p.counts[b] : p.n, p.n), base = p.lens ? p.lens[b] : 0;
-    const T *src = static_cast<const T *>(p.q) + b * p.q_sb + h * p.q_sh;
-    T *dst = static_cast<T *>(p.qo) + b * p.o_sb + h * p.o_sh;
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < count * units; i += gridDim.x * kThreads) {
-        const int t = i / units;
-        const Unit w = unit_of(i % units, p.R, p.interleaved);
-        float x[8];
-        load_unit(p, src + t * p.q_ss, w, min(max(base + t, 0), p.max_pos - 1), q_vec, x);
-        store4(dst + t * p.o_ss + w.first, o_vec, x);
-        store4(dst + t * p.o_ss + w.second, o_vec, x + 4);
+kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned page_blocks, int k_vec, int v_vec, int q_vec, int o_vec) {
+    const Kv8Cache &c = p.c;
+    if (blockIdx.x >= page_blocks) {
+        rotate_queries<T, W, HB>(p, (long long)(blockIdx.x - page_blocks) * kThreads + threadIdx.x, q_vec, o_vec);
+        return;
     }
+    const long long task = BLOCK ? blockIdx.x : (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int page_no = (int)(task % pages_per_seq);
+    const long long bhh = task / pages_per_seq;
+    const int half = (int)(bhh & 1), bh = (int)(bhh >> 1);
+    if (bh >= p.B * c.Hkv) return;
+    append_page<T, W, BLOCK>(p, bh, half, page_no, BLOCK ? threadIdx.x : threadIdx.x & 31, BLOCK ? kThreads : 32,
+                             half ? v_vec : k_vec);
 }
 
-// A thread takes 16 channels of a token.
+// A thread takes 16 channels of four tokens at a time: their loads are in flight together.
+constexpr int kReadTokens = 4;
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 kv8_read_kernel(const Kv8StoreProblem p, int k_vec, int v_vec) {
@@ -210,51 +336,82 @@ kv8_read_kernel(const Kv8StoreProblem p, int k_vec, int v_vec) {
     const int len = kv8_length(p.lens, b, c.per_seq * c.P, p.status), start = p.starts ? p.starts[b] : 0;
     T *out = static_cast<T *>(half ? p.vo : p.ko) + (long long)bh * p.n * D;
     const bool vec = half ? v_vec : k_vec;
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < p.n * per; i += gridDim.x * kThreads) {
-        const int t = i / per, ch = i % per * 16;
-        const long long pos = (long long)start + t;
-        const int page = pos >= 0 && pos < len ? kv8_page(c, b, (int)pos, p.status) : -1;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float scale = 0.f;
-        if (page >= 0) {
-            const long long at = ((long long)page * 2 + half) * c.Hkv + h;
-            w = *reinterpret_cast<const uint4 *>(c.pages + (at * c.P + pos % c.P) * D + ch);
-            scale = pow2_of(kv8_exponent(c.scales[at]));
-        }
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    const int total = p.n * per, step = gridDim.x * kThreads;
+    for (int i0 = blockIdx.x * kThreads + threadIdx.x; i0 < total; i0 += kReadTokens * step) {
+        int entry[kReadTokens];
+        bool have[kReadTokens];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 lo = e4m3x2_to_f32(v[e]), hi = e4m3x2_to_f32(v[e] >> 16);
-            const float x[4] = {lo.x * scale, lo.y * scale, hi.x * scale, hi.y * scale};
-            store4(out + (long long)t * D + ch + 4 * e, vec, x);
+        for (int e = 0; e < kReadTokens; ++e) {
+            const int i = i0 + e * step;
+            const long long pos = (long long)start + i / per;
+            have[e] = i < total && i >= i0 && pos >= 0 && pos < len;
+            entry[e] = have[e] ? kv8_entry(c, b, (int)pos) : 0;
+        }
+        uint4 v[kReadTokens];
+        float scale[kReadTokens];
+#pragma unroll
+        for (int e = 0; e < kReadTokens; ++e) {
+            const int i = i0 + e * step, page = have[e] ? kv8_checked(c, entry[e], p.status) : -1;
+            v[e] = make_uint4(0, 0, 0, 0);
+            scale[e] = 1.f;
+            if (page >= 0) {
+                const long long at = ((long long)page * 2 + half) * c.Hkv + h;
+                v[e] = *reinterpret_cast<const uint4 *>(c.pages + (at * c.P + ((start + i / per) & (c.P - 1))) * D + i % per * 16);
+                scale[e] = c.scales[at];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kReadTokens; ++e) {
+            const int i = i0 + e * step;
+            if (i >= total || i < i0) break;
+            const float f = pow2_of(kv8_exponent(scale[e]));
+            const uint32_t w[4] = {v[e].x, v[e].y, v[e].z, v[e].w};
+            float x[16];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 lo = e4m3x2_to_f32(w[k]), hi = e4m3x2_to_f32(w[k] >> 16);
+                x[4 * k] = lo.x * f; x[4 * k + 1] = lo.y * f; x[4 * k + 2] = hi.x * f; x[4 * k + 3] = hi.y * f;
+            }
+            store_run<8>(out + (long long)i * 16, vec, x);
+            store_run<8>(out + (long long)i * 16 + 8, vec, x + 8);
         }
     }
 }
 
-bool rows_vec(const void *q, long long a, long long b, long long c, int es) {
-    const int unit = 4 * es;   // four channels
-    return (reinterpret_cast<uintptr_t>(q) % unit) == 0 && (a | b | c) % 4 == 0;
+// Whether runs of W channels of every row can be read or written 16 (bfloat16 and W = 4: 8) bytes at a time.
+bool rows_vec(const void *q, long long a, long long b, long long c, int es, int W) {
+    const int bytes = W * es < 16 ? W * es : 16, elems = bytes / es;
+    return (reinterpret_cast<uintptr_t>(q) % bytes) == 0 && (a | b | c) % elems == 0;
 }
 
-template <typename T>
-cudaError_t append_t(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
+template <typename T, int W, bool BLOCK, int HB>
+cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s) {
     const Kv8Cache &c = p.c;
     const int es = sizeof(T);
-    const long long pages = ((long long)p.n + 2 * c.P - 2) / c.P;
-    const int tokens = p.n < c.P ? p.n : c.P, want = (tokens * (c.D / 8) + 31) / 32 * 32;
-    const dim3 grid((unsigned)(pages < c.per_seq ? pages : c.per_seq), (unsigned)(p.B * c.Hkv), 2);
-    kv8_append_kernel<T><<<grid, want < kThreads ? want : kThreads, 0, s>>>(
-        p, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es), rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es));
-    count_launches(1);
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || !p.q) return e;
-    const long long work = ((long long)p.n * (c.D / 8) + kThreads - 1) / kThreads;
-    const long long most = (16LL * sm_count + p.B * p.Hq - 1) / (p.B * p.Hq);
-    const dim3 gq((unsigned)(work < most ? work : most), (unsigned)(p.B * p.Hq));
-    kv8_rotate_kernel<T><<<gq, kThreads, 0, s>>>(p, rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es),
-                                                 rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es));
+    const long long tasks = (long long)p.B * c.Hkv * 2 * pages_per_seq;
+    const long long page_blocks = BLOCK ? tasks : (tasks + kThreads / 32 - 1) / (kThreads / 32);
+    const long long q_threads = p.q ? (long long)p.B * ((p.Hq + HB - 1) / HB) * p.n * (c.D / (2 * W)) : 0;
+    const long long blocks = page_blocks + (q_threads + kThreads - 1) / kThreads;
+    if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    kv8_append_kernel<T, W, BLOCK, HB><<<(unsigned)blocks, kThreads, 0, s>>>(
+        p, pages_per_seq, (unsigned)page_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
+        rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
+        rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es, W));
     count_launches(1);
     return cudaGetLastError();
+}
+
+template <typename T, int W>
+cudaError_t append_w(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
+    const Kv8Cache &c = p.c;
+    const long long pages = ((long long)p.n + 2 * c.P - 2) / c.P;
+    const int per_seq = (int)(pages < c.per_seq ? pages : c.per_seq);
+    // a warp to a page while a page's new tokens are four units to a lane at most
+    const bool block = (long long)(p.n < c.P ? p.n : c.P) * (c.D / (2 * W)) > 128;
+    // several heads to a thread once there are threads enough
+    const bool heads = (long long)p.B * p.Hq * p.n * (c.D / (2 * W)) >= 8LL * 1024 * sm_count;
+    if (block) return heads ? append_k<T, W, true, 4>(p, per_seq, s) : append_k<T, W, true, 1>(p, per_seq, s);
+    return heads ? append_k<T, W, false, 4>(p, per_seq, s) : append_k<T, W, false, 1>(p, per_seq, s);
 }
 
 template <typename T>
@@ -263,15 +420,19 @@ cudaError_t read_t(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
     const long long work = ((long long)p.n * (c.D / 16) + kThreads - 1) / kThreads;
     const long long most = (16LL * sm_count + p.B * c.Hkv * 2 - 1) / (p.B * c.Hkv * 2);
     const dim3 grid((unsigned)(work < most ? work : most), (unsigned)(p.B * c.Hkv), 2);
-    kv8_read_kernel<T><<<grid, kThreads, 0, s>>>(p, rows_vec(p.ko, 0, 0, 0, sizeof(T)), rows_vec(p.vo, 0, 0, 0, sizeof(T)));
+    kv8_read_kernel<T><<<grid, kThreads, 0, s>>>(p, rows_vec(p.ko, 0, 0, 0, sizeof(T), 8), rows_vec(p.vo, 0, 0, 0, sizeof(T), 8));
     count_launches(1);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_kv8_append(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
-    return p.dtype == OSF_F32 ? append_t<float>(p, sm_count, s) : append_t<__nv_bfloat16>(p, sm_count, s);
+cudaError_t launch_kv8_append(const Kv8StoreProblem &p0, int sm_count, cudaStream_t s) {
+    Kv8StoreProblem p = p0;
+    const bool wide = p.R % 16 == 0;   // units of 16 channels; else (multiples of 8) of 8
+    p.table_vec = ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15u) == 0;
+    if (p.dtype == OSF_F32) return wide ? append_w<float, 8>(p, sm_count, s) : append_w<float, 4>(p, sm_count, s);
+    return wide ? append_w<__nv_bfloat16, 8>(p, sm_count, s) : append_w<__nv_bfloat16, 4>(p, sm_count, s);
 }
 cudaError_t launch_kv8_read(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
     return p.dtype == OSF_F32 ? read_t<float>(p, sm_count, s) : read_t<__nv_bfloat16>(p, sm_count, s);

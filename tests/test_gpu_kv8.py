@@ -1,6 +1,7 @@
 """The paged 8-bit cache (osf_kv8_append, osf_kv8_read, osf_attn_kv8) against oracle.kv8 and oracle.attention_window.
 
-Codes, scales and the values read back are exact: equal.  Rotated queries: one rounding to the type, equal too.
+Codes, scales and the values read back are exact: equal.  Rotated queries, a c - b s in float32: the product b s rounded
+(2^-24 of it), the fused difference (2^-24 of that), then the type (2^-8 in bfloat16).
 Attention, from what is rounded: bfloat16 O once (2^-8 |O|), P to float16 (2^-11 of size = sum P |V|); the queries
 are exact, scores and sums float32 (2^-24 a step, D + log steps deep: below 2^-15 of size with the inputs here).
 float32: 2e-5 of size, as the windowed forward.  lse: 2e-5 absolute and relative.
@@ -48,6 +49,14 @@ def rows(rng, shape, dtype):
     return x, torch.from_numpy(x).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
 
 
+def check_rotated(got, q, ref, dtype):
+    """ref: rotated exactly, but for one rounding to float32 (2^-24 more)."""
+    u = 2.0 ** -8 if dtype == "bf16" else 0.0
+    pair = np.abs(q).max(-1, keepdims=True)   # |b s| is at most the row's largest
+    bound = 2.0 ** -24 * pair + (u + 2.0 ** -23) * np.abs(ref)
+    assert np.all(np.abs(got.double().cpu().numpy() - ref) <= bound * (1 + 1 / 16))
+
+
 CASES = [
     # B, Hkv, n, D, P, per, lens, counts, rot, interleaved
     (1, 1, 1, 32, 16, 1, [0], None, 32, False),
@@ -90,8 +99,7 @@ def test_append_and_read(osf, dtype, B, Hkv, n, D, P, per, lens, counts, rot, in
     for b in range(B):
         ref = oracle.rotate(q[b], np.arange(lens[b], lens[b] + n) if cos is None else
                             np.minimum(np.arange(lens[b], lens[b] + n), len(cos) - 1), cos, sin, inter)
-        want = torch.from_numpy(ref).cuda().to(Q.dtype)
-        assert torch.equal(qo[b, :, :new[b]], want[:, :new[b]])
+        check_rotated(qo[b, :, :new[b]], q[b, :, :new[b]], ref[:, :new[b]], dtype)
         assert (qo[b, :, new[b]:] == 77).all()
     # read back from around the new tokens
     starts = np.array([x - 2 for x in lens], np.int32)
@@ -128,7 +136,7 @@ def test_codes_at_every_tie_and_edge(osf):
 
 
 def test_rotation_is_rounded_once(osf):
-    """Products that cancel to their last bits: the float32 nearest to a c - b s, and its code."""
+    """K's products that cancel to their last bits: the code of the float32 nearest to a c - b s."""
     rng = np.random.default_rng(8)
     n, D = 64, 64
     c = rng.uniform(0.5, 1, (n, 32)).astype(np.float32)
@@ -137,10 +145,18 @@ def test_rotation_is_rounded_once(osf):
     k[0, 0, :, 32:] = (k[0, 0, :, :32] * (c / s)).astype(np.float32)   # a c = b s to 2^-24
     pages, scales, table = new_cache(1, 1, 1, 64, D)
     gp, gs, gt, gc, gsn = to_gpu(pages, scales, table, c, s)
-    qo = osf.osf_kv8_append(f32_tensor(k), f32_tensor(k), gp, gs, gt, cos=gc, sin=gsn, q=f32_tensor(k))
+    osf.osf_kv8_append(f32_tensor(k), f32_tensor(k), gp, gs, gt, cos=gc, sin=gsn)
+    oracle.kv8_append(k, k, pages, scales, table, None, None, c, s)
+    assert np.array_equal(gp.cpu().numpy(), pages) and np.array_equal(gs.cpu().numpy(), scales)
     ref = oracle.rotate(k[0], np.arange(n), c, s, False)
-    assert np.array_equal(qo[0].cpu().numpy(), ref)
     assert (np.abs(ref[0, :, :32]) < 1e-5).mean() > 0.9   # the input does what it is for
+    # a = b and c = s to a step: both results are differences or twice a product, by turns of the sign
+    k3 = np.repeat(k[..., :32], 2, -1).reshape(1, 1, n, 32, 2).transpose(0, 1, 2, 4, 3).reshape(1, 1, n, D).copy()
+    s3 = np.nextafter(c, np.float32(2)) * np.where(np.arange(32) % 2, 1, -1).astype(np.float32)
+    gp, gs, gt, g3 = to_gpu(pages, scales, table, s3)
+    osf.osf_kv8_append(f32_tensor(k3), f32_tensor(k3), gp, gs, gt, cos=gc, sin=g3)
+    oracle.kv8_append(k3, k3, pages, scales, table, None, None, c, s3)
+    assert np.array_equal(gp.cpu().numpy(), pages) and np.array_equal(gs.cpu().numpy(), scales)
 
 
 def test_nan_and_infinity_are_stored_as_nan(osf):
@@ -233,6 +249,11 @@ ATTN = [
     (1, 4, 2, 40, 32, [333], 50, 3),
     (1, 4, 2, 40, 32, [33], 0, 0),
     (2, 3, 3, 2, 64, [5000, 4000], 1500, 4),
+    # long enough to be cut over CTAs
+    (3, 4, 1, 1, 64, [9000, 5, 4100], 0, 0),
+    (1, 8, 1, 1, 32, [6001], 0, 0),
+    (2, 16, 1, 1, 64, [0, 7000], 0, 0),
+    (2, 4, 1, 5, 128, [8000, 6500], 4000, 200),
 ]
 
 
