@@ -88,6 +88,9 @@ __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     return fabsf(h) <= kMaxF32 ? __fadd_rn(h, __fadd_rn(he, __fsub_rn(pe, qe))) : h;
 }
 
+// i / d for inv = floor(2^32 / d) + 1: exact for i < 2^32 / d.
+__device__ __forceinline__ int quotient(int i, uint32_t inv) { return (int)__umulhi((uint32_t)i, inv); }
+
 // Where the 2 W channels of unit u of a row lie: two runs of W, at first and second.  The W pairs of a unit that is rotated
 // have the angles in columns angle .. angle + W - 1 of the tables.
 struct Unit {
@@ -143,28 +146,29 @@ __device__ __forceinline__ void rotate_unit(const Kv8StoreProblem &p, const Unit
     join_pairs<W>(x, p.interleaved, a, b);
 }
 
+// Codes of four values.  ODD: some of the page's are NaN or infinite.
+template <bool ODD>
 __device__ __forceinline__ uint32_t code4(const float *x, float inv) {
     uint32_t w = f32_to_e4m3x2(x[0] * inv, x[1] * inv) | f32_to_e4m3x2(x[2] * inv, x[3] * inv) << 16;
-    const float top = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-    if (!(top <= kMaxF32) || x[0] != x[0] || x[1] != x[1] || x[2] != x[2] || x[3] != x[3]) {   // NaN and infinities
+    if constexpr (ODD) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (!(fabsf(x[i]) <= kMaxF32)) w = (w & ~(0xffu << 8 * i)) | 0x7fu << 8 * i;
     }
     return w;
 }
-template <int W>
+template <int W, bool ODD>
 __device__ __forceinline__ void store_codes(unsigned char *p, const float *x, float inv) {
-    if constexpr (W == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(code4(x, inv), code4(x + 4, inv));
-    else *reinterpret_cast<uint32_t *>(p) = code4(x, inv);
+    if constexpr (W == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(code4<ODD>(x, inv), code4<ODD>(x + 4, inv));
+    else *reinterpret_cast<uint32_t *>(p) = code4<ODD>(x, inv);
 }
 
 // The new tokens of one page of one kv head, K or V, by `size` threads: a warp (few tokens) or a block.  K units per thread
 // stay in registers between the search for the largest magnitude and the rounding.
 template <typename T, int W, bool BLOCK>
 __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, int half, int page_no, int me, int size, bool vec) {
-    constexpr int KEEP = 4;
-    __shared__ float sh_max[kThreads / 32];
+    constexpr int KEEP = W == 8 ? 2 : 4;
+    __shared__ uint32_t sh_max[kThreads / 32];
     const Kv8Cache &c = p.c;
     const int D = c.D, P = c.P, units = D / (2 * W);
     const int b = bh / c.Hkv, h = bh % c.Hkv;
@@ -185,29 +189,48 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
                          : static_cast<const T *>(p.k) + b * p.k_sb + h * p.k_sh;
     const long long ss = half ? p.v_ss : p.k_ss;
     const int R = half ? 0 : p.R, work = (t1 - t0) * units;
-    auto load = [&](int i, float (&x)[2 * W]) {
-        const int tok = t0 + i / units;
-        const Unit w = unit_of<W>(i % units, R, p.interleaved);
-        const T *row = rows + (tok - base) * ss;
-        load_run<W>(row + w.first, vec, x);
-        load_run<W>(row + w.second, vec, x + W);
+    rows += (t0 - base) * ss;
+    struct Spot {
+        int t;   // token behind t0
+        Unit w;
     };
-    auto rotate = [&](int i, float (&x)[2 * W]) {
-        const Unit w = unit_of<W>(i % units, R, p.interleaved);
-        if (w.rotated) rotate_unit<W>(p, w, min(t0 + i / units, p.max_pos - 1), x);
+    auto spot_of = [&](int i) {
+        const int t = quotient(i, p.units_inv);
+        return Spot{t, unit_of<W>(i - t * units, R, p.interleaved)};
     };
-    float mx = 0.f;
+    auto load = [&](const Spot &o, float (&x)[2 * W]) {
+        const T *row = rows + o.t * ss;
+        load_run<W>(row + o.w.first, vec, x);
+        load_run<W>(row + o.w.second, vec, x + W);
+    };
+    auto rotate = [&](const Spot &o, float (&x)[2 * W]) {
+        if (o.w.rotated) rotate_unit<W>(p, o.w, min(t0 + o.t, p.max_pos - 1), x);
+    };
+    // the largest magnitude, as bits: a NaN or an infinity shows
+    constexpr uint32_t INF = 0x7f800000u;
+    uint32_t mx = 0;
     auto largest = [&](const float (&x)[2 * W]) {
 #pragma unroll
-        for (int e = 0; e < 2 * W; ++e) {
-            const float a = fabsf(x[e]);
-            mx = a <= kMaxF32 ? fmaxf(mx, a) : mx;
+        for (int e = 0; e < 2 * W; ++e) mx = max(mx, __float_as_uint(x[e]) & 0x7fffffffu);
+    };
+    auto of_all = [&](uint32_t m) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if constexpr (BLOCK) {
+            __syncthreads();
+            if ((me & 31) == 0) sh_max[me >> 5] = m;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kThreads / 32; ++w) m = max(m, sh_max[w]);
         }
+        return m;
     };
     float kept[KEEP][2 * W];
+    Spot spot[KEEP];
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        if (me + k * size < work) load(me + k * size, kept[k]);
+    for (int k = 0; k < KEEP; ++k) {
+        spot[k] = spot_of(me + k * size);
+        if (me + k * size < work) load(spot[k], kept[k]);
+    }
     const int page = kv8_checked(c, entry, p.status);
     if (page < 0) return;
     const long long at = ((long long)page * 2 + half) * c.Hkv + h;
@@ -215,24 +238,35 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
         if (me + k * size < work) {
-            rotate(me + k * size, kept[k]);
+            rotate(spot[k], kept[k]);
             largest(kept[k]);
         }
     for (int i = me + KEEP * size; i < work; i += size) {
         float x[2 * W];
-        load(i, x);
-        rotate(i, x);
+        const Spot o = spot_of(i);
+        load(o, x);
+        rotate(o, x);
         largest(x);
     }
-    mx = warp_max(mx);
-    if constexpr (BLOCK) {
-        if ((me & 31) == 0) sh_max[me >> 5] = mx;
-        __syncthreads();
-        for (int w = 0; w < size / 32; ++w) mx = fmaxf(mx, sh_max[w]);
+    mx = of_all(mx);
+    const bool odd = mx >= INF;
+    if (odd) {   // once more, without them
+        mx = 0;
+        for (int i = me; i < work; i += size) {
+            float x[2 * W];
+            const Spot o = spot_of(i);
+            load(o, x);
+            rotate(o, x);
+#pragma unroll
+            for (int e = 0; e < 2 * W; ++e) {
+                const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
+                mx = max(mx, u < INF ? u : 0u);
+            }
+        }
+        mx = of_all(mx);
     }
     // mx = (1 + m / 2^23) 2^x: the least e with mx <= 1.75 * 2^(8 + e)
-    const uint32_t bits = __float_as_uint(mx);
-    int e = max((int)(bits >> 23) - 127 - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0), kKv8MinExp);
+    int e = max((int)(mx >> 23) - 127 - 8 + ((mx & 0x7fffffu) > 0x600000u ? 1 : 0), kKv8MinExp);
     unsigned char *codes = c.pages + at * P * D;
     if (t0 > first) {   // earlier tokens: the scale only grows, and their codes follow it
         const int old = kv8_exponent(old_scale);
@@ -248,20 +282,25 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
         e = max(e, old);
     }
     const float inv = pow2_of(-e);
-    auto store = [&](int i, const float (&x)[2 * W]) {
-        const Unit w = unit_of<W>(i % units, R, p.interleaved);
-        unsigned char *row = codes + (long long)(t0 + i / units - first) * D;
-        store_codes<W>(row + w.first, x, inv);
-        store_codes<W>(row + w.second, x + W, inv);
+    auto store = [&](const Spot &o, const float (&x)[2 * W]) {
+        unsigned char *row = codes + (t0 - first + o.t) * D;
+        if (odd) {
+            store_codes<W, true>(row + o.w.first, x, inv);
+            store_codes<W, true>(row + o.w.second, x + W, inv);
+        } else {
+            store_codes<W, false>(row + o.w.first, x, inv);
+            store_codes<W, false>(row + o.w.second, x + W, inv);
+        }
     };
 #pragma unroll
     for (int k = 0; k < KEEP; ++k)
-        if (me + k * size < work) store(me + k * size, kept[k]);
+        if (me + k * size < work) store(spot[k], kept[k]);
     for (int i = me + KEEP * size; i < work; i += size) {   // pages of more: once more from the start
         float x[2 * W];
-        load(i, x);
-        rotate(i, x);
-        store(i, x);
+        const Spot o = spot_of(i);
+        load(o, x);
+        rotate(o, x);
+        store(o, x);
     }
     if constexpr (BLOCK) __syncthreads();   // (every thread has read the old scale)
     else __syncwarp();
@@ -270,12 +309,10 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
 
 // The queries of the new tokens, rotated in float32.  A thread takes a unit of a token for HB heads: the angles are read once.
 template <typename T, int W, int HB>
-__device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, long long i, int q_vec, int o_vec) {
+__device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc, int i, int q_vec, int o_vec) {
     const int units = p.c.D / (2 * W), chunks = (p.Hq + HB - 1) / HB;
-    const int u = (int)(i % units);
-    const long long row = i / units;
-    const int t = (int)(row % p.n), bc = (int)(row / p.n), b = bc / chunks, h0 = bc % chunks * HB;
-    if (b >= p.B || t >= (p.counts ? min(p.counts[b], p.n) : p.n)) return;
+    const int b = bc / chunks, h0 = bc % chunks * HB, t = quotient(i, p.units_inv), u = i - t * units;
+    if (t >= (p.counts ? min(p.counts[b], p.n) : p.n)) return;
     const Unit w = unit_of<W>(u, p.R, p.interleaved);
     const T *src = static_cast<const T *>(p.q) + b * p.q_sb + h0 * p.q_sh + t * p.q_ss;
     T *dst = static_cast<T *>(p.qo) + b * p.o_sb + h0 * p.o_sh + t * p.o_ss;
@@ -309,17 +346,19 @@ __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, long lo
 
 // One launch: the pages that new tokens may fall into, then the queries.
 template <typename T, int W, bool BLOCK, int HB>
-__global__ void __launch_bounds__(kThreads)
-kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned page_blocks, int k_vec, int v_vec, int q_vec, int o_vec) {
+__global__ void __launch_bounds__(kThreads, 3)
+kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned page_blocks, unsigned q_blocks, int k_vec, int v_vec,
+                  int q_vec, int o_vec) {
     const Kv8Cache &c = p.c;
     if (blockIdx.x >= page_blocks) {
-        rotate_queries<T, W, HB>(p, (long long)(blockIdx.x - page_blocks) * kThreads + threadIdx.x, q_vec, o_vec);
+        // q_blocks blocks to each (batch, HB heads)
+        const unsigned qb = blockIdx.x - page_blocks, bc = qb / q_blocks;
+        rotate_queries<T, W, HB>(p, (int)bc, (int)((qb - bc * q_blocks) * kThreads + threadIdx.x), q_vec, o_vec);
         return;
     }
-    const long long task = BLOCK ? blockIdx.x : (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int page_no = (int)(task % pages_per_seq);
-    const long long bhh = task / pages_per_seq;
-    const int half = (int)(bhh & 1), bh = (int)(bhh >> 1);
+    const unsigned task = BLOCK ? blockIdx.x : blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const unsigned bhh = task / pages_per_seq;
+    const int page_no = (int)(task - bhh * pages_per_seq), half = (int)(bhh & 1), bh = (int)(bhh >> 1);
     if (bh >= p.B * c.Hkv) return;
     append_page<T, W, BLOCK>(p, bh, half, page_no, BLOCK ? threadIdx.x : threadIdx.x & 31, BLOCK ? kThreads : 32,
                              half ? v_vec : k_vec);
@@ -390,11 +429,11 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
     const int es = sizeof(T);
     const long long tasks = (long long)p.B * c.Hkv * 2 * pages_per_seq;
     const long long page_blocks = BLOCK ? tasks : (tasks + kThreads / 32 - 1) / (kThreads / 32);
-    const long long q_threads = p.q ? (long long)p.B * ((p.Hq + HB - 1) / HB) * p.n * (c.D / (2 * W)) : 0;
-    const long long blocks = page_blocks + (q_threads + kThreads - 1) / kThreads;
-    if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    const long long q_blocks = ((long long)p.n * (c.D / (2 * W)) + kThreads - 1) / kThreads;
+    const long long blocks = page_blocks + (p.q ? (long long)p.B * ((p.Hq + HB - 1) / HB) * q_blocks : 0);
+    if (blocks >= (1LL << 31) || tasks >= (1LL << 31)) return cudaErrorInvalidValue;
     kv8_append_kernel<T, W, BLOCK, HB><<<(unsigned)blocks, kThreads, 0, s>>>(
-        p, pages_per_seq, (unsigned)page_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
+        p, pages_per_seq, (unsigned)page_blocks, (unsigned)q_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
         rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
         rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es, W));
     count_launches(1);
@@ -402,12 +441,13 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
 }
 
 template <typename T, int W>
-cudaError_t append_w(const Kv8StoreProblem &p, int sm_count, cudaStream_t s) {
+cudaError_t append_w(Kv8StoreProblem p, int sm_count, cudaStream_t s) {
     const Kv8Cache &c = p.c;
+    p.units_inv = (unsigned)((1ULL << 32) / (c.D / (2 * W)) + 1);
     const long long pages = ((long long)p.n + 2 * c.P - 2) / c.P;
     const int per_seq = (int)(pages < c.per_seq ? pages : c.per_seq);
-    // a warp to a page while a page's new tokens are four units to a lane at most
-    const bool block = (long long)(p.n < c.P ? p.n : c.P) * (c.D / (2 * W)) > 128;
+    // a warp to a page while a page's new tokens fit its lanes' registers
+    const bool block = (long long)(p.n < c.P ? p.n : c.P) * (c.D / (2 * W)) > (W == 8 ? 64 : 128);
     // several heads to a thread once there are threads enough
     const bool heads = (long long)p.B * p.Hq * p.n * (c.D / (2 * W)) >= 8LL * 1024 * sm_count;
     if (block) return heads ? append_k<T, W, true, 4>(p, per_seq, s) : append_k<T, W, true, 1>(p, per_seq, s);
