@@ -147,9 +147,7 @@ __global__ void __launch_bounds__(256) bwd_dq_simt_kernel(BwdProblem p) {
     }
     const float lse2 = p.lse[row] * kLog2e, dv = p.dvec[row];
     const int j_end = p.causal ? min(p.Sk, max(0, i + p.causal_off + 1)) : p.Sk;
-    // with a window: the sinks, then the window
-    const int j_near = p.window ? max(0, i + p.causal_off - p.window + 1) : 0, j_sinks = min(p.sinks, j_near);
-    for (int j = j_sinks > 0 ? 0 : j_near; j < j_end; j = j + 1 == j_sinks ? j_near : j + 1) {
+    for (int j = 0; j < j_end; ++j) {
         float s = 0.f, dp = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -200,13 +198,11 @@ __global__ void __launch_bounds__(256) bwd_dkdv_simt_kernel(BwdProblem p) {
         dk[c] = dv[c] = 0.f;
     }
     const int i_begin = p.causal ? max(0, j - p.causal_off) : 0;
-    // with a window: a key that is no sink leaves it after `window` rows
-    const int i_end = p.window && j >= p.sinks ? min(p.Sq, max(0, j - p.causal_off + p.window)) : p.Sq;
     for (int g = 0; g < G; ++g) {
         const long long bh = (long long)b * p.Hq + kvh * G + g;
         const T *Q = static_cast<const T *>(p.q) + bh * p.Sq * D;
         const T *GO = static_cast<const T *>(p.dout) + bh * p.Sq * D;
-        for (int i = i_begin; i < i_end; ++i) {
+        for (int i = i_begin; i < p.Sq; ++i) {
             float s = 0.f, dp = 0.f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
@@ -240,6 +236,177 @@ __global__ void __launch_bounds__(256) bwd_dkdv_simt_kernel(BwdProblem p) {
             gv[d] = from_f32<T>(dv[c]);
         }
     }
+}
+
+// ------------------------------------------------------------------ a window, on the CUDA cores
+// dK, dV (DKV) of KPW keys per warp, or dQ of KPW query rows per warp, of a problem with a window (BwdProblem::window); any D up
+// to 256, float32 or bfloat16.  A block's eight warps own neighbouring keys (rows), whose rows (keys) overlap for the most part:
+// chunks of 32 of those are staged in shared memory for all of them.  For a chunk a lane first takes one of its rows (keys)
+// and both dot products with each of the warp's vectors (16-byte reads, KPW products to each), which gives P and dS; then a
+// channel of each 32, and adds up dS . b1 and P . b2 over the chunk.  Nothing is shared between blocks, so sums have one order.
+// float32, B=1 Hq=4 Hkv=2, 301 tokens of D=64, window 65: 264 us with a warp that reduces over its lanes for every pair.
+constexpr int RW_WARPS = 8, RW_CHUNK = 32;
+
+__host__ __device__ __forceinline__ int rows_pitch(int D) { return (D + 3) / 4 * 4 + 4; }   // an odd number of 16-byte pieces, or all lanes' reads clash
+template <int KPW>
+__host__ __device__ __forceinline__ size_t rows_smem(int D) {
+    const int Dp = (D + 3) / 4 * 4;
+    return sizeof(float) * ((size_t)2 * RW_CHUNK * rows_pitch(D) + (size_t)RW_WARPS * KPW * 2 * Dp + (size_t)RW_WARPS * RW_CHUNK * 2 * KPW);
+}
+
+template <typename T, int C, int KPW, bool DKV>
+__global__ void __launch_bounds__(RW_WARPS * 32)
+bwd_window_rows_kernel(BwdProblem p, int tiles) {
+    extern __shared__ __align__(16) float rw_smem[];
+    __shared__ float s_lse[RW_CHUNK], s_dvec[RW_CHUNK];
+    const int D = p.D, Dp = (D + 3) / 4 * 4, pitch = rows_pitch(D);
+    float *b1 = rw_smem, *b2 = b1 + RW_CHUNK * pitch, *av = b2 + RW_CHUNK * pitch, *spd = av + RW_WARPS * KPW * 2 * Dp;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = blockIdx.x % tiles, head = blockIdx.x / tiles, G = p.Hq / p.Hkv;
+    const int b = DKV ? head / p.Hkv : head / p.Hq, kvh = DKV ? head % p.Hkv : head % p.Hq / G;
+    const int n_outer = DKV ? p.Sk : p.Sq, o0 = tile * RW_WARPS * KPW, o1 = min(o0 + RW_WARPS * KPW, n_outer);
+    const T *A1 = static_cast<const T *>(DKV ? p.k : p.q) + (long long)head * n_outer * D;
+    const T *A2 = static_cast<const T *>(DKV ? p.v : p.dout) + (long long)head * n_outer * D;
+    for (int i = tid; i < RW_WARPS * KPW * Dp; i += RW_WARPS * 32) {
+        const int o = i / Dp, d = i % Dp;
+        const bool ok = o0 + o < o1 && d < D;
+        av[(o * 2) * Dp + d] = ok ? ldf(A1 + (long long)(o0 + o) * D + d) : 0.f;
+        av[(o * 2 + 1) * Dp + d] = ok ? ldf(A2 + (long long)(o0 + o) * D + d) : 0.f;
+    }
+    // what the block's vectors meet: rows [i0, i1) of each of the group's heads, or the keys of a stream of chunks
+    int i0 = 0, i1 = 0, steps;
+    KeyStream ks{};
+    if (DKV) {
+        i0 = max(0, o0 - p.causal_off);
+        i1 = o0 < p.sinks ? p.Sq : min(p.Sq, max(0, o1 - 1 - p.causal_off + p.window));
+        steps = i1 > i0 ? G * ((i1 - i0 + RW_CHUNK - 1) / RW_CHUNK) : 0;
+    } else {
+        ks = key_stream(o0 + p.causal_off, o1 - 1 + p.causal_off, p.Sk, p.window, p.sinks, RW_CHUNK);
+        steps = ks.n;
+    }
+    const int per_head = DKV && steps ? steps / G : 1;
+    float acc1[KPW][C], acc2[KPW][C], lse_o[KPW], dvec_o[KPW];
+#pragma unroll
+    for (int k = 0; k < KPW; ++k) {
+        const int o = o0 + warp * KPW + k;
+        lse_o[k] = !DKV && o < o1 ? p.lse[(long long)head * p.Sq + o] * kLog2e : 0.f;
+        dvec_o[k] = !DKV && o < o1 ? p.dvec[(long long)head * p.Sq + o] : 0.f;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc1[k][c] = acc2[k][c] = 0.f;
+    }
+    const float *mine = av + warp * KPW * 2 * Dp;
+    float *mp = spd + warp * RW_CHUNK * 2 * KPW;
+    for (int st = 0; st < steps; ++st) {
+        // the chunk: rows c0 .. c0 + cnt - 1 of two arrays
+        const int g = st / per_head;
+        const long long bh = DKV ? (long long)b * p.Hq + kvh * G + g : (long long)b * p.Hkv + kvh;
+        const int c0 = DKV ? i0 + (st - g * per_head) * RW_CHUNK : ks.tile(st) * RW_CHUNK;
+        const int n_inner = DKV ? p.Sq : p.Sk, cnt = min(RW_CHUNK, (DKV ? i1 : p.Sk) - c0);
+        const T *B1 = static_cast<const T *>(DKV ? p.q : p.k) + (bh * n_inner + c0) * D;
+        const T *B2 = static_cast<const T *>(DKV ? p.dout : p.v) + (bh * n_inner + c0) * D;
+        __syncthreads();   // the previous chunk is done with (and the vectors are there, first time)
+        for (int i = tid; i < RW_CHUNK * Dp; i += RW_WARPS * 32) {
+            const int r = i / Dp, d = i % Dp;
+            const bool ok = r < cnt && d < D;
+            b1[r * pitch + d] = ok ? ldf(B1 + (long long)r * D + d) : 0.f;
+            b2[r * pitch + d] = ok ? ldf(B2 + (long long)r * D + d) : 0.f;
+        }
+        if (DKV && tid < RW_CHUNK) {
+            s_lse[tid] = tid < cnt ? p.lse[bh * p.Sq + c0 + tid] * kLog2e : 0.f;
+            s_dvec[tid] = tid < cnt ? p.dvec[bh * p.Sq + c0 + tid] : 0.f;
+        }
+        __syncthreads();
+        float s[KPW], t[KPW];
+#pragma unroll
+        for (int k = 0; k < KPW; ++k) s[k] = t[k] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < Dp; d += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(b1 + lane * pitch + d);
+            const float4 y = *reinterpret_cast<const float4 *>(b2 + lane * pitch + d);
+#pragma unroll
+            for (int k = 0; k < KPW; ++k) {
+                const float4 u = *reinterpret_cast<const float4 *>(mine + 2 * k * Dp + d);
+                const float4 v = *reinterpret_cast<const float4 *>(mine + (2 * k + 1) * Dp + d);
+                s[k] = fmaf(x.x, u.x, s[k]); s[k] = fmaf(x.y, u.y, s[k]); s[k] = fmaf(x.z, u.z, s[k]); s[k] = fmaf(x.w, u.w, s[k]);
+                t[k] = fmaf(y.x, v.x, t[k]); t[k] = fmaf(y.y, v.y, t[k]); t[k] = fmaf(y.z, v.z, t[k]); t[k] = fmaf(y.w, v.w, t[k]);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < KPW; ++k) {
+            const int o = o0 + warp * KPW + k, key = DKV ? o : c0 + lane, pos = (DKV ? c0 + lane : o) + p.causal_off;
+            const bool sees = o < o1 && lane < cnt && key <= pos && (key > pos - p.window || key < p.sinks);
+            const float pr = sees ? ex2_approx(s[k] * p.scale_log2 - (DKV ? s_lse[lane] : lse_o[k])) : 0.f;
+            mp[lane * 2 * KPW + k] = sees ? pr * (t[k] - (DKV ? s_dvec[lane] : dvec_o[k])) : 0.f;
+            if (DKV) mp[lane * 2 * KPW + KPW + k] = pr;
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int r = 0; r < RW_CHUNK; ++r) {
+            float ds[KPW], pr[KPW], x[C], y[C];
+#pragma unroll
+            for (int k = 0; k < KPW; ++k) {
+                ds[k] = mp[r * 2 * KPW + k];
+                pr[k] = DKV ? mp[r * 2 * KPW + KPW + k] : 0.f;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const int d = lane + 32 * c;
+                x[c] = d < D ? b1[r * pitch + d] : 0.f;
+                y[c] = DKV && d < D ? b2[r * pitch + d] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < KPW; ++k)
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    acc1[k][c] = fmaf(ds[k], x[c], acc1[k][c]);
+                    if (DKV) acc2[k][c] = fmaf(pr[k], y[c], acc2[k][c]);
+                }
+        }
+    }
+    T *O1 = static_cast<T *>(DKV ? p.dk : p.dq) + (long long)head * n_outer * D;
+    T *O2 = static_cast<T *>(p.dv) + (long long)head * n_outer * D;
+#pragma unroll
+    for (int k = 0; k < KPW; ++k) {
+        const int o = o0 + warp * KPW + k;
+        if (o >= o1) break;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int d = lane + 32 * c;
+            if (d < D) {
+                O1[(long long)o * D + d] = from_f32<T>(acc1[k][c] * p.scale);
+                if (DKV) O2[(long long)o * D + d] = from_f32<T>(acc2[k][c]);
+            }
+        }
+    }
+}
+
+template <typename T, int C, int KPW, bool DKV>
+cudaError_t launch_rows_k(const BwdProblem &p, cudaStream_t s) {
+    const size_t smem = rows_smem<KPW>(p.D);
+    const cudaError_t e = set_max_dynamic_smem((const void *)bwd_window_rows_kernel<T, C, KPW, DKV>, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int tiles = ((DKV ? p.Sk : p.Sq) + RW_WARPS * KPW - 1) / (RW_WARPS * KPW);
+    const long long blocks = (long long)tiles * p.B * (DKV ? p.Hkv : p.Hq);
+    if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
+    bwd_window_rows_kernel<T, C, KPW, DKV><<<(unsigned)blocks, RW_WARPS * 32, smem, s>>>(p, tiles);
+    count_launches(1);
+    return cudaGetLastError();
+}
+template <typename T, bool DKV>
+cudaError_t launch_rows(const BwdProblem &p, int sm_count, cudaStream_t s) {
+    // four vectors to a warp where that leaves every SM two blocks
+    const long long vectors = (long long)p.B * (DKV ? (long long)p.Hkv * p.Sk : (long long)p.Hq * p.Sq);
+    const bool wide = vectors >= 2LL * sm_count * RW_WARPS * 4;
+    if (p.D <= 64) return wide ? launch_rows_k<T, 2, 4, DKV>(p, s) : launch_rows_k<T, 2, 1, DKV>(p, s);
+    if (p.D <= 128) return wide ? launch_rows_k<T, 4, 4, DKV>(p, s) : launch_rows_k<T, 4, 1, DKV>(p, s);
+    return wide ? launch_rows_k<T, 8, 4, DKV>(p, s) : launch_rows_k<T, 8, 1, DKV>(p, s);
+}
+template <typename T>
+cudaError_t launch_window_rows(const BwdProblem &p, cudaStream_t s) {
+    int sms = 0;
+    if (device_sm_count(&sms) != OSF_OK) return cudaErrorInvalidValue;
+    const cudaError_t e = launch_rows<T, true>(p, sms, s);
+    return e == cudaSuccess ? launch_rows<T, false>(p, sms, s) : e;
 }
 
 // ------------------------------------------------------------------ tensor-core version (bf16)
@@ -579,7 +746,8 @@ cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     if (attn_bwd_tc_supported(p)) return launch_attn_bwd_tc(p, s);
-    if (!p.window && attn_bwd_mma_supported(p)) return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
+    if (p.window) return p.dtype == OSF_BF16 ? launch_window_rows<__nv_bfloat16>(p, s) : launch_window_rows<float>(p, s);
+    if (attn_bwd_mma_supported(p)) return p.D == 64 ? launch_mma<64>(p, s) : launch_mma<128>(p, s);
     return p.dtype == OSF_BF16 ? launch_simt<__nv_bfloat16>(p, s) : launch_simt<float>(p, s);
 }
 
