@@ -247,31 +247,49 @@ __global__ void __launch_bounds__(256) bwd_dkdv_simt_kernel(BwdProblem p) {
 // float32, B=1 Hq=4 Hkv=2, 301 tokens of D=64, window 65: 264 us with a warp that reduces over its lanes for every pair.
 constexpr int RW_WARPS = 8, RW_CHUNK = 32;
 
-__host__ __device__ __forceinline__ int rows_pitch(int D) { return (D + 3) / 4 * 4 + 4; }   // an odd number of 16-byte pieces, or all lanes' reads clash
-template <int KPW>
-__host__ __device__ __forceinline__ size_t rows_smem(int D) {
-    const int Dp = (D + 3) / 4 * 4;
-    return sizeof(float) * ((size_t)2 * RW_CHUNK * rows_pitch(D) + (size_t)RW_WARPS * KPW * 2 * Dp + (size_t)RW_WARPS * RW_CHUNK * 2 * KPW);
+template <int C, int KPW>
+struct RowsCfg {
+    static constexpr int DP = 32 * C, PITCH = DP + 4;   // an odd number of 16-byte pieces: reads of 32 rows do not clash
+    static constexpr int B_FLOATS = RW_CHUNK * PITCH, A_FLOATS = RW_WARPS * KPW * 2 * DP, P_FLOATS = RW_WARPS * RW_CHUNK * 2 * KPW;
+    static constexpr size_t SMEM = sizeof(float) * (2 * B_FLOATS + A_FLOATS + P_FLOATS);
+};
+
+// Four channels from d on, zeros from D on.  vec: rows start on 16-byte (bfloat16: 8-byte) boundaries and D % 4 == 0.
+__device__ __forceinline__ float4 ld_four(const float *p, int d, int D, bool vec) {
+    if (vec) return d < D ? *reinterpret_cast<const float4 *>(p + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(d < D ? p[d] : 0.f, d + 1 < D ? p[d + 1] : 0.f, d + 2 < D ? p[d + 2] : 0.f, d + 3 < D ? p[d + 3] : 0.f);
+}
+__device__ __forceinline__ float4 ld_four(const __nv_bfloat16 *p, int d, int D, bool vec) {
+    if (vec) {
+        if (d >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
+        const uint2 v = *reinterpret_cast<const uint2 *>(p + d);
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+    return make_float4(d < D ? ldf(p + d) : 0.f, d + 1 < D ? ldf(p + d + 1) : 0.f, d + 2 < D ? ldf(p + d + 2) : 0.f,
+                       d + 3 < D ? ldf(p + d + 3) : 0.f);
 }
 
 template <typename T, int C, int KPW, bool DKV>
-__global__ void __launch_bounds__(RW_WARPS * 32)
-bwd_window_rows_kernel(BwdProblem p, int tiles) {
+__device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int tiles, bool vec) {
+    using R = RowsCfg<C, KPW>;
+    constexpr int PITCH = R::PITCH, DP = R::DP;
     extern __shared__ __align__(16) float rw_smem[];
     __shared__ float s_lse[RW_CHUNK], s_dvec[RW_CHUNK];
-    const int D = p.D, Dp = (D + 3) / 4 * 4, pitch = rows_pitch(D);
-    float *b1 = rw_smem, *b2 = b1 + RW_CHUNK * pitch, *av = b2 + RW_CHUNK * pitch, *spd = av + RW_WARPS * KPW * 2 * Dp;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x % tiles, head = blockIdx.x / tiles, G = p.Hq / p.Hkv;
+    float *b1 = rw_smem, *b2 = b1 + R::B_FLOATS, *av = b2 + R::B_FLOATS, *spd = av + R::A_FLOATS;
+    const int D = p.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tile = bid % tiles, head = bid / tiles, G = p.Hq / p.Hkv;
     const int b = DKV ? head / p.Hkv : head / p.Hq, kvh = DKV ? head % p.Hkv : head % p.Hq / G;
     const int n_outer = DKV ? p.Sk : p.Sq, o0 = tile * RW_WARPS * KPW, o1 = min(o0 + RW_WARPS * KPW, n_outer);
     const T *A1 = static_cast<const T *>(DKV ? p.k : p.q) + (long long)head * n_outer * D;
     const T *A2 = static_cast<const T *>(DKV ? p.v : p.dout) + (long long)head * n_outer * D;
-    for (int i = tid; i < RW_WARPS * KPW * Dp; i += RW_WARPS * 32) {
-        const int o = i / Dp, d = i % Dp;
-        const bool ok = o0 + o < o1 && d < D;
-        av[(o * 2) * Dp + d] = ok ? ldf(A1 + (long long)(o0 + o) * D + d) : 0.f;
-        av[(o * 2 + 1) * Dp + d] = ok ? ldf(A2 + (long long)(o0 + o) * D + d) : 0.f;
+#pragma unroll
+    for (int i = tid; i < RW_WARPS * KPW * DP / 4; i += RW_WARPS * 32) {
+        const int o = i / (DP / 4), d = i % (DP / 4) * 4;
+        const bool ok = o0 + o < o1;
+        const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+        *reinterpret_cast<float4 *>(av + (o * 2) * DP + d) = ok ? ld_four(A1 + (long long)(o0 + o) * D, d, D, vec) : z;
+        *reinterpret_cast<float4 *>(av + (o * 2 + 1) * DP + d) = ok ? ld_four(A2 + (long long)(o0 + o) * D, d, D, vec) : z;
     }
     // what the block's vectors meet: rows [i0, i1) of each of the group's heads, or the keys of a stream of chunks
     int i0 = 0, i1 = 0, steps;
@@ -285,48 +303,77 @@ bwd_window_rows_kernel(BwdProblem p, int tiles) {
         steps = ks.n;
     }
     const int per_head = DKV && steps ? steps / G : 1;
+    // chunk st: rows c0 .. c0 + cnt - 1 of head bh of the two arrays
+    auto chunk = [&](int st, long long &bh, int &c0, int &cnt) {
+        const int g = st / per_head;
+        bh = DKV ? (long long)b * p.Hq + kvh * G + g : (long long)b * p.Hkv + kvh;
+        c0 = DKV ? i0 + (st - g * per_head) * RW_CHUNK : ks.tile(st) * RW_CHUNK;
+        cnt = min(RW_CHUNK, (DKV ? i1 : p.Sk) - c0);
+    };
+    float4 n1[C], n2[C];   // the next chunk, on its way
+    float n_lse = 0.f;
+    auto fetch = [&](int st) {
+        long long bh;
+        int c0, cnt;
+        chunk(st, bh, c0, cnt);
+        const int n_inner = DKV ? p.Sq : p.Sk;
+        const T *B1 = static_cast<const T *>(DKV ? p.q : p.k) + (bh * n_inner + c0) * D;
+        const T *B2 = static_cast<const T *>(DKV ? p.dout : p.v) + (bh * n_inner + c0) * D;
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+            const int f = tid + 256 * e, r = f / (DP / 4), d = f % (DP / 4) * 4;
+            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            n1[e] = r < cnt ? ld_four(B1 + (long long)r * D, d, D, vec) : z;
+            n2[e] = r < cnt ? ld_four(B2 + (long long)r * D, d, D, vec) : z;
+        }
+        if (DKV && tid < 2 * RW_CHUNK) {
+            const int r = tid & (RW_CHUNK - 1);
+            n_lse = r >= cnt ? 0.f : tid < RW_CHUNK ? p.lse[bh * p.Sq + c0 + r] * kLog2e : p.dvec[bh * p.Sq + c0 + r];
+        }
+    };
     float acc1[KPW][C], acc2[KPW][C], lse_o[KPW], dvec_o[KPW];
 #pragma unroll
     for (int k = 0; k < KPW; ++k) {
         const int o = o0 + warp * KPW + k;
         lse_o[k] = !DKV && o < o1 ? p.lse[(long long)head * p.Sq + o] * kLog2e : 0.f;
-        dvec_o[k] = !DKV && o < o1 ? p.dvec[(long long)head * p.Sq + o] : 0.f;
 #pragma unroll
         for (int c = 0; c < C; ++c) acc1[k][c] = acc2[k][c] = 0.f;
     }
-    const float *mine = av + warp * KPW * 2 * Dp;
+    griddep_wait();   // launched as a dependent of the kernel that writes the row sums
+#pragma unroll
+    for (int k = 0; k < KPW; ++k) {
+        const int o = o0 + warp * KPW + k;
+        dvec_o[k] = !DKV && o < o1 ? p.dvec[(long long)head * p.Sq + o] : 0.f;
+    }
+    if (steps > 0) fetch(0);
+    const float *mine = av + warp * KPW * 2 * DP;
     float *mp = spd + warp * RW_CHUNK * 2 * KPW;
+    const int d_end = (D + 3) / 4 * 4;
     for (int st = 0; st < steps; ++st) {
-        // the chunk: rows c0 .. c0 + cnt - 1 of two arrays
-        const int g = st / per_head;
-        const long long bh = DKV ? (long long)b * p.Hq + kvh * G + g : (long long)b * p.Hkv + kvh;
-        const int c0 = DKV ? i0 + (st - g * per_head) * RW_CHUNK : ks.tile(st) * RW_CHUNK;
-        const int n_inner = DKV ? p.Sq : p.Sk, cnt = min(RW_CHUNK, (DKV ? i1 : p.Sk) - c0);
-        const T *B1 = static_cast<const T *>(DKV ? p.q : p.k) + (bh * n_inner + c0) * D;
-        const T *B2 = static_cast<const T *>(DKV ? p.dout : p.v) + (bh * n_inner + c0) * D;
+        long long bh;
+        int c0, cnt;
+        chunk(st, bh, c0, cnt);
         __syncthreads();   // the previous chunk is done with (and the vectors are there, first time)
-        for (int i = tid; i < RW_CHUNK * Dp; i += RW_WARPS * 32) {
-            const int r = i / Dp, d = i % Dp;
-            const bool ok = r < cnt && d < D;
-            b1[r * pitch + d] = ok ? ldf(B1 + (long long)r * D + d) : 0.f;
-            b2[r * pitch + d] = ok ? ldf(B2 + (long long)r * D + d) : 0.f;
+#pragma unroll
+        for (int e = 0; e < C; ++e) {
+            const int f = tid + 256 * e, r = f / (DP / 4), d = f % (DP / 4) * 4;
+            *reinterpret_cast<float4 *>(b1 + r * PITCH + d) = n1[e];
+            *reinterpret_cast<float4 *>(b2 + r * PITCH + d) = n2[e];
         }
-        if (DKV && tid < RW_CHUNK) {
-            s_lse[tid] = tid < cnt ? p.lse[bh * p.Sq + c0 + tid] * kLog2e : 0.f;
-            s_dvec[tid] = tid < cnt ? p.dvec[bh * p.Sq + c0 + tid] : 0.f;
-        }
+        if (DKV && tid < 2 * RW_CHUNK) (tid < RW_CHUNK ? s_lse : s_dvec)[tid & (RW_CHUNK - 1)] = n_lse;
         __syncthreads();
+        if (st + 1 < steps) fetch(st + 1);
         float s[KPW], t[KPW];
 #pragma unroll
         for (int k = 0; k < KPW; ++k) s[k] = t[k] = 0.f;
 #pragma unroll 4
-        for (int d = 0; d < Dp; d += 4) {
-            const float4 x = *reinterpret_cast<const float4 *>(b1 + lane * pitch + d);
-            const float4 y = *reinterpret_cast<const float4 *>(b2 + lane * pitch + d);
+        for (int d = 0; d < d_end; d += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(b1 + lane * PITCH + d);
+            const float4 y = *reinterpret_cast<const float4 *>(b2 + lane * PITCH + d);
 #pragma unroll
             for (int k = 0; k < KPW; ++k) {
-                const float4 u = *reinterpret_cast<const float4 *>(mine + 2 * k * Dp + d);
-                const float4 v = *reinterpret_cast<const float4 *>(mine + (2 * k + 1) * Dp + d);
+                const float4 u = *reinterpret_cast<const float4 *>(mine + 2 * k * DP + d);
+                const float4 v = *reinterpret_cast<const float4 *>(mine + (2 * k + 1) * DP + d);
                 s[k] = fmaf(x.x, u.x, s[k]); s[k] = fmaf(x.y, u.y, s[k]); s[k] = fmaf(x.z, u.z, s[k]); s[k] = fmaf(x.w, u.w, s[k]);
                 t[k] = fmaf(y.x, v.x, t[k]); t[k] = fmaf(y.y, v.y, t[k]); t[k] = fmaf(y.z, v.z, t[k]); t[k] = fmaf(y.w, v.w, t[k]);
             }
@@ -340,27 +387,31 @@ bwd_window_rows_kernel(BwdProblem p, int tiles) {
             if (DKV) mp[lane * 2 * KPW + KPW + k] = pr;
         }
         __syncwarp();
-#pragma unroll 4
+#pragma unroll 8
         for (int r = 0; r < RW_CHUNK; ++r) {
-            float ds[KPW], pr[KPW], x[C], y[C];
-#pragma unroll
-            for (int k = 0; k < KPW; ++k) {
-                ds[k] = mp[r * 2 * KPW + k];
-                pr[k] = DKV ? mp[r * 2 * KPW + KPW + k] : 0.f;
+            float ds[KPW], pr[KPW];
+            if constexpr (KPW == 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(mp + 8 * r);
+                ds[0] = a.x; ds[1] = a.y; ds[2] = a.z; ds[3] = a.w;
+                if (DKV) {
+                    const float4 q = *reinterpret_cast<const float4 *>(mp + 8 * r + 4);
+                    pr[0] = q.x; pr[1] = q.y; pr[2] = q.z; pr[3] = q.w;
+                }
+            } else {
+                ds[0] = mp[2 * r];
+                pr[0] = DKV ? mp[2 * r + 1] : 0.f;
             }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                const int d = lane + 32 * c;
-                x[c] = d < D ? b1[r * pitch + d] : 0.f;
-                y[c] = DKV && d < D ? b2[r * pitch + d] : 0.f;
-            }
+                const float x = b1[r * PITCH + lane + 32 * c];
 #pragma unroll
-            for (int k = 0; k < KPW; ++k)
+                for (int k = 0; k < KPW; ++k) acc1[k][c] = fmaf(ds[k], x, acc1[k][c]);
+                if (DKV) {
+                    const float y = b2[r * PITCH + lane + 32 * c];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    acc1[k][c] = fmaf(ds[k], x[c], acc1[k][c]);
-                    if (DKV) acc2[k][c] = fmaf(pr[k], y[c], acc2[k][c]);
+                    for (int k = 0; k < KPW; ++k) acc2[k][c] = fmaf(pr[k], y, acc2[k][c]);
                 }
+            }
         }
     }
     T *O1 = static_cast<T *>(DKV ? p.dk : p.dq) + (long long)head * n_outer * D;
@@ -380,33 +431,39 @@ bwd_window_rows_kernel(BwdProblem p, int tiles) {
     }
 }
 
-template <typename T, int C, int KPW, bool DKV>
-cudaError_t launch_rows_k(const BwdProblem &p, cudaStream_t s) {
-    const size_t smem = rows_smem<KPW>(p.D);
-    const cudaError_t e = set_max_dynamic_smem((const void *)bwd_window_rows_kernel<T, C, KPW, DKV>, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int tiles = ((DKV ? p.Sk : p.Sq) + RW_WARPS * KPW - 1) / (RW_WARPS * KPW);
-    const long long blocks = (long long)tiles * p.B * (DKV ? p.Hkv : p.Hq);
-    if (blocks >= (1LL << 31)) return cudaErrorInvalidValue;
-    bwd_window_rows_kernel<T, C, KPW, DKV><<<(unsigned)blocks, RW_WARPS * 32, smem, s>>>(p, tiles);
-    count_launches(1);
-    return cudaGetLastError();
+// One grid: the blocks of dK and dV, then those of dQ.
+template <typename T, int C, int KPW>
+__global__ void __launch_bounds__(RW_WARPS * 32)
+bwd_window_rows_kernel(BwdProblem p, unsigned kv_blocks, int kv_tiles, int q_tiles, int vec) {
+    if (blockIdx.x < kv_blocks) window_rows<T, C, KPW, true>(p, blockIdx.x, kv_tiles, vec);
+    else window_rows<T, C, KPW, false>(p, blockIdx.x - kv_blocks, q_tiles, vec);
 }
-template <typename T, bool DKV>
-cudaError_t launch_rows(const BwdProblem &p, int sm_count, cudaStream_t s) {
-    // four vectors to a warp where that leaves every SM two blocks
-    const long long vectors = (long long)p.B * (DKV ? (long long)p.Hkv * p.Sk : (long long)p.Hq * p.Sq);
-    const bool wide = vectors >= 2LL * sm_count * RW_WARPS * 4;
-    if (p.D <= 64) return wide ? launch_rows_k<T, 2, 4, DKV>(p, s) : launch_rows_k<T, 2, 1, DKV>(p, s);
-    if (p.D <= 128) return wide ? launch_rows_k<T, 4, 4, DKV>(p, s) : launch_rows_k<T, 4, 1, DKV>(p, s);
-    return wide ? launch_rows_k<T, 8, 4, DKV>(p, s) : launch_rows_k<T, 8, 1, DKV>(p, s);
+
+template <typename T, int C, int KPW>
+cudaError_t launch_rows_k(const BwdProblem &p, cudaStream_t s) {
+    constexpr size_t smem = RowsCfg<C, KPW>::SMEM;
+    const cudaError_t e = set_max_dynamic_smem((const void *)bwd_window_rows_kernel<T, C, KPW>, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int per = RW_WARPS * KPW, kv_tiles = (p.Sk + per - 1) / per, q_tiles = (p.Sq + per - 1) / per;
+    const long long kv = (long long)kv_tiles * p.B * p.Hkv, all = kv + (long long)q_tiles * p.B * p.Hq;
+    if (all >= (1LL << 31)) return cudaErrorInvalidValue;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) |
+                         reinterpret_cast<uintptr_t>(p.dout);
+    const int vec = p.D % 4 == 0 && at % (4 * sizeof(T)) == 0;
+    count_launches(1);
+    return launch_dependent(bwd_window_rows_kernel<T, C, KPW>, dim3((unsigned)all), dim3(RW_WARPS * 32), smem, s, p, (unsigned)kv,
+                            kv_tiles, q_tiles, vec);
 }
 template <typename T>
 cudaError_t launch_window_rows(const BwdProblem &p, cudaStream_t s) {
     int sms = 0;
     if (device_sm_count(&sms) != OSF_OK) return cudaErrorInvalidValue;
-    const cudaError_t e = launch_rows<T, true>(p, sms, s);
-    return e == cudaSuccess ? launch_rows<T, false>(p, sms, s) : e;
+    // four vectors to a warp where that leaves every SM two blocks
+    const long long vectors = (long long)p.B * ((long long)p.Hkv * p.Sk + (long long)p.Hq * p.Sq);
+    const bool wide = vectors >= 2LL * sms * RW_WARPS * 4;
+    if (p.D <= 64) return wide ? launch_rows_k<T, 2, 4>(p, s) : launch_rows_k<T, 2, 1>(p, s);
+    if (p.D <= 128) return wide ? launch_rows_k<T, 4, 4>(p, s) : launch_rows_k<T, 4, 1>(p, s);
+    return wide ? launch_rows_k<T, 8, 4>(p, s) : launch_rows_k<T, 8, 1>(p, s);
 }
 
 // ------------------------------------------------------------------ tensor-core version (bf16)
