@@ -172,11 +172,13 @@ int osf_attn_fwd_gqa_ex(const void *Q, const void *K, const void *V, void *O, in
  *     j <= p  and  (p - j < window  or  j < sinks).
  * Key tiles that no row sees are not read: the work grows with the window, not with Sk.
  * window >= 1 (1: a row sees itself and the sinks), sinks >= 0.  A window that hides nothing (window + sinks >= Sk) is
- * OSF_MASK_BOTTOM_RIGHT of osf_attn_fwd_gqa_ex, by the same kernels.
+ * OSF_MASK_BOTTOM_RIGHT of osf_attn_fwd_gqa_ex, by the same kernels (bfloat16 rows of 32 or 96 channels: by the windowed ones).
+ * K and V of keys that no row sees are not read, or (in a tile of 32 .. 128 keys that some row sees a part of) of no effect as
+ * long as V is finite.
  * strides, scale, lse, errors: as there.  A row that sees no key (p < 0, or Sk == 0) gets O = 0 and lse = -inf.
  * workspace: osf_attn_window_workspace_bytes with the same sizes, window and sinks.
  * Sq or Sk >= 2^29: OSF_ERR_UNSUPPORTED.
- * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores, CUDA cores.
+ * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores (bfloat16 with D 32 and 96 too), CUDA cores.
  */
 int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O, int dtype,
                             int B, int Hq, int Hkv, int Sq, int Sk, int D, const long long *strides,

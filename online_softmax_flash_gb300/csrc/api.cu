@@ -716,9 +716,10 @@ int osf_attn_bwd_gqa(const void *Q, const void *K, const void *V, const void *O,
 }
 
 // ------------------------------------------------------------------ a window with sinks
-// The checks of a windowed problem: those of a bottom-right one, then the window.  One that hides nothing is dropped.
+// The checks of a windowed problem: those of a bottom-right one, then the window.  One that hides nothing is dropped, but where
+// the windowed kernels are the faster ones: `keep` (the window then is the whole sequence).
 static int check_window(const void *Q, const void *K, const void *V, void *O, int dtype, int B, int Hq, int Hkv, int Sq,
-                        int Sk, int D, const long long *strides, int window, int sinks, float scale, float *lse,
+                        int Sk, int D, const long long *strides, int window, int sinks, float scale, float *lse, bool keep,
                         AttnProblem &p, bool &empty) {
     empty = false;
     if (window < 1 || sinks < 0) return OSF_ERR_INVALID;
@@ -727,14 +728,20 @@ static int check_window(const void *Q, const void *K, const void *V, void *O, in
     // kernels add lengths and the window in ints
     if (Sq >= (1 << 29) || Sk >= (1 << 29)) return OSF_ERR_UNSUPPORTED;
     // the last row sees the most hidden keys: those between the sinks and its window
-    if ((long long)window + sinks < Sk) {
+    const bool hides = (long long)window + sinks < Sk;
+    if (hides || keep) {
         p.causal = 1;
         p.causal_off = Sk - Sq;
-        p.window = window;
-        p.sinks = sinks;
+        p.window = hides ? window : Sk;
+        p.sinks = hides ? sinks : 0;
     }
     return OSF_OK;
 }
+// bfloat16 rows of 32 and 96 channels run on the tensor cores with a window, and on the CUDA cores without one.
+static bool keep_fwd_window(int dtype, int D) { return dtype == OSF_BF16 && (D == 32 || D == 96); }
+// The backward pass on the CUDA cores: chunks of 32 with a window, a warp per row without one.
+static bool keep_bwd_window(int dtype, int D) { return !(dtype == OSF_BF16 && (D == 64 || D == 128)); }
+static bool window_tc(int dtype, int D) { return dtype == OSF_BF16 && (D == 32 || D == 64 || D == 96 || D == 128); }
 
 int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
                                     size_t *bytes) {
@@ -744,13 +751,13 @@ int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, i
     bool empty;
     const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
     const int st = check_window(ph, ph, ph, reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, Sk, D,
-                                nullptr, window, sinks, 0.f, nullptr, p, empty);
+                                nullptr, window, sinks, 0.f, nullptr, keep_fwd_window(dtype, D), p, empty);
     if (st != OSF_OK || empty) return st;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     // the largest of the possible paths' needs (alignment decides the path at call time)
     size_t need = path_workspace(p, Path::Simt, plan_splits(p, Path::Simt, dev->sm_count, 0));
-    if (Sq > 1 && ((dtype == OSF_BF16 && (D == 64 || D == 128)) || (dtype == OSF_F32 && D == 64)))
+    if (Sq > 1 && (window_tc(dtype, D) || (dtype == OSF_F32 && D == 64)))
         need = std::max(need, path_workspace(p, Path::TensorCore, plan_splits(p, Path::TensorCore, dev->sm_count, 0)));
     if (dtype == OSF_BF16 && (long long)(Hq / Hkv) * Sq <= 16)
         need = std::max(need, path_workspace(p, Path::Decode, plan_splits(p, Path::Decode, dev->sm_count, 0)));
@@ -763,7 +770,8 @@ int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O
                             void *workspace, size_t workspace_bytes, osf_stream stream) {
     AttnProblem p;
     bool empty;
-    int st = check_window(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, window, sinks, scale, lse, p, empty);
+    int st = check_window(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, window, sinks, scale, lse, keep_fwd_window(dtype, D),
+                          p, empty);
     if (st != OSF_OK || B == 0 || Sq == 0) return st;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
@@ -774,9 +782,10 @@ int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O
             sd[i] = strides[i];
             sd[9 + i] = strides[9 + i];
         }
-        st = check_window(Q, Q, Q, O, dtype, B, Hq, Hkv, Sq, 1, D, strides ? sd : nullptr, window, sinks, scale, lse, p, empty);
+        st = check_window(Q, Q, Q, O, dtype, B, Hq, Hkv, Sq, 1, D, strides ? sd : nullptr, window, sinks, scale, lse, false,
+                          p, empty);
         if (st != OSF_OK) return st;
-        p.Sk = p.causal = 0;
+        p.Sk = p.causal = p.window = 0;
         return run_gqa(p, Path::Simt, nullptr, 0, 1, dev, (cudaStream_t)stream);
     }
     const Path path = choose_path(p, Q, K, V, O);
@@ -792,14 +801,15 @@ struct BwdWindowLayout {
 static BwdWindowLayout bwd_window_layout(const AttnProblem &p, int sm_count) {
     BwdWindowLayout L;
     L.rows = align256((size_t)p.B * p.Hq * p.Sq * sizeof(float));
-    if (p.dtype != OSF_BF16 || (p.D != 64 && p.D != 128)) return L;
+    if (!window_tc(p.dtype, p.D)) return L;
     L.slots = bwd_window_slots(p.Sk, p.window, p.sinks);
     L.parts = bwd_window_sink_parts(p.B, p.Hkv, p.Sq, p.Sk, p.window, p.sinks, sm_count);
     const size_t tile = (size_t)128 * 128 * 2, per_head = (size_t)L.slots * (((size_t)p.Sq + 127) / 128) * tile;
     const size_t cap = (size_t)16 << 30, heads = (size_t)p.B * p.Hq;
     if (per_head <= cap / heads) L.ds = per_head * heads;
     if (L.parts > 1)
-        L.sink = (size_t)bwd_window_sink_tiles(p.Sk, p.sinks) * L.parts * p.B * p.Hkv * 2 * 128 * p.D * sizeof(float);
+        L.sink = (size_t)bwd_window_sink_tiles(p.Sk, p.sinks) * L.parts * p.B * p.Hkv * 2 * 128 * (p.D <= 64 ? 64 : 128) *
+                 sizeof(float);
     return L;
 }
 
@@ -811,7 +821,7 @@ int osf_attn_bwd_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int S
     bool empty;
     const void *ph = reinterpret_cast<const void *>(uintptr_t(1) << 40);
     const int st = check_window(ph, ph, ph, reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, Sk, D,
-                                nullptr, window, sinks, 0.f, nullptr, p, empty);
+                                nullptr, window, sinks, 0.f, nullptr, keep_bwd_window(dtype, D), p, empty);
     if (st != OSF_OK || empty) return st;
     if (!p.window) return osf_attn_bwd_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, bytes);
     DeviceInfo *dev;
@@ -826,7 +836,8 @@ int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const v
                             int window, int sinks, float scale, void *workspace, size_t workspace_bytes, osf_stream stream) {
     AttnProblem p;
     bool empty;
-    const int st = check_window(Q, K, V, dQ, dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, window, sinks, scale, nullptr, p, empty);
+    const int st = check_window(Q, K, V, dQ, dtype, B, Hq, Hkv, Sq, Sk, D, nullptr, window, sinks, scale, nullptr,
+                                keep_bwd_window(dtype, D), p, empty);
     if (st != OSF_OK) return st;
     if (empty) {   // no rows, or no keys: what gradients there are are zero
         const size_t es = elem_size(dtype), nq = (size_t)B * Hq * Sq * D * es, nk = (size_t)B * Hkv * Sk * D * es;
@@ -850,8 +861,8 @@ int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const v
     if (!workspace || workspace_bytes < need) return OSF_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & (L.ds + L.sink ? 127u : 3u)) != 0) return OSF_ERR_INVALID;
     char *at = static_cast<char *>(workspace);
-    b.window = window;
-    b.sinks = sinks;
+    b.window = p.window;
+    b.sinks = p.sinks;
     b.dvec = reinterpret_cast<float *>(at);
     b.sink_parts = L.parts;
     b.ds_slots = L.slots;

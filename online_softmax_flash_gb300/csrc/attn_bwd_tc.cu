@@ -168,7 +168,8 @@ __device__ __forceinline__ void init_bars(BtBars &bars, volatile int &abort_flag
 // ====================================================================== dQ
 // The two bodies below run as one grid (bwd_tc_kernel): CTA `bid` of each.  The tensor maps are
 // the kernel's __grid_constant__ parameters, passed by reference so TMA sees their addresses.
-// WIN: a window with sinks (BwdProblem::window).
+// WIN: a window with sinks (BwdProblem::window); rows may then have fewer channels than D (p.D, a multiple of 32), the rest of
+// the tiles being zeros.
 template <int D, bool WIN>
 __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtensorMap &mg, const CUtensorMap &mk,
                                             const CUtensorMap &mv, const BwdProblem &p, unsigned bid) {
@@ -207,15 +208,15 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
         // ------------------------------------------------------------ TMA: Q, dO; then K_j V_j
         bool ok = true;
         mbar_expect_tx(smem_u32(&bars.a_full), 2 * C::TILE);
-        tma_load_5d(sQ, &mq, smem_u32(&bars.a_full), 0, q0, 0, hq, b);
-        tma_load_5d(sG, &mg, smem_u32(&bars.a_full), 0, q0, 0, hq, b);
+        tma_load_tile<D>(sQ, &mq, smem_u32(&bars.a_full), q0, hq, b, WIN && p.D != D);
+        tma_load_tile<D>(sG, &mg, smem_u32(&bars.a_full), q0, hq, b, WIN && p.D != D);
         for (int m = 0; m < 2 * n && ok; ++m) {
             const int st = m % C::RING;
             ok = mbar_wait(smem_u32(&bars.empty[st]), ((m / C::RING) & 1) ^ 1, &abort_flag);
             if (!ok) break;
             mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
-            tma_load_5d(sRing + st * C::TILE, (m & 1) ? &mv : &mk, smem_u32(&bars.full[st]), 0, key_of(m >> 1), 0, kvh,
-                        b);
+            tma_load_tile<D>(sRing + st * C::TILE, (m & 1) ? &mv : &mk, smem_u32(&bars.full[st]), key_of(m >> 1), kvh, b,
+                             WIN && p.D != D);
         }
         if (!ok) {
             bt_timeout(&abort_flag, p.status);
@@ -374,11 +375,11 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
             if (!have) bt_timeout(&abort_flag, p.status);
             tc_fence_after();
         }
-        __nv_bfloat16 *dq = static_cast<__nv_bfloat16 *>(p.dq) + (row_ok ? grow : 0) * D;
+        __nv_bfloat16 *dq = static_cast<__nv_bfloat16 *>(p.dq) + (row_ok ? grow : 0) * (WIN ? p.D : D);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c) {
             const int cc = h * (D / 64) + c;   // 32-column chunk of dQ
-            tmem_to_bf16(tQ + lane_off + cc * 32, have, p.scale, row_ok, dq + cc * 32);
+            tmem_to_bf16(tQ + lane_off + cc * 32, have, p.scale, row_ok && (!WIN || cc * 32 < p.D), dq + cc * 32);
         }
     }
     tc_fence_before();
@@ -455,8 +456,8 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
         // ------------------------------------------------------------ TMA: K, V; then Q_m dO_m
         bool ok = true;
         mbar_expect_tx(smem_u32(&bars.a_full), 2 * C::TILE);
-        tma_load_5d(sK, &mk, smem_u32(&bars.a_full), 0, key0, 0, kvh, b);
-        tma_load_5d(sV, &mv, smem_u32(&bars.a_full), 0, key0, 0, kvh, b);
+        tma_load_tile<D>(sK, &mk, smem_u32(&bars.a_full), key0, kvh, b, WIN && p.D != D);
+        tma_load_tile<D>(sV, &mv, smem_u32(&bars.a_full), key0, kvh, b, WIN && p.D != D);
         for (int m = 0; m < 2 * n && ok; ++m) {
             const int st = m % C::RING;
             ok = mbar_wait(smem_u32(&bars.empty[st]), ((m / C::RING) & 1) ^ 1, &abort_flag);
@@ -465,8 +466,9 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
             step_at(m >> 1, hq, qt);
             mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
             // Q and dO tiles are read again by the CTAs of the other key tiles: keep them in L2
-            tma_load_5d_hint(sRing + st * C::TILE, (m & 1) ? &mg : &mq, smem_u32(&bars.full[st]), 0, qt * TB, 0, hq, b,
-                             l2_policy_evict_last());
+            const CUtensorMap *map = (m & 1) ? &mg : &mq;
+            if (WIN && p.D != D) tma_load_tile<D>(sRing + st * C::TILE, map, smem_u32(&bars.full[st]), qt * TB, hq, b, true);
+            else tma_load_5d_hint(sRing + st * C::TILE, map, smem_u32(&bars.full[st]), 0, qt * TB, 0, hq, b, l2_policy_evict_last());
         }
         if (!ok) {
             bt_timeout(&abort_flag, p.status);
@@ -703,11 +705,11 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
             }
         } else {
         const long long gk = (long long)bk * p.Sk + (key_ok ? key : 0);
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(h ? p.dv : p.dk) + gk * D;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(h ? p.dv : p.dk) + gk * (WIN ? p.D : D);
         const uint32_t src = (h ? tV : tK) + lane_off;
         const float sc = h ? 1.f : p.scale;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) tmem_to_bf16(src + c * 32, have, sc, key_ok, out + c * 32);
+        for (int c = 0; c < D / 32; ++c) tmem_to_bf16(src + c * 32, have, sc, key_ok && (!WIN || c * 32 < p.D), out + c * 32);
         }
     }
     tc_fence_before();
@@ -732,13 +734,13 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
 
 // dK and dV of the keys in tiles that hold sinks: the parts' sums, added in the order of the parts.  One thread per four
 // channels of a key: gridDim = (keys of the tiles * D / 4 / 256, b * kv head, dK | dV).
-__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdProblem p) {
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdProblem p, int D) {   // D: channels of a sum
     griddep_wait();
-    const int per = p.D / 4, i = blockIdx.x * 256 + threadIdx.x;
+    const int per = D / 4, i = blockIdx.x * 256 + threadIdx.x;
     const int key = i / per, c = i % per * 4, BK = gridDim.y, bk = blockIdx.y, h = blockIdx.z;
-    if (key >= p.Sk) return;
-    const size_t part = (size_t)BK * 2 * TB * p.D;
-    const float *src = p.sink_acc + (((size_t)(key / TB) * p.sink_parts * BK + bk) * 2 + h) * TB * p.D + (size_t)(key % TB) * p.D + c;
+    if (key >= p.Sk || c >= p.D) return;
+    const size_t part = (size_t)BK * 2 * TB * D;
+    const float *src = p.sink_acc + (((size_t)(key / TB) * p.sink_parts * BK + bk) * 2 + h) * TB * D + (size_t)(key % TB) * D + c;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int s = 0; s < p.sink_parts; ++s) {
@@ -872,7 +874,7 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
                                          WIN ? (int)(((long long)(bh + h) * (p.ds_ld / TB) + q0 / TB) * p.ds_slots + j)
                                              : (int)(((long long)(bh + h) * (p.ds_rows / TB) + j) * (p.ds_ld / TB) + q0 / TB),
                                          l2_policy_evict_first());
-                    else tma_load_5d(dst, &mk, smem_u32(&full[st]), 0, (WIN ? ks.tile(j) : j) * TB, 0, kvh, b);
+                    else tma_load_tile<D>(dst, &mk, smem_u32(&full[st]), (WIN ? ks.tile(j) : j) * TB, kvh, b, WIN && p.D != D);
                 }
             }
         }
@@ -946,10 +948,10 @@ bwd_dq_gemm_kernel(const __grid_constant__ CUtensorMap mds, const __grid_constan
             }
             for (int h = 0; h < hp; ++h) {
                 __nv_bfloat16 *dq =
-                    static_cast<__nv_bfloat16 *>(p.dq) + ((long long)(bh + h) * p.Sq + (row_ok ? row : 0)) * D;
+                    static_cast<__nv_bfloat16 *>(p.dq) + ((long long)(bh + h) * p.Sq + (row_ok ? row : 0)) * (WIN ? p.D : D);
                 const uint32_t src = tmem + (uint32_t)((buf * 2 + h) * D) + lane_off;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) tmem_to_bf16(src + c * 32, have, p.scale, row_ok, dq + c * 32);
+                for (int c = 0; c < D / 32; ++c) tmem_to_bf16(src + c * 32, have, p.scale, row_ok && (!WIN || c * 32 < p.D), dq + c * 32);
             }
             if (n > 0) {
                 tc_fence_before();
@@ -973,12 +975,13 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
     using C = BtCfg<D>;
     const cudaError_t attr_err = set_max_dynamic_smem((const void *)bwd_tc_kernel<D, WIN>, (int)C::SMEM_BYTES);
     if (attr_err != cudaSuccess) return attr_err;
-    const long long qs = (long long)p.Sq * D, ks = (long long)p.Sk * D;
+    const int pd = WIN ? p.D : D;
+    const long long qs = (long long)p.Sq * pd, ks = (long long)p.Sk * pd;
     CUtensorMap mq, mg, mk, mv;
-    if (!make_bf16_tile_map_strided(&mq, p.q, D, p.Sq, p.Hq, p.B, D, qs, qs * p.Hq, TB) ||
-        !make_bf16_tile_map_strided(&mg, p.dout, D, p.Sq, p.Hq, p.B, D, qs, qs * p.Hq, TB) ||
-        !make_bf16_tile_map_strided(&mk, p.k, D, p.Sk, p.Hkv, p.B, D, ks, ks * p.Hkv, TB) ||
-        !make_bf16_tile_map_strided(&mv, p.v, D, p.Sk, p.Hkv, p.B, D, ks, ks * p.Hkv, TB))
+    if (!make_bf16_rows_map(&mq, p.q, pd, p.Sq, p.Hq, p.B, pd, qs, qs * p.Hq, TB) ||
+        !make_bf16_rows_map(&mg, p.dout, pd, p.Sq, p.Hq, p.B, pd, qs, qs * p.Hq, TB) ||
+        !make_bf16_rows_map(&mk, p.k, pd, p.Sk, p.Hkv, p.B, pd, ks, ks * p.Hkv, TB) ||
+        !make_bf16_rows_map(&mv, p.v, pd, p.Sk, p.Hkv, p.B, pd, ks, ks * p.Hkv, TB))
         return cudaErrorInvalidValue;
     const int sink_tiles = WIN ? bwd_window_sink_tiles(p.Sk, p.sinks) : 0;
     const unsigned nkv = (unsigned)((p.Sk + TB - 1) / TB + (WIN ? sink_tiles * (p.sink_parts - 1) : 0)) * (unsigned)(p.B * p.Hkv);
@@ -988,7 +991,7 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
         if (!WIN || sink_tiles == 0 || p.sink_parts == 1) return cudaSuccess;
         const dim3 g((unsigned)(((long long)sink_tiles * TB * D / 4 + 255) / 256), (unsigned)(p.B * p.Hkv), 2);
         count_launches(1);
-        return launch_dependent(bwd_sink_sum_kernel, g, dim3(256), 0, s, p);
+        return launch_dependent(bwd_sink_sum_kernel, g, dim3(256), 0, s, p, D);
     };
     if (!p.ds) {
         // dK/dV and dQ CTAs in one grid
@@ -1026,7 +1029,7 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
 }  // namespace
 
 bool attn_bwd_tc_supported(const BwdProblem &p) {
-    if (p.dtype != OSF_BF16 || (p.D != 64 && p.D != 128)) return false;
+    if (p.dtype != OSF_BF16 || !(p.D == 64 || p.D == 128 || (p.window && (p.D == 32 || p.D == 96)))) return false;
     const uintptr_t a = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) |
                         reinterpret_cast<uintptr_t>(p.v) | reinterpret_cast<uintptr_t>(p.dout) |
                         reinterpret_cast<uintptr_t>(p.dq) | reinterpret_cast<uintptr_t>(p.dk) |
@@ -1040,7 +1043,7 @@ bool attn_bwd_tc_supported(const BwdProblem &p) {
 }
 
 cudaError_t launch_attn_bwd_tc(const BwdProblem &p, cudaStream_t s) {
-    if (p.window) return p.D == 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s);
+    if (p.window) return p.D <= 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s);
     return p.D == 64 ? launch_t<64, false>(p, s) : launch_t<128, false>(p, s);
 }
 

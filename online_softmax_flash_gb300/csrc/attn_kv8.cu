@@ -1,7 +1,7 @@
 // Attention over the paged 8-bit K/V cache (format: kv8.cuh): the last Sq tokens of each sequence against it, with or
 // without a window and sinks.
 //
-// General kernel (any D that is a multiple of 32, float32 or bfloat16 queries): a CTA takes up to 4 query rows of one (b, kv
+// General kernel (float32 queries, or D above 128): a CTA takes up to 4 query rows of one (b, kv
 // head) and a part of the keys that they see; a warp copies the rows of 32 keys to shared memory, takes a key per lane
 // (its whole dot product with the rows), then a channel of every 32 per lane.
 #include "kv8.cuh"
@@ -185,7 +185,8 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 
 
 // ============================================================================ tensor-core kernel
-// bfloat16 queries, D 64 or 128.  The codes go from memory to the tensor cores as they are: TMA copies pages into shared
+// bfloat16 queries, D up to 128 (the template's D is 64 or 128: rows of 32 and 96 channels are filled up with zeros on their
+// way into shared memory).  The codes go from memory to the tensor cores as they are: TMA copies pages into shared
 // memory, and tcgen05.mma (kind::f8f6f4) takes both products' large operands from there,
 //   S^T[128 tokens x columns]   = K[128 x D] . Q parts^T,      O^T[D x columns] += V^T[D x 128] . P parts[128 x columns],
 // so no thread touches a code but at a sequence's edges.  The small operands are sums of e4m3 parts, one column of the
@@ -574,13 +575,13 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         while (live && walk_next<NR>(kp, row_blocks, flat, w)) {
             // ------------------------------------------------------------ Q parts: a warp per row
             for (int r = warp; r < NR; r += 4 * C::GROUPS) {
-                constexpr int E = D / 32;   // channels E * lane ..
+                constexpr int E = D / 32;   // channels E * lane .., zeros from p.D on
                 const int gr = w.r0 + r;
                 float x[E], mx = 0.f;
                 bool bad = false;
 #pragma unroll
                 for (int e = 0; e < E; ++e) x[e] = 0.f;
-                if (r < w.rows) {
+                if (r < w.rows && E * lane < p.D) {
                     const __nv_bfloat16 *Q = static_cast<const __nv_bfloat16 *>(p.q) +
                                              q_at(p, w.b, w.kvh * G + gr / p.Sq, gr % p.Sq) + E * lane;
                     if (q_vec) {
@@ -901,8 +902,9 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                     if (nan & 4u) A.z = NAN;
                     if (nan & 8u) A.w = NAN;
                 }
-                if (w.whole) write_row(p, w.b, w.kvh * G + gr / p.Sq, gr % p.Sq, c4, A, M, L);
-                else {
+                if (w.whole) {
+                    if (c4 < p.D) write_row(p, w.b, w.kvh * G + gr / p.Sq, gr % p.Sq, c4, A, M, L);
+                } else {
                     *reinterpret_cast<float4 *>(kp.part + (slot * NR + r) * D + c4) = A;
                     if (c4 == 0) kp.part_ml[slot * NR + r] = make_float2(M, L);
                 }
@@ -944,6 +946,7 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnProblem k
     constexpr int KG = 8;   // pieces whose states are loaded together
     for (int x = threadIdx.x; x < rows * (D / 4); x += blockDim.x) {
         const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
+        if (c >= p.D) continue;
         float M = -INFINITY, L = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int k0 = c0; k0 <= c1; k0 += KG) {
@@ -989,7 +992,7 @@ size_t round256(size_t x) { return (x + 255) & ~size_t(255); }
 }  // namespace
 
 static bool use_tc(const AttnProblem &p) {
-    return p.dtype == OSF_BF16 && (p.D == 64 || p.D == 128) && p.Sk > 0 && tensor_map_encoder() != nullptr;
+    return p.dtype == OSF_BF16 && p.D <= 128 && p.Sk > 0 && tensor_map_encoder() != nullptr;
 }
 
 // Launch shape of the tensor-core kernel.  Whole items, a CTA each, need one launch and no join; cut, all tiles are shared by
@@ -1022,7 +1025,7 @@ size_t kv8_attn_partial_bytes(const Kv8AttnProblem &kp, int sm_count) {
     if (use_tc(p)) {
         const TcPlan t = tc_plan(p, sm_count);
         const size_t rows = 2 * (size_t)t.grid * t.nr;
-        return t.flat ? round256(rows * p.D * sizeof(float)) + round256(rows * sizeof(float2)) : 0;
+        return t.flat ? round256(rows * (p.D <= 64 ? 64 : 128) * sizeof(float)) + round256(rows * sizeof(float2)) : 0;
     }
     const int splits = general_splits(p, sm_count);
     const size_t rows = (size_t)splits * p.B * p.Hq * p.Sq;
@@ -1037,7 +1040,7 @@ static cudaError_t launch_tc_t(Kv8AttnProblem kp, const TcPlan &t, char *partial
     if (e != cudaSuccess) return e;
     CUtensorMap m;
     const long long rows = (long long)kp.c.n_pages * 2 * kp.c.Hkv * kp.c.P;
-    if (!make_u8_rows_map(&m, kp.c.pages, D, rows, (uint32_t)kp.c.P)) return cudaErrorInvalidValue;
+    if (!make_u8_rows_map(&m, kp.c.pages, p.D, D, rows, (uint32_t)kp.c.P)) return cudaErrorInvalidValue;
     kp.part = reinterpret_cast<float *>(partials);
     kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * NR * D * sizeof(float)));
     const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 1) == 0;
@@ -1057,7 +1060,7 @@ cudaError_t launch_attn_kv8(const Kv8AttnProblem &kp0, void *partials, int sm_co
     char *at = static_cast<char *>(partials);
     if (use_tc(p)) {
         const TcPlan t = tc_plan(p, sm_count);
-        if (p.D == 64)
+        if (p.D <= 64)
             return t.nr == 4 ? launch_tc_t<64, 4>(kp, t, at, s) : t.nr == 8 ? launch_tc_t<64, 8>(kp, t, at, s) : launch_tc_t<64, 16>(kp, t, at, s);
         return t.nr == 4 ? launch_tc_t<128, 4>(kp, t, at, s) : t.nr == 8 ? launch_tc_t<128, 8>(kp, t, at, s) : launch_tc_t<128, 16>(kp, t, at, s);
     }

@@ -205,7 +205,8 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
 // MERGE (key splits, one item per CTA): the CTAs of a thread-block cluster run the splits of one
 // item and merge their results through distributed shared memory at the end, instead of writing
 // partial states for a separate combine kernel.
-// WIN: a window with sinks (AttnProblem::window).
+// WIN: a window with sinks (AttnProblem::window); rows may then have fewer channels than D (p.D, a multiple of 32), the rest of
+// the tiles being zeros.
 template <int D, bool X3, bool MERGE, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -291,8 +292,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 #pragma unroll
                 for (int part = 0; part < C::QP; ++part)
                     for (int t = 0; t < w.ntiles; ++t)
-                        tma_load_5d(sQ + (2 * part + t) * C::TILE, part == 0 ? &mq : part == 1 ? &mqm : &mql,
-                                    smem_u32(&bars.q_full), 0, w.q0 + t * BM, 0, w.hq, w.b);
+                        tma_load_tile<D>(sQ + (2 * part + t) * C::TILE, part == 0 ? &mq : part == 1 ? &mqm : &mql,
+                                         smem_u32(&bars.q_full), w.q0 + t * BM, w.hq, w.b, WIN && p.D != D);
             }
             for (int j = 0; j < w.n_kv && ok; ++j) {
 #pragma unroll
@@ -303,8 +304,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (!ok) break;
                     mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
                     const CUtensorMap *mp = part == 0 ? map : (part == 2 || odd) ? map_lo : &mkm;
-                    tma_load_5d(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), 0, key_at<WIN>(w, j), 0,
-                                w.kvh, w.b);
+                    tma_load_tile<D>(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), key_at<WIN>(w, j), w.kvh, w.b,
+                                     WIN && p.D != D);
                 }
             }
             gt += w.n_kv;
@@ -736,6 +737,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                                        (uintptr_t)(p.o_sh * 2) | (uintptr_t)(p.o_sb * 2)) & 31) == 0;
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
+                        if (WIN && c * 32 >= p.D) break;
                         uint32_t o[32];
                         if (have_o) {
                             tmem_ld32(o_addr + c * 32, o);
@@ -765,9 +767,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     fin_l = have_o ? l : 0.f;
                     fin_have = have_o;
                 } else {
-                    float *A = p.part_acc + ((size_t)blockIdx.y * rows_total + grow) * D;
+                    float *A = p.part_acc + ((size_t)blockIdx.y * rows_total + grow) * (WIN ? p.D : D);
 #pragma unroll
                     for (int c = 0; c < D / 32; ++c) {
+                        if (WIN && c * 32 >= p.D) break;
                         uint32_t o[32];
                         if (have_o) {
                             tmem_ld32(o_addr + c * 32, o);
@@ -858,6 +861,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
             const int rl = rank * R + task / CH, ch = task % CH;
             const int row = w.q0 + rl;
             if (rl >= 2 * BM || row >= p.Sq) break;   // tasks go by row
+            if (WIN && ch * 4 >= p.D) continue;
             float ms[8], ls[8], M = -INFINITY;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -907,11 +911,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------------- host side
-// Q, K, V tile maps of a problem (5-D strided views); false when TMA cannot address them.
+// Q, K, V maps of a problem (strided views); false when TMA cannot address them.
 bool make_maps(const AttnProblem &p, CUtensorMap *mq, CUtensorMap *mk, CUtensorMap *mv) {
-    return make_bf16_tile_map_strided(mq, p.q, p.D, p.Sq, p.Hq, p.B, p.q_ss, p.q_sh, p.q_sb, BM) &&
-           make_bf16_tile_map_strided(mk, p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb, BN) &&
-           make_bf16_tile_map_strided(mv, p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb, BN);
+    return make_bf16_rows_map(mq, p.q, p.D, p.Sq, p.Hq, p.B, p.q_ss, p.q_sh, p.q_sb, BM) &&
+           make_bf16_rows_map(mk, p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb, BN) &&
+           make_bf16_rows_map(mv, p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb, BN);
 }
 
 // x3 pre-pass: every float32 element of Q, K, V (any b/h/s strides) into its bf16 parts,
@@ -1061,7 +1065,7 @@ cudaError_t launch_bf16(const AttnProblem &p, int sm_count, cudaStream_t s, bool
     m[3] = m[6] = m[0];
     m[4] = m[7] = m[1];
     m[5] = m[2];
-    return p.D == 64 ? launch_t<64, false>(p, m, sm_count, s, merged) : launch_t<128, false>(p, m, sm_count, s, merged);
+    return p.D <= 64 ? launch_t<64, false>(p, m, sm_count, s, merged) : launch_t<128, false>(p, m, sm_count, s, merged);
 }
 
 // float32 inputs (D = 64): split Q, K, V into bf16 parts in the workspace, then run x3 mode on
@@ -1111,15 +1115,15 @@ bool attn_tc_supported(const AttnProblem &p, const void *Q, const void *K, const
         if (p.Sq < 2 || p.D != 64 || !aligned16(O) || ((p.o_ss | p.o_sh | p.o_sb) * 4) % 16 != 0) return false;
         return tc_ctas(p) < (1LL << 31) && tensor_map_encoder() != nullptr;
     }
-    if (p.dtype != OSF_BF16 || p.Sq < 2 || (p.D != 64 && p.D != 128)) return false;
+    if (p.dtype != OSF_BF16 || p.Sq < 2 || !(p.D == 64 || p.D == 128 || (p.window && (p.D == 32 || p.D == 96)))) return false;
     if (!aligned16(Q) || !aligned16(K) || !aligned16(V) || !aligned16(O)) return false;
     // the epilogue stores 16-byte pieces of each O row
     if (((p.o_ss | p.o_sh | p.o_sb) * 2) % 16 != 0) return false;
     if (tc_ctas(p) >= (1LL << 31)) return false;
     return tensor_map_encoder() != nullptr &&
-           tile_map_addressable(p.q, p.D, p.Sq, p.Hq, p.B, p.q_ss, p.q_sh, p.q_sb) &&
-           tile_map_addressable(p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb) &&
-           tile_map_addressable(p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb);
+           rows_map_addressable(p.q, p.D, p.Sq, p.Hq, p.B, p.q_ss, p.q_sh, p.q_sb) &&
+           rows_map_addressable(p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb) &&
+           rows_map_addressable(p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb);
 }
 
 size_t attn_tc_extra_bytes(const AttnProblem &p) {

@@ -54,7 +54,8 @@ __device__ __forceinline__ uint32_t ld_bf16x2(const __nv_bfloat16 *p) {
     return *reinterpret_cast<const uint32_t *>(p);
 }
 
-// WIN: a window with sinks (AttnProblem::window); the tiles are then those of the rows' key_stream.
+// WIN: a window with sinks (AttnProblem::window); the tiles are then those of the rows' key_stream, and rows may have fewer
+// channels than D (p.D, a multiple of 32), the rest of the tiles being zeros.
 template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 2)
 decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
@@ -105,7 +106,13 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
                 if (!ok) break;
                 const uint32_t bar = smem_u32(&full[st]);
                 mbar_expect_tx(bar, C::TILE);
-                tma_load_5d(ring + st * C::TILE, map, bar, 0, key_at(i), 0, kvh, b);
+                if (!WIN || p.D == D) {
+                    tma_load_5d(ring + st * C::TILE, map, bar, 0, key_at(i), 0, kvh, b);
+                } else {
+#pragma unroll
+                    for (int x = 0; x < C::BOXES; ++x)
+                        tma_load_4d(ring + st * C::TILE + x * BOXB, map, bar, 64 * x, key_at(i), kvh, b);
+                }
                 issued = i + 1;
             }
             if (!ok) {
@@ -131,10 +138,11 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     uint32_t qa[D / 16][4];
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
-        qa[kk][0] = r0 < R ? ld_bf16x2(Q0 + kk * 16 + kc) : 0u;
-        qa[kk][1] = r1 < R ? ld_bf16x2(Q1 + kk * 16 + kc) : 0u;
-        qa[kk][2] = r0 < R ? ld_bf16x2(Q0 + kk * 16 + 8 + kc) : 0u;
-        qa[kk][3] = r1 < R ? ld_bf16x2(Q1 + kk * 16 + 8 + kc) : 0u;
+        const bool in = !WIN || kk * 16 < p.D;
+        qa[kk][0] = r0 < R && in ? ld_bf16x2(Q0 + kk * 16 + kc) : 0u;
+        qa[kk][1] = r1 < R && in ? ld_bf16x2(Q1 + kk * 16 + kc) : 0u;
+        qa[kk][2] = r0 < R && in ? ld_bf16x2(Q0 + kk * 16 + 8 + kc) : 0u;
+        qa[kk][3] = r1 < R && in ? ld_bf16x2(Q1 + kk * 16 + 8 + kc) : 0u;
     }
     // last key each of this thread's two rows may see (exclusive bound)
     const int lim0 = p.causal ? min(key_end, r0 % p.Sq + p.causal_off + 1) : key_end;
@@ -245,6 +253,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     const long long rows_total = (long long)p.B * p.Hq * p.Sq;
     for (int idx = tid; idx < R * D; idx += NCW * 32) {
         const int row = idx / D, d = idx % D;
+        if (WIN && d >= p.D) continue;
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NCW; ++w) M = fmaxf(M, sm_m[w][row]);
@@ -263,7 +272,7 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
             static_cast<__nv_bfloat16 *>(p.o)[o_at(p, b, hq, qi) + d] = __float2bfloat16_rn(acc * inv);
             if (p.lse && d == 0) p.lse[grow] = L > 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
         } else {
-            p.part_acc[((size_t)split * rows_total + grow) * D + d] = acc;
+            p.part_acc[((size_t)split * rows_total + grow) * (WIN ? p.D : D) + d] = acc;
             if (d == 0) {
                 p.part_m[(size_t)split * rows_total + grow] = M;
                 p.part_l[(size_t)split * rows_total + grow] = L;
@@ -272,10 +281,10 @@ decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CU
     }
 }
 
-// K and V tile maps of a problem (5-D strided views); false when TMA cannot address them.
+// K and V maps of a problem (strided views); false when TMA cannot address them.
 bool make_maps(const AttnProblem &p, CUtensorMap *mk, CUtensorMap *mv) {
-    return make_bf16_tile_map_strided(mk, p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb, KT) &&
-           make_bf16_tile_map_strided(mv, p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb, KT);
+    return make_bf16_rows_map(mk, p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb, KT) &&
+           make_bf16_rows_map(mv, p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb, KT);
 }
 
 // Key tiles that a call goes through.
@@ -303,14 +312,14 @@ cudaError_t launch_t(const AttnProblem &p, cudaStream_t s) {
 
 bool decode_supported(const AttnProblem &p, const void *Q, const void *K, const void *V, const void *O) {
     (void)O;
-    if (p.dtype != OSF_BF16 || p.Sq < 1 || (p.D != 64 && p.D != 128)) return false;
+    if (p.dtype != OSF_BF16 || p.Sq < 1 || !(p.D == 64 || p.D == 128 || (p.window && (p.D == 32 || p.D == 96)))) return false;
     if ((long long)(p.Hq / p.Hkv) * p.Sq > MAX_G) return false;
     if (!aligned16(K) || !aligned16(V) || (reinterpret_cast<uintptr_t>(Q) & 3u) != 0) return false;
     if (((p.q_sb | p.q_sh | p.q_ss) & 1) != 0) return false;   // Q is read as bf16 pairs
     if ((long long)p.B * p.Hkv >= (1LL << 31)) return false;
     return tensor_map_encoder() != nullptr &&
-           tile_map_addressable(p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb) &&
-           tile_map_addressable(p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb);
+           rows_map_addressable(p.k, p.D, p.Sk, p.Hkv, p.B, p.k_ss, p.k_sh, p.k_sb) &&
+           rows_map_addressable(p.v, p.D, p.Sk, p.Hkv, p.B, p.v_ss, p.v_sh, p.v_sb);
 }
 
 int decode_pick_splits(const AttnProblem &p, int sm_count, int requested) {
@@ -332,7 +341,7 @@ int decode_pick_splits(const AttnProblem &p, int sm_count, int requested) {
 }
 
 cudaError_t launch_decode(const AttnProblem &p, cudaStream_t s) {
-    cudaError_t e = p.window ? p.D == 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s)
+    cudaError_t e = p.window ? p.D <= 64 ? launch_t<64, true>(p, s) : launch_t<128, true>(p, s)
                              : p.D == 64 ? launch_t<64, false>(p, s) : launch_t<128, false>(p, s);
     if (e == cudaSuccess && p.splits > 1) e = launch_attn_combine(p, s);
     return e;

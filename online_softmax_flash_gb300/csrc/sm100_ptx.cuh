@@ -160,6 +160,23 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *map
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
         : "memory");
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1, int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+// A [128 x D] tile of rows from `row` on of head h of batch b: one box of a tile map, or (blocks: a row has fewer than D
+// channels) a box of a block map for each 64 channels, which fills the rest with zeros.  The bytes are the same.
+template <int D>
+__device__ __forceinline__ void tma_load_tile(uint32_t dst, const CUtensorMap *map, uint32_t bar, int row, int h, int b, bool blocks) {
+    if (!blocks) {
+        tma_load_5d(dst, map, bar, 0, row, 0, h, b);
+    } else {
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) tma_load_4d(dst + c * (128 * 128), map, bar, 64 * c, row, h, b);
+    }
+}
 // 16 bytes to shared memory.
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");

@@ -99,17 +99,38 @@ inline bool make_bf16_tile_map_strided(CUtensorMap *m, const void *g, int D, lon
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// 2-D map over contiguous 8-bit rows [rows][D], D 64 or 128: boxes of box_rows whole rows, swizzled over the row's bytes
-// (D = 128: 16-byte piece c of row r at c ^ (r % 8); D = 64: at c ^ ((r / 2) % 4)); rows past the end read as zero.
-inline bool make_u8_rows_map(CUtensorMap *m, const void *g, int D, long long rows, uint32_t box_rows) {
+// 2-D map over contiguous 8-bit rows [rows][D], D a multiple of 16 up to DP, which is 64 or 128: boxes of box_rows rows of DP
+// bytes, zeros from D on, swizzled over the row's bytes (DP = 128: 16-byte piece c of row r at c ^ (r % 8); DP = 64: at
+// c ^ ((r / 2) % 4)); rows past the end read as zero.
+inline bool make_u8_rows_map(CUtensorMap *m, const void *g, int D, int DP, long long rows, uint32_t box_rows) {
     auto enc = tensor_map_encoder();
-    if (!enc || (D != 64 && D != 128)) return false;
+    if (!enc || (DP != 64 && DP != 128) || D > DP || D % 16 != 0) return false;
     cuuint64_t dims[2] = {(cuuint64_t)D, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)D};
-    cuuint32_t box[2] = {(cuuint32_t)D, box_rows};
+    cuuint32_t box[2] = {(cuuint32_t)DP, box_rows};
     cuuint32_t es[2] = {1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(g), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               DP == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 4-D view (d, s, h, b) of a bf16 tensor [B][H][S][D] with element strides sb, sh, ss (d contiguous, D a multiple of 8): boxes
+// of box_rows rows of 64 channels, zeros from D on, laid out as a 64-channel block of make_bf16_tile_map.
+inline bool make_bf16_block_map_strided(CUtensorMap *m, const void *g, int D, long long S, long long H, long long B,
+                                        long long ss, long long sh, long long sb, uint32_t box_rows) {
+    auto enc = tensor_map_encoder();
+    if (!enc || D % 8 != 0) return false;
+    auto fix = [&](long long extent, long long stride_elems) -> cuuint64_t {
+        return extent > 1 ? (cuuint64_t)stride_elems * 2 : (cuuint64_t)D * 2;
+    };
+    cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)S, (cuuint64_t)H, (cuuint64_t)B};
+    cuuint64_t strides[3] = {fix(S, ss), fix(H, sh), fix(B, sb)};
+    for (int i = 0; i < 3; ++i)
+        if (strides[i] == 0 || strides[i] % 16 != 0) return false;
+    cuuint32_t box[4] = {64, box_rows, 1, 1};
+    cuuint32_t es[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(g), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -123,6 +144,19 @@ inline bool tile_map_addressable(const void *g, int D, long long S, long long H,
     for (int i = 0; i < 3; ++i)
         if (ext[i] > 1 && (st[i] <= 0 || (st[i] * 2) % 16 != 0 || st[i] * 2 >= (1LL << 40))) return false;
     return true;
+}
+
+// The map that tma_load_tile takes for rows of D channels: a tile map where D is a multiple of 64, else (a multiple of 8) a
+// block map; and whether one can be made.
+inline bool make_bf16_rows_map(CUtensorMap *m, const void *g, int D, long long S, long long H, long long B, long long ss,
+                               long long sh, long long sb, uint32_t box_rows) {
+    return D % 64 == 0 ? make_bf16_tile_map_strided(m, g, D, S, H, B, ss, sh, sb, box_rows)
+                       : make_bf16_block_map_strided(m, g, D, S, H, B, ss, sh, sb, box_rows);
+}
+inline bool rows_map_addressable(const void *g, int D, long long S, long long H, long long B, long long ss, long long sh,
+                                 long long sb) {
+    // (strides and alignment are what tile maps ask for)
+    return D % 8 == 0 && tile_map_addressable(g, 64, S, H, B, ss, sh, sb);
 }
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -257,7 +257,7 @@ ATTN = [
 ]
 
 
-@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 96), ("f32", 64), ("f32", 128), ("f32", 256)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 96), ("bf16", 128), ("bf16", 160), ("f32", 64), ("f32", 128), ("f32", 256)])
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,P,lens,window,sinks", ATTN)
 def test_attention(osf, dtype, D, B, Hq, Hkv, Sq, P, lens, window, sinks):
     pages, scales, table = fill_cache(B, Hkv, P, D, lens, seed=D + Sq)

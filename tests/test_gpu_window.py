@@ -81,25 +81,25 @@ SHAPES = [
 ]
 
 
-@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("bf16", 96), ("f32", 64), ("f32", 40), ("f32", 256)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 96), ("bf16", 128), ("bf16", 72), ("f32", 64), ("f32", 40), ("f32", 256)])
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,window,sinks", SHAPES)
 def test_forward(osf, dtype, D, B, Hq, Hkv, Sq, Sk, window, sinks):
     run(osf, dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks)
 
 
-@pytest.mark.parametrize("dtype,D", [("bf16", 64), ("bf16", 128), ("f32", 64), ("bf16", 32)])
+@pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 96), ("bf16", 128), ("bf16", 72), ("f32", 64), ("f32", 100), ("f32", 250)])
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,window,sinks", SHAPES)
 def test_gradients(osf, dtype, D, B, Hq, Hkv, Sq, Sk, window, sinks):
     run(osf, dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks, grad=True)
 
 
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 96, 128])
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,window,sinks", [s for s in SHAPES if s[5] + s[6] < s[4]])
 def test_gradients_without_stored_ds(osf, D, B, Hq, Hkv, Sq, Sk, window, sinks):
     run(osf, "bf16", B, Hq, Hkv, Sq, Sk, D, window, sinks, grad=True, store_ds=False)
 
 
-@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("D", [64, 96, 128])
 def test_many_items(osf, D):
     """More query blocks than SMs, so that a CTA goes from one to the next."""
     run(osf, "bf16", 5, 8, 4, 1100, 1100, D, 190, 3, grad=True)
