@@ -327,6 +327,12 @@ int decode_pick_splits(const AttnProblem &p, int sm_count, int requested) {
     int s;
     if (requested > 0) {
         s = requested;
+    } else if (p.window) {
+        // one wave of two CTAs per SM, of at least five tiles each: a window's chunks are short, and what a CTA costs besides them
+        // is not (B=8 Hkv=8 D=128, 65 tiles: 29 us with 4 chunks, 35 with 5, 32 with 8, 37 with 19; B=1 Hkv=8: 14 us with 8 or 12,
+        // 15 with 32)
+        const long long most = std::max(1LL, 2LL * sm_count / ((long long)p.B * p.Hkv));
+        s = (int)std::min(most, std::max(1LL, (long long)n_kt / 5));
     } else {
         // about four waves of two CTAs per SM, so the last wave's imbalance stays small
         const long long items = (long long)p.B * p.Hkv;
