@@ -79,6 +79,43 @@ __device__ __forceinline__ void store_run(__nv_bfloat16 *p, bool vec, const floa
     }
 }
 
+// A run as it is in memory, and its values.
+template <typename T, int W>
+struct Raw;
+template <int W>
+struct Raw<float, W> {
+    float v[W];
+    __device__ __forceinline__ void load(const float *p, bool vec) { load_run<W>(p, vec, v); }
+    __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+        for (int i = 0; i < W; ++i) x[i] = v[i];
+    }
+};
+template <int W>
+struct Raw<__nv_bfloat16, W> {
+    uint32_t v[W / 2];
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p, bool vec) {
+        if (!vec) {
+            const unsigned short *h = reinterpret_cast<const unsigned short *>(p);
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) v[i] = h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+        } else if constexpr (W == 8) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(p);
+            v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+        } else {
+            const uint2 q = *reinterpret_cast<const uint2 *>(p);
+            v[0] = q.x; v[1] = q.y;
+        }
+    }
+    __device__ __forceinline__ void values(float *x) const {
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) {
+            x[2 * i] = lo_bf16(v[i]);
+            x[2 * i + 1] = hi_bf16(v[i]);
+        }
+    }
+};
+
 // The float32 nearest to a c - b s.
 __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
@@ -318,45 +355,51 @@ __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc,
     T *dst = static_cast<T *>(p.qo) + b * p.o_sb + h0 * p.o_sh + t * p.o_ss;
     float c[W], s[W];
     if (w.rotated) load_angles<W>(p, w, min(max((p.lens ? p.lens[b] : 0) + t, 0), p.max_pos - 1), c, s);
-    float x[HB][2 * W];
+    Raw<T, W> lo[HB], hi[HB];
 #pragma unroll
     for (int k = 0; k < HB; ++k)
         if (h0 + k < p.Hq) {
-            load_run<W>(src + k * p.q_sh + w.first, q_vec, x[k]);
-            load_run<W>(src + k * p.q_sh + w.second, q_vec, x[k] + W);
+            lo[k].load(src + k * p.q_sh + w.first, q_vec);
+            hi[k].load(src + k * p.q_sh + w.second, q_vec);
         }
 #pragma unroll
     for (int k = 0; k < HB; ++k)
         if (h0 + k < p.Hq) {
+            float x[2 * W];
+            lo[k].values(x);
+            hi[k].values(x + W);
             if (w.rotated) {
                 float a[W], b2[W];
-                split_pairs<W>(x[k], p.interleaved, a, b2);
+                split_pairs<W>(x, p.interleaved, a, b2);
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     const float ra = fmaf(a[e], c[e], -(b2[e] * s[e])), rb = fmaf(b2[e], c[e], a[e] * s[e]);
                     a[e] = ra;
                     b2[e] = rb;
                 }
-                join_pairs<W>(x[k], p.interleaved, a, b2);
+                join_pairs<W>(x, p.interleaved, a, b2);
             }
-            store_run<W>(dst + k * p.o_sh + w.first, o_vec, x[k]);
-            store_run<W>(dst + k * p.o_sh + w.second, o_vec, x[k] + W);
+            store_run<W>(dst + k * p.o_sh + w.first, o_vec, x);
+            store_run<W>(dst + k * p.o_sh + w.second, o_vec, x + W);
         }
 }
 
-// One launch: the pages that new tokens may fall into, then the queries.
+// One launch: blocks for the pages that new tokens may fall into, and among them, spread evenly, blocks for the queries; the
+// former are bound by what they issue and the latter by memory.  Of the blocks before block i, i * page_share / 2^32 have
+// pages.
 template <typename T, int W, bool BLOCK, int HB>
 __global__ void __launch_bounds__(kThreads, 3)
-kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned page_blocks, unsigned q_blocks, int k_vec, int v_vec,
-                  int q_vec, int o_vec) {
+kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned long long page_share, unsigned q_blocks, int k_vec,
+                  int v_vec, int q_vec, int o_vec) {
     const Kv8Cache &c = p.c;
-    if (blockIdx.x >= page_blocks) {
+    const unsigned page_block = (unsigned)(blockIdx.x * page_share >> 32);
+    if ((unsigned)((blockIdx.x + 1) * page_share >> 32) == page_block) {
         // q_blocks blocks to each (batch, HB heads)
-        const unsigned qb = blockIdx.x - page_blocks, bc = qb / q_blocks;
+        const unsigned qb = blockIdx.x - page_block, bc = qb / q_blocks;
         rotate_queries<T, W, HB>(p, (int)bc, (int)((qb - bc * q_blocks) * kThreads + threadIdx.x), q_vec, o_vec);
         return;
     }
-    const unsigned task = BLOCK ? blockIdx.x : blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const unsigned task = BLOCK ? page_block : page_block * (kThreads / 32) + (threadIdx.x >> 5);
     const unsigned bhh = task / pages_per_seq;
     const int page_no = (int)(task - bhh * pages_per_seq), half = (int)(bhh & 1), bh = (int)(bhh >> 1);
     if (bh >= p.B * c.Hkv) return;
@@ -433,7 +476,7 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
     const long long blocks = page_blocks + (p.q ? (long long)p.B * ((p.Hq + HB - 1) / HB) * q_blocks : 0);
     if (blocks >= (1LL << 31) || tasks >= (1LL << 31)) return cudaErrorInvalidValue;
     kv8_append_kernel<T, W, BLOCK, HB><<<(unsigned)blocks, kThreads, 0, s>>>(
-        p, pages_per_seq, (unsigned)page_blocks, (unsigned)q_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
+        p, pages_per_seq, (((unsigned long long)page_blocks << 32) + blocks - 1) / blocks, (unsigned)q_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
         rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
         rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es, W));
     count_launches(1);
@@ -448,11 +491,11 @@ cudaError_t append_w(Kv8StoreProblem p, int sm_count, cudaStream_t s) {
     const int per_seq = (int)(pages < c.per_seq ? pages : c.per_seq);
     // a warp to a page while a page's new tokens fit its lanes' registers
     const bool block = (long long)(p.n < c.P ? p.n : c.P) * (c.D / (2 * W)) > (W == 8 ? 64 : 128);
-    // two heads to a thread once there are threads enough (queries of 8 prompts of 4096 tokens, 32 heads of 128: with 1, 2, 4, 8
-    // heads the call takes 191, 187, 201, 244 us)
+    // four heads to a thread once there are threads enough (queries of 8 prompts of 4096 tokens, 32 heads of 128: with 2, 4, 8
+    // heads the call takes 177, 154, 195 us)
     const bool heads = (long long)p.B * p.Hq * p.n * (c.D / (2 * W)) >= 8LL * 1024 * sm_count;
-    if (block) return heads ? append_k<T, W, true, 2>(p, per_seq, s) : append_k<T, W, true, 1>(p, per_seq, s);
-    return heads ? append_k<T, W, false, 2>(p, per_seq, s) : append_k<T, W, false, 1>(p, per_seq, s);
+    if (block) return heads ? append_k<T, W, true, 4>(p, per_seq, s) : append_k<T, W, true, 1>(p, per_seq, s);
+    return heads ? append_k<T, W, false, 4>(p, per_seq, s) : append_k<T, W, false, 1>(p, per_seq, s);
 }
 
 template <typename T>
