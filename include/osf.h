@@ -190,9 +190,10 @@ int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, i
 /*
  * osf_attn_bwd_gqa_window -- gradients of osf_attn_fwd_gqa_window: osf_attn_bwd_gqa (same tensors, formulas and errors)
  * with the keys that a row sees given by window and sinks, as in the forward call.
- * workspace: osf_attn_bwd_window_workspace_bytes bytes, 128-byte aligned: row sums, the sums of the key tiles that hold
- *     sinks (whose rows are shared out over several CTAs), and dS^T in bf16 of the tile pairs that some row sees while it
- *     stays within 16 GiB.  A workspace short of the last part selects the path that keeps no dS.
+ * workspace: osf_attn_bwd_window_workspace_bytes bytes, 128-byte aligned: row sums; the sums of key tiles whose rows are
+ *     shared out over several CTAs (those that hold sinks, or all of a small problem); and, of larger problems, dS^T in bf16 of
+ *     the tile pairs that some row sees while it stays within 16 GiB.  A workspace short of the last part selects the path
+ *     that keeps no dS.
  * The result does not depend on the order in which anything runs.  Sq == 0 or Sk == 0: what gradients there are are zero.
  */
 int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const void *O, const void *dO,

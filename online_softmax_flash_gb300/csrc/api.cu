@@ -792,25 +792,30 @@ int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O
     return run_gqa(p, path, workspace, workspace_bytes, plan_splits(p, path, dev->sm_count, 0), dev, (cudaStream_t)stream);
 }
 
-// Workspace of the windowed backward: row sums | sums of the tiles that hold sinks | dS^T tiles that some row sees.  The
-// last are left out where they would pass 16 GiB, and may be left out by the caller (dQ then recomputes S and dP).
+// Workspace of the windowed backward: row sums | sums of the key tiles that several CTAs share | dS^T tiles that some row sees,
+// where the plan stores them and they stay within 16 GiB; they may be left out by the caller (dQ then recomputes S and dP).
 struct BwdWindowLayout {
-    size_t rows = 0, ds = 0, sink = 0;
-    int slots = 0, parts = 1;
+    size_t rows = 0, ds = 0, parts = 0;
+    BwdWindowPlan plan{};
 };
 static BwdWindowLayout bwd_window_layout(const AttnProblem &p, int sm_count) {
     BwdWindowLayout L;
     L.rows = align256((size_t)p.B * p.Hq * p.Sq * sizeof(float));
     if (!window_tc(p.dtype, p.D)) return L;
-    L.slots = bwd_window_slots(p.Sk, p.window, p.sinks);
-    L.parts = bwd_window_sink_parts(p.B, p.Hkv, p.Sq, p.Sk, p.window, p.sinks, sm_count);
-    const size_t tile = (size_t)128 * 128 * 2, per_head = (size_t)L.slots * (((size_t)p.Sq + 127) / 128) * tile;
+    L.plan = bwd_window_plan(p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks, sm_count);
+    const size_t tile = (size_t)128 * 128 * 2, per_head = (size_t)L.plan.slots * (((size_t)p.Sq + 127) / 128) * tile;
     const size_t cap = (size_t)16 << 30, heads = (size_t)p.B * p.Hq;
-    if (per_head <= cap / heads) L.ds = per_head * heads;
-    if (L.parts > 1)
-        L.sink = (size_t)bwd_window_sink_tiles(p.Sk, p.sinks) * L.parts * p.B * p.Hkv * 2 * 128 * (p.D <= 64 ? 64 : 128) *
-                 sizeof(float);
+    if (L.plan.store_ds && per_head <= cap / heads) L.ds = per_head * heads;
+    if (L.plan.parts > 1)
+        L.parts = (size_t)L.plan.shared_tiles * L.plan.parts * p.B * p.Hkv * 2 * 128 * (p.D <= 64 ? 64 : 128) * sizeof(float);
     return L;
+}
+// A problem whose window hides nothing runs on the causal kernels, but a small one: those share no key tile out.
+static void keep_small(AttnProblem &p, int sm_count) {
+    if (p.window || 2LL * p.B * p.Hkv * ((p.Sk + 127) / 128) > sm_count) return;
+    p.causal = 1;
+    p.causal_off = p.Sk - p.Sq;
+    p.window = p.Sk;
 }
 
 int osf_attn_bwd_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks,
@@ -823,11 +828,12 @@ int osf_attn_bwd_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int S
     const int st = check_window(ph, ph, ph, reinterpret_cast<void *>(uintptr_t(1) << 44), dtype, B, Hq, Hkv, Sq, Sk, D,
                                 nullptr, window, sinks, 0.f, nullptr, keep_bwd_window(dtype, D), p, empty);
     if (st != OSF_OK || empty) return st;
-    if (!p.window) return osf_attn_bwd_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, bytes);
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    keep_small(p, dev->sm_count);
+    if (!p.window) return osf_attn_bwd_workspace_bytes(dtype, B, Hq, Hkv, Sq, Sk, D, bytes);
     const BwdWindowLayout L = bwd_window_layout(p, dev->sm_count);
-    *bytes = L.rows + L.ds + L.sink;
+    *bytes = L.rows + L.ds + L.parts;
     return OSF_OK;
 }
 
@@ -848,27 +854,30 @@ int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const v
             return OSF_ERR_CUDA;
         return OSF_OK;
     }
-    if (!p.window)
-        return osf_attn_bwd_gqa(Q, K, V, O, dO, lse, dQ, dK, dV, dtype, B, Hq, Hkv, Sq, Sk, D, OSF_MASK_BOTTOM_RIGHT, scale,
-                                workspace, workspace_bytes, stream);
     BwdProblem b;
     const int sb = check_bwd(p, O, dO, lse, dK, dV, b);
     if (sb != OSF_OK) return sb;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
+    keep_small(p, dev->sm_count);
+    if (!p.window)
+        return osf_attn_bwd_gqa(Q, K, V, O, dO, lse, dQ, dK, dV, dtype, B, Hq, Hkv, Sq, Sk, D, OSF_MASK_BOTTOM_RIGHT, scale,
+                                workspace, workspace_bytes, stream);
+    b.causal = p.causal;
+    b.causal_off = p.causal_off;
     const BwdWindowLayout L = bwd_window_layout(p, dev->sm_count);
-    const size_t need = L.rows + L.sink;
+    const size_t need = L.rows + L.parts;
     if (!workspace || workspace_bytes < need) return OSF_ERR_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & (L.ds + L.sink ? 127u : 3u)) != 0) return OSF_ERR_INVALID;
+    if ((reinterpret_cast<uintptr_t>(workspace) & (L.ds + L.parts ? 127u : 3u)) != 0) return OSF_ERR_INVALID;
     char *at = static_cast<char *>(workspace);
     b.window = p.window;
     b.sinks = p.sinks;
     b.dvec = reinterpret_cast<float *>(at);
-    b.sink_parts = L.parts;
-    b.ds_slots = L.slots;
+    b.shared_tiles = L.plan.shared_tiles;
+    b.parts = L.plan.parts;
+    b.ds_slots = L.plan.slots;
     b.ds_ld = ((long long)Sq + 127) / 128 * 128;
-    b.ds_rows = (long long)L.slots * 128;
-    if (L.sink) b.sink_acc = reinterpret_cast<float *>(at + L.rows);
+    if (L.parts) b.part_acc = reinterpret_cast<float *>(at + L.rows);
     if (L.ds && workspace_bytes >= need + L.ds) b.ds = at + need;
     b.status = dev->status;
     return launch_status(launch_attn_bwd(b, (cudaStream_t)stream));

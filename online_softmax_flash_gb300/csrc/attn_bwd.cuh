@@ -23,19 +23,21 @@ struct BwdProblem {
     void *ds;
     long long ds_rows, ds_ld;
     int ds_slots;
-    // with a window: the query tiles of each key tile that holds sinks are shared out over sink_parts CTAs, whose sums
-    // of dK and dV (float32 [128][D] each) meet in sink_acc [sink tile][part][b, kv head][2]; 1: no sharing out
-    int sink_parts;
-    float *sink_acc;
+    // with a window: the steps (query head, query tile) of each of the first shared_tiles key tiles are shared out over
+    // `parts` CTAs, whose sums of dK and dV (float32 [128][D] each) meet in part_acc [tile][part][b, kv head][2]
+    int shared_tiles, parts;
+    float *part_acc;
     int *status;
 };
 // True when the bf16 tensor-core (mma.sync) kernels handle the problem.
 bool attn_bwd_mma_supported(const BwdProblem &p);
 cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s);
 
-// Sizes of a windowed problem on the tensor-core path: tiles of the longest key stream, key tiles that hold sinks, and
-// CTAs that share the rows of each of those.
-int bwd_window_slots(int Sk, int window, int sinks);
-int bwd_window_sink_tiles(int Sk, int sinks);
-int bwd_window_sink_parts(int B, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count);
+// How a windowed problem runs on the tensor-core path.
+struct BwdWindowPlan {
+    int slots;                 // tiles of the longest key stream
+    int shared_tiles, parts;
+    bool store_ds;             // dQ as a product over stored dS^T tiles
+};
+BwdWindowPlan bwd_window_plan(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count);
 }  // namespace osf

@@ -392,8 +392,9 @@ __device__ __forceinline__ void bwd_dq_body(const CUtensorMap &mq, const CUtenso
 }
 
 // ====================================================================== dK, dV
-// WIN: the CTAs of the key tiles that hold sinks come first, sink_parts of them for each tile and (b, kv head): every later
-// row sees a sink, so one CTA would walk Sq / 128 query tiles while the others walk window / 128.
+// WIN: the CTAs of the first shared_tiles key tiles come first, `parts` of them for each tile and (b, kv head).  Those are the
+// tiles that hold sinks (every later row sees a sink, so one CTA would walk Sq / 128 query tiles while the others walk
+// window / 128), or all tiles where they would leave SMs idle.
 template <int D, bool WIN>
 __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUtensorMap &mg, const CUtensorMap &mk,
                                               const CUtensorMap &mv, const CUtensorMap &mdst, const BwdProblem &p,
@@ -411,12 +412,11 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
     const int BK = p.B * p.Hkv;
     int kt = (int)(bid / BK), part = 0;
     if constexpr (WIN) {
-        const int shared_out = min((p.sinks - 1 + TB) / TB, (p.Sk - 1) / TB + 1) * p.sink_parts;
-        if (kt < shared_out) {
-            part = kt % p.sink_parts;
-            kt /= p.sink_parts;
+        if (kt < p.shared_tiles * p.parts) {
+            part = kt % p.parts;
+            kt /= p.parts;
         } else {
-            kt += shared_out / p.sink_parts - shared_out;
+            kt -= p.shared_tiles * (p.parts - 1);
         }
     }
     const int key0 = kt * TB;
@@ -426,20 +426,19 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
     int q_first = p.causal ? max(0, key0 - p.causal_off) : 0;
     q_first /= TB;
     int n_qt = (p.Sq + TB - 1) / TB;
-    bool partial = false;   // this CTA has only a part of the rows
     if constexpr (WIN) {
         if (key0 >= p.sinks) {
             const int last = key0 + TB - 1 + p.window - 1 - p.causal_off;   // last row whose window holds a key of the block
             n_qt = last < 0 ? 0 : min(n_qt, last / TB + 1);
-        } else if (p.sink_parts > 1) {
-            const int all = max(0, n_qt - q_first), per = (all + p.sink_parts - 1) / p.sink_parts;
-            q_first = min(n_qt, q_first + part * per);
-            n_qt = min(n_qt, q_first + per);
-            partial = true;
         }
     }
     const int per_head = max(0, n_qt - q_first);
-    const int n = G * per_head;   // steps: (head g, query tile) pairs
+    int m0 = 0, n = G * per_head;   // steps: (head g, query tile) pairs
+    const bool partial = WIN && kt < p.shared_tiles && p.parts > 1;   // this CTA has steps m0 .. m0 + n - 1 alone
+    if (partial) {
+        m0 = (int)((long long)n * part / p.parts);
+        n = (int)((long long)n * (part + 1) / p.parts) - m0;
+    }
     if (warp == 0) tmem_alloc(smem_u32(&tmem_sh), TMEM_COLS);
     if (tid == 32) init_bars<D>(bars, abort_flag);
     tc_fence_before();
@@ -448,6 +447,7 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
     const uint32_t tmem = tmem_sh;
     const uint32_t tS = tmem, tP = tmem + 128, tK = tmem + 256, tV = tmem + 256 + D;
     auto step_at = [&](int m, int &hq, int &qt) {
+        if (WIN) m += m0;
         hq = kvh * G + m / per_head;
         qt = q_first + m % per_head;
     };
@@ -687,7 +687,7 @@ __device__ __forceinline__ void bwd_dkdv_body(const CUtensorMap &mq, const CUten
         const bool key_ok = key < p.Sk;
         if (WIN && partial) {
             // this part's sums, [key][D] float32, zero where it has no rows
-            float *out = p.sink_acc + ((((size_t)kt * p.sink_parts + part) * BK + bk) * 2 + h) * TB * D + (size_t)r * D;
+            float *out = p.part_acc + ((((size_t)kt * p.parts + part) * BK + bk) * 2 + h) * TB * D + (size_t)r * D;
             const uint32_t src = (h ? tV : tK) + lane_off;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
@@ -732,18 +732,18 @@ bwd_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CU
     else bwd_dq_body<D, WIN>(mq, mg, mk, mv, p, blockIdx.x - n_dkdv);
 }
 
-// dK and dV of the keys in tiles that hold sinks: the parts' sums, added in the order of the parts.  One thread per four
+// dK and dV of the keys in shared tiles: the parts' sums, added in the order of the parts.  One thread per four
 // channels of a key: gridDim = (keys of the tiles * D / 4 / 256, b * kv head, dK | dV).
-__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdProblem p, int D) {   // D: channels of a sum
+__global__ void __launch_bounds__(256) bwd_part_sum_kernel(const BwdProblem p, int D) {   // D: channels of a sum
     griddep_wait();
     const int per = D / 4, i = blockIdx.x * 256 + threadIdx.x;
     const int key = i / per, c = i % per * 4, BK = gridDim.y, bk = blockIdx.y, h = blockIdx.z;
     if (key >= p.Sk || c >= p.D) return;
     const size_t part = (size_t)BK * 2 * TB * D;
-    const float *src = p.sink_acc + (((size_t)(key / TB) * p.sink_parts * BK + bk) * 2 + h) * TB * D + (size_t)(key % TB) * D + c;
+    const float *src = p.part_acc + (((size_t)(key / TB) * p.parts * BK + bk) * 2 + h) * TB * D + (size_t)(key % TB) * D + c;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int s = 0; s < p.sink_parts; ++s) {
+    for (int s = 0; s < p.parts; ++s) {
         const float4 x = *reinterpret_cast<const float4 *>(src + s * part);
         a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
     }
@@ -983,21 +983,20 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
         !make_bf16_rows_map(&mk, p.k, pd, p.Sk, p.Hkv, p.B, pd, ks, ks * p.Hkv, TB) ||
         !make_bf16_rows_map(&mv, p.v, pd, p.Sk, p.Hkv, p.B, pd, ks, ks * p.Hkv, TB))
         return cudaErrorInvalidValue;
-    const int sink_tiles = WIN ? bwd_window_sink_tiles(p.Sk, p.sinks) : 0;
-    const unsigned nkv = (unsigned)((p.Sk + TB - 1) / TB + (WIN ? sink_tiles * (p.sink_parts - 1) : 0)) * (unsigned)(p.B * p.Hkv);
+    const unsigned nkv = (unsigned)((p.Sk + TB - 1) / TB + (WIN ? p.shared_tiles * (p.parts - 1) : 0)) * (unsigned)(p.B * p.Hkv);
     const unsigned nq = (unsigned)((p.Sq + TB - 1) / TB) * (unsigned)(p.B * p.Hq);
     if ((unsigned long long)nkv + nq >= (1ull << 31)) return cudaErrorInvalidValue;
-    auto sink_sums = [&]() -> cudaError_t {
-        if (!WIN || sink_tiles == 0 || p.sink_parts == 1) return cudaSuccess;
-        const dim3 g((unsigned)(((long long)sink_tiles * TB * D / 4 + 255) / 256), (unsigned)(p.B * p.Hkv), 2);
+    auto part_sums = [&]() -> cudaError_t {
+        if (!WIN || p.shared_tiles == 0 || p.parts == 1) return cudaSuccess;
+        const dim3 g((unsigned)(((long long)p.shared_tiles * TB * D / 4 + 255) / 256), (unsigned)(p.B * p.Hkv), 2);
         count_launches(1);
-        return launch_dependent(bwd_sink_sum_kernel, g, dim3(256), 0, s, p, D);
+        return launch_dependent(bwd_part_sum_kernel, g, dim3(256), 0, s, p, D);
     };
     if (!p.ds) {
         // dK/dV and dQ CTAs in one grid
         cudaError_t e = launch_dependent(bwd_tc_kernel<D, WIN>, dim3(nkv + nq), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg,
                                          mk, mv, mq, p, nkv);   // (no dS stores: the fifth map is unused)
-        if (e == cudaSuccess) e = sink_sums();
+        if (e == cudaSuccess) e = part_sums();
         if (e != cudaSuccess) return e;
         count_launches(1);
         return cudaGetLastError();
@@ -1015,7 +1014,7 @@ cudaError_t launch_t(const BwdProblem &p, cudaStream_t s) {
     if (device_sm_count(&sms) != OSF_OK || sms <= 0) return cudaErrorInvalidValue;
     e = launch_dependent(bwd_tc_kernel<D, WIN>, dim3(nkv), dim3(NT_THREADS), C::SMEM_BYTES, s, mq, mg, mk, mv, mdst, p,
                          nkv);
-    if (e == cudaSuccess) e = sink_sums();
+    if (e == cudaSuccess) e = part_sums();
     if (e != cudaSuccess) return e;
     const int hp = (p.Hq / p.Hkv) % 2 == 0 ? 2 : 1;   // query heads per item: two of one kv group
     const int n_items = (int)nq / hp;
@@ -1047,21 +1046,36 @@ cudaError_t launch_attn_bwd_tc(const BwdProblem &p, cudaStream_t s) {
     return p.D == 64 ? launch_t<64, false>(p, s) : launch_t<128, false>(p, s);
 }
 
-int bwd_window_slots(int Sk, int window, int sinks) { return key_stream_max(TB, Sk, window, sinks, TB); }
-int bwd_window_sink_tiles(int Sk, int sinks) {
-    const long long tiles = ((long long)sinks + TB - 1) / TB, all = ((long long)Sk + TB - 1) / TB;
-    return (int)(tiles < all ? tiles : all);
-}
-int bwd_window_sink_parts(int B, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count) {
-    const long long tiles = bwd_window_sink_tiles(Sk, sinks);
-    if (tiles == 0) return 1;
-    // parts as long as the walk of a key tile without sinks, as long as they stay within four CTAs to an SM (which bounds
-    // the sums' memory too: 128 KB a CTA at D = 128)
-    const long long q_tiles = ((long long)Sq + TB - 1) / TB, walk = ((long long)window + TB - 1) / TB + 1;
-    long long parts = (q_tiles + walk - 1) / walk;
-    const long long most = (4LL * sm_count + tiles * B * Hkv - 1) / (tiles * B * Hkv);
-    if (parts > most) parts = most;
-    return (int)(parts < 1 ? 1 : parts);
+BwdWindowPlan bwd_window_plan(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count) {
+    BwdWindowPlan w;
+    const long long kts = ((long long)Sk + TB - 1) / TB, qts = ((long long)Sq + TB - 1) / TB;
+    const long long heads = (long long)B * Hkv, kv = kts * heads, q = qts * B * Hq;
+    const long long walk = ((long long)window + TB - 1) / TB + 1;   // query tiles that see a key tile without sinks
+    w.slots = key_stream_max(TB, Sk, window, sinks, TB);
+    // dS^T is stored where dK and dV alone fill the GPU: recomputing it takes seven products a pair of tiles instead of five, but
+    // no third launch, and its CTAs fill SMs that are idle otherwise.  (bfloat16, us, stored against recomputed: Hq=8 Hkv=2
+    // D=128 window 600, 1024 tokens 75 against 63; Hq=32 Hkv=8, B=2 of 512 55 against 45, B=1 of 2048 96 against 100, B=4
+    // of 1024 143 against 164; window 100, B=1 of 4096 120 against 139.)
+    w.store_ds = kv + q > 4LL * sm_count;
+    if (2 * kv <= sm_count) {
+        // fewer key tiles than half the SMs: the steps of each are shared out, two of them to a CTA at least
+        const long long steps = (long long)(Hq / Hkv) * (walk < qts ? walk : qts);
+        long long parts = sm_count / kv;
+        if (parts > steps / 2) parts = steps / 2;
+        w.shared_tiles = (int)kts;
+        w.parts = (int)(parts < 1 ? 1 : parts);
+        return w;
+    }
+    // else those of the tiles that hold sinks, in parts as long as the walk of a tile without, as long as they stay within
+    // four CTAs to an SM (which bounds the sums' memory too: 128 KB a CTA at D = 128)
+    const long long sink_tiles = ((long long)sinks + TB - 1) / TB;
+    w.shared_tiles = (int)(sink_tiles < kts ? sink_tiles : kts);
+    w.parts = 1;
+    if (w.shared_tiles) {
+        const long long parts = (qts + walk - 1) / walk, most = (4LL * sm_count + w.shared_tiles * heads - 1) / (w.shared_tiles * heads);
+        w.parts = (int)(parts < most ? parts : most);
+    }
+    return w;
 }
 
 }  // namespace osf
