@@ -277,7 +277,8 @@ __device__ __forceinline__ int cta_of(const FlatCut &w, long long x) { return (i
 
 // A CTA's pieces, one after another.  Every warp walks them for itself.
 struct Walk {
-    int rest, b, item, unit0;                    // what is left
+    long long rest;                              // what is left
+    int b, item, unit0;
     int kvh, r0, rows, n, tile0, tiles, whole;   // the piece: tiles [tile0, tile0 + tiles) of the sequence's stream
     KeyStream ks;
 };
@@ -294,7 +295,7 @@ __device__ __forceinline__ bool walk_begin(const Kv8AttnProblem &kp, int items_p
     const FlatCut f = flat_cut(kp, items_per_b, 0, gridDim.x);
     if ((int)blockIdx.x >= f.nc) return false;
     const long long pos = f.total * blockIdx.x / f.nc;
-    w.rest = (int)(f.total * (blockIdx.x + 1) / f.nc - pos);
+    w.rest = f.total * (blockIdx.x + 1) / f.nc - pos;
     long long at = 0;   // units before batch b: 32 batches at a time, a lane each
     for (int b0 = 0;; b0 += 32) {
         const int bi = b0 + lane;
@@ -326,7 +327,7 @@ __device__ __forceinline__ bool walk_next(const Kv8AttnProblem &kp, int row_bloc
     const AttnProblem &p = kp.a;
     w.ks = stream_of(kp, w.b, w.n);
     const int all = max(1, w.ks.n), units = all + kItemCost;   // the item's first kItemCost units hold no tiles
-    const int take = flat ? min(units - w.unit0, w.rest) : units;
+    const int take = flat ? (int)min((long long)(units - w.unit0), w.rest) : units;
     w.tile0 = max(0, w.unit0 - kItemCost);
     const int tile1 = w.unit0 + take - kItemCost;
     if (tile1 <= w.tile0) {   // the part ends before the item's first tile
@@ -511,7 +512,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         uint32_t st_par = 0, g_par = 0, q_par = 0;   // and the parities of their barriers
         bool again = false;                          // the groups have had a tile each
         while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
-            if (lane == 0) {
+            if (lane == 0 && w.tiles > 0) {
                 if (is_s) ok = mbar_wait(smem_u32(&bars.q_full), q_par, &abort_flag);
                 q_par ^= 1;
                 const uint64_t qd = sdesc_any(sQ, 16, C::GROUP8, C::SWZ), pd0 = sdesc_any(sP, 128, TT * 16, 0);
@@ -632,7 +633,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             if (r128 < 2 * RT) ref[gi][r128] = kRowFloor;
             fence_proxy_async_smem();
             named_barrier(1, SOFT);
-            if (lane == 0) mbar_arrive(smem_u32(&bars.q_full));
+            // (a piece without tiles waits for no product, so several could pass while the issuer sleeps: they are not counted)
+            if (lane == 0 && w.tiles > 0) mbar_arrive(smem_u32(&bars.q_full));
 
             float m[RT], mp[RT], l[RT];   // -m, -m' and this thread's part of the denominator
 #pragma unroll

@@ -458,3 +458,34 @@ def test_two_streams_at_once(osf):
     torch.cuda.synchronize()
     for i in range(2):
         assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
+def test_mostly_empty_batch(osf):
+    """Hundreds of sequences of which few hold tokens: every CTA goes through several empty ones in a row before and after the
+    pieces that it has to work on."""
+    B, Hq, Hkv, D, P, per = 600, 4, 2, 64, 32, 1000
+    rng = np.random.default_rng(2)
+    lens = np.zeros(B, np.int32)
+    for b in (0, 7, 8, 40, 41, 43, 200, 299, 300, 450, 598):
+        lens[b] = rng.integers(1, 700)
+    lens[301] = 3000
+    used = int(sum(-(-n // P) for n in lens))
+    pages, scales, _ = new_cache(1, Hkv, used, P, D, seed=5)
+    table, at = np.full((B, per), -1, np.int32), 0   # (entries behind a sequence's last page are not read)
+    for b in np.flatnonzero(lens):
+        n = -(-int(lens[b]) // P)
+        table[b, :n] = np.arange(at, at + n)
+        at += n
+        kv = rng.standard_normal((2, 1, Hkv, int(lens[b]), D))
+        oracle.kv8_append(kv[0], kv[1], pages, scales, table[b:b + 1])
+    q, Q = rows(rng, (B, Hq, 1, D), "bf16")
+    gp, gs, gt, gl = to_gpu(pages, scales, table, lens)
+    lse = torch.empty(B, Hq, 1, device="cuda")
+    some = np.flatnonzero(lens)
+    ref = reference(q[some].astype(np.float64), pages, scales, table[some], lens[some], 0, 0)
+    for _ in range(20):
+        o = osf.osf_attn_kv8(Q, gp, gs, gt, lens=gl, lse=lse)
+        check_attn(o[some], lse[some], ref, "bf16", "mostly empty")
+        rest = torch.from_numpy(lens == 0).cuda()
+        assert (o[rest] == 0).all() and torch.isneginf(lse[rest]).all()
+    assert osf.osf_device_status() == osf.OSF_OK
