@@ -125,8 +125,9 @@ __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     return fabsf(h) <= kMaxF32 ? __fadd_rn(h, __fadd_rn(he, __fsub_rn(pe, qe))) : h;
 }
 
-// i / d for inv = floor(2^32 / d) + 1: exact for i < 2^32 / d.
-__device__ __forceinline__ int quotient(int i, uint32_t inv) { return (int)__umulhi((uint32_t)i, inv); }
+// i / d, exact for 0 <= i < 2^31: with 2^(s - 1) < d <= 2^s and inv = floor(2^(31 + s) / d) + 1, inv * d - 2^(31 + s) is in
+// 1 .. d, which moves i * inv / 2^(31 + s) away from i / d by less than 2^31 / 2^(31 + s) <= 1 / d.
+__device__ __forceinline__ int quotient(int i, uint32_t inv, int shift) { return (int)(__umulhi((uint32_t)i, inv) >> shift); }
 
 // Where the 2 W channels of unit u of a row lie: two runs of W, at first and second.  The W pairs of a unit that is rotated
 // have the angles in columns angle .. angle + W - 1 of the tables.
@@ -232,7 +233,7 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
         Unit w;
     };
     auto spot_of = [&](int i) {
-        const int t = quotient(i, p.units_inv);
+        const int t = quotient(i, p.units_inv, p.units_shift);
         return Spot{t, unit_of<W>(i - t * units, R, p.interleaved)};
     };
     auto load = [&](const Spot &o, float (&x)[2 * W]) {
@@ -348,7 +349,7 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
 template <typename T, int W, int HB>
 __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc, int i, int q_vec, int o_vec) {
     const int units = p.c.D / (2 * W), chunks = (p.Hq + HB - 1) / HB;
-    const int b = bc / chunks, h0 = bc % chunks * HB, t = quotient(i, p.units_inv), u = i - t * units;
+    const int b = bc / chunks, h0 = bc % chunks * HB, t = quotient(i, p.units_inv, p.units_shift), u = i - t * units;
     if (t >= (p.counts ? min(p.counts[b], p.n) : p.n)) return;
     const Unit w = unit_of<W>(u, p.R, p.interleaved);
     const T *src = static_cast<const T *>(p.q) + b * p.q_sb + h0 * p.q_sh + t * p.q_ss;
@@ -486,7 +487,9 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
 template <typename T, int W>
 cudaError_t append_w(Kv8StoreProblem p, int sm_count, cudaStream_t s) {
     const Kv8Cache &c = p.c;
-    p.units_inv = (unsigned)((1ULL << 32) / (c.D / (2 * W)) + 1);
+    const int units = c.D / (2 * W);   // 2 .. 32
+    p.units_shift = 31 - __builtin_clz(units - 1);   // s - 1
+    p.units_inv = (unsigned)((1ULL << (32 + p.units_shift)) / units + 1);
     const long long pages = ((long long)p.n + 2 * c.P - 2) / c.P;
     const int per_seq = (int)(pages < c.per_seq ? pages : c.per_seq);
     // a warp to a page while a page's new tokens fit its lanes' registers

@@ -28,7 +28,8 @@ struct Kv8StoreProblem {
     const int *starts;          // read: first token of each sequence (nullable: 0)
     const float *cos, *sin;     // [max_pos][R / 2], or null
     int max_pos, R, interleaved;
-    unsigned units_inv;         // 2^32 over the units of a row, rounded up
+    unsigned units_inv;         // for divisions by the units of a row
+    int units_shift;
     int table_vec;              // the tables' rows can be read 16 bytes at a time
     int dtype, B, Hq, n;
     long long k_sb, k_sh, k_ss, v_sb, v_sh, v_ss, q_sb, q_sh, q_ss, o_sb, o_sh, o_ss;

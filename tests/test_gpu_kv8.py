@@ -489,3 +489,53 @@ def test_mostly_empty_batch(osf):
         rest = torch.from_numpy(lens == 0).cuda()
         assert (o[rest] == 0).all() and torch.isneginf(lse[rest]).all()
     assert osf.osf_device_status() == osf.OSF_OK
+
+
+def test_a_cache_past_2_31_bytes(osf):
+    """More tokens than 2^22 of D = 256 in one call, into more than 2^31 bytes of pages: what is stored, rotated and read there."""
+    D, P, R, n = 256, 128, 8, (1 << 22) + 37
+    per = -(-n // P)
+    rng = np.random.default_rng(3)
+    k, K = rows(rng, (1, 1, 1, D), "bf16")
+    v, V = rows(rng, (1, 1, 1, D), "bf16")
+    q, Q = rows(rng, (1, 1, 1, D), "bf16")
+    wide = [x.expand(1, 1, n, D) for x in (K, V, Q)]   # every token the same row
+    ang = torch.arange(n, device="cuda", dtype=torch.float64)[:, None] * torch.tensor([1.0, 0.1, 0.01, 0.001], device="cuda", dtype=torch.float64)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    gp = torch.zeros(per, 2, 1, P, D, dtype=torch.uint8, device="cuda")
+    gs = torch.ones(per, 2, 1, device="cuda")
+    table = torch.randperm(per, device="cuda", dtype=torch.int32)[None]
+    qo = osf.osf_kv8_append(wide[0], wide[1], gp, gs, table, cos=cos, sin=sin, q=wide[2])
+    some = np.r_[0, 1, 4097, n // 2, (1 << 22) - 2:(1 << 22) + 2, n - 40:n]
+    c, s = cos.cpu().numpy(), sin.cpu().numpy()
+    ref = oracle.rotate(np.repeat(q[0], len(some), 1), some, c, s, False)
+    check_rotated(qo[0][:, some], np.repeat(q[0], len(some), 1), ref, "bf16")
+    # the pages of those tokens, filled again by the oracle
+    pages = np.unique(some // P)
+    for pg in pages:
+        t = np.arange(pg * P, min(n, (pg + 1) * P))
+        op, os_ = np.zeros((1, 2, 1, P, D), np.uint8), np.ones((1, 2, 1), np.float32)
+        oracle.kv8_append(np.repeat(k, len(t), 2), np.repeat(v, len(t), 2), op, os_, np.zeros((1, 1), np.int32), None, None, c[t], s[t])
+        at = int(table[0, pg])
+        assert np.array_equal(gp[at].cpu().numpy(), op[0]) and np.array_equal(gs[at].cpu().numpy(), os_[0])
+        rk, rv = osf.osf_kv8_read(gp, gs, table, len(t), starts=torch.tensor([t[0]], dtype=torch.int32, device="cuda"),
+                                  dtype=torch.float32)
+        kv = oracle.kv8_values(op, os_, np.zeros(1, np.int32), len(t))
+        assert np.array_equal(rk[0].cpu().numpy(), kv[0]) and np.array_equal(rv[0].cpu().numpy(), kv[1])
+    assert osf.osf_device_status() == osf.OSF_OK
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 128), ("bf16", 256)])
+def test_attention_over_pages_past_2_31_bytes(osf, dtype, D):
+    """A short sequence whose pages lie at the end of a large cache gives what it gives with the same pages in a small one."""
+    Hkv, P, n = 8, 128, 1000
+    pages, scales, table = fill_cache(1, Hkv, P, D, [n], seed=12)
+    n_pages = (1 << 31) // (2 * Hkv * P * D) + 20
+    big = torch.zeros(n_pages, 2, Hkv, P, D, dtype=torch.uint8, device="cuda")
+    bs = torch.ones(n_pages, 2, Hkv, device="cuda")
+    gp, gs, gt, gl = to_gpu(pages, scales, table, np.array([n], np.int32))
+    big[-len(pages):], bs[-len(pages):] = gp, gs
+    q = torch.randn(1, 32, 1, D, device="cuda").to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    o = osf.osf_attn_kv8(q, gp, gs, gt, lens=gl)
+    assert torch.equal(osf.osf_attn_kv8(q, big, bs, gt + (n_pages - len(pages)), lens=gl), o)
+    assert osf.osf_device_status() == osf.OSF_OK
