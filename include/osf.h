@@ -176,7 +176,8 @@ int osf_attn_fwd_gqa_ex(const void *Q, const void *K, const void *V, void *O, in
  * K and V of keys that no row sees are not read, or (in a tile of 32 .. 128 keys that some row sees a part of) of no effect as
  * long as V is finite.
  * strides, scale, lse, errors: as there.  A row that sees no key (p < 0, or Sk == 0) gets O = 0 and lse = -inf.
- * workspace: osf_attn_window_workspace_bytes with the same sizes, window and sinks.
+ * workspace: osf_attn_window_workspace_bytes bytes, with the same sizes, window and sinks, 16-byte aligned.
+ * Buffers that do not start on a boundary of their elements: OSF_ERR_INVALID.
  * Sq or Sk >= 2^29: OSF_ERR_UNSUPPORTED.
  * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores (bfloat16 with D 32 and 96 too), CUDA cores.
  */
@@ -381,7 +382,8 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
  * Tokens that would fall behind table_len * P are not stored, and recorded as OSF_ERR_INVALID in the device status word, as
  * are counts out of range (cut to it), a negative length (nothing of that sequence is stored) and positions that the tables
  * do not hold (the last one is taken).
- * n == 0 or B == 0: OSF_OK.  n > table_len * P without counts, outputs that overlap an input, NULL pointers: OSF_ERR_INVALID.
+ * n == 0 or B == 0: OSF_OK.  n > table_len * P without counts, outputs that overlap an input, NULL pointers, buffers that do
+ * not start on a boundary of their elements: OSF_ERR_INVALID.
  */
 int osf_kv8_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D,
                    const long long *strides, void *pages, float *scales, int n_pages, int page_tokens,

@@ -715,6 +715,16 @@ int osf_attn_bwd_gqa(const void *Q, const void *K, const void *V, const void *O,
     return launch_status(launch_attn_bwd(b, (cudaStream_t)stream));
 }
 
+// A workspace of `need` bytes: large enough, and aligned for the 16-byte accesses that the kernels make to it.
+static int check_workspace(const void *workspace, size_t bytes, size_t need) {
+    if (need == 0) return OSF_OK;
+    if (!workspace || bytes < need) return OSF_ERR_WORKSPACE;
+    return (reinterpret_cast<uintptr_t>(workspace) & 15u) ? OSF_ERR_INVALID : OSF_OK;
+}
+
+// Whether a pointer is not on a boundary of its elements (a kernel's access to it would be a fault).
+static bool misaligned(const void *q, size_t es) { return reinterpret_cast<uintptr_t>(q) % es != 0; }
+
 // ------------------------------------------------------------------ a window with sinks
 // The checks of a windowed problem: those of a bottom-right one, then the window.  One that hides nothing is dropped, but where
 // the windowed kernels are the faster ones: `keep` (the window then is the whole sequence).
@@ -725,6 +735,8 @@ static int check_window(const void *Q, const void *K, const void *V, void *O, in
     if (window < 1 || sinks < 0) return OSF_ERR_INVALID;
     const int st = check_gqa_ex(Q, K, V, O, dtype, B, Hq, Hkv, Sq, Sk, D, strides, OSF_MASK_BOTTOM_RIGHT, scale, lse, p, empty);
     if (st != OSF_OK || empty) return st;
+    const size_t es = elem_size(dtype);
+    if (misaligned(Q, es) || misaligned(K, es) || misaligned(V, es) || misaligned(O, es) || misaligned(lse, 4)) return OSF_ERR_INVALID;
     // kernels add lengths and the window in ints
     if (Sq >= (1 << 29) || Sk >= (1 << 29)) return OSF_ERR_UNSUPPORTED;
     // the last row sees the most hidden keys: those between the sinks and its window
@@ -789,7 +801,10 @@ int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O
         return run_gqa(p, Path::Simt, nullptr, 0, 1, dev, (cudaStream_t)stream);
     }
     const Path path = choose_path(p, Q, K, V, O);
-    return run_gqa(p, path, workspace, workspace_bytes, plan_splits(p, path, dev->sm_count, 0), dev, (cudaStream_t)stream);
+    const int splits = plan_splits(p, path, dev->sm_count, 0);
+    const int ws = check_workspace(workspace, workspace_bytes, path_workspace(p, path, splits));
+    if (ws != OSF_OK) return ws;
+    return run_gqa(p, path, workspace, workspace_bytes, splits, dev, (cudaStream_t)stream);
 }
 
 // Workspace of the windowed backward: row sums | sums of the key tiles that several CTAs share | dS^T tiles that some row sees,
@@ -857,6 +872,8 @@ int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const v
     BwdProblem b;
     const int sb = check_bwd(p, O, dO, lse, dK, dV, b);
     if (sb != OSF_OK) return sb;
+    const size_t es = elem_size(dtype);
+    if (misaligned(O, es) || misaligned(dO, es) || misaligned(lse, 4) || misaligned(dK, es) || misaligned(dV, es)) return OSF_ERR_INVALID;
     DeviceInfo *dev;
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     keep_small(p, dev->sm_count);
@@ -926,13 +943,6 @@ int osf_softmax_rows_ex(const void *x, void *z, int x_dtype, int z_dtype, long l
     SoftmaxExProblem q{x, z, x_dtype, z_dtype, rows, T, xs, zs, sc * kLog2e, causal_period, dev->sm_count,
                        dev->status};
     return launch_status(launch_softmax_ex(q, static_cast<float *>(workspace), (cudaStream_t)stream));
-}
-
-// A workspace of `need` bytes: large enough, and aligned for the 16-byte accesses that the kernels make to it.
-static int check_workspace(const void *workspace, size_t bytes, size_t need) {
-    if (need == 0) return OSF_OK;
-    if (!workspace || bytes < need) return OSF_ERR_WORKSPACE;
-    return (reinterpret_cast<uintptr_t>(workspace) & 15u) ? OSF_ERR_INVALID : OSF_OK;
 }
 
 // ------------------------------------------------------------------ weights of keys
@@ -1226,6 +1236,7 @@ static int check_kv8(const void *pages, const float *scales, int n_pages, int pa
 }
 static int check_kv8_buffers(const Kv8Cache &c, int B) {
     if ((c.n_pages > 0 && (!c.pages || !c.scales)) || (B > 0 && c.per_seq > 0 && !c.table)) return OSF_ERR_INVALID;
+    if (misaligned(c.scales, 4) || misaligned(c.table, 4)) return OSF_ERR_INVALID;
     return (reinterpret_cast<uintptr_t>(c.pages) & 15u) != 0 ? OSF_ERR_INVALID : OSF_OK;
 }
 // The cache's three buffers, for the checks of overlaps.
@@ -1270,7 +1281,11 @@ int osf_kv8_append(const void *K, const void *V, int dtype, int B, int Hkv, int 
     st = check_kv8_buffers(c, B);
     if (st != OSF_OK) return st;
     if ((long long)table_len * page_tokens < n && !counts) return OSF_ERR_INVALID;
-    const size_t es = elem_size(dtype), nt = (size_t)max_positions * (rotary_dim / 2) * sizeof(float);
+    const size_t es = elem_size(dtype);
+    if (misaligned(K, es) || misaligned(V, es) || misaligned(Q, es) || misaligned(Q_out, es) || misaligned(lens, 4) ||
+        misaligned(counts, 4) || misaligned(cos_table, 4) || misaligned(sin_table, 4))
+        return OSF_ERR_INVALID;
+    const size_t nt = (size_t)max_positions * (rotary_dim / 2) * sizeof(float);
     const size_t nk = span_bytes(B, Hkv, n, D, sd[0], sd[1], sd[2], es), nv = span_bytes(B, Hkv, n, D, sd[3], sd[4], sd[5], es);
     const size_t nq = Q ? span_bytes(B, Hq, n, D, sd[6], sd[7], sd[8], es) : 0;
     const size_t no = Q ? span_bytes(B, Hq, n, D, sd[9], sd[10], sd[11], es) : 0;
@@ -1312,7 +1327,8 @@ int osf_kv8_read(const void *pages, const float *scales, int n_pages, int page_t
     if (!K || !V) return OSF_ERR_INVALID;
     st = check_kv8_buffers(p.c, B);
     if (st != OSF_OK) return st;
-    const size_t no = (size_t)B * Hkv * n * D * elem_size(dtype);
+    const size_t es = elem_size(dtype), no = (size_t)B * Hkv * n * D * es;
+    if (misaligned(K, es) || misaligned(V, es) || misaligned(starts, 4) || misaligned(lens, 4)) return OSF_ERR_INVALID;
     const Kv8Buffers cb = kv8_buffers(p.c, B);
     const void *in[5] = {cb.at[0], cb.at[1], cb.at[2], starts, lens};
     const size_t in_n[5] = {cb.size[0], cb.size[1], cb.size[2], (size_t)B * 4, (size_t)B * 4};
@@ -1348,6 +1364,7 @@ static int check_attn_kv8(const void *Q, const void *pages, const float *scales,
     if (st != OSF_OK) return st;
     if (!rows_disjoint(B, Hq, Sq, D, sd[3], sd[4], sd[5])) return OSF_ERR_INVALID;
     const size_t es = elem_size(dtype);
+    if (misaligned(Q, es) || misaligned(O, es) || misaligned(lse, 4) || misaligned(lens, 4)) return OSF_ERR_INVALID;
     const Kv8Buffers cb = kv8_buffers(kp.c, B);
     const void *bufs[7] = {O, lse, Q, cb.at[0], cb.at[1], cb.at[2], lens};
     const size_t size[7] = {span_bytes(B, Hq, Sq, D, sd[3], sd[4], sd[5], es), (size_t)B * Hq * Sq * sizeof(float),

@@ -210,3 +210,40 @@ def test_attn_kv8_refusals(osf):
     assert f(1, 1, 4, 2, 1, 64, 17, 2, 0, 0, ctypes.byref(n)) == U and n.value == 0
     assert f(1, 1, 4, 2, 1, 64, 16, 2, -1, 0, ctypes.byref(n)) == I
     assert f(1, 1, 4, 2, 0, 64, 16, 2, 0, 0, ctypes.byref(n)) == osf.OSF_OK and n.value == 0
+
+
+def test_misaligned_buffers_are_refused(osf):
+    """A buffer that does not start on a boundary of its elements would fault in a kernel."""
+    lib, I = osf.lib(), osf.OSF_ERR_INVALID
+
+    def off(p, by):
+        return ctypes.c_void_p(p.value + by)
+    for dtype, by in ((1, 1), (0, 2)):
+        for i in range(4):
+            ptrs = list(P[:4])
+            ptrs[i] = off(ptrs[i], by)
+            assert _window(lib, dtype=dtype, ptrs=ptrs) == I, i
+        for i in range(9):
+            ptrs = list(P[:9])
+            ptrs[i] = off(ptrs[i], by)
+            assert _window(lib, False, dtype=dtype, ptrs=ptrs) == I, i
+        for name, p in (("k", P[0]), ("v", P[1]), ("Q", P[8]), ("Qo", P[9])):
+            assert _append(lib, dtype=dtype, **{**dict(Q=P[8], Qo=P[9], Hq=2), name: off(p, by)}) == I, name
+        for i in range(2):
+            kv = [P[3], P[4]]
+            kv[i] = off(kv[i], by)
+            assert lib.osf_kv8_read(P[0], P[1], 4, 16, P[2], 2, *kv, dtype, 1, 2, 3, 64, None, None, None) == I
+            qo = [P[3], P[4]]
+            qo[i] = off(qo[i], by)
+            assert lib.osf_attn_kv8(qo[0], P[0], P[1], qo[1], dtype, 1, 4, 2, 1, 4, 16, 64, None, P[2], 2, None, 0, 0, 0.0, None,
+                                    None, 0, None) == I
+    assert _window(lib, lse=off(P[4], 2)) == I
+    for name, p in (("scales", P[3]), ("table", P[4]), ("cos", P[5]), ("sin", P[6]), ("lens", P[10]), ("counts", P[11])):
+        assert _append(lib, **{name: off(p, 2)}) == I, name
+    for args in ((off(P[1], 2), P[2], None, None), (P[1], off(P[2], 1), None, None), (P[1], P[2], off(P[5], 2), None),
+                 (P[1], P[2], None, off(P[6], 2))):
+        scales, table, lens, lse = args
+        assert lib.osf_attn_kv8(P[3], P[0], scales, P[4], 1, 1, 4, 2, 1, 4, 16, 64, None, table, 2, lens, 0, 0, 0.0, lse, None, 0,
+                                None) == I
+        if lse is None:
+            assert lib.osf_kv8_read(P[0], scales, 4, 16, table, 2, P[3], P[4], 1, 1, 2, 3, 64, lens, None, None) == I
