@@ -539,3 +539,68 @@ def test_attention_over_pages_past_2_31_bytes(osf, dtype, D):
     o = osf.osf_attn_kv8(q, gp, gs, gt, lens=gl)
     assert torch.equal(osf.osf_attn_kv8(q, big, bs, gt + (n_pages - len(pages)), lens=gl), o)
     assert osf.osf_device_status() == osf.OSF_OK
+
+
+@pytest.mark.parametrize("dtype,B,Hq,Hkv,Sq,D,P,per,lens,window", [
+    ("bf16", 1, 8, 2, 1, 128, 64, 100, [6000], 0), ("bf16", 2, 16, 2, 2, 64, 16, 400, [10, 6000], 4000),
+    ("bf16", 3, 12, 1, 3, 96, 32, 300, [9000, 1, 0], 0), ("f32", 2, 4, 2, 1, 64, 64, 40, [2000, 30], 0),
+    ("bf16", 1, 4, 4, 3, 160, 64, 40, [2500], 1500)])
+def test_attention_stays_in_its_workspace(osf, dtype, B, Hq, Hkv, Sq, D, P, per, lens, window):
+    code = osf.OSF_BF16 if dtype == "bf16" else osf.OSF_F32
+    pages, scales, table = fill_cache(B, Hkv, P, D, [per * P] * B, seed=2)
+    gp, gs, gt, gl = to_gpu(pages, scales, table, np.array(lens, np.int32))
+    _, Q = rows(np.random.default_rng(1), (B, Hq, Sq, D), dtype)
+    n = osf.osf_attn_kv8_workspace_bytes(code, B, Hq, Hkv, Sq, D, P, per, window, 4)
+    assert n > 0
+    whole = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    ref = osf.osf_attn_kv8(Q, gp, gs, gt, lens=gl, window=window, sinks=4)
+    assert torch.equal(osf.osf_attn_kv8(Q, gp, gs, gt, lens=gl, window=window, sinks=4, workspace=whole[:n]), ref)
+    assert (whole[n:] == 0xA5).all()
+    for part, status in ((whole[:n - 1], osf.OSF_ERR_WORKSPACE), (whole[8:n + 8], osf.OSF_ERR_INVALID)):
+        with pytest.raises(osf.OsfError) as e:
+            osf.osf_attn_kv8(Q, gp, gs, gt, lens=gl, window=window, sinks=4, workspace=part)
+        assert e.value.status == status
+
+
+def test_a_prefix_shared_by_two_sequences(osf):
+    """Two sequences whose tables name the same full pages, then pages of their own."""
+    Hkv, D, P = 2, 64, 16
+    rng = np.random.default_rng(4)
+    pages, scales, _ = new_cache(1, Hkv, 12, P, D, seed=9)
+    table = np.array([[0, 1, 2, 3, -1, -1], [0, 1, 2, 5, 6, 7]], np.int32)
+    kv = rng.standard_normal((2, 1, Hkv, 48, D))
+    oracle.kv8_append(kv[0], kv[1], pages, scales, table[:1])
+    gp, gs, gt, gl = to_gpu(pages, scales, table, np.array([48, 48], np.int32))
+    k, K = rows(rng, (2, Hkv, 20, D), "bf16")
+    counts = [9, 20]
+    osf.osf_kv8_append(K, K, gp, gs, gt, lens=gl, counts=to_gpu(np.array(counts, np.int32))[0])
+    oracle.kv8_append(k, k, pages, scales, table, [48, 48], counts)
+    assert np.array_equal(gp.cpu().numpy(), pages) and np.array_equal(gs.cpu().numpy(), scales)
+    lens = [57, 68]
+    q, Q = rows(rng, (2, 4, 3, D), "bf16")
+    lse = torch.empty(2, 4, 3, device="cuda")
+    o = osf.osf_attn_kv8(Q, gp, gs, gt, lens=to_gpu(np.array(lens, np.int32))[0], lse=lse)
+    check_attn(o, lse, reference(q.astype(np.float64), pages, scales, table, lens, 0, 0), "bf16", "shared prefix")
+    assert osf.osf_device_status() == osf.OSF_OK
+
+
+def test_two_graphs_with_one_workspace(osf):
+    """Two captured calls of different sizes that use one workspace, replayed in turn on one stream."""
+    lens = [5000]
+    pages, scales, table = fill_cache(1, 2, 64, 64, lens, seed=8)
+    gp, gs, gt, gl = to_gpu(pages, scales, table, np.array(lens, np.int32))
+    qs = [torch.randn(1, 8, s, 64, device="cuda").bfloat16() for s in (1, 4)]
+    need = [osf.osf_attn_kv8_workspace_bytes(osf.OSF_BF16, 1, 8, 2, s, 64, 64, gt.shape[1], 0, 0) for s in (1, 4)]
+    ws = torch.empty(max(need), dtype=torch.uint8, device="cuda")
+    alone = [osf.osf_attn_kv8(q, gp, gs, gt, lens=gl) for q in qs]
+    outs, graphs = [torch.empty_like(q) for q in qs], []
+    for q, o in zip(qs, outs):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            osf.osf_attn_kv8(q, gp, gs, gt, lens=gl, out=o, workspace=ws)
+    for _ in range(5):
+        for o in outs:
+            o.zero_()
+        for g in graphs:
+            g.replay()
+        assert all(torch.equal(a, b) for a, b in zip(outs, alone))

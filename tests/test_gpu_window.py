@@ -236,3 +236,88 @@ def test_captured_training_step(osf):
     got = [x.clone() for x in (o, lse, *grads)]
     step()
     assert all(torch.equal(a, b) for a, b in zip(got, (o, lse, *grads)))
+
+
+def guarded(n):
+    """A workspace of exactly n bytes, and the bytes behind it."""
+    whole = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+    return whole[:n], whole[n:]
+
+
+@pytest.mark.parametrize("dtype,B,Hq,Hkv,Sq,Sk,D,window,sinks", [
+    ("bf16", 1, 8, 2, 1, 9000, 128, 4096, 4), ("bf16", 1, 8, 2, 2, 5000, 96, 3000, 0), ("f32", 1, 4, 2, 3, 4000, 64, 3000, 9),
+    ("f32", 1, 2, 1, 40, 4000, 100, 3000, 9), ("bf16", 1, 4, 2, 100, 8000, 64, 5000, 4), ("bf16", 1, 2, 1, 17, 8000, 72, 5000, 4)])
+def test_forward_stays_in_its_workspace(osf, dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks):
+    dev, code = (bf16_tensor, osf.OSF_BF16) if dtype == "bf16" else (f32_tensor, osf.OSF_F32)
+    q, k, v = (dev(x) for x in si.qkv((B, Hq, Sq, D), (B, Hkv, Sk, D), seed=1, dtype=dtype))
+    n = osf.osf_attn_window_workspace_bytes(code, B, Hq, Hkv, Sq, Sk, D, window, sinks)
+    assert n > 0
+    ws, behind = guarded(n)
+    ref = osf.osf_attn_fwd_gqa_window(q, k, v, window, sinks)
+    assert torch.equal(osf.osf_attn_fwd_gqa_window(q, k, v, window, sinks, workspace=ws), ref)
+    assert (behind == 0xA5).all()
+    for part, status in ((ws[:16], osf.OSF_ERR_WORKSPACE), (guarded(n + 8)[0][8:], osf.OSF_ERR_INVALID)):
+        with pytest.raises(osf.OsfError) as e:
+            osf.osf_attn_fwd_gqa_window(q, k, v, window, sinks, workspace=part)
+        assert e.value.status == status
+
+
+@pytest.mark.parametrize("dtype,B,Hq,Hkv,Sq,Sk,D,window,sinks", [
+    ("bf16", 1, 4, 2, 1000, 1000, 64, 300, 4), ("bf16", 1, 8, 2, 700, 900, 96, 200, 0), ("bf16", 4, 32, 8, 1024, 1024, 128, 200, 5),
+    ("bf16", 2, 32, 8, 1500, 1500, 64, 100, 0), ("f32", 1, 4, 2, 301, 301, 64, 65, 3), ("bf16", 2, 32, 8, 1000, 1000, 64, 2000, 0)])
+def test_backward_stays_in_its_workspace(osf, dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks):
+    dev, code = (bf16_tensor, osf.OSF_BF16) if dtype == "bf16" else (f32_tensor, osf.OSF_F32)
+    q, k, v = (dev(x) for x in si.qkv((B, Hq, Sq, D), (B, Hkv, Sk, D), seed=1, dtype=dtype))
+    g = dev(si.qkv((B, Hq, Sq, D), (1, 1, 1, D), seed=2, dtype=dtype)[0])
+    lse = torch.empty(B, Hq, Sq, device="cuda")
+    o = osf.osf_attn_fwd_gqa_window(q, k, v, window, sinks, lse=lse)
+    n = osf.osf_attn_bwd_window_workspace_bytes(code, B, Hq, Hkv, Sq, Sk, D, window, sinks)
+    ws, behind = guarded(n)
+    ref = osf.osf_attn_bwd_gqa_window(q, k, v, o, g, lse, window, sinks)
+    got = osf.osf_attn_bwd_gqa_window(q, k, v, o, g, lse, window, sinks, workspace=ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, ref)) and (behind == 0xA5).all()
+    with pytest.raises(osf.OsfError) as e:
+        osf.osf_attn_bwd_gqa_window(q, k, v, o, g, lse, window, sinks, workspace=ws[:64])
+    assert e.value.status == osf.OSF_ERR_WORKSPACE
+    if dtype == "bf16" and window < Sk:
+        with pytest.raises(osf.OsfError) as e:
+            osf.osf_attn_bwd_gqa_window(q, k, v, o, g, lse, window, sinks, workspace=guarded(n + 64)[0][64:])
+        assert e.value.status == osf.OSF_ERR_INVALID
+
+
+def test_two_streams_train_at_once(osf):
+    """Forward and backward on two streams, each with its own workspaces, give what they give alone."""
+    S, D, window, sinks = 1200, 128, 200, 4
+    sets = [[torch.randn(1, h, S, D, device="cuda").bfloat16() for h in (8, 2, 2, 8)] for _ in range(2)]
+
+    def step(q, k, v, g):
+        lse = torch.empty(1, 8, S, device="cuda")
+        o = osf.osf_attn_fwd_gqa_window(q, k, v, window, sinks, lse=lse)
+        return (o, lse, *osf.osf_attn_bwd_gqa_window(q, k, v, o, g, lse, window, sinks))
+    alone = [step(*x) for x in sets]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(step(*sets[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for got in outs[i]:
+            assert all(torch.equal(a, b) for a, b in zip(got, alone[i]))
+    assert osf.osf_device_status() == osf.OSF_OK
+
+
+def test_shared_keys_across_the_batch(osf):
+    """K and V expanded over heads and batch (strides of 0, another kernel than their copies') give what their copies do, each
+    within the bounds."""
+    q, k, v = si.qkv((3, 4, 50, 64), (1, 1, 400, 64), seed=3, dtype="bf16")
+    Q, K, V = (bf16_tensor(x) for x in (q, k, v))
+    wide = [x.expand(3, 2, 400, 64) for x in (K, V)]
+    for n in (50, 1):
+        ref = oracle.attention_window(f64(q, "bf16")[:, :, :n], *(np.tile(f64(x, "bf16"), (3, 2, 1, 1)) for x in (k, v)), 100, 3)
+        for kv in (wide, [x.contiguous() for x in wide]):
+            lse = torch.empty(3, 4, n, device="cuda")
+            o = osf.osf_attn_fwd_gqa_window(Q[:, :, :n], *kv, 100, 3, lse=lse)
+            check_out(o, lse, ref, "bf16", f"{n} rows")
