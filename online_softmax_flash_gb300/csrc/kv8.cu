@@ -1,13 +1,17 @@
 // Storing rows in the paged 8-bit K/V cache, with the position rotation on the way, and reading them back (format:
 // kv8.cuh).
 //
-// Appending: a block takes one page of one kv head, K or V.  K's rows are rotated: channels a, b of a pair by the angle of
-// their position become a c - b s and b c + a s, rounded once to float32 (both products and their difference are kept with
-// their rounding errors, so the codes are those of the formulas and not of some order of float32 operations).  The page's
-// scale is 2^e with the least e for which its largest magnitude is at most 448 * 2^e; a page that holds earlier tokens
+// Appending: a block (or, of few tokens, a warp) takes one page of one kv head, K or V.  K's rows are rotated: channels a, b of
+// a pair by the angle of their position become a c - b s and b c + a s, rounded once to float32, so the codes are those of the
+// formulas and not of some order of float32 operations (rotate1; all but the few values near a tie need only rotate2).  The
+// page's scale is 2^e with the least e for which its largest magnitude is at most 448 * 2^e; a page that holds earlier tokens
 // keeps its scale unless the new ones need a larger one, and then the codes there are rounded again: e4m3 codes only
 // change their exponent, so that is exact but for those that fall among the subnormals.  NaN and infinities are stored as
 // NaN and leave the scale alone.
+// A block goes through one chain: lengths and table, then rows and angles, then the scale; the reduction; the stores.  That, not
+// DRAM, bounds it: three blocks of 256 threads to an SM hide most of it (8 prompts of 4096 tokens, 8 heads of 128, 168 MB
+// without queries: 74 us, 2.3 TB/s; two or four blocks 87, 107; two blocks of 512 threads 111; angles loaded behind the check of the
+// table's entry 85; every value by rotate1 2 us more).  With the queries of 32 heads, 704 MB: 138 us, 5.1 TB/s.
 #include "kv8.cuh"
 #include "sm100_ptx.cuh"
 
@@ -124,6 +128,15 @@ __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     const float he = __fsub_rn(__fsub_rn(p, __fsub_rn(h, t)), __fadd_rn(q, t));   // h + he = p - q
     return fabsf(h) <= kMaxF32 ? __fadd_rn(h, __fadd_rn(he, __fsub_rn(pe, qe))) : h;
 }
+// a c - b s within 2 units in the last place, whatever cancels: the rounding error of b s, exact, is added back.
+__device__ __forceinline__ float rotate2(float a, float c, float b, float s) {
+    const float q = __fmul_rn(b, s);
+    return __fadd_rn(__fmaf_rn(a, c, -q), __fmaf_rn(-b, s, q));
+}
+// Whether the code (or the page's scale) could be another if x were up to 8 units off.  An e4m3 code keeps 3 bits of the
+// fraction or fewer, so ties have zeros in the last 19 (of a coarser code more of them), and so have 448 * 2^e, infinity and NaN
+// (its last bits are ones).
+__device__ __forceinline__ bool near_tie(float x) { return ((__float_as_uint(x) + 8u) & 0x7ffffu) < 16u; }
 
 // i / d, exact for 0 <= i < 2^31: with 2^(s - 1) < d <= 2^s and inv = floor(2^(31 + s) / d) + 1, inv * d - 2^(31 + s) is in
 // 1 .. d, which moves i * inv / 2^(31 + s) away from i / d by less than 2^31 / 2^(31 + s) <= 1 / d.
@@ -169,19 +182,22 @@ __device__ __forceinline__ void join_pairs(float (&x)[2 * W], bool interleaved, 
     }
 }
 
-// A unit of K, rotated exactly.
+// A unit of K, rotated: the values that near_tie lets through give the codes that the exact ones would give.
 template <int W>
-__device__ __forceinline__ void rotate_unit(const Kv8StoreProblem &p, const Unit &w, int pos, float (&x)[2 * W]) {
-    float c[W], s[W], a[W], b[W];
-    load_angles<W>(p, w, pos, c, s);
-    split_pairs<W>(x, p.interleaved, a, b);
+__device__ __forceinline__ void rotate_unit(bool interleaved, const float (&c)[W], const float (&s)[W], float (&x)[2 * W]) {
+    float a[W], b[W];
+    split_pairs<W>(x, interleaved, a, b);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
-        const float ra = rotate1(a[i], c[i], b[i], s[i]), rb = rotate1(b[i], c[i], -a[i], s[i]);
+        float ra = rotate2(a[i], c[i], b[i], s[i]), rb = rotate2(b[i], c[i], -a[i], s[i]);
+        if (near_tie(ra) || near_tie(rb)) {
+            ra = rotate1(a[i], c[i], b[i], s[i]);
+            rb = rotate1(b[i], c[i], -a[i], s[i]);
+        }
         a[i] = ra;
         b[i] = rb;
     }
-    join_pairs<W>(x, p.interleaved, a, b);
+    join_pairs<W>(x, interleaved, a, b);
 }
 
 // Codes of four values.  ODD: some of the page's are NaN or infinite.
@@ -204,7 +220,7 @@ __device__ __forceinline__ void store_codes(unsigned char *p, const float *x, fl
 // The new tokens of one page of one kv head, K or V, by `size` threads: a warp (few tokens) or a block.  K units per thread
 // stay in registers between the search for the largest magnitude and the rounding.
 template <typename T, int W, bool BLOCK>
-__device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, int half, int page_no, int me, int size, bool vec) {
+__device__ __forceinline__ void append_page(const Kv8StoreProblem &p, bool interleaved, int bh, int half, int page_no, int me, int size, bool vec) {
     constexpr int KEEP = W == 8 ? 2 : 4;
     __shared__ uint32_t sh_max[kThreads / 32];
     const Kv8Cache &c = p.c;
@@ -234,15 +250,18 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
     };
     auto spot_of = [&](int i) {
         const int t = quotient(i, p.units_inv, p.units_shift);
-        return Spot{t, unit_of<W>(i - t * units, R, p.interleaved)};
+        return Spot{t, unit_of<W>(i - t * units, R, interleaved)};
+    };
+    auto angles = [&](const Spot &o, float (&c)[W], float (&s)[W]) {
+        if (o.w.rotated) load_angles<W>(p, o.w, min(t0 + o.t, p.max_pos - 1), c, s);
     };
     auto load = [&](const Spot &o, float (&x)[2 * W]) {
         const T *row = rows + o.t * ss;
+        float c[W], s[W];
         load_run<W>(row + o.w.first, vec, x);
         load_run<W>(row + o.w.second, vec, x + W);
-    };
-    auto rotate = [&](const Spot &o, float (&x)[2 * W]) {
-        if (o.w.rotated) rotate_unit<W>(p, o.w, min(t0 + o.t, p.max_pos - 1), x);
+        angles(o, c, s);
+        if (o.w.rotated) rotate_unit<W>(interleaved, c, s, x);
     };
     // the largest magnitude, as bits: a NaN or an infinity shows
     constexpr uint32_t INF = 0x7f800000u;
@@ -262,28 +281,42 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
         }
         return m;
     };
+    int page;
+    long long at;
+    float old_scale;
+    // (rows, angles and the table's entry on their way together)
     float kept[KEEP][2 * W];
     Spot spot[KEEP];
+    {
+        Raw<T, W> lo[KEEP], hi[KEEP];
+        float c[KEEP][W], s[KEEP][W];
 #pragma unroll
-    for (int k = 0; k < KEEP; ++k) {
-        spot[k] = spot_of(me + k * size);
-        if (me + k * size < work) load(spot[k], kept[k]);
-    }
-    const int page = kv8_checked(c, entry, p.status);
-    if (page < 0) return;
-    const long long at = ((long long)page * 2 + half) * c.Hkv + h;
-    const float old_scale = c.scales[at];
-#pragma unroll
-    for (int k = 0; k < KEEP; ++k)
-        if (me + k * size < work) {
-            rotate(spot[k], kept[k]);
-            largest(kept[k]);
+        for (int k = 0; k < KEEP; ++k) {
+            spot[k] = spot_of(me + k * size);
+            if (me + k * size < work) {
+                const T *row = rows + spot[k].t * ss;
+                lo[k].load(row + spot[k].w.first, vec);
+                hi[k].load(row + spot[k].w.second, vec);
+                angles(spot[k], c[k], s[k]);
+            }
         }
+        page = kv8_checked(p.c, entry, p.status);
+        if (page < 0) return;
+        at = ((long long)page * 2 + half) * p.c.Hkv + h;
+        old_scale = p.c.scales[at];
+#pragma unroll
+        for (int k = 0; k < KEEP; ++k)
+            if (me + k * size < work) {
+                lo[k].values(kept[k]);
+                hi[k].values(kept[k] + W);
+                if (spot[k].w.rotated) rotate_unit<W>(interleaved, c[k], s[k], kept[k]);
+                largest(kept[k]);
+            }
+    }
     for (int i = me + KEEP * size; i < work; i += size) {
         float x[2 * W];
         const Spot o = spot_of(i);
         load(o, x);
-        rotate(o, x);
         largest(x);
     }
     mx = of_all(mx);
@@ -294,7 +327,6 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
             float x[2 * W];
             const Spot o = spot_of(i);
             load(o, x);
-            rotate(o, x);
 #pragma unroll
             for (int e = 0; e < 2 * W; ++e) {
                 const uint32_t u = __float_as_uint(x[e]) & 0x7fffffffu;
@@ -337,7 +369,6 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
         float x[2 * W];
         const Spot o = spot_of(i);
         load(o, x);
-        rotate(o, x);
         store(o, x);
     }
     if constexpr (BLOCK) __syncthreads();   // (every thread has read the old scale)
@@ -347,11 +378,11 @@ __device__ __forceinline__ void append_page(const Kv8StoreProblem &p, int bh, in
 
 // The queries of the new tokens, rotated in float32.  A thread takes a unit of a token for HB heads: the angles are read once.
 template <typename T, int W, int HB>
-__device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc, int i, int q_vec, int o_vec) {
+__device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, bool interleaved, int bc, int i, int q_vec, int o_vec) {
     const int units = p.c.D / (2 * W), chunks = (p.Hq + HB - 1) / HB;
     const int b = bc / chunks, h0 = bc % chunks * HB, t = quotient(i, p.units_inv, p.units_shift), u = i - t * units;
     if (t >= (p.counts ? min(p.counts[b], p.n) : p.n)) return;
-    const Unit w = unit_of<W>(u, p.R, p.interleaved);
+    const Unit w = unit_of<W>(u, p.R, interleaved);
     const T *src = static_cast<const T *>(p.q) + b * p.q_sb + h0 * p.q_sh + t * p.q_ss;
     T *dst = static_cast<T *>(p.qo) + b * p.o_sb + h0 * p.o_sh + t * p.o_ss;
     float c[W], s[W];
@@ -371,14 +402,14 @@ __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc,
             hi[k].values(x + W);
             if (w.rotated) {
                 float a[W], b2[W];
-                split_pairs<W>(x, p.interleaved, a, b2);
+                split_pairs<W>(x, interleaved, a, b2);
 #pragma unroll
                 for (int e = 0; e < W; ++e) {
                     const float ra = fmaf(a[e], c[e], -(b2[e] * s[e])), rb = fmaf(b2[e], c[e], a[e] * s[e]);
                     a[e] = ra;
                     b2[e] = rb;
                 }
-                join_pairs<W>(x, p.interleaved, a, b2);
+                join_pairs<W>(x, interleaved, a, b2);
             }
             store_run<W>(dst + k * p.o_sh + w.first, o_vec, x);
             store_run<W>(dst + k * p.o_sh + w.second, o_vec, x + W);
@@ -386,25 +417,27 @@ __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, int bc,
 }
 
 // One launch: blocks for the pages that new tokens may fall into, and among them, spread evenly, blocks for the queries; the
-// former are bound by what they issue and the latter by memory.  Of the blocks before block i, i * page_share / 2^32 have
+// former wait on their chain of loads, a reduction and stores, and the latter are bound by memory.  Of the blocks before block i, i * page_share / 2^32 have
 // pages.
-template <typename T, int W, bool BLOCK, int HB>
+// INTER: whether pairs are interleaved (2: to be seen at run time).
+template <typename T, int W, bool BLOCK, int HB, int INTER>
 __global__ void __launch_bounds__(kThreads, 3)
 kv8_append_kernel(const Kv8StoreProblem p, int pages_per_seq, unsigned long long page_share, unsigned q_blocks, int k_vec,
                   int v_vec, int q_vec, int o_vec) {
     const Kv8Cache &c = p.c;
+    const bool inter = INTER == 2 ? p.interleaved != 0 : INTER != 0;
     const unsigned page_block = (unsigned)(blockIdx.x * page_share >> 32);
     if ((unsigned)((blockIdx.x + 1) * page_share >> 32) == page_block) {
         // q_blocks blocks to each (batch, HB heads)
         const unsigned qb = blockIdx.x - page_block, bc = qb / q_blocks;
-        rotate_queries<T, W, HB>(p, (int)bc, (int)((qb - bc * q_blocks) * kThreads + threadIdx.x), q_vec, o_vec);
+        rotate_queries<T, W, HB>(p, inter, (int)bc, (int)((qb - bc * q_blocks) * kThreads + threadIdx.x), q_vec, o_vec);
         return;
     }
     const unsigned task = BLOCK ? page_block : page_block * (kThreads / 32) + (threadIdx.x >> 5);
     const unsigned bhh = task / pages_per_seq;
     const int page_no = (int)(task - bhh * pages_per_seq), half = (int)(bhh & 1), bh = (int)(bhh >> 1);
     if (bh >= p.B * c.Hkv) return;
-    append_page<T, W, BLOCK>(p, bh, half, page_no, BLOCK ? threadIdx.x : threadIdx.x & 31, BLOCK ? kThreads : 32,
+    append_page<T, W, BLOCK>(p, inter, bh, half, page_no, BLOCK ? threadIdx.x : threadIdx.x & 31, BLOCK ? kThreads : 32,
                              half ? v_vec : k_vec);
 }
 
@@ -476,7 +509,7 @@ bool rows_vec(const void *q, long long a, long long b, long long c, int es, int 
     return (reinterpret_cast<uintptr_t>(q) % bytes) == 0 && (a | b | c) % elems == 0;
 }
 
-template <typename T, int W, bool BLOCK, int HB>
+template <typename T, int W, bool BLOCK, int HB, int INTER>
 cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s) {
     const Kv8Cache &c = p.c;
     const int es = sizeof(T);
@@ -485,7 +518,7 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
     const long long q_blocks = ((long long)p.n * (c.D / (2 * W)) + kThreads - 1) / kThreads;
     const long long blocks = page_blocks + (p.q ? (long long)p.B * ((p.Hq + HB - 1) / HB) * q_blocks : 0);
     if (blocks >= (1LL << 31) || tasks >= (1LL << 31)) return cudaErrorInvalidValue;
-    kv8_append_kernel<T, W, BLOCK, HB><<<(unsigned)blocks, kThreads, 0, s>>>(
+    kv8_append_kernel<T, W, BLOCK, HB, INTER><<<(unsigned)blocks, kThreads, 0, s>>>(
         p, pages_per_seq, (((unsigned long long)page_blocks << 32) + blocks - 1) / blocks, (unsigned)q_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
         rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
         rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es, W));
@@ -510,8 +543,9 @@ cudaError_t append_w(Kv8StoreProblem p, int sm_count, cudaStream_t s) {
     // four heads to a thread once there are threads enough (queries of 8 prompts of 4096 tokens, 32 heads of 128: with 2, 4, 8
     // heads the call takes 177, 154, 195 us)
     const bool heads = (long long)p.B * p.Hq * p.n * (c.D / (2 * W)) >= 8LL * 1024 * sm_count;
-    if (block) return heads ? append_k<T, W, true, 4>(p, per_seq, s) : append_k<T, W, true, 1>(p, per_seq, s);
-    return heads ? append_k<T, W, false, 4>(p, per_seq, s) : append_k<T, W, false, 1>(p, per_seq, s);
+    if (!block) return heads ? append_k<T, W, false, 4, 2>(p, per_seq, s) : append_k<T, W, false, 1, 2>(p, per_seq, s);
+    if (p.interleaved) return heads ? append_k<T, W, true, 4, 1>(p, per_seq, s) : append_k<T, W, true, 1, 1>(p, per_seq, s);
+    return heads ? append_k<T, W, true, 4, 0>(p, per_seq, s) : append_k<T, W, true, 1, 0>(p, per_seq, s);
 }
 
 template <typename T>

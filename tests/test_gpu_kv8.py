@@ -159,6 +159,35 @@ def test_rotation_is_rounded_once(osf):
     assert np.array_equal(gp.cpu().numpy(), pages) and np.array_equal(gs.cpu().numpy(), scales)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_to_the_ties_of_codes(osf, dtype, inter):
+    """a c - b s (b = 1) a quarter of a unit in the last place after another around the midpoints of codes and around 448, where
+    the scale grows: the code of the value rounded once to float32."""
+    v = oracle.e4m3_values()[:127]
+    mids = np.r_[(v[9:] + v[8:-1]) / 2, v[8:127:7], 448.0, 448.0]
+    n, D, R = 64, 64, 64
+    for shift in (0, -30):
+        rng = np.random.default_rng(11 - shift)
+        mid = np.ldexp(rng.choice(mids, (n, R // 2)), shift).astype(np.float64)
+        a = rows(rng, (1, 1, n, R // 2), dtype)[0][0, 0]
+        a[a == 0] = 1
+        c = (mid / a).astype(np.float32)
+        step = np.spacing(mid.astype(np.float32)).astype(np.float64)
+        s = (a.astype(np.float64) * c - mid - rng.integers(-12, 13, mid.shape) * step / 4).astype(np.float32)
+        k = np.ones((1, 1, n, D), np.float32)
+        k[0, 0, :, slice(0, None, 2) if inter else slice(0, R // 2)] = a
+        near = oracle.rotate(k[0], np.arange(n), c, s, inter)[0][:, slice(0, None, 2) if inter else slice(0, R // 2)]
+        assert np.all(np.abs(near - mid) <= 5 * step)   # the input does what it is for
+        for P in (16, 64):
+            pages, scales, table = new_cache(1, 1, n // P, P, D, seed=2)
+            gp, gs, gt, gc, gsn = to_gpu(pages, scales, table, c, s)
+            K = torch.from_numpy(k).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+            osf.osf_kv8_append(K, K, gp, gs, gt, cos=gc, sin=gsn, interleaved=inter)
+            oracle.kv8_append(k, k, pages, scales, table, None, None, c, s, inter)
+            assert np.array_equal(gp.cpu().numpy(), pages) and np.array_equal(gs.cpu().numpy(), scales)
+
+
 def test_nan_and_infinity_are_stored_as_nan(osf):
     for dt in (torch.float32, torch.bfloat16):
         k = torch.ones(1, 1, 20, 32, device="cuda", dtype=dt)
