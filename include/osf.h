@@ -195,7 +195,8 @@ int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, i
  *     shared out over several CTAs (those that hold sinks, or all of a small problem); and, of larger problems, dS^T in bf16 of
  *     the tile pairs that some row sees while it stays within 16 GiB.  A workspace short of the last part selects the path
  *     that keeps no dS.
- * The result does not depend on the order in which anything runs.  Sq == 0 or Sk == 0: what gradients there are are zero.
+ * The result does not depend on the order in which anything runs.  Q, K, V, dO have to be finite: in a tile of which some row
+ * sees a part, a hidden pair counts 0 times what stands there.  Sq == 0 or Sk == 0: what gradients there are are zero.
  */
 int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const void *O, const void *dO,
                             const float *lse, void *dQ, void *dK, void *dV, int dtype, int B, int Hq,

@@ -816,7 +816,12 @@ struct BwdWindowLayout {
 static BwdWindowLayout bwd_window_layout(const AttnProblem &p, int sm_count) {
     BwdWindowLayout L;
     L.rows = align256((size_t)p.B * p.Hq * p.Sq * sizeof(float));
-    if (!window_tc(p.dtype, p.D)) return L;
+    if (!window_tc(p.dtype, p.D)) {
+        L.plan = bwd_rows_plan(p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.D, p.window, p.sinks, sm_count);
+        if (L.plan.parts > 1)
+            L.parts = (size_t)L.plan.shared_tiles * L.plan.parts * p.B * p.Hkv * 2 * L.plan.part_keys * p.D * sizeof(float);
+        return L;
+    }
     L.plan = bwd_window_plan(p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks, sm_count);
     const size_t tile = (size_t)128 * 128 * 2, per_head = (size_t)L.plan.slots * (((size_t)p.Sq + 127) / 128) * tile;
     const size_t cap = (size_t)16 << 30, heads = (size_t)p.B * p.Hq;
@@ -892,6 +897,7 @@ int osf_attn_bwd_gqa_window(const void *Q, const void *K, const void *V, const v
     b.dvec = reinterpret_cast<float *>(at);
     b.shared_tiles = L.plan.shared_tiles;
     b.parts = L.plan.parts;
+    b.part_keys = L.plan.part_keys;
     b.ds_slots = L.plan.slots;
     b.ds_ld = ((long long)Sq + 127) / 128 * 128;
     if (L.parts) b.part_acc = reinterpret_cast<float *>(at + L.rows);

@@ -243,8 +243,12 @@ __global__ void __launch_bounds__(256) bwd_dkdv_simt_kernel(BwdProblem p) {
 // to 256, float32 or bfloat16.  A block's eight warps own neighbouring keys (rows), whose rows (keys) overlap for the most part:
 // chunks of 32 of those are staged in shared memory for all of them.  For a chunk a lane first takes one of its rows (keys)
 // and both dot products with each of the warp's vectors (16-byte reads, KPW products to each), which gives P and dS; then a
-// channel of each 32, and adds up dS . b1 and P . b2 over the chunk.  Nothing is shared between blocks, so sums have one order.
-// float32, B=1 Hq=4 Hkv=2, 301 tokens of D=64, window 65: 264 us with a warp that reduces over its lanes for every pair.
+// channel of each 32, and adds up dS . b1 and P . b2 over the chunk.  Sums have one order.
+// Keys of tiles with sinks are seen by every later row: their chunks of rows are shared out over p.parts blocks, whose sums meet
+// in a second kernel.  (float32, B=1 Hq=8 Hkv=2, 2000 tokens of D=64, window 65, 3 sinks: 627 us with a block for all of them,
+// 106 shared out.)
+// This form, of many vectors, is bound by its reads of shared memory: KPW vectors to a warp divide them.  float32, B=4 Hq=32
+// Hkv=8, 512 tokens of D=64, window 65: 300 us; the multiplications of the pairs seen alone take 39.
 constexpr int RW_WARPS = 8, RW_CHUNK = 32;
 
 template <int C, int KPW>
@@ -261,13 +265,25 @@ __device__ __forceinline__ float4 ld_four(const float *p, int d, int D, bool vec
 }
 __device__ __forceinline__ float4 ld_four(const __nv_bfloat16 *p, int d, int D, bool vec) {
     if (vec) {
-        if (d >= D) return make_float4(0.f, 0.f, 0.f, 0.f);
-        const uint2 v = *reinterpret_cast<const uint2 *>(p + d);
+        const uint2 v = d < D ? *reinterpret_cast<const uint2 *>(p + d) : make_uint2(0u, 0u);
         return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
                            __uint_as_float(v.y & 0xffff0000u));
     }
     return make_float4(d < D ? ldf(p + d) : 0.f, d + 1 < D ? ldf(p + d + 1) : 0.f, d + 2 < D ? ldf(p + d + 2) : 0.f,
                        d + 3 < D ? ldf(p + d + 3) : 0.f);
+}
+
+// Which tile of `bid`'s head a block has (the shared ones come first, a block for each part), and its part.
+__device__ __forceinline__ int part_tile(const BwdProblem &p, bool dkv, int t, int &part) {
+    part = 0;
+    if (!dkv) return t;
+    if (t >= p.shared_tiles * p.parts) return t - p.shared_tiles * (p.parts - 1);
+    part = t % p.parts;
+    return t / p.parts;
+}
+// Sums of a part: [key][D] of dK (h = 0) or dV (1).
+__device__ __forceinline__ float *part_sums(const BwdProblem &p, int tile, int part, int head, int h) {
+    return p.part_acc + ((((size_t)tile * p.parts + part) * p.B * p.Hkv + head) * 2 + h) * p.part_keys * p.D;
 }
 
 template <typename T, int C, int KPW, bool DKV>
@@ -278,7 +294,8 @@ __device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int ti
     __shared__ float s_lse[RW_CHUNK], s_dvec[RW_CHUNK];
     float *b1 = rw_smem, *b2 = b1 + R::B_FLOATS, *av = b2 + R::B_FLOATS, *spd = av + R::A_FLOATS;
     const int D = p.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = bid % tiles, head = bid / tiles, G = p.Hq / p.Hkv;
+    int part;
+    const int tile = part_tile(p, DKV, bid % tiles, part), head = bid / tiles, G = p.Hq / p.Hkv;
     const int b = DKV ? head / p.Hkv : head / p.Hq, kvh = DKV ? head % p.Hkv : head % p.Hq / G;
     const int n_outer = DKV ? p.Sk : p.Sq, o0 = tile * RW_WARPS * KPW, o1 = min(o0 + RW_WARPS * KPW, n_outer);
     const T *A1 = static_cast<const T *>(DKV ? p.k : p.q) + (long long)head * n_outer * D;
@@ -303,6 +320,12 @@ __device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int ti
         steps = ks.n;
     }
     const int per_head = DKV && steps ? steps / G : 1;
+    const bool partial = DKV && p.parts > 1 && tile < p.shared_tiles;   // this block has steps st0 .. steps - 1 alone
+    int st0 = 0;
+    if (partial) {
+        st0 = (int)((long long)steps * part / p.parts);
+        steps = (int)((long long)steps * (part + 1) / p.parts);
+    }
     // chunk st: rows c0 .. c0 + cnt - 1 of head bh of the two arrays
     auto chunk = [&](int st, long long &bh, int &c0, int &cnt) {
         const int g = st / per_head;
@@ -319,13 +342,16 @@ __device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int ti
         const int n_inner = DKV ? p.Sq : p.Sk;
         const T *B1 = static_cast<const T *>(DKV ? p.q : p.k) + (bh * n_inner + c0) * D;
         const T *B2 = static_cast<const T *>(DKV ? p.dout : p.v) + (bh * n_inner + c0) * D;
+        auto rows = [&](auto v) {   // (a test of `vec` at each load keeps them from being in flight together)
 #pragma unroll
-        for (int e = 0; e < C; ++e) {
-            const int f = tid + 256 * e, r = f / (DP / 4), d = f % (DP / 4) * 4;
-            const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-            n1[e] = r < cnt ? ld_four(B1 + (long long)r * D, d, D, vec) : z;
-            n2[e] = r < cnt ? ld_four(B2 + (long long)r * D, d, D, vec) : z;
-        }
+            for (int e = 0; e < C; ++e) {
+                const int f = tid + 256 * e, r = f / (DP / 4), d = f % (DP / 4) * 4;
+                n1[e] = ld_four(B1 + (long long)min(r, cnt - 1) * D, r < cnt ? d : D, D, decltype(v)::value);
+                n2[e] = ld_four(B2 + (long long)min(r, cnt - 1) * D, r < cnt ? d : D, D, decltype(v)::value);
+            }
+        };
+        if (vec) rows(std::true_type{});
+        else rows(std::false_type{});
         if (DKV && tid < 2 * RW_CHUNK) {
             const int r = tid & (RW_CHUNK - 1);
             n_lse = r >= cnt ? 0.f : tid < RW_CHUNK ? p.lse[bh * p.Sq + c0 + r] * kLog2e : p.dvec[bh * p.Sq + c0 + r];
@@ -345,11 +371,11 @@ __device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int ti
         const int o = o0 + warp * KPW + k;
         dvec_o[k] = !DKV && o < o1 ? p.dvec[(long long)head * p.Sq + o] : 0.f;
     }
-    if (steps > 0) fetch(0);
+    if (steps > st0) fetch(st0);
     const float *mine = av + warp * KPW * 2 * DP;
     float *mp = spd + warp * RW_CHUNK * 2 * KPW;
     const int d_end = (D + 3) / 4 * 4;
-    for (int st = 0; st < steps; ++st) {
+    for (int st = st0; st < steps; ++st) {
         long long bh;
         int c0, cnt;
         chunk(st, bh, c0, cnt);
@@ -423,12 +449,201 @@ __device__ __forceinline__ void window_rows(const BwdProblem &p, int bid, int ti
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int d = lane + 32 * c;
-            if (d < D) {
+            if (d >= D) continue;
+            if (partial) {
+                part_sums(p, tile, part, head, 0)[(o - o0) * D + d] = acc1[k][c];
+                part_sums(p, tile, part, head, 1)[(o - o0) * D + d] = acc2[k][c];
+            } else {
                 O1[(long long)o * D + d] = from_f32<T>(acc1[k][c] * p.scale);
                 if (DKV) O2[(long long)o * D + d] = from_f32<T>(acc2[k][c]);
             }
         }
     }
+}
+
+// The same where there are few vectors, D up to 128: all warps of a block take its eight vectors, each against every NW-th
+// chunk, which it stages for itself, and their sums meet in the order of the warps: a block's walk is NW times shorter, and no
+// warp waits for another's chunk.  Bound by what a block does one after another (loads, two products, sums, the join).
+// float32, B=1 Hq=4 Hkv=2, 301 tokens of D=64, window 65, 3 sinks: 20 us with the row sums and the join of the parts, of which
+// launches 10 (52 with a key to a warp and chunks shared by the block, 264 with a reduction over the lanes for every pair).
+template <int C>
+struct FewCfg {
+    static constexpr int V = 8, NW = C == 2 ? 8 : 4, DP = 32 * C, PITCH = DP + 4, SP = 2 * V + 4;
+    static constexpr int B_FLOATS = RW_CHUNK * PITCH, WARP_FLOATS = 2 * B_FLOATS + RW_CHUNK * SP;
+    static constexpr size_t SMEM = sizeof(float) * (V * 2 * DP + NW * WARP_FLOATS);
+    static_assert(2 * V * DP <= WARP_FLOATS, "a warp's sums take its chunk's place");
+};
+template <typename T, int C, bool DKV>
+__device__ __forceinline__ void window_few(const BwdProblem &p, int bid, int tiles, bool vec) {
+    using F = FewCfg<C>;
+    constexpr int V = F::V, NW = F::NW, DP = F::DP, PITCH = F::PITCH;
+    extern __shared__ __align__(16) float rw_smem[];
+    const int D = p.D, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    float *av = rw_smem, *b1 = av + V * 2 * DP + warp * F::WARP_FLOATS, *b2 = b1 + F::B_FLOATS, *sp = b2 + F::B_FLOATS;
+    int part;
+    const int tile = part_tile(p, DKV, bid % tiles, part), head = bid / tiles, G = p.Hq / p.Hkv;
+    const int b = DKV ? head / p.Hkv : head / p.Hq, kvh = DKV ? head % p.Hkv : head % p.Hq / G;
+    const int n_outer = DKV ? p.Sk : p.Sq, n_inner = DKV ? p.Sq : p.Sk, o0 = tile * V, o1 = min(o0 + V, n_outer);
+    const T *A1 = static_cast<const T *>(DKV ? p.k : p.q) + (long long)head * n_outer * D;
+    const T *A2 = static_cast<const T *>(DKV ? p.v : p.dout) + (long long)head * n_outer * D;
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = tid; i < V * DP / 4; i += NW * 32) {
+        const int o = i / (DP / 4), d = i % (DP / 4) * 4;
+        const bool ok = o0 + o < o1;
+        *reinterpret_cast<float4 *>(av + (o * 2) * DP + d) = ok ? ld_four(A1 + (long long)(o0 + o) * D, d, D, vec) : z;
+        *reinterpret_cast<float4 *>(av + (o * 2 + 1) * DP + d) = ok ? ld_four(A2 + (long long)(o0 + o) * D, d, D, vec) : z;
+    }
+    int i0 = 0, i1 = 0, steps;
+    KeyStream ks{};
+    if (DKV) {
+        i0 = max(0, o0 - p.causal_off);
+        i1 = o0 < p.sinks ? p.Sq : min(p.Sq, max(0, o1 - 1 - p.causal_off + p.window));
+        steps = i1 > i0 ? G * ((i1 - i0 + RW_CHUNK - 1) / RW_CHUNK) : 0;
+    } else {
+        ks = key_stream(o0 + p.causal_off, o1 - 1 + p.causal_off, p.Sk, p.window, p.sinks, RW_CHUNK);
+        steps = ks.n;
+    }
+    const int per_head = DKV && steps ? steps / G : 1, d_end = (D + 3) / 4 * 4;
+    const bool partial = DKV && p.parts > 1 && tile < p.shared_tiles;   // this block has steps st0 .. steps - 1 alone
+    int st0 = 0;
+    if (partial) {
+        st0 = (int)((long long)steps * part / p.parts);
+        steps = (int)((long long)steps * (part + 1) / p.parts);
+    }
+    float acc1[V][C], acc2[V][C];
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc1[k][c] = acc2[k][c] = 0.f;
+    griddep_wait();   // launched as a dependent of the kernel that writes the row sums
+    __syncthreads();
+    for (int st = st0 + warp; st < steps; st += NW) {
+        const int g = st / per_head;
+        const long long bh = DKV ? (long long)b * p.Hq + kvh * G + g : (long long)b * p.Hkv + kvh;
+        const int c0 = DKV ? i0 + (st - g * per_head) * RW_CHUNK : ks.tile(st) * RW_CHUNK;
+        const int cnt = min(RW_CHUNK, (DKV ? i1 : p.Sk) - c0);
+        const T *B1 = static_cast<const T *>(DKV ? p.q : p.k) + (bh * n_inner + c0) * D;
+        const T *B2 = static_cast<const T *>(DKV ? p.dout : p.v) + (bh * n_inner + c0) * D;
+        float lse = 0.f, dvec = 0.f;
+        if (DKV && lane < cnt) {
+            lse = p.lse[bh * p.Sq + c0 + lane] * kLog2e;
+            dvec = p.dvec[bh * p.Sq + c0 + lane];
+        }
+        constexpr int ROUND = 8;   // loads of each array that are in flight together
+        auto stage = [&](auto v) {   // (see above)
+#pragma unroll 1
+            for (int f0 = 0; f0 < RW_CHUNK * DP / 4; f0 += 32 * ROUND) {
+                float4 n1[ROUND], n2[ROUND];
+#pragma unroll
+                for (int e = 0; e < ROUND; ++e) {
+                    const int f = f0 + 32 * e + lane, r = f / (DP / 4), d = f % (DP / 4) * 4;
+                    n1[e] = ld_four(B1 + (long long)min(r, cnt - 1) * D, r < cnt ? d : D, D, decltype(v)::value);
+                    n2[e] = ld_four(B2 + (long long)min(r, cnt - 1) * D, r < cnt ? d : D, D, decltype(v)::value);
+                }
+#pragma unroll
+                for (int e = 0; e < ROUND; ++e) {
+                    const int f = f0 + 32 * e + lane, r = f / (DP / 4), d = f % (DP / 4) * 4;
+                    *reinterpret_cast<float4 *>(b1 + r * PITCH + d) = n1[e];
+                    *reinterpret_cast<float4 *>(b2 + r * PITCH + d) = n2[e];
+                }
+            }
+        };
+        if (vec) stage(std::true_type{});
+        else stage(std::false_type{});
+        __syncwarp();
+        float s[V], t[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) s[k] = t[k] = 0.f;
+#pragma unroll 2
+        for (int d = 0; d < d_end; d += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(b1 + lane * PITCH + d);
+            const float4 y = *reinterpret_cast<const float4 *>(b2 + lane * PITCH + d);
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float4 u = *reinterpret_cast<const float4 *>(av + 2 * k * DP + d);
+                const float4 v = *reinterpret_cast<const float4 *>(av + (2 * k + 1) * DP + d);
+                s[k] = fmaf(x.x, u.x, s[k]); s[k] = fmaf(x.y, u.y, s[k]); s[k] = fmaf(x.z, u.z, s[k]); s[k] = fmaf(x.w, u.w, s[k]);
+                t[k] = fmaf(y.x, v.x, t[k]); t[k] = fmaf(y.y, v.y, t[k]); t[k] = fmaf(y.z, v.z, t[k]); t[k] = fmaf(y.w, v.w, t[k]);
+            }
+        }
+        float pr[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const int o = o0 + k, key = DKV ? o : c0 + lane, pos = (DKV ? c0 + lane : o) + p.causal_off;
+            const bool sees = o < o1 && lane < cnt && key <= pos && (key > pos - p.window || key < p.sinks);
+            if (!DKV) {
+                lse = sees ? p.lse[(long long)head * p.Sq + o] * kLog2e : 0.f;
+                dvec = sees ? p.dvec[(long long)head * p.Sq + o] : 0.f;
+            }
+            pr[k] = sees ? ex2_approx(s[k] * p.scale_log2 - lse) : 0.f;
+            t[k] = sees ? pr[k] * (t[k] - dvec) : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < V; k += 4) {
+            *reinterpret_cast<float4 *>(sp + lane * F::SP + k) = make_float4(t[k], t[k + 1], t[k + 2], t[k + 3]);
+            if (DKV) *reinterpret_cast<float4 *>(sp + lane * F::SP + V + k) = make_float4(pr[k], pr[k + 1], pr[k + 2], pr[k + 3]);
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int r = 0; r < RW_CHUNK; ++r) {
+            float ds[V], q[V];
+#pragma unroll
+            for (int k = 0; k < V; k += 4) {
+                const float4 a = *reinterpret_cast<const float4 *>(sp + r * F::SP + k);
+                ds[k] = a.x; ds[k + 1] = a.y; ds[k + 2] = a.z; ds[k + 3] = a.w;
+                if (DKV) {
+                    const float4 e = *reinterpret_cast<const float4 *>(sp + r * F::SP + V + k);
+                    q[k] = e.x; q[k + 1] = e.y; q[k + 2] = e.z; q[k + 3] = e.w;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                const float x = b1[r * PITCH + lane + 32 * c];
+#pragma unroll
+                for (int k = 0; k < V; ++k) acc1[k][c] = fmaf(ds[k], x, acc1[k][c]);
+                if (DKV) {
+                    const float y = b2[r * PITCH + lane + 32 * c];
+#pragma unroll
+                    for (int k = 0; k < V; ++k) acc2[k][c] = fmaf(q[k], y, acc2[k][c]);
+                }
+            }
+        }
+        __syncwarp();
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k)
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            b1[(2 * k) * DP + lane + 32 * c] = acc1[k][c];
+            if (DKV) b1[(2 * k + 1) * DP + lane + 32 * c] = acc2[k][c];
+        }
+    __syncthreads();
+    const float *sums = av + V * 2 * DP;
+    T *O1 = static_cast<T *>(DKV ? p.dk : p.dq) + ((long long)head * n_outer + o0) * D;
+    T *O2 = static_cast<T *>(p.dv) + ((long long)head * n_outer + o0) * D;
+    const int used = min(NW, steps - st0);
+    for (int i = tid; i < (o1 - o0) * DP; i += NW * 32) {
+        const int o = i / DP, d = i % DP;
+        if (d >= D) continue;
+        float a = 0.f, e = 0.f;
+        for (int w = 0; w < used; ++w) {
+            a += sums[w * F::WARP_FLOATS + 2 * o * DP + d];
+            if (DKV) e += sums[w * F::WARP_FLOATS + (2 * o + 1) * DP + d];
+        }
+        if (partial) {
+            part_sums(p, tile, part, head, 0)[o * D + d] = a;
+            part_sums(p, tile, part, head, 1)[o * D + d] = e;
+            continue;
+        }
+        O1[(long long)o * D + d] = from_f32<T>(a * p.scale);
+        if (DKV) O2[(long long)o * D + d] = from_f32<T>(e);
+    }
+}
+template <typename T, int C>
+__global__ void __launch_bounds__(FewCfg<C>::NW * 32)
+bwd_window_few_kernel(BwdProblem p, unsigned kv_blocks, int kv_tiles, int q_tiles, int vec) {
+    if (blockIdx.x < kv_blocks) window_few<T, C, true>(p, blockIdx.x, kv_tiles, vec);
+    else window_few<T, C, false>(p, blockIdx.x - kv_blocks, q_tiles, vec);
 }
 
 // One grid: the blocks of dK and dV, then those of dQ.
@@ -439,31 +654,67 @@ bwd_window_rows_kernel(BwdProblem p, unsigned kv_blocks, int kv_tiles, int q_til
     else window_rows<T, C, KPW, false>(p, blockIdx.x - kv_blocks, q_tiles, vec);
 }
 
-template <typename T, int C, int KPW>
-cudaError_t launch_rows_k(const BwdProblem &p, cudaStream_t s) {
-    constexpr size_t smem = RowsCfg<C, KPW>::SMEM;
-    const cudaError_t e = set_max_dynamic_smem((const void *)bwd_window_rows_kernel<T, C, KPW>, (int)smem);
+// dK and dV of the keys in shared tiles: the parts' sums, added in the order of the parts.  gridDim = (values of the tiles / 256,
+// b * kv head, dK | dV).
+template <typename T>
+__global__ void __launch_bounds__(256) bwd_rows_sum_kernel(const BwdProblem p) {
+    griddep_wait();
+    const int i = blockIdx.x * 256 + threadIdx.x, key = i / p.D, d = i % p.D, head = blockIdx.y, h = blockIdx.z;
+    if (key >= min(p.shared_tiles * p.part_keys, p.Sk)) return;
+    const size_t part = (size_t)p.B * p.Hkv * 2 * p.part_keys * p.D;
+    const float *src = part_sums(p, key / p.part_keys, 0, head, h) + key % p.part_keys * p.D + d;
+    float a = 0.f;
+#pragma unroll 8
+    for (int s = 0; s < p.parts; ++s) a += src[s * part];
+    static_cast<T *>(h ? p.dv : p.dk)[((long long)head * p.Sk + key) * p.D + d] = from_f32<T>(h ? a : a * p.scale);
+}
+
+using RowsKernel = void (*)(BwdProblem, unsigned, int, int, int);
+template <typename T>
+cudaError_t launch_rows_k(BwdProblem p, RowsKernel kernel, int per, int threads, size_t smem, cudaStream_t s) {
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, (int)smem);
     if (e != cudaSuccess) return e;
-    const int per = RW_WARPS * KPW, kv_tiles = (p.Sk + per - 1) / per, q_tiles = (p.Sq + per - 1) / per;
+    if (p.part_keys != per || p.shared_tiles == 0 || p.parts <= 1) {   // (or the plan is the tensor-core path's, whose sizes TMA did not address)
+        p.shared_tiles = 0;
+        p.parts = 1;
+    }
+    const int kv_tiles = (p.Sk + per - 1) / per + p.shared_tiles * (p.parts - 1), q_tiles = (p.Sq + per - 1) / per;
     const long long kv = (long long)kv_tiles * p.B * p.Hkv, all = kv + (long long)q_tiles * p.B * p.Hq;
     if (all >= (1LL << 31)) return cudaErrorInvalidValue;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v) |
                          reinterpret_cast<uintptr_t>(p.dout);
     const int vec = p.D % 4 == 0 && at % (4 * sizeof(T)) == 0;
     count_launches(1);
-    return launch_dependent(bwd_window_rows_kernel<T, C, KPW>, dim3((unsigned)all), dim3(RW_WARPS * 32), smem, s, p, (unsigned)kv,
-                            kv_tiles, q_tiles, vec);
+    e = launch_dependent(kernel, dim3((unsigned)all), dim3(threads), smem, s, p, (unsigned)kv, kv_tiles, q_tiles, vec);
+    if (e != cudaSuccess || p.parts == 1) return e;
+    count_launches(1);
+    return launch_dependent(bwd_rows_sum_kernel<T>, dim3((unsigned)(((long long)p.shared_tiles * per * p.D + 255) / 256), (unsigned)(p.B * p.Hkv), 2),
+                            dim3(256), 0, s, p);
+}
+template <typename T, int C, int KPW>
+cudaError_t launch_rows(const BwdProblem &p, cudaStream_t s) {
+    return launch_rows_k<T>(p, bwd_window_rows_kernel<T, C, KPW>, RW_WARPS * KPW, RW_WARPS * 32, RowsCfg<C, KPW>::SMEM, s);
+}
+template <typename T, int C>
+cudaError_t launch_few(const BwdProblem &p, cudaStream_t s) {
+    return launch_rows_k<T>(p, bwd_window_few_kernel<T, C>, FewCfg<C>::V, FewCfg<C>::NW * 32, FewCfg<C>::SMEM, s);
+}
+// Vectors to a block: 8 (the form for few vectors, or a vector to a warp where D > 128), or 32 where there are many: a block
+// then runs long, and reads less.  (us, 8 against 32, window 600: float32 D = 64, 1806 vectors 27 against 78, 12000 158, 316, 20480
+// 228, 406, 40960 439, 408, 81920 861, 678; D = 128, 1806 48, 126, 12000 318, 443, 20480 465, 377, 40960 904, 674; window 65, D = 64,
+// 12000 75, 78, 40960 227, 161.)
+int rows_per_block(long long B, int Hq, int Hkv, int Sq, int Sk, int D, int sm_count) {
+    const long long vectors = B * ((long long)Hkv * Sk + (long long)Hq * Sq);
+    return vectors >= (D > 128 ? 64LL : D > 64 ? 108LL : 216LL) * sm_count ? 32 : 8;
 }
 template <typename T>
 cudaError_t launch_window_rows(const BwdProblem &p, cudaStream_t s) {
     int sms = 0;
     if (device_sm_count(&sms) != OSF_OK) return cudaErrorInvalidValue;
-    // four vectors to a warp where that leaves every SM two blocks
-    const long long vectors = (long long)p.B * ((long long)p.Hkv * p.Sk + (long long)p.Hq * p.Sq);
-    const bool wide = vectors >= 2LL * sms * RW_WARPS * 4;
-    if (p.D <= 64) return wide ? launch_rows_k<T, 2, 4>(p, s) : launch_rows_k<T, 2, 1>(p, s);
-    if (p.D <= 128) return wide ? launch_rows_k<T, 4, 4>(p, s) : launch_rows_k<T, 4, 1>(p, s);
-    return wide ? launch_rows_k<T, 8, 4>(p, s) : launch_rows_k<T, 8, 1>(p, s);
+    const bool wide = rows_per_block(p.B, p.Hq, p.Hkv, p.Sq, p.Sk, p.D, sms) == 32;
+    if (p.D <= 64) return wide ? launch_rows<T, 2, 4>(p, s) : launch_few<T, 2>(p, s);
+    if (p.D <= 128) return wide ? launch_rows<T, 4, 4>(p, s) : launch_few<T, 4>(p, s);
+    return wide ? launch_rows<T, 8, 4>(p, s) : launch_rows<T, 8, 1>(p, s);
 }
 
 // ------------------------------------------------------------------ tensor-core version (bf16)
@@ -778,6 +1029,25 @@ bool attn_bwd_mma_supported(const BwdProblem &p) {
                         reinterpret_cast<uintptr_t>(p.dq) | reinterpret_cast<uintptr_t>(p.dk) |
                         reinterpret_cast<uintptr_t>(p.dv);
     return (a & 15u) == 0 && (p.Sk + 63) / 64 < 65536 && (long long)p.B * p.Hq < 65536;
+}
+
+BwdWindowPlan bwd_rows_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks, int sm_count) {
+    BwdWindowPlan w{};
+    w.part_keys = rows_per_block(B, Hq, Hkv, Sq, Sk, D, sm_count);
+    w.parts = 1;
+    w.shared_tiles = (int)(((long long)sinks + w.part_keys - 1) / w.part_keys);
+    const int tiles = (Sk - 1) / w.part_keys + 1;
+    if (w.shared_tiles > tiles) w.shared_tiles = tiles;
+    if (w.shared_tiles == 0) return w;
+    // Keys of tiles with sinks are seen by every later row: their chunks of rows are shared out in parts as long as the others'
+    // walks, or than a step of all warps, as long as the parts are within four blocks to an SM
+    const long long chunks = ((long long)Sq + RW_CHUNK - 1) / RW_CHUNK, group = Hq / Hkv;
+    long long walk = group * ((window + w.part_keys - 1) / RW_CHUNK + 1);
+    if (walk < RW_WARPS) walk = RW_WARPS;
+    const long long tiles_all = (long long)w.shared_tiles * B * Hkv;
+    const long long parts = (group * chunks + walk - 1) / walk, most = (4LL * sm_count + tiles_all - 1) / tiles_all;
+    w.parts = (int)(parts < most ? parts : most);
+    return w;
 }
 
 cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s) {

@@ -23,9 +23,9 @@ struct BwdProblem {
     void *ds;
     long long ds_rows, ds_ld;
     int ds_slots;
-    // with a window: the steps (query head, query tile) of each of the first shared_tiles key tiles are shared out over
-    // `parts` CTAs, whose sums of dK and dV (float32 [128][D] each) meet in part_acc [tile][part][b, kv head][2]
-    int shared_tiles, parts;
+    // with a window: the steps (query head, query tile) of each of the first shared_tiles tiles of part_keys keys are shared out
+    // over `parts` CTAs, whose sums of dK and dV (float32 [part_keys][D] each) meet in part_acc [tile][part][b, kv head][2]
+    int shared_tiles, parts, part_keys;
     float *part_acc;
     int *status;
 };
@@ -33,11 +33,12 @@ struct BwdProblem {
 bool attn_bwd_mma_supported(const BwdProblem &p);
 cudaError_t launch_attn_bwd(const BwdProblem &p, cudaStream_t s);
 
-// How a windowed problem runs on the tensor-core path.
+// How a windowed problem runs on the tensor-core path, and on the CUDA cores.
 struct BwdWindowPlan {
-    int slots;                 // tiles of the longest key stream
-    int shared_tiles, parts;
-    bool store_ds;             // dQ as a product over stored dS^T tiles
+    int shared_tiles, parts, part_keys;
+    int slots;                 // tensor cores: tiles of the longest key stream,
+    bool store_ds;             // and dQ as a product over stored dS^T tiles
 };
 BwdWindowPlan bwd_window_plan(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count);
+BwdWindowPlan bwd_rows_plan(int B, int Hq, int Hkv, int Sq, int Sk, int D, int window, int sinks, int sm_count);
 }  // namespace osf

@@ -1047,7 +1047,8 @@ cudaError_t launch_attn_bwd_tc(const BwdProblem &p, cudaStream_t s) {
 }
 
 BwdWindowPlan bwd_window_plan(int B, int Hq, int Hkv, int Sq, int Sk, int window, int sinks, int sm_count) {
-    BwdWindowPlan w;
+    BwdWindowPlan w{};
+    w.part_keys = TB;
     const long long kts = ((long long)Sk + TB - 1) / TB, qts = ((long long)Sq + TB - 1) / TB;
     const long long heads = (long long)B * Hkv, kv = kts * heads, q = qts * B * Hq;
     const long long walk = ((long long)window + TB - 1) / TB + 1;   // query tiles that see a key tile without sinks

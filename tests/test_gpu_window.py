@@ -321,3 +321,26 @@ def test_shared_keys_across_the_batch(osf):
             lse = torch.empty(3, 4, n, device="cuda")
             o = osf.osf_attn_fwd_gqa_window(Q[:, :, :n], *kv, 100, 3, lse=lse)
             check_out(o, lse, ref, "bf16", f"{n} rows")
+
+
+@pytest.mark.parametrize("dtype,D,B,Hq,Hkv,S,window,sinks", [
+    ("f32", 64, 3, 20, 10, 390, 70, 3), ("f32", 40, 3, 20, 10, 390, 390, 0), ("bf16", 72, 3, 20, 10, 250, 30, 45),
+    ("bf16", 48, 4, 20, 10, 300, 500, 7), ("f32", 250, 2, 20, 10, 200, 33, 9), ("f32", 256, 1, 6, 3, 300, 64, 40),
+    ("f32", 64, 1, 4, 2, 1500, 65, 20), ("bf16", 80, 1, 3, 1, 1300, 40, 8), ("f32", 128, 1, 2, 2, 1000, 32, 1)])
+def test_gradients_on_the_cuda_cores(osf, dtype, D, B, Hq, Hkv, S, window, sinks):
+    """Many vectors (32 to a block) and few (8), sinks whose rows are shared out over blocks."""
+    run(osf, dtype, B, Hq, Hkv, S, S, D, window, sinks, grad=True)
+
+
+@pytest.mark.parametrize("D", [64, 96])
+def test_gradients_of_tensors_off_16_bytes(osf, D):
+    """bfloat16 tensors that the tensor-core path cannot address: the CUDA cores', with its workspace."""
+    B, Hq, Hkv, S, window, sinks = 1, 4, 2, 500, 100, 9
+    q, k, v = si.qkv((B, Hq, S, D), (B, Hkv, S, D), seed=4, dtype="bf16")
+    g = si.qkv((B, Hq, S, D), (1, 1, 1, D), seed=5, dtype="bf16")[0]
+    off = [torch.empty(x.size + 1, dtype=torch.bfloat16, device="cuda")[1:].view(x.shape).copy_(bf16_tensor(x)) for x in (q, k, v, g)]
+    ref = oracle.attention_window(f64(q, "bf16"), f64(k, "bf16"), f64(v, "bf16"), window, sinks, dO=f64(g, "bf16"))
+    lse = torch.empty(B, Hq, S, device="cuda")
+    o = osf.osf_attn_fwd_gqa_window(*off[:3], window, sinks, lse=lse)
+    check_out(o, lse, ref, "bf16", "off 16 bytes")
+    check_grads(osf.osf_attn_bwd_gqa_window(*off[:3], o, off[3], lse, window, sinks), ref, "bf16", "off 16 bytes")
