@@ -34,6 +34,53 @@ struct SimtCfg {
 template <typename T>
 __device__ __forceinline__ float ld(const T *p) { return to_f32(*p); }
 
+// Four channels of a row, at a 16-byte (bfloat16: 8-byte) boundary.
+__device__ __forceinline__ float4 ld_four(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 ld_four(const __nv_bfloat16 *p) {
+    const uint2 v = *reinterpret_cast<const uint2 *>(p);
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+}
+// Rows of DP channels in shared memory, `rows` of them valid (zeros elsewhere), four channels to a load, a thread's loads of up to
+// eight pieces in flight together.  TR: transposed, [DP][pitch], a lane to a row, so that the stores of a warp do not clash.
+template <typename T, int DP, int ROWS, int THREADS, bool TR>
+struct StageRows {
+    static constexpr int PER = ROWS * DP / 4 / THREADS, N = PER < 8 ? PER : 8;
+    float4 x[N];
+    // piece i of this thread: its row and first channel
+    static __device__ __forceinline__ void place(int i, int &r, int &d) {
+        const int u = threadIdx.x + i * THREADS;
+        if constexpr (TR) {
+            r = (u & 31) + (u >> 5) % (ROWS / 32) * 32;
+            d = (u >> 5) / (ROWS / 32) * 4;
+        } else {
+            r = u / (DP / 4);
+            d = u % (DP / 4) * 4;
+        }
+    }
+    __device__ __forceinline__ void load(const T *src, long long stride, int rows, int D, int i0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            int r, d;
+            place(i0 + e, r, d);
+            x[e] = r < rows && d < D ? ld_four(src + r * stride + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+    __device__ __forceinline__ void store(float *dst, int pitch, int i0) const {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            int r, d;
+            place(i0 + e, r, d);
+            if constexpr (TR) {
+                dst[d * pitch + r] = x[e].x; dst[(d + 1) * pitch + r] = x[e].y;
+                dst[(d + 2) * pitch + r] = x[e].z; dst[(d + 3) * pitch + r] = x[e].w;
+            } else {
+                *reinterpret_cast<float4 *>(dst + r * pitch + d) = x[e];
+            }
+        }
+    }
+};
+
 // WIN: a window with sinks (AttnProblem::window); the key tiles are then those of the block's key_stream.
 template <typename T, int DP, int BM, bool WIN>
 __global__ void __launch_bounds__(BM * 4)
@@ -74,9 +121,29 @@ attn_simt_kernel(const AttnProblem p) {
     int k_end = min(WIN ? ks.n * BN : p.Sk, (split + 1) * tps * BN);
     if (p.causal && !WIN) k_end = min(k_end, max(k_begin, q0 + BM + p.causal_off));
 
-    for (int idx = tid; idx < BM * DP; idx += C::THREADS) {
-        const int r = idx / DP, d = idx % DP;
-        Qs[d * C::QS + r] = (q0 + r < p.Sq && d < D) ? ld(Qg + (long long)r * p.q_ss + d) : 0.f;
+    // with a window, where rows allow it: pieces of four channels, all of a tile's loads in flight together (a call of few tiles is
+    // mostly their latency: float32, Hq=8 Hkv=2, 77 rows of 1001 keys of D=96, window 200: 20.5 us with single loads)
+    using StQ = StageRows<T, DP, BM, C::THREADS, true>;
+    using StK = StageRows<T, DP, BN, C::THREADS, true>;
+    using StV = StageRows<T, DP, BN, C::THREADS, false>;
+    bool vec = false;
+    if constexpr (WIN) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(p.q) | reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v);
+        const long long st = p.q_sb | p.q_sh | p.q_ss | p.k_sb | p.k_sh | p.k_ss | p.v_sb | p.v_sh | p.v_ss | D;
+        vec = at % (4 * sizeof(T)) == 0 && (st & 3) == 0;
+    }
+    if (vec) {
+#pragma unroll 1
+        for (int i = 0; i < StQ::PER; i += StQ::N) {
+            StQ q;
+            q.load(Qg, p.q_ss, p.Sq - q0, D, i);
+            q.store(Qs, C::QS, i);
+        }
+    } else {
+        for (int idx = tid; idx < BM * DP; idx += C::THREADS) {
+            const int r = idx / DP, d = idx % DP;
+            Qs[d * C::QS + r] = (q0 + r < p.Sq && d < D) ? ld(Qg + (long long)r * p.q_ss + d) : 0.f;
+        }
     }
 
     float m[4], l[4], acc[4][C::OC];
@@ -91,12 +158,30 @@ attn_simt_kernel(const AttnProblem p) {
     for (int at = k_begin; at < k_end; at += BN) {
         const int kt0 = WIN ? ks.tile(at / BN) * BN : at;   // the tile's first key, and the end of the keys that exist
         const int k_lim = WIN ? p.Sk : k_end;
-        __syncthreads();  // previous tile's K/V/P fully consumed (and Q stored, first time)
-        for (int idx = tid; idx < BN * DP; idx += C::THREADS) {
-            const int c = idx / DP, d = idx % DP;
-            const bool ok = (kt0 + c < k_lim) && d < D;
-            Ks[d * C::KS + c] = ok ? ld(Kg + (long long)(kt0 + c) * p.k_ss + d) : 0.f;
-            Vs[c * DP + d] = ok ? ld(Vg + (long long)(kt0 + c) * p.v_ss + d) : 0.f;
+        if (vec) {
+            StK k;
+            StV v;
+            const int rows = k_lim - kt0;
+            k.load(Kg + kt0 * p.k_ss, p.k_ss, rows, D, 0);
+            v.load(Vg + kt0 * p.v_ss, p.v_ss, rows, D, 0);
+            __syncthreads();  // previous tile's K/V/P fully consumed (and Q stored, first time)
+            k.store(Ks, C::KS, 0);
+            v.store(Vs, DP, 0);
+#pragma unroll 1
+            for (int i = StK::N; i < StK::PER; i += StK::N) {
+                k.load(Kg + kt0 * p.k_ss, p.k_ss, rows, D, i);
+                v.load(Vg + kt0 * p.v_ss, p.v_ss, rows, D, i);
+                k.store(Ks, C::KS, i);
+                v.store(Vs, DP, i);
+            }
+        } else {
+            __syncthreads();  // previous tile's K/V/P fully consumed (and Q stored, first time)
+            for (int idx = tid; idx < BN * DP; idx += C::THREADS) {
+                const int c = idx / DP, d = idx % DP;
+                const bool ok = (kt0 + c < k_lim) && d < D;
+                Ks[d * C::KS + c] = ok ? ld(Kg + (long long)(kt0 + c) * p.k_ss + d) : 0.f;
+                Vs[c * DP + d] = ok ? ld(Vg + (long long)(kt0 + c) * p.v_ss + d) : 0.f;
+            }
         }
         __syncthreads();
 
