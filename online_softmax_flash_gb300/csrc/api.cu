@@ -234,12 +234,24 @@ void carve_partials(AttnProblem &p, void *ws, long long rows) {
 // Which kernel runs a (validated, non-empty) problem.
 enum class Path { Simt, TensorCore, Decode };
 
+// float32 rows of 64 channels under a window: the tensor cores first split all of K and V into bfloat16 parts, whatever the window;
+// the CUDA cores take the keys of the window alone, at a fifth of the rate.  Fitted to measurements (us, CUDA cores against tensor
+// cores; rows x heads / keys, window 200: 77 x 8 / 1001 16, 29; 77 x 8 / 32000 17, 45; 500 x 8 / 1001 31, 32; 1000 x 8 / 2000 52,
+// 48; 1000 x 64 / 2000 226, 175; 77 x 128 / 20000 72, 220; window 1000: 77 x 8 / 8000 21, 32; 77 x 64 / 2000 124, 74; 77 x 128 /
+// 20000 188, 267; 4000: 655, 455).
+bool f32_window_small(const AttnProblem &p) {
+    if (!p.window || p.dtype != OSF_F32) return false;
+    const long long rows = (long long)p.B * p.Hq * p.Sq, keys = 64LL * key_stream_max(64, p.Sk, p.window, p.sinks, 64);
+    const long long split = (rows + 2LL * p.B * p.Hkv * p.Sk) * 64;   // elements to split
+    return (double)rows * keys < 2300000 + split / 3;
+}
+
 Path choose_path(const AttnProblem &p, const void *Q, const void *K, const void *V, const void *O) {
     // one or a few query rows per head (G * Sq <= 16): the HBM-bound decode kernel, which reads
     // each K/V byte once for all the query heads of its kv head
     if (p.dtype == OSF_BF16 && decode_supported(p, Q, K, V, O)) return Path::Decode;
     // bf16, and fp32 with D = 64 (as bf16 high / low parts)
-    if (p.Sq > 1 && attn_tc_supported(p, Q, K, V, O)) return Path::TensorCore;
+    if (p.Sq > 1 && !f32_window_small(p) && attn_tc_supported(p, Q, K, V, O)) return Path::TensorCore;
     return Path::Simt;
 }
 
@@ -769,7 +781,7 @@ int osf_attn_window_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, i
     if (device_info(&dev) != OSF_OK) return OSF_ERR_CUDA;
     // the largest of the possible paths' needs (alignment decides the path at call time)
     size_t need = path_workspace(p, Path::Simt, plan_splits(p, Path::Simt, dev->sm_count, 0));
-    if (Sq > 1 && (window_tc(dtype, D) || (dtype == OSF_F32 && D == 64)))
+    if (Sq > 1 && (window_tc(dtype, D) || (dtype == OSF_F32 && D == 64 && !f32_window_small(p))))
         need = std::max(need, path_workspace(p, Path::TensorCore, plan_splits(p, Path::TensorCore, dev->sm_count, 0)));
     if (dtype == OSF_BF16 && (long long)(Hq / Hkv) * Sq <= 16)
         need = std::max(need, path_workspace(p, Path::Decode, plan_splits(p, Path::Decode, dev->sm_count, 0)));

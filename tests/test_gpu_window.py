@@ -88,6 +88,14 @@ def test_forward(osf, dtype, D, B, Hq, Hkv, Sq, Sk, window, sinks):
     run(osf, dtype, B, Hq, Hkv, Sq, Sk, D, window, sinks)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,window,sinks", [
+    (2, 20, 4, 520, 700, 129, 130), (1, 32, 8, 700, 700, 64, 300), (3, 16, 16, 500, 1300, 200, 17), (1, 24, 8, 1000, 1000, 127, 0),
+    (2, 16, 2, 640, 640, 255, 1)])
+def test_forward_of_many_float32_rows(osf, B, Hq, Hkv, Sq, Sk, window, sinks):
+    """Enough rows for the tensor cores (D = 64, bfloat16 parts)."""
+    run(osf, "f32", B, Hq, Hkv, Sq, Sk, 64, window, sinks)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 32), ("bf16", 64), ("bf16", 96), ("bf16", 128), ("bf16", 72), ("f32", 64), ("f32", 100), ("f32", 250)])
 @pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,window,sinks", SHAPES)
 def test_gradients(osf, dtype, D, B, Hq, Hkv, Sq, Sk, window, sinks):
