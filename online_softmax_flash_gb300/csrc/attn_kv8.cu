@@ -1,9 +1,11 @@
 // Attention over the paged 8-bit K/V cache (format: kv8.cuh): the last Sq tokens of each sequence against it, with or
 // without a window and sinks.
 //
-// General kernel (float32 queries, or D above 128): a CTA takes up to 4 query rows of one (b, kv
+// General kernel (float32 queries, which e4m3 parts do not hold, or D above 128): a CTA takes up to 4 query rows of one (b, kv
 // head) and a part of the keys that they see; a warp copies the rows of 32 keys to shared memory, takes a key per lane
-// (its whole dot product with the rows), then a channel of every 32 per lane.
+// (its whole dot product with the rows), then a channel of every 32 per lane.  Bound by its reads of shared memory and the
+// conversions of codes, a few instructions to each four multiplications: float32, 16 sequences of 20000 tokens, 8 kv heads of 8 rows,
+// D = 128, 655 MB: 515 us, 1.3 TB/s.  A short one is a chain of loads and a join: 2 sequences of 777 tokens, D = 96: 14 us.
 #include "kv8.cuh"
 #include "sm100_ptx.cuh"
 #include "tma_host.cuh"
@@ -74,12 +76,12 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
             at = (s * c.P + (key & (c.P - 1))) * D;
         }
         const long long v_off = (long long)c.Hkv * c.P * D;
-        const int per = 2 * D / 16;   // 16-byte pieces of a key: K's, then V's
+        const int per = 2 * D / 16, inv = 65536 / per + 1;   // 16-byte pieces of a key: K's, then V's (i / per = i * inv >> 16)
         for (int i0 = 0; i0 < 32 * per; i0 += 32 * 8) {
             uint4 v[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int i = i0 + 32 * e + lane, k = i / per % 32, w = i % per;
+                const int i = i0 + 32 * e + lane, q = i * inv >> 16, k = q % 32, w = i - q * per;
                 const long long from = __shfl_sync(0xffffffffu, at, k);
                 const int have = __shfl_sync(0xffffffffu, page, k);
                 v[e] = make_uint4(0, 0, 0, 0);
@@ -88,7 +90,7 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const int i = i0 + 32 * e + lane, k = i / per, w = i % per;
+                const int i = i0 + 32 * e + lane, k = i * inv >> 16, w = i - k * per;
                 if (i < 32 * per)
                     *reinterpret_cast<uint4 *>(mine + (w < per / 2 ? k * pitch + w * 16 : (32 + k) * pitch + (w - per / 2) * 16)) = v[e];
             }
@@ -126,8 +128,8 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
         }
         *reinterpret_cast<float4 *>(sp[warp][lane]) = make_float4(pr[0], pr[1], pr[2], pr[3]);
         __syncwarp();
-        const int cnt = min(32, n - k0);
-        for (int k = 0; k < cnt; ++k) {
+#pragma unroll 8
+        for (int k = 0; k < 32; ++k) {   // (keys behind the last: no row sees them)
             const float4 pk4 = *reinterpret_cast<const float4 *>(sp[warp][k]);
             const float pk[RB] = {pk4.x, pk4.y, pk4.z, pk4.w};
             const unsigned char *row = mine + (32 + k) * pitch + lane;
@@ -200,9 +202,11 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 //
 // A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Two warps load, two issue the
 // products, and NG teams take the tiles in turn, each with its own S^T, O^T and references, one token's scores per thread;
-// their states meet at the end of the run.  A team is four warps, or with 16 rows two groups of four that take 8 rows each.  A group's next scores are computed while it works on these: S^T
-// is free as soon as the group has read it.  Runs are cut flat over all sequences (see FlatCut), and a
-// second kernel joins the pieces of a sequence that several CTAs share.
+// their states meet at the end of the run.  A team is four warps, or with 16 rows two groups of four that take 8 rows each.  A
+// group's next scores are computed while it works on these: S^T is free as soon as the group has read it.  Runs are cut flat over
+// all sequences (see FlatCut), and a second kernel joins the pieces of a sequence that several CTAs share.
+// Up to 8 rows of D = 128 are bound by DRAM: 8 sequences of 32768 tokens, 8 kv heads of 4 rows, 537 MB: 91 us with launches and
+// join, 5.9 TB/s (16 rows 106 us: what the groups issue for their weights; D = 64, 268 MB, 64 us: the same).
 constexpr int TT = 128;                   // tokens per tile
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
 constexpr int kMaxRing = 12;
@@ -231,13 +235,16 @@ struct Tc8 {
     static_assert(COLS <= 256, "TMEM");
 };
 
-// Work is cut flat: an item is one block of query rows of one (batch, kv head), worth its tiles and kItemCost more for what it
+// Work is cut flat: an item is one block of query rows of one (batch, kv head), worth its tiles and `cost` more for what it
 // costs besides them; the items lie one after another (batch, kv head, row block), and CTA c of nc takes the c-th part of the
 // whole, whatever items it spans.  So every CTA gets the same work, in one wave, for any mix of lengths.  An item whose tiles
 // all lie in one part is finished there; of the others a CTA holds at most two pieces, the end of one that began before (slot
 // 2 c of the partial states) and the start of one that goes on (slot 2 c + 1).
-constexpr int kItemCost = 3;
-constexpr int kMinTiles = 2;   // tiles worth a CTA
+// What an item costs: 10 tiles where a CTA has several (64 sequences of 1 to 16384 tokens, 8 kv heads of D = 128: 265 us with 0, 214
+// with 3, 182 with 6, 179 with 10 and 16; 56 of up to 600 tokens and 8 of up to 16384: 132, 71, 58, 51, 58; 64 of 16384 with 16 rows,
+// D = 64: 363, 285, 232, 197, 184), 3 where it has a part of one (8 items of 32 tiles: 17 us; with 10, which idles CTAs at the items'
+// starts, 20).
+constexpr int kMinTiles = 4;   // tiles worth a CTA (1, 2, 3, 4, 6: 8 items of 32 tiles 18, 18, 19, 17, 21 us)
 struct FlatCut {
     long long total, base;   // units of all items, and of the batches before b
     int nc;                  // CTAs that take part
@@ -248,16 +255,16 @@ __device__ __forceinline__ KeyStream stream_of(const Kv8AttnProblem &kp, int b, 
     if (n == 0) ks.n = 0;
     return ks;
 }
-__device__ __forceinline__ int item_units(const Kv8AttnProblem &kp, int b) {
+__device__ __forceinline__ int item_units(const Kv8AttnProblem &kp, int cost, int b) {
     int n;
-    return max(1, stream_of(kp, b, n).n) + kItemCost;
+    return max(1, stream_of(kp, b, n).n) + cost;
 }
 // Called by a whole warp.
-__device__ __forceinline__ FlatCut flat_cut(const Kv8AttnProblem &kp, int items_per_b, int b, int grid) {
+__device__ __forceinline__ FlatCut flat_cut(const Kv8AttnProblem &kp, int cost, int items_per_b, int b, int grid) {
     const int lane = threadIdx.x & 31;
     long long all = 0, before = 0;
     for (int i = lane; i < kp.a.B; i += 32) {
-        const long long n = item_units(kp, i);
+        const long long n = item_units(kp, cost, i);
         all += n;
         before += i < b ? n : 0;
     }
@@ -269,7 +276,7 @@ __device__ __forceinline__ FlatCut flat_cut(const Kv8AttnProblem &kp, int items_
     FlatCut f;
     f.total = all * items_per_b;
     f.base = before * items_per_b;
-    f.nc = (int)max(1LL, min((long long)grid, f.total / (kMinTiles + kItemCost)));
+    f.nc = (int)max(1LL, min((long long)grid, f.total / (kMinTiles + cost)));
     return f;
 }
 // The CTA that has unit x: the last one whose part begins at or before it.
@@ -283,23 +290,23 @@ struct Walk {
     KeyStream ks;
 };
 // False when this CTA has no work.  Called by a whole warp.
-__device__ __forceinline__ bool walk_begin(const Kv8AttnProblem &kp, int items_per_b, int flat, Walk &w) {
+__device__ __forceinline__ bool walk_begin(const Kv8AttnProblem &kp, int items_per_b, int cost, Walk &w) {
     const int lane = threadIdx.x & 31;
     w.unit0 = 0;
-    if (!flat) {
+    if (cost == 0) {   // whole items, a CTA each
         w.b = blockIdx.x / items_per_b;
         w.item = blockIdx.x % items_per_b;
         w.rest = 1;
         return true;
     }
-    const FlatCut f = flat_cut(kp, items_per_b, 0, gridDim.x);
+    const FlatCut f = flat_cut(kp, cost, items_per_b, 0, gridDim.x);
     if ((int)blockIdx.x >= f.nc) return false;
     const long long pos = f.total * blockIdx.x / f.nc;
     w.rest = f.total * (blockIdx.x + 1) / f.nc - pos;
     long long at = 0;   // units before batch b: 32 batches at a time, a lane each
     for (int b0 = 0;; b0 += 32) {
         const int bi = b0 + lane;
-        const long long ub = bi < kp.a.B ? (long long)item_units(kp, bi) * items_per_b : 0;
+        const long long ub = bi < kp.a.B ? (long long)item_units(kp, cost, bi) * items_per_b : 0;
         long long upto = ub;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -315,21 +322,21 @@ __device__ __forceinline__ bool walk_begin(const Kv8AttnProblem &kp, int items_p
         }
         at += __shfl_sync(0xffffffffu, upto, 31);
     }
-    const int ui = item_units(kp, w.b);
+    const int ui = item_units(kp, cost, w.b);
     w.item = (int)((pos - at) / ui);
     w.unit0 = (int)((pos - at) % ui);
     return true;
 }
 // The next piece; false behind the last one.
 template <int NR>
-__device__ __forceinline__ bool walk_next(const Kv8AttnProblem &kp, int row_blocks, int flat, Walk &w) {
+__device__ __forceinline__ bool walk_next(const Kv8AttnProblem &kp, int row_blocks, int cost, Walk &w) {
     if (w.rest <= 0) return false;
     const AttnProblem &p = kp.a;
     w.ks = stream_of(kp, w.b, w.n);
-    const int all = max(1, w.ks.n), units = all + kItemCost;   // the item's first kItemCost units hold no tiles
-    const int take = flat ? (int)min((long long)(units - w.unit0), w.rest) : units;
-    w.tile0 = max(0, w.unit0 - kItemCost);
-    const int tile1 = w.unit0 + take - kItemCost;
+    const int all = max(1, w.ks.n), units = all + cost;   // the item's first cost units hold no tiles
+    const int take = cost ? (int)min((long long)(units - w.unit0), w.rest) : units;
+    w.tile0 = max(0, w.unit0 - cost);
+    const int tile1 = w.unit0 + take - cost;
     if (tile1 <= w.tile0) {   // the part ends before the item's first tile
         w.rest = 0;
         return false;
@@ -339,7 +346,7 @@ __device__ __forceinline__ bool walk_next(const Kv8AttnProblem &kp, int row_bloc
     w.kvh = w.item / row_blocks;
     w.r0 = w.item % row_blocks * NR;
     w.rows = min(NR, p.Hq / p.Hkv * p.Sq - w.r0);
-    w.rest = flat ? w.rest - take : 0;
+    w.rest = cost ? w.rest - take : 0;
     w.unit0 = 0;
     return true;
 }
@@ -399,9 +406,11 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
     else tmem_ld32(addr, r);
 }
 
-template <int D, int NR>
+// FLAT: cut flat, or whole items (one kernel for both: 128 items of 128 tiles of 16 rows, D = 64, 95 us against 87).
+template <int D, int NR, bool FLAT>
 __global__ void __launch_bounds__((Tc8<D, NR>::THREADS), 1)
-attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProblem kp, int q_vec, int row_blocks, int flat) {
+attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProblem kp, int q_vec, int row_blocks, int item_cost) {
+    const int cost = FLAT ? item_cost : 0;   // 0: whole items, a CTA each
     using C = Tc8<D, NR>;
     constexpr int NG = C::NG, RT = C::RT, HS = C::HS, SOFT = 128 * C::GROUPS;
     const AttnProblem &p = kp.a;
@@ -448,7 +457,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     tc_fence_after();
     const uint32_t tmem = tmem_sh;
     Walk w;
-    bool live = walk_begin(kp, items_per_b, flat, w);
+    bool live = walk_begin(kp, items_per_b, cost, w);
 
     if (warp >= C::W_LOAD && warp < C::W_MMA) {
         // ================================================================ loads: K and V, a lane per page of the tile
@@ -459,7 +468,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         bool ok = true;
         int st = 0;
         uint32_t par = 1;
-        while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
+        while (ok && live && walk_next<NR>(kp, row_blocks, cost, w)) {
             // whether some row sees this lane's page of the piece's tile i, and the table's entry for it
             const int near = p.window ? w.n - p.Sq - p.window : -c.P;   // the window of the first row begins behind it
             const int *entries = c.table + (long long)w.b * c.per_seq;
@@ -511,7 +520,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         int st = 0, g = 0;                           // stage and group of the next tile,
         uint32_t st_par = 0, g_par = 0, q_par = 0;   // and the parities of their barriers
         bool again = false;                          // the groups have had a tile each
-        while (ok && live && walk_next<NR>(kp, row_blocks, flat, w)) {
+        while (ok && live && walk_next<NR>(kp, row_blocks, cost, w)) {
             if (lane == 0 && w.tiles > 0) {
                 if (is_s) ok = mbar_wait(smem_u32(&bars.q_full), q_par, &abort_flag);
                 q_par ^= 1;
@@ -573,7 +582,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         // a wait that ran out is told to the whole group at its next vote, so that all leave together
         bool failed = false;
         int gt = 0;   // tiles of the CTA so far; tile t is its team's t / NG-th
-        while (live && walk_next<NR>(kp, row_blocks, flat, w)) {
+        while (live && walk_next<NR>(kp, row_blocks, cost, w)) {
             // ------------------------------------------------------------ Q parts: a warp per row
             for (int r = warp; r < NR; r += 4 * C::GROUPS) {
                 constexpr int E = D / 32;   // channels E * lane .., zeros from p.D on
@@ -932,26 +941,31 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     }
 }
 
-// Rows of the items that several CTAs shared: a block per item, the same cut of the work as above.
+// Rows of the items that several CTAs shared, joined; the same cut of the work as above.  gridDim = (items, parts of their
+// rows): a block takes `rpb` rows of an item, four channels to a thread, and the groups of threads that are left take the pieces
+// in turn, KG at a time (one sequence of 100000 tokens in 152 pieces: 43 us with the pieces one round after another).
 template <int D, int NR>
-__global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnProblem kp, int row_blocks, int grid) {
+__global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnProblem kp, int row_blocks, int grid, int cost, int rpb) {
+    __shared__ float4 sA[256];
+    __shared__ float2 sML[256];
     const AttnProblem &p = kp.a;
     const int G = p.Hq / p.Hkv, R = G * p.Sq, items_per_b = p.Hkv * row_blocks;
     const int b = blockIdx.x / items_per_b, item = blockIdx.x % items_per_b;
-    const FlatCut w = flat_cut(kp, items_per_b, b, grid);
-    const int ui = item_units(kp, b);
+    const FlatCut w = flat_cut(kp, cost, items_per_b, b, grid);
+    const int ui = item_units(kp, cost, b);
     const long long p0 = w.base + (long long)item * ui;
-    const int c0 = cta_of(w, p0 + kItemCost), c1 = cta_of(w, p0 + ui - 1);   // CTAs of the first and the last tile
+    const int c0 = cta_of(w, p0 + cost), c1 = cta_of(w, p0 + ui - 1);   // CTAs of the first and the last tile
     griddep_wait();
     if (c0 == c1) return;
     const int r0 = item % row_blocks * NR, rows = min(NR, R - r0);
     constexpr int KG = 8;   // pieces whose states are loaded together
-    for (int x = threadIdx.x; x < rows * (D / 4); x += blockDim.x) {
-        const int r = x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
-        if (c >= p.D) continue;
+    const int per = rpb * (D / 4), groups = per < 256 ? 256 / per : 1, g = threadIdx.x / per;   // (rpb, D: powers of two)
+    for (int x = threadIdx.x % per; x < per; x += 256) {
+        const int r = blockIdx.y * rpb + x / (D / 4), c = x % (D / 4) * 4, gr = r0 + r;
+        const bool mine = r < rows && c < p.D;
         float M = -INFINITY, L = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k0 = c0; k0 <= c1; k0 += KG) {
+        for (int k0 = c0 + g * KG; mine && k0 <= c1; k0 += groups * KG) {
             float2 ml[KG];
             float4 v[KG];
             float mx = M;
@@ -975,7 +989,26 @@ __global__ void __launch_bounds__(256) kv8_combine_kernel(const Kv8AttnProblem k
                 L = fmaf(wt, ml[e].y, L);
             }
         }
-        write_row(p, b, item / row_blocks * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
+        if (groups > 1 && c1 - c0 + 1 > KG) {   // the groups' sums, in their order
+            sA[threadIdx.x] = A;
+            sML[threadIdx.x] = make_float2(M, L);
+            __syncthreads();
+            if (g > 0) return;
+            for (int e = 1; e < groups; ++e) M = fmaxf(M, sML[e * per + x].x);
+            const float ref = M == -INFINITY ? 0.f : M;
+            A = make_float4(0.f, 0.f, 0.f, 0.f);
+            L = 0.f;
+            for (int e = 0; e < groups; ++e) {
+                const float wt = ex2_approx(sML[e * per + x].x - ref);
+                const float4 v = sA[e * per + x];
+                A.x = fmaf(wt, v.x, A.x); A.y = fmaf(wt, v.y, A.y);
+                A.z = fmaf(wt, v.z, A.z); A.w = fmaf(wt, v.w, A.w);
+                L = fmaf(wt, sML[e * per + x].y, L);
+            }
+        } else if (g > 0) {
+            return;
+        }
+        if (mine) write_row(p, b, item / row_blocks * G + gr / p.Sq, gr % p.Sq, c, A, M, L);
     }
 }
 
@@ -1006,7 +1039,7 @@ static bool use_tc(const AttnProblem &p) {
 // against 68.2; 512 of 32 136 against 127.)
 constexpr int kCutCost = 20, kCutCost16 = 28;
 struct TcPlan {
-    int nr, row_blocks, flat, grid;
+    int nr, row_blocks, flat, grid, item_cost;
 };
 static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
     TcPlan t;
@@ -1018,6 +1051,7 @@ static TcPlan tc_plan(const AttnProblem &p, int sm_count) {
     const long long waves = (items + sm_count - 1) / sm_count;
     t.flat = waves * per - items * per / sm_count > (t.nr == 16 ? kCutCost16 : kCutCost);
     const long long worth = items * per / kMinTiles;
+    t.item_cost = items < sm_count ? 3 : 10;
     t.grid = (int)(!t.flat ? items : worth < sm_count ? (worth < 1 ? 1 : worth) : sm_count);
     return t;
 }
@@ -1038,7 +1072,8 @@ template <int D, int NR>
 static cudaError_t launch_tc_t(Kv8AttnProblem kp, const TcPlan &t, char *partials, cudaStream_t s) {
     using C = Tc8<D, NR>;
     const AttnProblem &p = kp.a;
-    cudaError_t e = set_max_dynamic_smem((const void *)attn_kv8_tc_kernel<D, NR>, (int)C::SMEM);
+    auto kernel = t.flat ? attn_kv8_tc_kernel<D, NR, true> : attn_kv8_tc_kernel<D, NR, false>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, (int)C::SMEM);
     if (e != cudaSuccess) return e;
     CUtensorMap m;
     const long long rows = (long long)kp.c.n_pages * 2 * kp.c.Hkv * kp.c.P;
@@ -1046,13 +1081,15 @@ static cudaError_t launch_tc_t(Kv8AttnProblem kp, const TcPlan &t, char *partial
     kp.part = reinterpret_cast<float *>(partials);
     kp.part_ml = reinterpret_cast<float2 *>(partials + round256(2 * (size_t)t.grid * NR * D * sizeof(float)));
     const int q_vec = (reinterpret_cast<uintptr_t>(p.q) & 3u) == 0 && ((p.q_sb | p.q_sh | p.q_ss) & 1) == 0;
-    attn_kv8_tc_kernel<D, NR><<<t.grid, C::THREADS, C::SMEM, s>>>(m, kp, q_vec, t.row_blocks, t.flat);
+    kernel<<<t.grid, C::THREADS, C::SMEM, s>>>(m, kp, q_vec, t.row_blocks, t.flat ? t.item_cost : 0);
     count_launches(1);
     e = cudaGetLastError();
     if (e != cudaSuccess || !t.flat) return e;
     count_launches(1);
-    return launch_dependent(kv8_combine_kernel<D, NR>, dim3((unsigned)(p.B * p.Hkv * t.row_blocks)), dim3(256), 0, s, kp,
-                            t.row_blocks, t.grid);
+    // a block per row where an item has more than one round of pieces (64 items of 16 rows in 152 CTAs: 91 us; a block per row 95)
+    const int items = p.B * p.Hkv * t.row_blocks, rpb = t.grid > 8LL * items ? 1 : NR;
+    return launch_dependent(kv8_combine_kernel<D, NR>, dim3((unsigned)items, (unsigned)(NR / rpb)), dim3(256), 0, s, kp, t.row_blocks,
+                            t.grid, t.item_cost, rpb);
 }
 
 cudaError_t launch_attn_kv8(const Kv8AttnProblem &kp0, void *partials, int sm_count, cudaStream_t s) {
