@@ -206,7 +206,13 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
 // item and merge their results through distributed shared memory at the end, instead of writing
 // partial states for a separate combine kernel.
 // WIN: a window with sinks (AttnProblem::window); rows may then have fewer channels than D (p.D, a multiple of 32), the rest of
-// the tiles being zeros.
+// the tiles being zeros.  The tile's time is the dense kernel's; what a window adds lies between items, which are short.  B=2 Hq=32
+// Hkv=8, 4096 tokens of D = 128, window 1024, 4 sinks: 157 us, 770 TFLOP/s of the pairs seen (without sinks 148, window 128 78).
+// A CTA's clock there: 3700 cycles a key tile (softmax 1750, hand-offs 400, P V and the next scores 1500), masked ones 4500, and 9000
+// from an item's last P to the next one's first scores (O's last product 1700, its store 3700, looking the item up 1300, waiting for
+// the scores 2300); an item is nine tiles.  Not kept: the next item's scores issued before tile 1 is done (the registers that the
+// issue loop spills for it cost more: 214 us), the next item looked up during the last product (164), an issuer to each Q tile
+// (170: the two tiles' products no longer alternate; D = 64 with scores computed ahead 132 against 131).
 template <int D, bool X3, bool MERGE, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,

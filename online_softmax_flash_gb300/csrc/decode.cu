@@ -55,7 +55,8 @@ __device__ __forceinline__ uint32_t ld_bf16x2(const __nv_bfloat16 *p) {
 }
 
 // WIN: a window with sinks (AttnProblem::window); the tiles are then those of the rows' key_stream, and rows may have fewer
-// channels than D (p.D, a multiple of 32), the rest of the tiles being zeros.
+// channels than D (p.D, a multiple of 32), the rest of the tiles being zeros.  Bound by DRAM and, the calls being short, by the
+// ramp up to it: B=8 Hq=32 Hkv=8 D=128, window 4096, 134 MB: 35 us with the join, 3.8 TB/s.
 template <int D, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 2)
 decode_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
