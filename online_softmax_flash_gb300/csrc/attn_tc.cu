@@ -149,8 +149,8 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
     const long long it = (long long)r * g + c;
     if (it >= n_items) return false;
     const int units = p.B * p.Hq;
-    const int qb_rank = (int)(it / units);
-    w.bh = (int)(it % units);
+    const int qb_rank = (int)((unsigned)it / (unsigned)units);
+    w.bh = (int)((unsigned)it - (unsigned)qb_rank * (unsigned)units);
     const int qb = p.causal ? (n_qb - 1 - qb_rank) : qb_rank;   // heaviest blocks first
     w.q0 = qb * 2 * BM;
     w.b = w.bh / p.Hq;
@@ -207,12 +207,13 @@ __device__ __forceinline__ bool item_at(const AttnProblem &p, int n_qb, int n_it
 // partial states for a separate combine kernel.
 // WIN: a window with sinks (AttnProblem::window); rows may then have fewer channels than D (p.D, a multiple of 32), the rest of
 // the tiles being zeros.  The tile's time is the dense kernel's; what a window adds lies between items, which are short.  B=2 Hq=32
-// Hkv=8, 4096 tokens of D = 128, window 1024, 4 sinks: 157 us, 770 TFLOP/s of the pairs seen (without sinks 148, window 128 78).
+// Hkv=8, 4096 tokens of D = 128, window 1024, 4 sinks: 157 us, 770 TFLOP/s of the pairs seen (without sinks 147, window 128 74).
 // A CTA's clock there: 3700 cycles a key tile (softmax 1750, hand-offs 400, P V and the next scores 1500), masked ones 4500, and 9000
 // from an item's last P to the next one's first scores (O's last product 1700, its store 3700, looking the item up 1300, waiting for
 // the scores 2300); an item is nine tiles.  Not kept: the next item's scores issued before tile 1 is done (the registers that the
-// issue loop spills for it cost more: 214 us), the next item looked up during the last product (164), an issuer to each Q tile
-// (170: the two tiles' products no longer alternate; D = 64 with scores computed ahead 132 against 131).
+// issue loop spills for it cost more: 214 us; 179 with the items handed to the issuer through shared memory), the next item looked
+// up during the last product (164), an issuer to each Q tile (170: the two tiles' products no longer alternate; D = 64 with scores
+// computed ahead 132 against 131), eight or sixteen registers moved from the softmax to the issuer (172, 240).
 template <int D, bool X3, bool MERGE, bool WIN>
 __global__ void __launch_bounds__(NTHREADS, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
@@ -741,7 +742,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     // 32-byte stores when every row starts on a 32-byte boundary
                     const bool o32 = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)(p.o_ss * 2) |
                                        (uintptr_t)(p.o_sh * 2) | (uintptr_t)(p.o_sb * 2)) & 31) == 0;
-#pragma unroll
+#pragma unroll(WIN ? 1 : D / 32)   // (with a window items are short, and code that runs once an item is fetched anew; window 128: 78 -> 74 us)
                     for (int c = 0; c < D / 32; ++c) {
                         if (WIN && c * 32 >= p.D) break;
                         uint32_t o[32];
