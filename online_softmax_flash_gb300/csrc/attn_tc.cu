@@ -537,13 +537,20 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     snk = p.sinks - key0;
                     need_mask = need_mask || (key0 + p.window <= row_first + BM - 1 + p.causal_off && key0 + BN > p.sinks);
                 }
-                uint32_t seen[WIN ? 4 : 1];   // a bit for each column
-                if constexpr (WIN)
+                auto seen_of = [&](int c) { return need_mask ? seen_bits(lim - 32 * c, low - 32 * c, snk - 32 * c) : ~0u; };
+                uint32_t seen[WIN && !X3 ? 4 : 1];   // a bit for each column
+                if constexpr (WIN && !X3)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) seen[c] = need_mask ? seen_bits(lim - 32 * c, low - 32 * c, snk - 32 * c) : ~0u;
-                auto hidden = [&](int c, int k) {
-                    if constexpr (WIN) return !(seen[c] >> k & 1u);
-                    else return c * 32 + k >= lim;
+                    for (int c = 0; c < 4; ++c) seen[c] = seen_of(c);
+                // the hidden columns of chunk c (columns 32 c .. 32 c + 31) of a float32 tile: -inf.  Behind a branch, since most tiles
+                // hide none, and from one word (float32, one head of 4096 rows and keys 34 us, with a selection at each column 43;
+                // 64 heads of 2000 rows, window 1000, 170, with the words of all chunks in an array 364)
+                auto mask_chunk = [&](int c, uint32_t (&s)[32]) {
+                    if (!need_mask) return;
+                    const uint32_t word = WIN ? seen_of(c) : bits_below(lim - 32 * c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if (!(word >> k & 1u)) s[k] = __float_as_uint(-INFINITY);
                 };
                 uint32_t sr[X3 ? 1 : 4][32];   // bf16 mode: the whole score row in registers
                 float mx;
@@ -555,11 +562,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(s_addr + c * 32, sr[0]);
                         tmem_ld_wait();
+                        mask_chunk(c, sr[0]);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            const float x = (need_mask && hidden(c, k)) ? -INFINITY : __uint_as_float(sr[0][k]);
-                            m4[k & 3] = fmaxf(m4[k & 3], x);
-                        }
+                        for (int k = 0; k < 32; ++k) m4[k & 3] = fmaxf(m4[k & 3], __uint_as_float(sr[0][k]));
                     }
                     mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
                 } else {
@@ -571,7 +576,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                         for (int c = 0; c < 4; ++c)
 #pragma unroll
                             for (int k = 0; k < 32; ++k)
-                                if (hidden(c, k)) sr[c][k] = __float_as_uint(-INFINITY);
+                                if (WIN ? !(seen[WIN ? c : 0] >> k & 1u) : c * 32 + k >= lim) sr[c][k] = __float_as_uint(-INFINITY);
                     }
                     // row max: eight independent chains of 3-input max, then a short tree
                     float mm[8];
@@ -607,14 +612,13 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     for (int c = 0; c < 4; ++c) {
                         tmem_ld32(s_addr + c * 32, sr[0]);
                         tmem_ld_wait();
+                        mask_chunk(c, sr[0]);
                         uint32_t ph[16], pl[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            const float s0 = (need_mask && hidden(c, 2 * k)) ? -INFINITY : __uint_as_float(sr[0][2 * k]);
-                            const float s1 = (need_mask && hidden(c, 2 * k + 1)) ? -INFINITY
-                                                                                       : __uint_as_float(sr[0][2 * k + 1]);
                             float p0, p1;
-                            f2_unpack(f2_fma(f2_pack(s0, s1), sc2, nm2), p0, p1);
+                            f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[0][2 * k]), __uint_as_float(sr[0][2 * k + 1])), sc2, nm2),
+                                      p0, p1);
                             p0 = ex2_approx(p0);
                             p1 = ex2_approx(p1);
                             acc = f2_add(acc, f2_pack(p0, p1));
