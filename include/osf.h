@@ -410,6 +410,9 @@ int osf_kv8_read(const void *pages, const float *scales, int n_pages, int page_t
  * window: 0 (none) or at least 1; sinks >= 0 (without a window of no effect).  Pages that no row sees are not read.
  * strides: NULL (contiguous) or 6 element strides, Q: b, h, s  O: b, h, s, under the rules of osf_attn_fwd_gqa_ex.
  * A row that sees nothing gets O = 0 and lse = -inf.
+ * Rounding (bfloat16, D <= 128): a token's weight times its page's scale counts with float16's 11 bits down to 2^-100 of the row's
+ * largest, whatever the scales, and with fewer below that; a query's 8 bits count down to 2^-14 of its row's largest entry (of
+ * smaller entries up to 2^-22 of that is lost).  Scores, sums and lse are float32; the other types are float32 throughout.
  * lse: optional contiguous float32 [B, Hq, Sq]; of a row that sees a score of NaN or +inf: NaN, as its O.
  * workspace: osf_attn_kv8_workspace_bytes bytes, 16-byte aligned.
  * (Hq / Hkv) * Sq <= 32768, else OSF_ERR_UNSUPPORTED.  Outputs must not overlap one another or an input -> else

@@ -193,12 +193,16 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 //   S^T[128 tokens x columns]   = K[128 x D] . Q parts^T,      O^T[D x columns] += V^T[D x 128] . P parts[128 x columns],
 // so no thread touches a code but at a sequence's edges.  The small operands are sums of e4m3 parts, one column of the
 // product each, the k-th part in units of 16^-k: a bfloat16 query has 8 bits, which are two parts exactly (its row scaled by
-// a power of two to a largest entry in 128 .. 256; entries below 2^-14 of that lose low bits, 2^-22 of it at most).  P takes
-// three parts: 12 bits, and at most 2^-26 of the row's reference is lost of a weight below that.
+// a power of two to a largest entry in 128 .. 256; entries below 2^-14 of that lose low bits, 2^-22 of it at most).
 // A token's V scale is not applied to its codes but to its weight.  Scales can lie far apart, so what goes into the
-// product is 2^(y + e - m'), y the base-2 score, e the exponent of the scale and m' a reference of the sums y + e: exact
-// relative to the largest P * scale, whichever page it comes from.  The denominator has its own reference m of the y.
-// Both references are whole numbers and move only when a value passes them, to 3 .. 4 above the largest.
+// product is 2^x with x = y + e - m', y the base-2 score, e the exponent of the scale and m' a reference of the sums y + e.  The
+// denominator has its own reference m of the y.  Both references are whole numbers and move only when a value passes
+// them, to 3 .. 4 above the largest.
+// One reference serves all tokens and channels, but a channel's sum can be due to tokens far below it (behind a heavy key
+// whose V is zero there, or a page with one large channel), so every weight keeps its 11 bits: it is rounded to float16 at one
+// of four levels, level l for x in (-28 (l + 1), -28 l] (the last one: all below) in units of 2^(-15 - 28 l), and split into
+// three e5m2 parts of 3 bits, which have float16's exponents (part_unit).  That is float16's rounding, 2^-11 of the weight, down
+// to 2^-112 of the reference.  Each level has columns of its own, which are zeros but for warps that have weights there.
 //
 // A CTA takes up to NR query rows of one (b, kv head) against a run of tiles of 128 tokens.  Two warps load, two issue the
 // products, and NG teams take the tiles in turn, each with its own S^T, O^T and references, one token's scores per thread;
@@ -211,6 +215,8 @@ constexpr int TT = 128;                   // tokens per tile
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
 constexpr int kMaxRing = 12;
 constexpr float kHeadroom = 3.f;              // a new reference is this, and up to 1 more, above the largest
+constexpr int kLevels = 4;                    // levels of weights, and the binades of one
+constexpr float kLevelBits = 28.f, kLevelUnit = 0x1p-28f;
 
 template <int D, int NR>
 struct Tc8 {
@@ -220,7 +226,8 @@ struct Tc8 {
     static constexpr int W_LOAD = 4 * GROUPS, W_MMA = W_LOAD + 2, THREADS = (W_MMA + 2) * 32;
     static constexpr uint32_t TILE = TT * D;                        // K or V of a tile
     static constexpr int NQ = 2 * NR < 16 ? 16 : 2 * NR;            // columns of Q parts: part p of row r at p * NR + r
-    static constexpr int PLANES = (3 * NR + 15) / 16, NP = 16 * PLANES;   // columns of P parts, in planes of 16
+    // columns of P parts, in planes of 16: part k of row r at level l at (3 l + k) * NR + r
+    static constexpr int NP = 3 * kLevels * NR, PLANES = NP / 16;
     static constexpr uint32_t Q_BYTES = 4096, P_BYTES = PLANES * TT * 16;
     static constexpr uint32_t O_BYTES = NG * NR * D * 4;
     static constexpr uint32_t Q_OFF = 0, P_OFF = Q_BYTES, O_OFF = P_OFF + NG * P_BYTES;
@@ -229,10 +236,11 @@ struct Tc8 {
     static constexpr int STAGES = FIT < kMaxRing ? FIT : kMaxRing;
     static constexpr uint32_t SMEM = RING_OFF + STAGES * 2 * TILE + 1024;
     static constexpr uint32_t SWZ = D == 128 ? 2 : 4, GROUP8 = 8 * D;   // swizzle type, bytes of eight rows
-    static constexpr uint32_t IDESC_S = idesc_e4m3_f32(TT, NQ, 0, 0), IDESC_O = idesc_e4m3_f32(D, NP, 1, 1);
+    static constexpr uint32_t IDESC_S = idesc_f8_f32(TT, NQ, 0, 0, kE4M3, kE4M3);
+    static constexpr uint32_t IDESC_O = idesc_f8_f32(D, NP, 1, 1, kE4M3, kE5M2);
     static constexpr uint32_t O_COL = NG * NQ, COLS = O_COL + NG * NP;   // S^T of team g at column NQ g, O^T at O_COL + NP g
-    static constexpr uint32_t TMEM = COLS <= 128 ? 128 : 256;
-    static_assert(COLS <= 256, "TMEM");
+    static constexpr uint32_t TMEM = COLS <= 256 ? 256 : 512;
+    static_assert(COLS <= 512, "TMEM");
 };
 
 // Work is cut flat: an item is one block of query rows of one (batch, kv head), worth its tiles and `cost` more for what it
@@ -406,6 +414,34 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t addr, uint32_t (&r)[N]) {
     else tmem_ld32(addr, r);
 }
 
+// Units of the e5m2 parts of a float16 weight.  The first has 3 of its 11 bits; what is left is at most 2^-3 of its binade, and
+// after the second part at most 2^-7, a whole number of the float16's last places up to 8: so in these units the parts lie in
+// e5m2's range, and the third is exact, for weights of 2^-13 and more.
+__device__ __forceinline__ constexpr float part_unit(int k) { return k == 0 ? 1.f : k == 1 ? 0x1p-3f : 0x1p-8f; }
+// A token's weights of RT rows at level lv, split into parts, to its row of P.
+template <int NR, int RT>
+__device__ __forceinline__ void store_parts(uint32_t p_row, int lv, const uint32_t (&w)[RT / 2]) {
+    uint32_t part[3][RT / 4];   // words of four rows
+#pragma unroll
+    for (int r = 0; r < RT / 2; ++r) {
+        uint32_t h = w[r];
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t x = f16x2_to_e5m2x2(h);
+            if (r % 2 == 0) part[k][r / 2] = x;
+            else part[k][r / 2] |= x << 16;
+            if (k < 2) h = f16x2_rest(h, e5m2x2_to_f16x2(x), k == 0 ? 0x48004800u : 0x50005000u);   // times 2^3, 2^5
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const int word = NR == RT ? (3 * lv + k) * (RT / 4) : 4 * (3 * lv + k);   // (16 rows: a plane to a part, and p_row says which half)
+        const uint32_t at = p_row + (word >> 2) * (TT * 16) + (word & 3) * 4;
+        if constexpr (RT == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(part[k][0]) : "memory");
+        else asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(part[k][0]), "r"(part[k][1]) : "memory");
+    }
+}
+
 // FLAT: cut flat, or whole items (one kernel for both: 128 items of 128 tiles of 16 rows, D = 64, 95 us against 87).
 template <int D, int NR, bool FLAT>
 __global__ void __launch_bounds__((Tc8<D, NR>::THREADS), 1)
@@ -425,6 +461,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
     __shared__ __align__(16) float ref[C::GROUPS][2 * RT], fac[C::GROUPS][2 * RT];   // references m, m', and what moves to them
     __shared__ float sum_l[C::GROUPS][4][RT];
     __shared__ uint32_t poison[NR][D / 32];   // channels that a NaN value reaches
+    __shared__ volatile int below[C::GROUPS];  // whether a group has had weights behind the first level in this piece
     griddep_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint8_t *sgen = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -450,7 +487,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         abort_flag = 0;
         mbar_init_fence();
     }
-    for (int i = tid; i < (int)C::Q_BYTES / 16; i += C::THREADS) st_shared_v4(sQ + 16 * i, 0u, 0u, 0u, 0u);   // unused columns
+    // unused columns of Q, and the levels of P that no weight is at
+    for (int i = tid; i < (int)C::O_OFF / 16; i += C::THREADS) st_shared_v4(sQ + 16 * i, 0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -581,6 +619,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
         const uint32_t p_row = sP + g * C::P_BYTES + r128 * 16 + rh;
         // a wait that ran out is told to the whole group at its next vote, so that all leave together
         bool failed = false;
+        bool deep = false;   // whether this warp's rows of P hold weights behind the first level
         int gt = 0;   // tiles of the CTA so far; tile t is its team's t / NG-th
         while (live && walk_next<NR>(kp, row_blocks, cost, w)) {
             // ------------------------------------------------------------ Q parts: a warp per row
@@ -640,6 +679,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             }
             for (int i = tid; i < NR * (D / 32); i += SOFT) poison[i / (D / 32)][i % (D / 32)] = 0;
             if (r128 < 2 * RT) ref[gi][r128] = kRowFloor;
+            if (r128 == 0) below[gi] = 0;
             fence_proxy_async_smem();
             named_barrier(1, SOFT);
             // (a piece without tiles waits for no product, so several could pass while the issuer sleeps: they are not counted)
@@ -693,7 +733,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&bars.s_free[g]));
-                const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs), ev8 = ev + 8.f;
+                const float kscale = pow2_of(kv8_exponent(ks)), ev = (float)kv8_exponent(vs), ev15 = ev + 15.f;
                 float y[RT];
 #pragma unroll
                 for (int r = 0; r < RT; r += 4) {
@@ -784,21 +824,21 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                         ok = mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
                         failed = !__all_sync(0xffffffffu, ok);
                         tc_fence_after();
+                        const int levels = below[gi] ? kLevels : 1;   // (of earlier tiles: seen since the barrier)
                         if constexpr (HS == 1) {
-#pragma unroll
-                            for (int pl = 0; pl < C::PLANES; ++pl) {
+#pragma unroll 1
+                            for (int pl = 0; pl < (levels * 3 * NR + 15) / 16; ++pl) {
                                 uint32_t o[16];
                                 tmem_ld16(o_addr + 16 * pl, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
-                                    if (16 * pl + e < 3 * NR) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[(16 * pl + e) % NR]);
+                                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f[e % NR]);
                                 tmem_st16(o_addr + 16 * pl, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7], o[8], o[9], o[10],
                                           o[11], o[12], o[13], o[14], o[15]);
                             }
                         } else {
-#pragma unroll
-                            for (int k = 0; k < 3; ++k) {
+#pragma unroll 1
+                            for (int k = 0; k < 3 * levels; ++k) {
                                 uint32_t o[8];
                                 tmem_ld8(o_addr + NR * k, o);
                                 tmem_ld_wait();
@@ -810,43 +850,59 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                         tmem_st_wait();
                     }
                 }
-                // weights, and their parts in words of four rows
-                uint32_t part[3][RT / 4];
+                // weights in float16, and the smallest of them
+                uint32_t h[RT / 2], low = 0x7bff7bffu;
 #pragma unroll
                 for (int r = 0; r < RT; r += 2) {
                     l[r] += ex2_approx(y[r] + m[r]);
                     l[r + 1] += ex2_approx(y[r + 1] + m[r + 1]);
-                    uint32_t h = f32_to_f16x2(ex2_approx(y[r] + (mp[r] + ev8)), ex2_approx(y[r + 1] + (mp[r + 1] + ev8)));
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) {
-                        const uint32_t x = f16x2_to_e4m3x2(h);
-                        if (r % 4 == 0) part[k][r / 4] = x;
-                        else part[k][r / 4] |= x << 16;
-                        if (k < 2) h = f16x2_rest16(h, e4m3x2_to_f16x2(x));
-                    }
+                    h[r / 2] = f32_to_f16x2(ex2_approx(y[r] + (mp[r] + ev15)), ex2_approx(y[r + 1] + (mp[r + 1] + ev15)));
+                    low = f16x2_min(low, h[r / 2]);
                 }
                 // the product that read the last weights is done
                 if (done > 0) {
                     ok = !failed && mbar_wait(smem_u32(&bars.pv_done[g]), (done - 1) & 1, &abort_flag);
                     failed = !__all_sync(0xffffffffu, ok);
                 }
-                if constexpr (HS == 1) {
+                // weights below the first level (hidden ones look like those at first)
+                constexpr uint32_t kLowest = 0x0800u;   // float16 2^(15 - kLevelBits)
+                if (__any_sync(0xffffffffu, deep || (low & 0xffffu) < kLowest || low >> 16 < kLowest)) {
+                    bool any = false;
 #pragma unroll
-                    for (int pl = 0; pl < C::PLANES; ++pl) {
-                        uint32_t x[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            constexpr int W = RT / 4;   // words of a part
-                            const int word = 4 * pl + e;
-                            x[e] = word < 3 * W ? part[word / W < 3 ? word / W : 0][word % W] : 0u;
-                        }
-                        st_shared_v4(p_row + pl * TT * 16, x[0], x[1], x[2], x[3]);
+                    for (int r = 0; r < RT; ++r) {
+                        const float x = y[r] + (mp[r] + ev);
+                        any |= x <= -kLevelBits && x > -125.f;   // (2^-125 of the reference is nothing at the last level either)
                     }
-                } else {   // a plane holds a part of all 16 rows
+                    any = __any_sync(0xffffffffu, any);
+                    if (any || deep) {
+#pragma unroll 1
+                        for (int lv = 0; lv < kLevels; ++lv) {
+                            const float from = -kLevelBits * lv, to = lv == kLevels - 1 ? -INFINITY : from - kLevelBits;
+                            uint32_t w[RT / 2];
 #pragma unroll
-                    for (int k = 0; k < 3; ++k)
-                        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(p_row + k * TT * 16), "r"(part[k][0]), "r"(part[k][1]) : "memory");
+                            for (int r = 0; r < RT; r += 2) {
+                                float v[2];
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const float x = y[r + e] + (mp[r + e] + ev);
+                                    // (a NaN is at the first level)
+                                    const bool here = (lv == 0 || x <= from) && !(x <= to);
+                                    v[e] = here ? ex2_approx(x - from + 15.f) : 0.f;
+                                }
+                                w[r / 2] = f32_to_f16x2(v[0], v[1]);
+                            }
+                            if (lv == 0) {
+#pragma unroll
+                                for (int r = 0; r < RT / 2; ++r) h[r] = w[r];
+                            } else {
+                                store_parts<NR, RT>(p_row, lv, w);
+                            }
+                        }
+                    }
+                    deep = any;
+                    if (any && lane == 0) below[gi] = 1;
                 }
+                store_parts<NR, RT>(p_row, 0, h);
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
@@ -863,15 +919,33 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 failed = !__all_sync(0xffffffffu, ok);
             }
             tc_fence_after();
-            uint32_t o[3 * RT < 16 ? 16 : 3 * RT];   // part k of row r at k * RT + r
-            if constexpr (HS == 1) {
-                tmem_ld16(o_addr, o);
-                if constexpr (NR == 8) tmem_ld8(o_addr + 16, o + 16);
-            } else {
+            // the sums of the levels that are not zero, each three parts: in units of 2^(m' - 15)
+            named_barrier(2 + gi, 128);
+            const int top_level = below[gi] ? kLevels - 1 : 0;
+            float sum_o[RT];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) tmem_ld8(o_addr + NR * k, o + RT * k);
+            for (int r = 0; r < RT; ++r) sum_o[r] = 0.f;
+#pragma unroll 1
+            for (int lv = top_level; lv >= 0; --lv) {
+                uint32_t o[3 * RT];   // part k of row r at k * RT + r
+                if constexpr (NR == 4) {
+                    tmem_ld8(o_addr + 3 * NR * lv, o);
+                    tmem_ld4(o_addr + 3 * NR * lv + 8, o + 8);
+                } else if constexpr (NR == 8) {
+                    tmem_ld16(o_addr + 3 * NR * lv, o);
+                    tmem_ld8(o_addr + 3 * NR * lv + 16, o + 16);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) tmem_ld8(o_addr + NR * (3 * lv + k), o + RT * k);
+                }
+                tmem_ld_wait();
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const float v = fmaf(__uint_as_float(o[2 * RT + r]), part_unit(2),
+                                         fmaf(__uint_as_float(o[RT + r]), part_unit(1), __uint_as_float(o[r])));
+                    sum_o[r] = fmaf(sum_o[r], kLevelUnit, v);
+                }
             }
-            tmem_ld_wait();
             tc_fence_before();
             const int ch = D == 128 ? r128 : w4 * 16 + lane;   // M = 64: 16 lanes of each warp's 32
             const bool mine = D == 128 || lane < 16;
@@ -879,9 +953,8 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
             for (int r = 0; r < RT; ++r) {
                 const float sum = warp_sum(l[r]);
                 if (lane == 0) sum_l[gi][w4][r] = sum;
-                float v = fmaf(__uint_as_float(o[2 * RT + r]), 0x1p-8f, fmaf(__uint_as_float(o[RT + r]), 0x1p-4f, __uint_as_float(o[r])));
-                // in units of 2^(m' - 8) so far: relative to m
-                v = taken > 0 ? scale_by(v * 0x1p-8f, (int)fmaxf(-250.f, fminf(250.f, m[r] - mp[r]))) : 0.f;
+                // relative to m
+                const float v = taken > 0 ? scale_by(sum_o[r] * 0x1p-15f, (int)fmaxf(-250.f, fminf(250.f, m[r] - mp[r]))) : 0.f;
                 if (mine) so[(g * NR + rh + r) * D + ch] = v;
             }
             named_barrier(1, SOFT);

@@ -92,26 +92,27 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x2(float lo, float hi) {
     return r;
 }
 
-// The same of two float16.
-__device__ __forceinline__ uint32_t f16x2_to_e4m3x2(uint32_t h) {
+// Two float16 as e5m2 codes (low byte first), to the nearest, ties to even, and back: the upper bytes of float16.
+__device__ __forceinline__ uint32_t f16x2_to_e5m2x2(uint32_t h) {
     unsigned short r;
-    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
     return r;
 }
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)codes));
-    return h;
+__device__ __forceinline__ uint32_t e5m2x2_to_f16x2(uint32_t codes) { return __byte_perm(codes, 0, 0x1404); }
+__device__ __forceinline__ uint32_t f16x2_min(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 __device__ __forceinline__ uint32_t f32_to_f16x2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// 16 (a - b) of two float16 pairs, exact where a - b is.
-__device__ __forceinline__ uint32_t f16x2_rest16(uint32_t a, uint32_t b) {
+// (a - b) f of float16 pairs, exact where a - b is and f a power of two.
+__device__ __forceinline__ uint32_t f16x2_rest(uint32_t a, uint32_t b, uint32_t f) {
     uint32_t r;
-    asm("{\n .reg .b32 t;\n sub.rn.f16x2 t, %1, %2;\n mul.rn.f16x2 %0, t, %3;\n}" : "=r"(r) : "r"(a), "r"(b), "r"(0x4c004c00u));
+    asm("{\n .reg .b32 t;\n sub.rn.f16x2 t, %1, %2;\n mul.rn.f16x2 %0, t, %3;\n}" : "=r"(r) : "r"(a), "r"(b), "r"(f));
     return r;
 }
 
