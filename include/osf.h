@@ -179,8 +179,8 @@ int osf_attn_fwd_gqa_ex(const void *Q, const void *K, const void *V, void *O, in
  * workspace: osf_attn_window_workspace_bytes bytes, with the same sizes, window and sinks, 16-byte aligned.
  * Buffers that do not start on a boundary of their elements: OSF_ERR_INVALID.
  * Sq or Sk >= 2^29: OSF_ERR_UNSUPPORTED.
- * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores (bfloat16 with D 32 and 96 too), CUDA cores (float32 with D = 64
- * too, where few keys are seen).
+ * Kernel choice as in osf_attn_fwd_gqa_ex: decode, tensor cores (bfloat16 with D 32 and 96 too; of float32 K and V with D = 64 what
+ * some row sees is split into bfloat16 parts in the workspace), CUDA cores (float32 with D = 64 too, where the call is short).
  */
 int osf_attn_fwd_gqa_window(const void *Q, const void *K, const void *V, void *O, int dtype,
                             int B, int Hq, int Hkv, int Sq, int Sk, int D, const long long *strides,

@@ -234,16 +234,17 @@ void carve_partials(AttnProblem &p, void *ws, long long rows) {
 // Which kernel runs a (validated, non-empty) problem.
 enum class Path { Simt, TensorCore, Decode };
 
-// float32 rows of 64 channels under a window: the tensor cores first split all of K and V into bfloat16 parts, whatever the window;
-// the CUDA cores take the keys of the window alone, at a fifth of the rate.  Fitted to measurements (us, CUDA cores against tensor
-// cores; rows x heads / keys, window 200: 77 x 8 / 1001 16, 29; 77 x 8 / 32000 17, 45; 500 x 8 / 1001 31, 32; 1000 x 8 / 2000 52,
-// 48; 1000 x 64 / 2000 226, 175; 77 x 128 / 20000 72, 220; window 1000: 77 x 8 / 8000 21, 32; 77 x 64 / 2000 124, 74; 77 x 128 /
-// 20000 188, 267; 4000: 655, 455).
+// float32 rows of 64 channels under a window, where the call is short: the tensor cores first split what is seen of K and V into
+// bfloat16 parts, in a launch of its own, and take 256 rows to a CTA; the CUDA cores take 64 at a sixth of the rate, which is less while
+// their tiles of 64 keys number no more than the SMs and none has many in a row.  (us, CUDA cores against tensor cores, rows x
+// heads / window: 20 x 2 / 200 15, 17; 200 x 2 / 1000 17, 22; 500 x 2 / 200 17, 20; 2 x 8 / 1000 17, 19; 77 x 8 / 200 17, 17; with more
+// tiles 1000 x 2 / 200 21, 19; 200 x 8 / 200 21, 19; 77 x 8 / 1000 21, 19; 1000 x 8 / 200 53, 25; 77 x 128 / 1000 194, 57; 4000 x 32 / 1000
+// 1307, 255; in a row: 20 x 2 / 4000 27, 20.)
 bool f32_window_small(const AttnProblem &p) {
-    if (!p.window || p.dtype != OSF_F32) return false;
-    const long long rows = (long long)p.B * p.Hq * p.Sq, keys = 64LL * key_stream_max(64, p.Sk, p.window, p.sinks, 64);
-    const long long split = (rows + 2LL * p.B * p.Hkv * p.Sk) * 64;   // elements to split
-    return (double)rows * keys < 2300000 + split / 3;
+    int sms = 0;
+    if (!p.window || p.dtype != OSF_F32 || device_sm_count(&sms) != OSF_OK) return false;
+    const long long tiles = key_stream_max(64, p.Sk, p.window, p.sinks, 64), blocks = (p.Sq + 63LL) / 64 * p.B * p.Hq;
+    return tiles <= 32 && blocks * tiles <= sms;
 }
 
 Path choose_path(const AttnProblem &p, const void *Q, const void *K, const void *V, const void *O) {

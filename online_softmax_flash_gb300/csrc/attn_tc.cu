@@ -311,7 +311,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     if (!ok) break;
                     mbar_expect_tx(smem_u32(&bars.full[st]), C::TILE);
                     const CUtensorMap *mp = part == 0 ? map : (part == 2 || odd) ? map_lo : &mkm;
-                    tma_load_tile<D>(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), key_at<WIN>(w, j), w.kvh, w.b,
+                    int row = key_at<WIN>(w, j);
+                    if (X3 && WIN && row >= p.x3_head) row -= p.x3_skip;
+                    tma_load_tile<D>(sRing + st * C::TILE, mp, smem_u32(&bars.full[st]), row, w.kvh, w.b,
                                      WIN && p.D != D);
                 }
             }
@@ -944,15 +946,16 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 __global__ void __launch_bounds__(256) split_parts_kernel(const AttnProblem p, __nv_bfloat16 *ws) {
     const int which = blockIdx.y;
     const int H = which == 0 ? p.Hq : p.Hkv;
-    const int S = which == 0 ? p.Sq : p.Sk;
-    const long long nq = (long long)p.B * p.Hq * p.Sq * p.D, nk = (long long)p.B * p.Hkv * p.Sk * p.D;
+    const int S = which == 0 ? p.Sq : p.Sk - p.x3_skip;
+    const long long nq = (long long)p.B * p.Hq * p.Sq * p.D, nk = (long long)p.B * p.Hkv * (p.Sk - p.x3_skip) * p.D;
     const long long n = which == 0 ? nq : nk;
     const long long g = (long long)blockIdx.x * blockDim.x + threadIdx.x;   // group of 4 elements
     if (g * 4 >= n) return;
     const int per_row = p.D >> 2;
     const long long row = g / per_row;
     const int d = (int)(g - row * per_row) * 4;
-    const long long sidx = row % S;
+    long long sidx = row % S;
+    if (which != 0 && sidx >= p.x3_head) sidx += p.x3_skip;
     const long long bh = row / S;
     const int h = (int)(bh % H), b = (int)(bh / H);
     const float *src;
@@ -1079,10 +1082,14 @@ cudaError_t launch_bf16(const AttnProblem &p, int sm_count, cudaStream_t s, bool
     return p.D <= 64 ? launch_t<64, false>(p, m, sm_count, s, merged) : launch_t<128, false>(p, m, sm_count, s, merged);
 }
 
-// float32 inputs (D = 64): split Q, K, V into bf16 parts in the workspace, then run x3 mode on
-// contiguous maps of the parts.  Map order: Qh Kh Vh Qm Km Ql Kl Vl.
-cudaError_t launch_x3(const AttnProblem &p, int sm_count, cudaStream_t s, bool &merged) {
-    const long long nq = (long long)p.B * p.Hq * p.Sq * p.D, nk = (long long)p.B * p.Hkv * p.Sk * p.D;
+// float32 inputs (D = 64): split Q, K, V (with a window: what some row sees of K and V) into bf16 parts in the workspace, then
+// run x3 mode on contiguous maps of the parts.  Map order: Qh Kh Vh Qm Km Ql Kl Vl.
+cudaError_t launch_x3(AttnProblem p, int sm_count, cudaStream_t s, bool &merged) {
+    const HiddenKeys hk = p.window ? hidden_keys(p.Sq, p.Sk, p.window, p.sinks, BN) : HiddenKeys{0, 0};
+    p.x3_head = hk.head;
+    p.x3_skip = hk.skip;
+    const int keys = p.Sk - hk.skip;
+    const long long nq = (long long)p.B * p.Hq * p.Sq * p.D, nk = (long long)p.B * p.Hkv * keys * p.D;
     __nv_bfloat16 *ws = static_cast<__nv_bfloat16 *>(p.x3_ws);
     if (!ws) return cudaErrorInvalidValue;
     const long long nmax = nq > nk ? nq : nk;
@@ -1096,12 +1103,12 @@ cudaError_t launch_x3(const AttnProblem &p, int sm_count, cudaStream_t s, bool &
     const __nv_bfloat16 *k[3] = {ws + 3 * nq, ws + 3 * nq + nk, ws + 3 * nq + 2 * nk};
     const __nv_bfloat16 *v[2] = {ws + 3 * nq + 3 * nk, ws + 3 * nq + 4 * nk};
     const int D = p.D;
-    const long long qs = (long long)p.Sq * D, ks = (long long)p.Sk * D;
+    const long long qs = (long long)p.Sq * D, ks = (long long)keys * D;
     auto qmap = [&](CUtensorMap *m, const void *g) {
         return make_bf16_tile_map_strided(m, g, D, p.Sq, p.Hq, p.B, D, qs, qs * p.Hq, BM);
     };
     auto kmap = [&](CUtensorMap *m, const void *g) {
-        return make_bf16_tile_map_strided(m, g, D, p.Sk, p.Hkv, p.B, D, ks, ks * p.Hkv, BN);
+        return make_bf16_tile_map_strided(m, g, D, keys, p.Hkv, p.B, D, ks, ks * p.Hkv, BN);
     };
     CUtensorMap m[8];
     if (!qmap(&m[0], q[0]) || !kmap(&m[1], k[0]) || !kmap(&m[2], v[0]) || !qmap(&m[3], q[1]) ||
@@ -1139,7 +1146,8 @@ bool attn_tc_supported(const AttnProblem &p, const void *Q, const void *K, const
 
 size_t attn_tc_extra_bytes(const AttnProblem &p) {
     if (p.dtype != OSF_F32) return 0;
-    const size_t nq = (size_t)p.B * p.Hq * p.Sq * p.D, nk = (size_t)p.B * p.Hkv * p.Sk * p.D;
+    const int skip = p.window ? hidden_keys(p.Sq, p.Sk, p.window, p.sinks, BN).skip : 0;
+    const size_t nq = (size_t)p.B * p.Hq * p.Sq * p.D, nk = (size_t)p.B * p.Hkv * (p.Sk - skip) * p.D;
     return 2 * (3 * nq + 5 * nk);   // bf16 parts: three of Q and K, two of V
 }
 

@@ -78,6 +78,8 @@ struct AttnProblem {
     int splits;
     float *part_acc, *part_m, *part_l;
     void *x3_ws;         // fp32 on the tensor-core path: bf16 high / low parts of Q, K, V
+    // of K and V those of the keys that some row sees: 0 .. x3_head - 1 and, at x3_head .., those from x3_head + x3_skip on
+    int x3_head, x3_skip;
     int *status;         // device status word
     int keep_nan;        // attn_combine_kernel: the lse of a row with a NaN score is NaN (0: -inf)
 };
@@ -119,6 +121,16 @@ inline int key_stream_max(int rows, int Sk, int window, int sinks, int tile) {
     const long long n_kt = ((long long)Sk + tile - 1) / tile, sink_tiles = ((long long)sinks + tile - 1) / tile;
     const long long n = sink_tiles + ((long long)window + rows - 1 + tile - 2) / tile + 1;
     return (int)(n < n_kt ? n : n_kt);
+}
+
+// Keys that no row of a windowed problem sees, in whole tiles: `skip` of them behind the first `head`.
+struct HiddenKeys {
+    int head, skip;
+};
+inline HiddenKeys hidden_keys(int Sq, int Sk, int window, int sinks, int tile) {
+    const int first = Sk - Sq - window + 1, ws = first > 0 ? first / tile : 0;   // (as in key_stream, of all rows)
+    const int sink_tiles = (sinks - 1 + tile) / tile, ns = sink_tiles < ws ? sink_tiles : ws;
+    return {ns * tile, (ws - ns) * tile};
 }
 
 // Bits 0 .. n - 1 of a word, for any n.
