@@ -96,16 +96,16 @@ SM_COUNT_GB300 = 152
 # each workload's dominant kernel, keyed by the sha256 of the CUDA source it was taken on; a
 # source that changed since the capture reports null.
 TRAFFIC = {
-    "gqa_causal_prefill": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "33729601088ac731",
-                           "bytes": 136.62e6, "scope": "attn_tc_kernel<128>, one launch"},
-    "gqa_causal_prefill_bshd": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "33729601088ac731",
-                                "bytes": 133.67e6, "scope": "attn_tc_kernel<128> on [B, S, H, D] views, one launch"},
-    "gqa_chunked_prefill": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "33729601088ac731",
-                            "bytes": 52.13e6, "scope": "attn_tc_kernel<128>, bottom-right mask, one launch"},
-    "gqa_decode": {"source": "online_softmax_flash_gb300/csrc/decode.cu", "sha": "08ba6f0fc6b184f5",
-                   "bytes": 1079.13e6, "scope": "decode_kernel<128>, one launch"},
-    "gqa_speculative_decode": {"source": "online_softmax_flash_gb300/csrc/decode.cu", "sha": "08ba6f0fc6b184f5",
-                               "bytes": 1085.72e6, "scope": "decode_kernel<128>, 16 rows per kv head, one launch"},
+    "gqa_causal_prefill": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "e85fbe23581f901b",
+                           "bytes": 137.83e6, "scope": "attn_tc_kernel<128>, one launch"},
+    "gqa_causal_prefill_bshd": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "e85fbe23581f901b",
+                                "bytes": 135.57e6, "scope": "attn_tc_kernel<128> on [B, S, H, D] views, one launch"},
+    "gqa_chunked_prefill": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "e85fbe23581f901b",
+                            "bytes": 52.27e6, "scope": "attn_tc_kernel<128>, bottom-right mask, one launch"},
+    "gqa_decode": {"source": "online_softmax_flash_gb300/csrc/decode.cu", "sha": "4aae727741fdcfb5",
+                   "bytes": 1079.19e6, "scope": "decode_kernel<128>, one launch"},
+    "gqa_speculative_decode": {"source": "online_softmax_flash_gb300/csrc/decode.cu", "sha": "4aae727741fdcfb5",
+                               "bytes": 1085.93e6, "scope": "decode_kernel<128>, 16 rows per kv head, one launch"},
     "softmax_rows": {"source": "online_softmax_flash_gb300/csrc/softmax.cu", "sha": "aa0692536436b66b",
                      "bytes": 1013.79e6, "scope": "softmax_rows_resident_kernel<8>, one launch"},
     "softmax_1d": {"source": "online_softmax_flash_gb300/csrc/softmax.cu", "sha": "aa0692536436b66b",
@@ -114,12 +114,12 @@ TRAFFIC = {
                           "bytes": 475.47e6, "scope": "softmax_ex_split_kernel<bf16, bf16, 256, 8>, one launch"},
     "softmax_causal_bf16": {"source": "online_softmax_flash_gb300/csrc/softmax_ex.cu", "sha": "d07ea9a9b6620ae0",
                             "bytes": 343.07e6, "scope": "softmax_ex_pair_kernel<bf16, bf16, 64>, one launch"},
-    "gqa_causal_backward": {"source": "online_softmax_flash_gb300/csrc/attn_bwd_tc.cu", "sha": "6b2edd0b274b2cfa",
-                            "bytes": 1441.99e6,
+    "gqa_causal_backward": {"source": "online_softmax_flash_gb300/csrc/attn_bwd_tc.cu", "sha": "1fdb92b26311dc6c",
+                            "bytes": 1449.79e6,
                             "scope": "bwd_tc_kernel<128> (dK/dV CTAs, writing 1.07 GB of dS^T), one launch"},
-    "single_head_4096_f32": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "33729601088ac731",
-                             "bytes": 4.34e6, "scope": "attn_tc_kernel<64, x3>, one launch"},
-    "single_head_4096_bf16": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "33729601088ac731",
+    "single_head_4096_f32": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "e85fbe23581f901b",
+                             "bytes": 4.33e6, "scope": "attn_tc_kernel<64, x3>, one launch"},
+    "single_head_4096_bf16": {"source": "online_softmax_flash_gb300/csrc/attn_tc.cu", "sha": "e85fbe23581f901b",
                               "bytes": 1.63e6, "scope": "attn_tc_kernel<64>, one launch (8 key splits)"},
 }
 

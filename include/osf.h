@@ -373,19 +373,21 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
  * (0 .. n; the rows behind them are padding and are not read).
  * A page that a sequence's first token falls into (slot 0 is new) gets its scale from the new tokens alone.  A page that
  * holds earlier tokens keeps its scale, unless the new ones need a larger one: then the codes there are rounded again, to
- * the new scale.  Two sequences of a call must not write to the same page.  Slots that hold no token of the sequence are
- * left as they were.
+ * the new scale.  A call must not write to the same page for two sequences, nor for two places of one.  Slots that hold no
+ * token of the sequence are left as they were.
  * Rotation: cos_table, sin_table: float32 [max_positions, rotary_dim / 2] (rotary_dim 0: none; a multiple of 8, at most D):
  *     (a, b) -> (a cos - b sin, b cos + a sin), rounded once to float32, for channels i and i + rotary_dim / 2, or with
  *     interleaved 2 i and 2 i + 1, at position lens[b] + t.  Channels from rotary_dim on are stored as they are.
  * Q, Q_out: NULL, or queries [B, Hq, n, D] of the same tokens, rotated by the same angles in float32 (one product rounded, the
- *     other fused into the difference) and rounded to `dtype`; Q_out may be Q (with the same strides).  Rows at and behind counts[b] are left as they were.
+ *     other fused into the difference) and rounded to `dtype`; Q_out may be Q (with the same strides).  Rows at and behind counts[b]
+ *     are left as they were.
  * strides: NULL (contiguous), or 6 element strides, K: b, h, s  V: b, h, s, and with Q 6 more, Q: b, h, s  Q_out: b, h, s.
  * Tokens that would fall behind table_len * P are not stored, and recorded as OSF_ERR_INVALID in the device status word, as
  * are counts out of range (cut to it), a negative length (nothing of that sequence is stored) and positions that the tables
  * do not hold (the last one is taken).
- * n == 0 or B == 0: OSF_OK.  n > table_len * P without counts, outputs that overlap an input, NULL pointers, buffers that do
- * not start on a boundary of their elements: OSF_ERR_INVALID.
+ * n == 0 or B == 0: OSF_OK.  n > table_len * P without counts, outputs that overlap an input (checked on address ranges, so not
+ * Q_out = Q in a buffer that Q shares with K and V), NULL pointers, buffers that do not start on a boundary of their
+ * elements: OSF_ERR_INVALID.
  */
 int osf_kv8_append(const void *K, const void *V, int dtype, int B, int Hkv, int n, int D,
                    const long long *strides, void *pages, float *scales, int n_pages, int page_tokens,

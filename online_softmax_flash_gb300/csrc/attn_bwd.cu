@@ -674,7 +674,8 @@ template <typename T>
 cudaError_t launch_rows_k(BwdProblem p, RowsKernel kernel, int per, int threads, size_t smem, cudaStream_t s) {
     cudaError_t e = set_max_dynamic_smem((const void *)kernel, (int)smem);
     if (e != cudaSuccess) return e;
-    if (p.part_keys != per || p.shared_tiles == 0 || p.parts <= 1) {   // (or the plan is the tensor-core path's, whose sizes TMA did not address)
+    // (nothing to share out, or the plan is the tensor-core path's, whose tensors TMA did not address)
+    if (p.part_keys != per || p.shared_tiles == 0 || p.parts <= 1) {
         p.shared_tiles = 0;
         p.parts = 1;
     }
@@ -688,8 +689,8 @@ cudaError_t launch_rows_k(BwdProblem p, RowsKernel kernel, int per, int threads,
     e = launch_dependent(kernel, dim3((unsigned)all), dim3(threads), smem, s, p, (unsigned)kv, kv_tiles, q_tiles, vec);
     if (e != cudaSuccess || p.parts == 1) return e;
     count_launches(1);
-    return launch_dependent(bwd_rows_sum_kernel<T>, dim3((unsigned)(((long long)p.shared_tiles * per * p.D + 255) / 256), (unsigned)(p.B * p.Hkv), 2),
-                            dim3(256), 0, s, p);
+    const dim3 g((unsigned)(((long long)p.shared_tiles * per * p.D + 255) / 256), (unsigned)(p.B * p.Hkv), 2);
+    return launch_dependent(bwd_rows_sum_kernel<T>, g, dim3(256), 0, s, p);
 }
 template <typename T, int C, int KPW>
 cudaError_t launch_rows(const BwdProblem &p, cudaStream_t s) {

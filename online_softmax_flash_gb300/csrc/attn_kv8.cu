@@ -209,8 +209,9 @@ attn_kv8_kernel(const Kv8AttnProblem kp) {
 // their states meet at the end of the run.  A team is four warps, or with 16 rows two groups of four that take 8 rows each.  A
 // group's next scores are computed while it works on these: S^T is free as soon as the group has read it.  Runs are cut flat over
 // all sequences (see FlatCut), and a second kernel joins the pieces of a sequence that several CTAs share.
-// Up to 8 rows of D = 128 are bound by DRAM: 8 sequences of 32768 tokens, 8 kv heads of 4 rows, 537 MB: 91 us with launches and
-// join, 5.9 TB/s (16 rows 106 us: what the groups issue for their weights; D = 64, 268 MB, 64 us: the same).
+// Up to 8 rows of D = 128 are bound by DRAM: 8 sequences of 32768 tokens, 8 kv heads of 4 rows, 537 MB: 90.5 us with launches and
+// join, 5.9 TB/s (16 rows 105 us: what the groups issue for their weights; D = 64, 268 MB, 62 us: the same).  The levels
+// cost these 0 to 1.5 %, filled or not, and calls of short items 1 to 2 us (128 items of 17 tiles of 16 rows 27.0 to 28.8).
 constexpr int TT = 128;                   // tokens per tile
 constexpr float kRowFloor = -3.4028235e38f;   // reference of a row that has seen nothing
 constexpr int kMaxRing = 12;
@@ -435,7 +436,8 @@ __device__ __forceinline__ void store_parts(uint32_t p_row, int lv, const uint32
     }
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-        const int word = NR == RT ? (3 * lv + k) * (RT / 4) : 4 * (3 * lv + k);   // (16 rows: a plane to a part, and p_row says which half)
+        // (16 rows: a plane to a part, and p_row says which half)
+        const int word = NR == RT ? (3 * lv + k) * (RT / 4) : 4 * (3 * lv + k);
         const uint32_t at = p_row + (word >> 2) * (TT * 16) + (word & 3) * 4;
         if constexpr (RT == 4) asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(part[k][0]) : "memory");
         else asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(part[k][0]), "r"(part[k][1]) : "memory");

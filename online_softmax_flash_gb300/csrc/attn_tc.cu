@@ -544,9 +544,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                 if constexpr (WIN && !X3)
 #pragma unroll
                     for (int c = 0; c < 4; ++c) seen[c] = seen_of(c);
-                // the hidden columns of chunk c (columns 32 c .. 32 c + 31) of a float32 tile: -inf.  Behind a branch, since most tiles
-                // hide none, and from one word (float32, one head of 4096 rows and keys 34 us, with a selection at each column 43;
-                // 64 heads of 2000 rows, window 1000, 170, with the words of all chunks in an array 364)
+                // the hidden columns of chunk c (columns 32 c .. 32 c + 31) of a float32 tile: -inf.  Behind a branch, since
+                // most tiles hide none, and from one word (float32, one head of 4096 rows and keys 34 us, with a selection at each
+                // column 43; 64 heads of 2000 rows, window 1000, 170, with the words of all chunks in an array 364)
                 auto mask_chunk = [&](int c, uint32_t (&s)[32]) {
                     if (!need_mask) return;
                     const uint32_t word = WIN ? seen_of(c) : bits_below(lim - 32 * c);
@@ -748,7 +748,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ C
                     // 32-byte stores when every row starts on a 32-byte boundary
                     const bool o32 = ((reinterpret_cast<uintptr_t>(p.o) | (uintptr_t)(p.o_ss * 2) |
                                        (uintptr_t)(p.o_sh * 2) | (uintptr_t)(p.o_sb * 2)) & 31) == 0;
-#pragma unroll(WIN ? 1 : D / 32)   // (with a window items are short, and code that runs once an item is fetched anew; window 128: 78 -> 74 us)
+// (with a window items are short, and code that runs once an item is fetched anew; window 128: 78 -> 74 us)
+#pragma unroll(WIN ? 1 : D / 32)
                     for (int c = 0; c < D / 32; ++c) {
                         if (WIN && c * 32 >= p.D) break;
                         uint32_t o[32];

@@ -9,9 +9,9 @@
 // change their exponent, so that is exact but for those that fall among the subnormals.  NaN and infinities are stored as
 // NaN and leave the scale alone.
 // A block goes through one chain: lengths and table, then rows and angles, then the scale; the reduction; the stores.  That, not
-// DRAM, bounds it: three blocks of 256 threads to an SM hide most of it (8 prompts of 4096 tokens, 8 heads of 128, 168 MB
-// without queries: 74 us, 2.3 TB/s; two or four blocks 87, 107; two blocks of 512 threads 111; angles loaded behind the check of the
-// table's entry 85; every value by rotate1 2 us more).  With the queries of 32 heads, 704 MB: 138 us, 5.1 TB/s.
+// DRAM, bounds it: three blocks of 256 threads to an SM hide most of it (8 prompts of 4096 tokens, 8 heads of 128, 201 MB
+// without queries: 74 us, 2.7 TB/s; two or four blocks 87, 107; two blocks of 512 threads 111; angles loaded behind the
+// check of the table's entry 85; every value by rotate1 2 us more).  With the queries of 32 heads, 738 MB: 138 us, 5.3 TB/s.
 #include "kv8.cuh"
 #include "sm100_ptx.cuh"
 
@@ -128,7 +128,7 @@ __device__ __forceinline__ float rotate1(float a, float c, float b, float s) {
     const float he = __fsub_rn(__fsub_rn(p, __fsub_rn(h, t)), __fadd_rn(q, t));   // h + he = p - q
     return fabsf(h) <= kMaxF32 ? __fadd_rn(h, __fadd_rn(he, __fsub_rn(pe, qe))) : h;
 }
-// a c - b s within 2 units in the last place, whatever cancels: the rounding error of b s, exact, is added back.
+// a c - b s within 2 units in the last place, whatever cancels (Kahan's): the rounding error of b s, exact, is added back.
 __device__ __forceinline__ float rotate2(float a, float c, float b, float s) {
     const float q = __fmul_rn(b, s);
     return __fadd_rn(__fmaf_rn(a, c, -q), __fmaf_rn(-b, s, q));
@@ -220,7 +220,8 @@ __device__ __forceinline__ void store_codes(unsigned char *p, const float *x, fl
 // The new tokens of one page of one kv head, K or V, by `size` threads: a warp (few tokens) or a block.  K units per thread
 // stay in registers between the search for the largest magnitude and the rounding.
 template <typename T, int W, bool BLOCK>
-__device__ __forceinline__ void append_page(const Kv8StoreProblem &p, bool interleaved, int bh, int half, int page_no, int me, int size, bool vec) {
+__device__ __forceinline__ void append_page(const Kv8StoreProblem &p, bool interleaved, int bh, int half, int page_no, int me, int size,
+                                            bool vec) {
     constexpr int KEEP = W == 8 ? 2 : 4;
     __shared__ uint32_t sh_max[kThreads / 32];
     const Kv8Cache &c = p.c;
@@ -417,8 +418,8 @@ __device__ __forceinline__ void rotate_queries(const Kv8StoreProblem &p, bool in
 }
 
 // One launch: blocks for the pages that new tokens may fall into, and among them, spread evenly, blocks for the queries; the
-// former wait on their chain of loads, a reduction and stores, and the latter are bound by memory.  Of the blocks before block i, i * page_share / 2^32 have
-// pages.
+// former wait on their chain of loads, a reduction and stores, and the latter are bound by memory.  Of the blocks before block i,
+// i * page_share / 2^32 have pages.
 // INTER: whether pairs are interleaved (2: to be seen at run time).
 template <typename T, int W, bool BLOCK, int HB, int INTER>
 __global__ void __launch_bounds__(kThreads, 3)
@@ -531,8 +532,8 @@ cudaError_t append_k(const Kv8StoreProblem &p, int pages_per_seq, cudaStream_t s
     const long long blocks = page_blocks + (!p.q ? 0 : per ? (heads + per - 1) / per : heads * q_blocks);
     if (blocks >= (1LL << 31) || tasks >= (1LL << 31)) return cudaErrorInvalidValue;
     kv8_append_kernel<T, W, BLOCK, HB, INTER><<<(unsigned)blocks, kThreads, 0, s>>>(
-        p, pages_per_seq, (((unsigned long long)page_blocks << 32) + blocks - 1) / blocks, (unsigned)q_blocks, rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W),
-        rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
+        p, pages_per_seq, (((unsigned long long)page_blocks << 32) + blocks - 1) / blocks, (unsigned)q_blocks,
+        rows_vec(p.k, p.k_sb, p.k_sh, p.k_ss, es, W), rows_vec(p.v, p.v_sb, p.v_sh, p.v_ss, es, W), rows_vec(p.q, p.q_sb, p.q_sh, p.q_ss, es, W),
         rows_vec(p.qo, p.o_sb, p.o_sh, p.o_ss, es, W));
     count_launches(1);
     return cudaGetLastError();
@@ -567,7 +568,8 @@ cudaError_t read_t(Kv8StoreProblem p, int sm_count, cudaStream_t s) {
     set_units(p, c.D / CH);
     const long long work = ((long long)p.n * (c.D / CH) + kThreads - 1) / kThreads;
     const long long heads = (long long)p.B * c.Hkv * 2, most = (16LL * sm_count + heads - 1) / heads;
-    const long long few = (work + kReadTokens - 1) / kReadTokens;   // (32 sequences of 64 tokens: 8.8 us; a block to each kThreads pieces 10.9)
+    // (32 sequences of 64 tokens: 8.8 us; a block to each kThreads pieces 10.9)
+    const long long few = (work + kReadTokens - 1) / kReadTokens;
     const dim3 grid((unsigned)(few < most ? few : most), (unsigned)(p.B * c.Hkv), 2);
     kv8_read_kernel<T><<<grid, kThreads, 0, s>>>(p, rows_vec(p.ko, 0, 0, 0, sizeof(T), CH), rows_vec(p.vo, 0, 0, 0, sizeof(T), CH));
     count_launches(1);
