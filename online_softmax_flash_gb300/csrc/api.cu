@@ -259,7 +259,7 @@ Path choose_path(const AttnProblem &p, const void *Q, const void *K, const void 
 int plan_splits(const AttnProblem &p, Path path, int sm_count, int requested) {
     if (path == Path::TensorCore) return attn_tc_pick_splits(p, sm_count);
     if (path == Path::Decode) return decode_pick_splits(p, sm_count, requested);
-    if (requested > 0) {
+    if (requested > 0 && (long long)p.B * p.Hq <= 65535) {
         const int n_kt = (p.Sk + 63) / 64;
         return requested < n_kt ? requested : n_kt;
     }

@@ -572,7 +572,37 @@ size_t attn_simt_partial_floats(int splits, long long rows, int D) {
     return (size_t)splits * rows * (size_t)(D + 2);
 }
 
+// The part of a problem from batch b and query head h on (one of them 0), with its sizes, as a problem of its own.
+static AttnProblem part_of(const AttnProblem &p, int b, int h, int B, int Hq, int Hkv) {
+    AttnProblem r = p;
+    const int kvh = h / (p.Hq / p.Hkv), es = p.dtype == OSF_F32 ? 4 : 2;
+    r.q = static_cast<const char *>(p.q) + q_at(p, b, h, 0) * es;
+    r.k = static_cast<const char *>(p.k) + k_at(p, b, kvh, 0) * es;
+    r.v = static_cast<const char *>(p.v) + v_at(p, b, kvh, 0) * es;
+    r.o = static_cast<char *>(p.o) + o_at(p, b, h, 0) * es;
+    if (p.lse) r.lse = p.lse + ((long long)b * p.Hq + h) * p.Sq;
+    r.B = B; r.Hq = Hq; r.Hkv = Hkv;
+    return r;
+}
+
 cudaError_t launch_attn_simt(const AttnProblem &p, cudaStream_t s) {
+    if ((long long)p.B * p.Hq > 65535) {   // more heads than the grid's second dimension holds: two halves, whole kv groups if there are any
+        if (p.splits != 1) return cudaErrorInvalidValue;
+        AttnProblem a, b;
+        if (p.B > 1) {
+            a = part_of(p, 0, 0, p.B / 2, p.Hq, p.Hkv);
+            b = part_of(p, p.B / 2, 0, p.B - p.B / 2, p.Hq, p.Hkv);
+        } else if (p.Hkv > 1) {
+            const int G = p.Hq / p.Hkv, half = p.Hkv / 2;
+            a = part_of(p, 0, 0, 1, half * G, half);
+            b = part_of(p, 0, half * G, 1, p.Hq - half * G, p.Hkv - half);
+        } else {
+            a = part_of(p, 0, 0, 1, p.Hq / 2, 1);
+            b = part_of(p, 0, p.Hq / 2, 1, p.Hq - p.Hq / 2, 1);
+        }
+        const cudaError_t e = launch_attn_simt(a, s);
+        return e == cudaSuccess ? launch_attn_simt(b, s) : e;
+    }
     if (p.splits == 1 && rows_eligible(p)) return p.D <= 32 ? launch_rows_t<32>(p, s) : launch_rows_t<64>(p, s);
     return p.dtype == OSF_F32 ? launch_dp<float>(p, s) : launch_dp<__nv_bfloat16>(p, s);
 }
