@@ -654,7 +654,7 @@ attn_kv8_tc_kernel(const __grid_constant__ CUtensorMap mpages, const Kv8AttnProb
                 }
                 mx = warp_max(mx);
                 bad = __any_sync(0xffffffffu, bad);
-                const int ex = max(-100, min(100, 7 - ((int)(__float_as_uint(mx) >> 23) - 127)));
+                const int ex = min(119, 7 - ((int)(__float_as_uint(mx) >> 23) - 127));   // -120 at least (larger is not finite)
                 const float up = pow2_of(ex);
 #pragma unroll
                 for (int part = 0; part < 2; ++part) {

@@ -131,3 +131,21 @@ def test_a_channel_for_each_depth_of_weight(osf, D, G, Sq, order):
     bound = (2.0 ** -8 * np.abs(O) + (2.0 ** -11 + 2.0 ** -15 + 2.0 ** -20 * nats) * size + slack) * (1 + 1 / 16) + 2.0 ** -133
     assert np.all(np.abs(got - O) <= bound)
     assert osf.osf_device_status() == osf.OSF_OK
+
+
+@pytest.mark.parametrize("D,G", [(64, 4), (128, 8), (128, 16)])
+def test_queries_of_any_size(osf, D, G):
+    """Rows up to the largest bfloat16 keep their bits, with a scale that makes up for it."""
+    n = 300
+    rng = np.random.default_rng(D)
+    pages, scales, table = new_cache(1, 1, 5, 64, D, seed=4)
+    kv = rng.standard_normal((2, 1, 1, n, D))
+    oracle.kv8_append(kv[0], kv[1], pages, scales, table)
+    gp, gs, gt, gl = to_gpu(pages, scales, table, np.array([n], np.int32))
+    for size in (-110, -100, 100, 105, 110, 120):
+        q, Q = rows(rng, (1, G, 1, D), "bf16")
+        q, Q = q * 2.0 ** size, Q * 2.0 ** size
+        assert torch.isfinite(Q).all()
+        scale = 0.1 * 2.0 ** -size
+        o = osf.osf_attn_kv8(Q, gp, gs, gt, lens=gl, scale=scale)
+        check(o, reference(q.astype(np.float64), pages, scales, table, [n], 0, 0, scale), f"2^{size}")
