@@ -365,6 +365,8 @@ int osf_attn_kv4_workspace_bytes(int dtype, int B, int Hq, int Hkv, int Sq, int 
  * that is more.  NaN and infinities are stored as NaN.  (From 2^127 * 1.9375 on a value reads back as infinity.)
  * An entry that is no page of the cache, and a length outside [0, table_len * P], are recorded as OSF_ERR_INVALID in the
  * device status word (osf_device_status); the tokens of such an entry are neither stored nor seen, such a length is cut.
+ * Other P or D, B * Hkv > 65535 (with queries to rotate: B * Hq), n * D or n_pages * 2 * Hkv * P >= 2^31, table_len * P >= 2^29:
+ * OSF_ERR_UNSUPPORTED.
  */
 
 /*
